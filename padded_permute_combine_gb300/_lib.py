@@ -13,6 +13,7 @@ import re
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmoe_route.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "moe_route.h")
+BLOCK_HEADER = os.path.join(os.path.dirname(PKG), "include", "moe_block.h")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA = 0, 1, 2, 3
 MOE_F32, MOE_BF16 = 0, 1
@@ -21,6 +22,7 @@ MOE_STATUS_TIMEOUT = 16
 MOE_MAX_EXPERTS, MOE_MAX_TOP_K = 4096, 64
 MOE_GATING_SOFTMAX, MOE_GATING_SIGMOID = 0, 1
 MOE_GATING_MAX_EXPERTS = 1024
+MOE_LAYER_MAX_TOKENS, MOE_LAYER_MAX_CHOICES = 256, 2048
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -60,6 +62,29 @@ SIGNATURES = {
     "moe_routing_map_to_indices_bwd": (ctypes.c_int, [_P, _P, _I64, _I32, _I32, _P, _P, _P]),
 }
 
+# The entry points of include/moe_block.h, in its order.
+BLOCK_SIGNATURES = {
+    "moe_layer_workspace_size": (_SZ, [_I64, _I64, _I64, _I32, _I32]),
+    "moe_layer": (ctypes.c_int, [_P, _I32, _I64, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _P, _P, _P, _P,
+                                 _SZ, _P, _P]),
+    "moe_experts": (ctypes.c_int, [_P, _I32, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _P, _P, _SZ, _P, _P]),
+    "moe_layer_norm_fwd": (ctypes.c_int, [_P, _I32, _I64, _P, _P, _I32, _I64, _I64, ctypes.c_float, _P, _P, _P, _P]),
+    "moe_layer_norm_bwd_workspace_size": (_SZ, [_I64, _I64]),
+    "moe_layer_norm_bwd": (ctypes.c_int, [_P, _I64, _P, _I32, _I64, _P, _I32, _P, _P, _I64, _I64, _P, _P, _P, _P, _SZ,
+                                          _P]),
+    "moe_grad_table_pieces": (_I64, [_P, _I64]),
+    "moe_grad_table_fill": (ctypes.c_int, [_P, _I64, _P, _I64]),
+    "moe_grad_norm_workspace_size": (_SZ, []),
+    "moe_grad_norm": (ctypes.c_int, [_P, _I64, _P, _P, _SZ, _P]),
+    "moe_clip_grads": (ctypes.c_int, [_P, _I64, ctypes.c_float, _P, _P, _SZ, _P]),
+}
+
+
+class GradTensor(ctypes.Structure):
+    """moe_grad_tensor; moe_grad_piece has the same layout."""
+
+    _fields_ = [("grad", _P), ("out", _P), ("numel", _I64), ("dtype", _I32), ("reserved", _I32)]
+
 
 class MoeError(RuntimeError):
     """A C-ABI call returned a nonzero MOE_ERR_* code."""
@@ -72,9 +97,9 @@ class MoeError(RuntimeError):
 _lib = None
 
 
-def header_functions() -> list[str]:
-    """Names of every function declared in include/moe_route.h."""
-    src = open(HEADER).read()
+def header_functions(header: str = HEADER) -> list[str]:
+    """Names of every function declared in include/moe_route.h (or another header)."""
+    src = open(header).read()
     src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
     return re.findall(r"\b(moe_\w+)\s*\(", src)
 
@@ -89,7 +114,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
         raise RuntimeError("libmoe_route.so is not built (%s); run "
                            "`python -m padded_permute_combine_gb300.build` first" % p)
     lib = ctypes.CDLL(p)
-    for name, (res, args) in SIGNATURES.items():
+    for name, (res, args) in (SIGNATURES | BLOCK_SIGNATURES).items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

@@ -15,12 +15,13 @@ the definitions the pages give:
 - Combine (the scatter, [binned] Workflow step 5, [padded] Workflow step 6):
   y[t] = sum_k w[a] * xe[row(a)], whose gradient is w[a] * dy[t] for the expert
   rows (the weighted gather) and dot(xe[row(a)], dy[t]) for the weights (wgrad).
+- LayerNorm (the norm in front of the router): moe_layer_norm_fwd / _bwd.
 """
 from __future__ import annotations
 
 import torch
 
-from . import ops
+from . import block, ops
 
 
 class RoutingMapToIndices(torch.autograd.Function):
@@ -120,3 +121,31 @@ def permute(x, route, num_experts, capacity=None, top_k=1):
 def combine(xe, weights, route, num_tokens, top_k, padded=False):
     """Weighted combine of expert rows, differentiable in xe and weights."""
     return Combine.apply(xe, weights, route, num_tokens, top_k, padded)
+
+
+class LayerNorm(torch.autograd.Function):
+    """x [..., H], weight and bias ([H] or None) -> the layer norm of x over its last dimension."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        rows = x.detach().reshape(-1, x.shape[-1])
+        if rows.stride(-1) != 1 or (rows.shape[0] > 1 and rows.stride(0) < rows.shape[1]):
+            rows = rows.contiguous()
+        y, mean, rstd = block.moe_layer_norm_fwd(rows, weight, bias, eps)
+        ctx.save_for_backward(rows, weight, mean, rstd)
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return y.view(x.shape)
+
+    @staticmethod
+    def backward(ctx, grad_y):
+        rows, weight, mean, rstd = ctx.saved_tensors
+        cols = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
+        dy = grad_y.reshape(rows.shape).contiguous()
+        dx, dw, db = block.moe_layer_norm_bwd(dy, rows, weight, mean, rstd, ctx.bias_dtype, need_cols=cols)
+        return (dx.view(grad_y.shape), dw if ctx.needs_input_grad[1] else None,
+                db if ctx.needs_input_grad[2] else None, None)
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5):
+    """Layer norm over the last dimension, differentiable in x, weight and bias."""
+    return LayerNorm.apply(x, weight, bias, eps)

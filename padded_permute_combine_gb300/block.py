@@ -1,0 +1,256 @@
+"""Python binding of include/moe_block.h: the operators around the routing in
+an MoE block (same names, same semantics).
+
+As in ops.py this is argument marshalling only. Rows (x, dy) may come with a
+row stride, such as a slice of a wider tensor; everything else is contiguous.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Sequence
+
+import torch
+
+from . import _lib
+from .ops import _act_dtype, _need, _ptr, _stream
+
+_MODES = {"softmax": _lib.MOE_GATING_SOFTMAX, "sigmoid": _lib.MOE_GATING_SIGMOID}
+
+
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype | None = None, shape=None, device=None) -> int:
+    """Checks a [rows, H] tensor whose rows are contiguous and returns its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError("%s must be %s, got %s" % (name, "2-D" if shape is None else list(shape), list(t.shape)))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    stride, inner = t.stride()
+    if t.shape[1] > 1 and inner != 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    if t.shape[0] > 1 and stride < t.shape[1]:
+        raise ValueError("%s must have rows that do not overlap" % name)
+    return stride
+
+
+def _shape(t: torch.Tensor, shape: tuple, name: str) -> torch.Tensor:
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    return t
+
+
+def _expert_weights(x, w_gate_up, w_down):
+    _need(w_gate_up, x.dtype, "w_gate_up", x.device)
+    _need(w_down, x.dtype, "w_down", x.device)
+    H = x.shape[1]
+    if w_down.dim() != 3 or w_down.shape[1] != H:
+        raise ValueError("w_down must be [E, %d, F], got %s" % (H, list(w_down.shape)))
+    E, F = w_down.shape[0], w_down.shape[2]
+    _shape(w_gate_up, (E, 2 * F, H), "w_gate_up")
+    return E, F
+
+
+def layer_workspace(num_tokens: int, hidden: int, ffn: int, num_experts: int, top_k: int, device) -> torch.Tensor:
+    """Workspace of moe_layer and moe_experts (one per stream that may run them at the same time)."""
+    size = _lib.load().moe_layer_workspace_size(num_tokens, hidden, ffn, num_experts, top_k)
+    return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def moe_layer(x: torch.Tensor, router: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, top_k: int,
+              mode: str = "softmax", normalize: bool = True, out: torch.Tensor | None = None,
+              routing: tuple[torch.Tensor, torch.Tensor] | None = None, workspace: torch.Tensor | None = None,
+              status: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """A whole MoE layer for a few tokens (at most 256, and 2048 choices):
+    x [T, H], router [E, H], w_gate_up [E, 2F, H], w_down [E, H, F] ->
+    (y [T, H], top_expert [T, top_k] int32, weights [T, top_k] fp32). mode and
+    normalize as for moe_topk_gating; ``routing``: the two tensors that take
+    top_expert and weights."""
+    stride = _rows(x, "x")
+    dt = _act_dtype(x, "x")
+    dev = x.device
+    T, H = x.shape
+    E, F = _expert_weights(x, w_gate_up, w_down)
+    _shape(_need(router, x.dtype, "router", dev), (E, H), "router")
+    if mode not in _MODES:
+        raise ValueError("mode must be softmax or sigmoid, got %r" % (mode,))
+    if routing is None:
+        routing = (torch.empty((T, top_k), dtype=torch.int32, device=dev),
+                   torch.empty((T, top_k), dtype=torch.float32, device=dev))
+    te = _shape(_need(routing[0], torch.int32, "top_expert", dev), (T, top_k), "top_expert")
+    w = _shape(_need(routing[1], torch.float32, "weights", dev), (T, top_k), "weights")
+    if out is None:
+        out = torch.empty((T, H), dtype=x.dtype, device=dev)
+    _shape(_need(out, x.dtype, "out", dev), (T, H), "out")
+    ws = workspace if workspace is not None else layer_workspace(T, H, F, E, top_k, dev)
+    _need(ws, torch.uint8, "workspace", dev)
+    _lib.call("moe_layer", _ptr(x), dt, stride, _ptr(router), _ptr(w_gate_up), _ptr(w_down), T, H, F, E, top_k,
+              _MODES[mode], int(bool(normalize)), _ptr(te), _ptr(w), _ptr(out), _ptr(ws), ws.numel(), _ptr(status),
+              _stream(x))
+    return out, te, w
+
+
+def moe_experts(x: torch.Tensor, top_expert: torch.Tensor, weights: torch.Tensor, w_gate_up: torch.Tensor,
+                w_down: torch.Tensor, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                status: torch.Tensor | None = None) -> torch.Tensor:
+    """The gated experts and their weighted sum for a routing already made:
+    x [T, H], top_expert [T, top_k] int32 (-1: no expert), weights [T, top_k]
+    fp32 -> y [T, H]. Sizes as for moe_layer."""
+    stride = _rows(x, "x")
+    dt = _act_dtype(x, "x")
+    dev = x.device
+    T, H = x.shape
+    E, F = _expert_weights(x, w_gate_up, w_down)
+    _need(top_expert, torch.int32, "top_expert", dev)
+    if top_expert.dim() != 2 or top_expert.shape[0] != T:
+        raise ValueError("top_expert must be [%d, top_k], got %s" % (T, list(top_expert.shape)))
+    K = top_expert.shape[1]
+    _shape(_need(weights, torch.float32, "weights", dev), (T, K), "weights")
+    if out is None:
+        out = torch.empty((T, H), dtype=x.dtype, device=dev)
+    _shape(_need(out, x.dtype, "out", dev), (T, H), "out")
+    ws = workspace if workspace is not None else layer_workspace(T, H, F, E, K, dev)
+    _need(ws, torch.uint8, "workspace", dev)
+    _lib.call("moe_experts", _ptr(x), dt, stride, _ptr(top_expert), _ptr(weights), _ptr(w_gate_up), _ptr(w_down), T, H,
+              F, E, K, _ptr(out), _ptr(ws), ws.numel(), _ptr(status), _stream(x))
+    return out
+
+
+def _affine(weight, bias, H, dev):
+    """The dtype of weight and bias ([H] each, or None), as a MOE_* value."""
+    code = _lib.MOE_F32
+    for t, name in ((bias, "bias"), (weight, "weight")):
+        if t is not None:
+            _need(t, None, name, dev)
+            _shape(t, (H,), name)
+            code = _act_dtype(t, name)
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must have one dtype, got %s and %s" % (weight.dtype, bias.dtype))
+    return code
+
+
+def moe_layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                       eps: float = 1e-5, out: torch.Tensor | None = None,
+                       stats: tuple[torch.Tensor, torch.Tensor] | None = None):
+    """Layer norm of the rows of x [rows, H]: (y [rows, H], mean [rows] fp32,
+    rstd [rows] fp32). ``stats``: the two tensors that take mean and rstd."""
+    stride = _rows(x, "x")
+    dt = _act_dtype(x, "x")
+    dev = x.device
+    M, H = x.shape
+    wdt = _affine(weight, bias, H, dev)
+    if out is None:
+        out = torch.empty((M, H), dtype=x.dtype, device=dev)
+    _shape(_need(out, x.dtype, "out", dev), (M, H), "out")
+    if stats is None:
+        stats = torch.empty((2, M), dtype=torch.float32, device=dev).unbind(0)
+    mean = _shape(_need(stats[0], torch.float32, "mean", dev), (M,), "mean")
+    rstd = _shape(_need(stats[1], torch.float32, "rstd", dev), (M,), "rstd")
+    _lib.call("moe_layer_norm_fwd", _ptr(x), dt, stride, _ptr(weight), _ptr(bias), wdt, M, H, eps, _ptr(out),
+              _ptr(mean), _ptr(rstd), _stream(x))
+    return out, mean, rstd
+
+
+def moe_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | None, mean: torch.Tensor,
+                       rstd: torch.Tensor, weight_dtype: torch.dtype | None = None, need_cols: bool = True,
+                       out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Gradients of moe_layer_norm_fwd: (dx [rows, H], dweight [H], dbias [H]).
+    dweight and dbias have weight's dtype (``weight_dtype`` without a weight,
+    fp32 by default), and are None with need_cols=False."""
+    stride = _rows(x, "x")
+    dt = _act_dtype(x, "x")
+    dev = x.device
+    M, H = x.shape
+    dy_stride = _rows(dy, "dy", x.dtype, x.shape, dev)
+    _shape(_need(mean, torch.float32, "mean", dev), (M,), "mean")
+    _shape(_need(rstd, torch.float32, "rstd", dev), (M,), "rstd")
+    if weight is not None:
+        weight_dtype = weight.dtype
+    wdt = weight_dtype or torch.float32
+    code = _affine(weight, None, H, dev) if weight is not None else _lib.MOE_BF16 if wdt == torch.bfloat16 else _lib.MOE_F32
+    if out is None:
+        out = torch.empty((M, H), dtype=x.dtype, device=dev)
+    _shape(_need(out, x.dtype, "out", dev), (M, H), "out")
+    dw = db = ws = None
+    if need_cols:
+        dw, db = torch.empty((2, H), dtype=wdt, device=dev).unbind(0)
+        ws = workspace
+        if ws is None:
+            with torch.cuda.device(dev):  # sized for this device's SM count
+                size = _lib.load().moe_layer_norm_bwd_workspace_size(M, H)
+            ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        _need(ws, torch.uint8, "workspace", dev)
+    _lib.call("moe_layer_norm_bwd", _ptr(dy), dy_stride, _ptr(x), dt, stride, _ptr(weight), code, _ptr(mean),
+              _ptr(rstd), M, H, _ptr(out), _ptr(dw), _ptr(db), _ptr(ws), 0 if ws is None else ws.numel(), _stream(x))
+    return out, dw, db
+
+
+class GradSet:
+    """The gradients that one norm covers, as the device table that
+    moe_grad_norm and moe_clip_grads read. Holds references to its tensors;
+    they must stay where they are (a gradient that is allocated anew needs a
+    new set). ``outs``: where clipping writes; the gradients themselves by
+    default."""
+
+    def __init__(self, grads: Sequence[torch.Tensor], outs: Sequence[torch.Tensor] | None = None):
+        self.grads, self.outs = list(grads), None if outs is None else list(outs)
+        if not self.grads:
+            raise ValueError("a set needs at least one tensor")
+        if self.outs is not None and len(self.outs) != len(self.grads):
+            raise ValueError("%d gradients and %d outs" % (len(self.grads), len(self.outs)))
+        dev = self.device = self.grads[0].device
+        entries = (_lib.GradTensor * len(self.grads))()
+        for i, g in enumerate(self.grads):
+            _need(g, None, "grads[%d]" % i, dev)
+            o = g if self.outs is None else self.outs[i]
+            _shape(_need(o, g.dtype, "outs[%d]" % i, dev), g.shape, "outs[%d]" % i)
+            entries[i] = _lib.GradTensor(g.data_ptr() or None, o.data_ptr() or None, g.numel(), _act_dtype(g, "grads[%d]" % i), 0)
+        lib = _lib.load()
+        self.pieces = lib.moe_grad_table_pieces(entries, len(entries))
+        if self.pieces < 0:
+            raise ValueError("invalid gradient tensors")
+        size = ctypes.sizeof(_lib.GradTensor)
+        host = torch.empty(max(1, self.pieces) * size, dtype=torch.uint8)
+        _lib.call("moe_grad_table_fill", entries, len(entries), host.data_ptr(), self.pieces)
+        self.table = host.to(dev)
+        with torch.cuda.device(dev):  # sized for this device's SM count
+            self.workspace_bytes = lib.moe_grad_norm_workspace_size()
+
+
+def moe_grad_set(grads: Sequence[torch.Tensor], outs: Sequence[torch.Tensor] | None = None) -> GradSet:
+    """The handle for moe_grad_norm and moe_clip_grads (fp32 and bf16 tensors may be mixed)."""
+    return GradSet(grads, outs)
+
+
+def _grad_args(grads, norm, workspace):
+    s = grads if isinstance(grads, GradSet) else GradSet(grads)
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=s.device)
+    _need(norm, torch.float32, "norm", s.device)
+    if norm.numel() != 1:
+        raise ValueError("norm must have one element, has %d" % norm.numel())
+    ws = workspace
+    if ws is None:
+        ws = torch.empty(s.workspace_bytes, dtype=torch.uint8, device=s.device)
+    _need(ws, torch.uint8, "workspace", s.device)
+    return s, norm, ws
+
+
+def moe_grad_norm(grads: GradSet | Sequence[torch.Tensor], norm: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """2-norm over all elements of all gradients, fp32 on the device."""
+    s, norm, ws = _grad_args(grads, norm, workspace)
+    _lib.call("moe_grad_norm", _ptr(s.table), s.pieces, _ptr(norm), _ptr(ws), ws.numel(), _stream(s.table))
+    return norm
+
+
+def moe_clip_grads(grads: GradSet | Sequence[torch.Tensor], max_norm: float, norm: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Scales the gradients by min(1, max_norm / (norm + 1e-6)), into the
+    set's outs or in place, and returns their norm before that."""
+    s, norm, ws = _grad_args(grads, norm, workspace)
+    _lib.call("moe_clip_grads", _ptr(s.table), s.pieces, max_norm, _ptr(norm), _ptr(ws), ws.numel(), _stream(s.table))
+    return norm
