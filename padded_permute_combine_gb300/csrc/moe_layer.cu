@@ -13,6 +13,9 @@
 // spares a launch.
 #include <math.h>
 
+#include <atomic>
+
+#include "bulk.cuh"
 #include "common.cuh"
 #include "moe_block.h"
 #include "vec_math.cuh"
@@ -67,7 +70,7 @@ __device__ __forceinline__ Segments sort_choices(const int32_t* __restrict__ top
     __syncwarp();
     for (int i0 = 0; i0 < n; i0 += kWarp) {
       const int i = i0 + lane;
-      int e = i < n ? top_expert[i] : -1;
+      int e = i < n ? __ldcg(top_expert + i) : -1;
       if (e < -1 || e >= E) {
         if (blockIdx.x == 0) flag_status(status, MOE_STATUS_BAD_EXPERT);
         e = -1;
@@ -104,7 +107,7 @@ __device__ __forceinline__ Segments sort_choices(const int32_t* __restrict__ top
     }
     __syncwarp();
     for (int i = lane; i < n; i += kWarp) {
-      const int e = top_expert[i];
+      const int e = __ldcg(top_expert + i);
       if (e >= 0 && e < E) s.order[count[e] + local[i]] = i;
     }
   }
@@ -270,20 +273,443 @@ template <int VB, typename ET> __global__ void __launch_bounds__(kThreads) down_
   }
 }
 
+// ------------------------------------------------- bf16 rows of 16 bytes
+//
+// Weights stream through a ring of shared-memory stages, filled row by row
+// with bulk copies by one producer warp and multiplied by eight consumer warps
+// with m16n8k16 tensor instructions: 16 weight rows by 8 tokens, an expert's
+// tokens in up to NT such tiles. With few tokens the time is that of the
+// weight bytes, so what matters is that copies are always in flight: the
+// producer runs ahead of the consumers across tiles, rows and experts, and
+// the work is cut so that each of the SMs streams the same number of bytes (an
+// equal share of the active experts' F gate/up row pairs; an equal share of
+// y's H columns for all experts), whatever the sizes.
+//
+// A stage holds kc elements of each row of the tile, weights first, then the
+// tokens', rows 2*KC + 64 bytes apart: lanes of a tile read 16 bytes each of
+// 8 rows by 4 places, two rows per 128-byte wavefront, without conflicts. A
+// 16-byte piece feeds two instructions; that pairs k's in another order than
+// the instruction's own, on both sides alike, which a dot product does not
+// see. The warps share a stage's tile: MT tiles of 16 rows by KS slices of kc,
+// and add their sums in shared memory at the tile's end, in a fixed order.
+
+constexpr int kConsumers = 8;
+constexpr int kStreamThreads = (kConsumers + 1) * kWarp;
+constexpr int kStages = 3;
+
+// Element steps of a stage: a multiple of 32 for each of the KS warps.
+__host__ __device__ constexpr int k_slices(int MT) { return MT == 4 ? 2 : 4; }
+__host__ __device__ constexpr int quantum(int MT) { return 32 * k_slices(MT); }
+// Elements of each row that a stage takes when the tile has `rows` rows.
+__host__ __device__ inline int stage_elems(int stage_bytes, int rows, int q, int K) {
+  const int fit = (stage_bytes / rows - 64) / 2 / q * q, all = (K + q - 1) / q * q;
+  return fit < all ? fit : all;
+}
+
+__device__ __forceinline__ void mbar_init_count(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// Lets the next kernel on the stream start while this one runs.
+__device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+__device__ __forceinline__ uint4 lds16(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
+  return v;
+}
+// d += A (16 rows x 16) * B (16 x 8), bf16 operands, fp32 sums.
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The ring's barriers and where one side stands in it.
+struct Ring {
+  uint32_t data, full, empty;  // shared-memory addresses
+  int stage_bytes;
+  int stage;
+  uint32_t parity;
+  bool ok;  // false after a wait gave up: nothing is waited for or copied any more
+  __device__ __forceinline__ uint32_t at() const { return data + stage * stage_bytes; }
+  // By a whole warp; bounded.
+  __device__ __forceinline__ void wait(uint32_t bars, int32_t* status) {
+    if (!ok) return;
+    ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * stage, parity));
+    if (!ok && lane_id() == 0) flag_status(status, MOE_STATUS_TIMEOUT);
+  }
+  __device__ __forceinline__ void advance() {
+    if (++stage == kStages) {
+      stage = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+__device__ __forceinline__ Ring make_ring(uint32_t data, uint32_t bars, int stage_bytes, bool producer) {
+  // The producer's first wait on each stage passes: a fresh barrier counts as one phase done.
+  return Ring{data, bars, bars + 8 * kStages, stage_bytes, 0, producer ? 1u : 0u, true};
+}
+__device__ __forceinline__ void init_ring(uint32_t bars) {
+  for (int i = 0; i < kStages; ++i) {
+    mbar_init(bars + 8 * i);
+    mbar_init_count(bars + 8 * (kStages + i), kConsumers);
+  }
+  fence_mbarrier_init();
+}
+
+// Adds one stage's products to acc: this warp's slice of the kc elements, its
+// 16 weight rows starting at row0 (rows at or beyond `rows` repeat the last)
+// and the tokens' rows from tok0 on. PARTS 2: the tokens' rows are held as the
+// sum of two bf16 numbers, the second ntok rows after the first.
+template <int NT, int PARTS>
+__device__ __forceinline__ void multiply_stage(float (&acc)[NT][4], uint32_t stage, int stride, int kc, int k_begin,
+                                               int k_end, int row0, int rows, int tok0, int ntok) {
+  const int lane = lane_id(), g = lane >> 2, c = (lane & 3) * 8;
+  const uint32_t a0p = stage + (uint32_t)(row0 + (g < rows ? g : rows - 1)) * stride;
+  const uint32_t a1p = stage + (uint32_t)(row0 + (g + 8 < rows ? g + 8 : rows - 1)) * stride;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const int end = k_end < kc ? k_end : kc;
+  for (int k = k_begin; k < end; k += 32) {
+    const bool in = k + c < kc;
+    const uint32_t off = (uint32_t)(k + c) * 2;
+    const uint4 a0 = in ? lds16(a0p + off) : zero, a1 = in ? lds16(a1p + off) : zero;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      if (j * 8 >= ntok) break;
+      const int t = j * 8 + g < ntok ? j * 8 + g : ntok - 1;
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) {
+        const uint4 b = in ? lds16(stage + (uint32_t)(tok0 + p * ntok + t) * stride + off) : zero;
+        mma16(acc[j], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
+        mma16(acc[j], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+      }
+    }
+  }
+}
+
+// A warp's 16 x 8 sums, row-major, for the threads that add the KS slices.
+__device__ __forceinline__ void put_tile(float* red, const float (&acc)[4]) {
+  const int lane = lane_id();
+  float* p = red + (lane >> 2) * 8 + (lane & 3) * 2;
+  p[0] = acc[0];
+  p[1] = acc[1];
+  p[64] = acc[2];
+  p[65] = acc[3];
+}
+
+struct StreamArgs {
+  LayerArgs a;
+  __nv_bfloat16* h_hi;  // [n, F] in sorted order: h = h_hi + h_lo
+  __nv_bfloat16* h_lo;
+  int stage_bytes;
+};
+
+// Tiles of up to 16 row pairs (gate, up) of one expert by up to NT * 8 of its
+// tokens, over the whole of H.
+struct GateUpWalk {
+  const Segments& s;
+  int64_t pos, end, F;
+  int q, nf, i0, ntok, K, KC, k0, kc, stage_bytes, per_pass;
+  int64_t f0;
+  __device__ GateUpWalk(const Segments& s_, const StreamArgs& p, int per_pass_)
+      : s(s_), F(p.a.F), K((int)p.a.H), stage_bytes(p.stage_bytes), per_pass(per_pass_) {
+    const int64_t rows = s.active * F;
+    pos = rows * blockIdx.x / gridDim.x;
+    end = rows * (blockIdx.x + 1) / gridDim.x;
+    if (pos < end) tile();
+  }
+  __device__ __forceinline__ bool more() const { return pos < end; }
+  __device__ __forceinline__ void tile() {
+    q = (int)(pos / F);
+    f0 = pos - q * F;
+    int64_t m = end - pos < F - f0 ? end - pos : F - f0;
+    nf = m < 16 ? (int)m : 16;
+    i0 = s.begin[q];
+    pass();
+  }
+  __device__ __forceinline__ void pass() {
+    const int left = s.begin[q + 1] - i0;
+    ntok = left < per_pass ? left : per_pass;
+    KC = stage_elems(stage_bytes, 2 * nf + ntok, quantum(2), K);
+    k0 = 0;
+    kc = K < KC ? K : KC;
+  }
+  __device__ __forceinline__ bool last_stage() const { return k0 + KC >= K; }
+  __device__ __forceinline__ void next() {
+    k0 += KC;
+    if (k0 < K) {
+      kc = K - k0 < KC ? K - k0 : KC;
+      return;
+    }
+    i0 += ntok;
+    if (i0 < s.begin[q + 1]) return pass();
+    pos += nf;
+    if (pos < end) tile();
+  }
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1) gate_up_stream_kernel(StreamArgs p) {
+  extern __shared__ __align__(128) unsigned char dyn[];
+  __shared__ uint64_t bars[2 * kStages];
+  __shared__ float red[kConsumers * 128];
+  const LayerArgs& a = p.a;
+  await_previous_kernel();
+  if (threadIdx.x == kStreamThreads - 1) init_ring(smem_u32(bars));
+  const Segments s = sort_choices(a.top_expert, a.n, a.E, a.status,
+                                  reinterpret_cast<int32_t*>(dyn + (size_t)kStages * p.stage_bytes));
+  allow_next_kernel();
+  const int warp = threadIdx.x / kWarp, lane = lane_id();
+  GateUpWalk w(s, p, NT * 8);
+  Ring r = make_ring(smem_u32(dyn), smem_u32(bars), p.stage_bytes, warp == kConsumers);
+  if (warp == kConsumers) {
+    const uint64_t once = l2_policy_evict_first();
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x);
+    const __nv_bfloat16* wt = static_cast<const __nv_bfloat16*>(a.w_gate_up);
+    for (; w.more() && r.ok; w.next(), r.advance()) {
+      r.wait(r.empty, a.status);
+      if (!r.ok) break;
+      const int rows = 2 * w.nf + w.ntok, stride = 2 * w.KC + 64;
+      const uint32_t bar = r.full + 8 * r.stage, dst = r.at();
+      if (lane == 0) mbar_expect(bar, (uint32_t)rows * w.kc * 2);
+      __syncwarp();
+      const __nv_bfloat16* gate = wt + ((int64_t)s.expert[w.q] * 2 * a.F + w.f0) * a.H + w.k0;
+      for (int i = lane; i < rows; i += kWarp) {
+        if (i < 2 * w.nf) {
+          const __nv_bfloat16* src = gate + (i < w.nf ? i : a.F + i - w.nf) * a.H;
+          bulk_copy_in(dst + i * stride, src, w.kc * 2, bar, once);
+        } else {
+          const int t = s.order[w.i0 + i - 2 * w.nf] / a.K;
+          bulk_copy_in(dst + i * stride, x + t * a.x_stride + w.k0, w.kc * 2, bar);
+        }
+      }
+    }
+    return;
+  }
+  // Warps 0..3: slices of the gate rows; 4..7: of the up rows.
+  constexpr int KS = k_slices(2);
+  const int mt = warp / KS, ks = warp % KS;
+  while (w.more()) {
+    float acc[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+    const int nf = w.nf, i0 = w.i0, ntok = w.ntok;
+    const int64_t f0 = w.f0;
+    for (bool last = false; !last; w.next(), r.advance()) {
+      last = w.last_stage();
+      r.wait(r.full, a.status);
+      const int part = w.KC / KS;
+      if (r.ok)
+        multiply_stage<NT, 1>(acc, r.at(), 2 * w.KC + 64, w.kc, ks * part, (ks + 1) * part, mt * nf, nf, 2 * nf, ntok);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(r.empty + 8 * r.stage);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      if (j * 8 >= ntok) break;
+      put_tile(red + warp * 128, acc[j]);
+      consumers_sync();
+      const int f = threadIdx.x & 15, c = threadIdx.x >> 4;
+      if (threadIdx.x < 128 && f < nf && j * 8 + c < ntok) {
+        float g = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          g += red[k * 128 + f * 8 + c];
+          u += red[(KS + k) * 128 + f * 8 + c];
+        }
+        const int i = i0 + j * 8 + c;
+        const float h = __ldcg(a.weights + s.order[i]) * (silu(g) * u);
+        // Two bf16 numbers keep 16 significant bits of h: one would round the layer's result twice.
+        const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+        const float rest = h - __bfloat162float(hi);
+        const int64_t at = i * a.F + f0 + f;
+        p.h_hi[at] = hi;
+        p.h_lo[at] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
+      }
+      consumers_sync();
+    }
+  }
+}
+
+// y's columns [r0, r0 + nr) for one expert's tokens after another, over the whole of F.
+template <int MT> struct DownWalk {
+  const Segments& s;
+  int64_t r0, end;
+  int nr, q, i0, ntok, K, KC, k0, kc, stage_bytes, per_pass;
+  __device__ DownWalk(const Segments& s_, const StreamArgs& p, int per_pass_)
+      : s(s_), K((int)p.a.F), stage_bytes(p.stage_bytes), per_pass(per_pass_) {
+    r0 = p.a.H * blockIdx.x / gridDim.x;
+    end = p.a.H * (blockIdx.x + 1) / gridDim.x;
+    if (s.active == 0) r0 = end;
+    if (more()) tile();
+  }
+  __device__ __forceinline__ bool more() const { return r0 < end; }
+  __device__ __forceinline__ void tile() {
+    nr = end - r0 < 16 * MT ? (int)(end - r0) : 16 * MT;
+    q = 0;
+    i0 = 0;
+    pass();
+  }
+  __device__ __forceinline__ void pass() {
+    const int left = s.begin[q + 1] - i0;
+    ntok = left < per_pass ? left : per_pass;
+    KC = stage_elems(stage_bytes, nr + 2 * ntok, quantum(MT), K);
+    k0 = 0;
+    kc = K < KC ? K : KC;
+  }
+  __device__ __forceinline__ bool last_stage() const { return k0 + KC >= K; }
+  __device__ __forceinline__ void next() {
+    k0 += KC;
+    if (k0 < K) {
+      kc = K - k0 < KC ? K - k0 : KC;
+      return;
+    }
+    i0 += ntok;
+    if (i0 < s.begin[q + 1]) return pass();
+    if (++q < s.active) return pass();
+    r0 += nr;
+    if (r0 < end) tile();
+  }
+};
+
+template <int NT, int MT>
+__global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1) down_stream_kernel(StreamArgs p) {
+  extern __shared__ __align__(128) unsigned char dyn[];
+  __shared__ uint64_t bars[2 * kStages];
+  __shared__ float red[kConsumers * 128];
+  const LayerArgs& a = p.a;
+  // The gate/up kernel has waited for all before it, so the routing may be
+  // read and weights copied while it still runs; h may not.
+  if (threadIdx.x == kStreamThreads - 1) init_ring(smem_u32(bars));
+  int32_t* seg = reinterpret_cast<int32_t*>(dyn + (size_t)kStages * p.stage_bytes);
+  const Segments s = sort_choices(a.top_expert, a.n, a.E, nullptr, seg);
+  float* ysum = reinterpret_cast<float*>(seg + segments_bytes(a.n, a.E) / sizeof(int32_t));  // [T, nr]
+  const int warp = threadIdx.x / kWarp, lane = lane_id();
+  DownWalk<MT> w(s, p, NT * 8);
+  Ring r = make_ring(smem_u32(dyn), smem_u32(bars), p.stage_bytes, warp == kConsumers);
+  if (warp == kConsumers) {
+    const uint64_t once = l2_policy_evict_first();
+    const __nv_bfloat16* wt = static_cast<const __nv_bfloat16*>(a.w_down);
+    auto weights = [&](const DownWalk<MT>& v, uint32_t bar, uint32_t dst) {
+      const int stride = 2 * v.KC + 64;
+      if (lane == 0) mbar_expect(bar, (uint32_t)(v.nr + 2 * v.ntok) * v.kc * 2);
+      __syncwarp();
+      const __nv_bfloat16* src = wt + ((int64_t)s.expert[v.q] * a.H + v.r0) * a.F + v.k0;
+      for (int i = lane; i < v.nr; i += kWarp) bulk_copy_in(dst + i * stride, src + i * a.F, v.kc * 2, bar, once);
+    };
+    auto tokens = [&](const DownWalk<MT>& v, uint32_t bar, uint32_t dst) {
+      const int stride = 2 * v.KC + 64;
+      for (int i = lane; i < 2 * v.ntok; i += kWarp) {
+        const __nv_bfloat16* h = i < v.ntok ? p.h_hi + (v.i0 + i) * a.F : p.h_lo + (v.i0 + i - v.ntok) * a.F;
+        bulk_copy_in(dst + (v.nr + i) * stride, h + v.k0, v.kc * 2, bar);
+      }
+    };
+    DownWalk<MT> first = w;
+    int ahead = 0;
+    for (; ahead < kStages && w.more(); ++ahead, w.next()) weights(w, r.full + 8 * ahead, r.data + ahead * r.stage_bytes);
+    await_previous_kernel();
+    fence_async_all();  // h was written by ordinary stores
+    for (int i = 0; i < ahead; ++i, first.next(), r.advance()) tokens(first, r.full + 8 * i, r.data + i * r.stage_bytes);
+    for (; w.more(); w.next(), r.advance()) {
+      r.wait(r.empty, a.status);
+      if (!r.ok) break;
+      weights(w, r.full + 8 * r.stage, r.at());
+      tokens(w, r.full + 8 * r.stage, r.at());
+    }
+    return;
+  }
+  constexpr int KS = k_slices(MT);
+  const int mt = warp / KS, ks = warp % KS;
+  int64_t r0 = a.H * blockIdx.x / gridDim.x;
+  const int64_t r_end = a.H * (blockIdx.x + 1) / gridDim.x;
+  for (; r0 < r_end; r0 += 16 * MT) {
+    const int nr = r_end - r0 < 16 * MT ? (int)(r_end - r0) : 16 * MT;
+    for (int i = threadIdx.x; i < a.T * nr; i += kConsumers * kWarp) ysum[i] = 0.0f;
+    float acc[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+    while (w.more() && w.r0 == r0) {
+      const int i0 = w.i0, ntok = w.ntok;
+      for (bool last = false; !last; w.next(), r.advance()) {
+        last = w.last_stage();
+        r.wait(r.full, a.status);
+        const int part = w.KC / KS, rows = nr - mt * 16;
+        if (r.ok && mt < MT && rows > 0)
+          multiply_stage<NT, 2>(acc, r.at(), 2 * w.KC + 64, w.kc, ks * part, (ks + 1) * part, mt * 16, rows, nr, ntok);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(r.empty + 8 * r.stage);
+      }
+      // One token's experts one after another need no sum in between.
+      if (ntok == 1 && w.more() && w.r0 == r0 && w.ntok == 1 && s.order[w.i0] / a.K == s.order[i0] / a.K) continue;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if (j * 8 >= ntok) break;
+        consumers_sync();  // the last tile's sums (or the zeros above) are done with
+        if (mt < MT) put_tile(red + warp * 128, acc[j]);
+        acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+        consumers_sync();
+        for (int i = threadIdx.x; i < MT * 128; i += kConsumers * kWarp) {
+          const int row = (i >> 7) * 16 + ((i & 127) >> 3), c = i & 7;
+          if (row >= nr || j * 8 + c >= ntok) continue;
+          const int* o = s.order + i0 + j * 8;
+          const int t = o[c] / a.K;
+          if (c > 0 && o[c - 1] / a.K == t) continue;  // a token that chose an expert twice: its first column adds both
+          float sum = ysum[t * nr + row];
+          for (int c2 = c; c2 < 8 && j * 8 + c2 < ntok && o[c2] / a.K == t; ++c2) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k) sum += red[((i >> 7) * KS + k) * 128 + (i & 127) + c2 - c];
+          }
+          ysum[t * nr + row] = sum;
+        }
+      }
+    }
+    consumers_sync();
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + r0;
+    for (int i = threadIdx.x; i < a.T * nr; i += kConsumers * kWarp) {
+      const int t = i / nr, row = i - t * nr;
+      y[t * a.H + row] = __float2bfloat16_rn(ysum[i]);
+    }
+    consumers_sync();
+  }
+}
+
+// Raises a kernel's dynamic shared memory limit once per device.
+template <typename Kernel> bool allow_smem(Kernel k, int bytes, std::atomic<int>* granted) {
+  int dev = 0;
+  (void)cudaGetDevice(&dev);
+  const bool cached = dev >= 0 && dev < 64;
+  if (cached && granted[dev].load(std::memory_order_relaxed) >= bytes) return true;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return false;
+  }
+  if (cached) granted[dev].store(bytes, std::memory_order_relaxed);
+  return true;
+}
+
 // ------------------------------------------------------------------ host
 
 template <int VB, typename ET>
-int run_rows(const LayerArgs& a, const void* router, float* logits, int32_t mode, int32_t normalize,
-             int32_t* top_expert, float* weights, cudaStream_t s) {
-  if (router != nullptr) {
-    auto k = router_rows_kernel<VB, ET>;
-    const int64_t warps = (int64_t)((a.T + kCols - 1) / kCols) * a.E;
-    launch(k, persistent_grid(k, kThreads, 0, (warps + kWarps - 1) / kWarps), kThreads, 0, s, a.x, a.x_stride, router,
-           a.H, a.T, a.E, logits);
-    const int rc = moe_topk_gating(logits, a.T, a.E, a.K, mode, normalize, top_expert, weights,
-                                   reinterpret_cast<moe_stream_t>(s));
-    if (rc != MOE_OK) return rc;
-  }
+int run_router(const LayerArgs& a, const void* router, float* logits, int32_t mode, int32_t normalize,
+               int32_t* top_expert, float* weights, cudaStream_t s) {
+  if (router == nullptr) return MOE_OK;
+  auto k = router_rows_kernel<VB, ET>;
+  const int64_t warps = (int64_t)((a.T + kCols - 1) / kCols) * a.E;
+  launch(k, persistent_grid(k, kThreads, 0, (warps + kWarps - 1) / kWarps), kThreads, 0, s, a.x, a.x_stride, router,
+         a.H, a.T, a.E, logits);
+  return moe_topk_gating(logits, a.T, a.E, a.K, mode, normalize, top_expert, weights,
+                         reinterpret_cast<moe_stream_t>(s));
+}
+
+template <int VB, typename ET> int run_rows(const LayerArgs& a, cudaStream_t s) {
   const size_t seg = segments_bytes(a.n, a.E);
   auto g = gate_up_rows_kernel<VB, ET>;
   launch(g, persistent_grid(g, kThreads, seg, ((a.n < a.E ? a.n : a.E) * a.F + kWarps - 1) / kWarps), kThreads, seg, s, a);
@@ -293,14 +719,61 @@ int run_rows(const LayerArgs& a, const void* router, float* logits, int32_t mode
   return check_launch();
 }
 
+
+template <int NT, int MT> int launch_stream(const StreamArgs& p, size_t seg, size_t ysum, cudaStream_t s) {
+  static std::atomic<int> granted_g[64], granted_d[64];
+  auto g = gate_up_stream_kernel<NT>;
+  auto d = down_stream_kernel<NT, MT>;
+  const size_t ring = (size_t)kStages * p.stage_bytes;
+  if (!allow_smem(g, (int)(ring + seg), granted_g) || !allow_smem(d, (int)(ring + seg + ysum), granted_d))
+    return MOE_ERR_CUDA;
+  const int64_t pairs = (p.a.n < p.a.E ? p.a.n : p.a.E) * p.a.F, sms = num_sms();
+  launch(g, (unsigned)(pairs < sms ? pairs : sms), kStreamThreads, ring + seg, s, p);
+  launch(d, (unsigned)(p.a.H < sms ? p.a.H : sms), kStreamThreads, ring + seg + ysum, s, p);
+  return check_launch();
+}
+
+template <int NT> int dispatch_stream(StreamArgs p, cudaStream_t s) {
+  const int64_t sms = num_sms();
+  const int64_t per_cta = (p.a.H + sms - 1) / sms;
+  const int MT = per_cta <= 16 ? 1 : (per_cta <= 32 ? 2 : 4);
+  const size_t seg = segments_bytes(p.a.n, p.a.E);
+  const size_t ysum = sizeof(float) * p.a.T * (per_cta < 16 * MT ? per_cta : 16 * MT);
+  // Up to 16 tokens: stages such that a CTA of each kernel fits on an SM
+  // together, so that the second kernel's first copies overlap the first's
+  // end. Beyond: as large as fit, for the tokens' rows beside the weights'.
+  p.stage_bytes = NT <= 2 ? 35968 : (int)((221184 - seg - ysum) / kStages / 128 * 128);
+  if (p.stage_bytes > 65536) p.stage_bytes = 65536;
+  switch (MT) {
+    case 1: return launch_stream<NT, 1>(p, seg, ysum, s);
+    case 2: return launch_stream<NT, 2>(p, seg, ysum, s);
+    default: return launch_stream<NT, 4>(p, seg, ysum, s);
+  }
+}
+
+int run_stream(const LayerArgs& a, cudaStream_t s) {
+  __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(a.h);
+  const StreamArgs p{a, h, h + (int64_t)a.n * a.F, 0};
+  if (a.T <= 8) return dispatch_stream<1>(p, s);
+  if (a.T <= 16) return dispatch_stream<2>(p, s);
+  if (a.T <= 32) return dispatch_stream<4>(p, s);
+  return dispatch_stream<8>(p, s);
+}
+
 template <typename ET>
 int dispatch(const LayerArgs& a, const void* router, float* logits, int32_t mode, int32_t normalize,
              int32_t* top_expert, float* weights, cudaStream_t s) {
   constexpr int kE = 16 / Elem<ET>::kBytes;
   const bool by16 = a.H % kE == 0 && a.F % kE == 0 && a.x_stride % kE == 0 && aligned(a.x, 16) &&
                     aligned(a.w_gate_up, 16) && aligned(a.w_down, 16) && aligned(router, 16);
-  if (by16) return run_rows<16, ET>(a, router, logits, mode, normalize, top_expert, weights, s);
-  return run_rows<Elem<ET>::kBytes, ET>(a, router, logits, mode, normalize, top_expert, weights, s);
+  const int rc = by16 ? run_router<16, ET>(a, router, logits, mode, normalize, top_expert, weights, s)
+                      : run_router<Elem<ET>::kBytes, ET>(a, router, logits, mode, normalize, top_expert, weights, s);
+  if (rc != MOE_OK) return rc;
+  if (!by16) return run_rows<Elem<ET>::kBytes, ET>(a, s);
+  if constexpr (Elem<ET>::kBytes == 2)
+    return run_stream(a, s);
+  else
+    return run_rows<16, ET>(a, s);
 }
 
 // Bytes of the workspace's parts: the logits, then h.
