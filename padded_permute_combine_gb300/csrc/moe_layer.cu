@@ -39,10 +39,11 @@ struct LayerArgs {
 // ------------------------------------------------------- choices by expert
 
 // The choices sorted by expert (stable), in dynamic shared memory:
-// order[i]: assignment at sorted place i; the active experts, and where each
-// begins in order.
+// order[i] and token[i]: assignment at sorted place i and its token; the
+// active experts, and where each begins in order.
 struct Segments {
   int32_t* order;   // [n]
+  int32_t* token;   // [n]
   int32_t* expert;  // [min(n, E)]
   int32_t* begin;   // [min(n, E) + 1]
   int32_t active;
@@ -50,16 +51,17 @@ struct Segments {
 
 __host__ __device__ inline size_t segments_bytes(int32_t n, int32_t E) {
   const int m = n < E ? n : E;
-  return sizeof(int32_t) * ((size_t)2 * n + E + 2 * m + 2);
+  return sizeof(int32_t) * ((size_t)3 * n + E + 2 * m + 2);
 }
 
 // Called by the whole CTA; warp 0 does the work.
-__device__ __forceinline__ Segments sort_choices(const int32_t* __restrict__ top_expert, int32_t n, int32_t E,
+__device__ __forceinline__ Segments sort_choices(const int32_t* __restrict__ top_expert, int32_t n, int32_t E, int32_t K,
                                                  int32_t* status, int32_t* smem) {
   const int m = n < E ? n : E;
   Segments s;
   s.order = smem;
-  int32_t* local = smem + n;   // rank of an assignment within its expert
+  s.token = smem + n;
+  int32_t* local = s.token + n;  // rank of an assignment within its expert
   int32_t* count = local + n;  // [E]: choices of the expert, then where they begin
   s.expert = count + E;
   s.begin = s.expert + m;
@@ -108,7 +110,10 @@ __device__ __forceinline__ Segments sort_choices(const int32_t* __restrict__ top
     __syncwarp();
     for (int i = lane; i < n; i += kWarp) {
       const int e = __ldcg(top_expert + i);
-      if (e >= 0 && e < E) s.order[count[e] + local[i]] = i;
+      if (e < 0 || e >= E) continue;
+      const int at = count[e] + local[i];
+      s.order[at] = i;
+      s.token[at] = i / K;
     }
   }
   __syncthreads();
@@ -179,7 +184,7 @@ template <int VB, typename ET> __global__ void __launch_bounds__(kThreads) gate_
   using V = typename L::V;
   extern __shared__ int32_t smem[];
   await_previous_kernel();
-  const Segments s = sort_choices(a.top_expert, a.n, a.E, a.status, smem);
+  const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, a.status, smem);
   const int lane = lane_id();
   const int64_t vecs = a.H / L::kElems;
   for (int64_t w = (int64_t)blockIdx.x * kWarps + threadIdx.x / kWarp; w < s.active * a.F;
@@ -195,7 +200,7 @@ template <int VB, typename ET> __global__ void __launch_bounds__(kThreads) gate_
       float g[kCols], u[kCols];
 #pragma unroll
       for (int c = 0; c < kCols; ++c) {
-        const int t = s.order[i0 + c < last ? i0 + c : last] / a.K;
+        const int t = s.token[i0 + c < last ? i0 + c : last];
         px[c] = reinterpret_cast<const V*>(static_cast<const ET*>(a.x) + t * a.x_stride);
         g[c] = u[c] = 0.0f;
       }
@@ -226,7 +231,7 @@ template <int VB, typename ET> __global__ void __launch_bounds__(kThreads) down_
   using V = typename L::V;
   extern __shared__ int32_t smem[];
   await_previous_kernel();
-  const Segments s = sort_choices(a.top_expert, a.n, a.E, a.status, smem);
+  const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, a.status, smem);
   const int lane = lane_id();
   // This warp's row of y for every token.
   float* sum = reinterpret_cast<float*>(smem + segments_bytes(a.n, a.E) / sizeof(int32_t)) +
@@ -258,7 +263,7 @@ template <int VB, typename ET> __global__ void __launch_bounds__(kThreads) down_
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
           const float v = warp_sum(acc[c]);
-          if (lane == 0 && i0 + c <= last) sum[s.order[i0 + c] / a.K] += v;
+          if (lane == 0 && i0 + c <= last) sum[s.token[i0 + c]] += v;
         }
       }
     }
@@ -275,12 +280,14 @@ template <int VB, typename ET> __global__ void __launch_bounds__(kThreads) down_
 
 // ------------------------------------------------- bf16 rows of 16 bytes
 //
-// Weights stream through a ring of shared-memory stages, filled row by row
-// with bulk copies by one producer warp and multiplied by eight consumer warps
-// with m16n8k16 tensor instructions: 16 weight rows by 8 tokens, an expert's
-// tokens in up to NT such tiles. With few tokens the time is that of the
-// weight bytes, so what matters is that copies are always in flight: the
-// producer runs ahead of the consumers across tiles, rows and experts, and
+// Weights stream through a ring of shared-memory stages, filled with 16-byte
+// asynchronous copies by four producer warps and multiplied by eight consumer
+// warps with m16n8k16 tensor instructions: 16 weight rows by 8 tokens, an
+// expert's tokens in up to NT such tiles. (Bulk copies of a row's piece were
+// slower: an SM starts one in 34 ns whatever its size, 30 bytes/ns at the 1 KB
+// that a stage has room for, against the 45 that the memory delivers.)
+// With few tokens the time is that of the weight bytes, so what matters is
+// that copies are always in flight: the producers run ahead of the consumers across tiles, rows and experts, and
 // the work is cut so that each of the SMs streams the same number of bytes (an
 // equal share of the active experts' F gate/up row pairs; an equal share of
 // y's H columns for all experts), whatever the sizes.
@@ -294,13 +301,15 @@ template <int VB, typename ET> __global__ void __launch_bounds__(kThreads) down_
 // and add their sums in shared memory at the tile's end, in a fixed order.
 
 constexpr int kConsumers = 8;
-constexpr int kStreamThreads = (kConsumers + 1) * kWarp;
+constexpr int kProducers = 4;
+constexpr int kStreamThreads = (kConsumers + kProducers) * kWarp;
 constexpr int kStages = 3;
 
 // Element steps of a stage: a multiple of 32 for each of the KS warps.
 __host__ __device__ constexpr int k_slices(int MT) { return MT == 4 ? 2 : 4; }
 __host__ __device__ constexpr int quantum(int MT) { return 32 * k_slices(MT); }
-// Elements of each row that a stage takes when the tile has `rows` rows.
+// Elements of each row that a stage takes when the tile has `rows` rows (not
+// 0: the host chooses stages that hold a tile's rows).
 __host__ __device__ inline int stage_elems(int stage_bytes, int rows, int q, int K) {
   const int fit = (stage_bytes / rows - 64) / 2 / q * q, all = (K + q - 1) / q * q;
   return fit < all ? fit : all;
@@ -315,7 +324,27 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 // Lets the next kernel on the stream start while this one runs.
 __device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void fence_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// 16 bytes from global to shared memory, not through L1.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The thread's arrival on the barrier, once all its copies so far have landed.
+__device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// A producer warp's share of `rows` rows, ld elements apart, to stage rows
+// `stride` bytes apart: every kProducers-th row, kc elements each.
+__device__ __forceinline__ void copy_rows(uint32_t dst, int stride, const __nv_bfloat16* src, int64_t ld, int rows, int kc) {
+  const int first = (int)threadIdx.x / kWarp - kConsumers, lane = lane_id();
+  const int64_t step = kProducers * ld;
+  for (int c = lane * 8; c < kc; c += kWarp * 8) {
+    const __nv_bfloat16* p = src + first * ld + c;
+    uint32_t d = dst + first * stride + c * 2;
+#pragma unroll 4
+    for (int i = first; i < rows; i += kProducers, p += step, d += kProducers * stride) copy16(d, p);
+  }
+}
 
 __device__ __forceinline__ uint4 lds16(uint32_t p) {
   uint4 v;
@@ -359,7 +388,7 @@ __device__ __forceinline__ Ring make_ring(uint32_t data, uint32_t bars, int stag
 }
 __device__ __forceinline__ void init_ring(uint32_t bars) {
   for (int i = 0; i < kStages; ++i) {
-    mbar_init(bars + 8 * i);
+    mbar_init_count(bars + 8 * i, kProducers * kWarp);
     mbar_init_count(bars + 8 * (kStages + i), kConsumers);
   }
   fence_mbarrier_init();
@@ -410,6 +439,7 @@ struct StreamArgs {
   __nv_bfloat16* h_hi;  // [n, F] in sorted order: h = h_hi + h_lo
   __nv_bfloat16* h_lo;
   int stage_bytes;
+  int gate_tokens, down_tokens;  // of an expert at a time: NT * 8, or fewer where a stage would not hold their rows
 };
 
 // Tiles of up to 16 row pairs (gate, up) of one expert by up to NT * 8 of its
@@ -464,33 +494,30 @@ __global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1) gate_up_strea
   const LayerArgs& a = p.a;
   await_previous_kernel();
   if (threadIdx.x == kStreamThreads - 1) init_ring(smem_u32(bars));
-  const Segments s = sort_choices(a.top_expert, a.n, a.E, a.status,
+  const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, a.status,
                                   reinterpret_cast<int32_t*>(dyn + (size_t)kStages * p.stage_bytes));
   allow_next_kernel();
   const int warp = threadIdx.x / kWarp, lane = lane_id();
-  GateUpWalk w(s, p, NT * 8);
-  Ring r = make_ring(smem_u32(dyn), smem_u32(bars), p.stage_bytes, warp == kConsumers);
-  if (warp == kConsumers) {
-    const uint64_t once = l2_policy_evict_first();
+  GateUpWalk w(s, p, p.gate_tokens);
+  Ring r = make_ring(smem_u32(dyn), smem_u32(bars), p.stage_bytes, warp >= kConsumers);
+  if (warp >= kConsumers) {
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x);
     const __nv_bfloat16* wt = static_cast<const __nv_bfloat16*>(a.w_gate_up);
-    for (; w.more() && r.ok; w.next(), r.advance()) {
+    for (; w.more(); w.next(), r.advance()) {
       r.wait(r.empty, a.status);
       if (!r.ok) break;
-      const int rows = 2 * w.nf + w.ntok, stride = 2 * w.KC + 64;
-      const uint32_t bar = r.full + 8 * r.stage, dst = r.at();
-      if (lane == 0) mbar_expect(bar, (uint32_t)rows * w.kc * 2);
-      __syncwarp();
+      const int stride = 2 * w.KC + 64;
+      const uint32_t dst = r.at();
       const __nv_bfloat16* gate = wt + ((int64_t)s.expert[w.q] * 2 * a.F + w.f0) * a.H + w.k0;
-      for (int i = lane; i < rows; i += kWarp) {
-        if (i < 2 * w.nf) {
-          const __nv_bfloat16* src = gate + (i < w.nf ? i : a.F + i - w.nf) * a.H;
-          bulk_copy_in(dst + i * stride, src, w.kc * 2, bar, once);
-        } else {
-          const int t = s.order[w.i0 + i - 2 * w.nf] / a.K;
-          bulk_copy_in(dst + i * stride, x + t * a.x_stride + w.k0, w.kc * 2, bar);
-        }
+      copy_rows(dst, stride, gate, a.H, w.nf, w.kc);
+      copy_rows(dst + w.nf * stride, stride, gate + a.F * a.H, a.H, w.nf, w.kc);
+      const uint32_t tok = dst + 2 * w.nf * stride;
+      for (int c = lane * 8; c < w.kc; c += kWarp * 8) {
+#pragma unroll 4
+        for (int i = warp - kConsumers; i < w.ntok; i += kProducers)
+          copy16(tok + i * stride + c * 2, x + s.token[w.i0 + i] * a.x_stride + w.k0 + c);
       }
+      arrive_after_copies(r.full + 8 * r.stage);
     }
     return;
   }
@@ -590,39 +617,36 @@ __global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1) down_stream_k
   // read and weights copied while it still runs; h may not.
   if (threadIdx.x == kStreamThreads - 1) init_ring(smem_u32(bars));
   int32_t* seg = reinterpret_cast<int32_t*>(dyn + (size_t)kStages * p.stage_bytes);
-  const Segments s = sort_choices(a.top_expert, a.n, a.E, nullptr, seg);
+  const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, nullptr, seg);
   float* ysum = reinterpret_cast<float*>(seg + segments_bytes(a.n, a.E) / sizeof(int32_t));  // [T, nr]
   const int warp = threadIdx.x / kWarp, lane = lane_id();
-  DownWalk<MT> w(s, p, NT * 8);
-  Ring r = make_ring(smem_u32(dyn), smem_u32(bars), p.stage_bytes, warp == kConsumers);
-  if (warp == kConsumers) {
-    const uint64_t once = l2_policy_evict_first();
+  DownWalk<MT> w(s, p, p.down_tokens);
+  Ring r = make_ring(smem_u32(dyn), smem_u32(bars), p.stage_bytes, warp >= kConsumers);
+  if (warp >= kConsumers) {
     const __nv_bfloat16* wt = static_cast<const __nv_bfloat16*>(a.w_down);
-    auto weights = [&](const DownWalk<MT>& v, uint32_t bar, uint32_t dst) {
-      const int stride = 2 * v.KC + 64;
-      if (lane == 0) mbar_expect(bar, (uint32_t)(v.nr + 2 * v.ntok) * v.kc * 2);
-      __syncwarp();
-      const __nv_bfloat16* src = wt + ((int64_t)s.expert[v.q] * a.H + v.r0) * a.F + v.k0;
-      for (int i = lane; i < v.nr; i += kWarp) bulk_copy_in(dst + i * stride, src + i * a.F, v.kc * 2, bar, once);
+    auto weights = [&](const DownWalk<MT>& v, uint32_t dst) {
+      copy_rows(dst, 2 * v.KC + 64, wt + ((int64_t)s.expert[v.q] * a.H + v.r0) * a.F + v.k0, a.F, v.nr, v.kc);
     };
-    auto tokens = [&](const DownWalk<MT>& v, uint32_t bar, uint32_t dst) {
+    auto tokens = [&](const DownWalk<MT>& v, uint32_t dst) {
       const int stride = 2 * v.KC + 64;
-      for (int i = lane; i < 2 * v.ntok; i += kWarp) {
-        const __nv_bfloat16* h = i < v.ntok ? p.h_hi + (v.i0 + i) * a.F : p.h_lo + (v.i0 + i - v.ntok) * a.F;
-        bulk_copy_in(dst + (v.nr + i) * stride, h + v.k0, v.kc * 2, bar);
-      }
+      const int64_t at = v.i0 * a.F + v.k0;
+      copy_rows(dst + v.nr * stride, stride, p.h_hi + at, a.F, v.ntok, v.kc);
+      copy_rows(dst + (v.nr + v.ntok) * stride, stride, p.h_lo + at, a.F, v.ntok, v.kc);
     };
     DownWalk<MT> first = w;
     int ahead = 0;
-    for (; ahead < kStages && w.more(); ++ahead, w.next()) weights(w, r.full + 8 * ahead, r.data + ahead * r.stage_bytes);
+    for (; ahead < kStages && w.more(); ++ahead, w.next()) weights(w, r.data + ahead * r.stage_bytes);
     await_previous_kernel();
-    fence_async_all();  // h was written by ordinary stores
-    for (int i = 0; i < ahead; ++i, first.next(), r.advance()) tokens(first, r.full + 8 * i, r.data + i * r.stage_bytes);
+    for (int i = 0; i < ahead; ++i, first.next(), r.advance()) {
+      tokens(first, r.at());
+      arrive_after_copies(r.full + 8 * r.stage);
+    }
     for (; w.more(); w.next(), r.advance()) {
       r.wait(r.empty, a.status);
       if (!r.ok) break;
-      weights(w, r.full + 8 * r.stage, r.at());
-      tokens(w, r.full + 8 * r.stage, r.at());
+      weights(w, r.at());
+      tokens(w, r.at());
+      arrive_after_copies(r.full + 8 * r.stage);
     }
     return;
   }
@@ -648,7 +672,7 @@ __global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1) down_stream_k
         if (lane == 0) mbar_arrive(r.empty + 8 * r.stage);
       }
       // One token's experts one after another need no sum in between.
-      if (ntok == 1 && w.more() && w.r0 == r0 && w.ntok == 1 && s.order[w.i0] / a.K == s.order[i0] / a.K) continue;
+      if (ntok == 1 && w.more() && w.r0 == r0 && w.ntok == 1 && s.token[w.i0] == s.token[i0]) continue;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         if (j * 8 >= ntok) break;
@@ -659,11 +683,11 @@ __global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1) down_stream_k
         for (int i = threadIdx.x; i < MT * 128; i += kConsumers * kWarp) {
           const int row = (i >> 7) * 16 + ((i & 127) >> 3), c = i & 7;
           if (row >= nr || j * 8 + c >= ntok) continue;
-          const int* o = s.order + i0 + j * 8;
-          const int t = o[c] / a.K;
-          if (c > 0 && o[c - 1] / a.K == t) continue;  // a token that chose an expert twice: its first column adds both
+          const int* o = s.token + i0 + j * 8;
+          const int t = o[c];
+          if (c > 0 && o[c - 1] == t) continue;  // a token that chose an expert twice: its first column adds both
           float sum = ysum[t * nr + row];
-          for (int c2 = c; c2 < 8 && j * 8 + c2 < ntok && o[c2] / a.K == t; ++c2) {
+          for (int c2 = c; c2 < 8 && j * 8 + c2 < ntok && o[c2] == t; ++c2) {
 #pragma unroll
             for (int k = 0; k < KS; ++k) sum += red[((i >> 7) * KS + k) * 128 + (i & 127) + c2 - c];
           }
@@ -742,8 +766,14 @@ template <int NT> int dispatch_stream(StreamArgs p, cudaStream_t s) {
   // Up to 16 tokens: stages such that a CTA of each kernel fits on an SM
   // together, so that the second kernel's first copies overlap the first's
   // end. Beyond: as large as fit, for the tokens' rows beside the weights'.
-  p.stage_bytes = NT <= 2 ? 35968 : (int)((221184 - seg - ysum) / kStages / 128 * 128);
+  p.stage_bytes = NT <= 2 ? 35968 : (int)((227328 - seg - ysum) / kStages / 128 * 128);
   if (p.stage_bytes > 65536) p.stage_bytes = 65536;
+  p.gate_tokens = p.down_tokens = NT * 8;
+  while (p.gate_tokens > 8 && stage_elems(p.stage_bytes, 32 + p.gate_tokens, quantum(2), INT32_MAX / 2) < quantum(2))
+    p.gate_tokens -= 8;
+  while (p.down_tokens > 8 &&
+         stage_elems(p.stage_bytes, 16 * MT + 2 * p.down_tokens, quantum(MT), INT32_MAX / 2) < quantum(MT))
+    p.down_tokens -= 8;
   switch (MT) {
     case 1: return launch_stream<NT, 1>(p, seg, ysum, s);
     case 2: return launch_stream<NT, 2>(p, seg, ysum, s);
@@ -753,7 +783,7 @@ template <int NT> int dispatch_stream(StreamArgs p, cudaStream_t s) {
 
 int run_stream(const LayerArgs& a, cudaStream_t s) {
   __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(a.h);
-  const StreamArgs p{a, h, h + (int64_t)a.n * a.F, 0};
+  const StreamArgs p{a, h, h + (int64_t)a.n * a.F, 0, 0, 0};
   if (a.T <= 8) return dispatch_stream<1>(p, s);
   if (a.T <= 16) return dispatch_stream<2>(p, s);
   if (a.T <= 32) return dispatch_stream<4>(p, s);
