@@ -11,6 +11,7 @@
 // the order of every sum is fixed. Each CTA sorts the (at most 2048) choices
 // by expert itself, in shared memory: that costs about a microsecond and
 // spares a launch.
+#include <cuda.h>  // types of the tensor maps
 #include <math.h>
 
 #include <atomic>
@@ -280,39 +281,46 @@ template <int VB, typename ET> __global__ void __launch_bounds__(kThreads) down_
 
 // ------------------------------------------------- bf16 rows of 16 bytes
 //
-// Weights stream through a ring of shared-memory stages, filled with 16-byte
-// asynchronous copies by four producer warps and multiplied by eight consumer
-// warps with m16n8k16 tensor instructions: 16 weight rows by 8 tokens, an
-// expert's tokens in up to NT such tiles. (Bulk copies of a row's piece were
-// slower: an SM starts one in 34 ns whatever its size, 30 bytes/ns at the 1 KB
-// that a stage has room for, against the 45 that the memory delivers.)
-// With few tokens the time is that of the weight bytes, so what matters is
-// that copies are always in flight: the producers run ahead of the consumers across tiles, rows and experts, and
-// the work is cut so that each of the SMs streams the same number of bytes (an
-// equal share of the active experts' F gate/up row pairs; an equal share of
-// y's H columns for all experts), whatever the sizes.
+// Weights stream through a ring of shared-memory stages and are multiplied by
+// eight consumer warps with m16n8k16 tensor instructions: 16 weight rows by 8
+// tokens, an expert's tokens in up to NT such tiles. With few tokens the time
+// is that of the weight bytes, so what matters is that copies are always in
+// flight: the copying warps run ahead of the consumers across tiles, rows and
+// experts, and the work is cut so that each of the SMs streams the same number
+// of bytes (an equal share of the active experts' F gate/up row pairs; an
+// equal share of y's H columns for all experts), whatever the sizes.
 //
-// A stage holds kc elements of each row of the tile, weights first, then the
-// tokens', rows 2*KC + 64 bytes apart: lanes of a tile read 16 bytes each of
-// 8 rows by 4 places, two rows per 128-byte wavefront, without conflicts. A
-// 16-byte piece feeds two instructions; that pairs k's in another order than
-// the instruction's own, on both sides alike, which a dot product does not
-// see. The warps share a stage's tile: MT tiles of 16 rows by KS slices of kc,
-// and add their sums in shared memory at the tile's end, in a fixed order.
+// The weights come by tensor copies (TMA), one thread's work: 4 KB and more
+// an instruction. The same ring filled with bulk copies of 1 KB pieces of rows
+// reached 4.5 TB/s (an SM starts one in 34 ns whatever its size), with 16-byte
+// asynchronous copies of four warps 5 TB/s (their instructions), with tensor
+// copies of 64 elements by 32 rows 7.0 TB/s. The tokens' rows, which lie
+// apart, come by 16-byte copies of kTokenWarps warps.
+//
+// A stage holds nb blocks of 64 elements: first the weights, block by block,
+// each row's 128 bytes with the 16-byte pieces exchanged by the copy's 128-byte
+// swizzle, then the tokens' rows, nb * 128 + 16 bytes apart. Lane (g, c) of a
+// warp reads pieces 2c and 2c + 1 of rows g and g + 8 and of token g: no bank
+// conflicts on either side. A piece feeds two instructions; that pairs k's in
+// another order than the instruction's own, on both sides alike, which a dot
+// product does not see. The warps share a stage's tile, MT tiles of 16 rows by
+// KS slices of the blocks, and add their sums in shared memory at the tile's
+// end, in a fixed order.
 
 constexpr int kConsumers = 8;
-constexpr int kProducers = 4;
-constexpr int kStreamThreads = (kConsumers + kProducers) * kWarp;
+constexpr int kTokenWarps = 3;
+constexpr int kCopyWarp = kConsumers + kTokenWarps;  // the warp that copies weights
+constexpr int kStreamThreads = (kCopyWarp + 1) * kWarp;
 constexpr int kStages = 3;
+constexpr int kBlock = 64;  // elements of a block: the 128 bytes of a swizzled row
 
-// Element steps of a stage: a multiple of 32 for each of the KS warps.
 __host__ __device__ constexpr int k_slices(int MT) { return MT == 4 ? 2 : 4; }
-__host__ __device__ constexpr int quantum(int MT) { return 32 * k_slices(MT); }
-// Elements of each row that a stage takes when the tile has `rows` rows (not
-// 0: the host chooses stages that hold a tile's rows).
-__host__ __device__ inline int stage_elems(int stage_bytes, int rows, int q, int K) {
-  const int fit = (stage_bytes / rows - 64) / 2 / q * q, all = (K + q - 1) / q * q;
-  return fit < all ? fit : all;
+// Bytes of a stage of nb blocks, and the blocks that fit (not 0: the host
+// chooses stages and tokens at a time that hold one). Swizzled blocks start
+// on 1 KB boundaries.
+__host__ __device__ inline int block_bytes(int rows) { return (rows + 7) / 8 * 1024; }
+__host__ __device__ inline int stage_blocks(int stage_bytes, int wrows, int trows) {
+  return (stage_bytes - 16 * trows) / (block_bytes(wrows) + 2 * kBlock * trows);
 }
 
 __device__ __forceinline__ void mbar_init_count(uint32_t bar, uint32_t count) {
@@ -325,6 +333,14 @@ __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 256
 // Lets the next kernel on the stream start while this one runs.
 __device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// A box of the tensor from coordinates (x, y, z); x is a multiple of 64.
+__device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2,%3,%4}], [%5];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
 // 16 bytes from global to shared memory, not through L1.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -332,18 +348,6 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
 // The thread's arrival on the barrier, once all its copies so far have landed.
 __device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-// A producer warp's share of `rows` rows, ld elements apart, to stage rows
-// `stride` bytes apart: every kProducers-th row, kc elements each.
-__device__ __forceinline__ void copy_rows(uint32_t dst, int stride, const __nv_bfloat16* src, int64_t ld, int rows, int kc) {
-  const int first = (int)threadIdx.x / kWarp - kConsumers, lane = lane_id();
-  const int64_t step = kProducers * ld;
-  for (int c = lane * 8; c < kc; c += kWarp * 8) {
-    const __nv_bfloat16* p = src + first * ld + c;
-    uint32_t d = dst + first * stride + c * 2;
-#pragma unroll 4
-    for (int i = first; i < rows; i += kProducers, p += step, d += kProducers * stride) copy16(d, p);
-  }
 }
 
 __device__ __forceinline__ uint4 lds16(uint32_t p) {
@@ -368,6 +372,7 @@ struct Ring {
   uint32_t parity;
   bool ok;  // false after a wait gave up: nothing is waited for or copied any more
   __device__ __forceinline__ uint32_t at() const { return data + stage * stage_bytes; }
+  __device__ __forceinline__ uint32_t full_bar() const { return full + 8 * stage; }
   // By a whole warp; bounded.
   __device__ __forceinline__ void wait(uint32_t bars, int32_t* status) {
     if (!ok) return;
@@ -382,43 +387,46 @@ struct Ring {
   }
 };
 
-__device__ __forceinline__ Ring make_ring(uint32_t data, uint32_t bars, int stage_bytes, bool producer) {
-  // The producer's first wait on each stage passes: a fresh barrier counts as one phase done.
-  return Ring{data, bars, bars + 8 * kStages, stage_bytes, 0, producer ? 1u : 0u, true};
+__device__ __forceinline__ Ring make_ring(uint32_t data, uint32_t bars, int stage_bytes, bool copies) {
+  // A copying warp's first wait on each stage passes: a fresh barrier counts as one phase done.
+  return Ring{data, bars, bars + 8 * kStages, stage_bytes, 0, copies ? 1u : 0u, true};
 }
 __device__ __forceinline__ void init_ring(uint32_t bars) {
   for (int i = 0; i < kStages; ++i) {
-    mbar_init_count(bars + 8 * i, kProducers * kWarp);
+    mbar_init_count(bars + 8 * i, kTokenWarps * kWarp + 1);
     mbar_init_count(bars + 8 * (kStages + i), kConsumers);
   }
   fence_mbarrier_init();
 }
+__device__ __forceinline__ uint32_t align_1k(uint32_t p) { return (p + 1023u) & ~1023u; }
 
-// Adds one stage's products to acc: this warp's slice of the kc elements, its
-// 16 weight rows starting at row0 (rows at or beyond `rows` repeat the last)
-// and the tokens' rows from tok0 on. PARTS 2: the tokens' rows are held as the
+// Adds one stage's products to acc: this warp's blocks (ks, ks + KS, ...), of
+// which weight rows row0 and row1 (this lane's two of 16) and the tokens at
+// tok. kc: elements of the stage; beyond them the weights are zero and the
+// tokens' places are taken as zero. PARTS 2: the tokens' rows are held as the
 // sum of two bf16 numbers, the second ntok rows after the first.
-template <int NT, int PARTS>
-__device__ __forceinline__ void multiply_stage(float (&acc)[NT][4], uint32_t stage, int stride, int kc, int k_begin,
-                                               int k_end, int row0, int rows, int tok0, int ntok) {
-  const int lane = lane_id(), g = lane >> 2, c = (lane & 3) * 8;
-  const uint32_t a0p = stage + (uint32_t)(row0 + (g < rows ? g : rows - 1)) * stride;
-  const uint32_t a1p = stage + (uint32_t)(row0 + (g + 8 < rows ? g + 8 : rows - 1)) * stride;
+template <int NT, int PARTS, int KS>
+__device__ __forceinline__ void multiply_stage(float (&acc)[NT][4], uint32_t weights, int block, int kc, int ks,
+                                               int row0, int row1, uint32_t tok, int tok_stride, int ntok) {
+  const int lane = lane_id(), g = lane >> 2, c = lane & 3;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  const int end = k_end < kc ? k_end : kc;
-  for (int k = k_begin; k < end; k += 32) {
-    const bool in = k + c < kc;
-    const uint32_t off = (uint32_t)(k + c) * 2;
-    const uint4 a0 = in ? lds16(a0p + off) : zero, a1 = in ? lds16(a1p + off) : zero;
+  for (int b = ks; b * kBlock < kc; b += KS) {
+    const uint32_t w = weights + b * block;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      if (j * 8 >= ntok) break;
-      const int t = j * 8 + g < ntok ? j * 8 + g : ntok - 1;
+    for (int s = 0; s < 2; ++s) {
+      const int piece = 2 * c + s, k = b * kBlock + piece * 8;
+      const uint4 a0 = lds16(w + row0 * 128 + ((piece ^ (row0 & 7)) << 4));
+      const uint4 a1 = lds16(w + row1 * 128 + ((piece ^ (row1 & 7)) << 4));
 #pragma unroll
-      for (int p = 0; p < PARTS; ++p) {
-        const uint4 b = in ? lds16(stage + (uint32_t)(tok0 + p * ntok + t) * stride + off) : zero;
-        mma16(acc[j], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
-        mma16(acc[j], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+      for (int j = 0; j < NT; ++j) {
+        if (j * 8 >= ntok) break;
+        const int t = j * 8 + g < ntok ? j * 8 + g : ntok - 1;
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+          const uint4 v = k < kc ? lds16(tok + (uint32_t)(p * ntok + t) * tok_stride + k * 2) : zero;
+          mma16(acc[j], a0.x, a1.x, a0.y, a1.y, v.x, v.y);
+          mma16(acc[j], a0.z, a1.z, a0.w, a1.w, v.z, v.w);
+        }
       }
     }
   }
@@ -440,17 +448,19 @@ struct StreamArgs {
   __nv_bfloat16* h_lo;
   int stage_bytes;
   int gate_tokens, down_tokens;  // of an expert at a time: NT * 8, or fewer where a stage would not hold their rows
+  int down_rows;                 // rows of a box of w_down
 };
 
-// Tiles of up to 16 row pairs (gate, up) of one expert by up to NT * 8 of its
-// tokens, over the whole of H.
+// Tiles of up to 16 row pairs (gate, up) of one expert by up to per_pass of
+// its tokens, over the whole of H. A box always has 16 pairs: those beyond a
+// CTA's share are read too (from L2, their owner reads them as well) and left.
 struct GateUpWalk {
   const Segments& s;
   int64_t pos, end, F;
-  int q, nf, i0, ntok, K, KC, k0, kc, stage_bytes, per_pass;
+  int q, nf, i0, ntok, K, nb, k0, stage_bytes, per_pass;
   int64_t f0;
-  __device__ GateUpWalk(const Segments& s_, const StreamArgs& p, int per_pass_)
-      : s(s_), F(p.a.F), K((int)p.a.H), stage_bytes(p.stage_bytes), per_pass(per_pass_) {
+  __device__ GateUpWalk(const Segments& s_, const StreamArgs& p)
+      : s(s_), F(p.a.F), K((int)p.a.H), stage_bytes(p.stage_bytes), per_pass(p.gate_tokens) {
     const int64_t rows = s.active * F;
     pos = rows * blockIdx.x / gridDim.x;
     end = rows * (blockIdx.x + 1) / gridDim.x;
@@ -460,7 +470,7 @@ struct GateUpWalk {
   __device__ __forceinline__ void tile() {
     q = (int)(pos / F);
     f0 = pos - q * F;
-    int64_t m = end - pos < F - f0 ? end - pos : F - f0;
+    const int64_t m = end - pos < F - f0 ? end - pos : F - f0;
     nf = m < 16 ? (int)m : 16;
     i0 = s.begin[q];
     pass();
@@ -468,17 +478,14 @@ struct GateUpWalk {
   __device__ __forceinline__ void pass() {
     const int left = s.begin[q + 1] - i0;
     ntok = left < per_pass ? left : per_pass;
-    KC = stage_elems(stage_bytes, 2 * nf + ntok, quantum(2), K);
+    nb = stage_blocks(stage_bytes, 32, ntok);
     k0 = 0;
-    kc = K < KC ? K : KC;
   }
-  __device__ __forceinline__ bool last_stage() const { return k0 + KC >= K; }
+  __device__ __forceinline__ int kc() const { return K - k0 < nb * kBlock ? K - k0 : nb * kBlock; }
+  __device__ __forceinline__ bool last_stage() const { return k0 + nb * kBlock >= K; }
   __device__ __forceinline__ void next() {
-    k0 += KC;
-    if (k0 < K) {
-      kc = K - k0 < KC ? K - k0 : KC;
-      return;
-    }
+    k0 += nb * kBlock;
+    if (k0 < K) return;
     i0 += ntok;
     if (i0 < s.begin[q + 1]) return pass();
     pos += nf;
@@ -487,43 +494,53 @@ struct GateUpWalk {
 };
 
 template <int NT>
-__global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1) gate_up_stream_kernel(StreamArgs p) {
-  extern __shared__ __align__(128) unsigned char dyn[];
+__global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1)
+    gate_up_stream_kernel(StreamArgs p, const __grid_constant__ CUtensorMap map) {
+  extern __shared__ __align__(1024) unsigned char dyn[];
   __shared__ uint64_t bars[2 * kStages];
   __shared__ float red[kConsumers * 128];
+  constexpr int kWeights = 32;  // weight rows of a stage: 16 gate rows, then 16 up rows
   const LayerArgs& a = p.a;
   await_previous_kernel();
   if (threadIdx.x == kStreamThreads - 1) init_ring(smem_u32(bars));
+  const uint32_t ring = align_1k(smem_u32(dyn));
   const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, a.status,
-                                  reinterpret_cast<int32_t*>(dyn + (size_t)kStages * p.stage_bytes));
+                                  reinterpret_cast<int32_t*>(dyn + (ring - smem_u32(dyn)) + (size_t)kStages * p.stage_bytes));
   allow_next_kernel();
   const int warp = threadIdx.x / kWarp, lane = lane_id();
-  GateUpWalk w(s, p, p.gate_tokens);
-  Ring r = make_ring(smem_u32(dyn), smem_u32(bars), p.stage_bytes, warp >= kConsumers);
-  if (warp >= kConsumers) {
-    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x);
-    const __nv_bfloat16* wt = static_cast<const __nv_bfloat16*>(a.w_gate_up);
+  GateUpWalk w(s, p);
+  Ring r = make_ring(ring, smem_u32(bars), p.stage_bytes, warp >= kConsumers);
+  if (warp == kCopyWarp) {
     for (; w.more(); w.next(), r.advance()) {
       r.wait(r.empty, a.status);
       if (!r.ok) break;
-      const int stride = 2 * w.KC + 64;
-      const uint32_t dst = r.at();
-      const __nv_bfloat16* gate = wt + ((int64_t)s.expert[w.q] * 2 * a.F + w.f0) * a.H + w.k0;
-      copy_rows(dst, stride, gate, a.H, w.nf, w.kc);
-      copy_rows(dst + w.nf * stride, stride, gate + a.F * a.H, a.H, w.nf, w.kc);
-      const uint32_t tok = dst + 2 * w.nf * stride;
-      for (int c = lane * 8; c < w.kc; c += kWarp * 8) {
-#pragma unroll 4
-        for (int i = warp - kConsumers; i < w.ntok; i += kProducers)
-          copy16(tok + i * stride + c * 2, x + s.token[w.i0 + i] * a.x_stride + w.k0 + c);
+      if (lane == 0) {
+        const int n = (w.kc() + kBlock - 1) / kBlock, z = 2 * s.expert[w.q];
+        mbar_expect(r.full_bar(), n * block_bytes(kWeights));
+        for (int b = 0; b < n; ++b)
+          tensor_copy(r.at() + b * block_bytes(kWeights), &map, w.k0 + b * kBlock, (int)w.f0, z, r.full_bar());
       }
-      arrive_after_copies(r.full + 8 * r.stage);
+    }
+    return;
+  }
+  if (warp >= kConsumers) {
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x);
+    for (; w.more(); w.next(), r.advance()) {
+      r.wait(r.empty, a.status);
+      if (!r.ok) break;
+      const uint32_t tok = r.at() + w.nb * block_bytes(kWeights);
+      const int stride = w.nb * 2 * kBlock + 16, kc = w.kc();
+      for (int i = warp - kConsumers; i < w.ntok; i += kTokenWarps) {
+        const __nv_bfloat16* src = x + s.token[w.i0 + i] * a.x_stride + w.k0;
+        for (int c = lane * 8; c < kc; c += kWarp * 8) copy16(tok + i * stride + c * 2, src + c);
+      }
+      arrive_after_copies(r.full_bar());
     }
     return;
   }
   // Warps 0..3: slices of the gate rows; 4..7: of the up rows.
   constexpr int KS = k_slices(2);
-  const int mt = warp / KS, ks = warp % KS;
+  const int mt = warp / KS, ks = warp % KS, row = mt * 16 + (lane >> 2);
   while (w.more()) {
     float acc[NT][4];
 #pragma unroll
@@ -533,9 +550,9 @@ __global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1) gate_up_strea
     for (bool last = false; !last; w.next(), r.advance()) {
       last = w.last_stage();
       r.wait(r.full, a.status);
-      const int part = w.KC / KS;
       if (r.ok)
-        multiply_stage<NT, 1>(acc, r.at(), 2 * w.KC + 64, w.kc, ks * part, (ks + 1) * part, mt * nf, nf, 2 * nf, ntok);
+        multiply_stage<NT, 1, KS>(acc, r.at(), block_bytes(kWeights), w.kc(), ks, row, row + 8,
+                                  r.at() + w.nb * block_bytes(kWeights), w.nb * 2 * kBlock + 16, ntok);
       __syncwarp();
       if (lane == 0) mbar_arrive(r.empty + 8 * r.stage);
     }
@@ -570,9 +587,9 @@ __global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1) gate_up_strea
 template <int MT> struct DownWalk {
   const Segments& s;
   int64_t r0, end;
-  int nr, q, i0, ntok, K, KC, k0, kc, stage_bytes, per_pass;
-  __device__ DownWalk(const Segments& s_, const StreamArgs& p, int per_pass_)
-      : s(s_), K((int)p.a.F), stage_bytes(p.stage_bytes), per_pass(per_pass_) {
+  int nr, box, q, i0, ntok, K, nb, k0, stage_bytes, per_pass;
+  __device__ DownWalk(const Segments& s_, const StreamArgs& p)
+      : s(s_), box(p.down_rows), K((int)p.a.F), stage_bytes(p.stage_bytes), per_pass(p.down_tokens) {
     r0 = p.a.H * blockIdx.x / gridDim.x;
     end = p.a.H * (blockIdx.x + 1) / gridDim.x;
     if (s.active == 0) r0 = end;
@@ -580,7 +597,7 @@ template <int MT> struct DownWalk {
   }
   __device__ __forceinline__ bool more() const { return r0 < end; }
   __device__ __forceinline__ void tile() {
-    nr = end - r0 < 16 * MT ? (int)(end - r0) : 16 * MT;
+    nr = end - r0 < box ? (int)(end - r0) : box;
     q = 0;
     i0 = 0;
     pass();
@@ -588,17 +605,14 @@ template <int MT> struct DownWalk {
   __device__ __forceinline__ void pass() {
     const int left = s.begin[q + 1] - i0;
     ntok = left < per_pass ? left : per_pass;
-    KC = stage_elems(stage_bytes, nr + 2 * ntok, quantum(MT), K);
+    nb = stage_blocks(stage_bytes, box, 2 * ntok);
     k0 = 0;
-    kc = K < KC ? K : KC;
   }
-  __device__ __forceinline__ bool last_stage() const { return k0 + KC >= K; }
+  __device__ __forceinline__ int kc() const { return K - k0 < nb * kBlock ? K - k0 : nb * kBlock; }
+  __device__ __forceinline__ bool last_stage() const { return k0 + nb * kBlock >= K; }
   __device__ __forceinline__ void next() {
-    k0 += KC;
-    if (k0 < K) {
-      kc = K - k0 < KC ? K - k0 : KC;
-      return;
-    }
+    k0 += nb * kBlock;
+    if (k0 < K) return;
     i0 += ntok;
     if (i0 < s.begin[q + 1]) return pass();
     if (++q < s.active) return pass();
@@ -608,54 +622,57 @@ template <int MT> struct DownWalk {
 };
 
 template <int NT, int MT>
-__global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1) down_stream_kernel(StreamArgs p) {
-  extern __shared__ __align__(128) unsigned char dyn[];
+__global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1)
+    down_stream_kernel(StreamArgs p, const __grid_constant__ CUtensorMap map) {
+  extern __shared__ __align__(1024) unsigned char dyn[];
   __shared__ uint64_t bars[2 * kStages];
   __shared__ float red[kConsumers * 128];
   const LayerArgs& a = p.a;
   // The gate/up kernel has waited for all before it, so the routing may be
   // read and weights copied while it still runs; h may not.
   if (threadIdx.x == kStreamThreads - 1) init_ring(smem_u32(bars));
-  int32_t* seg = reinterpret_cast<int32_t*>(dyn + (size_t)kStages * p.stage_bytes);
+  const uint32_t ring = align_1k(smem_u32(dyn));
+  int32_t* seg = reinterpret_cast<int32_t*>(dyn + (ring - smem_u32(dyn)) + (size_t)kStages * p.stage_bytes);
   const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, nullptr, seg);
   float* ysum = reinterpret_cast<float*>(seg + segments_bytes(a.n, a.E) / sizeof(int32_t));  // [T, nr]
   const int warp = threadIdx.x / kWarp, lane = lane_id();
-  DownWalk<MT> w(s, p, p.down_tokens);
-  Ring r = make_ring(smem_u32(dyn), smem_u32(bars), p.stage_bytes, warp >= kConsumers);
-  if (warp >= kConsumers) {
-    const __nv_bfloat16* wt = static_cast<const __nv_bfloat16*>(a.w_down);
-    auto weights = [&](const DownWalk<MT>& v, uint32_t dst) {
-      copy_rows(dst, 2 * v.KC + 64, wt + ((int64_t)s.expert[v.q] * a.H + v.r0) * a.F + v.k0, a.F, v.nr, v.kc);
-    };
-    auto tokens = [&](const DownWalk<MT>& v, uint32_t dst) {
-      const int stride = 2 * v.KC + 64;
-      const int64_t at = v.i0 * a.F + v.k0;
-      copy_rows(dst + v.nr * stride, stride, p.h_hi + at, a.F, v.ntok, v.kc);
-      copy_rows(dst + (v.nr + v.ntok) * stride, stride, p.h_lo + at, a.F, v.ntok, v.kc);
-    };
-    DownWalk<MT> first = w;
-    int ahead = 0;
-    for (; ahead < kStages && w.more(); ++ahead, w.next()) weights(w, r.data + ahead * r.stage_bytes);
-    await_previous_kernel();
-    for (int i = 0; i < ahead; ++i, first.next(), r.advance()) {
-      tokens(first, r.at());
-      arrive_after_copies(r.full + 8 * r.stage);
-    }
+  DownWalk<MT> w(s, p);
+  Ring r = make_ring(ring, smem_u32(bars), p.stage_bytes, warp >= kConsumers);
+  const int block = block_bytes(p.down_rows);
+  if (warp == kCopyWarp) {
     for (; w.more(); w.next(), r.advance()) {
       r.wait(r.empty, a.status);
       if (!r.ok) break;
-      weights(w, r.at());
-      tokens(w, r.at());
-      arrive_after_copies(r.full + 8 * r.stage);
+      if (lane == 0) {
+        const int n = (w.kc() + kBlock - 1) / kBlock;
+        mbar_expect(r.full_bar(), n * p.down_rows * 2 * kBlock);
+        for (int b = 0; b < n; ++b)
+          tensor_copy(r.at() + b * block, &map, w.k0 + b * kBlock, (int)w.r0, s.expert[w.q], r.full_bar());
+      }
+    }
+    return;
+  }
+  if (warp >= kConsumers) {
+    await_previous_kernel();
+    for (; w.more(); w.next(), r.advance()) {
+      r.wait(r.empty, a.status);
+      if (!r.ok) break;
+      const uint32_t tok = r.at() + w.nb * block;
+      const int stride = w.nb * 2 * kBlock + 16, kc = w.kc();
+      for (int i = warp - kConsumers; i < 2 * w.ntok; i += kTokenWarps) {
+        const __nv_bfloat16* src = (i < w.ntok ? p.h_hi + (w.i0 + i) * a.F : p.h_lo + (w.i0 + i - w.ntok) * a.F) + w.k0;
+        for (int c = lane * 8; c < kc; c += kWarp * 8) copy16(tok + i * stride + c * 2, src + c);
+      }
+      arrive_after_copies(r.full_bar());
     }
     return;
   }
   constexpr int KS = k_slices(MT);
-  const int mt = warp / KS, ks = warp % KS;
+  const int mt = warp / KS, ks = warp % KS, row = mt * 16 + (lane >> 2);
   int64_t r0 = a.H * blockIdx.x / gridDim.x;
   const int64_t r_end = a.H * (blockIdx.x + 1) / gridDim.x;
-  for (; r0 < r_end; r0 += 16 * MT) {
-    const int nr = r_end - r0 < 16 * MT ? (int)(r_end - r0) : 16 * MT;
+  for (; r0 < r_end; r0 += p.down_rows) {
+    const int nr = r_end - r0 < p.down_rows ? (int)(r_end - r0) : p.down_rows;
     for (int i = threadIdx.x; i < a.T * nr; i += kConsumers * kWarp) ysum[i] = 0.0f;
     float acc[NT][4];
 #pragma unroll
@@ -665,9 +682,10 @@ __global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1) down_stream_k
       for (bool last = false; !last; w.next(), r.advance()) {
         last = w.last_stage();
         r.wait(r.full, a.status);
-        const int part = w.KC / KS, rows = nr - mt * 16;
-        if (r.ok && mt < MT && rows > 0)
-          multiply_stage<NT, 2>(acc, r.at(), 2 * w.KC + 64, w.kc, ks * part, (ks + 1) * part, mt * 16, rows, nr, ntok);
+        if (r.ok && mt * 16 < nr)  // rows beyond nr repeat its last
+          multiply_stage<NT, 2, KS>(acc, r.at(), block, w.kc(), ks, row < nr ? row : nr - 1,
+                                    row + 8 < nr ? row + 8 : nr - 1, r.at() + w.nb * block, w.nb * 2 * kBlock + 16,
+                                    ntok);
         __syncwarp();
         if (lane == 0) mbar_arrive(r.empty + 8 * r.stage);
       }
@@ -681,25 +699,25 @@ __global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1) down_stream_k
         acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
         consumers_sync();
         for (int i = threadIdx.x; i < MT * 128; i += kConsumers * kWarp) {
-          const int row = (i >> 7) * 16 + ((i & 127) >> 3), c = i & 7;
-          if (row >= nr || j * 8 + c >= ntok) continue;
+          const int rr = (i >> 7) * 16 + ((i & 127) >> 3), c = i & 7;
+          if (rr >= nr || j * 8 + c >= ntok) continue;
           const int* o = s.token + i0 + j * 8;
           const int t = o[c];
           if (c > 0 && o[c - 1] == t) continue;  // a token that chose an expert twice: its first column adds both
-          float sum = ysum[t * nr + row];
+          float sum = ysum[t * nr + rr];
           for (int c2 = c; c2 < 8 && j * 8 + c2 < ntok && o[c2] == t; ++c2) {
 #pragma unroll
             for (int k = 0; k < KS; ++k) sum += red[((i >> 7) * KS + k) * 128 + (i & 127) + c2 - c];
           }
-          ysum[t * nr + row] = sum;
+          ysum[t * nr + rr] = sum;
         }
       }
     }
     consumers_sync();
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + r0;
     for (int i = threadIdx.x; i < a.T * nr; i += kConsumers * kWarp) {
-      const int t = i / nr, row = i - t * nr;
-      y[t * a.H + row] = __float2bfloat16_rn(ysum[i]);
+      const int t = i / nr, rr = i - t * nr;
+      y[t * a.H + rr] = __float2bfloat16_rn(ysum[i]);
     }
     consumers_sync();
   }
@@ -744,16 +762,50 @@ template <int VB, typename ET> int run_rows(const LayerArgs& a, cudaStream_t s) 
 }
 
 
-template <int NT, int MT> int launch_stream(const StreamArgs& p, size_t seg, size_t ysum, cudaStream_t s) {
+// cuTensorMapEncodeTiled through the runtime (the library links no driver library).
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_fn() {
+  static std::atomic<EncodeFn> cached{nullptr};
+  EncodeFn f = cached.load(std::memory_order_relaxed);
+  if (f != nullptr) return f;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess) {
+    (void)cudaGetLastError();
+    return nullptr;
+  }
+  f = reinterpret_cast<EncodeFn>(p);
+  cached.store(f, std::memory_order_relaxed);
+  return f;
+}
+
+// bf16 [nz, ny, nx], contiguous, read in boxes of 64 x by x bz, swizzled by 128 bytes; what lies outside reads as zero.
+bool tensor_map(CUtensorMap* map, const void* base, int64_t nx, int64_t ny, int64_t nz, int by, int bz) {
+  const EncodeFn f = encode_fn();
+  if (f == nullptr) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)nx, (cuuint64_t)ny, (cuuint64_t)nz};
+  const cuuint64_t strides[2] = {(cuuint64_t)nx * 2, (cuuint64_t)nx * ny * 2};
+  const cuuint32_t box[3] = {kBlock, (cuuint32_t)by, (cuuint32_t)bz}, step[3] = {1, 1, 1};
+  return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT, int MT>
+int launch_stream(const StreamArgs& p, const CUtensorMap& gate_up, const CUtensorMap& down, size_t seg, size_t ysum,
+                  cudaStream_t s) {
   static std::atomic<int> granted_g[64], granted_d[64];
   auto g = gate_up_stream_kernel<NT>;
   auto d = down_stream_kernel<NT, MT>;
-  const size_t ring = (size_t)kStages * p.stage_bytes;
+  const size_t ring = (size_t)kStages * p.stage_bytes + 1024;
   if (!allow_smem(g, (int)(ring + seg), granted_g) || !allow_smem(d, (int)(ring + seg + ysum), granted_d))
     return MOE_ERR_CUDA;
   const int64_t pairs = (p.a.n < p.a.E ? p.a.n : p.a.E) * p.a.F, sms = num_sms();
-  launch(g, (unsigned)(pairs < sms ? pairs : sms), kStreamThreads, ring + seg, s, p);
-  launch(d, (unsigned)(p.a.H < sms ? p.a.H : sms), kStreamThreads, ring + seg + ysum, s, p);
+  launch(g, (unsigned)(pairs < sms ? pairs : sms), kStreamThreads, ring + seg, s, p, gate_up);
+  launch(d, (unsigned)(p.a.H < sms ? p.a.H : sms), kStreamThreads, ring + seg + ysum, s, p, down);
   return check_launch();
 }
 
@@ -761,29 +813,31 @@ template <int NT> int dispatch_stream(StreamArgs p, cudaStream_t s) {
   const int64_t sms = num_sms();
   const int64_t per_cta = (p.a.H + sms - 1) / sms;
   const int MT = per_cta <= 16 ? 1 : (per_cta <= 32 ? 2 : 4);
+  p.down_rows = (int)(per_cta < 16 * MT ? per_cta : 16 * MT);
   const size_t seg = segments_bytes(p.a.n, p.a.E);
-  const size_t ysum = sizeof(float) * p.a.T * (per_cta < 16 * MT ? per_cta : 16 * MT);
+  const size_t ysum = sizeof(float) * p.a.T * p.down_rows;
   // Up to 16 tokens: stages such that a CTA of each kernel fits on an SM
   // together, so that the second kernel's first copies overlap the first's
   // end. Beyond: as large as fit, for the tokens' rows beside the weights'.
-  p.stage_bytes = NT <= 2 ? 35968 : (int)((227328 - seg - ysum) / kStages / 128 * 128);
+  p.stage_bytes = NT <= 2 ? 34816 : (int)((226304 - seg - ysum) / kStages / 1024 * 1024);
   if (p.stage_bytes > 65536) p.stage_bytes = 65536;
   p.gate_tokens = p.down_tokens = NT * 8;
-  while (p.gate_tokens > 8 && stage_elems(p.stage_bytes, 32 + p.gate_tokens, quantum(2), INT32_MAX / 2) < quantum(2))
-    p.gate_tokens -= 8;
-  while (p.down_tokens > 8 &&
-         stage_elems(p.stage_bytes, 16 * MT + 2 * p.down_tokens, quantum(MT), INT32_MAX / 2) < quantum(MT))
-    p.down_tokens -= 8;
+  while (p.gate_tokens > 8 && stage_blocks(p.stage_bytes, 32, p.gate_tokens) < 1) p.gate_tokens -= 8;
+  while (p.down_tokens > 8 && stage_blocks(p.stage_bytes, p.down_rows, 2 * p.down_tokens) < 1) p.down_tokens -= 8;
+  CUtensorMap gate_up, down;
+  if (!tensor_map(&gate_up, p.a.w_gate_up, p.a.H, p.a.F, 2 * (int64_t)p.a.E, 16, 2) ||
+      !tensor_map(&down, p.a.w_down, p.a.F, p.a.H, p.a.E, p.down_rows, 1))
+    return MOE_ERR_CUDA;
   switch (MT) {
-    case 1: return launch_stream<NT, 1>(p, seg, ysum, s);
-    case 2: return launch_stream<NT, 2>(p, seg, ysum, s);
-    default: return launch_stream<NT, 4>(p, seg, ysum, s);
+    case 1: return launch_stream<NT, 1>(p, gate_up, down, seg, ysum, s);
+    case 2: return launch_stream<NT, 2>(p, gate_up, down, seg, ysum, s);
+    default: return launch_stream<NT, 4>(p, gate_up, down, seg, ysum, s);
   }
 }
 
 int run_stream(const LayerArgs& a, cudaStream_t s) {
   __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(a.h);
-  const StreamArgs p{a, h, h + (int64_t)a.n * a.F, 0, 0, 0};
+  const StreamArgs p{a, h, h + (int64_t)a.n * a.F, 0, 0, 0, 0};
   if (a.T <= 8) return dispatch_stream<1>(p, s);
   if (a.T <= 16) return dispatch_stream<2>(p, s);
   if (a.T <= 32) return dispatch_stream<4>(p, s);
@@ -800,10 +854,10 @@ int dispatch(const LayerArgs& a, const void* router, float* logits, int32_t mode
                       : run_router<Elem<ET>::kBytes, ET>(a, router, logits, mode, normalize, top_expert, weights, s);
   if (rc != MOE_OK) return rc;
   if (!by16) return run_rows<Elem<ET>::kBytes, ET>(a, s);
-  if constexpr (Elem<ET>::kBytes == 2)
-    return run_stream(a, s);
-  else
-    return run_rows<16, ET>(a, s);
+  if constexpr (Elem<ET>::kBytes == 2) {
+    if (a.H >= kBlock && a.F >= kBlock) return run_stream(a, s);  // at least one box each way
+  }
+  return run_rows<16, ET>(a, s);
 }
 
 // Bytes of the workspace's parts: the logits, then h.
