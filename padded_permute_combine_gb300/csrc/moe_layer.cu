@@ -405,31 +405,63 @@ __device__ __forceinline__ uint32_t align_1k(uint32_t p) { return (p + 1023u) & 
 // tok. kc: elements of the stage; beyond them the weights are zero and the
 // tokens' places are taken as zero. PARTS 2: the tokens' rows are held as the
 // sum of two bf16 numbers, the second ntok rows after the first.
-template <int NT, int PARTS, int KS>
-__device__ __forceinline__ void multiply_stage(float (&acc)[NT][4], uint32_t weights, int block, int kc, int ks,
+template <int NT, int PARTS, int KS, int TILES>
+__device__ __forceinline__ void multiply_tiles(float (&acc)[NT][4], uint32_t weights, int block, int kc, int ks,
                                                int row0, int row1, uint32_t tok, int tok_stride, int ntok) {
   const int lane = lane_id(), g = lane >> 2, c = lane & 3;
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  // One tile: a second set of sums, so that an instruction does not wait for the one before it.
+  float odd[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  uint32_t at[TILES];
+#pragma unroll
+  for (int j = 0; j < TILES; ++j) at[j] = tok + (uint32_t)(j * 8 + g < ntok ? j * 8 + g : ntok - 1) * tok_stride + c * 32;
+  const uint32_t p0 = weights + row0 * 128, p1 = weights + row1 * 128;
   for (int b = ks; b * kBlock < kc; b += KS) {
-    const uint32_t w = weights + b * block;
+    uint4 a0[2], a1[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int piece = 2 * c + s, k = b * kBlock + piece * 8;
-      const uint4 a0 = lds16(w + row0 * 128 + ((piece ^ (row0 & 7)) << 4));
-      const uint4 a1 = lds16(w + row1 * 128 + ((piece ^ (row1 & 7)) << 4));
+      a0[s] = lds16(p0 + b * block + (((2 * c + s) ^ (row0 & 7)) << 4));
+      a1[s] = lds16(p1 + b * block + (((2 * c + s) ^ (row1 & 7)) << 4));
+    }
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        if (j * 8 >= ntok) break;
-        const int t = j * 8 + g < ntok ? j * 8 + g : ntok - 1;
+    for (int p = 0; p < PARTS; ++p) {
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) {
-          const uint4 v = k < kc ? lds16(tok + (uint32_t)(p * ntok + t) * tok_stride + k * 2) : zero;
-          mma16(acc[j], a0.x, a1.x, a0.y, a1.y, v.x, v.y);
-          mma16(acc[j], a0.z, a1.z, a0.w, a1.w, v.z, v.w);
+      for (int s = 0; s < 2; ++s) {
+        const bool in = b * kBlock + (2 * c + s) * 8 < kc;
+        uint4 v[TILES];
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) v[j] = in ? lds16(at[j] + p * ntok * tok_stride + b * 2 * kBlock + s * 16) : zero;
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) mma16(acc[j], a0[s].x, a1[s].x, a0[s].y, a1[s].y, v[j].x, v[j].y);
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) {
+          if (TILES == 1)
+            mma16(odd, a0[s].z, a1[s].z, a0[s].w, a1[s].w, v[j].z, v[j].w);
+          else
+            mma16(acc[j], a0[s].z, a1[s].z, a0[s].w, a1[s].w, v[j].z, v[j].w);
         }
       }
     }
   }
+  if (TILES == 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[0][i] += odd[i];
+  }
+}
+
+template <int NT, int PARTS, int KS>
+__device__ __forceinline__ void multiply_stage(float (&acc)[NT][4], uint32_t weights, int block, int kc, int ks,
+                                               int row0, int row1, uint32_t tok, int tok_stride, int ntok) {
+  if (NT == 1 || ntok <= 8)
+    multiply_tiles<NT, PARTS, KS, 1>(acc, weights, block, kc, ks, row0, row1, tok, tok_stride, ntok);
+  else if (NT == 2 || ntok <= 16)
+    multiply_tiles<NT, PARTS, KS, NT < 2 ? NT : 2>(acc, weights, block, kc, ks, row0, row1, tok, tok_stride, ntok);
+  else if (NT > 3 && ntok <= 24)
+    multiply_tiles<NT, PARTS, KS, NT < 3 ? NT : 3>(acc, weights, block, kc, ks, row0, row1, tok, tok_stride, ntok);
+  else if (NT == 4 || ntok <= 32)
+    multiply_tiles<NT, PARTS, KS, NT < 4 ? NT : 4>(acc, weights, block, kc, ks, row0, row1, tok, tok_stride, ntok);
+  else
+    multiply_tiles<NT, PARTS, KS, NT>(acc, weights, block, kc, ks, row0, row1, tok, tok_stride, ntok);
 }
 
 // A warp's 16 x 8 sums, row-major, for the threads that add the KS slices.
@@ -696,7 +728,6 @@ __global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1)
         if (j * 8 >= ntok) break;
         consumers_sync();  // the last tile's sums (or the zeros above) are done with
         if (mt < MT) put_tile(red + warp * 128, acc[j]);
-        acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
         consumers_sync();
         for (int i = threadIdx.x; i < MT * 128; i += kConsumers * kWarp) {
           const int rr = (i >> 7) * 16 + ((i & 127) >> 3), c = i & 7;
@@ -712,6 +743,9 @@ __global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1)
           ysum[t * nr + rr] = sum;
         }
       }
+      // All of them: multiply_stage may have rounded the number of tiles up.
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
     }
     consumers_sync();
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + r0;
