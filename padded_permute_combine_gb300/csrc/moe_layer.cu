@@ -281,47 +281,51 @@ template <int VB, typename ET> __global__ void __launch_bounds__(kThreads) down_
 
 // ------------------------------------------------- bf16 rows of 16 bytes
 //
-// Weights stream through a ring of shared-memory stages and are multiplied by
-// eight consumer warps with m16n8k16 tensor instructions: 16 weight rows by 8
-// tokens, an expert's tokens in up to NT such tiles. With few tokens the time
-// is that of the weight bytes, so what matters is that copies are always in
-// flight: the copying warps run ahead of the consumers across tiles, rows and
-// experts, and the work is cut so that each of the SMs streams the same number
-// of bytes (an equal share of the active experts' F gate/up row pairs; an
-// equal share of y's H columns for all experts), whatever the sizes.
+// Weights stream through a ring of shared-memory stages into the tensor cores:
+// tcgen05.mma with 128 weight rows as one operand and an expert's tokens (up
+// to 64 at a time) as the other, sums in tensor memory. With few tokens the
+// time is that of the weight bytes, so what matters is that copies are always
+// in flight: the copying warps run ahead across tiles, rows and experts, and
+// the work is cut so that each of the SMs streams the same number of bytes (an
+// equal share of the active experts' F gate/up row pairs; an equal share of
+// y's H columns for all experts), whatever the sizes.
 //
-// The weights come by tensor copies (TMA), one thread's work: 4 KB and more
-// an instruction. The same ring filled with bulk copies of 1 KB pieces of rows
-// reached 4.5 TB/s (an SM starts one in 34 ns whatever its size), with 16-byte
+// The weights come by tensor copies (TMA) of 4 KB and more, one thread's work.
+// The same ring filled with bulk copies of 1 KB pieces of rows reached 4.5
+// TB/s (an SM starts one in 34 ns whatever its size), with 16-byte
 // asynchronous copies of four warps 5 TB/s (their instructions), with tensor
 // copies of 64 elements by 32 rows 7.0 TB/s. The tokens' rows, which lie
-// apart, come by 16-byte copies of kTokenWarps warps.
+// apart, come by 16-byte copies of four warps. Multiplying with
+// mma.sync instead of tcgen05 took 1618 us for the first kernel at 128 tokens
+// of the Mixtral-8x7B shape (it is bound by its instructions from about 16
+// tokens an expert on).
 //
-// A stage holds nb blocks of 64 elements: first the weights, block by block,
-// each row's 128 bytes with the 16-byte pieces exchanged by the copy's 128-byte
-// swizzle, then the tokens' rows, nb * 128 + 16 bytes apart. Lane (g, c) of a
-// warp reads pieces 2c and 2c + 1 of rows g and g + 8 and of token g: no bank
-// conflicts on either side. A piece feeds two instructions; that pairs k's in
-// another order than the instruction's own, on both sides alike, which a dot
-// product does not see. The warps share a stage's tile, MT tiles of 16 rows by
-// KS slices of the blocks, and add their sums in shared memory at the tile's
-// end, in a fixed order.
+// A stage holds one or a few blocks of 64 elements of each row: the weights,
+// 128 bytes a row, then the tokens, both in the 128-byte swizzle that the
+// tensor copies write and tcgen05 reads (16-byte piece q of row r lies at
+// place q ^ (r & 7); blocks start on 1 KB boundaries).
+//
+// Warps: 0..3 take sums out of tensor memory (warp w its lanes 32w ..), 4..7
+// copy tokens, 8 copies weights, 9 issues the products. Sums are double
+// buffered. Every wait is bounded: a warp that gives up sets
+// MOE_STATUS_TIMEOUT and does no more work; all warps meet at the end, where
+// the tensor memory is freed.
 
-constexpr int kConsumers = 8;
-constexpr int kTokenWarps = 3;
-constexpr int kCopyWarp = kConsumers + kTokenWarps;  // the warp that copies weights
-constexpr int kStreamThreads = (kCopyWarp + 1) * kWarp;
-constexpr int kStages = 3;
-constexpr int kBlock = 64;  // elements of a block: the 128 bytes of a swizzled row
+constexpr int kOutWarps = 4;
+constexpr int kTokenWarps = 4;
+constexpr int kCopyWarp = kOutWarps + kTokenWarps;
+constexpr int kMulWarp = kCopyWarp + 1;
+constexpr int kStreamThreads = (kMulWarp + 1) * kWarp;
+constexpr int kMaxStages = 8;
+constexpr int kBlock = 64;       // elements of a block: the 128 bytes of a swizzled row
+constexpr int kRowBytes = 128;
+constexpr int kTileRows = 128;   // weight rows of a product
+constexpr int kPairs = 64;       // gate/up row pairs of a tile
+constexpr int kMaxTokens = 64;   // of an expert at a time
+constexpr uint64_t kWaitNs = 2000000000;  // after which a wait gives up
 
-__host__ __device__ constexpr int k_slices(int MT) { return MT == 4 ? 2 : 4; }
-// Bytes of a stage of nb blocks, and the blocks that fit (not 0: the host
-// chooses stages and tokens at a time that hold one). Swizzled blocks start
-// on 1 KB boundaries.
-__host__ __device__ inline int block_bytes(int rows) { return (rows + 7) / 8 * 1024; }
-__host__ __device__ inline int stage_blocks(int stage_bytes, int wrows, int trows) {
-  return (stage_bytes - 16 * trows) / (block_bytes(wrows) + 2 * kBlock * trows);
-}
+__device__ __forceinline__ uint32_t align_1k(uint32_t p) { return (p + 1023u) & ~1023u; }
+__host__ __device__ constexpr int round_to(int v, int m) { return (v + m - 1) / m * m; }
 
 __device__ __forceinline__ void mbar_init_count(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -329,7 +333,6 @@ __device__ __forceinline__ void mbar_init_count(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 // Lets the next kernel on the stream start while this one runs.
 __device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -341,158 +344,192 @@ __device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-// 16 bytes from global to shared memory, not through L1.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes from global to shared memory, not through L1; zeros when !in (src is not read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 // The thread's arrival on the barrier, once all its copies so far have landed.
 __device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ uint4 lds16(uint32_t p) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
-  return v;
-}
-// d += A (16 rows x 16) * B (16 x 8), bf16 operands, fp32 sums.
-__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                      uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// True in one lane of a converged warp. Tensor copies and products are issued
+// behind this and not behind a test of the lane's number: the compiler then
+// knows that one lane issues them (237 against 104 clocks a product, 44 with
+// the four of a block unrolled).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
 }
 
-// The ring's barriers and where one side stands in it.
+// Tensor memory: allocation by one warp, whose address lands in shared memory.
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Eight columns from `at` on: lane l of the warp gets its row's.
+__device__ __forceinline__ void tmem_load8(float (&v)[8], uint32_t at) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(at));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+// Arrives on the barrier when this thread's products so far are done.
+__device__ __forceinline__ void products_arrive(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Descriptor of a block in shared memory: rows of 128 bytes along k, 128-byte
+// swizzle, groups of 8 rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t block_desc(uint32_t addr) {
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// sums[128 rows][n columns] (+)= 16 elements of each row by 16 of each column; bf16, fp32 sums.
+__device__ __forceinline__ void product(uint32_t sums, uint64_t rows, uint64_t cols, int n, bool add) {
+  const uint32_t kind = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((kTileRows >> 4) << 24);
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(sums),
+      "l"(rows), "l"(cols), "r"(kind), "r"((uint32_t)add)
+      : "memory");
+}
+
+// Where a warp stands in the ring of stages or in the two buffers of sums.
 struct Ring {
-  uint32_t data, full, empty;  // shared-memory addresses
-  int stage_bytes;
-  int stage;
+  int n, i;
   uint32_t parity;
-  bool ok;  // false after a wait gave up: nothing is waited for or copied any more
-  __device__ __forceinline__ uint32_t at() const { return data + stage * stage_bytes; }
-  __device__ __forceinline__ uint32_t full_bar() const { return full + 8 * stage; }
-  // By a whole warp; bounded.
-  __device__ __forceinline__ void wait(uint32_t bars, int32_t* status) {
-    if (!ok) return;
-    ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * stage, parity));
-    if (!ok && lane_id() == 0) flag_status(status, MOE_STATUS_TIMEOUT);
-  }
   __device__ __forceinline__ void advance() {
-    if (++stage == kStages) {
-      stage = 0;
+    if (++i == n) {
+      i = 0;
       parity ^= 1;
     }
   }
 };
 
-__device__ __forceinline__ Ring make_ring(uint32_t data, uint32_t bars, int stage_bytes, bool copies) {
-  // A copying warp's first wait on each stage passes: a fresh barrier counts as one phase done.
-  return Ring{data, bars, bars + 8 * kStages, stage_bytes, 0, copies ? 1u : 0u, true};
-}
-__device__ __forceinline__ void init_ring(uint32_t bars) {
-  for (int i = 0; i < kStages; ++i) {
-    mbar_init_count(bars + 8 * i, kTokenWarps * kWarp + 1);
-    mbar_init_count(bars + 8 * (kStages + i), kConsumers);
-  }
-  fence_mbarrier_init();
-}
-__device__ __forceinline__ uint32_t align_1k(uint32_t p) { return (p + 1023u) & ~1023u; }
-
-// Adds one stage's products to acc: this warp's blocks (ks, ks + KS, ...), of
-// which weight rows row0 and row1 (this lane's two of 16) and the tokens at
-// tok. kc: elements of the stage; beyond them the weights are zero and the
-// tokens' places are taken as zero. PARTS 2: the tokens' rows are held as the
-// sum of two bf16 numbers, the second ntok rows after the first.
-template <int NT, int PARTS, int KS, int TILES>
-__device__ __forceinline__ void multiply_tiles(float (&acc)[NT][4], uint32_t weights, int block, int kc, int ks,
-                                               int row0, int row1, uint32_t tok, int tok_stride, int ntok) {
-  const int lane = lane_id(), g = lane >> 2, c = lane & 3;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  // One tile: a second set of sums, so that an instruction does not wait for the one before it.
-  float odd[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  uint32_t at[TILES];
-#pragma unroll
-  for (int j = 0; j < TILES; ++j) at[j] = tok + (uint32_t)(j * 8 + g < ntok ? j * 8 + g : ntok - 1) * tok_stride + c * 32;
-  const uint32_t p0 = weights + row0 * 128, p1 = weights + row1 * 128;
-  for (int b = ks; b * kBlock < kc; b += KS) {
-    uint4 a0[2], a1[2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      a0[s] = lds16(p0 + b * block + (((2 * c + s) ^ (row0 & 7)) << 4));
-      a1[s] = lds16(p1 + b * block + (((2 * c + s) ^ (row1 & 7)) << 4));
-    }
-#pragma unroll
-    for (int p = 0; p < PARTS; ++p) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const bool in = b * kBlock + (2 * c + s) * 8 < kc;
-        uint4 v[TILES];
-#pragma unroll
-        for (int j = 0; j < TILES; ++j) v[j] = in ? lds16(at[j] + p * ntok * tok_stride + b * 2 * kBlock + s * 16) : zero;
-#pragma unroll
-        for (int j = 0; j < TILES; ++j) mma16(acc[j], a0[s].x, a1[s].x, a0[s].y, a1[s].y, v[j].x, v[j].y);
-#pragma unroll
-        for (int j = 0; j < TILES; ++j) {
-          if (TILES == 1)
-            mma16(odd, a0[s].z, a1[s].z, a0[s].w, a1[s].w, v[j].z, v[j].w);
-          else
-            mma16(acc[j], a0[s].z, a1[s].z, a0[s].w, a1[s].w, v[j].z, v[j].w);
-        }
-      }
-    }
-  }
-  if (TILES == 1) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[0][i] += odd[i];
-  }
-}
-
-template <int NT, int PARTS, int KS>
-__device__ __forceinline__ void multiply_stage(float (&acc)[NT][4], uint32_t weights, int block, int kc, int ks,
-                                               int row0, int row1, uint32_t tok, int tok_stride, int ntok) {
-  if (NT == 1 || ntok <= 8)
-    multiply_tiles<NT, PARTS, KS, 1>(acc, weights, block, kc, ks, row0, row1, tok, tok_stride, ntok);
-  else if (NT == 2 || ntok <= 16)
-    multiply_tiles<NT, PARTS, KS, NT < 2 ? NT : 2>(acc, weights, block, kc, ks, row0, row1, tok, tok_stride, ntok);
-  else if (NT > 3 && ntok <= 24)
-    multiply_tiles<NT, PARTS, KS, NT < 3 ? NT : 3>(acc, weights, block, kc, ks, row0, row1, tok, tok_stride, ntok);
-  else if (NT == 4 || ntok <= 32)
-    multiply_tiles<NT, PARTS, KS, NT < 4 ? NT : 4>(acc, weights, block, kc, ks, row0, row1, tok, tok_stride, ntok);
-  else
-    multiply_tiles<NT, PARTS, KS, NT>(acc, weights, block, kc, ks, row0, row1, tok, tok_stride, ntok);
-}
-
-// A warp's 16 x 8 sums, row-major, for the threads that add the KS slices.
-__device__ __forceinline__ void put_tile(float* red, const float (&acc)[4]) {
-  const int lane = lane_id();
-  float* p = red + (lane >> 2) * 8 + (lane & 3) * 2;
-  p[0] = acc[0];
-  p[1] = acc[1];
-  p[64] = acc[2];
-  p[65] = acc[3];
-}
-
 struct StreamArgs {
   LayerArgs a;
   __nv_bfloat16* h_hi;  // [n, F] in sorted order: h = h_hi + h_lo
   __nv_bfloat16* h_lo;
-  int stage_bytes;
-  int gate_tokens, down_tokens;  // of an expert at a time: NT * 8, or fewer where a stage would not hold their rows
-  int down_rows;                 // rows of a box of w_down
+};
+// A kernel's cut of its work and of its shared memory.
+struct StreamShape {
+  int stages, stage_bytes, blocks;  // blocks of 64 elements in a stage
+  int tokens;                       // of an expert at a time (a multiple of 16, the products' columns; 8 in the second kernel)
+  int rows;                         // second kernel: weight rows of a tile
+  int slices;                       // second kernel: CTAs of a cluster, which share a tile's elements
+  uint32_t cols;                    // tensor memory columns
 };
 
-// Tiles of up to 16 row pairs (gate, up) of one expert by up to per_pass of
-// its tokens, over the whole of H. A box always has 16 pairs: those beyond a
-// CTA's share are read too (from L2, their owner reads them as well) and left.
+struct StreamShared {
+  uint64_t full[kMaxStages], empty[kMaxStages], sums_full[2], sums_empty[2];
+  uint32_t tmem;
+};
+
+__device__ __forceinline__ void init_shared(StreamShared& sh, int stages) {
+  for (int i = 0; i < stages; ++i) {
+    mbar_init_count(smem_u32(&sh.full[i]), kTokenWarps * kWarp + 1);  // the tokens' copies and the weights'
+    mbar_init_count(smem_u32(&sh.empty[i]), 1);
+  }
+  for (int i = 0; i < 2; ++i) {
+    mbar_init_count(smem_u32(&sh.sums_full[i]), 1);
+    mbar_init_count(smem_u32(&sh.sums_empty[i]), kOutWarps);
+  }
+  fence_mbarrier_init();
+}
+
+// By a whole warp, bounded in polls and in time; false once a wait has given up.
+__device__ __forceinline__ bool wait_bar(bool ok, uint64_t* bar, uint32_t parity, int32_t* status) {
+  if (!ok) return false;
+  const uint32_t at = smem_u32(bar);
+  uint64_t since = 0;
+  ok = false;
+  for (int it = 0; it < kSpinLimit; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(at), "r"(parity)
+        : "memory");
+    if (__all_sync(0xffffffffu, done != 0)) {
+      ok = true;
+      break;
+    }
+    if ((it & 255) == 255) {
+      uint64_t now;
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+      now = __shfl_sync(0xffffffffu, now, 0);
+      if (since == 0) since = now;
+      if (now - since > kWaitNs) break;
+    }
+  }
+  if (!ok && lane_id() == 0) flag_status(status, MOE_STATUS_TIMEOUT);
+  return ok;
+}
+
+// The products of every stage, one thread's work. WALK: tiles and their
+// stages; `columns(w)`: columns of a tile's products; `tokens_at(w)`: offset of
+// the tokens in a stage; block: bytes of a block of weight rows.
+template <typename WALK, typename C, typename O>
+__device__ __forceinline__ void multiply(WALK w, StreamShared& sh, const StreamShape& z, uint32_t ring, int block,
+                                         int32_t* status, C columns, O tokens_at) {
+  Ring r{z.stages, 0, 0}, d{2, 0, 1};
+  const uint32_t tmem = sh.tmem;
+  bool ok = true;
+  while (w.more()) {
+    ok = wait_bar(ok, &sh.sums_empty[d.i], d.parity, status);
+    tmem_fence_after();
+    const int n = columns(w);
+    bool add = false;
+    for (bool last = false; !last; w.next(), r.advance()) {
+      last = w.last_stage();
+      ok = wait_bar(ok, &sh.full[r.i], r.parity, status);
+      fence_async_shared();  // the tokens' copies were ordinary writes; the products read by another path
+      tmem_fence_after();
+      __syncwarp();
+      if (ok && elect_lane()) {
+        const uint32_t at = ring + r.i * z.stage_bytes, sums = tmem + d.i * (z.cols / 2);
+        const uint32_t tokens = at + tokens_at(w);
+        const int kc = w.kc();
+        for (int b = 0; b * kBlock < kc; ++b) {
+          const uint64_t rows = block_desc(at + b * block), cols = block_desc(tokens + b * n * kRowBytes);
+          // 16 elements are 32 bytes: 2 in the descriptor.
+          if (kc - b * kBlock >= kBlock) {
+#pragma unroll
+            for (int k = 0; k < kBlock / 16; ++k) product(sums, rows + 2 * k, cols + 2 * k, n, k > 0 || add);
+          } else {
+            for (int k = 0; k * 16 < kc - b * kBlock; ++k) product(sums, rows + 2 * k, cols + 2 * k, n, k > 0 || add);
+          }
+          add = true;
+        }
+        products_arrive(smem_u32(&sh.empty[r.i]));
+        if (last) products_arrive(smem_u32(&sh.sums_full[d.i]));
+      }
+      add = true;
+      __syncwarp();
+    }
+    d.advance();
+  }
+  // Every arrival lands before the CTA may end.
+  for (int i = 0; i < z.stages; ++i) ok = wait_bar(ok, &sh.empty[i], i < r.i ? r.parity : r.parity ^ 1, status);
+}
+
+// Tiles of up to 64 row pairs (gate, up) of one expert by up to z.tokens of
+// its tokens, over the whole of H. A box has 16 pairs: those beyond a CTA's
+// share are read too (their owner reads them as well) and left.
 struct GateUpWalk {
   const Segments& s;
-  int64_t pos, end, F;
-  int q, nf, i0, ntok, K, nb, k0, stage_bytes, per_pass;
-  int64_t f0;
-  __device__ GateUpWalk(const Segments& s_, const StreamArgs& p)
-      : s(s_), F(p.a.F), K((int)p.a.H), stage_bytes(p.stage_bytes), per_pass(p.gate_tokens) {
+  int64_t pos, end, F, f0;
+  int q, nf, i0, ntok, K, k0, per_stage, per_pass;
+  __device__ GateUpWalk(const Segments& s_, const LayerArgs& a, const StreamShape& z)
+      : s(s_), F(a.F), K((int)a.H), per_stage(z.blocks * kBlock), per_pass(z.tokens) {
     const int64_t rows = s.active * F;
     pos = rows * blockIdx.x / gridDim.x;
     end = rows * (blockIdx.x + 1) / gridDim.x;
@@ -503,133 +540,148 @@ struct GateUpWalk {
     q = (int)(pos / F);
     f0 = pos - q * F;
     const int64_t m = end - pos < F - f0 ? end - pos : F - f0;
-    nf = m < 16 ? (int)m : 16;
+    nf = m < kPairs ? (int)m : kPairs;
     i0 = s.begin[q];
     pass();
   }
   __device__ __forceinline__ void pass() {
     const int left = s.begin[q + 1] - i0;
     ntok = left < per_pass ? left : per_pass;
-    nb = stage_blocks(stage_bytes, 32, ntok);
     k0 = 0;
   }
-  __device__ __forceinline__ int kc() const { return K - k0 < nb * kBlock ? K - k0 : nb * kBlock; }
-  __device__ __forceinline__ bool last_stage() const { return k0 + nb * kBlock >= K; }
+  __device__ __forceinline__ int kc() const { return K - k0 < per_stage ? K - k0 : per_stage; }
+  __device__ __forceinline__ bool last_stage() const { return k0 + per_stage >= K; }
   __device__ __forceinline__ void next() {
-    k0 += nb * kBlock;
+    k0 += per_stage;
     if (k0 < K) return;
     i0 += ntok;
     if (i0 < s.begin[q + 1]) return pass();
     pos += nf;
     if (pos < end) tile();
   }
+  __device__ __forceinline__ void next_pass() {
+    k0 = K;
+    next();
+  }
 };
 
-template <int NT>
-__global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1)
-    gate_up_stream_kernel(StreamArgs p, const __grid_constant__ CUtensorMap map) {
+__global__ void __launch_bounds__(kStreamThreads, 2)
+    gate_up_stream_kernel(StreamArgs p, StreamShape z, const __grid_constant__ CUtensorMap map) {
   extern __shared__ __align__(1024) unsigned char dyn[];
-  __shared__ uint64_t bars[2 * kStages];
-  __shared__ float red[kConsumers * 128];
-  constexpr int kWeights = 32;  // weight rows of a stage: 16 gate rows, then 16 up rows
+  __shared__ StreamShared sh;
+  constexpr int kBytes = kTileRows * kRowBytes;  // of a block of weights
   const LayerArgs& a = p.a;
   await_previous_kernel();
-  if (threadIdx.x == kStreamThreads - 1) init_ring(smem_u32(bars));
-  const uint32_t ring = align_1k(smem_u32(dyn));
-  const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, a.status,
-                                  reinterpret_cast<int32_t*>(dyn + (ring - smem_u32(dyn)) + (size_t)kStages * p.stage_bytes));
-  allow_next_kernel();
   const int warp = threadIdx.x / kWarp, lane = lane_id();
-  GateUpWalk w(s, p);
-  Ring r = make_ring(ring, smem_u32(bars), p.stage_bytes, warp >= kConsumers);
+  if (warp == kMulWarp) tmem_alloc(smem_u32(&sh.tmem), z.cols);
+  if (threadIdx.x == kCopyWarp * kWarp) init_shared(sh, z.stages);
+  const uint32_t ring = align_1k(smem_u32(dyn));
+  unsigned char* rest = dyn + (ring - smem_u32(dyn)) + (size_t)z.stages * z.stage_bytes;
+  tmem_fence_before();
+  const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, a.status,
+                                  reinterpret_cast<int32_t*>(rest));
+  tmem_fence_after();
+  allow_next_kernel();
+  GateUpWalk w(s, a, z);
+  bool ok = true;
   if (warp == kCopyWarp) {
-    for (; w.more(); w.next(), r.advance()) {
-      r.wait(r.empty, a.status);
-      if (!r.ok) break;
-      if (lane == 0) {
-        const int n = (w.kc() + kBlock - 1) / kBlock, z = 2 * s.expert[w.q];
-        mbar_expect(r.full_bar(), n * block_bytes(kWeights));
-        for (int b = 0; b < n; ++b)
-          tensor_copy(r.at() + b * block_bytes(kWeights), &map, w.k0 + b * kBlock, (int)w.f0, z, r.full_bar());
-      }
-    }
-    return;
-  }
-  if (warp >= kConsumers) {
-    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x);
-    for (; w.more(); w.next(), r.advance()) {
-      r.wait(r.empty, a.status);
-      if (!r.ok) break;
-      const uint32_t tok = r.at() + w.nb * block_bytes(kWeights);
-      const int stride = w.nb * 2 * kBlock + 16, kc = w.kc();
-      for (int i = warp - kConsumers; i < w.ntok; i += kTokenWarps) {
-        const __nv_bfloat16* src = x + s.token[w.i0 + i] * a.x_stride + w.k0;
-        for (int c = lane * 8; c < kc; c += kWarp * 8) copy16(tok + i * stride + c * 2, src + c);
-      }
-      arrive_after_copies(r.full_bar());
-    }
-    return;
-  }
-  // Warps 0..3: slices of the gate rows; 4..7: of the up rows.
-  constexpr int KS = k_slices(2);
-  const int mt = warp / KS, ks = warp % KS, row = mt * 16 + (lane >> 2);
-  while (w.more()) {
-    float acc[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-    const int nf = w.nf, i0 = w.i0, ntok = w.ntok;
-    const int64_t f0 = w.f0;
-    for (bool last = false; !last; w.next(), r.advance()) {
-      last = w.last_stage();
-      r.wait(r.full, a.status);
-      if (r.ok)
-        multiply_stage<NT, 1, KS>(acc, r.at(), block_bytes(kWeights), w.kc(), ks, row, row + 8,
-                                  r.at() + w.nb * block_bytes(kWeights), w.nb * 2 * kBlock + 16, ntok);
+    for (Ring r{z.stages, 0, 1}; w.more(); w.next(), r.advance()) {
+      ok = wait_bar(ok, &sh.empty[r.i], r.parity, a.status);
+      if (!ok) break;
       __syncwarp();
-      if (lane == 0) mbar_arrive(r.empty + 8 * r.stage);
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      if (j * 8 >= ntok) break;
-      put_tile(red + warp * 128, acc[j]);
-      consumers_sync();
-      const int f = threadIdx.x & 15, c = threadIdx.x >> 4;
-      if (threadIdx.x < 128 && f < nf && j * 8 + c < ntok) {
-        float g = 0.0f, u = 0.0f;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          g += red[k * 128 + f * 8 + c];
-          u += red[(KS + k) * 128 + f * 8 + c];
-        }
-        const int i = i0 + j * 8 + c;
-        const float h = __ldcg(a.weights + s.order[i]) * (silu(g) * u);
-        // Two bf16 numbers keep 16 significant bits of h: one would round the layer's result twice.
-        const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-        const float rest = h - __bfloat162float(hi);
-        const int64_t at = i * a.F + f0 + f;
-        p.h_hi[at] = hi;
-        p.h_lo[at] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
+      if (elect_lane()) {
+        const uint32_t bar = smem_u32(&sh.full[r.i]), at = ring + r.i * z.stage_bytes;
+        const int n = (w.kc() + kBlock - 1) / kBlock, boxes = (w.nf + 15) / 16, e = s.expert[w.q];
+        mbar_expect(bar, n * boxes * 32 * kRowBytes);
+        for (int b = 0; b < n; ++b)
+          for (int g = 0; g < boxes; ++g)
+            tensor_copy(at + b * kBytes + g * 32 * kRowBytes, &map, w.k0 + b * kBlock, (int)w.f0 + g * 16, 2 * e, bar);
       }
-      consumers_sync();
+    }
+  } else if (warp == kMulWarp) {
+    multiply(w, sh, z, ring, kBytes, a.status, [](const GateUpWalk& v) { return round_to(v.ntok, 16); },
+             [&](const GateUpWalk&) { return z.blocks * kBytes; });
+  } else if (warp >= kOutWarps) {
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x);
+    const int piece = lane & 7, first = (warp - kOutWarps) * 4 + (lane >> 3);
+    for (Ring r{z.stages, 0, 1}; w.more(); w.next(), r.advance()) {
+      ok = wait_bar(ok, &sh.empty[r.i], r.parity, a.status);
+      if (!ok) break;
+      const uint32_t at = ring + r.i * z.stage_bytes + z.blocks * kBytes;
+      const int kc = w.kc(), n = round_to(w.ntok, 16);
+      for (int i = first; i < w.ntok; i += 4 * kTokenWarps) {
+        const __nv_bfloat16* src = x + s.token[w.i0 + i] * a.x_stride + w.k0 + piece * 8;
+        const uint32_t dst = at + i * kRowBytes + ((piece ^ (i & 7)) << 4);
+        for (int b = 0; b * kBlock < kc; ++b) {
+          const bool in = b * kBlock + piece * 8 < kc;
+          copy16(dst + b * n * kRowBytes, in ? src + b * kBlock : x, in);
+        }
+      }
+      arrive_after_copies(smem_u32(&sh.full[r.i]));
+    }
+  } else {
+    // Rows of the sums: 16 gate rows, their 16 up rows, the next 16 gate rows ...
+    const bool gate = lane < 16;
+    const int f = warp * 16 + (lane & 15);
+    for (Ring d{2, 0, 0}; w.more(); w.next_pass(), d.advance()) {
+      ok = wait_bar(ok, &sh.sums_full[d.i], d.parity, a.status);
+      tmem_fence_after();
+      if (ok && warp * 16 < w.nf) {
+        const uint32_t at = sh.tmem + d.i * (z.cols / 2) + ((uint32_t)(warp * 32) << 16);
+        for (int c0 = 0; c0 < w.ntok; c0 += 8) {
+          float v[8];
+          __syncwarp();
+          tmem_load8(v, at + c0);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            // Lower lanes finish columns 0..3, upper lanes 4..7.
+            const float other = __shfl_xor_sync(0xffffffffu, gate ? v[c + 4] : v[c], 16);
+            const float g = gate ? v[c] : other, u = gate ? other : v[c + 4];
+            const int col = c0 + c + (gate ? 0 : 4);
+            if (f < w.nf && col < w.ntok) {
+              const int i = w.i0 + col;
+              const float h = __ldcg(a.weights + s.order[i]) * (silu(g) * u);
+              // Two bf16 numbers keep 16 significant bits of h: one would round the layer's result twice.
+              const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+              const float rest = h - __bfloat162float(hi);
+              p.h_hi[i * a.F + w.f0 + f] = hi;
+              p.h_lo[i * a.F + w.f0 + f] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
+            }
+          }
+        }
+      }
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.sums_empty[d.i]));
     }
   }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  if (warp == kMulWarp) tmem_free(sh.tmem, z.cols);
 }
 
-// y's columns [r0, r0 + nr) for one expert's tokens after another, over the whole of F.
-template <int MT> struct DownWalk {
+// y's columns [r0, r0 + nr) for one expert's tokens after another, over this
+// slice of F (all of it without a cluster).
+struct DownWalk {
   const Segments& s;
   int64_t r0, end;
-  int nr, box, q, i0, ntok, K, nb, k0, stage_bytes, per_pass;
-  __device__ DownWalk(const Segments& s_, const StreamArgs& p)
-      : s(s_), box(p.down_rows), K((int)p.a.F), stage_bytes(p.stage_bytes), per_pass(p.down_tokens) {
-    r0 = p.a.H * blockIdx.x / gridDim.x;
-    end = p.a.H * (blockIdx.x + 1) / gridDim.x;
-    if (s.active == 0) r0 = end;
+  int nr, q, i0, ntok, K0, K, k0, per_stage, per_pass, rows;
+  __device__ DownWalk(const Segments& s_, const LayerArgs& a, const StreamShape& z)
+      : s(s_), per_stage(z.blocks * kBlock), per_pass(z.tokens), rows(z.rows) {
+    const int64_t tiles = gridDim.x / z.slices, tile_id = blockIdx.x / z.slices, slice = blockIdx.x % z.slices;
+    r0 = a.H * tile_id / tiles;
+    end = a.H * (tile_id + 1) / tiles;
+    const int64_t blocks = (a.F + kBlock - 1) / kBlock;
+    K0 = (int)(blocks * slice / z.slices * kBlock);
+    const int64_t k_end = blocks * (slice + 1) / z.slices * kBlock;
+    K = (int)(k_end < a.F ? k_end : a.F);
+    if (s.active == 0 || K0 >= K) r0 = end;
     if (more()) tile();
   }
   __device__ __forceinline__ bool more() const { return r0 < end; }
   __device__ __forceinline__ void tile() {
-    nr = end - r0 < box ? (int)(end - r0) : box;
+    nr = end - r0 < rows ? (int)(end - r0) : rows;
     q = 0;
     i0 = 0;
     pass();
@@ -637,13 +689,12 @@ template <int MT> struct DownWalk {
   __device__ __forceinline__ void pass() {
     const int left = s.begin[q + 1] - i0;
     ntok = left < per_pass ? left : per_pass;
-    nb = stage_blocks(stage_bytes, box, 2 * ntok);
-    k0 = 0;
+    k0 = K0;
   }
-  __device__ __forceinline__ int kc() const { return K - k0 < nb * kBlock ? K - k0 : nb * kBlock; }
-  __device__ __forceinline__ bool last_stage() const { return k0 + nb * kBlock >= K; }
+  __device__ __forceinline__ int kc() const { return K - k0 < per_stage ? K - k0 : per_stage; }
+  __device__ __forceinline__ bool last_stage() const { return k0 + per_stage >= K; }
   __device__ __forceinline__ void next() {
-    k0 += nb * kBlock;
+    k0 += per_stage;
     if (k0 < K) return;
     i0 += ntok;
     if (i0 < s.begin[q + 1]) return pass();
@@ -651,109 +702,136 @@ template <int MT> struct DownWalk {
     r0 += nr;
     if (r0 < end) tile();
   }
+  __device__ __forceinline__ void next_pass() {
+    k0 = K;
+    next();
+  }
 };
 
-template <int NT, int MT>
-__global__ void __launch_bounds__(kStreamThreads, NT <= 2 ? 2 : 1)
-    down_stream_kernel(StreamArgs p, const __grid_constant__ CUtensorMap map) {
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// A float of another CTA of the cluster, at the place where this CTA has `p`.
+__device__ __forceinline__ float load_peer(const float* p, uint32_t rank) {
+  uint32_t at;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kStreamThreads, 2)
+    down_stream_kernel(StreamArgs p, StreamShape z, const __grid_constant__ CUtensorMap map) {
   extern __shared__ __align__(1024) unsigned char dyn[];
-  __shared__ uint64_t bars[2 * kStages];
-  __shared__ float red[kConsumers * 128];
+  __shared__ StreamShared sh;
   const LayerArgs& a = p.a;
+  const int warp = threadIdx.x / kWarp, lane = lane_id();
   // The gate/up kernel has waited for all before it, so the routing may be
   // read and weights copied while it still runs; h may not.
-  if (threadIdx.x == kStreamThreads - 1) init_ring(smem_u32(bars));
+  if (warp == kMulWarp) tmem_alloc(smem_u32(&sh.tmem), z.cols);
+  if (threadIdx.x == kCopyWarp * kWarp) init_shared(sh, z.stages);
   const uint32_t ring = align_1k(smem_u32(dyn));
-  int32_t* seg = reinterpret_cast<int32_t*>(dyn + (ring - smem_u32(dyn)) + (size_t)kStages * p.stage_bytes);
+  unsigned char* rest = dyn + (ring - smem_u32(dyn)) + (size_t)z.stages * z.stage_bytes;
+  int32_t* seg = reinterpret_cast<int32_t*>(rest);
+  tmem_fence_before();
   const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, nullptr, seg);
+  tmem_fence_after();
   float* ysum = reinterpret_cast<float*>(seg + segments_bytes(a.n, a.E) / sizeof(int32_t));  // [T, nr]
-  const int warp = threadIdx.x / kWarp, lane = lane_id();
-  DownWalk<MT> w(s, p);
-  Ring r = make_ring(ring, smem_u32(bars), p.stage_bytes, warp >= kConsumers);
-  const int block = block_bytes(p.down_rows);
+  DownWalk w(s, a, z);
+  const int block = round_to(z.rows, 8) * kRowBytes;
+  bool ok = true;
   if (warp == kCopyWarp) {
-    for (; w.more(); w.next(), r.advance()) {
-      r.wait(r.empty, a.status);
-      if (!r.ok) break;
-      if (lane == 0) {
+    for (Ring r{z.stages, 0, 1}; w.more(); w.next(), r.advance()) {
+      ok = wait_bar(ok, &sh.empty[r.i], r.parity, a.status);
+      if (!ok) break;
+      __syncwarp();
+      if (elect_lane()) {
+        const uint32_t bar = smem_u32(&sh.full[r.i]), at = ring + r.i * z.stage_bytes;
         const int n = (w.kc() + kBlock - 1) / kBlock;
-        mbar_expect(r.full_bar(), n * p.down_rows * 2 * kBlock);
+        mbar_expect(bar, n * z.rows * kRowBytes);
         for (int b = 0; b < n; ++b)
-          tensor_copy(r.at() + b * block, &map, w.k0 + b * kBlock, (int)w.r0, s.expert[w.q], r.full_bar());
+          tensor_copy(at + b * block, &map, w.k0 + b * kBlock, (int)w.r0, s.expert[w.q], bar);
       }
     }
-    return;
-  }
-  if (warp >= kConsumers) {
+  } else if (warp == kMulWarp) {
+    // The tile reads 128 rows; what lies beyond its weights lands in rows of the sums that nobody reads.
+    multiply(w, sh, z, ring, block, a.status, [](const DownWalk& v) { return 2 * round_to(v.ntok, 8); },
+             [&](const DownWalk&) { return z.blocks * block; });
+  } else if (warp >= kOutWarps) {
     await_previous_kernel();
-    for (; w.more(); w.next(), r.advance()) {
-      r.wait(r.empty, a.status);
-      if (!r.ok) break;
-      const uint32_t tok = r.at() + w.nb * block;
-      const int stride = w.nb * 2 * kBlock + 16, kc = w.kc();
-      for (int i = warp - kConsumers; i < 2 * w.ntok; i += kTokenWarps) {
-        const __nv_bfloat16* src = (i < w.ntok ? p.h_hi + (w.i0 + i) * a.F : p.h_lo + (w.i0 + i - w.ntok) * a.F) + w.k0;
-        for (int c = lane * 8; c < kc; c += kWarp * 8) copy16(tok + i * stride + c * 2, src + c);
-      }
-      arrive_after_copies(r.full_bar());
-    }
-    return;
-  }
-  constexpr int KS = k_slices(MT);
-  const int mt = warp / KS, ks = warp % KS, row = mt * 16 + (lane >> 2);
-  int64_t r0 = a.H * blockIdx.x / gridDim.x;
-  const int64_t r_end = a.H * (blockIdx.x + 1) / gridDim.x;
-  for (; r0 < r_end; r0 += p.down_rows) {
-    const int nr = r_end - r0 < p.down_rows ? (int)(r_end - r0) : p.down_rows;
-    for (int i = threadIdx.x; i < a.T * nr; i += kConsumers * kWarp) ysum[i] = 0.0f;
-    float acc[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-    while (w.more() && w.r0 == r0) {
-      const int i0 = w.i0, ntok = w.ntok;
-      for (bool last = false; !last; w.next(), r.advance()) {
-        last = w.last_stage();
-        r.wait(r.full, a.status);
-        if (r.ok && mt * 16 < nr)  // rows beyond nr repeat its last
-          multiply_stage<NT, 2, KS>(acc, r.at(), block, w.kc(), ks, row < nr ? row : nr - 1,
-                                    row + 8 < nr ? row + 8 : nr - 1, r.at() + w.nb * block, w.nb * 2 * kBlock + 16,
-                                    ntok);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(r.empty + 8 * r.stage);
-      }
-      // One token's experts one after another need no sum in between.
-      if (ntok == 1 && w.more() && w.r0 == r0 && w.ntok == 1 && s.token[w.i0] == s.token[i0]) continue;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        if (j * 8 >= ntok) break;
-        consumers_sync();  // the last tile's sums (or the zeros above) are done with
-        if (mt < MT) put_tile(red + warp * 128, acc[j]);
-        consumers_sync();
-        for (int i = threadIdx.x; i < MT * 128; i += kConsumers * kWarp) {
-          const int rr = (i >> 7) * 16 + ((i & 127) >> 3), c = i & 7;
-          if (rr >= nr || j * 8 + c >= ntok) continue;
-          const int* o = s.token + i0 + j * 8;
-          const int t = o[c];
-          if (c > 0 && o[c - 1] == t) continue;  // a token that chose an expert twice: its first column adds both
-          float sum = ysum[t * nr + rr];
-          for (int c2 = c; c2 < 8 && j * 8 + c2 < ntok && o[c2] == t; ++c2) {
-#pragma unroll
-            for (int k = 0; k < KS; ++k) sum += red[((i >> 7) * KS + k) * 128 + (i & 127) + c2 - c];
-          }
-          ysum[t * nr + rr] = sum;
+    const int piece = lane & 7, first = (warp - kOutWarps) * 4 + (lane >> 3);
+    for (Ring r{z.stages, 0, 1}; w.more(); w.next(), r.advance()) {
+      ok = wait_bar(ok, &sh.empty[r.i], r.parity, a.status);
+      if (!ok) break;
+      // Columns: the tokens' high parts, then from a multiple of 8 on their low parts.
+      const uint32_t at = ring + r.i * z.stage_bytes + z.blocks * block;
+      const int kc = w.kc(), n = round_to(w.ntok, 8);
+      for (int i = first; i < w.ntok; i += 4 * kTokenWarps) {
+        const int64_t from = (w.i0 + i) * a.F + w.k0 + piece * 8;
+        const uint32_t dst = at + i * kRowBytes + ((piece ^ (i & 7)) << 4);
+        for (int b = 0; b * kBlock < kc; ++b) {
+          const bool in = b * kBlock + piece * 8 < kc;
+          copy16(dst + b * 2 * n * kRowBytes, in ? p.h_hi + from + b * kBlock : p.h_hi, in);
+          copy16(dst + (b * 2 + 1) * n * kRowBytes, in ? p.h_lo + from + b * kBlock : p.h_lo, in);
         }
       }
-      // All of them: multiply_stage may have rounded the number of tiles up.
+      arrive_after_copies(smem_u32(&sh.full[r.i]));
+    }
+  } else {
+    const int64_t tiles = gridDim.x / z.slices, tile_id = blockIdx.x / z.slices;
+    const int64_t r_end = a.H * (tile_id + 1) / tiles;
+    const int row = threadIdx.x;  // of the tile: this thread's sums, for every token
+    Ring d{2, 0, 0};
+    for (int64_t r0 = a.H * tile_id / tiles; r0 < r_end; r0 += z.rows) {
+      const int nr = r_end - r0 < z.rows ? (int)(r_end - r0) : z.rows;
+      if (row < nr)
+        for (int t = 0; t < a.T; ++t) ysum[t * nr + row] = 0.0f;
+      for (; w.more() && w.r0 == r0; w.next_pass(), d.advance()) {
+        ok = wait_bar(ok, &sh.sums_full[d.i], d.parity, a.status);
+        tmem_fence_after();
+        if (ok && warp * 32 < nr) {
+          const uint32_t at = sh.tmem + d.i * (z.cols / 2) + ((uint32_t)(warp * 32) << 16);
+          const int n = round_to(w.ntok, 8);
+          for (int c0 = 0; c0 < w.ntok; c0 += 8) {
+            float hi[8], lo[8];
+            __syncwarp();
+            tmem_load8(hi, at + c0);
+            tmem_load8(lo, at + n + c0);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+            for (int c = 0; c < 8; ++c)
+              if (row < nr && c0 + c < w.ntok) ysum[s.token[w.i0 + c0 + c] * nr + row] += hi[c] + lo[c];
+          }
+        }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.sums_empty[d.i]));
+      }
+      if (z.slices == 1 && row < nr) {
+        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + r0 + row;
+        for (int t = 0; t < a.T; ++t) y[t * a.H] = __float2bfloat16_rn(ysum[t * nr + row]);
+      }
     }
-    consumers_sync();
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  if (warp == kMulWarp) tmem_free(sh.tmem, z.cols);
+  if (z.slices > 1) {
+    // The cluster's CTAs hold sums over their slices of F for the same columns
+    // of y (one tile: the host cuts no more): each adds a share of them.
+    __syncwarp();
+    cluster_sync();
+    const int64_t tiles = gridDim.x / z.slices, tile_id = blockIdx.x / z.slices;
+    const int64_t r0 = a.H * tile_id / tiles;
+    const int nr = (int)(a.H * (tile_id + 1) / tiles - r0), all = a.T * nr, slice = blockIdx.x % z.slices;
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + r0;
-    for (int i = threadIdx.x; i < a.T * nr; i += kConsumers * kWarp) {
-      const int t = i / nr, rr = i - t * nr;
-      y[t * a.H + rr] = __float2bfloat16_rn(ysum[i]);
+    for (int i = all * slice / z.slices + threadIdx.x; i < all * (slice + 1) / z.slices; i += kStreamThreads) {
+      float sum = 0.0f;
+      for (int k = 0; k < z.slices; ++k) sum += load_peer(ysum + i, k);
+      y[i / nr * a.H + i % nr] = __float2bfloat16_rn(sum);
     }
-    consumers_sync();
+    __syncwarp();
+    cluster_sync();  // nobody leaves while its sums are read
   }
 }
 
@@ -828,54 +906,96 @@ bool tensor_map(CUtensorMap* map, const void* base, int64_t nx, int64_t ny, int6
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT, int MT>
-int launch_stream(const StreamArgs& p, const CUtensorMap& gate_up, const CUtensorMap& down, size_t seg, size_t ysum,
-                  cudaStream_t s) {
-  static std::atomic<int> granted_g[64], granted_d[64];
-  auto g = gate_up_stream_kernel<NT>;
-  auto d = down_stream_kernel<NT, MT>;
-  const size_t ring = (size_t)kStages * p.stage_bytes + 1024;
-  if (!allow_smem(g, (int)(ring + seg), granted_g) || !allow_smem(d, (int)(ring + seg + ysum), granted_d))
-    return MOE_ERR_CUDA;
-  const int64_t pairs = (p.a.n < p.a.E ? p.a.n : p.a.E) * p.a.F, sms = num_sms();
-  launch(g, (unsigned)(pairs < sms ? pairs : sms), kStreamThreads, ring + seg, s, p, gate_up);
-  launch(d, (unsigned)(p.a.H < sms ? p.a.H : sms), kStreamThreads, ring + seg + ysum, s, p, down);
-  return check_launch();
-}
+constexpr int kSmPairBytes = 112 * 1024;  // dynamic shared memory of a CTA when one of each kernel shares an SM
+constexpr int kSmBytes = 226 * 1024;
 
-template <int NT> int dispatch_stream(StreamArgs p, cudaStream_t s) {
-  const int64_t sms = num_sms();
-  const int64_t per_cta = (p.a.H + sms - 1) / sms;
-  const int MT = per_cta <= 16 ? 1 : (per_cta <= 32 ? 2 : 4);
-  p.down_rows = (int)(per_cta < 16 * MT ? per_cta : 16 * MT);
-  const size_t seg = segments_bytes(p.a.n, p.a.E);
-  const size_t ysum = sizeof(float) * p.a.T * p.down_rows;
-  // Up to 16 tokens: stages such that a CTA of each kernel fits on an SM
-  // together, so that the second kernel's first copies overlap the first's
-  // end. Beyond: as large as fit, for the tokens' rows beside the weights'.
-  p.stage_bytes = NT <= 2 ? 34816 : (int)((226304 - seg - ysum) / kStages / 1024 * 1024);
-  if (p.stage_bytes > 65536) p.stage_bytes = 65536;
-  p.gate_tokens = p.down_tokens = NT * 8;
-  while (p.gate_tokens > 8 && stage_blocks(p.stage_bytes, 32, p.gate_tokens) < 1) p.gate_tokens -= 8;
-  while (p.down_tokens > 8 && stage_blocks(p.stage_bytes, p.down_rows, 2 * p.down_tokens) < 1) p.down_tokens -= 8;
-  CUtensorMap gate_up, down;
-  if (!tensor_map(&gate_up, p.a.w_gate_up, p.a.H, p.a.F, 2 * (int64_t)p.a.E, 16, 2) ||
-      !tensor_map(&down, p.a.w_down, p.a.F, p.a.H, p.a.E, p.down_rows, 1))
-    return MOE_ERR_CUDA;
-  switch (MT) {
-    case 1: return launch_stream<NT, 1>(p, gate_up, down, seg, ysum, s);
-    case 2: return launch_stream<NT, 2>(p, gate_up, down, seg, ysum, s);
-    default: return launch_stream<NT, 4>(p, gate_up, down, seg, ysum, s);
+// Stages that fit beside `rest` bytes: sharing the SM where that leaves at least `least`.
+bool fit_stages(StreamShape* z, size_t rest, int least) {
+  for (const int budget : {kSmPairBytes, kSmBytes}) {
+    const int64_t n = ((int64_t)budget - (int64_t)sizeof(StreamShared) - 1024 - (int64_t)rest) / z->stage_bytes;
+    if (n < least && budget == kSmPairBytes) continue;
+    z->stages = (int)(n < kMaxStages ? n : kMaxStages);
+    return n >= 2;
   }
+  return false;
+}
+uint32_t tmem_cols(int cols) {
+  uint32_t c = 32;
+  while ((int)c < cols) c *= 2;
+  return c;
 }
 
 int run_stream(const LayerArgs& a, cudaStream_t s) {
+  static std::atomic<int> granted_g[64], granted_d[64];
   __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(a.h);
-  const StreamArgs p{a, h, h + (int64_t)a.n * a.F, 0, 0, 0, 0};
-  if (a.T <= 8) return dispatch_stream<1>(p, s);
-  if (a.T <= 16) return dispatch_stream<2>(p, s);
-  if (a.T <= 32) return dispatch_stream<4>(p, s);
-  return dispatch_stream<8>(p, s);
+  const StreamArgs p{a, h, h + (int64_t)a.n * a.F};
+  const int64_t sms = num_sms();
+  const size_t seg = segments_bytes(a.n, a.E);
+  CUtensorMap map;
+
+  StreamShape g{};
+  g.blocks = 1;
+  g.slices = 1;
+  g.rows = kTileRows;
+  g.tokens = a.T < kMaxTokens ? round_to(a.T, 16) : kMaxTokens;
+  g.cols = tmem_cols(2 * g.tokens);
+  g.stage_bytes = kTileRows * kRowBytes + g.tokens * kRowBytes;
+  if (!fit_stages(&g, seg, 4)) return MOE_ERR_UNSUPPORTED;
+  size_t smem = (size_t)g.stages * g.stage_bytes + seg + 1024;
+  if (!allow_smem(gate_up_stream_kernel, (int)smem, granted_g) ||
+      !tensor_map(&map, a.w_gate_up, a.H, a.F, 2 * (int64_t)a.E, 16, 2))
+    return MOE_ERR_CUDA;
+  const int64_t pairs = (a.n < a.E ? a.n : a.E) * a.F;
+  launch(gate_up_stream_kernel, (unsigned)(pairs < sms ? pairs : sms), kStreamThreads, smem, s, p, g, map);
+
+  // Rows of a tile: an SM's share of H where that is 54 or more; below, two or
+  // four SMs share a tile's F between them, since a product takes the time of
+  // 128 rows whatever it holds and every tile reads all of h.
+  StreamShape d{};
+  d.tokens = a.T < kMaxTokens ? round_to(a.T, 8) : kMaxTokens;
+  d.cols = tmem_cols(4 * d.tokens);
+  int64_t grid = 0;
+  bool fits = false;
+  for (int slices = 4, cap = kTileRows; !fits && cap >= 64;) {
+    const int64_t tiles = sms / slices < a.H ? sms / slices : a.H;
+    const int64_t share = (a.H + tiles - 1) / tiles;
+    if (share <= cap || slices == 1) {
+      d.slices = slices;
+      d.rows = (int)(share < cap ? share : cap);
+      grid = tiles * slices;
+      const int block = round_to(d.rows, 8) * kRowBytes;
+      d.blocks = kTileRows * kRowBytes / (block + 2 * d.tokens * kRowBytes);
+      if (d.blocks < 1) d.blocks = 1;
+      d.stage_bytes = d.blocks * (block + 2 * d.tokens * kRowBytes);
+      // A product's 128 rows from the last block on stay inside the CTA's memory.
+      smem = seg + sizeof(float) * a.T * d.rows;
+      if (smem < kTileRows * kRowBytes) smem = kTileRows * kRowBytes;
+      fits = fit_stages(&d, smem, 4);
+    }
+    if (slices > 1)
+      slices /= 2;
+    else
+      cap /= 2;  // sums of 256 tokens by 128 rows and the ring: too much for an SM
+  }
+  if (!fits) return MOE_ERR_UNSUPPORTED;
+  smem += (size_t)d.stages * d.stage_bytes + 1024;
+  if (!allow_smem(down_stream_kernel, (int)smem, granted_d) ||
+      !tensor_map(&map, a.w_down, a.F, a.H, a.E, d.rows, 1))
+    return MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kStreamThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)d.slices, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = d.slices > 1 ? 2 : 1;
+  (void)cudaLaunchKernelEx(&cfg, down_stream_kernel, p, d, map);
+  return check_launch();
 }
 
 template <typename ET>
