@@ -140,43 +140,62 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / kWarp;
 constexpr int kCols = 4;
 
+// Router logits: a CTA takes kRouterRows experts by kCols tokens (16 products
+// of 8 loaded vectors), its warps slices of H.
+constexpr int kRouterRows = 4;
 template <int VB, typename ET>
 __global__ void __launch_bounds__(kThreads)
     router_rows_kernel(const void* __restrict__ x, int64_t x_stride, const void* __restrict__ router, int64_t H, int32_t T,
                        int32_t E, float* __restrict__ logits) {
   using L = Lanes<VB, ET>;
   using V = typename L::V;
+  __shared__ float part[kWarps][kRouterRows * kCols];
   await_previous_kernel();
-  const int lane = lane_id();
-  const int tiles = (T + kCols - 1) / kCols;
+  const int lane = lane_id(), warp = threadIdx.x / kWarp;
+  const int e0 = (int)blockIdx.x * kRouterRows, t0 = (int)blockIdx.y * kCols;
   const int64_t vecs = H / L::kElems;
-  for (int64_t w = (int64_t)blockIdx.x * kWarps + threadIdx.x / kWarp; w < (int64_t)tiles * E;
-       w += (int64_t)gridDim.x * kWarps) {
-    const int e = (int)(w % E), t0 = (int)(w / E) * kCols;
-    const V* r = reinterpret_cast<const V*>(static_cast<const ET*>(router) + e * H);
-    const V* px[kCols];
-    float acc[kCols];
+  const V* pr[kRouterRows];
+  const V* px[kCols];
+  float acc[kRouterRows][kCols];
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) {
-      const int t = t0 + c < T ? t0 + c : T - 1;
-      px[c] = reinterpret_cast<const V*>(static_cast<const ET*>(x) + t * x_stride);
-      acc[c] = 0.0f;
-    }
-#pragma unroll 2
-    for (int64_t i = lane; i < vecs; i += kWarp) {
-      const V rv = ld_l1(r + i);
+  for (int r = 0; r < kRouterRows; ++r) {  // past the end: the last expert or token again
+    pr[r] = reinterpret_cast<const V*>(static_cast<const ET*>(router) + (int64_t)(e0 + r < E ? e0 + r : E - 1) * H);
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) acc[r][c] = 0.0f;
+  }
+#pragma unroll
+  for (int c = 0; c < kCols; ++c)
+    px[c] = reinterpret_cast<const V*>(static_cast<const ET*>(x) + (t0 + c < T ? t0 + c : T - 1) * x_stride);
+  for (int64_t i = threadIdx.x; i < vecs; i += kThreads) {
+    V rv[kRouterRows], xv[kCols];
+#pragma unroll
+    for (int r = 0; r < kRouterRows; ++r) rv[r] = ld_l1(pr[r] + i);
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) xv[c] = ld_l1(px[c] + i);
+#pragma unroll
+    for (int r = 0; r < kRouterRows; ++r) {
 #pragma unroll
       for (int c = 0; c < kCols; ++c) {
-        const V xv = ld_l1(px[c] + i);
 #pragma unroll
-        for (int q = 0; q < L::kElems; ++q) acc[c] += L::get(rv, q) * L::get(xv, q);
+        for (int q = 0; q < L::kElems; ++q) acc[r][c] += L::get(rv[r], q) * L::get(xv[c], q);
       }
     }
+  }
+#pragma unroll
+  for (int r = 0; r < kRouterRows; ++r) {
 #pragma unroll
     for (int c = 0; c < kCols; ++c) {
-      const float s = warp_sum(acc[c]);
-      if (lane == 0 && t0 + c < T) logits[(int64_t)(t0 + c) * E + e] = s;
+      const float s = warp_sum(acc[r][c]);
+      if (lane == 0) part[warp][r * kCols + c] = s;
     }
+  }
+  __syncthreads();
+  if (threadIdx.x < kRouterRows * kCols) {
+    const int r = threadIdx.x / kCols, c = threadIdx.x % kCols;
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += part[w][threadIdx.x];
+    if (e0 + r < E && t0 + c < T) logits[(int64_t)(t0 + c) * E + e0 + r] = s;
   }
 }
 
@@ -320,7 +339,6 @@ constexpr int kMaxStages = 8;
 constexpr int kBlock = 64;       // elements of a block: the 128 bytes of a swizzled row
 constexpr int kRowBytes = 128;
 constexpr int kTileRows = 128;   // weight rows of a product
-constexpr int kPairs = 64;       // gate/up row pairs of a tile
 constexpr int kMaxTokens = 64;   // of an expert at a time
 constexpr uint64_t kWaitNs = 2000000000;  // after which a wait gives up
 
@@ -423,7 +441,7 @@ struct StreamArgs {
 struct StreamShape {
   int stages, stage_bytes, blocks;  // blocks of 64 elements in a stage
   int tokens;                       // of an expert at a time (a multiple of 16, the products' columns; 8 in the second kernel)
-  int rows;                         // second kernel: weight rows of a tile
+  int rows;                         // weight rows of a tile (first kernel: two for each gate/up pair)
   int slices;                       // second kernel: CTAs of a cluster, which share a tile's elements
   uint32_t cols;                    // tensor memory columns
 };
@@ -521,15 +539,15 @@ __device__ __forceinline__ void multiply(WALK w, StreamShared& sh, const StreamS
   for (int i = 0; i < z.stages; ++i) ok = wait_bar(ok, &sh.empty[i], i < r.i ? r.parity : r.parity ^ 1, status);
 }
 
-// Tiles of up to 64 row pairs (gate, up) of one expert by up to z.tokens of
-// its tokens, over the whole of H. A box has 16 pairs: those beyond a CTA's
+// Tiles of up to z.rows / 2 row pairs (gate, up) of one expert by up to
+// z.tokens of its tokens, over the whole of H. A box has 16 pairs: those beyond a CTA's
 // share are read too (their owner reads them as well) and left.
 struct GateUpWalk {
   const Segments& s;
   int64_t pos, end, F, f0;
-  int q, nf, i0, ntok, K, k0, per_stage, per_pass;
+  int q, nf, i0, ntok, K, k0, per_stage, per_pass, pairs;
   __device__ GateUpWalk(const Segments& s_, const LayerArgs& a, const StreamShape& z)
-      : s(s_), F(a.F), K((int)a.H), per_stage(z.blocks * kBlock), per_pass(z.tokens) {
+      : s(s_), F(a.F), K((int)a.H), per_stage(z.blocks * kBlock), per_pass(z.tokens), pairs(z.rows / 2) {
     const int64_t rows = s.active * F;
     pos = rows * blockIdx.x / gridDim.x;
     end = rows * (blockIdx.x + 1) / gridDim.x;
@@ -540,7 +558,7 @@ struct GateUpWalk {
     q = (int)(pos / F);
     f0 = pos - q * F;
     const int64_t m = end - pos < F - f0 ? end - pos : F - f0;
-    nf = m < kPairs ? (int)m : kPairs;
+    nf = m < pairs ? (int)m : pairs;
     i0 = s.begin[q];
     pass();
   }
@@ -565,12 +583,12 @@ struct GateUpWalk {
   }
 };
 
-__global__ void __launch_bounds__(kStreamThreads, 2)
+__global__ void __launch_bounds__(kStreamThreads)
     gate_up_stream_kernel(StreamArgs p, StreamShape z, const __grid_constant__ CUtensorMap map) {
   extern __shared__ __align__(1024) unsigned char dyn[];
   __shared__ StreamShared sh;
-  constexpr int kBytes = kTileRows * kRowBytes;  // of a block of weights
   const LayerArgs& a = p.a;
+  const int block = z.rows * kRowBytes;
   await_previous_kernel();
   const int warp = threadIdx.x / kWarp, lane = lane_id();
   if (warp == kMulWarp) tmem_alloc(smem_u32(&sh.tmem), z.cols);
@@ -595,19 +613,19 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         mbar_expect(bar, n * boxes * 32 * kRowBytes);
         for (int b = 0; b < n; ++b)
           for (int g = 0; g < boxes; ++g)
-            tensor_copy(at + b * kBytes + g * 32 * kRowBytes, &map, w.k0 + b * kBlock, (int)w.f0 + g * 16, 2 * e, bar);
+            tensor_copy(at + b * block + g * 32 * kRowBytes, &map, w.k0 + b * kBlock, (int)w.f0 + g * 16, 2 * e, bar);
       }
     }
   } else if (warp == kMulWarp) {
-    multiply(w, sh, z, ring, kBytes, a.status, [](const GateUpWalk& v) { return round_to(v.ntok, 16); },
-             [&](const GateUpWalk&) { return z.blocks * kBytes; });
+    multiply(w, sh, z, ring, block, a.status, [](const GateUpWalk& v) { return round_to(v.ntok, 16); },
+             [&](const GateUpWalk&) { return z.blocks * block; });
   } else if (warp >= kOutWarps) {
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x);
     const int piece = lane & 7, first = (warp - kOutWarps) * 4 + (lane >> 3);
     for (Ring r{z.stages, 0, 1}; w.more(); w.next(), r.advance()) {
       ok = wait_bar(ok, &sh.empty[r.i], r.parity, a.status);
       if (!ok) break;
-      const uint32_t at = ring + r.i * z.stage_bytes + z.blocks * kBytes;
+      const uint32_t at = ring + r.i * z.stage_bytes + z.blocks * block;
       const int kc = w.kc(), n = round_to(w.ntok, 16);
       for (int i = first; i < w.ntok; i += 4 * kTokenWarps) {
         const __nv_bfloat16* src = x + s.token[w.i0 + i] * a.x_stride + w.k0 + piece * 8;
@@ -720,14 +738,15 @@ __device__ __forceinline__ float load_peer(const float* p, uint32_t rank) {
   return v;
 }
 
-__global__ void __launch_bounds__(kStreamThreads, 2)
+__global__ void __launch_bounds__(kStreamThreads)
     down_stream_kernel(StreamArgs p, StreamShape z, const __grid_constant__ CUtensorMap map) {
   extern __shared__ __align__(1024) unsigned char dyn[];
   __shared__ StreamShared sh;
   const LayerArgs& a = p.a;
   const int warp = threadIdx.x / kWarp, lane = lane_id();
   // The gate/up kernel has waited for all before it, so the routing may be
-  // read and weights copied while it still runs; h may not.
+  // read and weights copied while it still runs (a CTA starts as one of the
+  // other kernel leaves its SM); h may not be read.
   if (warp == kMulWarp) tmem_alloc(smem_u32(&sh.tmem), z.cols);
   if (threadIdx.x == kCopyWarp * kWarp) init_shared(sh, z.stages);
   const uint32_t ring = align_1k(smem_u32(dyn));
@@ -856,9 +875,8 @@ int run_router(const LayerArgs& a, const void* router, float* logits, int32_t mo
                int32_t* top_expert, float* weights, cudaStream_t s) {
   if (router == nullptr) return MOE_OK;
   auto k = router_rows_kernel<VB, ET>;
-  const int64_t warps = (int64_t)((a.T + kCols - 1) / kCols) * a.E;
-  launch(k, persistent_grid(k, kThreads, 0, (warps + kWarps - 1) / kWarps), kThreads, 0, s, a.x, a.x_stride, router,
-         a.H, a.T, a.E, logits);
+  launch(k, dim3((unsigned)((a.E + kRouterRows - 1) / kRouterRows), (unsigned)((a.T + kCols - 1) / kCols)), kThreads, 0, s,
+         a.x, a.x_stride, router, a.H, a.T, a.E, logits);
   return moe_topk_gating(logits, a.T, a.E, a.K, mode, normalize, top_expert, weights,
                          reinterpret_cast<moe_stream_t>(s));
 }
@@ -906,23 +924,27 @@ bool tensor_map(CUtensorMap* map, const void* base, int64_t nx, int64_t ny, int6
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kSmPairBytes = 112 * 1024;  // dynamic shared memory of a CTA when one of each kernel shares an SM
-constexpr int kSmBytes = 226 * 1024;
+constexpr int kSmBytes = 226 * 1024;  // dynamic shared memory of a CTA at most, beside its static part
 
-// Stages that fit beside `rest` bytes: sharing the SM where that leaves at least `least`.
-bool fit_stages(StreamShape* z, size_t rest, int least) {
-  for (const int budget : {kSmPairBytes, kSmBytes}) {
-    const int64_t n = ((int64_t)budget - (int64_t)sizeof(StreamShared) - 1024 - (int64_t)rest) / z->stage_bytes;
-    if (n < least && budget == kSmPairBytes) continue;
-    z->stages = (int)(n < kMaxStages ? n : kMaxStages);
-    return n >= 2;
-  }
-  return false;
+// Stages of stage_bytes that fit beside `rest` bytes; false for fewer than two.
+bool fit_stages(StreamShape* z, size_t rest) {
+  const int64_t n = ((int64_t)kSmBytes - (int64_t)sizeof(StreamShared) - 1024 - (int64_t)rest) / z->stage_bytes;
+  z->stages = (int)(n < kMaxStages ? n : kMaxStages);
+  return n >= 2;
 }
 uint32_t tmem_cols(int cols) {
   uint32_t c = 32;
   while ((int)c < cols) c *= 2;
   return c;
+}
+
+// Blocks of a stage, `most` or as many fewer as leave three stages (two with one block).
+bool cut_stages(StreamShape* z, int block_bytes, int most, size_t rest) {
+  for (z->blocks = most; z->blocks >= 1; --z->blocks) {
+    z->stage_bytes = z->blocks * block_bytes;
+    if (fit_stages(z, rest) && (z->stages >= 3 || z->blocks == 1)) return true;
+  }
+  return false;
 }
 
 int run_stream(const LayerArgs& a, cudaStream_t s) {
@@ -931,61 +953,68 @@ int run_stream(const LayerArgs& a, cudaStream_t s) {
   const StreamArgs p{a, h, h + (int64_t)a.n * a.F};
   const int64_t sms = num_sms();
   const size_t seg = segments_bytes(a.n, a.E);
-  CUtensorMap map;
+  // Tokens of an expert at a time: twice the mean and 16, so that few experts
+  // take a second pass over their weights and stages hold weights in the main.
+  const int cap = 2 * a.n / a.E + 16 < kMaxTokens ? round_to(2 * a.n / a.E + 16, 16) : kMaxTokens;
 
+  // Blocks of a stage: consecutive 128-byte pieces of a row, which the memory
+  // delivers better the more there are (the first kernel's weights of the
+  // Mixtral-8x7B shape, 8 tokens: 5.7 TB/s with one block, 6.6 with three; 64
+  // rows and four blocks: 6.7, but 5.3 instead of 5.9 at one token).
   StreamShape g{};
-  g.blocks = 1;
   g.slices = 1;
   g.rows = kTileRows;
-  g.tokens = a.T < kMaxTokens ? round_to(a.T, 16) : kMaxTokens;
+  g.tokens = round_to(a.T, 16) < cap ? round_to(a.T, 16) : cap;
   g.cols = tmem_cols(2 * g.tokens);
-  g.stage_bytes = kTileRows * kRowBytes + g.tokens * kRowBytes;
-  if (!fit_stages(&g, seg, 4)) return MOE_ERR_UNSUPPORTED;
-  size_t smem = (size_t)g.stages * g.stage_bytes + seg + 1024;
-  if (!allow_smem(gate_up_stream_kernel, (int)smem, granted_g) ||
-      !tensor_map(&map, a.w_gate_up, a.H, a.F, 2 * (int64_t)a.E, 16, 2))
-    return MOE_ERR_CUDA;
-  const int64_t pairs = (a.n < a.E ? a.n : a.E) * a.F;
-  launch(gate_up_stream_kernel, (unsigned)(pairs < sms ? pairs : sms), kStreamThreads, smem, s, p, g, map);
+  if (!cut_stages(&g, (g.rows + g.tokens) * kRowBytes, 3, seg)) return MOE_ERR_UNSUPPORTED;
+  const size_t g_smem = seg + (size_t)g.stages * g.stage_bytes + 1024;
 
-  // Rows of a tile: an SM's share of H where that is 54 or more; below, two or
-  // four SMs share a tile's F between them, since a product takes the time of
-  // 128 rows whatever it holds and every tile reads all of h.
+  // Pairs of SMs share a tile's F between them where the tile then has at most
+  // 128 rows: every tile reads all of h, and a tile of few rows copies little
+  // per instruction. (Four SMs a tile leave some of them idle, since their
+  // clusters do not fill the chip: 84 instead of 46 us for one token's second
+  // kernel at the Mixtral-8x7B shape.) Stages of up to 64 KB, for the reason
+  // above: 48 tokens of the Mixtral-8x22B shape 3.9 TB/s at 32 KB, 6.2 at 64.
   StreamShape d{};
-  d.tokens = a.T < kMaxTokens ? round_to(a.T, 8) : kMaxTokens;
+  d.tokens = round_to(a.T, 8) < cap ? round_to(a.T, 8) : cap;
   d.cols = tmem_cols(4 * d.tokens);
   int64_t grid = 0;
+  size_t d_smem = 0;
   bool fits = false;
-  for (int slices = 4, cap = kTileRows; !fits && cap >= 64;) {
+  for (int slices = 2, most = kTileRows; !fits && most >= 64;) {
     const int64_t tiles = sms / slices < a.H ? sms / slices : a.H;
     const int64_t share = (a.H + tiles - 1) / tiles;
-    if (share <= cap || slices == 1) {
+    if (tiles >= 1 && (share <= most || slices == 1)) {
       d.slices = slices;
-      d.rows = (int)(share < cap ? share : cap);
+      d.rows = (int)(share < most ? share : most);
       grid = tiles * slices;
-      const int block = round_to(d.rows, 8) * kRowBytes;
-      d.blocks = kTileRows * kRowBytes / (block + 2 * d.tokens * kRowBytes);
-      if (d.blocks < 1) d.blocks = 1;
-      d.stage_bytes = d.blocks * (block + 2 * d.tokens * kRowBytes);
-      // A product's 128 rows from the last block on stay inside the CTA's memory.
-      smem = seg + sizeof(float) * a.T * d.rows;
-      if (smem < kTileRows * kRowBytes) smem = kTileRows * kRowBytes;
-      fits = fit_stages(&d, smem, 4);
+      const int block = (round_to(d.rows, 8) + 2 * d.tokens) * kRowBytes;
+      // A product reads 128 rows from a block's start whatever the tile holds:
+      // behind the ring lie at least as many bytes of the CTA's memory.
+      d_smem = seg + sizeof(float) * a.T * d.rows;
+      if (d_smem < kTileRows * kRowBytes) d_smem = kTileRows * kRowBytes;
+      fits = cut_stages(&d, block, block < 65536 ? 65536 / block : 1, d_smem);
     }
     if (slices > 1)
       slices /= 2;
     else
-      cap /= 2;  // sums of 256 tokens by 128 rows and the ring: too much for an SM
+      most /= 2;  // sums of 256 tokens by 128 rows and the ring: too much for an SM
   }
   if (!fits) return MOE_ERR_UNSUPPORTED;
-  smem += (size_t)d.stages * d.stage_bytes + 1024;
-  if (!allow_smem(down_stream_kernel, (int)smem, granted_d) ||
-      !tensor_map(&map, a.w_down, a.F, a.H, a.E, d.rows, 1))
+  d_smem += (size_t)d.stages * d.stage_bytes + 1024;
+
+  CUtensorMap g_map, d_map;
+  if (!allow_smem(gate_up_stream_kernel, (int)g_smem, granted_g) ||
+      !allow_smem(down_stream_kernel, (int)d_smem, granted_d) ||
+      !tensor_map(&g_map, a.w_gate_up, a.H, a.F, 2 * (int64_t)a.E, 16, 2) ||
+      !tensor_map(&d_map, a.w_down, a.F, a.H, a.E, d.rows, 1))
     return MOE_ERR_CUDA;
+  const int64_t pairs = (a.n < a.E ? a.n : a.E) * a.F;
+  launch(gate_up_stream_kernel, (unsigned)(pairs < sms ? pairs : sms), kStreamThreads, g_smem, s, p, g, g_map);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kStreamThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = d_smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -994,7 +1023,7 @@ int run_stream(const LayerArgs& a, cudaStream_t s) {
   attr[1].val.clusterDim = {(unsigned)d.slices, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = d.slices > 1 ? 2 : 1;
-  (void)cudaLaunchKernelEx(&cfg, down_stream_kernel, p, d, map);
+  (void)cudaLaunchKernelEx(&cfg, down_stream_kernel, p, d, d_map);
   return check_launch();
 }
 
