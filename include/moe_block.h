@@ -107,8 +107,8 @@ int moe_layer_norm_bwd(const void* dy, int64_t dy_stride, const void* x, int32_t
  * (then nothing is written while the coefficient is 1). Apart from that no
  * out may overlap a grad or another out.
  *   norm [1] fp32 out;
- *   workspace >= moe_grad_norm_workspace_size() bytes (for the current
- *   device), 8-byte aligned, contents need no initialisation.
+ *   workspace >= moe_grad_norm_workspace_size() bytes, 8-byte aligned,
+ *   contents need no initialisation.
  * The sum has a fixed order on a device: repeated calls give the same bits.
  */
 typedef struct moe_grad_tensor {

@@ -12,9 +12,18 @@ from typing import Sequence
 import torch
 
 from . import _lib
-from .ops import _act_dtype, _need, _ptr, _stream
+from .ops import _act_dtype, _need
 
 _MODES = {"softmax": _lib.MOE_GATING_SOFTMAX, "sigmoid": _lib.MOE_GATING_SIGMOID}
+
+
+def _stream(device: torch.device) -> int:
+    # torch.cuda.current_stream(device).cuda_stream without building the Stream object (2 us).
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _ptr(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
 
 
 def _rows(t: torch.Tensor, name: str, dtype: torch.dtype | None = None, shape=None, device=None) -> int:
@@ -29,11 +38,12 @@ def _rows(t: torch.Tensor, name: str, dtype: torch.dtype | None = None, shape=No
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if device is not None and t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    stride, inner = t.stride()
-    if t.shape[1] > 1 and inner != 1:
-        raise ValueError("%s must have contiguous rows" % name)
-    if t.shape[0] > 1 and stride < t.shape[1]:
-        raise ValueError("%s must have rows that do not overlap" % name)
+    stride = t.stride(0)
+    if not t.is_contiguous():
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError("%s must have contiguous rows" % name)
+        if t.shape[0] > 1 and stride < t.shape[1]:
+            raise ValueError("%s must have rows that do not overlap" % name)
     return stride
 
 
@@ -41,6 +51,23 @@ def _shape(t: torch.Tensor, shape: tuple, name: str) -> torch.Tensor:
     if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
     return t
+
+
+def _out(t: torch.Tensor | None, shape: tuple, dtype: torch.dtype, name: str, device) -> torch.Tensor:
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _shape(_need(t, dtype, name, device), shape, name)
+
+
+def _workspace(t: torch.Tensor | None, size: int, device) -> torch.Tensor:
+    if t is None:
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    return _need(t, torch.uint8, "workspace", device)
+
+
+def _status(t: torch.Tensor | None, device) -> int | None:
+    return None if t is None else _need(t, torch.int32, "status", device).data_ptr()
 
 
 def _expert_weights(x, w_gate_up, w_down):
@@ -77,19 +104,14 @@ def moe_layer(x: torch.Tensor, router: torch.Tensor, w_gate_up: torch.Tensor, w_
     _shape(_need(router, x.dtype, "router", dev), (E, H), "router")
     if mode not in _MODES:
         raise ValueError("mode must be softmax or sigmoid, got %r" % (mode,))
-    if routing is None:
-        routing = (torch.empty((T, top_k), dtype=torch.int32, device=dev),
-                   torch.empty((T, top_k), dtype=torch.float32, device=dev))
-    te = _shape(_need(routing[0], torch.int32, "top_expert", dev), (T, top_k), "top_expert")
-    w = _shape(_need(routing[1], torch.float32, "weights", dev), (T, top_k), "weights")
-    if out is None:
-        out = torch.empty((T, H), dtype=x.dtype, device=dev)
-    _shape(_need(out, x.dtype, "out", dev), (T, H), "out")
-    ws = workspace if workspace is not None else layer_workspace(T, H, F, E, top_k, dev)
-    _need(ws, torch.uint8, "workspace", dev)
-    _lib.call("moe_layer", _ptr(x), dt, stride, _ptr(router), _ptr(w_gate_up), _ptr(w_down), T, H, F, E, top_k,
-              _MODES[mode], int(bool(normalize)), _ptr(te), _ptr(w), _ptr(out), _ptr(ws), ws.numel(), _ptr(status),
-              _stream(x))
+    te, w = (None, None) if routing is None else routing
+    te = _out(te, (T, top_k), torch.int32, "top_expert", dev)
+    w = _out(w, (T, top_k), torch.float32, "weights", dev)
+    out = _out(out, (T, H), x.dtype, "out", dev)
+    ws = _workspace(workspace, _lib.load().moe_layer_workspace_size(T, H, F, E, top_k), dev)
+    _lib.call("moe_layer", x.data_ptr(), dt, stride, router.data_ptr(), w_gate_up.data_ptr(), w_down.data_ptr(), T, H, F,
+              E, top_k, _MODES[mode], int(bool(normalize)), te.data_ptr(), w.data_ptr(), out.data_ptr(), ws.data_ptr(),
+              ws.numel(), _status(status, dev), _stream(dev))
     return out, te, w
 
 
@@ -109,13 +131,11 @@ def moe_experts(x: torch.Tensor, top_expert: torch.Tensor, weights: torch.Tensor
         raise ValueError("top_expert must be [%d, top_k], got %s" % (T, list(top_expert.shape)))
     K = top_expert.shape[1]
     _shape(_need(weights, torch.float32, "weights", dev), (T, K), "weights")
-    if out is None:
-        out = torch.empty((T, H), dtype=x.dtype, device=dev)
-    _shape(_need(out, x.dtype, "out", dev), (T, H), "out")
-    ws = workspace if workspace is not None else layer_workspace(T, H, F, E, K, dev)
-    _need(ws, torch.uint8, "workspace", dev)
-    _lib.call("moe_experts", _ptr(x), dt, stride, _ptr(top_expert), _ptr(weights), _ptr(w_gate_up), _ptr(w_down), T, H,
-              F, E, K, _ptr(out), _ptr(ws), ws.numel(), _ptr(status), _stream(x))
+    out = _out(out, (T, H), x.dtype, "out", dev)
+    ws = _workspace(workspace, _lib.load().moe_layer_workspace_size(T, H, F, E, K), dev)
+    _lib.call("moe_experts", x.data_ptr(), dt, stride, top_expert.data_ptr(), weights.data_ptr(), w_gate_up.data_ptr(),
+              w_down.data_ptr(), T, H, F, E, K, out.data_ptr(), ws.data_ptr(), ws.numel(), _status(status, dev),
+              _stream(dev))
     return out
 
 
@@ -142,15 +162,12 @@ def moe_layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias
     dev = x.device
     M, H = x.shape
     wdt = _affine(weight, bias, H, dev)
-    if out is None:
-        out = torch.empty((M, H), dtype=x.dtype, device=dev)
-    _shape(_need(out, x.dtype, "out", dev), (M, H), "out")
-    if stats is None:
-        stats = torch.empty((2, M), dtype=torch.float32, device=dev).unbind(0)
-    mean = _shape(_need(stats[0], torch.float32, "mean", dev), (M,), "mean")
-    rstd = _shape(_need(stats[1], torch.float32, "rstd", dev), (M,), "rstd")
-    _lib.call("moe_layer_norm_fwd", _ptr(x), dt, stride, _ptr(weight), _ptr(bias), wdt, M, H, eps, _ptr(out),
-              _ptr(mean), _ptr(rstd), _stream(x))
+    out = _out(out, (M, H), x.dtype, "out", dev)
+    mean, rstd = (None, None) if stats is None else stats
+    mean = _out(mean, (M,), torch.float32, "mean", dev)
+    rstd = _out(rstd, (M,), torch.float32, "rstd", dev)
+    _lib.call("moe_layer_norm_fwd", x.data_ptr(), dt, stride, _ptr(weight), _ptr(bias), wdt, M, H, eps, out.data_ptr(),
+              mean.data_ptr(), rstd.data_ptr(), _stream(dev))
     return out, mean, rstd
 
 
@@ -171,20 +188,15 @@ def moe_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor |
         weight_dtype = weight.dtype
     wdt = weight_dtype or torch.float32
     code = _affine(weight, None, H, dev) if weight is not None else _lib.MOE_BF16 if wdt == torch.bfloat16 else _lib.MOE_F32
-    if out is None:
-        out = torch.empty((M, H), dtype=x.dtype, device=dev)
-    _shape(_need(out, x.dtype, "out", dev), (M, H), "out")
+    out = _out(out, (M, H), x.dtype, "out", dev)
     dw = db = ws = None
     if need_cols:
-        dw, db = torch.empty((2, H), dtype=wdt, device=dev).unbind(0)
-        ws = workspace
-        if ws is None:
-            with torch.cuda.device(dev):  # sized for this device's SM count
-                size = _lib.load().moe_layer_norm_bwd_workspace_size(M, H)
-            ws = torch.empty(size, dtype=torch.uint8, device=dev)
-        _need(ws, torch.uint8, "workspace", dev)
-    _lib.call("moe_layer_norm_bwd", _ptr(dy), dy_stride, _ptr(x), dt, stride, _ptr(weight), code, _ptr(mean),
-              _ptr(rstd), M, H, _ptr(out), _ptr(dw), _ptr(db), _ptr(ws), 0 if ws is None else ws.numel(), _stream(x))
+        dw = torch.empty(H, dtype=wdt, device=dev)
+        db = torch.empty(H, dtype=wdt, device=dev)
+        ws = _workspace(workspace, _lib.load().moe_layer_norm_bwd_workspace_size(M, H), dev)
+    _lib.call("moe_layer_norm_bwd", dy.data_ptr(), dy_stride, x.data_ptr(), dt, stride, _ptr(weight), code,
+              mean.data_ptr(), rstd.data_ptr(), M, H, out.data_ptr(), _ptr(dw), _ptr(db), _ptr(ws),
+              0 if ws is None else ws.numel(), _stream(dev))
     return out, dw, db
 
 
@@ -216,8 +228,7 @@ class GradSet:
         host = torch.empty(max(1, self.pieces) * size, dtype=torch.uint8)
         _lib.call("moe_grad_table_fill", entries, len(entries), host.data_ptr(), self.pieces)
         self.table = host.to(dev)
-        with torch.cuda.device(dev):  # sized for this device's SM count
-            self.workspace_bytes = lib.moe_grad_norm_workspace_size()
+        self.workspace_bytes = lib.moe_grad_norm_workspace_size()
 
 
 def moe_grad_set(grads: Sequence[torch.Tensor], outs: Sequence[torch.Tensor] | None = None) -> GradSet:
@@ -229,21 +240,17 @@ def _grad_args(grads, norm, workspace):
     s = grads if isinstance(grads, GradSet) else GradSet(grads)
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=s.device)
-    _need(norm, torch.float32, "norm", s.device)
-    if norm.numel() != 1:
+    elif _need(norm, torch.float32, "norm", s.device).numel() != 1:
         raise ValueError("norm must have one element, has %d" % norm.numel())
-    ws = workspace
-    if ws is None:
-        ws = torch.empty(s.workspace_bytes, dtype=torch.uint8, device=s.device)
-    _need(ws, torch.uint8, "workspace", s.device)
-    return s, norm, ws
+    return s, norm, _workspace(workspace, s.workspace_bytes, s.device)
 
 
 def moe_grad_norm(grads: GradSet | Sequence[torch.Tensor], norm: torch.Tensor | None = None,
                   workspace: torch.Tensor | None = None) -> torch.Tensor:
     """2-norm over all elements of all gradients, fp32 on the device."""
     s, norm, ws = _grad_args(grads, norm, workspace)
-    _lib.call("moe_grad_norm", _ptr(s.table), s.pieces, _ptr(norm), _ptr(ws), ws.numel(), _stream(s.table))
+    _lib.call("moe_grad_norm", s.table.data_ptr(), s.pieces, norm.data_ptr(), ws.data_ptr(), ws.numel(),
+              _stream(s.device))
     return norm
 
 
@@ -252,5 +259,6 @@ def moe_clip_grads(grads: GradSet | Sequence[torch.Tensor], max_norm: float, nor
     """Scales the gradients by min(1, max_norm / (norm + 1e-6)), into the
     set's outs or in place, and returns their norm before that."""
     s, norm, ws = _grad_args(grads, norm, workspace)
-    _lib.call("moe_clip_grads", _ptr(s.table), s.pieces, max_norm, _ptr(norm), _ptr(ws), ws.numel(), _stream(s.table))
+    _lib.call("moe_clip_grads", s.table.data_ptr(), s.pieces, max_norm, norm.data_ptr(), ws.data_ptr(), ws.numel(),
+              _stream(s.device))
     return norm

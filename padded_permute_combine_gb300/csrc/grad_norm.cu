@@ -26,6 +26,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int64_t kPieceBytes = 65536;
 constexpr int kCtasPerSm = 4;
+constexpr int kMaxCtas = 1024;  // a partial sum each
 
 // Plain (not read-only-path) loads: the scaling pass may write in place.
 __device__ __forceinline__ u32x8 ld_vec(const u32x8* p) {
@@ -210,7 +211,8 @@ bool valid(const moe_grad_tensor& t) {
 }
 
 int grid_of(int64_t P) {
-  const int64_t g = (int64_t)num_sms() * kCtasPerSm;
+  int64_t g = (int64_t)num_sms() * kCtasPerSm;
+  if (g > kMaxCtas) g = kMaxCtas;
   return (int)(P < g ? (P < 1 ? 1 : P) : g);
 }
 
@@ -250,7 +252,7 @@ extern "C" int moe_grad_table_fill(const moe_grad_tensor* tensors, int64_t n, mo
   return MOE_OK;
 }
 
-extern "C" size_t moe_grad_norm_workspace_size(void) { return (size_t)num_sms() * kCtasPerSm * sizeof(double); }
+extern "C" size_t moe_grad_norm_workspace_size(void) { return kMaxCtas * sizeof(double); }
 
 extern "C" int moe_grad_norm(const moe_grad_piece* pieces, int64_t P, float* norm, void* workspace, size_t bytes,
                              moe_stream_t stream) {

@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(512) cols_kernel(const float* __restrict__ par
 // ------------------------------------------------------------------ host
 
 constexpr int kRowWarps = 8;     // rows per CTA when a warp takes a row
-constexpr int kBwdCtasPerSm = 2; // CTAs that write partial column sums
+constexpr int kMaxParts = 304;   // CTAs of the backward pass, each with a row of partial column sums
 
 struct RowShape {
   bool warp_row;
@@ -413,10 +413,7 @@ RowShape row_shape(int64_t vecs, int max_nv, int want_threads, int max_threads) 
   return {false, 0, 0};
 }
 
-int bwd_parts(int64_t rows) {
-  const int64_t most = (int64_t)num_sms() * kBwdCtasPerSm;
-  return (int)(rows < most ? rows : most);
-}
+int bwd_parts(int64_t rows) { return (int)(rows < kMaxParts ? rows : kMaxParts); }
 
 template <int VB, typename ET, typename WT, int NV>
 int launch_fwd(const FwdArgs& a, const RowShape& r, cudaStream_t s) {

@@ -37,6 +37,10 @@ struct LayerArgs {
   int32_t* status;
 };
 
+// Lets the next kernel on the stream start while this one runs; it waits for
+// this one's end before it reads what this one writes.
+__device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------------- choices by expert
 
 // The choices sorted by expert (stable), in dynamic shared memory:
@@ -151,6 +155,7 @@ __global__ void __launch_bounds__(kThreads)
   using V = typename L::V;
   __shared__ float part[kWarps][kRouterRows * kCols];
   await_previous_kernel();
+  allow_next_kernel();  // the gating, whose few CTAs then wait in place
   const int lane = lane_id(), warp = threadIdx.x / kWarp;
   const int e0 = (int)blockIdx.x * kRouterRows, t0 = (int)blockIdx.y * kCols;
   const int64_t vecs = H / L::kElems;
@@ -351,8 +356,6 @@ __device__ __forceinline__ void mbar_init_count(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Lets the next kernel on the stream start while this one runs.
-__device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // A box of the tensor from coordinates (x, y, z); x is a multiple of 64.
 __device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
@@ -361,6 +364,9 @@ __device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map
           dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 // 16 bytes from global to shared memory, not through L1; zeros when !in (src is not read then).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
@@ -589,10 +595,13 @@ __global__ void __launch_bounds__(kStreamThreads)
   __shared__ StreamShared sh;
   const LayerArgs& a = p.a;
   const int block = z.rows * kRowBytes;
-  await_previous_kernel();
   const int warp = threadIdx.x / kWarp, lane = lane_id();
   if (warp == kMulWarp) tmem_alloc(smem_u32(&sh.tmem), z.cols);
-  if (threadIdx.x == kCopyWarp * kWarp) init_shared(sh, z.stages);
+  if (threadIdx.x == kCopyWarp * kWarp) {
+    prefetch_map(&map);
+    init_shared(sh, z.stages);
+  }
+  await_previous_kernel();
   const uint32_t ring = align_1k(smem_u32(dyn));
   unsigned char* rest = dyn + (ring - smem_u32(dyn)) + (size_t)z.stages * z.stage_bytes;
   tmem_fence_before();
@@ -748,7 +757,10 @@ __global__ void __launch_bounds__(kStreamThreads)
   // read and weights copied while it still runs (a CTA starts as one of the
   // other kernel leaves its SM); h may not be read.
   if (warp == kMulWarp) tmem_alloc(smem_u32(&sh.tmem), z.cols);
-  if (threadIdx.x == kCopyWarp * kWarp) init_shared(sh, z.stages);
+  if (threadIdx.x == kCopyWarp * kWarp) {
+    prefetch_map(&map);
+    init_shared(sh, z.stages);
+  }
   const uint32_t ring = align_1k(smem_u32(dyn));
   unsigned char* rest = dyn + (ring - smem_u32(dyn)) + (size_t)z.stages * z.stage_bytes;
   int32_t* seg = reinterpret_cast<int32_t*>(rest);
