@@ -4,14 +4,14 @@
 //             dweight = sum_rows dy * xhat, dbias = sum_rows dy
 //
 // Bound by HBM: forward reads x and writes y, backward reads x and dy and
-// writes dx. A row stays in the registers of the threads that loaded it (one
-// warp for short rows, one CTA otherwise): each element is read once, the
-// variance is taken from the centred values, and the next row is loaded
-// before the current one is reduced. In the backward pass a thread owns the
-// same columns in every row it meets, so the two sums over rows live in its
-// registers; each CTA writes one row of partial sums, and a second launch adds
-// those in a fixed order. Rows too long for the registers take kernels that
-// read a row again for each pass over it.
+// writes dx. A row stays in the registers of the threads that loaded it (8, 16
+// or 32 lanes for short rows, a CTA otherwise): each element is read once and
+// the variance is taken from the centred values. The next rows (DEPTH of them)
+// are on their way into registers while one is reduced. In the backward pass a
+// thread owns the same columns in every row it meets, so the two sums over
+// rows live in its registers; each CTA writes one row of partial sums, and a
+// second launch adds those in a fixed order. Rows too long for the registers
+// take kernels that read a row again for each pass over it.
 #include <math.h>
 
 #include "common.cuh"
@@ -20,6 +20,9 @@
 
 namespace moe {
 namespace {
+
+constexpr int kMaxThreads = 1024;  // of a CTA that takes a row
+constexpr int kRowWarps = 8;       // warps of a CTA whose lanes share rows: up to 85 registers
 
 struct FwdArgs {
   const void* x;
@@ -53,36 +56,77 @@ template <> __device__ __forceinline__ float load1<__nv_bfloat16>(const void* p,
 __device__ __forceinline__ void store1(float* p, int64_t i, float v) { p[i] = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, int64_t i, float v) { p[i] = __float2bfloat16_rn(v); }
 
+// A row's values in registers: pairs for the packed fp32 instructions where a
+// vector holds several elements (they halve the arithmetic, which bounded the
+// bf16 kernels: 4.2 TB/s without them), single floats otherwise.
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+template <int kE> struct Pack {
+  using T = uint64_t;
+  static constexpr int N = kE / 2;
+  __device__ __forceinline__ static T splat(float v) { return f2_pack(__float_as_uint(v), __float_as_uint(v)); }
+  template <typename ET, typename V> __device__ __forceinline__ static T get(const V& v, int q) { return f2_elems<ET>(v, q); }
+  __device__ __forceinline__ static T add(T a, T b) { return f2_add(a, b); }
+  __device__ __forceinline__ static T sub(T a, T b) { return f2_sub(a, b); }
+  __device__ __forceinline__ static T mul(T a, T b) { return f2_mul(a, b); }
+  __device__ __forceinline__ static T fma(T a, T b, T c) { return f2_fma(a, b, c); }
+  __device__ __forceinline__ static void put(T v, float* out) { f2_unpack(v, out[0], out[1]); }
+  __device__ __forceinline__ static float sum(T v) {
+    float a, b;
+    f2_unpack(v, a, b);
+    return a + b;
+  }
+};
+template <> struct Pack<1> {
+  using T = float;
+  static constexpr int N = 1;
+  __device__ __forceinline__ static T splat(float v) { return v; }
+  template <typename ET, typename V> __device__ __forceinline__ static T get(const V& v, int) {
+    return Lanes<Elem<ET>::kBytes, ET>::get(v, 0);
+  }
+  __device__ __forceinline__ static T add(T a, T b) { return a + b; }
+  __device__ __forceinline__ static T sub(T a, T b) { return a - b; }
+  __device__ __forceinline__ static T mul(T a, T b) { return __fmul_rn(a, b); }
+  __device__ __forceinline__ static T fma(T a, T b, T c) { return fmaf(a, b, c); }
+  __device__ __forceinline__ static void put(T v, float* out) { *out = v; }
+  __device__ __forceinline__ static float sum(T v) { return v; }
+};
+
 // kE consecutive weights from column c (c and the array are aligned to the
 // vector that a row uses), or `otherwise` where the array is absent.
 template <typename WT, int kE>
-__device__ __forceinline__ void load_cols(const void* w, int64_t c, float otherwise, float* out) {
+__device__ __forceinline__ void load_cols(const void* w, int64_t c, float otherwise, typename Pack<kE>::T* out) {
+  using P = Pack<kE>;
   if (w == nullptr) {
 #pragma unroll
-    for (int q = 0; q < kE; ++q) out[q] = otherwise;
+    for (int q = 0; q < P::N; ++q) out[q] = P::splat(otherwise);
     return;
   }
-  constexpr int kBytes = kE * Elem<WT>::kBytes;
-  constexpr int kPart = kBytes > 16 ? 16 : kBytes;
-  using L = Lanes<kPart, WT>;
-  using V = typename L::V;
+  // One load of up to 32 bytes: two of 16 would each touch every other half line.
+  using V = typename Lanes<kE * Elem<WT>::kBytes, WT>::V;
+  const V v = ld_l1(reinterpret_cast<const V*>(static_cast<const char*>(w) + c * Elem<WT>::kBytes));
 #pragma unroll
-  for (int p = 0; p < kBytes / kPart; ++p) {
-    const V v = ld_l1(reinterpret_cast<const V*>(static_cast<const char*>(w) + c * Elem<WT>::kBytes) + p);
-#pragma unroll
-    for (int q = 0; q < L::kElems; ++q) out[p * L::kElems + q] = L::get(v, q);
-  }
+  for (int q = 0; q < P::N; ++q) out[q] = P::template get<WT>(v, q);
 }
 
-// Sums of N values over the threads that share a row: a warp, or the CTA
-// (`buf` alternates between two halves of `red`, so one barrier suffices).
-template <int N, bool WARP_ROW> __device__ __forceinline__ void row_sum(float (&s)[N], float* red, int& buf) {
+// Sums of N values over LPR lanes, in each of them.
+template <int N, int LPR> __device__ __forceinline__ void lane_sum(float (&s)[N]) {
 #pragma unroll
-  for (int d = kWarp / 2; d > 0; d >>= 1) {
+  for (int d = LPR / 2; d > 0; d >>= 1) {
 #pragma unroll
     for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
   }
-  if constexpr (!WARP_ROW) {
+}
+
+// Sums of N values over the threads that share a row: LPR lanes of a warp, or
+// (LPR 0) the CTA, where `buf` alternates between two halves of `red`, so that
+// one barrier suffices.
+template <int N, int LPR> __device__ __forceinline__ void row_sum(float (&s)[N], float* red, int& buf) {
+  lane_sum<N, LPR ? LPR : kWarp>(s);
+  if constexpr (LPR == 0) {
     const int warps = (int)blockDim.x / kWarp, lane = lane_id();
     float* r = red + buf * (N * kWarp);
     buf ^= 1;
@@ -92,175 +136,239 @@ template <int N, bool WARP_ROW> __device__ __forceinline__ void row_sum(float (&
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      s[i] = lane < warps ? r[i * kWarp + lane] : 0.0f;
-#pragma unroll
-      for (int d = kWarp / 2; d > 0; d >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
-    }
+    for (int i = 0; i < N; ++i) s[i] = lane < warps ? r[i * kWarp + lane] : 0.0f;
+    lane_sum<N, kWarp>(s);
   }
 }
 
-template <int VB, typename ET, typename WT, int NV, bool WARP_ROW, int MAXT>
-__global__ void __launch_bounds__(MAXT) fwd_kernel(FwdArgs a) {
+// The rows that a thread works on: rows0 + i * step for its group of LPR lanes
+// (or its CTA). Warps stay together: a group past the last row idles.
+template <int LPR> struct Rows {
+  int tid, tpr;
+  int64_t at, step, warp_at;
+  __device__ Rows() {
+    if constexpr (LPR == 0) {
+      tid = threadIdx.x;
+      tpr = blockDim.x;
+      at = warp_at = blockIdx.x;
+      step = gridDim.x;
+    } else {
+      constexpr int kPer = kWarp / LPR;
+      tid = threadIdx.x % LPR;
+      tpr = LPR;
+      warp_at = ((int64_t)blockIdx.x * (blockDim.x / kWarp) + threadIdx.x / kWarp) * kPer;
+      at = warp_at + lane_id() / LPR;
+      step = (int64_t)gridDim.x * (blockDim.x / kWarp) * kPer;
+    }
+  }
+};
+
+template <int VB, typename ET, typename WT, int NV, int LPR, int DEPTH, int MAXT>
+__global__ void __launch_bounds__(LPR ? kRowWarps * kWarp : MAXT, LPR ? 3 : 1) fwd_kernel(FwdArgs a) {
   using L = Lanes<VB, ET>;
   using V = typename L::V;
   constexpr int kE = L::kElems;
-  __shared__ float red[2 * kWarp];
+  __shared__ float red[2 * 3 * kWarp];
   await_previous_kernel();
-  const int tid = WARP_ROW ? lane_id() : (int)threadIdx.x;
-  const int tpr = WARP_ROW ? kWarp : (int)blockDim.x;
-  const int64_t step = WARP_ROW ? (int64_t)gridDim.x * (blockDim.x / kWarp) : gridDim.x;
-  const int64_t first = WARP_ROW ? (int64_t)blockIdx.x * (blockDim.x / kWarp) + threadIdx.x / kWarp : blockIdx.x;
+  const Rows<LPR> r;
   const int vecs = (int)(a.H / kE);
   const float inv_h = 1.0f / (float)a.H;
   int buf = 0;
-  V nxt[NV];
-  auto load = [&](int64_t row) {
+  using P = Pack<kE>;
+  using T = typename P::T;
+  // Elements of the row in this warp (or group), and one over it.
+  int held = 0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int left = vecs - (LPR ? 0 : (int)(threadIdx.x / kWarp) * kWarp) - j * r.tpr;
+    held += left < 0 ? 0 : (left < (LPR ? LPR : kWarp) ? left : (LPR ? LPR : kWarp));
+  }
+  const float n_warp = (float)(held * kE), inv_warp = held ? 1.0f / n_warp : 0.0f;
+  V ahead[DEPTH][NV];
+  auto load = [&](V (&v)[NV], int64_t row) {
     const V* p = reinterpret_cast<const V*>(static_cast<const char*>(a.x) + row * a.x_stride * Elem<ET>::kBytes);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int i = tid + j * tpr;
-      if (i < vecs) nxt[j] = ld_stream(p + i);
+      const int i = r.tid + j * r.tpr;
+      v[j] = i < vecs && row < a.rows ? ld_stream(p + i) : zero_vec<V>();
     }
   };
-  if (first < a.rows) load(first);
-  for (int64_t row = first; row < a.rows; row += step) {
-    float v[NV][kE];
-    float s[1] = {0.0f};
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const bool in = tid + j * tpr < vecs;
+  for (int d = 0; d < DEPTH; ++d) load(ahead[d], r.at + d * r.step);
+  for (int64_t done = 0; r.warp_at + done < a.rows;) {
 #pragma unroll
-      for (int q = 0; q < kE; ++q) {
-        v[j][q] = in ? L::get(nxt[j], q) : 0.0f;
-        s[0] += v[j][q];
-      }
-    }
-    if (row + step < a.rows) load(row + step);
-    row_sum<1, WARP_ROW>(s, red, buf);
-    const float mean = s[0] * inv_h;
-    s[0] = 0.0f;
+    for (int d = 0; d < DEPTH; ++d) {
+      const int64_t row = r.at + done;
+      if (r.warp_at + done >= a.rows) break;
+      done += r.step;
+      T v[NV][P::N], t = P::splat(0.0f);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (tid + j * tpr < vecs) {
+      for (int j = 0; j < NV; ++j) {
 #pragma unroll
-        for (int q = 0; q < kE; ++q) {
-          v[j][q] -= mean;
-          s[0] += v[j][q] * v[j][q];
+        for (int q = 0; q < P::N; ++q) {
+          v[j][q] = P::template get<ET>(ahead[d][j], q);
+          t = P::add(t, v[j][q]);
         }
       }
-    }
-    row_sum<1, WARP_ROW>(s, red, buf);
-    const float rstd = rsqrtf(s[0] * inv_h + a.eps);
-    if (tid == 0) {
-      if (a.mean != nullptr) a.mean[row] = mean;
-      if (a.rstd != nullptr) a.rstd[row] = rstd;
-    }
-    V* out = reinterpret_cast<V*>(static_cast<char*>(a.y) + row * a.H * Elem<ET>::kBytes);
+      load(ahead[d], row + DEPTH * r.step);
+      // Mean and squared deviations of the warp's part, then those of the row:
+      // sum (x - mean)^2 = sum over warps of (sum (x - m_w)^2 + n_w (m_w - mean)^2).
+      float s[1] = {P::sum(t)};
+      lane_sum<1, LPR ? LPR : kWarp>(s);
+      float mean = s[0] * inv_warp;
+      const T part = P::splat(mean);
+      t = P::splat(0.0f);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = tid + j * tpr;
-      if (i >= vecs) break;
-      float w[kE], b[kE], o[kE];
-      load_cols<WT, kE>(a.weight, (int64_t)i * kE, 1.0f, w);
-      load_cols<WT, kE>(a.bias, (int64_t)i * kE, 0.0f, b);
+      for (int j = 0; j < NV; ++j) {
+        if (r.tid + j * r.tpr >= vecs) break;
 #pragma unroll
-      for (int q = 0; q < kE; ++q) {
-        o[q] = fmaf(v[j][q] * rstd, w[q], b[q]);
+        for (int q = 0; q < P::N; ++q) {
+          const T c = P::sub(v[j][q], part);
+          t = P::fma(c, c, t);
+        }
       }
-      st_stream(out + i, L::pack(o));
+      float dev[1] = {P::sum(t)};
+      lane_sum<1, LPR ? LPR : kWarp>(dev);
+      if constexpr (LPR == 0) {
+        const int warps = (int)blockDim.x / kWarp, lane = lane_id();
+        float* b = red + buf * (3 * kWarp);
+        buf ^= 1;
+        if (lane == 0) {
+          b[threadIdx.x / kWarp] = s[0];
+          b[kWarp + threadIdx.x / kWarp] = dev[0];
+          b[2 * kWarp + threadIdx.x / kWarp] = n_warp;
+        }
+        __syncthreads();
+        const bool in = lane < warps;
+        const float ws = in ? b[lane] : 0.0f, wd = in ? b[kWarp + lane] : 0.0f, wn = in ? b[2 * kWarp + lane] : 0.0f;
+        s[0] = ws;
+        lane_sum<1, kWarp>(s);
+        mean = s[0] * inv_h;
+        const float off = wn > 0.0f ? ws / wn - mean : 0.0f;
+        dev[0] = fmaf(wn * off, off, wd);
+        lane_sum<1, kWarp>(dev);
+      }
+      const float rstd = rsqrtf(dev[0] * inv_h + a.eps);
+      if (row >= a.rows) continue;
+      if (r.tid == 0) {
+        if (a.mean != nullptr) a.mean[row] = mean;
+        if (a.rstd != nullptr) a.rstd[row] = rstd;
+      }
+      V* out = reinterpret_cast<V*>(static_cast<char*>(a.y) + row * a.H * Elem<ET>::kBytes);
+      const T m2 = P::splat(mean), r2 = P::splat(rstd);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int i = r.tid + j * r.tpr;
+        if (i >= vecs) break;
+        T w[P::N], b[P::N];
+        float o[kE];
+        load_cols<WT, kE>(a.weight, (int64_t)i * kE, 1.0f, w);
+        load_cols<WT, kE>(a.bias, (int64_t)i * kE, 0.0f, b);
+#pragma unroll
+        for (int q = 0; q < P::N; ++q) P::put(P::fma(P::mul(P::sub(v[j][q], m2), r2), w[q], b[q]), o + q * (kE / P::N));
+        st_stream(out + i, L::pack(o));
+      }
     }
   }
 }
 
-template <int VB, typename ET, typename WT, int NV, bool WARP_ROW, int MAXT>
-__global__ void __launch_bounds__(MAXT) bwd_kernel(BwdArgs a) {
+template <int VB, typename ET, typename WT, int NV, int LPR, int DEPTH, int MAXT>
+__global__ void __launch_bounds__(LPR ? kRowWarps * kWarp : MAXT, LPR ? 3 : 1) bwd_kernel(BwdArgs a) {
   using L = Lanes<VB, ET>;
   using V = typename L::V;
   constexpr int kE = L::kElems;
   __shared__ float red[4 * kWarp];
   await_previous_kernel();
-  const int tid = WARP_ROW ? lane_id() : (int)threadIdx.x;
-  const int tpr = WARP_ROW ? kWarp : (int)blockDim.x;
-  const int64_t step = WARP_ROW ? (int64_t)gridDim.x * (blockDim.x / kWarp) : gridDim.x;
-  const int64_t first = WARP_ROW ? (int64_t)blockIdx.x * (blockDim.x / kWarp) + threadIdx.x / kWarp : blockIdx.x;
+  const Rows<LPR> r;
   const int vecs = (int)(a.H / kE);
   const float inv_h = 1.0f / (float)a.H;
   int buf = 0;
-  float aw[NV][kE], ab[NV][kE];
+  using P = Pack<kE>;
+  using T = typename P::T;
+  T aw2[NV][P::N], ab2[NV][P::N];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
 #pragma unroll
-    for (int q = 0; q < kE; ++q) aw[j][q] = ab[j][q] = 0.0f;
+    for (int q = 0; q < P::N; ++q) aw2[j][q] = ab2[j][q] = P::splat(0.0f);
   }
-  V nx[NV], nd[NV];
-  float nmean = 0.0f, nrstd = 0.0f;
-  auto load = [&](int64_t row) {
+  T w[NV][P::N];  // this thread's columns in every row
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    load_cols<WT, kE>(r.tid + j * r.tpr < vecs ? a.weight : nullptr, (int64_t)(r.tid + j * r.tpr) * kE, 1.0f, w[j]);
+  V nx[DEPTH][NV], nd[DEPTH][NV];
+  float nmean[DEPTH], nrstd[DEPTH];
+  auto load = [&](int d, int64_t row) {
     const V* px = reinterpret_cast<const V*>(static_cast<const char*>(a.x) + row * a.x_stride * Elem<ET>::kBytes);
     const V* pd = reinterpret_cast<const V*>(static_cast<const char*>(a.dy) + row * a.dy_stride * Elem<ET>::kBytes);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int i = tid + j * tpr;
-      nx[j] = i < vecs ? ld_stream(px + i) : zero_vec<V>();
-      nd[j] = i < vecs ? ld_stream(pd + i) : zero_vec<V>();
+      const int i = r.tid + j * r.tpr;
+      const bool in = i < vecs && row < a.rows;
+      nx[d][j] = in ? ld_stream(px + i) : zero_vec<V>();
+      nd[d][j] = in ? ld_stream(pd + i) : zero_vec<V>();
     }
-    nmean = __ldg(a.mean + row);
-    nrstd = __ldg(a.rstd + row);
+    nmean[d] = row < a.rows ? __ldg(a.mean + row) : 0.0f;
+    nrstd[d] = row < a.rows ? __ldg(a.rstd + row) : 0.0f;
   };
-  if (first < a.rows) load(first);
-  for (int64_t row = first; row < a.rows; row += step) {
-    V cx[NV], cd[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      cx[j] = nx[j];
-      cd[j] = nd[j];
-    }
-    const float mean = nmean, rstd = nrstd;
-    if (row + step < a.rows) load(row + step);
-    float s[2] = {0.0f, 0.0f};
+  for (int d = 0; d < DEPTH; ++d) load(d, r.at + d * r.step);
+  for (int64_t done = 0; r.warp_at + done < a.rows;) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = tid + j * tpr;
-      if (i >= vecs) break;
-      float w[kE];
-      load_cols<WT, kE>(a.weight, (int64_t)i * kE, 1.0f, w);
+    for (int d = 0; d < DEPTH; ++d) {
+      const int64_t row = r.at + done;
+      if (r.warp_at + done >= a.rows) break;
+      done += r.step;
+      T xhat[NV][P::N], v[NV][P::N], s0 = P::splat(0.0f), s1 = s0;
+      const T r2 = P::splat(nrstd[d]), m2 = P::splat(nmean[d]);
 #pragma unroll
-      for (int q = 0; q < kE; ++q) {
-        const float dy = L::get(cd[j], q);
-        const float xhat = (L::get(cx[j], q) - mean) * rstd;
-        const float v = dy * w[q];
-        s[0] += v;
-        s[1] += v * xhat;
-        aw[j][q] += dy * xhat;
-        ab[j][q] += dy;
+      for (int j = 0; j < NV; ++j) {
+        const int i = r.tid + j * r.tpr;
+        if (i >= vecs) break;
+#pragma unroll
+        for (int q = 0; q < P::N; ++q) {
+          const T dy = P::template get<ET>(nd[d][j], q);
+          xhat[j][q] = P::mul(P::sub(P::template get<ET>(nx[d][j], q), m2), r2);
+          v[j][q] = P::mul(dy, w[j][q]);
+          s0 = P::add(s0, v[j][q]);
+          s1 = P::fma(v[j][q], xhat[j][q], s1);
+          aw2[j][q] = P::fma(dy, xhat[j][q], aw2[j][q]);  // a row past the last has dy = 0
+          ab2[j][q] = P::add(ab2[j][q], dy);
+        }
       }
-    }
-    row_sum<2, WARP_ROW>(s, red, buf);
-    const float c0 = s[0] * inv_h, c1 = s[1] * inv_h;
-    V* out = reinterpret_cast<V*>(static_cast<char*>(a.dx) + row * a.H * Elem<ET>::kBytes);
+      load(d, row + DEPTH * r.step);
+      float s[2] = {P::sum(s0), P::sum(s1)};
+      row_sum<2, LPR>(s, red, buf);
+      if (row >= a.rows) continue;
+      const T c0 = P::splat(s[0] * inv_h), c1 = P::splat(-s[1] * inv_h);
+      V* out = reinterpret_cast<V*>(static_cast<char*>(a.dx) + row * a.H * Elem<ET>::kBytes);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = tid + j * tpr;
-      if (i >= vecs) break;
-      float w[kE], o[kE];
-      load_cols<WT, kE>(a.weight, (int64_t)i * kE, 1.0f, w);
+      for (int j = 0; j < NV; ++j) {
+        const int i = r.tid + j * r.tpr;
+        if (i >= vecs) break;
+        float o[kE];
 #pragma unroll
-      for (int q = 0; q < kE; ++q) {
-        const float dy = L::get(cd[j], q);
-        const float xhat = (L::get(cx[j], q) - mean) * rstd;
-        const float v = dy * w[q];
-        o[q] = rstd * (v - c0 - xhat * c1);
+        for (int q = 0; q < P::N; ++q)
+          P::put(P::mul(P::fma(xhat[j][q], c1, P::sub(v[j][q], c0)), r2), o + q * (kE / P::N));
+        st_stream(out + i, L::pack(o));
       }
-      st_stream(out + i, L::pack(o));
     }
   }
   if (a.partial == nullptr) return;
+  float aw[NV][kE], ab[NV][kE];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+#pragma unroll
+    for (int q = 0; q < P::N; ++q) {
+      P::put(aw2[j][q], &aw[j][q * (kE / P::N)]);
+      P::put(ab2[j][q], &ab[j][q * (kE / P::N)]);
+    }
+  }
   float* pw = a.partial + (int64_t)blockIdx.x * a.H;
   float* pb = pw + (int64_t)gridDim.x * a.H;
-  if constexpr (!WARP_ROW) {
+  if constexpr (LPR == 0) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int i = tid + j * tpr;
+      const int i = r.tid + j * r.tpr;
       if (i >= vecs) break;
 #pragma unroll
       for (int q = 0; q < kE; ++q) {
@@ -269,16 +377,27 @@ __global__ void __launch_bounds__(MAXT) bwd_kernel(BwdArgs a) {
       }
     }
   } else {
-    // The CTA's warps hold the same columns: added warp by warp.
-    extern __shared__ float acc[];  // [2][NV * 32 * kE]
-    constexpr int kCols = NV * kWarp * kE;
+    // The CTA's groups hold the same columns: added within a warp, then warp by warp.
+    extern __shared__ float acc[];  // [2][NV * LPR * kE]
+    constexpr int kCols = NV * LPR * kE;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int q = 0; q < kE; ++q) {
+#pragma unroll
+        for (int d = LPR; d < kWarp; d <<= 1) {
+          aw[j][q] += __shfl_xor_sync(0xffffffffu, aw[j][q], d);
+          ab[j][q] += __shfl_xor_sync(0xffffffffu, ab[j][q], d);
+        }
+      }
+    }
     for (int w = 0; w < (int)(blockDim.x / kWarp); ++w) {
-      if ((int)(threadIdx.x / kWarp) == w) {
+      if ((int)(threadIdx.x / kWarp) == w && lane_id() < LPR) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
 #pragma unroll
           for (int q = 0; q < kE; ++q) {
-            const int c = (tid + j * kWarp) * kE + q;
+            const int c = (r.tid + j * LPR) * kE + q;
             acc[c] = (w ? acc[c] : 0.0f) + aw[j][q];
             acc[kCols + c] = (w ? acc[kCols + c] : 0.0f) + ab[j][q];
           }
@@ -303,14 +422,14 @@ template <typename ET, typename WT> __global__ void __launch_bounds__(512) fwd_l
     const ET* x = static_cast<const ET*>(a.x) + row * a.x_stride;
     float s[1] = {0.0f};
     for (int64_t c = threadIdx.x; c < a.H; c += blockDim.x) s[0] += load1<ET>(x, c);
-    row_sum<1, false>(s, red, buf);
+    row_sum<1, 0>(s, red, buf);
     const float mean = s[0] * inv_h;
     s[0] = 0.0f;
     for (int64_t c = threadIdx.x; c < a.H; c += blockDim.x) {
       const float d = load1<ET>(x, c) - mean;
       s[0] += d * d;
     }
-    row_sum<1, false>(s, red, buf);
+    row_sum<1, 0>(s, red, buf);
     const float rstd = rsqrtf(s[0] * inv_h + a.eps);
     if (threadIdx.x == 0) {
       if (a.mean != nullptr) a.mean[row] = mean;
@@ -340,7 +459,7 @@ template <typename ET, typename WT> __global__ void __launch_bounds__(512) bwd_l
       s[0] += v;
       s[1] += v * ((load1<ET>(x, c) - mean) * rstd);
     }
-    row_sum<2, false>(s, red, buf);
+    row_sum<2, 0>(s, red, buf);
     for (int64_t c = threadIdx.x; c < a.H; c += blockDim.x) {
       const float v = load1<ET>(dy, c) * (a.weight != nullptr ? load1<WT>(a.weight, c) : 1.0f);
       store1(static_cast<ET*>(a.dx), row * a.H + c,
@@ -393,99 +512,76 @@ __global__ void __launch_bounds__(512) cols_kernel(const float* __restrict__ par
 
 // ------------------------------------------------------------------ host
 
-constexpr int kRowWarps = 8;     // rows per CTA when a warp takes a row
-constexpr int kMaxParts = 304;   // CTAs of the backward pass, each with a row of partial column sums
+constexpr int kMinParts = 304;    // CTAs of the backward pass, each with a row of partial column sums,
+constexpr int kMaxParts = 2432;   // more of them for shorter rows:
+constexpr int64_t kPartElems = (int64_t)304 * 8192;
 
-struct RowShape {
-  bool warp_row;
-  int nv, threads;  // threads == 0: the row does not fit
-};
-
-// Vectors per thread (a power of two up to max_nv) and threads per row.
-RowShape row_shape(int64_t vecs, int max_nv, int want_threads, int max_threads) {
-  if (vecs <= kWarp * 4) return {true, vecs <= kWarp ? 1 : (vecs <= kWarp * 2 ? 2 : 4), kRowWarps * kWarp};
-  for (int limit : {want_threads, max_threads}) {
-    for (int nv = 1; nv <= max_nv; nv <<= 1) {
-      const int64_t t = ((vecs + nv - 1) / nv + kWarp - 1) / kWarp * kWarp;
-      if (t <= limit) return {false, nv, (int)t};
-    }
-  }
-  return {false, 0, 0};
+int64_t bwd_parts(int64_t rows, int64_t H) {
+  int64_t most = kPartElems / H;
+  most = most < kMinParts ? kMinParts : (most > kMaxParts ? kMaxParts : most);
+  return rows < most ? rows : most;
 }
 
-int bwd_parts(int64_t rows) { return (int)(rows < kMaxParts ? rows : kMaxParts); }
+int cta_threads(int64_t vecs, int nv) { return (int)(((vecs + nv - 1) / nv + kWarp - 1) / kWarp * kWarp); }
 
-template <int VB, typename ET, typename WT, int NV>
-int launch_fwd(const FwdArgs& a, const RowShape& r, cudaStream_t s) {
-  if (r.warp_row) {
-    if constexpr (NV <= 4) {
-      auto k = fwd_kernel<VB, ET, WT, NV, true, kRowWarps * kWarp>;
-      launch(k, persistent_grid(k, r.threads, 0, (a.rows + kRowWarps - 1) / kRowWarps), r.threads, 0, s, a);
-    }
-  } else if (r.threads <= 256) {
-    auto k = fwd_kernel<VB, ET, WT, NV, false, 256>;
-    launch(k, persistent_grid(k, r.threads, 0, a.rows), r.threads, 0, s, a);
-  } else {
-    auto k = fwd_kernel<VB, ET, WT, NV, false, 1024>;
-    launch(k, persistent_grid(k, r.threads, 0, a.rows), r.threads, 0, s, a);
-  }
+template <int VB, typename ET, typename WT, int NV, int LPR, int DEPTH, int MAXT = kMaxThreads>
+int go_fwd(const FwdArgs& a, cudaStream_t s) {
+  const int threads = LPR ? kRowWarps * kWarp : cta_threads(a.H / Lanes<VB, ET>::kElems, NV);
+  constexpr int kRows = LPR ? kRowWarps * (kWarp / (LPR ? LPR : 1)) : 1;
+  auto k = fwd_kernel<VB, ET, WT, NV, LPR, DEPTH, MAXT>;
+  launch(k, persistent_grid(k, threads, 0, (a.rows + kRows - 1) / kRows), threads, 0, s, a);
   return check_launch();
 }
 
+// Vectors of a row decide: lanes of a warp up to 128 of them, a CTA beyond.
 template <int VB, typename ET, typename WT> int dispatch_fwd(const FwdArgs& a, cudaStream_t s) {
-  const RowShape r = row_shape(a.H / Lanes<VB, ET>::kElems, VB == 16 ? 4 : 16, 256, 1024);
-  switch (r.nv) {
-    case 1: return launch_fwd<VB, ET, WT, 1>(a, r, s);
-    case 2: return launch_fwd<VB, ET, WT, 2>(a, r, s);
-    case 4: return launch_fwd<VB, ET, WT, 4>(a, r, s);
-    default: break;
-  }
-  if constexpr (VB != 16) {
-    if (r.nv == 8) return launch_fwd<VB, ET, WT, 8>(a, r, s);
-    if (r.nv == 16) return launch_fwd<VB, ET, WT, 16>(a, r, s);
+  const int64_t vecs = a.H / Lanes<VB, ET>::kElems;
+  if (vecs <= 8) return go_fwd<VB, ET, WT, 1, 8, 4>(a, s);
+  if (vecs <= 16) return go_fwd<VB, ET, WT, 1, 16, 4>(a, s);
+  if (vecs <= 32) return go_fwd<VB, ET, WT, 1, 32, 4>(a, s);
+  if (vecs <= 64) return go_fwd<VB, ET, WT, 2, 32, 2>(a, s);
+  if (vecs <= 128) return go_fwd<VB, ET, WT, 4, 32, 1>(a, s);
+  if constexpr (VB == 16) {
+    if (vecs <= 4 * 256) return go_fwd<VB, ET, WT, 4, 0, 1, 256>(a, s);
+    if (vecs <= 4 * kMaxThreads) return go_fwd<VB, ET, WT, 4, 0, 1>(a, s);
+  } else {
+    if (vecs <= 8 * kMaxThreads) return go_fwd<VB, ET, WT, 8, 0, 2>(a, s);
+    if (vecs <= 16 * kMaxThreads) return go_fwd<VB, ET, WT, 16, 0, 1>(a, s);
   }
   auto k = fwd_long_kernel<ET, WT>;
   launch(k, persistent_grid(k, 512, 0, a.rows), 512, 0, s, a);
   return check_launch();
 }
 
-template <int VB, typename ET, typename WT, int NV>
-int launch_bwd(const BwdArgs& a, const RowShape& r, int* parts, cudaStream_t s) {
-  const int64_t most = bwd_parts(a.rows);
-  auto go = [&](auto k, size_t smem, int64_t work) {
-    const int grid = persistent_grid(k, r.threads, smem, work < most ? work : most);
-    *parts = grid;
-    launch(k, grid, r.threads, smem, s, a);
-  };
-  if (r.warp_row) {
-    if constexpr (NV <= 4)
-      go(bwd_kernel<VB, ET, WT, NV, true, kRowWarps * kWarp>, sizeof(float) * 2 * NV * kWarp * Lanes<VB, ET>::kElems,
-         (a.rows + kRowWarps - 1) / kRowWarps);
-  } else {
-    go(bwd_kernel<VB, ET, WT, NV, false, 512>, 0, a.rows);
-  }
+template <int VB, typename ET, typename WT, int NV, int LPR, int DEPTH, int MAXT = kMaxThreads>
+int go_bwd(const BwdArgs& a, int* parts, cudaStream_t s) {
+  const int threads = LPR ? kRowWarps * kWarp : cta_threads(a.H / Lanes<VB, ET>::kElems, NV);
+  constexpr int kRows = LPR ? kRowWarps * (kWarp / (LPR ? LPR : 1)) : 1;
+  const int64_t most = bwd_parts(a.rows, a.H), work = (a.rows + kRows - 1) / kRows;
+  const size_t smem = LPR ? sizeof(float) * 2 * NV * LPR * Lanes<VB, ET>::kElems : 0;
+  auto k = bwd_kernel<VB, ET, WT, NV, LPR, DEPTH, MAXT>;
+  *parts = persistent_grid(k, threads, smem, work < most ? work : most);
+  launch(k, *parts, threads, smem, s, a);
   return check_launch();
 }
 
 template <int VB, typename ET, typename WT> int dispatch_bwd(const BwdArgs& a, int* parts, cudaStream_t s) {
-  const RowShape r = row_shape(a.H / Lanes<VB, ET>::kElems, VB == 16 ? 4 : 16, 512, 512);
-  switch (r.nv) {
-    case 1: return launch_bwd<VB, ET, WT, 1>(a, r, parts, s);
-    case 2: return launch_bwd<VB, ET, WT, 2>(a, r, parts, s);
-    case 4: return launch_bwd<VB, ET, WT, 4>(a, r, parts, s);
-    default: break;
-  }
-  if constexpr (VB != 16) {
-    if (r.nv == 8) return launch_bwd<VB, ET, WT, 8>(a, r, parts, s);
-    if (r.nv == 16) return launch_bwd<VB, ET, WT, 16>(a, r, parts, s);
+  const int64_t vecs = a.H / Lanes<VB, ET>::kElems;
+  if (vecs <= 8) return go_bwd<VB, ET, WT, 1, 8, 2>(a, parts, s);
+  if (vecs <= 16) return go_bwd<VB, ET, WT, 1, 16, 2>(a, parts, s);
+  if (vecs <= 32) return go_bwd<VB, ET, WT, 1, 32, 2>(a, parts, s);
+  if constexpr (VB == 16) {
+    if (vecs <= 2 * 512) return go_bwd<VB, ET, WT, 2, 0, 2, 512>(a, parts, s);
+    if (vecs <= 2 * kMaxThreads) return go_bwd<VB, ET, WT, 2, 0, 1>(a, parts, s);
+  } else {
+    if (vecs <= 4 * kMaxThreads) return go_bwd<VB, ET, WT, 4, 0, 2>(a, parts, s);
+    if (vecs <= 8 * kMaxThreads) return go_bwd<VB, ET, WT, 8, 0, 1>(a, parts, s);
   }
   auto k = bwd_long_kernel<ET, WT>;
   launch(k, persistent_grid(k, 512, 0, a.rows), 512, 0, s, a);
-  *parts = bwd_parts(a.rows);
-  if (a.partial != nullptr) {
-    if (*parts > 32) *parts = 32;
+  *parts = (int)(a.rows < 32 ? a.rows : 32);
+  if (a.partial != nullptr)
     launch(bwd_long_cols_kernel<ET>, dim3((unsigned)((a.H + 255) / 256), (unsigned)*parts), 256, 0, s, a);
-  }
   return check_launch();
 }
 
@@ -511,8 +607,10 @@ bool bad_stride(int64_t stride, int64_t rows, int64_t H) {
 
 template <typename ET, typename WT> int run_fwd(FwdArgs a, cudaStream_t s) {
   if (a.rows < 2) a.x_stride = a.H;
-  const void* ptrs[] = {a.x, a.y, a.weight, a.bias};
-  if (rows_by_16<ET>(a.H, &a.x_stride, 1, ptrs, 4)) return dispatch_fwd<16, ET, WT>(a, s);
+  const void* ptrs[] = {a.x, a.y};
+  constexpr int kCols = 16 / Elem<ET>::kBytes * Elem<WT>::kBytes;  // of the weights beside 16 bytes of a row
+  if (rows_by_16<ET>(a.H, &a.x_stride, 1, ptrs, 2) && aligned(a.weight, kCols) && aligned(a.bias, kCols))
+    return dispatch_fwd<16, ET, WT>(a, s);
   return dispatch_fwd<Elem<ET>::kBytes, ET, WT>(a, s);
 }
 
@@ -521,8 +619,8 @@ template <typename ET, typename WT> int run_bwd(BwdArgs a, void* dweight, void* 
   int parts = 0, rc = MOE_OK;
   if (a.rows > 0) {
     const int64_t strides[] = {a.x_stride, a.dy_stride};
-    const void* ptrs[] = {a.x, a.dy, a.dx, a.weight};
-    rc = rows_by_16<ET>(a.H, strides, 2, ptrs, 4) ? dispatch_bwd<16, ET, WT>(a, &parts, s)
+    const void* ptrs[] = {a.x, a.dy, a.dx};
+    rc = rows_by_16<ET>(a.H, strides, 2, ptrs, 3) && aligned(a.weight, 16 / Elem<ET>::kBytes * Elem<WT>::kBytes) ? dispatch_bwd<16, ET, WT>(a, &parts, s)
                                                   : dispatch_bwd<Elem<ET>::kBytes, ET, WT>(a, &parts, s);
   }
   if (rc != MOE_OK || (dweight == nullptr && dbias == nullptr)) return rc;
@@ -556,7 +654,7 @@ extern "C" int moe_layer_norm_fwd(const void* x, int32_t dtype, int64_t x_stride
 
 extern "C" size_t moe_layer_norm_bwd_workspace_size(int64_t rows, int64_t H) {
   if (rows < 0 || H < 1) return 0;
-  return (size_t)bwd_parts(rows < 1 ? 1 : rows) * 2 * (size_t)H * sizeof(float);
+  return (size_t)bwd_parts(rows < 1 ? 1 : rows, H) * 2 * (size_t)H * sizeof(float);
 }
 
 extern "C" int moe_layer_norm_bwd(const void* dy, int64_t dy_stride, const void* x, int32_t dtype, int64_t x_stride,
