@@ -10,10 +10,15 @@
 // are on their way into registers while one is reduced. In the backward pass a
 // thread owns the same columns in every row it meets, so the two sums over
 // rows live in its registers; each CTA writes one row of partial sums, and a
-// second launch adds those in a fixed order. Rows too long for the registers
-// take kernels that read a row again for each pass over it.
+// second launch adds those in a fixed order. Rows of 2 to 16 KB in 16-byte
+// pieces come through a ring in shared memory filled by bulk copies, two rows
+// at a time. Rows too long for the registers take kernels that read a row
+// again for each pass over it.
 #include <math.h>
 
+#include <atomic>
+
+#include "bulk.cuh"
 #include "common.cuh"
 #include "moe_block.h"
 #include "vec_math.cuh"
@@ -412,6 +417,289 @@ __global__ void __launch_bounds__(LPR ? kRowWarps * kWarp : MAXT, LPR ? 3 : 1) b
   }
 }
 
+// ------------------------------------------- rows through shared memory
+//
+// One 16-byte vector of the row per thread, kRingRows consecutive rows at a
+// time, copied into a ring of slots by bulk copies (one for both rows where
+// they are adjacent). What that buys over loads into registers: the copies
+// ahead cost none, so the weights (and the column sums) fit in them instead of
+// being read again for each row, which at fp32 was four times the row's bytes,
+// and one barrier and one round of exchanges serve two rows. A slot is free
+// again after the next iteration's barrier. Waits are bounded; after one gives
+// up the CTA writes NaN instead of waiting again.
+
+constexpr int kRingRows = 2;
+constexpr int kMaxSlots = 16;
+constexpr int kRingSm = 200 * 1024;  // shared memory of an SM for rings
+
+// Sums of a and of b over a warp, in every lane: each half of the lanes
+// carries one of the two after the first exchange.
+__device__ __forceinline__ void warp_sum2(float& a, float& b) {
+  const bool upper = (lane_id() & 16) != 0;
+  float s = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  const float other = __shfl_xor_sync(0xffffffffu, s, 16);
+  a = upper ? other : s;
+  b = upper ? s : other;
+}
+
+struct RowRing {
+  uint32_t data, bars;
+  int slots, slot_bytes, row_bytes;
+  // One thread: the rows [row, row + n) of up to two matrices into slot i.
+  __device__ __forceinline__ void fill(int i, const char* x, int64_t x_stride, const char* y, int64_t y_stride, int n) const {
+    const uint32_t bar = bars + 8 * i, dst = data + i * slot_bytes;
+    mbar_expect(bar, (uint32_t)(n * row_bytes * (y != nullptr ? 2 : 1)));
+    copy(dst, x, x_stride, n, bar);
+    if (y != nullptr) copy(dst + kRingRows * row_bytes, y, y_stride, n, bar);
+  }
+  __device__ __forceinline__ void copy(uint32_t dst, const char* src, int64_t stride, int n, uint32_t bar) const {
+    if (stride == row_bytes) {
+      bulk_copy_in(dst, src, n * row_bytes, bar);
+    } else {
+      for (int r = 0; r < n; ++r) bulk_copy_in(dst + r * row_bytes, src + r * stride, row_bytes, bar);
+    }
+  }
+};
+
+__device__ __forceinline__ uint4 lds_vec(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
+  return v;
+}
+
+template <typename ET, typename WT> __global__ void __launch_bounds__(kMaxThreads) fwd_ring_kernel(FwdArgs a, int slots) {
+  using L = Lanes<16, ET>;
+  constexpr int kE = L::kElems;
+  using P = Pack<kE>;
+  using T = typename P::T;
+  extern __shared__ __align__(128) unsigned char dyn[];
+  __shared__ uint64_t bars[kMaxSlots];
+  __shared__ float4 red[2][kWarp];
+  const int lane = lane_id(), warp = threadIdx.x / kWarp, warps = blockDim.x / kWarp;
+  const int vecs = (int)(a.H / kE);
+  const bool in = (int)threadIdx.x < vecs;
+  const int row_bytes = vecs * 16;
+  const RowRing ring{smem_u32(dyn), smem_u32(bars), slots, kRingRows * row_bytes, row_bytes};
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < slots; ++i) mbar_init(ring.bars + 8 * i);
+    fence_mbarrier_init();
+  }
+  await_previous_kernel();
+  __syncthreads();
+  const int64_t stride = a.x_stride * Elem<ET>::kBytes, step = (int64_t)gridDim.x * kRingRows;
+  const int64_t first = (int64_t)blockIdx.x * kRingRows;
+  auto fill = [&](int i, int64_t row) {
+    if (row < a.rows)
+      ring.fill(i, static_cast<const char*>(a.x) + row * stride, stride, nullptr, 0,
+                a.rows - row < kRingRows ? (int)(a.rows - row) : kRingRows);
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < slots - 1; ++i) fill(i, first + i * step);
+  T w[P::N], b[P::N];
+  load_cols<WT, kE>(in ? a.weight : nullptr, (int64_t)threadIdx.x * kE, 1.0f, w);
+  load_cols<WT, kE>(in ? a.bias : nullptr, (int64_t)threadIdx.x * kE, 0.0f, b);
+  const float inv_h = 1.0f / (float)a.H;
+  auto held = [&](int wp) {
+    const int left = vecs - wp * kWarp;
+    return (float)((left < 0 ? 0 : (left < kWarp ? left : kWarp)) * kE);
+  };
+  const float inv_warp = 1.0f / held(warp);
+  const bool is_peer = lane < warps;
+  const float n_peer = is_peer ? held(lane) : 0.0f, inv_peer = is_peer ? 1.0f / n_peer : 0.0f;
+  int slot = 0, buf = 0;
+  uint32_t parity = 0;
+  bool ok = true;
+  for (int64_t row = first; row < a.rows; row += step) {
+    ok = ok && mbar_wait(ring.bars + 8 * slot, parity);
+    const uint32_t at = ring.data + slot * ring.slot_bytes + threadIdx.x * 16;
+    T v[kRingRows][P::N];
+    float s[kRingRows], dev[kRingRows], mean[kRingRows];
+#pragma unroll
+    for (int r = 0; r < kRingRows; ++r) {
+      const uint4 raw = in && row + r < a.rows ? lds_vec(at + r * row_bytes) : make_uint4(0, 0, 0, 0);
+      T t = P::splat(0.0f);
+#pragma unroll
+      for (int q = 0; q < P::N; ++q) {
+        v[r][q] = P::template get<ET>(raw, q);
+        t = P::add(t, v[r][q]);
+      }
+      s[r] = P::sum(t);
+    }
+    // Mean and squared deviations of the warp's part, then those of the row:
+    // sum (x - mean)^2 = sum over warps of (sum (x - m_w)^2 + n_w (m_w - mean)^2).
+    warp_sum2(s[0], s[1]);
+#pragma unroll
+    for (int r = 0; r < kRingRows; ++r) {
+      const T m = P::splat(s[r] * inv_warp);
+      T t = P::splat(0.0f);
+#pragma unroll
+      for (int q = 0; q < P::N; ++q) {
+        const T c = P::sub(v[r][q], m);
+        t = P::fma(c, c, t);
+      }
+      dev[r] = in ? P::sum(t) : 0.0f;
+    }
+    warp_sum2(dev[0], dev[1]);
+    if (lane == 0) red[buf][warp] = make_float4(s[0], s[1], dev[0], dev[1]);
+    __syncthreads();
+    const float4 p = is_peer ? red[buf][lane] : make_float4(0, 0, 0, 0);
+    buf ^= 1;
+    if (threadIdx.x == 0) {  // everybody has read the slot before this one
+      fence_async_shared();
+      fill(slot == 0 ? slots - 1 : slot - 1, row + (slots - 1) * step);
+    }
+    mean[0] = p.x;
+    mean[1] = p.y;
+    warp_sum2(mean[0], mean[1]);
+#pragma unroll
+    for (int r = 0; r < kRingRows; ++r) {
+      mean[r] = ok ? mean[r] * inv_h : __int_as_float(0x7fffffff);
+      const float off = (r ? p.y : p.x) * inv_peer - mean[r];
+      dev[r] = is_peer ? fmaf(n_peer * off, off, r ? p.w : p.z) : 0.0f;
+    }
+    warp_sum2(dev[0], dev[1]);
+#pragma unroll
+    for (int r = 0; r < kRingRows; ++r) {
+      if (row + r >= a.rows) break;
+      const float rstd = rsqrtf(dev[r] * inv_h + a.eps);
+      if (threadIdx.x == 0) {
+        if (a.mean != nullptr) a.mean[row + r] = mean[r];
+        if (a.rstd != nullptr) a.rstd[row + r] = rstd;
+      }
+      if (!in) continue;
+      const T m2 = P::splat(mean[r]), r2 = P::splat(rstd);
+      float o[kE];
+#pragma unroll
+      for (int q = 0; q < P::N; ++q) P::put(P::fma(P::mul(P::sub(v[r][q], m2), r2), w[q], b[q]), o + 2 * q);
+      st_stream(reinterpret_cast<uint4*>(static_cast<char*>(a.y) + (row + r) * row_bytes) + threadIdx.x, L::pack(o));
+    }
+    if (++slot == slots) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+}
+
+template <typename ET, typename WT> __global__ void __launch_bounds__(kMaxThreads) bwd_ring_kernel(BwdArgs a, int slots) {
+  using L = Lanes<16, ET>;
+  constexpr int kE = L::kElems;
+  using P = Pack<kE>;
+  using T = typename P::T;
+  extern __shared__ __align__(128) unsigned char dyn[];
+  __shared__ uint64_t bars[kMaxSlots];
+  __shared__ float4 red[2][kWarp];
+  const int lane = lane_id(), warp = threadIdx.x / kWarp, warps = blockDim.x / kWarp;
+  const int vecs = (int)(a.H / kE);
+  const bool in = (int)threadIdx.x < vecs;
+  const int row_bytes = vecs * 16;
+  const RowRing ring{smem_u32(dyn), smem_u32(bars), slots, 2 * kRingRows * row_bytes, row_bytes};
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < slots; ++i) mbar_init(ring.bars + 8 * i);
+    fence_mbarrier_init();
+  }
+  await_previous_kernel();
+  __syncthreads();
+  const int64_t x_stride = a.x_stride * Elem<ET>::kBytes, dy_stride = a.dy_stride * Elem<ET>::kBytes;
+  const int64_t step = (int64_t)gridDim.x * kRingRows, first = (int64_t)blockIdx.x * kRingRows;
+  auto fill = [&](int i, int64_t row) {
+    if (row < a.rows)
+      ring.fill(i, static_cast<const char*>(a.x) + row * x_stride, x_stride,
+                static_cast<const char*>(a.dy) + row * dy_stride, dy_stride,
+                a.rows - row < kRingRows ? (int)(a.rows - row) : kRingRows);
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < slots - 1; ++i) fill(i, first + i * step);
+  T w[P::N], aw[P::N], ab[P::N];
+  load_cols<WT, kE>(in ? a.weight : nullptr, (int64_t)threadIdx.x * kE, 1.0f, w);
+#pragma unroll
+  for (int q = 0; q < P::N; ++q) aw[q] = ab[q] = P::splat(0.0f);
+  const float inv_h = 1.0f / (float)a.H;
+  int slot = 0, buf = 0;
+  uint32_t parity = 0;
+  bool ok = true;
+  for (int64_t row = first; row < a.rows; row += step) {
+    float mean[kRingRows], rstd[kRingRows], s0[kRingRows], s1[kRingRows];
+#pragma unroll
+    for (int r = 0; r < kRingRows; ++r) {
+      const bool there = row + r < a.rows;
+      mean[r] = there ? __ldg(a.mean + row + r) : 0.0f;
+      rstd[r] = there ? __ldg(a.rstd + row + r) : 0.0f;
+    }
+    ok = ok && mbar_wait(ring.bars + 8 * slot, parity);
+    const uint32_t at = ring.data + slot * ring.slot_bytes + threadIdx.x * 16;
+#pragma unroll
+    for (int r = 0; r < kRingRows; ++r) {
+      const bool there = in && row + r < a.rows;
+      const uint4 x = there ? lds_vec(at + r * row_bytes) : make_uint4(0, 0, 0, 0);
+      const uint4 d = there ? lds_vec(at + (kRingRows + r) * row_bytes) : make_uint4(0, 0, 0, 0);
+      const T m2 = P::splat(mean[r]), r2 = P::splat(rstd[r]);
+      T t0 = P::splat(0.0f), t1 = t0;
+#pragma unroll
+      for (int q = 0; q < P::N; ++q) {
+        const T dy = P::template get<ET>(d, q);
+        const T xhat = P::mul(P::sub(P::template get<ET>(x, q), m2), r2);
+        const T v = P::mul(dy, w[q]);
+        t0 = P::add(t0, v);
+        t1 = P::fma(v, xhat, t1);
+        aw[q] = P::fma(dy, xhat, aw[q]);  // a row past the last has dy = 0
+        ab[q] = P::add(ab[q], dy);
+      }
+      s0[r] = P::sum(t0);
+      s1[r] = P::sum(t1);
+    }
+    warp_sum2(s0[0], s0[1]);
+    warp_sum2(s1[0], s1[1]);
+    if (lane == 0) red[buf][warp] = make_float4(s0[0], s0[1], s1[0], s1[1]);
+    __syncthreads();
+    const float4 p = lane < warps ? red[buf][lane] : make_float4(0, 0, 0, 0);
+    buf ^= 1;
+    if (threadIdx.x == 0) {  // everybody has read the slot before this one
+      fence_async_shared();
+      fill(slot == 0 ? slots - 1 : slot - 1, row + (slots - 1) * step);
+    }
+    s0[0] = p.x;
+    s0[1] = p.y;
+    s1[0] = p.z;
+    s1[1] = p.w;
+    warp_sum2(s0[0], s0[1]);
+    warp_sum2(s1[0], s1[1]);
+#pragma unroll
+    for (int r = 0; r < kRingRows; ++r) {
+      if (!in || row + r >= a.rows) break;
+      const uint4 x = lds_vec(at + r * row_bytes), d = lds_vec(at + (kRingRows + r) * row_bytes);
+      const T m2 = P::splat(mean[r]), r2 = P::splat(ok ? rstd[r] : __int_as_float(0x7fffffff));
+      const T c0 = P::splat(s0[r] * inv_h), c1 = P::splat(-s1[r] * inv_h);
+      float o[kE];
+#pragma unroll
+      for (int q = 0; q < P::N; ++q) {
+        const T xhat = P::mul(P::sub(P::template get<ET>(x, q), m2), r2);
+        const T v = P::mul(P::template get<ET>(d, q), w[q]);
+        P::put(P::mul(P::fma(xhat, c1, P::sub(v, c0)), r2), o + 2 * q);
+      }
+      st_stream(reinterpret_cast<uint4*>(static_cast<char*>(a.dx) + (row + r) * row_bytes) + threadIdx.x, L::pack(o));
+    }
+    if (++slot == slots) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+  if (a.partial == nullptr || !in) return;
+  float* pw = a.partial + (int64_t)blockIdx.x * a.H + (int64_t)threadIdx.x * kE;
+  float* pb = pw + (int64_t)gridDim.x * a.H;
+#pragma unroll
+  for (int q = 0; q < P::N; ++q) {
+    float v[2];
+    P::put(aw[q], v);
+    if (!ok) v[0] = v[1] = __int_as_float(0x7fffffff);
+    *reinterpret_cast<float2*>(pw + 2 * q) = make_float2(v[0], v[1]);
+    P::put(ab[q], v);
+    if (!ok) v[0] = v[1] = __int_as_float(0x7fffffff);
+    *reinterpret_cast<float2*>(pb + 2 * q) = make_float2(v[0], v[1]);
+  }
+}
+
 // Rows of any length, one CTA each: a pass for the mean, one for the variance, one to write.
 template <typename ET, typename WT> __global__ void __launch_bounds__(512) fwd_long_kernel(FwdArgs a) {
   __shared__ float red[2 * kWarp];
@@ -524,6 +812,42 @@ int64_t bwd_parts(int64_t rows, int64_t H) {
 
 int cta_threads(int64_t vecs, int nv) { return (int)(((vecs + nv - 1) / nv + kWarp - 1) / kWarp * kWarp); }
 
+// Grid, threads and slots of the ring kernels for rows of `vecs` vectors, of
+// which a slot holds `held`; false where fewer than two slots fit.
+struct RingShape {
+  int threads, grid, slots;
+  size_t smem;
+};
+bool ring_shape(int64_t vecs, int64_t rows, int held, int64_t most, RingShape* z) {
+  if (vecs < 128 || vecs > kMaxThreads) return false;
+  z->threads = (int)((vecs + kWarp - 1) / kWarp * kWarp);
+  int per_sm = kMaxThreads / z->threads;  // 64 registers a thread
+  const size_t slot = (size_t)held * vecs * 16;
+  if (per_sm > 4) per_sm = 4;
+  const int64_t n = kRingSm / per_sm / (int64_t)slot;
+  z->slots = (int)(n < kMaxSlots ? n : kMaxSlots);
+  z->smem = z->slots * slot;
+  int64_t g = (int64_t)num_sms() * per_sm;
+  if (g > most) g = most;
+  const int64_t work = (rows + kRingRows - 1) / kRingRows;
+  z->grid = (int)(work < g ? work : g);
+  return z->slots >= 2;
+}
+
+// Raises a kernel's dynamic shared memory limit once per device.
+template <typename Kernel> bool allow_smem(Kernel k, int bytes, std::atomic<int>* granted) {
+  int dev = 0;
+  (void)cudaGetDevice(&dev);
+  const bool cached = dev >= 0 && dev < 64;
+  if (cached && granted[dev].load(std::memory_order_relaxed) >= bytes) return true;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return false;
+  }
+  if (cached) granted[dev].store(bytes, std::memory_order_relaxed);
+  return true;
+}
+
 template <int VB, typename ET, typename WT, int NV, int LPR, int DEPTH, int MAXT = kMaxThreads>
 int go_fwd(const FwdArgs& a, cudaStream_t s) {
   const int threads = LPR ? kRowWarps * kWarp : cta_threads(a.H / Lanes<VB, ET>::kElems, NV);
@@ -542,6 +866,14 @@ template <int VB, typename ET, typename WT> int dispatch_fwd(const FwdArgs& a, c
   if (vecs <= 64) return go_fwd<VB, ET, WT, 2, 32, 2>(a, s);
   if (vecs <= 128) return go_fwd<VB, ET, WT, 4, 32, 1>(a, s);
   if constexpr (VB == 16) {
+    static std::atomic<int> granted[64];
+    RingShape z;
+    if (ring_shape(vecs, a.rows, kRingRows, INT32_MAX, &z)) {
+      auto k = fwd_ring_kernel<ET, WT>;
+      if (!allow_smem(k, (int)z.smem, granted)) return MOE_ERR_CUDA;
+      launch(k, z.grid, z.threads, z.smem, s, a, z.slots);
+      return check_launch();
+    }
     if (vecs <= 4 * 256) return go_fwd<VB, ET, WT, 4, 0, 1, 256>(a, s);
     if (vecs <= 4 * kMaxThreads) return go_fwd<VB, ET, WT, 4, 0, 1>(a, s);
   } else {
@@ -571,6 +903,15 @@ template <int VB, typename ET, typename WT> int dispatch_bwd(const BwdArgs& a, i
   if (vecs <= 16) return go_bwd<VB, ET, WT, 1, 16, 2>(a, parts, s);
   if (vecs <= 32) return go_bwd<VB, ET, WT, 1, 32, 2>(a, parts, s);
   if constexpr (VB == 16) {
+    static std::atomic<int> granted[64];
+    RingShape z;
+    if (ring_shape(vecs, a.rows, 2 * kRingRows, bwd_parts(a.rows, a.H), &z)) {
+      auto k = bwd_ring_kernel<ET, WT>;
+      if (!allow_smem(k, (int)z.smem, granted)) return MOE_ERR_CUDA;
+      *parts = z.grid;
+      launch(k, z.grid, z.threads, z.smem, s, a, z.slots);
+      return check_launch();
+    }
     if (vecs <= 2 * 512) return go_bwd<VB, ET, WT, 2, 0, 2, 512>(a, parts, s);
     if (vecs <= 2 * kMaxThreads) return go_bwd<VB, ET, WT, 2, 0, 1>(a, parts, s);
   } else {
