@@ -34,9 +34,9 @@ extern "C" {
  * moe_topk_gating's), where an entry -1 is a slot without an expert: a token
  * whose slots are all -1 gets +0.0. Any other entry outside [0, E) sets
  * MOE_STATUS_BAD_EXPERT and counts as -1.
- * Sums are held in fp32 and y is rounded once; the experts of a token are
- * added in increasing expert id (slot order among equal ids). A token's row
- * depends on its own experts only. Repeated calls give the same bits.
+ * Sums are held in fp32 and y is rounded once. A token's row depends on its
+ * own experts only. The order of every sum is fixed: repeated calls give the
+ * same bits.
  *   x         [T, H] dtype, row stride x_stride; router [E, H] dtype
  *   w_gate_up [E, 2F, H] dtype, the gate rows of an expert before its up rows
  *   w_down    [E, H, F] dtype

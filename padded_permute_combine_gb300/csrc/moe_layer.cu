@@ -136,58 +136,164 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // ------------------------------------------------- any type, any alignment
 //
-// A warp per weight row: its lanes stride over the row in vectors of VB
-// bytes (the widest that the lengths and addresses allow), kCols tokens at a
-// time, in fp32. Takes fp32 layers and rows that are not a multiple of 16 bytes.
+// Products on the ordinary cores, in fp32, for fp32 layers and for rows that
+// are not a multiple of 16 bytes: a warp takes four weight rows by four
+// tokens, its lanes 16 bytes of each, so that 8 loads feed 16 dot products
+// (packed in pairs). Weight rows may begin anywhere (SHIFT): a lane then loads
+// the two aligned 16-byte pieces that hold its elements (the second is the
+// next lane's first, in L1) and shifts them together; a row's last piece is
+// masked. Loading such rows element by element reached a quarter of the rate
+// (the odd fp32 layer of 5 tokens, 1001 x 777: 26 and 68 us for the two
+// kernels). The tokens' rows are aligned, x in the workspace where it is not.
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / kWarp;
+constexpr int kRows = 4;
 constexpr int kCols = 4;
+constexpr int kSliceChoices = 256;  // up to so many choices, an expert's F may be sliced (its parts lie in shared memory)
 
-// Router logits: a CTA takes kRouterRows experts by kCols tokens (16 products
-// of 8 loaded vectors), its warps slices of H.
-constexpr int kRouterRows = 4;
-template <int VB, typename ET>
-__global__ void __launch_bounds__(kThreads)
-    router_rows_kernel(const void* __restrict__ x, int64_t x_stride, const void* __restrict__ router, int64_t H, int32_t T,
-                       int32_t E, float* __restrict__ logits) {
-  using L = Lanes<VB, ET>;
-  using V = typename L::V;
-  __shared__ float part[kWarps][kRouterRows * kCols];
-  await_previous_kernel();
-  allow_next_kernel();  // the gating, whose few CTAs then wait in place
-  const int lane = lane_id(), warp = threadIdx.x / kWarp;
-  const int e0 = (int)blockIdx.x * kRouterRows, t0 = (int)blockIdx.y * kCols;
-  const int64_t vecs = H / L::kElems;
-  const V* pr[kRouterRows];
-  const V* px[kCols];
-  float acc[kRouterRows][kCols];
-#pragma unroll
-  for (int r = 0; r < kRouterRows; ++r) {  // past the end: the last expert or token again
-    pr[r] = reinterpret_cast<const V*>(static_cast<const ET*>(router) + (int64_t)(e0 + r < E ? e0 + r : E - 1) * H);
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) acc[r][c] = 0.0f;
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float f2_sum(uint64_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return a + b;
+}
+
+// A row of `len` elements read in 16-byte pieces from its first element on.
+template <typename ET, bool SHIFT> struct WeightRow {
+  static constexpr int kE = 16 / Elem<ET>::kBytes;
+  const uint4* p;
+  int shift, last, len;  // bytes before the first element in *p; the last piece with an element
+  __device__ __forceinline__ WeightRow() {}
+  __device__ __forceinline__ WeightRow(const ET* row, int64_t n) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row);
+    shift = SHIFT ? (int)(at & 15) : 0;
+    p = reinterpret_cast<const uint4*>(at - shift);
+    len = (int)n;
+    last = (int)((shift + n * Elem<ET>::kBytes - 1) / 16);
   }
+  // Piece i, zeros past the row's end.
+  __device__ __forceinline__ uint4 get(int i) const {
+    if constexpr (!SHIFT) return __ldg(p + i);
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const uint4 a = i <= last ? __ldg(p + i) : zero, b = i < last ? __ldg(p + i + 1) : zero;
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (shift & 8) {
 #pragma unroll
-  for (int c = 0; c < kCols; ++c)
-    px[c] = reinterpret_cast<const V*>(static_cast<const ET*>(x) + (t0 + c < T ? t0 + c : T - 1) * x_stride);
-  for (int64_t i = threadIdx.x; i < vecs; i += kThreads) {
-    V rv[kRouterRows], xv[kCols];
+      for (int q = 0; q < 6; ++q) w[q] = w[q + 2];
+    }
+    if (shift & 4) {
 #pragma unroll
-    for (int r = 0; r < kRouterRows; ++r) rv[r] = ld_l1(pr[r] + i);
+      for (int q = 0; q < 5; ++q) w[q] = w[q + 1];
+    }
+    uint4 v;
+    v.x = __funnelshift_r(w[0], w[1], 8 * (shift & 3));
+    v.y = __funnelshift_r(w[1], w[2], 8 * (shift & 3));
+    v.z = __funnelshift_r(w[2], w[3], 8 * (shift & 3));
+    v.w = __funnelshift_r(w[3], w[4], 8 * (shift & 3));
+    const int left = len - i * kE;  // elements of the row from this piece on
+    if (left < kE) {
+      v.x &= word_mask(left, 0);
+      v.y &= word_mask(left, 1);
+      v.z &= word_mask(left, 2);
+      v.w &= word_mask(left, 3);
+    }
+    return v;
+  }
+  __device__ __forceinline__ static uint32_t word_mask(int left, int word) {
+    if constexpr (Elem<ET>::kBytes == 4) return left > word ? 0xffffffffu : 0u;
+    const int m = left - 2 * word;
+    return m >= 2 ? 0xffffffffu : (m == 1 ? 0xffffu : 0u);
+  }
+};
+
+// kE elements of a token's row as fp32 pairs: of ET, or fp32 already.
+template <typename ET, typename XT> struct TokenRow {
+  static constexpr int kE = 16 / Elem<ET>::kBytes;
+  static constexpr int kBytes = kE * Elem<XT>::kBytes;
+  const char* p;
+  __device__ __forceinline__ void get(int i, uint64_t (&out)[kE / 2]) const {
+    using V = typename Vec<kBytes>::T;
+    const V v = ld_l1(reinterpret_cast<const V*>(p) + i);
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) xv[c] = ld_l1(px[c] + i);
+    for (int q = 0; q < kE / 2; ++q) out[q] = f2_elems<XT>(v, q);
+  }
+};
+
+// Dot products of kRows weight rows with kCols tokens over pieces [from, to): this lane's part.
+template <typename ET, typename XT, bool SHIFT>
+__device__ __forceinline__ void dots(const WeightRow<ET, SHIFT> (&w)[kRows], const TokenRow<ET, XT> (&x)[kCols], int from,
+                                     int to, float (&out)[kRows][kCols]) {
+  constexpr int kP = WeightRow<ET, SHIFT>::kE / 2;
+  uint64_t acc[kRows][kCols];
 #pragma unroll
-    for (int r = 0; r < kRouterRows; ++r) {
+  for (int r = 0; r < kRows; ++r) {
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) {
+    for (int c = 0; c < kCols; ++c) acc[r][c] = 0ull;
+  }
+#pragma unroll 2
+  for (int i = from + lane_id(); i < to; i += kWarp) {
+    uint4 wv[kRows];
+    uint64_t xv[kCols][kP];
 #pragma unroll
-        for (int q = 0; q < L::kElems; ++q) acc[r][c] += L::get(rv[r], q) * L::get(xv[c], q);
+    for (int r = 0; r < kRows; ++r) wv[r] = w[r].get(i);
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) x[c].get(i, xv[c]);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+      for (int q = 0; q < kP; ++q) {
+        const uint64_t e = f2_elems<ET>(wv[r], q);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[r][c] = f2_fma(e, xv[c][q], acc[r][c]);
       }
     }
   }
 #pragma unroll
-  for (int r = 0; r < kRouterRows; ++r) {
+  for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) out[r][c] = f2_sum(acc[r][c]);
+  }
+}
+
+// x's rows at 16-byte boundaries, padded with zeros to pieces of 16 bytes.
+template <typename ET>
+__global__ void __launch_bounds__(kThreads) align_rows_kernel(const ET* __restrict__ x, int64_t x_stride, int64_t H, int64_t padded,
+                                                              ET* __restrict__ out) {
+  await_previous_kernel();
+  allow_next_kernel();
+  const int64_t t = blockIdx.y;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < padded; i += (int64_t)gridDim.x * kThreads)
+    out[t * padded + i] = i < H ? x[t * x_stride + i] : ET(0.0f);
+}
+
+// Router logits: a CTA takes kRows experts by kCols tokens, its warps slices of H.
+template <typename ET, bool SHIFT>
+__global__ void __launch_bounds__(kThreads)
+    router_rows_kernel(const ET* __restrict__ x, int64_t x_ld, const ET* __restrict__ router, int64_t H, int32_t T, int32_t E,
+                       float* __restrict__ logits) {
+  __shared__ float part[kWarps][kRows * kCols];
+  await_previous_kernel();
+  allow_next_kernel();  // the gating, whose few CTAs then wait in place
+  const int lane = lane_id(), warp = threadIdx.x / kWarp;
+  const int e0 = (int)blockIdx.x * kRows, t0 = (int)blockIdx.y * kCols;
+  WeightRow<ET, SHIFT> w[kRows];
+  TokenRow<ET, ET> xr[kCols];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r)  // past the end: the last expert or token again
+    w[r] = WeightRow<ET, SHIFT>(router + (int64_t)(e0 + r < E ? e0 + r : E - 1) * H, H);
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) xr[c].p = reinterpret_cast<const char*>(x + (t0 + c < T ? t0 + c : T - 1) * x_ld);
+  const int pieces = (int)((H + w[0].kE - 1) / w[0].kE);
+  const int per = ((pieces + kWarps - 1) / kWarps + kWarp - 1) / kWarp * kWarp;
+  float acc[kRows][kCols];
+  dots<ET, ET, SHIFT>(w, xr, warp * per, (warp + 1) * per < pieces ? (warp + 1) * per : pieces, acc);
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
 #pragma unroll
     for (int c = 0; c < kCols; ++c) {
       const float s = warp_sum(acc[r][c]);
@@ -195,111 +301,120 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   __syncthreads();
-  if (threadIdx.x < kRouterRows * kCols) {
+  if (threadIdx.x < kRows * kCols) {
     const int r = threadIdx.x / kCols, c = threadIdx.x % kCols;
     float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += part[w][threadIdx.x];
+    for (int w2 = 0; w2 < kWarps; ++w2) s += part[w2][threadIdx.x];
     if (e0 + r < E && t0 + c < T) logits[(int64_t)(t0 + c) * E + e0 + r] = s;
   }
 }
 
-template <int VB, typename ET> __global__ void __launch_bounds__(kThreads) gate_up_rows_kernel(LayerArgs a) {
-  using L = Lanes<VB, ET>;
-  using V = typename L::V;
+// A warp takes the gate and up rows of two f's of one expert, for all its tokens.
+template <typename ET, bool SHIFT>
+__global__ void __launch_bounds__(kThreads) gate_up_rows_kernel(LayerArgs a, const ET* __restrict__ x, int64_t x_ld, int64_t h_ld) {
   extern __shared__ int32_t smem[];
   await_previous_kernel();
   const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, a.status, smem);
   const int lane = lane_id();
-  const int64_t vecs = a.H / L::kElems;
-  for (int64_t w = (int64_t)blockIdx.x * kWarps + threadIdx.x / kWarp; w < s.active * a.F;
-       w += (int64_t)gridDim.x * kWarps) {
-    const int q = (int)(w / a.F);
-    const int64_t f = w % a.F;
-    const ET* gate = static_cast<const ET*>(a.w_gate_up) + ((int64_t)s.expert[q] * 2 * a.F + f) * a.H;
-    const V* pg = reinterpret_cast<const V*>(gate);
-    const V* pu = reinterpret_cast<const V*>(gate + a.F * a.H);
-    for (int i0 = s.begin[q]; i0 < s.begin[q + 1]; i0 += kCols) {
-      const int last = s.begin[q + 1] - 1;
-      const V* px[kCols];
-      float g[kCols], u[kCols];
+  const int64_t couples = (a.F + 1) / 2;
+  const int pieces = (int)((a.H + WeightRow<ET, SHIFT>::kE - 1) / WeightRow<ET, SHIFT>::kE);
+  for (int64_t v = (int64_t)blockIdx.x * kWarps + threadIdx.x / kWarp; v < s.active * couples;
+       v += (int64_t)gridDim.x * kWarps) {
+    const int q = (int)(v / couples);
+    const int64_t f0 = v % couples * 2, f1 = f0 + 1 < a.F ? f0 + 1 : f0;
+    const ET* gate = static_cast<const ET*>(a.w_gate_up) + (int64_t)s.expert[q] * 2 * a.F * a.H;
+    const ET* up = gate + a.F * a.H;
+    const WeightRow<ET, SHIFT> w[kRows] = {{gate + f0 * a.H, a.H}, {gate + f1 * a.H, a.H}, {up + f0 * a.H, a.H}, {up + f1 * a.H, a.H}};
+    const int last = s.begin[q + 1] - 1;
+    for (int i0 = s.begin[q]; i0 <= last; i0 += kCols) {
+      TokenRow<ET, ET> xr[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c)
+        xr[c].p = reinterpret_cast<const char*>(x + s.token[i0 + c < last ? i0 + c : last] * x_ld);
+      float acc[kRows][kCols];
+      dots<ET, ET, SHIFT>(w, xr, 0, pieces, acc);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[r][c] = warp_sum(acc[r][c]);
+      }
+      // Lane 2c + f finishes token c's f.
 #pragma unroll
       for (int c = 0; c < kCols; ++c) {
-        const int t = s.token[i0 + c < last ? i0 + c : last];
-        px[c] = reinterpret_cast<const V*>(static_cast<const ET*>(a.x) + t * a.x_stride);
-        g[c] = u[c] = 0.0f;
-      }
-#pragma unroll 2
-      for (int64_t i = lane; i < vecs; i += kWarp) {
-        const V gv = ld_l1(pg + i), uv = ld_l1(pu + i);
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-          const V xv = ld_l1(px[c] + i);
-#pragma unroll
-          for (int k = 0; k < L::kElems; ++k) {
-            g[c] += L::get(gv, k) * L::get(xv, k);
-            u[c] += L::get(uv, k) * L::get(xv, k);
-          }
+        for (int f = 0; f < 2; ++f) {
+          if (lane == 2 * c + f && i0 + c <= last && f0 + f < a.F)
+            a.h[(i0 + c) * h_ld + f0 + f] = __ldcg(a.weights + s.order[i0 + c]) * (silu(acc[f][c]) * acc[2 + f][c]);
         }
       }
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        const float gs = warp_sum(g[c]), us = warp_sum(u[c]);
-        if (lane == 0 && i0 + c <= last) a.h[(i0 + c) * a.F + f] = a.weights[s.order[i0 + c]] * (silu(gs) * us);
-      }
     }
+    // The places that pad a row of h.
+    if (f0 + 2 >= a.F)
+      for (int i = s.begin[q]; i <= last; ++i)
+        for (int64_t f = a.F + lane; f < h_ld; f += kWarp) a.h[i * h_ld + f] = 0.0f;
   }
 }
 
-template <int VB, typename ET> __global__ void __launch_bounds__(kThreads) down_rows_kernel(LayerArgs a) {
-  using L = Lanes<VB, ET>;
-  using V = typename L::V;
+// A CTA takes kRows columns of y, its warps the active experts (and slices of
+// F where those are fewer than the warps); then each token's parts are added
+// in the order of its slots.
+template <typename ET, bool SHIFT>
+__global__ void __launch_bounds__(kThreads) down_rows_kernel(LayerArgs a, int64_t h_ld) {
   extern __shared__ int32_t smem[];
   await_previous_kernel();
-  const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, a.status, smem);
-  const int lane = lane_id();
-  // This warp's row of y for every token.
-  float* sum = reinterpret_cast<float*>(smem + segments_bytes(a.n, a.E) / sizeof(int32_t)) +
-               (threadIdx.x / kWarp) * a.T;
-  const int64_t vecs = a.F / L::kElems;
-  for (int64_t r = (int64_t)blockIdx.x * kWarps + threadIdx.x / kWarp; r < a.H; r += (int64_t)gridDim.x * kWarps) {
-    for (int t = lane; t < a.T; t += kWarp) sum[t] = 0.0f;
-    __syncwarp();
-    for (int q = 0; q < s.active; ++q) {
-      const V* pw = reinterpret_cast<const V*>(static_cast<const ET*>(a.w_down) + ((int64_t)s.expert[q] * a.H + r) * a.F);
+  const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, nullptr, smem);
+  const int lane = lane_id(), warp = threadIdx.x / kWarp;
+  int32_t* place = smem + segments_bytes(a.n, a.E) / sizeof(int32_t);  // [n]: of an assignment, -1 without
+  float* part = reinterpret_cast<float*>(place + a.n);                 // [slices][n][kRows]
+  for (int i = threadIdx.x; i < a.n; i += kThreads) place[i] = -1;
+  __syncthreads();
+  const int placed = s.begin[s.active];
+  for (int i = threadIdx.x; i < placed; i += kThreads) place[s.order[i]] = i;
+  const int slices = a.n <= kSliceChoices && s.active > 0 && s.active < kWarps ? kWarps / s.active : 1;
+  const int pieces = (int)((a.F + WeightRow<ET, SHIFT>::kE - 1) / WeightRow<ET, SHIFT>::kE);
+  const int per = ((pieces + slices - 1) / slices + kWarp - 1) / kWarp * kWarp;
+  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.H; r0 += (int64_t)gridDim.x * kRows) {
+    for (int v = warp; v < s.active * slices; v += kWarps) {
+      const int q = v / slices, slice = v % slices;
+      const ET* base = static_cast<const ET*>(a.w_down) + (int64_t)s.expert[q] * a.H * a.F;
+      WeightRow<ET, SHIFT> w[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) w[r] = WeightRow<ET, SHIFT>(base + (r0 + r < a.H ? r0 + r : a.H - 1) * a.F, a.F);
       const int last = s.begin[q + 1] - 1;
       for (int i0 = s.begin[q]; i0 <= last; i0 += kCols) {
-        const float* ph[kCols];
-        float acc[kCols];
+        TokenRow<ET, float> hr[kCols];
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-          ph[c] = a.h + (i0 + c < last ? i0 + c : last) * a.F;
-          acc[c] = 0.0f;
-        }
-#pragma unroll 2
-        for (int64_t i = lane; i < vecs; i += kWarp) {
-          const V wv = ld_l1(pw + i);
+        for (int c = 0; c < kCols; ++c)
+          hr[c].p = reinterpret_cast<const char*>(a.h + (i0 + c < last ? i0 + c : last) * h_ld);
+        float acc[kRows][kCols];
+        dots<ET, float, SHIFT>(w, hr, slice * per, (slice + 1) * per < pieces ? (slice + 1) * per : pieces, acc);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {
-#pragma unroll
-            for (int k = 0; k < L::kElems; ++k) acc[c] += L::get(wv, k) * __ldg(ph[c] + i * L::kElems + k);
+            const float v2 = warp_sum(acc[r][c]);
+            if (lane == r * kCols + c && i0 + c <= last) part[((int64_t)slice * a.n + i0 + c) * kRows + r] = v2;
           }
-        }
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-          const float v = warp_sum(acc[c]);
-          if (lane == 0 && i0 + c <= last) sum[s.token[i0 + c]] += v;
         }
       }
     }
-    __syncwarp();
-    for (int t = lane; t < a.T; t += kWarp) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.T * kRows; i += kThreads) {
+      const int t = i / kRows, r = i % kRows;
+      if (r0 + r >= a.H) continue;
+      float sum = 0.0f;
+      for (int k = 0; k < a.K; ++k) {
+        const int at = place[t * a.K + k];
+        if (at < 0) continue;
+        for (int slice = 0; slice < slices; ++slice) sum += part[((int64_t)slice * a.n + at) * kRows + r];
+      }
       if constexpr (Elem<ET>::kBytes == 4)
-        static_cast<float*>(a.y)[t * a.H + r] = sum[t];
+        static_cast<float*>(a.y)[t * a.H + r0 + r] = sum;
       else
-        static_cast<__nv_bfloat16*>(a.y)[t * a.H + r] = __float2bfloat16_rn(sum[t]);
+        static_cast<__nv_bfloat16*>(a.y)[t * a.H + r0 + r] = __float2bfloat16_rn(sum);
     }
-    __syncwarp();
+    __syncthreads();
   }
 }
 
@@ -866,6 +981,8 @@ __global__ void __launch_bounds__(kStreamThreads)
   }
 }
 
+// ------------------------------------------------------------------ host
+
 // Raises a kernel's dynamic shared memory limit once per device.
 template <typename Kernel> bool allow_smem(Kernel k, int bytes, std::atomic<int>* granted) {
   int dev = 0;
@@ -880,29 +997,31 @@ template <typename Kernel> bool allow_smem(Kernel k, int bytes, std::atomic<int>
   return true;
 }
 
-// ------------------------------------------------------------------ host
+// Elements of a row padded to 32 bytes (of fp32, what 16 bytes of bf16 weights go with).
+int64_t padded_row(int64_t n) { return (n + 7) / 8 * 8; }
 
-template <int VB, typename ET>
-int run_router(const LayerArgs& a, const void* router, float* logits, int32_t mode, int32_t normalize,
-               int32_t* top_expert, float* weights, cudaStream_t s) {
-  if (router == nullptr) return MOE_OK;
-  auto k = router_rows_kernel<VB, ET>;
-  launch(k, dim3((unsigned)((a.E + kRouterRows - 1) / kRouterRows), (unsigned)((a.T + kCols - 1) / kCols)), kThreads, 0, s,
-         a.x, a.x_stride, router, a.H, a.T, a.E, logits);
+template <typename ET, bool SHIFT>
+int run_router(const LayerArgs& a, const ET* x, int64_t x_ld, const void* router, float* logits, int32_t mode,
+               int32_t normalize, int32_t* top_expert, float* weights, cudaStream_t s) {
+  launch(router_rows_kernel<ET, SHIFT>, dim3((unsigned)((a.E + kRows - 1) / kRows), (unsigned)((a.T + kCols - 1) / kCols)),
+         kThreads, 0, s, x, x_ld, static_cast<const ET*>(router), a.H, a.T, a.E, logits);
   return moe_topk_gating(logits, a.T, a.E, a.K, mode, normalize, top_expert, weights,
                          reinterpret_cast<moe_stream_t>(s));
 }
 
-template <int VB, typename ET> int run_rows(const LayerArgs& a, cudaStream_t s) {
+template <typename ET, bool SHIFT> int run_rows(const LayerArgs& a, const ET* x, int64_t x_ld, cudaStream_t s) {
+  static std::atomic<int> granted[64];
   const size_t seg = segments_bytes(a.n, a.E);
-  auto g = gate_up_rows_kernel<VB, ET>;
-  launch(g, persistent_grid(g, kThreads, seg, ((a.n < a.E ? a.n : a.E) * a.F + kWarps - 1) / kWarps), kThreads, seg, s, a);
-  const size_t down = seg + sizeof(float) * kWarps * a.T;
-  auto d = down_rows_kernel<VB, ET>;
-  launch(d, persistent_grid(d, kThreads, down, (a.H + kWarps - 1) / kWarps), kThreads, down, s, a);
+  const int64_t h_ld = padded_row(a.F), couples = (a.F + 1) / 2;
+  auto g = gate_up_rows_kernel<ET, SHIFT>;
+  launch(g, persistent_grid(g, kThreads, seg, ((a.n < a.E ? a.n : a.E) * couples + kWarps - 1) / kWarps), kThreads, seg, s, a, x,
+         x_ld, h_ld);
+  const size_t smem = seg + sizeof(int32_t) * a.n + sizeof(float) * kRows * a.n * (a.n <= kSliceChoices ? kWarps : 1);
+  auto d = down_rows_kernel<ET, SHIFT>;
+  if (!allow_smem(d, (int)smem, granted)) return MOE_ERR_CUDA;
+  launch(d, persistent_grid(d, kThreads, smem, (a.H + kRows - 1) / kRows), kThreads, smem, s, a, h_ld);
   return check_launch();
 }
-
 
 // cuTensorMapEncodeTiled through the runtime (the library links no driver library).
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -1040,23 +1159,40 @@ int run_stream(const LayerArgs& a, cudaStream_t s) {
 }
 
 template <typename ET>
-int dispatch(const LayerArgs& a, const void* router, float* logits, int32_t mode, int32_t normalize,
+int dispatch(const LayerArgs& a, const void* router, float* logits, ET* x_copy, int32_t mode, int32_t normalize,
              int32_t* top_expert, float* weights, cudaStream_t s) {
   constexpr int kE = 16 / Elem<ET>::kBytes;
-  const bool by16 = a.H % kE == 0 && a.F % kE == 0 && a.x_stride % kE == 0 && aligned(a.x, 16) &&
-                    aligned(a.w_gate_up, 16) && aligned(a.w_down, 16) && aligned(router, 16);
-  const int rc = by16 ? run_router<16, ET>(a, router, logits, mode, normalize, top_expert, weights, s)
-                      : run_router<Elem<ET>::kBytes, ET>(a, router, logits, mode, normalize, top_expert, weights, s);
-  if (rc != MOE_OK) return rc;
-  if (!by16) return run_rows<Elem<ET>::kBytes, ET>(a, s);
-  if constexpr (Elem<ET>::kBytes == 2) {
-    if (a.H >= kBlock && a.F >= kBlock) return run_stream(a, s);  // at least one box each way
+  const ET* x = static_cast<const ET*>(a.x);
+  int64_t x_ld = a.x_stride;
+  if (a.H % kE != 0 || x_ld % kE != 0 || !aligned(a.x, 16)) {
+    const int64_t padded = padded_row(a.H);
+    launch(align_rows_kernel<ET>, dim3((unsigned)((padded + 4 * kThreads - 1) / (4 * kThreads)), (unsigned)a.T), kThreads, 0, s, x,
+           x_ld, a.H, padded, x_copy);
+    x = x_copy;
+    x_ld = padded;
   }
-  return run_rows<16, ET>(a, s);
+  if (router != nullptr) {
+    const int rc = a.H % kE == 0 && aligned(router, 16)
+                       ? run_router<ET, false>(a, x, x_ld, router, logits, mode, normalize, top_expert, weights, s)
+                       : run_router<ET, true>(a, x, x_ld, router, logits, mode, normalize, top_expert, weights, s);
+    if (rc != MOE_OK) return rc;
+  }
+  const bool by16 = a.H % kE == 0 && a.F % kE == 0 && aligned(a.w_gate_up, 16) && aligned(a.w_down, 16);
+  if (!by16) return run_rows<ET, true>(a, x, x_ld, s);
+  if constexpr (Elem<ET>::kBytes == 2) {
+    if (a.H >= kBlock && a.F >= kBlock) {  // at least one box each way
+      LayerArgs b = a;
+      b.x = x;
+      b.x_stride = x_ld;
+      return run_stream(b, s);
+    }
+  }
+  return run_rows<ET, false>(a, x, x_ld, s);
 }
 
-// Bytes of the workspace's parts: the logits, then h.
+// Bytes of the workspace's parts: the logits, h, and x where its rows are not aligned.
 size_t logits_bytes(int64_t T, int32_t E) { return ((size_t)T * E * sizeof(float) + 255) / 256 * 256; }
+size_t h_bytes(int64_t n, int64_t F) { return ((size_t)n * (size_t)padded_row(F) * sizeof(float) + 255) / 256 * 256; }
 
 bool sizes_ok(int64_t T, int64_t H, int64_t F, int32_t E, int32_t K) {
   return T >= 0 && H >= 1 && F >= 1 && E >= 1 && K >= 1 && K <= E && K <= MOE_MAX_TOP_K &&
@@ -1082,13 +1218,17 @@ int run_layer(const void* x, int32_t dtype, int64_t x_stride, const void* router
   if (!aligned(x, eb) || !aligned(router, eb) || !aligned(w_gate_up, eb) || !aligned(w_down, eb) || !aligned(y, eb) ||
       !aligned(top_expert, 4) || !aligned(weights, 4) || !aligned(workspace, 16) || !aligned(d_status, 4))
     return MOE_ERR_UNSUPPORTED;
-  float* logits = static_cast<float*>(workspace);
-  float* h = reinterpret_cast<float*>(static_cast<char*>(workspace) + logits_bytes(T, E));
+  char* base = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~(uintptr_t)255);
+  float* logits = reinterpret_cast<float*>(base);
+  float* h = reinterpret_cast<float*>(base + logits_bytes(T, E));
   const LayerArgs a{x, w_gate_up, w_down, top_expert, weights, h, y, T > 1 ? x_stride : H, H, F,
                     (int32_t)T, E, K, (int32_t)(T * K), d_status};
+  void* x_copy = reinterpret_cast<char*>(h) + h_bytes(T * K, F);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == MOE_F32) return dispatch<float>(a, router, logits, mode, normalize, top_out, weights_out, s);
-  return dispatch<__nv_bfloat16>(a, router, logits, mode, normalize, top_out, weights_out, s);
+  if (dtype == MOE_F32)
+    return dispatch<float>(a, router, logits, static_cast<float*>(x_copy), mode, normalize, top_out, weights_out, s);
+  return dispatch<__nv_bfloat16>(a, router, logits, static_cast<__nv_bfloat16*>(x_copy), mode, normalize, top_out,
+                                 weights_out, s);
 }
 
 }  // namespace
@@ -1098,7 +1238,7 @@ using namespace moe;
 
 extern "C" size_t moe_layer_workspace_size(int64_t T, int64_t H, int64_t F, int32_t E, int32_t K) {
   if (!sizes_ok(T, H, F, E, K) || !few(T, E, K)) return 0;
-  return logits_bytes(T, E) + ((size_t)T * K * (size_t)F * sizeof(float) + 255) / 256 * 256 + 256;
+  return logits_bytes(T, E) + h_bytes(T * K, F) + (size_t)T * (size_t)padded_row(H) * sizeof(float) + 256;
 }
 
 extern "C" int moe_layer(const void* x, int32_t dtype, int64_t x_stride, const void* router, const void* w_gate_up,
