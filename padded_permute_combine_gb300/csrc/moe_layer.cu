@@ -15,6 +15,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "bulk.cuh"
 #include "common.cuh"
@@ -150,6 +151,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / kWarp;
 constexpr int kRows = 4;
 constexpr int kCols = 4;
+template <int N> using Cols = std::integral_constant<int, N>;
 constexpr int kSliceChoices = 256;  // up to so many choices, an expert's F may be sliced (its parts lie in shared memory)
 
 __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
@@ -224,39 +226,39 @@ template <typename ET, typename XT> struct TokenRow {
   }
 };
 
-// Dot products of kRows weight rows with kCols tokens over pieces [from, to): this lane's part.
-template <typename ET, typename XT, bool SHIFT>
-__device__ __forceinline__ void dots(const WeightRow<ET, SHIFT> (&w)[kRows], const TokenRow<ET, XT> (&x)[kCols], int from,
-                                     int to, float (&out)[kRows][kCols]) {
+// Dot products of kRows weight rows with C tokens over pieces [from, to): this lane's part.
+template <int C, typename ET, typename XT, bool SHIFT>
+__device__ __forceinline__ void dots(const WeightRow<ET, SHIFT> (&w)[kRows], const TokenRow<ET, XT> (&x)[C], int from, int to,
+                                     float (&out)[kRows][C]) {
   constexpr int kP = WeightRow<ET, SHIFT>::kE / 2;
-  uint64_t acc[kRows][kCols];
+  uint64_t acc[kRows][C];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) acc[r][c] = 0ull;
+    for (int c = 0; c < C; ++c) acc[r][c] = 0ull;
   }
-#pragma unroll 2
+#pragma unroll(C == 1 ? 4 : 2)
   for (int i = from + lane_id(); i < to; i += kWarp) {
     uint4 wv[kRows];
-    uint64_t xv[kCols][kP];
+    uint64_t xv[C][kP];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) wv[r] = w[r].get(i);
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) x[c].get(i, xv[c]);
+    for (int c = 0; c < C; ++c) x[c].get(i, xv[c]);
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
 #pragma unroll
       for (int q = 0; q < kP; ++q) {
         const uint64_t e = f2_elems<ET>(wv[r], q);
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) acc[r][c] = f2_fma(e, xv[c][q], acc[r][c]);
+        for (int c = 0; c < C; ++c) acc[r][c] = f2_fma(e, xv[c][q], acc[r][c]);
       }
     }
   }
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) out[r][c] = f2_sum(acc[r][c]);
+    for (int c = 0; c < C; ++c) out[r][c] = f2_sum(acc[r][c]);
   }
 }
 
@@ -291,7 +293,7 @@ __global__ void __launch_bounds__(kThreads)
   const int pieces = (int)((H + w[0].kE - 1) / w[0].kE);
   const int per = ((pieces + kWarps - 1) / kWarps + kWarp - 1) / kWarp * kWarp;
   float acc[kRows][kCols];
-  dots<ET, ET, SHIFT>(w, xr, warp * per, (warp + 1) * per < pieces ? (warp + 1) * per : pieces, acc);
+  dots(w, xr, warp * per, (warp + 1) * per < pieces ? (warp + 1) * per : pieces, acc);
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
 #pragma unroll
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(kThreads)
 
 // A warp takes the gate and up rows of two f's of one expert, for all its tokens.
 template <typename ET, bool SHIFT>
-__global__ void __launch_bounds__(kThreads) gate_up_rows_kernel(LayerArgs a, const ET* __restrict__ x, int64_t x_ld, int64_t h_ld) {
+__global__ void __launch_bounds__(kThreads, 2) gate_up_rows_kernel(LayerArgs a, const ET* __restrict__ x, int64_t x_ld, int64_t h_ld) {
   extern __shared__ int32_t smem[];
   await_previous_kernel();
   const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, a.status, smem);
@@ -327,27 +329,34 @@ __global__ void __launch_bounds__(kThreads) gate_up_rows_kernel(LayerArgs a, con
     const ET* up = gate + a.F * a.H;
     const WeightRow<ET, SHIFT> w[kRows] = {{gate + f0 * a.H, a.H}, {gate + f1 * a.H, a.H}, {up + f0 * a.H, a.H}, {up + f1 * a.H, a.H}};
     const int last = s.begin[q + 1] - 1;
-    for (int i0 = s.begin[q]; i0 <= last; i0 += kCols) {
-      TokenRow<ET, ET> xr[kCols];
+    // C tokens from place i0 on; past the last, the last again.
+    auto tile = [&](auto cols, int i0) {
+      constexpr int C = decltype(cols)::value;
+      TokenRow<ET, ET> xr[C];
 #pragma unroll
-      for (int c = 0; c < kCols; ++c)
-        xr[c].p = reinterpret_cast<const char*>(x + s.token[i0 + c < last ? i0 + c : last] * x_ld);
-      float acc[kRows][kCols];
-      dots<ET, ET, SHIFT>(w, xr, 0, pieces, acc);
+      for (int c = 0; c < C; ++c) xr[c].p = reinterpret_cast<const char*>(x + s.token[i0 + c < last ? i0 + c : last] * x_ld);
+      float acc[kRows][C];
+      dots(w, xr, 0, pieces, acc);
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) acc[r][c] = warp_sum(acc[r][c]);
+        for (int c = 0; c < C; ++c) acc[r][c] = warp_sum(acc[r][c]);
       }
       // Lane 2c + f finishes token c's f.
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) {
+      for (int c = 0; c < C; ++c) {
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
           if (lane == 2 * c + f && i0 + c <= last && f0 + f < a.F)
             a.h[(i0 + c) * h_ld + f0 + f] = __ldcg(a.weights + s.order[i0 + c]) * (silu(acc[f][c]) * acc[2 + f][c]);
         }
       }
+    };
+    for (int i0 = s.begin[q]; i0 <= last; i0 += kCols) {
+      if (i0 == last)
+        tile(Cols<1>(), i0);
+      else
+        tile(Cols<kCols>(), i0);
     }
     // The places that pad a row of h.
     if (f0 + 2 >= a.F)
@@ -360,7 +369,7 @@ __global__ void __launch_bounds__(kThreads) gate_up_rows_kernel(LayerArgs a, con
 // F where those are fewer than the warps); then each token's parts are added
 // in the order of its slots.
 template <typename ET, bool SHIFT>
-__global__ void __launch_bounds__(kThreads) down_rows_kernel(LayerArgs a, int64_t h_ld) {
+__global__ void __launch_bounds__(kThreads, 2) down_rows_kernel(LayerArgs a, int64_t h_ld) {
   extern __shared__ int32_t smem[];
   await_previous_kernel();
   const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, nullptr, smem);
@@ -382,21 +391,27 @@ __global__ void __launch_bounds__(kThreads) down_rows_kernel(LayerArgs a, int64_
 #pragma unroll
       for (int r = 0; r < kRows; ++r) w[r] = WeightRow<ET, SHIFT>(base + (r0 + r < a.H ? r0 + r : a.H - 1) * a.F, a.F);
       const int last = s.begin[q + 1] - 1;
-      for (int i0 = s.begin[q]; i0 <= last; i0 += kCols) {
-        TokenRow<ET, float> hr[kCols];
+      auto tile = [&](auto cols, int i0) {
+        constexpr int C = decltype(cols)::value;
+        TokenRow<ET, float> hr[C];
 #pragma unroll
-        for (int c = 0; c < kCols; ++c)
-          hr[c].p = reinterpret_cast<const char*>(a.h + (i0 + c < last ? i0 + c : last) * h_ld);
-        float acc[kRows][kCols];
-        dots<ET, float, SHIFT>(w, hr, slice * per, (slice + 1) * per < pieces ? (slice + 1) * per : pieces, acc);
+        for (int c = 0; c < C; ++c) hr[c].p = reinterpret_cast<const char*>(a.h + (i0 + c < last ? i0 + c : last) * h_ld);
+        float acc[kRows][C];
+        dots(w, hr, slice * per, (slice + 1) * per < pieces ? (slice + 1) * per : pieces, acc);
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) {
+          for (int c = 0; c < C; ++c) {
             const float v2 = warp_sum(acc[r][c]);
-            if (lane == r * kCols + c && i0 + c <= last) part[((int64_t)slice * a.n + i0 + c) * kRows + r] = v2;
+            if (lane == r * C + c && i0 + c <= last) part[((int64_t)slice * a.n + i0 + c) * kRows + r] = v2;
           }
         }
+      };
+      for (int i0 = s.begin[q]; i0 <= last; i0 += kCols) {
+        if (i0 == last)
+          tile(Cols<1>(), i0);
+        else
+          tile(Cols<kCols>(), i0);
       }
     }
     __syncthreads();
