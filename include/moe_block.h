@@ -113,7 +113,7 @@ int moe_layer_norm_bwd(const void* dy, int64_t dy_stride, const void* x, int32_t
  */
 typedef struct moe_grad_tensor {
   const void* grad;
-  void* out;     /* nullable when only norms are taken */
+  void* out;     /* nullable: then moe_clip_grads leaves the tensor alone */
   int64_t numel;
   int32_t dtype; /* MOE_F32 or MOE_BF16, of grad and out */
   int32_t reserved;

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads)
   if (c > 1.0f) c = 1.0f;  // NaN stays
   for (int64_t i = P - 1 - blockIdx.x; i >= 0; i -= gridDim.x) {
     const moe_grad_piece p = pieces[i];
-    if (c == 1.0f && p.out == p.grad) continue;
+    if (p.out == nullptr || (c == 1.0f && p.out == p.grad)) continue;
     if (p.dtype == MOE_F32)
       scale_piece<float>(p.grad, p.out, (int)p.numel, c);
     else
