@@ -10,9 +10,8 @@
 // are on their way into registers while one is reduced. In the backward pass a
 // thread owns the same columns in every row it meets, so the two sums over
 // rows live in its registers; each CTA writes one row of partial sums, and a
-// second launch adds those in a fixed order. Rows of 2 to 16 KB in 16-byte
-// pieces come through a ring in shared memory filled by bulk copies, two rows
-// at a time. Rows too long for the registers take kernels that read a row
+// second launch adds those in a fixed order. The backward pass takes rows of up
+// to 32 KB through a ring in shared memory. Rows too long for the registers take kernels that read a row
 // again for each pass over it.
 #include <math.h>
 
@@ -419,16 +418,20 @@ __global__ void __launch_bounds__(LPR ? kRowWarps * kWarp : MAXT, LPR ? 3 : 1) b
 
 // ------------------------------------------- rows through shared memory
 //
-// One 16-byte vector of the row per thread, kRingRows consecutive rows at a
-// time, copied into a ring of slots by bulk copies (one for both rows where
-// they are adjacent). What that buys over loads into registers: the copies
-// ahead cost none, so the weights (and the column sums) fit in them instead of
-// being read again for each row, which at fp32 was four times the row's bytes,
-// and one barrier and one round of exchanges serve two rows. A slot is free
-// again after the next iteration's barrier. Waits are bounded; after one gives
-// up the CTA writes NaN instead of waiting again.
+// The backward pass for rows of more than 512 bytes, up to 32 KB: two 16-byte
+// vectors of the row per thread, two consecutive rows at a time (above 16 KB
+// four vectors and one row of bf16), copied into a ring of slots
+// by bulk copies (one for both rows where they are adjacent). What that buys
+// over loads into registers: the copies ahead cost none (they read x and dy
+// from the slot again after the sums instead of keeping them), and one barrier
+// and one round of exchanges serve two rows. Those are a warp's cost whatever
+// it holds: with one vector a thread they bounded the kernel (79 instead of 73
+// us at 8192 x 7168 bf16, 84 with loads into registers). A slot is free again
+// after the next iteration's barrier. Waits are bounded; after one gives up
+// the CTA writes NaN instead of waiting again. (The forward pass gains nothing
+// this way: 47 us instead of 45.)
 
-constexpr int kRingRows = 2;
+constexpr int kRingThreads = 512;
 constexpr int kMaxSlots = 16;
 constexpr int kRingSm = 200 * 1024;  // shared memory of an SM for rings
 
@@ -446,13 +449,13 @@ __device__ __forceinline__ void warp_sum2(float& a, float& b) {
 
 struct RowRing {
   uint32_t data, bars;
-  int slots, slot_bytes, row_bytes;
-  // One thread: the rows [row, row + n) of up to two matrices into slot i.
-  __device__ __forceinline__ void fill(int i, const char* x, int64_t x_stride, const char* y, int64_t y_stride, int n) const {
+  int slot_bytes, row_bytes, dy_at;  // dy_at: where a slot's rows of dy begin
+  // One thread: n rows of x, then of dy, into slot i.
+  __device__ __forceinline__ void fill(int i, const char* x, int64_t x_stride, const char* dy, int64_t dy_stride, int n) const {
     const uint32_t bar = bars + 8 * i, dst = data + i * slot_bytes;
-    mbar_expect(bar, (uint32_t)(n * row_bytes * (y != nullptr ? 2 : 1)));
+    mbar_expect(bar, (uint32_t)(2 * n * row_bytes));
     copy(dst, x, x_stride, n, bar);
-    if (y != nullptr) copy(dst + kRingRows * row_bytes, y, y_stride, n, bar);
+    copy(dst + dy_at, dy, dy_stride, n, bar);
   }
   __device__ __forceinline__ void copy(uint32_t dst, const char* src, int64_t stride, int n, uint32_t bar) const {
     if (stride == row_bytes) {
@@ -469,7 +472,9 @@ __device__ __forceinline__ uint4 lds_vec(uint32_t p) {
   return v;
 }
 
-template <typename ET, typename WT> __global__ void __launch_bounds__(kMaxThreads) fwd_ring_kernel(FwdArgs a, int slots) {
+// NV vectors a thread, R rows at a time; KEEP: the weights stay in registers.
+template <typename ET, typename WT, int NV, int R, bool KEEP>
+__global__ void __maxnreg__(NV == 2 ? 96 : 128) bwd_ring_kernel(BwdArgs a, int slots) {
   using L = Lanes<16, ET>;
   constexpr int kE = L::kElems;
   using P = Pack<kE>;
@@ -478,123 +483,12 @@ template <typename ET, typename WT> __global__ void __launch_bounds__(kMaxThread
   __shared__ uint64_t bars[kMaxSlots];
   __shared__ float4 red[2][kWarp];
   const int lane = lane_id(), warp = threadIdx.x / kWarp, warps = blockDim.x / kWarp;
-  const int vecs = (int)(a.H / kE);
-  const bool in = (int)threadIdx.x < vecs;
+  const int vecs = (int)(a.H / kE), apart = (int)blockDim.x * 16;
+  bool in[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) in[j] = (int)(threadIdx.x + j * blockDim.x) < vecs;
   const int row_bytes = vecs * 16;
-  const RowRing ring{smem_u32(dyn), smem_u32(bars), slots, kRingRows * row_bytes, row_bytes};
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < slots; ++i) mbar_init(ring.bars + 8 * i);
-    fence_mbarrier_init();
-  }
-  await_previous_kernel();
-  __syncthreads();
-  const int64_t stride = a.x_stride * Elem<ET>::kBytes, step = (int64_t)gridDim.x * kRingRows;
-  const int64_t first = (int64_t)blockIdx.x * kRingRows;
-  auto fill = [&](int i, int64_t row) {
-    if (row < a.rows)
-      ring.fill(i, static_cast<const char*>(a.x) + row * stride, stride, nullptr, 0,
-                a.rows - row < kRingRows ? (int)(a.rows - row) : kRingRows);
-  };
-  if (threadIdx.x == 0)
-    for (int i = 0; i < slots - 1; ++i) fill(i, first + i * step);
-  T w[P::N], b[P::N];
-  load_cols<WT, kE>(in ? a.weight : nullptr, (int64_t)threadIdx.x * kE, 1.0f, w);
-  load_cols<WT, kE>(in ? a.bias : nullptr, (int64_t)threadIdx.x * kE, 0.0f, b);
-  const float inv_h = 1.0f / (float)a.H;
-  auto held = [&](int wp) {
-    const int left = vecs - wp * kWarp;
-    return (float)((left < 0 ? 0 : (left < kWarp ? left : kWarp)) * kE);
-  };
-  const float inv_warp = 1.0f / held(warp);
-  const bool is_peer = lane < warps;
-  const float n_peer = is_peer ? held(lane) : 0.0f, inv_peer = is_peer ? 1.0f / n_peer : 0.0f;
-  int slot = 0, buf = 0;
-  uint32_t parity = 0;
-  bool ok = true;
-  for (int64_t row = first; row < a.rows; row += step) {
-    ok = ok && mbar_wait(ring.bars + 8 * slot, parity);
-    const uint32_t at = ring.data + slot * ring.slot_bytes + threadIdx.x * 16;
-    T v[kRingRows][P::N];
-    float s[kRingRows], dev[kRingRows], mean[kRingRows];
-#pragma unroll
-    for (int r = 0; r < kRingRows; ++r) {
-      const uint4 raw = in && row + r < a.rows ? lds_vec(at + r * row_bytes) : make_uint4(0, 0, 0, 0);
-      T t = P::splat(0.0f);
-#pragma unroll
-      for (int q = 0; q < P::N; ++q) {
-        v[r][q] = P::template get<ET>(raw, q);
-        t = P::add(t, v[r][q]);
-      }
-      s[r] = P::sum(t);
-    }
-    // Mean and squared deviations of the warp's part, then those of the row:
-    // sum (x - mean)^2 = sum over warps of (sum (x - m_w)^2 + n_w (m_w - mean)^2).
-    warp_sum2(s[0], s[1]);
-#pragma unroll
-    for (int r = 0; r < kRingRows; ++r) {
-      const T m = P::splat(s[r] * inv_warp);
-      T t = P::splat(0.0f);
-#pragma unroll
-      for (int q = 0; q < P::N; ++q) {
-        const T c = P::sub(v[r][q], m);
-        t = P::fma(c, c, t);
-      }
-      dev[r] = in ? P::sum(t) : 0.0f;
-    }
-    warp_sum2(dev[0], dev[1]);
-    if (lane == 0) red[buf][warp] = make_float4(s[0], s[1], dev[0], dev[1]);
-    __syncthreads();
-    const float4 p = is_peer ? red[buf][lane] : make_float4(0, 0, 0, 0);
-    buf ^= 1;
-    if (threadIdx.x == 0) {  // everybody has read the slot before this one
-      fence_async_shared();
-      fill(slot == 0 ? slots - 1 : slot - 1, row + (slots - 1) * step);
-    }
-    mean[0] = p.x;
-    mean[1] = p.y;
-    warp_sum2(mean[0], mean[1]);
-#pragma unroll
-    for (int r = 0; r < kRingRows; ++r) {
-      mean[r] = ok ? mean[r] * inv_h : __int_as_float(0x7fffffff);
-      const float off = (r ? p.y : p.x) * inv_peer - mean[r];
-      dev[r] = is_peer ? fmaf(n_peer * off, off, r ? p.w : p.z) : 0.0f;
-    }
-    warp_sum2(dev[0], dev[1]);
-#pragma unroll
-    for (int r = 0; r < kRingRows; ++r) {
-      if (row + r >= a.rows) break;
-      const float rstd = rsqrtf(dev[r] * inv_h + a.eps);
-      if (threadIdx.x == 0) {
-        if (a.mean != nullptr) a.mean[row + r] = mean[r];
-        if (a.rstd != nullptr) a.rstd[row + r] = rstd;
-      }
-      if (!in) continue;
-      const T m2 = P::splat(mean[r]), r2 = P::splat(rstd);
-      float o[kE];
-#pragma unroll
-      for (int q = 0; q < P::N; ++q) P::put(P::fma(P::mul(P::sub(v[r][q], m2), r2), w[q], b[q]), o + 2 * q);
-      st_stream(reinterpret_cast<uint4*>(static_cast<char*>(a.y) + (row + r) * row_bytes) + threadIdx.x, L::pack(o));
-    }
-    if (++slot == slots) {
-      slot = 0;
-      parity ^= 1;
-    }
-  }
-}
-
-template <typename ET, typename WT> __global__ void __launch_bounds__(kMaxThreads) bwd_ring_kernel(BwdArgs a, int slots) {
-  using L = Lanes<16, ET>;
-  constexpr int kE = L::kElems;
-  using P = Pack<kE>;
-  using T = typename P::T;
-  extern __shared__ __align__(128) unsigned char dyn[];
-  __shared__ uint64_t bars[kMaxSlots];
-  __shared__ float4 red[2][kWarp];
-  const int lane = lane_id(), warp = threadIdx.x / kWarp, warps = blockDim.x / kWarp;
-  const int vecs = (int)(a.H / kE);
-  const bool in = (int)threadIdx.x < vecs;
-  const int row_bytes = vecs * 16;
-  const RowRing ring{smem_u32(dyn), smem_u32(bars), slots, 2 * kRingRows * row_bytes, row_bytes};
+  const RowRing ring{smem_u32(dyn), smem_u32(bars), 2 * R * row_bytes, row_bytes, R * row_bytes};
   if (threadIdx.x == 0) {
     for (int i = 0; i < slots; ++i) mbar_init(ring.bars + 8 * i);
     fence_mbarrier_init();
@@ -602,56 +496,75 @@ template <typename ET, typename WT> __global__ void __launch_bounds__(kMaxThread
   await_previous_kernel();
   __syncthreads();
   const int64_t x_stride = a.x_stride * Elem<ET>::kBytes, dy_stride = a.dy_stride * Elem<ET>::kBytes;
-  const int64_t step = (int64_t)gridDim.x * kRingRows, first = (int64_t)blockIdx.x * kRingRows;
+  const int64_t step = (int64_t)gridDim.x * R, first = (int64_t)blockIdx.x * R;
   auto fill = [&](int i, int64_t row) {
     if (row < a.rows)
       ring.fill(i, static_cast<const char*>(a.x) + row * x_stride, x_stride,
                 static_cast<const char*>(a.dy) + row * dy_stride, dy_stride,
-                a.rows - row < kRingRows ? (int)(a.rows - row) : kRingRows);
+                a.rows - row < R ? (int)(a.rows - row) : R);
   };
   if (threadIdx.x == 0)
     for (int i = 0; i < slots - 1; ++i) fill(i, first + i * step);
-  T w[P::N], aw[P::N], ab[P::N];
-  load_cols<WT, kE>(in ? a.weight : nullptr, (int64_t)threadIdx.x * kE, 1.0f, w);
+  auto cols = [&](int j, T (&c)[P::N]) {
+    load_cols<WT, kE>(in[j] ? a.weight : nullptr, (int64_t)(threadIdx.x + j * blockDim.x) * kE, 1.0f, c);
+  };
+  T w[KEEP ? NV : 1][P::N], aw[NV][P::N], ab[NV][P::N];
 #pragma unroll
-  for (int q = 0; q < P::N; ++q) aw[q] = ab[q] = P::splat(0.0f);
+  for (int j = 0; j < NV; ++j) {
+    if (KEEP) cols(j, w[j]);
+#pragma unroll
+    for (int q = 0; q < P::N; ++q) aw[j][q] = ab[j][q] = P::splat(0.0f);
+  }
   const float inv_h = 1.0f / (float)a.H;
   int slot = 0, buf = 0;
   uint32_t parity = 0;
   bool ok = true;
-  for (int64_t row = first; row < a.rows; row += step) {
-    float mean[kRingRows], rstd[kRingRows], s0[kRingRows], s1[kRingRows];
+  char* out = static_cast<char*>(a.dx) + first * row_bytes + threadIdx.x * 16;
+  for (int64_t row = first; row < a.rows; row += step, out += step * row_bytes) {
+    const bool second = R > 1 && row + 1 < a.rows;
+    float s0[R], s1[R], mean[R], rstd[R];
 #pragma unroll
-    for (int r = 0; r < kRingRows; ++r) {
-      const bool there = row + r < a.rows;
-      mean[r] = there ? __ldg(a.mean + row + r) : 0.0f;
-      rstd[r] = there ? __ldg(a.rstd + row + r) : 0.0f;
+    for (int r = 0; r < R; ++r) {
+      mean[r] = r == 0 || second ? __ldg(a.mean + row + r) : 0.0f;
+      rstd[r] = r == 0 || second ? __ldg(a.rstd + row + r) : 0.0f;
     }
     ok = ok && mbar_wait(ring.bars + 8 * slot, parity);
     const uint32_t at = ring.data + slot * ring.slot_bytes + threadIdx.x * 16;
 #pragma unroll
-    for (int r = 0; r < kRingRows; ++r) {
-      const bool there = in && row + r < a.rows;
-      const uint4 x = there ? lds_vec(at + r * row_bytes) : make_uint4(0, 0, 0, 0);
-      const uint4 d = there ? lds_vec(at + (kRingRows + r) * row_bytes) : make_uint4(0, 0, 0, 0);
+    for (int r = 0; r < R; ++r) {
       const T m2 = P::splat(mean[r]), r2 = P::splat(rstd[r]);
       T t0 = P::splat(0.0f), t1 = t0;
 #pragma unroll
-      for (int q = 0; q < P::N; ++q) {
-        const T dy = P::template get<ET>(d, q);
-        const T xhat = P::mul(P::sub(P::template get<ET>(x, q), m2), r2);
-        const T v = P::mul(dy, w[q]);
-        t0 = P::add(t0, v);
-        t1 = P::fma(v, xhat, t1);
-        aw[q] = P::fma(dy, xhat, aw[q]);  // a row past the last has dy = 0
-        ab[q] = P::add(ab[q], dy);
+      for (int j = 0; j < NV; ++j) {
+        const bool there = in[j] && (r == 0 || second);
+        const uint4 x = there ? lds_vec(at + r * row_bytes + j * apart) : make_uint4(0, 0, 0, 0);
+        const uint4 d = there ? lds_vec(at + (R + r) * row_bytes + j * apart) : make_uint4(0, 0, 0, 0);
+        T(&wj)[P::N] = w[KEEP ? j : 0];
+        if (!KEEP) cols(j, wj);
+#pragma unroll
+        for (int q = 0; q < P::N; ++q) {
+          const T dy = P::template get<ET>(d, q);
+          const T xhat = P::mul(P::sub(P::template get<ET>(x, q), m2), r2);
+          const T v = P::mul(dy, wj[q]);
+          t0 = P::add(t0, v);
+          t1 = P::fma(v, xhat, t1);
+          aw[j][q] = P::fma(dy, xhat, aw[j][q]);  // a row past the last has dy = 0
+          ab[j][q] = P::add(ab[j][q], dy);
+        }
       }
       s0[r] = P::sum(t0);
       s1[r] = P::sum(t1);
     }
-    warp_sum2(s0[0], s0[1]);
-    warp_sum2(s1[0], s1[1]);
-    if (lane == 0) red[buf][warp] = make_float4(s0[0], s0[1], s1[0], s1[1]);
+    auto sums = [&] {
+      if constexpr (R == 1) {
+        warp_sum2(s0[0], s1[0]);
+      } else {
+        warp_sum2(s0[0], s0[1]);
+        warp_sum2(s1[0], s1[1]);
+      }
+    };
+    sums();
+    if (lane == 0) red[buf][warp] = make_float4(s0[0], s0[R - 1], s1[0], s1[R - 1]);
     __syncthreads();
     const float4 p = lane < warps ? red[buf][lane] : make_float4(0, 0, 0, 0);
     buf ^= 1;
@@ -659,44 +572,53 @@ template <typename ET, typename WT> __global__ void __launch_bounds__(kMaxThread
       fence_async_shared();
       fill(slot == 0 ? slots - 1 : slot - 1, row + (slots - 1) * step);
     }
+    s0[R - 1] = p.y;
+    s1[R - 1] = p.w;
     s0[0] = p.x;
-    s0[1] = p.y;
     s1[0] = p.z;
-    s1[1] = p.w;
-    warp_sum2(s0[0], s0[1]);
-    warp_sum2(s1[0], s1[1]);
+    sums();
 #pragma unroll
-    for (int r = 0; r < kRingRows; ++r) {
-      if (!in || row + r >= a.rows) break;
-      const uint4 x = lds_vec(at + r * row_bytes), d = lds_vec(at + (kRingRows + r) * row_bytes);
+    for (int r = 0; r < R; ++r) {
+      if (r == 1 && !second) break;
       const T m2 = P::splat(mean[r]), r2 = P::splat(ok ? rstd[r] : __int_as_float(0x7fffffff));
       const T c0 = P::splat(s0[r] * inv_h), c1 = P::splat(-s1[r] * inv_h);
-      float o[kE];
 #pragma unroll
-      for (int q = 0; q < P::N; ++q) {
-        const T xhat = P::mul(P::sub(P::template get<ET>(x, q), m2), r2);
-        const T v = P::mul(P::template get<ET>(d, q), w[q]);
-        P::put(P::mul(P::fma(xhat, c1, P::sub(v, c0)), r2), o + 2 * q);
+      for (int j = 0; j < NV; ++j) {
+        if (!in[j]) break;
+        const uint4 x = lds_vec(at + r * row_bytes + j * apart), d = lds_vec(at + (R + r) * row_bytes + j * apart);
+        T(&wj)[P::N] = w[KEEP ? j : 0];
+        if (!KEEP) cols(j, wj);
+        float o[kE];
+#pragma unroll
+        for (int q = 0; q < P::N; ++q) {
+          const T xhat = P::mul(P::sub(P::template get<ET>(x, q), m2), r2);
+          const T v = P::mul(P::template get<ET>(d, q), wj[q]);
+          P::put(P::mul(P::fma(xhat, c1, P::sub(v, c0)), r2), o + 2 * q);
+        }
+        st_stream(reinterpret_cast<uint4*>(out + r * row_bytes + j * apart), L::pack(o));
       }
-      st_stream(reinterpret_cast<uint4*>(static_cast<char*>(a.dx) + (row + r) * row_bytes) + threadIdx.x, L::pack(o));
     }
     if (++slot == slots) {
       slot = 0;
       parity ^= 1;
     }
   }
-  if (a.partial == nullptr || !in) return;
-  float* pw = a.partial + (int64_t)blockIdx.x * a.H + (int64_t)threadIdx.x * kE;
-  float* pb = pw + (int64_t)gridDim.x * a.H;
+  if (a.partial == nullptr) return;
 #pragma unroll
-  for (int q = 0; q < P::N; ++q) {
-    float v[2];
-    P::put(aw[q], v);
-    if (!ok) v[0] = v[1] = __int_as_float(0x7fffffff);
-    *reinterpret_cast<float2*>(pw + 2 * q) = make_float2(v[0], v[1]);
-    P::put(ab[q], v);
-    if (!ok) v[0] = v[1] = __int_as_float(0x7fffffff);
-    *reinterpret_cast<float2*>(pb + 2 * q) = make_float2(v[0], v[1]);
+  for (int j = 0; j < NV; ++j) {
+    if (!in[j]) break;
+    float* pw = a.partial + (int64_t)blockIdx.x * a.H + (int64_t)(threadIdx.x + j * blockDim.x) * kE;
+    float* pb = pw + (int64_t)gridDim.x * a.H;
+#pragma unroll
+    for (int q = 0; q < P::N; ++q) {
+      float v[2];
+      P::put(aw[j][q], v);
+      if (!ok) v[0] = v[1] = __int_as_float(0x7fffffff);
+      *reinterpret_cast<float2*>(pw + 2 * q) = make_float2(v[0], v[1]);
+      P::put(ab[j][q], v);
+      if (!ok) v[0] = v[1] = __int_as_float(0x7fffffff);
+      *reinterpret_cast<float2*>(pb + 2 * q) = make_float2(v[0], v[1]);
+    }
   }
 }
 
@@ -812,24 +734,24 @@ int64_t bwd_parts(int64_t rows, int64_t H) {
 
 int cta_threads(int64_t vecs, int nv) { return (int)(((vecs + nv - 1) / nv + kWarp - 1) / kWarp * kWarp); }
 
-// Grid, threads and slots of the ring kernels for rows of `vecs` vectors, of
-// which a slot holds `held`; false where fewer than two slots fit.
+// Grid, threads and slots of the ring kernel for rows of `vecs` vectors, nv a
+// thread and r rows at a time; false where they are too short or long for it.
 struct RingShape {
   int threads, grid, slots;
   size_t smem;
 };
-bool ring_shape(int64_t vecs, int64_t rows, int held, int64_t most, RingShape* z) {
-  if (vecs < 128 || vecs > kMaxThreads) return false;
-  z->threads = (int)((vecs + kWarp - 1) / kWarp * kWarp);
-  int per_sm = kMaxThreads / z->threads;  // 64 registers a thread
-  const size_t slot = (size_t)held * vecs * 16;
-  if (per_sm > 4) per_sm = 4;
-  const int64_t n = kRingSm / per_sm / (int64_t)slot;
+bool ring_shape(int64_t vecs, int nv, int r, int registers, int64_t rows, int64_t most, RingShape* z) {
+  z->threads = cta_threads(vecs, nv);
+  if (vecs <= kWarp || z->threads > kRingThreads) return false;
+  int per_sm = 65536 / ((registers + 7) / 8 * 8) / z->threads;
+  if (per_sm > 16) per_sm = 16;
+  if (per_sm < 1) per_sm = 1;
+  const int64_t slot = 2 * r * vecs * 16, n = kRingSm / per_sm / slot;
   z->slots = (int)(n < kMaxSlots ? n : kMaxSlots);
-  z->smem = z->slots * slot;
+  z->smem = (size_t)(z->slots * slot);
   int64_t g = (int64_t)num_sms() * per_sm;
   if (g > most) g = most;
-  const int64_t work = (rows + kRingRows - 1) / kRingRows;
+  const int64_t work = (rows + r - 1) / r;
   z->grid = (int)(work < g ? work : g);
   return z->slots >= 2;
 }
@@ -866,14 +788,6 @@ template <int VB, typename ET, typename WT> int dispatch_fwd(const FwdArgs& a, c
   if (vecs <= 64) return go_fwd<VB, ET, WT, 2, 32, 2>(a, s);
   if (vecs <= 128) return go_fwd<VB, ET, WT, 4, 32, 1>(a, s);
   if constexpr (VB == 16) {
-    static std::atomic<int> granted[64];
-    RingShape z;
-    if (ring_shape(vecs, a.rows, kRingRows, INT32_MAX, &z)) {
-      auto k = fwd_ring_kernel<ET, WT>;
-      if (!allow_smem(k, (int)z.smem, granted)) return MOE_ERR_CUDA;
-      launch(k, z.grid, z.threads, z.smem, s, a, z.slots);
-      return check_launch();
-    }
     if (vecs <= 4 * 256) return go_fwd<VB, ET, WT, 4, 0, 1, 256>(a, s);
     if (vecs <= 4 * kMaxThreads) return go_fwd<VB, ET, WT, 4, 0, 1>(a, s);
   } else {
@@ -897,23 +811,40 @@ int go_bwd(const BwdArgs& a, int* parts, cudaStream_t s) {
   return check_launch();
 }
 
+template <typename ET, typename WT, int NV, int R, bool KEEP> int go_ring(const BwdArgs& a, int* parts, cudaStream_t s) {
+  static std::atomic<int> granted[64], registers{0};
+  RingShape z;
+  auto k = bwd_ring_kernel<ET, WT, NV, R, KEEP>;
+  int regs = registers.load(std::memory_order_relaxed);
+  if (regs == 0) {  // they and shared memory decide how many CTAs an SM holds
+    cudaFuncAttributes f;
+    if (cudaFuncGetAttributes(&f, k) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return MOE_ERR_CUDA;
+    }
+    regs = f.numRegs;
+    registers.store(regs, std::memory_order_relaxed);
+  }
+  if (!ring_shape(a.H / Lanes<16, ET>::kElems, NV, R, regs, a.rows, bwd_parts(a.rows, a.H), &z) ||
+      !allow_smem(k, (int)z.smem, granted))
+    return MOE_ERR_CUDA;
+  *parts = z.grid;
+  launch(k, z.grid, z.threads, z.smem, s, a, z.slots);
+  return check_launch();
+}
+
 template <int VB, typename ET, typename WT> int dispatch_bwd(const BwdArgs& a, int* parts, cudaStream_t s) {
   const int64_t vecs = a.H / Lanes<VB, ET>::kElems;
   if (vecs <= 8) return go_bwd<VB, ET, WT, 1, 8, 2>(a, parts, s);
   if (vecs <= 16) return go_bwd<VB, ET, WT, 1, 16, 2>(a, parts, s);
   if (vecs <= 32) return go_bwd<VB, ET, WT, 1, 32, 2>(a, parts, s);
   if constexpr (VB == 16) {
-    static std::atomic<int> granted[64];
-    RingShape z;
-    if (ring_shape(vecs, a.rows, 2 * kRingRows, bwd_parts(a.rows, a.H), &z)) {
-      auto k = bwd_ring_kernel<ET, WT>;
-      if (!allow_smem(k, (int)z.smem, granted)) return MOE_ERR_CUDA;
-      *parts = z.grid;
-      launch(k, z.grid, z.threads, z.smem, s, a, z.slots);
-      return check_launch();
+    if (vecs <= 2 * kRingThreads) return go_ring<ET, WT, 2, 2, true>(a, parts, s);
+    if constexpr (Elem<ET>::kBytes == 2) {
+      if (vecs <= 4 * kRingThreads) return go_ring<ET, WT, 4, 1, false>(a, parts, s);
+    } else {
+      if (vecs <= 2 * kMaxThreads) return go_bwd<VB, ET, WT, 2, 0, 1>(a, parts, s);
     }
-    if (vecs <= 2 * 512) return go_bwd<VB, ET, WT, 2, 0, 2, 512>(a, parts, s);
-    if (vecs <= 2 * kMaxThreads) return go_bwd<VB, ET, WT, 2, 0, 1>(a, parts, s);
   } else {
     if (vecs <= 4 * kMaxThreads) return go_bwd<VB, ET, WT, 4, 0, 2>(a, parts, s);
     if (vecs <= 8 * kMaxThreads) return go_bwd<VB, ET, WT, 8, 0, 1>(a, parts, s);
