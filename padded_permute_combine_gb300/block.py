@@ -66,6 +66,11 @@ def _workspace(t: torch.Tensor | None, size: int, device) -> torch.Tensor:
     return _need(t, torch.uint8, "workspace", device)
 
 
+def _done(name: str, rc: int) -> None:
+    if rc != _lib.MOE_OK:
+        raise _lib.MoeError(name, rc, _lib.load().moe_error_string(rc).decode())
+
+
 def _status(t: torch.Tensor | None, device) -> int | None:
     return None if t is None else _need(t, torch.int32, "status", device).data_ptr()
 
@@ -109,9 +114,11 @@ def moe_layer(x: torch.Tensor, router: torch.Tensor, w_gate_up: torch.Tensor, w_
     w = _out(w, (T, top_k), torch.float32, "weights", dev)
     out = _out(out, (T, H), x.dtype, "out", dev)
     ws = _workspace(workspace, _lib.load().moe_layer_workspace_size(T, H, F, E, top_k), dev)
-    _lib.call("moe_layer", x.data_ptr(), dt, stride, router.data_ptr(), w_gate_up.data_ptr(), w_down.data_ptr(), T, H, F,
-              E, top_k, _MODES[mode], int(bool(normalize)), te.data_ptr(), w.data_ptr(), out.data_ptr(), ws.data_ptr(),
-              ws.numel(), _status(status, dev), _stream(dev))
+    rc = _lib.load().moe_layer(
+        x.data_ptr(), dt, stride, router.data_ptr(), w_gate_up.data_ptr(), w_down.data_ptr(), T, H, F, E, top_k,
+        _MODES[mode], int(bool(normalize)), te.data_ptr(), w.data_ptr(), out.data_ptr(), ws.data_ptr(),
+        ws.numel(), _status(status, dev), _stream(dev))
+    _done("moe_layer", rc)
     return out, te, w
 
 
@@ -133,9 +140,10 @@ def moe_experts(x: torch.Tensor, top_expert: torch.Tensor, weights: torch.Tensor
     _shape(_need(weights, torch.float32, "weights", dev), (T, K), "weights")
     out = _out(out, (T, H), x.dtype, "out", dev)
     ws = _workspace(workspace, _lib.load().moe_layer_workspace_size(T, H, F, E, K), dev)
-    _lib.call("moe_experts", x.data_ptr(), dt, stride, top_expert.data_ptr(), weights.data_ptr(), w_gate_up.data_ptr(),
-              w_down.data_ptr(), T, H, F, E, K, out.data_ptr(), ws.data_ptr(), ws.numel(), _status(status, dev),
-              _stream(dev))
+    rc = _lib.load().moe_experts(
+        x.data_ptr(), dt, stride, top_expert.data_ptr(), weights.data_ptr(), w_gate_up.data_ptr(), w_down.data_ptr(), T,
+        H, F, E, K, out.data_ptr(), ws.data_ptr(), ws.numel(), _status(status, dev), _stream(dev))
+    _done("moe_experts", rc)
     return out
 
 
@@ -166,8 +174,10 @@ def moe_layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias
     mean, rstd = (None, None) if stats is None else stats
     mean = _out(mean, (M,), torch.float32, "mean", dev)
     rstd = _out(rstd, (M,), torch.float32, "rstd", dev)
-    _lib.call("moe_layer_norm_fwd", x.data_ptr(), dt, stride, _ptr(weight), _ptr(bias), wdt, M, H, eps, out.data_ptr(),
-              mean.data_ptr(), rstd.data_ptr(), _stream(dev))
+    rc = _lib.load().moe_layer_norm_fwd(
+        x.data_ptr(), dt, stride, _ptr(weight), _ptr(bias), wdt, M, H, eps, out.data_ptr(), mean.data_ptr(),
+        rstd.data_ptr(), _stream(dev))
+    _done("moe_layer_norm_fwd", rc)
     return out, mean, rstd
 
 
@@ -194,9 +204,10 @@ def moe_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor |
         dw = torch.empty(H, dtype=wdt, device=dev)
         db = torch.empty(H, dtype=wdt, device=dev)
         ws = _workspace(workspace, _lib.load().moe_layer_norm_bwd_workspace_size(M, H), dev)
-    _lib.call("moe_layer_norm_bwd", dy.data_ptr(), dy_stride, x.data_ptr(), dt, stride, _ptr(weight), code,
-              mean.data_ptr(), rstd.data_ptr(), M, H, out.data_ptr(), _ptr(dw), _ptr(db), _ptr(ws),
-              0 if ws is None else ws.numel(), _stream(dev))
+    rc = _lib.load().moe_layer_norm_bwd(
+        dy.data_ptr(), dy_stride, x.data_ptr(), dt, stride, _ptr(weight), code, mean.data_ptr(), rstd.data_ptr(), M, H,
+        out.data_ptr(), _ptr(dw), _ptr(db), _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev))
+    _done("moe_layer_norm_bwd", rc)
     return out, dw, db
 
 
@@ -205,7 +216,8 @@ class GradSet:
     moe_grad_norm and moe_clip_grads read. Holds references to its tensors;
     they must stay where they are (a gradient that is allocated anew needs a
     new set). ``outs``: where clipping writes; the gradients themselves by
-    default."""
+    default. A set has one workspace: calls with it on several streams that
+    may run at the same time need workspaces of their own."""
 
     def __init__(self, grads: Sequence[torch.Tensor], outs: Sequence[torch.Tensor] | None = None):
         self.grads, self.outs = list(grads), None if outs is None else list(outs)
@@ -228,7 +240,7 @@ class GradSet:
         host = torch.empty(max(1, self.pieces) * size, dtype=torch.uint8)
         _lib.call("moe_grad_table_fill", entries, len(entries), host.data_ptr(), self.pieces)
         self.table = host.to(dev)
-        self.workspace_bytes = lib.moe_grad_norm_workspace_size()
+        self.workspace = torch.empty(lib.moe_grad_norm_workspace_size(), dtype=torch.uint8, device=dev)
 
 
 def moe_grad_set(grads: Sequence[torch.Tensor], outs: Sequence[torch.Tensor] | None = None) -> GradSet:
@@ -242,15 +254,16 @@ def _grad_args(grads, norm, workspace):
         norm = torch.empty((), dtype=torch.float32, device=s.device)
     elif _need(norm, torch.float32, "norm", s.device).numel() != 1:
         raise ValueError("norm must have one element, has %d" % norm.numel())
-    return s, norm, _workspace(workspace, s.workspace_bytes, s.device)
+    return s, norm, s.workspace if workspace is None else _need(workspace, torch.uint8, "workspace", s.device)
 
 
 def moe_grad_norm(grads: GradSet | Sequence[torch.Tensor], norm: torch.Tensor | None = None,
                   workspace: torch.Tensor | None = None) -> torch.Tensor:
     """2-norm over all elements of all gradients, fp32 on the device."""
     s, norm, ws = _grad_args(grads, norm, workspace)
-    _lib.call("moe_grad_norm", s.table.data_ptr(), s.pieces, norm.data_ptr(), ws.data_ptr(), ws.numel(),
-              _stream(s.device))
+    rc = _lib.load().moe_grad_norm(
+        s.table.data_ptr(), s.pieces, norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream(s.device))
+    _done("moe_grad_norm", rc)
     return norm
 
 
@@ -259,6 +272,7 @@ def moe_clip_grads(grads: GradSet | Sequence[torch.Tensor], max_norm: float, nor
     """Scales the gradients by min(1, max_norm / (norm + 1e-6)), into the
     set's outs or in place, and returns their norm before that."""
     s, norm, ws = _grad_args(grads, norm, workspace)
-    _lib.call("moe_clip_grads", s.table.data_ptr(), s.pieces, max_norm, norm.data_ptr(), ws.data_ptr(), ws.numel(),
-              _stream(s.device))
+    rc = _lib.load().moe_clip_grads(
+        s.table.data_ptr(), s.pieces, max_norm, norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream(s.device))
+    _done("moe_clip_grads", rc)
     return norm

@@ -1,7 +1,7 @@
 // Global norm of many gradients, and clipping by it:
 //   norm = sqrt(sum g^2),  out = g * min(1, max_norm / (norm + 1e-6)).
 //
-// The tensors are cut, on the host and once, into pieces of at most 64 KB; a
+// The tensors are cut, on the host and once, into pieces of at most 32 KB; a
 // kernel's CTAs stride over the pieces, so one launch covers any number of
 // tensors of any sizes. Two launches: partial sums of squares, one per CTA,
 // then either the norm (one CTA) or the scaling pass, whose CTAs each add the
@@ -23,10 +23,14 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int64_t kPieceBytes = 65536;
-constexpr int kCtasPerSm = 4;
-constexpr int kMaxCtas = 1024;  // a partial sum each
+// 128 bytes of a piece a thread. 5.6 GB of fp32 clipped in 2.42 ms, 1.6 GB of
+// bf16 summed in 233 us; with 512 threads, 64 KB and 4 CTAs 2.49 ms and 259 us,
+// with 64 KB and 256 threads 2.50 ms and 298 us. More CTAs than fit at once
+// (two or three) even out pieces of different lengths.
+constexpr int kThreads = 256;
+constexpr int64_t kPieceBytes = 32768;
+constexpr int kCtasPerSm = 8;
+constexpr int kMaxCtas = 2048;  // a partial sum each
 
 // Plain (not read-only-path) loads: the scaling pass may write in place.
 __device__ __forceinline__ u32x8 ld_vec(const u32x8* p) {

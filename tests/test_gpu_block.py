@@ -501,7 +501,7 @@ def test_grad_norm_streams_graphs_and_repeats():
     grads = [randn((n,), n, BF) for n in (10, 70001, 3, 999999)]
     outs = [torch.empty_like(g) for g in grads]
     s = p.moe_grad_set(grads, outs)
-    norm, ws = torch.empty(1, device=DEV), torch.empty(s.workspace_bytes, dtype=torch.uint8, device=DEV)
+    norm, ws = torch.empty(1, device=DEV), torch.empty_like(s.workspace)
     want = p.moe_clip_grads(s, 0.5).clone()
     keep = [o.clone() for o in outs]
     side = torch.cuda.Stream()
