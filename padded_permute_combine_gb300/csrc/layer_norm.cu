@@ -167,8 +167,11 @@ template <int LPR> struct Rows {
   }
 };
 
-template <int VB, typename ET, typename WT, int NV, int LPR, int DEPTH, int MAXT>
-__global__ void __launch_bounds__(LPR ? kRowWarps * kWarp : MAXT, LPR ? 3 : 1) fwd_kernel(FwdArgs a) {
+// FULL: every thread of the CTA has all its vectors and needs no masks; three
+// CTAs an SM then, 80 registers a thread (8192 x 7168 bf16: 43 us, with masks 45;
+// at 134 registers and two CTAs 62).
+template <int VB, typename ET, typename WT, int NV, int LPR, int DEPTH, int MAXT, bool FULL>
+__global__ void __launch_bounds__(LPR ? kRowWarps * kWarp : MAXT, LPR || (FULL && MAXT == 256) ? 3 : 1) fwd_kernel(FwdArgs a) {
   using L = Lanes<VB, ET>;
   using V = typename L::V;
   constexpr int kE = L::kElems;
@@ -190,11 +193,12 @@ __global__ void __launch_bounds__(LPR ? kRowWarps * kWarp : MAXT, LPR ? 3 : 1) f
   const float n_warp = (float)(held * kE), inv_warp = held ? 1.0f / n_warp : 0.0f;
   V ahead[DEPTH][NV];
   auto load = [&](V (&v)[NV], int64_t row) {
+    if (FULL && row >= a.rows) row = a.rows - 1;  // read again and left; a branch here keeps the load from running ahead
     const V* p = reinterpret_cast<const V*>(static_cast<const char*>(a.x) + row * a.x_stride * Elem<ET>::kBytes);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = r.tid + j * r.tpr;
-      v[j] = i < vecs && row < a.rows ? ld_stream(p + i) : zero_vec<V>();
+      v[j] = FULL || (i < vecs && row < a.rows) ? ld_stream(p + i) : zero_vec<V>();
     }
   };
 #pragma unroll
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(LPR ? kRowWarps * kWarp : MAXT, LPR ? 3 : 1) f
       t = P::splat(0.0f);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (r.tid + j * r.tpr >= vecs) break;
+        if (!FULL && r.tid + j * r.tpr >= vecs) break;
 #pragma unroll
         for (int q = 0; q < P::N; ++q) {
           const T c = P::sub(v[j][q], part);
@@ -253,7 +257,7 @@ __global__ void __launch_bounds__(LPR ? kRowWarps * kWarp : MAXT, LPR ? 3 : 1) f
         lane_sum<1, kWarp>(dev);
       }
       const float rstd = rsqrtf(dev[0] * inv_h + a.eps);
-      if (row >= a.rows) continue;
+      if (!FULL && row >= a.rows) continue;
       if (r.tid == 0) {
         if (a.mean != nullptr) a.mean[row] = mean;
         if (a.rstd != nullptr) a.rstd[row] = rstd;
@@ -263,7 +267,7 @@ __global__ void __launch_bounds__(LPR ? kRowWarps * kWarp : MAXT, LPR ? 3 : 1) f
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int i = r.tid + j * r.tpr;
-        if (i >= vecs) break;
+        if (!FULL && i >= vecs) break;
         T w[P::N], b[P::N];
         float o[kE];
         load_cols<WT, kE>(a.weight, (int64_t)i * kE, 1.0f, w);
@@ -429,7 +433,7 @@ __global__ void __launch_bounds__(LPR ? kRowWarps * kWarp : MAXT, LPR ? 3 : 1) b
 // us at 8192 x 7168 bf16, 84 with loads into registers). A slot is free again
 // after the next iteration's barrier. Waits are bounded; after one gives up
 // the CTA writes NaN instead of waiting again. (The forward pass gains nothing
-// this way: 47 us instead of 45.)
+// this way: 47 us instead of 43.)
 
 constexpr int kRingThreads = 512;
 constexpr int kMaxSlots = 16;
@@ -472,8 +476,9 @@ __device__ __forceinline__ uint4 lds_vec(uint32_t p) {
   return v;
 }
 
-// NV vectors a thread, R rows at a time; KEEP: the weights stay in registers.
-template <typename ET, typename WT, int NV, int R, bool KEEP>
+// NV vectors a thread, R rows at a time; KEEP: the weights stay in registers;
+// FULL: every thread has all its vectors.
+template <typename ET, typename WT, int NV, int R, bool KEEP, bool FULL>
 __global__ void __maxnreg__(NV == 2 ? 96 : 128) bwd_ring_kernel(BwdArgs a, int slots) {
   using L = Lanes<16, ET>;
   constexpr int kE = L::kElems;
@@ -486,7 +491,7 @@ __global__ void __maxnreg__(NV == 2 ? 96 : 128) bwd_ring_kernel(BwdArgs a, int s
   const int vecs = (int)(a.H / kE), apart = (int)blockDim.x * 16;
   bool in[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) in[j] = (int)(threadIdx.x + j * blockDim.x) < vecs;
+  for (int j = 0; j < NV; ++j) in[j] = FULL || (int)(threadIdx.x + j * blockDim.x) < vecs;
   const int row_bytes = vecs * 16;
   const RowRing ring{smem_u32(dyn), smem_u32(bars), 2 * R * row_bytes, row_bytes, R * row_bytes};
   if (threadIdx.x == 0) {
@@ -774,9 +779,14 @@ template <int VB, typename ET, typename WT, int NV, int LPR, int DEPTH, int MAXT
 int go_fwd(const FwdArgs& a, cudaStream_t s) {
   const int threads = LPR ? kRowWarps * kWarp : cta_threads(a.H / Lanes<VB, ET>::kElems, NV);
   constexpr int kRows = LPR ? kRowWarps * (kWarp / (LPR ? LPR : 1)) : 1;
-  auto k = fwd_kernel<VB, ET, WT, NV, LPR, DEPTH, MAXT>;
-  launch(k, persistent_grid(k, threads, 0, (a.rows + kRows - 1) / kRows), threads, 0, s, a);
-  return check_launch();
+  auto go = [&](auto k) {
+    launch(k, persistent_grid(k, threads, 0, (a.rows + kRows - 1) / kRows), threads, 0, s, a);
+    return check_launch();
+  };
+  if constexpr (LPR == 0 && VB == 16 && MAXT == 256) {
+    if (a.H / Lanes<VB, ET>::kElems == (int64_t)threads * NV) return go(fwd_kernel<VB, ET, WT, NV, LPR, DEPTH, MAXT, true>);
+  }
+  return go(fwd_kernel<VB, ET, WT, NV, LPR, DEPTH, MAXT, false>);
 }
 
 // Vectors of a row decide: lanes of a warp up to 128 of them, a CTA beyond.
@@ -811,10 +821,15 @@ int go_bwd(const BwdArgs& a, int* parts, cudaStream_t s) {
   return check_launch();
 }
 
-template <typename ET, typename WT, int NV, int R, bool KEEP> int go_ring(const BwdArgs& a, int* parts, cudaStream_t s) {
+template <typename ET, typename WT, int NV, int R, bool KEEP, bool FULL = false>
+int go_ring(const BwdArgs& a, int* parts, cudaStream_t s) {
   static std::atomic<int> granted[64], registers{0};
   RingShape z;
-  auto k = bwd_ring_kernel<ET, WT, NV, R, KEEP>;
+  const int64_t vecs = a.H / Lanes<16, ET>::kElems;
+  if constexpr (!FULL) {
+    if (vecs == (int64_t)cta_threads(vecs, NV) * NV) return go_ring<ET, WT, NV, R, KEEP, true>(a, parts, s);
+  }
+  auto k = bwd_ring_kernel<ET, WT, NV, R, KEEP, FULL>;
   int regs = registers.load(std::memory_order_relaxed);
   if (regs == 0) {  // they and shared memory decide how many CTAs an SM holds
     cudaFuncAttributes f;
@@ -825,7 +840,7 @@ template <typename ET, typename WT, int NV, int R, bool KEEP> int go_ring(const 
     regs = f.numRegs;
     registers.store(regs, std::memory_order_relaxed);
   }
-  if (!ring_shape(a.H / Lanes<16, ET>::kElems, NV, R, regs, a.rows, bwd_parts(a.rows, a.H), &z) ||
+  if (!ring_shape(vecs, NV, R, regs, a.rows, bwd_parts(a.rows, a.H), &z) ||
       !allow_smem(k, (int)z.smem, granted))
     return MOE_ERR_CUDA;
   *parts = z.grid;
