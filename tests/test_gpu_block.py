@@ -351,6 +351,35 @@ def test_layer_norm_strides_and_alignment(H, dtype):
     check(p.moe_layer_norm_fwd(misaligned_like(x), misaligned_like(w), b)[0], ref, tol, "misaligned")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H", [123, 125, 129, 247, 249, 250, 255, 257, 495, 497, 505, 993, 1985, 2047, 3969, 7935, 7937, 9001])
+def test_layer_norm_unaligned_rows(H, dtype):
+    """Rows off 16 bytes, with ends at and around a warp's 31 vectors; neighbours of every output stay untouched."""
+    M = 5
+    wide = randn((M, H + 3), H, dtype)
+    x, dy = wide[:, 1:H + 1], randn((M, H + 1), H + 1, dtype)[:, 1:]
+    w, b = 1 + randn((H + 1,), 3, scale=0.1)[1:], randn((H,), 4)
+    guard = torch.full((2, M * H + 16), 7.0, dtype=dtype, device=DEV)
+    y, dx = guard[0, 3:3 + M * H].view(M, H), guard[1, 5:5 + M * H].view(M, H)
+    _, mean, rstd = p.moe_layer_norm_fwd(x, w, b, out=y)
+    _, dw, db = p.moe_layer_norm_bwd(dy, x, w, mean, rstd, out=dx)
+    assert bool((guard[0, :3] == 7).all()) and bool((guard[0, 3 + M * H:] == 7).all())
+    assert bool((guard[1, :5] == 7).all()) and bool((guard[1, 5 + M * H:] == 7).all())
+    ref, rmean, rrstd, xhat = norm_ref(x, w, b, 1e-5)
+    mag = x.double().abs().mean(1)[:, None]
+    check(mean, rmean, ROW * mag[:, 0], "mean")
+    check(y, ref, 3 * ROW * (mag * rrstd[:, None] + xhat.abs() + 1) * w.double().abs() + 4 * U * (ref.abs() + b.double().abs())
+          + type_round(ref, dtype), "y")
+    xh = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    v = dy.double() * w.double()
+    c0, c1 = v.mean(1, keepdim=True), (v * xh).mean(1, keepdim=True)
+    ref = rstd.double()[:, None] * (v - c0 - xh * c1)
+    size = rstd.double()[:, None] * (v.abs() + v.abs().mean(1, keepdim=True) + xh.abs() * (v * xh).abs().mean(1, keepdim=True))
+    check(dx, ref, 3 * ROW * size + type_round(ref, dtype), "dx")
+    check(dw, (dy.double() * xh).sum(0), 64 * U * (dy.double() * xh).abs().sum(0) + 16 * U * dy.double().abs().sum(0), "dw")
+    check(db, dy.double().sum(0), 64 * U * dy.double().abs().sum(0), "db")
+
+
 def test_layer_norm_special_rows():
     x = randn((6, 512), 1)
     clean = p.moe_layer_norm_fwd(x)[0]
