@@ -441,8 +441,8 @@ __global__ void __launch_bounds__(kThreads, 2) down_rows_kernel(LayerArgs a, int
 // time is that of the weight bytes, so what matters is that copies are always
 // in flight: the copying warps run ahead across tiles, rows and experts, and
 // the work is cut so that each of the SMs streams the same number of bytes (an
-// equal share of the active experts' F gate/up row pairs; an equal share of
-// y's H columns for all experts), whatever the sizes.
+// equal share of the active experts' F gate/up row pairs; about 128 of y's H
+// columns for an equal share of the active experts' F), whatever the sizes.
 //
 // The weights come by tensor copies (TMA) of 4 KB and more, one thread's work.
 // The same ring filled with bulk copies of 1 KB pieces of rows reached 4.5
@@ -572,13 +572,14 @@ struct StreamArgs {
   LayerArgs a;
   __nv_bfloat16* h_hi;  // [n, F] in sorted order: h = h_hi + h_lo
   __nv_bfloat16* h_lo;
+  float* parts;  // [slices, T, H]: the slices' sums, where there are more than two
 };
 // A kernel's cut of its work and of its shared memory.
 struct StreamShape {
   int stages, stage_bytes, blocks;  // blocks of 64 elements in a stage
   int tokens;                       // of an expert at a time (a multiple of 16, the products' columns; 8 in the second kernel)
   int rows;                         // weight rows of a tile (first kernel: two for each gate/up pair)
-  int slices;                       // second kernel: CTAs of a cluster, which share a tile's elements
+  int slices;                       // second kernel: CTAs that share a tile's experts and elements
   uint32_t cols;                    // tensor memory columns
 };
 
@@ -819,28 +820,32 @@ __global__ void __launch_bounds__(kStreamThreads)
 }
 
 // y's columns [r0, r0 + nr) for one expert's tokens after another, over this
-// slice of F (all of it without a cluster).
+// slice's range of all experts' blocks (all of them without slices).
 struct DownWalk {
   const Segments& s;
   int64_t r0, end;
-  int nr, q, i0, ntok, K0, K, k0, per_stage, per_pass, rows;
+  int nr, q, i0, ntok, K0, K, k0, per_stage, per_pass, rows, F, blocks, first, last;
   __device__ DownWalk(const Segments& s_, const LayerArgs& a, const StreamShape& z)
-      : s(s_), per_stage(z.blocks * kBlock), per_pass(z.tokens), rows(z.rows) {
+      : s(s_), per_stage(z.blocks * kBlock), per_pass(z.tokens), rows(z.rows), F((int)a.F), blocks((F + kBlock - 1) / kBlock) {
     const int64_t tiles = gridDim.x / z.slices, tile_id = blockIdx.x / z.slices, slice = blockIdx.x % z.slices;
     r0 = a.H * tile_id / tiles;
     end = a.H * (tile_id + 1) / tiles;
-    const int64_t blocks = (a.F + kBlock - 1) / kBlock;
-    K0 = (int)(blocks * slice / z.slices * kBlock);
-    const int64_t k_end = blocks * (slice + 1) / z.slices * kBlock;
-    K = (int)(k_end < a.F ? k_end : a.F);
-    if (s.active == 0 || K0 >= K) r0 = end;
+    first = (int)((int64_t)s.active * blocks * slice / z.slices);
+    last = (int)((int64_t)s.active * blocks * (slice + 1) / z.slices);
+    if (first >= last) r0 = end;
     if (more()) tile();
   }
   __device__ __forceinline__ bool more() const { return r0 < end; }
   __device__ __forceinline__ void tile() {
     nr = end - r0 < rows ? (int)(end - r0) : rows;
-    q = 0;
-    i0 = 0;
+    q = first / blocks;
+    expert();
+  }
+  __device__ __forceinline__ void expert() {
+    const int from = q * blocks;
+    K0 = (first > from ? first - from : 0) * kBlock;
+    K = last - from < blocks ? (last - from) * kBlock : F;
+    i0 = s.begin[q];
     pass();
   }
   __device__ __forceinline__ void pass() {
@@ -855,7 +860,7 @@ struct DownWalk {
     if (k0 < K) return;
     i0 += ntok;
     if (i0 < s.begin[q + 1]) return pass();
-    if (++q < s.active) return pass();
+    if (++q * blocks < last) return expert();
     r0 += nr;
     if (r0 < end) tile();
   }
@@ -897,6 +902,7 @@ __global__ void __launch_bounds__(kStreamThreads)
   tmem_fence_before();
   const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, nullptr, seg);
   tmem_fence_after();
+  allow_next_kernel();
   float* ysum = reinterpret_cast<float*>(seg + segments_bytes(a.n, a.E) / sizeof(int32_t));  // [T, nr]
   DownWalk w(s, a, z);
   const int block = round_to(z.rows, 8) * kRowBytes;
@@ -967,9 +973,12 @@ __global__ void __launch_bounds__(kStreamThreads)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.sums_empty[d.i]));
       }
-      if (z.slices == 1 && row < nr) {
+      if (row < nr && z.slices == 1) {
         __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + r0 + row;
         for (int t = 0; t < a.T; ++t) y[t * a.H] = __float2bfloat16_rn(ysum[t * nr + row]);
+      } else if (row < nr && z.slices > 2) {
+        float* part = p.parts + blockIdx.x % z.slices * a.T * a.H + r0 + row;
+        for (int t = 0; t < a.T; ++t) part[t * a.H] = ysum[t * nr + row];
       }
     }
   }
@@ -977,9 +986,9 @@ __global__ void __launch_bounds__(kStreamThreads)
   __syncthreads();
   tmem_fence_after();
   if (warp == kMulWarp) tmem_free(sh.tmem, z.cols);
-  if (z.slices > 1) {
-    // The cluster's CTAs hold sums over their slices of F for the same columns
-    // of y (one tile: the host cuts no more): each adds a share of them.
+  if (z.slices == 2) {
+    // The cluster's CTAs hold sums over their slices for the same columns of y
+    // (one tile: the host cuts no more): each adds a share of them.
     __syncwarp();
     cluster_sync();
     const int64_t tiles = gridDim.x / z.slices, tile_id = blockIdx.x / z.slices;
@@ -994,6 +1003,27 @@ __global__ void __launch_bounds__(kStreamThreads)
     __syncwarp();
     cluster_sync();  // nobody leaves while its sums are read
   }
+}
+
+// y = the sum of the slices' parts, in their order; four columns a thread.
+__global__ void __launch_bounds__(kThreads)
+    sum_parts_kernel(const float* __restrict__ parts, int slices, int64_t n, __nv_bfloat16* __restrict__ y) {
+  await_previous_kernel();
+  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+  if (i >= n) return;
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+  for (int k = 0; k < slices; ++k) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(parts + k * n + i));
+    sum.x += v.x;
+    sum.y += v.y;
+    sum.z += v.z;
+    sum.w += v.w;
+  }
+  y[i] = __float2bfloat16_rn(sum.x);
+  y[i + 1] = __float2bfloat16_rn(sum.y);
+  y[i + 2] = __float2bfloat16_rn(sum.z);
+  y[i + 3] = __float2bfloat16_rn(sum.w);
 }
 
 // ------------------------------------------------------------------ host
@@ -1070,6 +1100,7 @@ bool tensor_map(CUtensorMap* map, const void* base, int64_t nx, int64_t ny, int6
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr int kMaxSms = 192;             // that the layer uses: bounds the workspace
 constexpr int kSmBytes = 226 * 1024;  // dynamic shared memory of a CTA at most, beside its static part
 
 // Stages of stage_bytes that fit beside `rest` bytes; false for fewer than two.
@@ -1093,11 +1124,11 @@ bool cut_stages(StreamShape* z, int block_bytes, int most, size_t rest) {
   return false;
 }
 
-int run_stream(const LayerArgs& a, cudaStream_t s) {
+int run_stream(const LayerArgs& a, float* parts, cudaStream_t s) {
   static std::atomic<int> granted_g[64], granted_d[64];
   __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(a.h);
-  const StreamArgs p{a, h, h + (int64_t)a.n * a.F};
-  const int64_t sms = num_sms();
+  const StreamArgs p{a, h, h + (int64_t)a.n * a.F, parts};
+  const int64_t sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
   const size_t seg = segments_bytes(a.n, a.E);
   // Tokens of an expert at a time: twice the mean and 16, so that few experts
   // take a second pass over their weights and stages hold weights in the main.
@@ -1115,36 +1146,33 @@ int run_stream(const LayerArgs& a, cudaStream_t s) {
   if (!cut_stages(&g, (g.rows + g.tokens) * kRowBytes, 3, seg)) return MOE_ERR_UNSUPPORTED;
   const size_t g_smem = seg + (size_t)g.stages * g.stage_bytes + 1024;
 
-  // Pairs of SMs share a tile's F between them where the tile then has at most
-  // 128 rows: every tile reads all of h, and a tile of few rows copies little
-  // per instruction. (Four SMs a tile leave some of them idle, since their
-  // clusters do not fill the chip: 84 instead of 46 us for one token's second
-  // kernel at the Mixtral-8x7B shape.) Stages of up to 64 KB, for the reason
-  // above: 48 tokens of the Mixtral-8x22B shape 3.9 TB/s at 32 KB, 6.2 at 64.
+  // A product costs the same whatever rows of its 128 the tile holds (27 rows,
+  // H 2048 over pairs of SMs: 2.3 TB/s), and every tile reads all of h. So
+  // tiles have close to 128 rows, and as many SMs share one as there are for
+  // it: each takes an equal share of the active experts' blocks, and the sums
+  // meet in the pair's shared memory or, for more than two, in the workspace
+  // and a kernel that adds them (16 tokens, 2048 x 768, 64 experts, 8 each:
+  // 43 us and 3 instead of 78; 64 tokens, 1024 x 1024, 256 experts: 102 and 3
+  // instead of 364). Stages of up to 64 KB, for the reason above: 48 tokens of
+  // the Mixtral-8x22B shape 3.9 TB/s at 32 KB, 6.2 at 64.
   StreamShape d{};
   d.tokens = round_to(a.T, 8) < cap ? round_to(a.T, 8) : cap;
   d.cols = tmem_cols(4 * d.tokens);
   int64_t grid = 0;
   size_t d_smem = 0;
   bool fits = false;
-  for (int slices = 2, most = kTileRows; !fits && most >= 64;) {
-    const int64_t tiles = sms / slices < a.H ? sms / slices : a.H;
-    const int64_t share = (a.H + tiles - 1) / tiles;
-    if (tiles >= 1 && (share <= most || slices == 1)) {
-      d.slices = slices;
-      d.rows = (int)(share < most ? share : most);
-      grid = tiles * slices;
-      const int block = (round_to(d.rows, 8) + 2 * d.tokens) * kRowBytes;
-      // A product reads 128 rows from a block's start whatever the tile holds:
-      // behind the ring lie at least as many bytes of the CTA's memory.
-      d_smem = seg + sizeof(float) * a.T * d.rows;
-      if (d_smem < kTileRows * kRowBytes) d_smem = kTileRows * kRowBytes;
-      fits = cut_stages(&d, block, block < 65536 ? 65536 / block : 1, d_smem);
-    }
-    if (slices > 1)
-      slices /= 2;
-    else
-      most /= 2;  // sums of 256 tokens by 128 rows and the ring: too much for an SM
+  for (int most = kTileRows; !fits && most >= 16; most /= 2) {  // sums of 256 tokens by 128 rows and the ring: too much for an SM
+    const int64_t need = (a.H + most - 1) / most;
+    d.slices = need < sms ? (int)(sms / need) : 1;
+    const int64_t tiles = sms / d.slices < a.H ? sms / d.slices : a.H, share = (a.H + tiles - 1) / tiles;
+    d.rows = (int)(share < most ? share : most);
+    grid = tiles * d.slices;
+    const int block = (round_to(d.rows, 8) + 2 * d.tokens) * kRowBytes;
+    // A product reads 128 rows from a block's start whatever the tile holds:
+    // behind the ring lie at least as many bytes of the CTA's memory.
+    d_smem = seg + sizeof(float) * a.T * d.rows;
+    if (d_smem < kTileRows * kRowBytes) d_smem = kTileRows * kRowBytes;
+    fits = cut_stages(&d, block, block < 65536 ? 65536 / block : 1, d_smem);
   }
   if (!fits) return MOE_ERR_UNSUPPORTED;
   d_smem += (size_t)d.stages * d.stage_bytes + 1024;
@@ -1168,13 +1196,18 @@ int run_stream(const LayerArgs& a, cudaStream_t s) {
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim = {(unsigned)d.slices, 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = d.slices > 1 ? 2 : 1;
+  cfg.numAttrs = d.slices == 2 ? 2 : 1;
   (void)cudaLaunchKernelEx(&cfg, down_stream_kernel, p, d, d_map);
+  if (d.slices > 2) {
+    const int64_t y_n = a.T * a.H;
+    launch(sum_parts_kernel, (unsigned)((y_n / 4 + kThreads - 1) / kThreads), kThreads, 0, s, p.parts, d.slices, y_n,
+           static_cast<__nv_bfloat16*>(a.y));
+  }
   return check_launch();
 }
 
 template <typename ET>
-int dispatch(const LayerArgs& a, const void* router, float* logits, ET* x_copy, int32_t mode, int32_t normalize,
+int dispatch(const LayerArgs& a, const void* router, float* logits, float* parts, ET* x_copy, int32_t mode, int32_t normalize,
              int32_t* top_expert, float* weights, cudaStream_t s) {
   constexpr int kE = 16 / Elem<ET>::kBytes;
   const ET* x = static_cast<const ET*>(a.x);
@@ -1199,15 +1232,18 @@ int dispatch(const LayerArgs& a, const void* router, float* logits, ET* x_copy, 
       LayerArgs b = a;
       b.x = x;
       b.x_stride = x_ld;
-      return run_stream(b, s);
+      return run_stream(b, parts, s);
     }
   }
   return run_rows<ET, false>(a, x, x_ld, s);
 }
 
-// Bytes of the workspace's parts: the logits, h, and x where its rows are not aligned.
+// Bytes of the workspace's parts: the logits, h, the slices' sums of y, and x where its rows are not aligned.
 size_t logits_bytes(int64_t T, int32_t E) { return ((size_t)T * E * sizeof(float) + 255) / 256 * 256; }
 size_t h_bytes(int64_t n, int64_t F) { return ((size_t)n * (size_t)padded_row(F) * sizeof(float) + 255) / 256 * 256; }
+
+// slices * H <= SMs * the rows of a tile, and a tile has no more rows than y columns.
+size_t parts_bytes(int64_t T, int64_t H) { return (size_t)T * kMaxSms * (H < kTileRows ? H : kTileRows) * sizeof(float); }
 
 bool sizes_ok(int64_t T, int64_t H, int64_t F, int32_t E, int32_t K) {
   return T >= 0 && H >= 1 && F >= 1 && E >= 1 && K >= 1 && K <= E && K <= MOE_MAX_TOP_K &&
@@ -1238,11 +1274,12 @@ int run_layer(const void* x, int32_t dtype, int64_t x_stride, const void* router
   float* h = reinterpret_cast<float*>(base + logits_bytes(T, E));
   const LayerArgs a{x, w_gate_up, w_down, top_expert, weights, h, y, T > 1 ? x_stride : H, H, F,
                     (int32_t)T, E, K, (int32_t)(T * K), d_status};
-  void* x_copy = reinterpret_cast<char*>(h) + h_bytes(T * K, F);
+  float* parts = reinterpret_cast<float*>(reinterpret_cast<char*>(h) + h_bytes(T * K, F));
+  void* x_copy = reinterpret_cast<char*>(parts) + parts_bytes(T, H);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == MOE_F32)
-    return dispatch<float>(a, router, logits, static_cast<float*>(x_copy), mode, normalize, top_out, weights_out, s);
-  return dispatch<__nv_bfloat16>(a, router, logits, static_cast<__nv_bfloat16*>(x_copy), mode, normalize, top_out,
+    return dispatch<float>(a, router, logits, parts, static_cast<float*>(x_copy), mode, normalize, top_out, weights_out, s);
+  return dispatch<__nv_bfloat16>(a, router, logits, parts, static_cast<__nv_bfloat16*>(x_copy), mode, normalize, top_out,
                                  weights_out, s);
 }
 
@@ -1253,7 +1290,7 @@ using namespace moe;
 
 extern "C" size_t moe_layer_workspace_size(int64_t T, int64_t H, int64_t F, int32_t E, int32_t K) {
   if (!sizes_ok(T, H, F, E, K) || !few(T, E, K)) return 0;
-  return logits_bytes(T, E) + h_bytes(T * K, F) + (size_t)T * (size_t)padded_row(H) * sizeof(float) + 256;
+  return logits_bytes(T, E) + h_bytes(T * K, F) + parts_bytes(T, H) + (size_t)T * (size_t)padded_row(H) * sizeof(float) + 256;
 }
 
 extern "C" int moe_layer(const void* x, int32_t dtype, int64_t x_stride, const void* router, const void* w_gate_up,
