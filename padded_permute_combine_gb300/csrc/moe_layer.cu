@@ -44,6 +44,9 @@ __device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontr
 
 // ------------------------------------------------------- choices by expert
 
+constexpr int kExpertBits = 16;
+static_assert(MOE_GATING_MAX_EXPERTS < 1 << kExpertBits && MOE_LAYER_MAX_CHOICES < 1 << (31 - kExpertBits), "expert and rank in one word");
+
 // The choices sorted by expert (stable), in dynamic shared memory:
 // order[i] and token[i]: assignment at sorted place i and its token; the
 // active experts, and where each begins in order.
@@ -60,31 +63,35 @@ __host__ __device__ inline size_t segments_bytes(int32_t n, int32_t E) {
   return sizeof(int32_t) * ((size_t)3 * n + E + 2 * m + 2);
 }
 
-// Called by the whole CTA; warp 0 does the work.
+// Called by the whole CTA: all load the choices and place them, warp 0 ranks them.
 __device__ __forceinline__ Segments sort_choices(const int32_t* __restrict__ top_expert, int32_t n, int32_t E, int32_t K,
                                                  int32_t* status, int32_t* smem) {
   const int m = n < E ? n : E;
   Segments s;
   s.order = smem;
   s.token = smem + n;
-  int32_t* local = s.token + n;  // rank of an assignment within its expert
+  int32_t* local = s.token + n;  // a choice's expert, then its rank there above it
   int32_t* count = local + n;  // [E]: choices of the expert, then where they begin
   s.expert = count + E;
   s.begin = s.expert + m;
   int32_t* active = s.begin + m + 1;
   const int lane = lane_id();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    int e = __ldcg(top_expert + i);
+    if (e < -1 || e >= E) {
+      if (blockIdx.x == 0) flag_status(status, MOE_STATUS_BAD_EXPERT);
+      e = -1;
+    }
+    local[i] = e;
+  }
+  for (int e = threadIdx.x; e < E; e += blockDim.x) count[e] = 0;
+  __syncthreads();
   if (threadIdx.x < kWarp) {
-    for (int e = lane; e < E; e += kWarp) count[e] = 0;
-    __syncwarp();
     for (int i0 = 0; i0 < n; i0 += kWarp) {
       const int i = i0 + lane;
-      int e = i < n ? __ldcg(top_expert + i) : -1;
-      if (e < -1 || e >= E) {
-        if (blockIdx.x == 0) flag_status(status, MOE_STATUS_BAD_EXPERT);
-        e = -1;
-      }
+      const int e = i < n ? local[i] : -1;
       const unsigned peers = __match_any_sync(0xffffffffu, e);
-      if (e >= 0) local[i] = count[e] + __popc(peers & lanemask_lt());
+      if (e >= 0) local[i] = e | (count[e] + __popc(peers & lanemask_lt())) << kExpertBits;
       __syncwarp();
       if (e >= 0 && (peers & lanemask_lt()) == 0) count[e] += __popc(peers);
       __syncwarp();
@@ -113,14 +120,14 @@ __device__ __forceinline__ Segments sort_choices(const int32_t* __restrict__ top
       s.begin[found] = place;
       *active = found;
     }
-    __syncwarp();
-    for (int i = lane; i < n; i += kWarp) {
-      const int e = __ldcg(top_expert + i);
-      if (e < 0 || e >= E) continue;
-      const int at = count[e] + local[i];
-      s.order[at] = i;
-      s.token[at] = i / K;
-    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int v = local[i];
+    if (v < 0) continue;
+    const int at = count[v & ((1 << kExpertBits) - 1)] + (v >> kExpertBits);
+    s.order[at] = i;
+    s.token[at] = i / K;
   }
   __syncthreads();
   s.active = *active;
@@ -1206,6 +1213,8 @@ int run_stream(const LayerArgs& a, float* parts, cudaStream_t s) {
   return check_launch();
 }
 
+constexpr int64_t kSmallLayer = 1 << 24;
+
 template <typename ET>
 int dispatch(const LayerArgs& a, const void* router, float* logits, float* parts, ET* x_copy, int32_t mode, int32_t normalize,
              int32_t* top_expert, float* weights, cudaStream_t s) {
@@ -1228,7 +1237,14 @@ int dispatch(const LayerArgs& a, const void* router, float* logits, float* parts
   const bool by16 = a.H % kE == 0 && a.F % kE == 0 && aligned(a.w_gate_up, 16) && aligned(a.w_down, 16);
   if (!by16) return run_rows<ET, true>(a, x, x_ld, s);
   if constexpr (Elem<ET>::kBytes == 2) {
-    if (a.H >= kBlock && a.F >= kBlock) {  // at least one box each way
+    // The tensor path costs some 8 us more to start: below 100 MB of weights
+    // (every choice's own) the ordinary cores are ahead. One token, 512 x 512,
+    // 2 of 8 experts: 10.8 us on these, 22.2 on tensor cores; 1024 x 2048:
+    // 15.9 and 24.2; 4 tokens of it (100 MB): 31.3 and 31.5; 8: 39.1 and 35.3.
+    // Many tokens to an expert are slow on them: 16 tokens, 512 x 512: 21 and
+    // 24.6 us; 32 (8 an expert): 26.9 and 25.8.
+    const bool small = a.n * a.H * a.F <= kSmallLayer && a.n <= 4 * a.E;
+    if (a.H >= kBlock && a.F >= kBlock && !small) {  // at least one box each way
       LayerArgs b = a;
       b.x = x;
       b.x_stride = x_ld;

@@ -107,6 +107,106 @@ def test_layer(T, H, F, E, K, dtype):
         check(y, ref, tol, "y %s" % mode)
 
 
+# Beyond 2^24 elements of the choices' matrices, where bf16 layers run on the tensor cores; H and F of every remainder
+# by the blocks of 64, one, two and more SMs to a tile of y's columns, two tiles an SM, several passes over an expert.
+LARGE = [(16, 1024, 1040, 8, 2), (1, 4096, 4104, 4, 1), (5, 1096, 1048, 16, 3), (70, 512, 264, 8, 2), (256, 136, 72, 8, 8),
+         (256, 64, 136, 8, 8), (64, 264, 1000, 300, 4), (130, 2048, 72, 2, 1), (3, 12288, 520, 6, 1), (2, 20480, 1024, 4, 2),
+         (40, 6144, 136, 5, 2), (256, 1024, 80, 8, 8), (23, 1400, 904, 12, 5), (8, 7168, 512, 32, 8)]
+
+
+@pytest.mark.parametrize("T,H,F,E,K", LARGE)
+def test_large_layer(T, H, F, E, K):
+    x, router, wgu, wd = layer_inputs(T, H, F, E, BF, T + H + F)
+    y, te, w = p.moe_layer(x, router, wgu, wd, K)
+    top, wref = route_ref(x, router, K, "softmax", True)
+    assert torch.equal(te.long(), top)
+    check(w, wref, 1e-5 * (1 + wref.abs()), "weights")
+    ref, tol = experts_ref(x, top, w.double(), wgu, wd)
+    check(y, ref, tol, "y")
+    out, ws = torch.empty_like(y), p.block.layer_workspace(T, H, F, E, K, DEV).fill_(0xff)
+    assert torch.equal(p.moe_experts(x, te, w, wgu, wd, out=out, workspace=ws), y)
+    wide = torch.full((T, H + 8), float("nan"), dtype=BF, device=DEV)
+    wide[:, :H] = x
+    assert torch.equal(p.moe_experts(wide[:, :H], te, w, wgu, wd), y)
+
+
+@pytest.mark.parametrize("T,H,F,K", [(40, 1032, 520, 3), (256, 264, 88, 8), (9, 5120, 1024, 2)])
+def test_large_experts_one_expert_takes_all_and_empty_slots(T, H, F, K):
+    E = 8
+    x, _, wgu, wd = layer_inputs(T, H, F, E, BF, 5)
+    w = randn((T, K), 6).abs()
+    top = torch.full((T, K), 3, dtype=torch.int32, device=DEV)
+    ref, tol = experts_ref(x, top, w.double(), wgu, wd)
+    check(p.moe_experts(x, top, w, wgu, wd), ref, tol, "one expert")
+    top = torch.randint(-1, E, (T, K), generator=torch.Generator().manual_seed(T), dtype=torch.int32).to(DEV)
+    top[T // 2] = -1
+    top[0, 0] = E + 7
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = p.moe_experts(x, top, w, wgu, wd, status=status)
+    ref, tol = experts_ref(x, top, w.double(), wgu, wd)
+    check(y, ref, tol, "empty slots")
+    assert bool((y[T // 2] == 0).all()) and not bool(torch.signbit(y[T // 2].float()).any())
+    assert int(status) == _lib.MOE_STATUS_BAD_EXPERT
+    status.zero_()
+    assert bool((p.moe_experts(x, torch.full_like(top, -1), w, wgu, wd, status=status) == 0).all())
+    assert int(status) == 0
+
+
+@pytest.mark.parametrize("T", [4, 24])
+def test_large_layer_nan_and_infinity_stay_with_their_token(T):
+    H, F, E = 2048, 1160, 6
+    x, _, wgu, wd = layer_inputs(T, H, F, E, BF, 9)
+    top = torch.tensor([[t % 3, 3 + t % 2] for t in range(T)], dtype=torch.int32, device=DEV)
+    w = torch.full((T, 2), 0.5, device=DEV)
+    wd[5] = float("nan")  # chosen by nobody
+    wgu[5] = float("inf")
+    clean = p.moe_experts(x, top, w, wgu, wd)
+    assert bool(torch.isfinite(clean).all())
+    wd[2, 100, :] = float("nan")  # one row of an expert of tokens 2, 5, ...
+    hit = torch.tensor([t % 3 == 2 for t in range(T)], device=DEV)
+    y = p.moe_experts(x, top, w, wgu, wd)
+    rest = torch.arange(H, device=DEV) != 100
+    assert torch.equal(y[:, rest], clean[:, rest]) and torch.equal(y[~hit], clean[~hit])
+    assert bool(torch.isnan(y[hit, 100]).all())
+    x2 = x.clone()
+    x2[1, 0] = float("nan")
+    y = p.moe_experts(x2, top, w, wgu, wd)
+    keep = ~hit
+    keep[1] = False
+    assert torch.equal(y[keep], clean[keep]) and bool(torch.isnan(y[1]).all())
+
+
+def test_large_layer_streams_graphs_and_repeats():
+    T, H, F, E, K = 11, 1024, 1024, 8, 2
+    x, router, wgu, wd = layer_inputs(T, H, F, E, BF, 12)
+    y, te, w = p.moe_layer(x, router, wgu, wd, K)
+    ref, tol = experts_ref(x, te, w.double(), wgu, wd)
+    check(y, ref, tol, "y")
+    for which in range(4):
+        args = [x, router, wgu, wd]
+        args[which] = misaligned_like(args[which])
+        y2, te2, _ = p.moe_layer(*args, K)
+        assert torch.equal(te2, te)
+        check(y2, ref, tol, "misaligned %d" % which)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        y2 = p.moe_layer(x, router, wgu, wd, K)[0]
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(y2, y)
+    out, ws = torch.empty_like(y), p.block.layer_workspace(T, H, F, E, K, DEV)
+    routing = (torch.empty_like(te), torch.empty_like(w))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):  # the same workspace in calls that follow one another
+            p.moe_layer(x, router, wgu, wd, K, out=out, routing=routing, workspace=ws)
+    for _ in range(2):
+        out.fill_(float("nan"))
+        ws.fill_(0xff)
+        graph.replay()
+        assert torch.equal(out, y) and torch.equal(routing[0], te)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("T,K", [(1, 1), (6, 2), (40, 3), (256, 8)])
 def test_experts_one_expert_takes_all_and_empty_slots(T, K, dtype):
