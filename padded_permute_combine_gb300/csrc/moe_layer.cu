@@ -144,8 +144,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // ------------------------------------------------- any type, any alignment
 //
-// Products on the ordinary cores, in fp32, for fp32 layers and for rows that
-// are not a multiple of 16 bytes: a warp takes four weight rows by four
+// Products on the ordinary cores, in fp32, for fp32 layers, small ones and
+// rows of fewer than 64 elements: a warp takes four weight rows by four
 // tokens, its lanes 16 bytes of each, so that 8 loads feed 16 dot products
 // (packed in pairs). Weight rows may begin anywhere (SHIFT): a lane then loads
 // the two aligned 16-byte pieces that hold its elements (the second is the
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 2) down_rows_kernel(LayerArgs a, int
   }
 }
 
-// ------------------------------------------------- bf16 rows of 16 bytes
+// ---------------------------------------------- bf16 on the tensor cores
 //
 // Weights stream through a ring of shared-memory stages into the tensor cores:
 // tcgen05.mma with 128 weight rows as one operand and an expert's tokens (up
@@ -466,17 +466,21 @@ __global__ void __launch_bounds__(kThreads, 2) down_rows_kernel(LayerArgs a, int
 // tensor copies write and tcgen05 reads (16-byte piece q of row r lies at
 // place q ^ (r & 7); blocks start on 1 KB boundaries).
 //
+// Rows that are not a multiple of 16 bytes, or do not begin on one, are out of
+// reach of tensor copies: 16 warps copy and shift their pieces.
+//
 // Warps: 0..3 take sums out of tensor memory (warp w its lanes 32w ..), 4..7
-// copy tokens, 8 copies weights, 9 issues the products. Sums are double
-// buffered. Every wait is bounded: a warp that gives up sets
+// copy tokens, 8 (SHIFT: 8..23) copies weights, the last issues the products.
+// Sums are double buffered. Every wait is bounded: a warp that gives up sets
 // MOE_STATUS_TIMEOUT and does no more work; all warps meet at the end, where
 // the tensor memory is freed.
 
 constexpr int kOutWarps = 4;
 constexpr int kTokenWarps = 4;
-constexpr int kCopyWarp = kOutWarps + kTokenWarps;
-constexpr int kMulWarp = kCopyWarp + 1;
-constexpr int kStreamThreads = (kMulWarp + 1) * kWarp;
+constexpr int kCopyWarp = kOutWarps + kTokenWarps;  // the first
+template <bool SHIFT> constexpr int kCopyWarps = SHIFT ? 16 : 1;
+template <bool SHIFT> constexpr int kMulWarp = kCopyWarp + kCopyWarps<SHIFT>;
+template <bool SHIFT> constexpr int kStreamThreads = (kMulWarp<SHIFT> + 1) * kWarp;
 constexpr int kMaxStages = 8;
 constexpr int kBlock = 64;       // elements of a block: the 128 bytes of a swizzled row
 constexpr int kRowBytes = 128;
@@ -508,6 +512,14 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
 // 16 bytes from global to shared memory, not through L1; zeros when !in (src is not read then).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void st_shared16(uint32_t dst, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+  return v;
 }
 // The thread's arrival on the barrier, once all its copies so far have landed.
 __device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
@@ -577,9 +589,11 @@ struct Ring {
 
 struct StreamArgs {
   LayerArgs a;
-  __nv_bfloat16* h_hi;  // [n, F] in sorted order: h = h_hi + h_lo
+  __nv_bfloat16* h_hi;  // [n, h_ld] in sorted order: h = h_hi + h_lo, zeros past F
   __nv_bfloat16* h_lo;
+  int64_t h_ld;
   float* parts;  // [slices, T, H]: the slices' sums, where there are more than two
+  int64_t parts_ld;
 };
 // A kernel's cut of its work and of its shared memory.
 struct StreamShape {
@@ -595,9 +609,9 @@ struct StreamShared {
   uint32_t tmem;
 };
 
-__device__ __forceinline__ void init_shared(StreamShared& sh, int stages) {
+template <bool SHIFT> __device__ __forceinline__ void init_shared(StreamShared& sh, int stages) {
   for (int i = 0; i < stages; ++i) {
-    mbar_init_count(smem_u32(&sh.full[i]), kTokenWarps * kWarp + 1);  // the tokens' copies and the weights'
+    mbar_init_count(smem_u32(&sh.full[i]), kTokenWarps * kWarp + (SHIFT ? kCopyWarps<true> * kWarp : 1));  // the tokens' copies and the weights'
     mbar_init_count(smem_u32(&sh.empty[i]), 1);
   }
   for (int i = 0; i < 2; ++i) {
@@ -683,6 +697,91 @@ __device__ __forceinline__ void multiply(WALK w, StreamShared& sh, const StreamS
   for (int i = 0; i < z.stages; ++i) ok = wait_bar(ok, &sh.empty[i], i < r.i ? r.parity : r.parity ^ 1, status);
 }
 
+// The weights of every stage where rows are not a multiple of 16 bytes (or do
+// not begin on one). A warp copies the aligned 16-byte pieces that hold a
+// stage's elements of its rows into a buffer of its own, kRawDepth stages
+// ahead; then its lanes shift two neighbouring pieces of a row together and
+// store them where tensor copies would. Pieces held in registers instead, one
+// stage ahead: 8 tokens, 2045 x 8191, 2 of 16 experts, 386 us; 291 so (three
+// stages ahead, in stages of two blocks: no better). The ordinary cores took
+// 469 for it, and 2177 instead of 577 for 48 tokens, 4093 x 4099, 4 of 16.
+// ROWS: where this warp's i-th row of a tile begins (first(w) + i * step
+// bytes), how many it has, and the i-th's place in the tile; len: elements of
+// a row.
+constexpr int kRawDepth = 2;
+constexpr int kEach = kTileRows / kCopyWarps<true>;  // rows of a copying warp
+__host__ __device__ constexpr int raw_row(int blocks) { return blocks * kRowBytes + 16; }
+__host__ __device__ constexpr int raw_bytes(int blocks) { return kRawDepth * kTileRows * raw_row(blocks); }
+
+template <typename WALK, typename ROWS>
+__device__ __forceinline__ void copy_shifted(WALK w, StreamShared& sh, const StreamShape& z, uint32_t ring, int block, int64_t len,
+                                             int32_t* status, const ROWS& rows) {
+  const int lane = lane_id(), row_bytes = raw_row(z.blocks);
+  const uint32_t raw = ring + z.stages * z.stage_bytes + (threadIdx.x / kWarp - kCopyWarp) * (kRawDepth * kEach) * row_bytes + lane * 16;
+  const bool mine = lane < z.blocks * 8;
+  WALK ahead = w;
+  auto fetch = [&](int slot) {
+    if (ahead.more()) {
+      const int n = rows.count(ahead), pieces = (ahead.kc() + 7) / 8, left = (int)(len - ahead.k0) - lane * 8;
+      uintptr_t from = rows.first(ahead) + 2 * ahead.k0;
+      const uint32_t dst = raw + slot * kEach * row_bytes;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int shift = (int)(from & 15);
+        if (i < n && lane <= pieces && 2 * left + shift > 0)
+          copy16(dst + i * row_bytes, reinterpret_cast<const void*>(from - shift + 16 * lane), true);
+        from += rows.step;
+      }
+      ahead.next();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int d = 0; d < kRawDepth; ++d) fetch(d);
+  bool ok = true;
+  int slot = 0;
+  for (Ring r{z.stages, 0, 1}; w.more(); w.next(), r.advance()) {
+    const int n = rows.count(w), left = (int)(len - w.k0) - lane * 8;  // elements of the row from this lane's piece on
+    const int shift0 = (int)((rows.first(w) + 2 * w.k0) & 15);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRawDepth - 1) : "memory");
+    ok = wait_bar(ok, &sh.empty[r.i], r.parity, status);
+    if (!ok) break;
+    __syncwarp();
+    const uint32_t stage = ring + r.i * z.stage_bytes + (lane >> 3) * block, src = raw + slot * kEach * row_bytes;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (mine && i < n) {
+        const int shift = (shift0 + i * (int)(rows.step & 15)) & 15, bits = 8 * (shift & 3);
+        const uint4 v = ld_shared16(src + i * row_bytes), next = ld_shared16(src + i * row_bytes + 16);
+        // The shift is the same in all lanes.
+        const bool by8 = shift & 8, by4 = shift & 4;
+        const uint32_t a0 = by8 ? v.z : v.x, a1 = by8 ? v.w : v.y, a2 = by8 ? next.x : v.z, a3 = by8 ? next.y : v.w,
+                       a4 = by8 ? next.z : next.x, a5 = by8 ? next.w : next.y;
+        const uint32_t u0 = by4 ? a1 : a0, u1 = by4 ? a2 : a1, u2 = by4 ? a3 : a2, u3 = by4 ? a4 : a3, u4 = by4 ? a5 : a4;
+        uint4 o;
+        o.x = __funnelshift_r(u0, u1, bits);
+        o.y = __funnelshift_r(u1, u2, bits);
+        o.z = __funnelshift_r(u2, u3, bits);
+        o.w = __funnelshift_r(u3, u4, bits);
+        if (left < 8) {  // beyond the row: zeros
+          o.x &= WeightRow<__nv_bfloat16, true>::word_mask(left, 0);
+          o.y &= WeightRow<__nv_bfloat16, true>::word_mask(left, 1);
+          o.z &= WeightRow<__nv_bfloat16, true>::word_mask(left, 2);
+          o.w &= WeightRow<__nv_bfloat16, true>::word_mask(left, 3);
+        }
+        const int at = rows.place(i);
+        st_shared16(stage + at * kRowBytes + (((lane ^ at) & 7) << 4), o);
+      }
+    }
+    __syncwarp();
+    fetch(slot);
+    slot = slot + 1 == kRawDepth ? 0 : slot + 1;
+    fence_async_shared();
+    mbar_arrive(smem_u32(&sh.full[r.i]));
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // Tiles of up to z.rows / 2 row pairs (gate, up) of one expert by up to
 // z.tokens of its tokens, over the whole of H. A box has 16 pairs: those beyond a CTA's
 // share are read too (their owner reads them as well) and left.
@@ -727,21 +826,37 @@ struct GateUpWalk {
   }
 };
 
-__global__ void __launch_bounds__(kStreamThreads)
+// Rows of a copying warp: even warps gate rows, odd ones up rows, every eighth.
+struct GateUpRows {
+  const Segments& s;
+  uintptr_t base;
+  int64_t F, H, step;
+  int up, f;
+  __device__ GateUpRows(const Segments& s_, const LayerArgs& a, int warp)
+      : s(s_), base(reinterpret_cast<uintptr_t>(a.w_gate_up)), F(a.F), H(a.H), step(16 * a.H), up(warp & 1), f(warp >> 1) {}
+  __device__ __forceinline__ uintptr_t first(const GateUpWalk& w) const {
+    return base + 2 * (((2 * s.expert[w.q] + up) * F + w.f0 + f) * H);
+  }
+  __device__ __forceinline__ int count(const GateUpWalk& w) const { return (w.nf - f + 7) >> 3; }
+  __device__ __forceinline__ int place(int i) const { return (i >> 1) * 32 + (i & 1) * 8 + up * 16 + f; }
+};
+
+template <bool SHIFT>
+__global__ void __launch_bounds__(kStreamThreads<SHIFT>)
     gate_up_stream_kernel(StreamArgs p, StreamShape z, const __grid_constant__ CUtensorMap map) {
   extern __shared__ __align__(1024) unsigned char dyn[];
   __shared__ StreamShared sh;
   const LayerArgs& a = p.a;
   const int block = z.rows * kRowBytes;
   const int warp = threadIdx.x / kWarp, lane = lane_id();
-  if (warp == kMulWarp) tmem_alloc(smem_u32(&sh.tmem), z.cols);
+  if (warp == kMulWarp<SHIFT>) tmem_alloc(smem_u32(&sh.tmem), z.cols);
   if (threadIdx.x == kCopyWarp * kWarp) {
-    prefetch_map(&map);
-    init_shared(sh, z.stages);
+    if constexpr (!SHIFT) prefetch_map(&map);
+    init_shared<SHIFT>(sh, z.stages);
   }
   await_previous_kernel();
   const uint32_t ring = align_1k(smem_u32(dyn));
-  unsigned char* rest = dyn + (ring - smem_u32(dyn)) + (size_t)z.stages * z.stage_bytes;
+  unsigned char* rest = dyn + (ring - smem_u32(dyn)) + (size_t)z.stages * z.stage_bytes + (SHIFT ? raw_bytes(z.blocks) : 0);
   tmem_fence_before();
   const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, a.status,
                                   reinterpret_cast<int32_t*>(rest));
@@ -749,7 +864,9 @@ __global__ void __launch_bounds__(kStreamThreads)
   allow_next_kernel();
   GateUpWalk w(s, a, z);
   bool ok = true;
-  if (warp == kCopyWarp) {
+  if (SHIFT && warp >= kCopyWarp && warp < kMulWarp<SHIFT>) {
+    copy_shifted(w, sh, z, ring, block, a.H, a.status, GateUpRows(s, a, warp - kCopyWarp));
+  } else if (!SHIFT && warp == kCopyWarp) {
     for (Ring r{z.stages, 0, 1}; w.more(); w.next(), r.advance()) {
       ok = wait_bar(ok, &sh.empty[r.i], r.parity, a.status);
       if (!ok) break;
@@ -763,7 +880,7 @@ __global__ void __launch_bounds__(kStreamThreads)
             tensor_copy(at + b * block + g * 32 * kRowBytes, &map, w.k0 + b * kBlock, (int)w.f0 + g * 16, 2 * e, bar);
       }
     }
-  } else if (warp == kMulWarp) {
+  } else if (warp == kMulWarp<SHIFT>) {
     multiply(w, sh, z, ring, block, a.status, [](const GateUpWalk& v) { return round_to(v.ntok, 16); },
              [&](const GateUpWalk&) { return z.blocks * block; });
   } else if (warp >= kOutWarps) {
@@ -809,11 +926,15 @@ __global__ void __launch_bounds__(kStreamThreads)
               // Two bf16 numbers keep 16 significant bits of h: one would round the layer's result twice.
               const __nv_bfloat16 hi = __float2bfloat16_rn(h);
               const float rest = h - __bfloat162float(hi);
-              p.h_hi[i * a.F + w.f0 + f] = hi;
-              p.h_lo[i * a.F + w.f0 + f] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
+              p.h_hi[i * p.h_ld + w.f0 + f] = hi;
+              p.h_lo[i * p.h_ld + w.f0 + f] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
             }
           }
         }
+      }
+      if (SHIFT && warp == 0 && w.f0 + w.nf == a.F && lane < p.h_ld - a.F) {
+        for (int i = w.i0; i < w.i0 + w.ntok; ++i)
+          p.h_hi[i * p.h_ld + a.F + lane] = p.h_lo[i * p.h_ld + a.F + lane] = __float2bfloat16_rn(0.0f);
       }
       tmem_fence_before();
       __syncwarp();
@@ -823,7 +944,7 @@ __global__ void __launch_bounds__(kStreamThreads)
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  if (warp == kMulWarp) tmem_free(sh.tmem, z.cols);
+  if (warp == kMulWarp<SHIFT>) tmem_free(sh.tmem, z.cols);
 }
 
 // y's columns [r0, r0 + nr) for one expert's tokens after another, over this
@@ -877,6 +998,19 @@ struct DownWalk {
   }
 };
 
+// Rows of a copying warp: every sixteenth.
+struct DownRows {
+  const Segments& s;
+  uintptr_t base;
+  int64_t F, H, step;
+  int warp;
+  __device__ DownRows(const Segments& s_, const LayerArgs& a, int warp_)
+      : s(s_), base(reinterpret_cast<uintptr_t>(a.w_down)), F(a.F), H(a.H), step(32 * a.F), warp(warp_) {}
+  __device__ __forceinline__ uintptr_t first(const DownWalk& w) const { return base + 2 * ((s.expert[w.q] * H + w.r0 + warp) * F); }
+  __device__ __forceinline__ int count(const DownWalk& w) const { return (w.nr - warp + 15) >> 4; }
+  __device__ __forceinline__ int place(int i) const { return i * 16 + warp; }
+};
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
 }
@@ -889,7 +1023,8 @@ __device__ __forceinline__ float load_peer(const float* p, uint32_t rank) {
   return v;
 }
 
-__global__ void __launch_bounds__(kStreamThreads)
+template <bool SHIFT>
+__global__ void __launch_bounds__(kStreamThreads<SHIFT>)
     down_stream_kernel(StreamArgs p, StreamShape z, const __grid_constant__ CUtensorMap map) {
   extern __shared__ __align__(1024) unsigned char dyn[];
   __shared__ StreamShared sh;
@@ -898,13 +1033,13 @@ __global__ void __launch_bounds__(kStreamThreads)
   // The gate/up kernel has waited for all before it, so the routing may be
   // read and weights copied while it still runs (a CTA starts as one of the
   // other kernel leaves its SM); h may not be read.
-  if (warp == kMulWarp) tmem_alloc(smem_u32(&sh.tmem), z.cols);
+  if (warp == kMulWarp<SHIFT>) tmem_alloc(smem_u32(&sh.tmem), z.cols);
   if (threadIdx.x == kCopyWarp * kWarp) {
-    prefetch_map(&map);
-    init_shared(sh, z.stages);
+    if constexpr (!SHIFT) prefetch_map(&map);
+    init_shared<SHIFT>(sh, z.stages);
   }
   const uint32_t ring = align_1k(smem_u32(dyn));
-  unsigned char* rest = dyn + (ring - smem_u32(dyn)) + (size_t)z.stages * z.stage_bytes;
+  unsigned char* rest = dyn + (ring - smem_u32(dyn)) + (size_t)z.stages * z.stage_bytes + (SHIFT ? raw_bytes(z.blocks) : 0);
   int32_t* seg = reinterpret_cast<int32_t*>(rest);
   tmem_fence_before();
   const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, nullptr, seg);
@@ -914,7 +1049,9 @@ __global__ void __launch_bounds__(kStreamThreads)
   DownWalk w(s, a, z);
   const int block = round_to(z.rows, 8) * kRowBytes;
   bool ok = true;
-  if (warp == kCopyWarp) {
+  if (SHIFT && warp >= kCopyWarp && warp < kMulWarp<SHIFT>) {
+    copy_shifted(w, sh, z, ring, block, a.F, a.status, DownRows(s, a, warp - kCopyWarp));
+  } else if (!SHIFT && warp == kCopyWarp) {
     for (Ring r{z.stages, 0, 1}; w.more(); w.next(), r.advance()) {
       ok = wait_bar(ok, &sh.empty[r.i], r.parity, a.status);
       if (!ok) break;
@@ -927,7 +1064,7 @@ __global__ void __launch_bounds__(kStreamThreads)
           tensor_copy(at + b * block, &map, w.k0 + b * kBlock, (int)w.r0, s.expert[w.q], bar);
       }
     }
-  } else if (warp == kMulWarp) {
+  } else if (warp == kMulWarp<SHIFT>) {
     // The tile reads 128 rows; what lies beyond its weights lands in rows of the sums that nobody reads.
     multiply(w, sh, z, ring, block, a.status, [](const DownWalk& v) { return 2 * round_to(v.ntok, 8); },
              [&](const DownWalk&) { return z.blocks * block; });
@@ -941,7 +1078,7 @@ __global__ void __launch_bounds__(kStreamThreads)
       const uint32_t at = ring + r.i * z.stage_bytes + z.blocks * block;
       const int kc = w.kc(), n = round_to(w.ntok, 8);
       for (int i = first; i < w.ntok; i += 4 * kTokenWarps) {
-        const int64_t from = (w.i0 + i) * a.F + w.k0 + piece * 8;
+        const int64_t from = (w.i0 + i) * p.h_ld + w.k0 + piece * 8;
         const uint32_t dst = at + i * kRowBytes + ((piece ^ (i & 7)) << 4);
         for (int b = 0; b * kBlock < kc; ++b) {
           const bool in = b * kBlock + piece * 8 < kc;
@@ -984,7 +1121,7 @@ __global__ void __launch_bounds__(kStreamThreads)
         __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + r0 + row;
         for (int t = 0; t < a.T; ++t) y[t * a.H] = __float2bfloat16_rn(ysum[t * nr + row]);
       } else if (row < nr && z.slices > 2) {
-        float* part = p.parts + blockIdx.x % z.slices * a.T * a.H + r0 + row;
+        float* part = p.parts + blockIdx.x % z.slices * p.parts_ld + r0 + row;
         for (int t = 0; t < a.T; ++t) part[t * a.H] = ysum[t * nr + row];
       }
     }
@@ -992,7 +1129,7 @@ __global__ void __launch_bounds__(kStreamThreads)
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  if (warp == kMulWarp) tmem_free(sh.tmem, z.cols);
+  if (warp == kMulWarp<SHIFT>) tmem_free(sh.tmem, z.cols);
   if (z.slices == 2) {
     // The cluster's CTAs hold sums over their slices for the same columns of y
     // (one tile: the host cuts no more): each adds a share of them.
@@ -1002,7 +1139,7 @@ __global__ void __launch_bounds__(kStreamThreads)
     const int64_t r0 = a.H * tile_id / tiles;
     const int nr = (int)(a.H * (tile_id + 1) / tiles - r0), all = a.T * nr, slice = blockIdx.x % z.slices;
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + r0;
-    for (int i = all * slice / z.slices + threadIdx.x; i < all * (slice + 1) / z.slices; i += kStreamThreads) {
+    for (int i = all * slice / z.slices + threadIdx.x; i < all * (slice + 1) / z.slices; i += kStreamThreads<SHIFT>) {
       float sum = 0.0f;
       for (int k = 0; k < z.slices; ++k) sum += load_peer(ysum + i, k);
       y[i / nr * a.H + i % nr] = __float2bfloat16_rn(sum);
@@ -1014,23 +1151,23 @@ __global__ void __launch_bounds__(kStreamThreads)
 
 // y = the sum of the slices' parts, in their order; four columns a thread.
 __global__ void __launch_bounds__(kThreads)
-    sum_parts_kernel(const float* __restrict__ parts, int slices, int64_t n, __nv_bfloat16* __restrict__ y) {
+    sum_parts_kernel(const float* __restrict__ parts, int64_t ld, int slices, int64_t n, __nv_bfloat16* __restrict__ y) {
   await_previous_kernel();
   const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
   if (i >= n) return;
   float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
   for (int k = 0; k < slices; ++k) {
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(parts + k * n + i));
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(parts + k * ld + i));
     sum.x += v.x;
     sum.y += v.y;
     sum.z += v.z;
     sum.w += v.w;
   }
   y[i] = __float2bfloat16_rn(sum.x);
-  y[i + 1] = __float2bfloat16_rn(sum.y);
-  y[i + 2] = __float2bfloat16_rn(sum.z);
-  y[i + 3] = __float2bfloat16_rn(sum.w);
+  if (i + 1 < n) y[i + 1] = __float2bfloat16_rn(sum.y);
+  if (i + 2 < n) y[i + 2] = __float2bfloat16_rn(sum.z);
+  if (i + 3 < n) y[i + 3] = __float2bfloat16_rn(sum.w);
 }
 
 // ------------------------------------------------------------------ host
@@ -1122,19 +1259,21 @@ uint32_t tmem_cols(int cols) {
   return c;
 }
 
-// Blocks of a stage, `most` or as many fewer as leave three stages (two with one block).
-bool cut_stages(StreamShape* z, int block_bytes, int most, size_t rest) {
+// Blocks of a stage, `most` or as many fewer as leave `least` stages (two with one block).
+template <bool SHIFT> bool cut_stages(StreamShape* z, int block_bytes, int most, size_t rest) {
+  constexpr int least = SHIFT ? 2 : 3;
   for (z->blocks = most; z->blocks >= 1; --z->blocks) {
     z->stage_bytes = z->blocks * block_bytes;
-    if (fit_stages(z, rest) && (z->stages >= 3 || z->blocks == 1)) return true;
+    if (fit_stages(z, rest + (SHIFT ? raw_bytes(z->blocks) : 0)) && (z->stages >= least || z->blocks == 1)) return true;
   }
   return false;
 }
 
-int run_stream(const LayerArgs& a, float* parts, cudaStream_t s) {
+template <bool SHIFT> int run_stream(const LayerArgs& a, float* parts, cudaStream_t s) {
   static std::atomic<int> granted_g[64], granted_d[64];
   __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(a.h);
-  const StreamArgs p{a, h, h + (int64_t)a.n * a.F, parts};
+  const int64_t h_ld = padded_row(a.F), y_n = a.T * a.H, parts_ld = (y_n + 3) / 4 * 4;
+  const StreamArgs p{a, h, h + a.n * h_ld, h_ld, parts, parts_ld};
   const int64_t sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
   const size_t seg = segments_bytes(a.n, a.E);
   // Tokens of an expert at a time: twice the mean and 16, so that few experts
@@ -1150,8 +1289,8 @@ int run_stream(const LayerArgs& a, float* parts, cudaStream_t s) {
   g.rows = kTileRows;
   g.tokens = round_to(a.T, 16) < cap ? round_to(a.T, 16) : cap;
   g.cols = tmem_cols(2 * g.tokens);
-  if (!cut_stages(&g, (g.rows + g.tokens) * kRowBytes, 3, seg)) return MOE_ERR_UNSUPPORTED;
-  const size_t g_smem = seg + (size_t)g.stages * g.stage_bytes + 1024;
+  if (!cut_stages<SHIFT>(&g, (g.rows + g.tokens) * kRowBytes, 3, seg)) return MOE_ERR_UNSUPPORTED;
+  const size_t g_smem = seg + (size_t)g.stages * g.stage_bytes + (SHIFT ? raw_bytes(g.blocks) : 0) + 1024;
 
   // A product costs the same whatever rows of its 128 the tile holds (27 rows,
   // H 2048 over pairs of SMs: 2.3 TB/s), and every tile reads all of h. So
@@ -1179,22 +1318,22 @@ int run_stream(const LayerArgs& a, float* parts, cudaStream_t s) {
     // behind the ring lie at least as many bytes of the CTA's memory.
     d_smem = seg + sizeof(float) * a.T * d.rows;
     if (d_smem < kTileRows * kRowBytes) d_smem = kTileRows * kRowBytes;
-    fits = cut_stages(&d, block, block < 65536 ? 65536 / block : 1, d_smem);
+    fits = cut_stages<SHIFT>(&d, block, SHIFT ? 3 : block < 65536 ? 65536 / block : 1, d_smem);
   }
   if (!fits) return MOE_ERR_UNSUPPORTED;
-  d_smem += (size_t)d.stages * d.stage_bytes + 1024;
+  d_smem += (size_t)d.stages * d.stage_bytes + (SHIFT ? raw_bytes(d.blocks) : 0) + 1024;
 
-  CUtensorMap g_map, d_map;
-  if (!allow_smem(gate_up_stream_kernel, (int)g_smem, granted_g) ||
-      !allow_smem(down_stream_kernel, (int)d_smem, granted_d) ||
-      !tensor_map(&g_map, a.w_gate_up, a.H, a.F, 2 * (int64_t)a.E, 16, 2) ||
-      !tensor_map(&d_map, a.w_down, a.F, a.H, a.E, d.rows, 1))
+  CUtensorMap g_map = {}, d_map = {};
+  if (!allow_smem(gate_up_stream_kernel<SHIFT>, (int)g_smem, granted_g) ||
+      !allow_smem(down_stream_kernel<SHIFT>, (int)d_smem, granted_d) ||
+      (!SHIFT && (!tensor_map(&g_map, a.w_gate_up, a.H, a.F, 2 * (int64_t)a.E, 16, 2) ||
+                  !tensor_map(&d_map, a.w_down, a.F, a.H, a.E, d.rows, 1))))
     return MOE_ERR_CUDA;
   const int64_t pairs = (a.n < a.E ? a.n : a.E) * a.F;
-  launch(gate_up_stream_kernel, (unsigned)(pairs < sms ? pairs : sms), kStreamThreads, g_smem, s, p, g, g_map);
+  launch(gate_up_stream_kernel<SHIFT>, (unsigned)(pairs < sms ? pairs : sms), kStreamThreads<SHIFT>, g_smem, s, p, g, g_map);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kStreamThreads);
+  cfg.blockDim = dim3(kStreamThreads<SHIFT>);
   cfg.dynamicSmemBytes = d_smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -1204,12 +1343,10 @@ int run_stream(const LayerArgs& a, float* parts, cudaStream_t s) {
   attr[1].val.clusterDim = {(unsigned)d.slices, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = d.slices == 2 ? 2 : 1;
-  (void)cudaLaunchKernelEx(&cfg, down_stream_kernel, p, d, d_map);
-  if (d.slices > 2) {
-    const int64_t y_n = a.T * a.H;
-    launch(sum_parts_kernel, (unsigned)((y_n / 4 + kThreads - 1) / kThreads), kThreads, 0, s, p.parts, d.slices, y_n,
+  (void)cudaLaunchKernelEx(&cfg, down_stream_kernel<SHIFT>, p, d, d_map);
+  if (d.slices > 2)
+    launch(sum_parts_kernel, (unsigned)((parts_ld / 4 + kThreads - 1) / kThreads), kThreads, 0, s, p.parts, parts_ld, d.slices, y_n,
            static_cast<__nv_bfloat16*>(a.y));
-  }
   return check_launch();
 }
 
@@ -1235,7 +1372,6 @@ int dispatch(const LayerArgs& a, const void* router, float* logits, float* parts
     if (rc != MOE_OK) return rc;
   }
   const bool by16 = a.H % kE == 0 && a.F % kE == 0 && aligned(a.w_gate_up, 16) && aligned(a.w_down, 16);
-  if (!by16) return run_rows<ET, true>(a, x, x_ld, s);
   if constexpr (Elem<ET>::kBytes == 2) {
     // The tensor path costs some 8 us more to start: below 100 MB of weights
     // (every choice's own) the ordinary cores are ahead. One token, 512 x 512,
@@ -1248,9 +1384,10 @@ int dispatch(const LayerArgs& a, const void* router, float* logits, float* parts
       LayerArgs b = a;
       b.x = x;
       b.x_stride = x_ld;
-      return run_stream(b, parts, s);
+      return by16 ? run_stream<false>(b, parts, s) : run_stream<true>(b, parts, s);
     }
   }
+  if (!by16) return run_rows<ET, true>(a, x, x_ld, s);
   return run_rows<ET, false>(a, x, x_ld, s);
 }
 
@@ -1259,7 +1396,7 @@ size_t logits_bytes(int64_t T, int32_t E) { return ((size_t)T * E * sizeof(float
 size_t h_bytes(int64_t n, int64_t F) { return ((size_t)n * (size_t)padded_row(F) * sizeof(float) + 255) / 256 * 256; }
 
 // slices * H <= SMs * the rows of a tile, and a tile has no more rows than y columns.
-size_t parts_bytes(int64_t T, int64_t H) { return (size_t)T * kMaxSms * (H < kTileRows ? H : kTileRows) * sizeof(float); }
+size_t parts_bytes(int64_t T, int64_t H) { return kMaxSms * ((size_t)T * (H < kTileRows ? H : kTileRows) + 4) * sizeof(float); }
 
 bool sizes_ok(int64_t T, int64_t H, int64_t F, int32_t E, int32_t K) {
   return T >= 0 && H >= 1 && F >= 1 && E >= 1 && K >= 1 && K <= E && K <= MOE_MAX_TOP_K &&

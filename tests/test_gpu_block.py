@@ -111,7 +111,11 @@ def test_layer(T, H, F, E, K, dtype):
 # by the blocks of 64, one, two and more SMs to a tile of y's columns, two tiles an SM, several passes over an expert.
 LARGE = [(16, 1024, 1040, 8, 2), (1, 4096, 4104, 4, 1), (5, 1096, 1048, 16, 3), (70, 512, 264, 8, 2), (256, 136, 72, 8, 8),
          (256, 64, 136, 8, 8), (64, 264, 1000, 300, 4), (130, 2048, 72, 2, 1), (3, 12288, 520, 6, 1), (2, 20480, 1024, 4, 2),
-         (40, 6144, 136, 5, 2), (256, 1024, 80, 8, 8), (23, 1400, 904, 12, 5), (8, 7168, 512, 32, 8)]
+         (40, 6144, 136, 5, 2), (256, 1024, 80, 8, 8), (23, 1400, 904, 12, 5), (8, 7168, 512, 32, 8),
+         # rows off 16 bytes
+         (16, 1025, 1041, 8, 2), (1, 4099, 4102, 4, 1), (5, 1097, 1049, 16, 3), (70, 513, 263, 8, 2), (256, 137, 73, 8, 8),
+         (256, 65, 135, 8, 8), (64, 267, 1001, 300, 4), (130, 2046, 77, 2, 1), (3, 12289, 521, 6, 1), (2, 20481, 1023, 4, 2),
+         (40, 6145, 137, 5, 2), (255, 1023, 81, 8, 8), (23, 1400, 903, 12, 5), (23, 1401, 904, 12, 5), (8, 7167, 513, 32, 8)]
 
 
 @pytest.mark.parametrize("T,H,F,E,K", LARGE)
