@@ -22,10 +22,6 @@ def _stream(device: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _ptr(t: torch.Tensor | None) -> int | None:
-    return None if t is None else t.data_ptr()
-
-
 def _rows(t: torch.Tensor, name: str, dtype: torch.dtype | None = None, shape=None, device=None) -> int:
     """Checks a [rows, H] tensor whose rows are contiguous and returns its row stride."""
     if not isinstance(t, torch.Tensor):
@@ -38,26 +34,24 @@ def _rows(t: torch.Tensor, name: str, dtype: torch.dtype | None = None, shape=No
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if device is not None and t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.is_contiguous():
+        return t.shape[1]
     stride = t.stride(0)
-    if not t.is_contiguous():
-        if t.shape[1] > 1 and t.stride(1) != 1:
-            raise ValueError("%s must have contiguous rows" % name)
-        if t.shape[0] > 1 and stride < t.shape[1]:
-            raise ValueError("%s must have rows that do not overlap" % name)
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    if t.shape[0] > 1 and stride < t.shape[1]:
+        raise ValueError("%s must have rows that do not overlap" % name)
     return stride
 
 
-def _shape(t: torch.Tensor, shape: tuple, name: str) -> torch.Tensor:
-    if t.shape != shape:
-        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
-    return t
-
-
-def _out(t: torch.Tensor | None, shape: tuple, dtype: torch.dtype, name: str, device) -> torch.Tensor:
-    """The caller's output tensor, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return _shape(_need(t, dtype, name, device), shape, name)
+def _take(t: torch.Tensor, shape: tuple, dtype: torch.dtype, name: str, device) -> int:
+    """Checks a contiguous tensor and returns its address (one test of all at
+    once: a few calls here are as long as a small kernel)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _need(t, dtype, name, device)
+    raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
 
 
 def _workspace(t: torch.Tensor | None, size: int, device) -> torch.Tensor:
@@ -75,15 +69,14 @@ def _status(t: torch.Tensor | None, device) -> int | None:
     return None if t is None else _need(t, torch.int32, "status", device).data_ptr()
 
 
-def _expert_weights(x, w_gate_up, w_down):
-    _need(w_gate_up, x.dtype, "w_gate_up", x.device)
-    _need(w_down, x.dtype, "w_down", x.device)
-    H = x.shape[1]
-    if w_down.dim() != 3 or w_down.shape[1] != H:
+def _expert_weights(x, H, w_gate_up, w_down):
+    """E, F and the addresses of the experts' matrices, which go with x."""
+    if not isinstance(w_down, torch.Tensor) or w_down.dim() != 3 or w_down.shape[1] != H:
+        _need(w_down, x.dtype, "w_down", x.device)
         raise ValueError("w_down must be [E, %d, F], got %s" % (H, list(w_down.shape)))
-    E, F = w_down.shape[0], w_down.shape[2]
-    _shape(w_gate_up, (E, 2 * F, H), "w_gate_up")
-    return E, F
+    E, _, F = w_down.shape
+    down = _take(w_down, (E, H, F), x.dtype, "w_down", x.device)
+    return E, F, _take(w_gate_up, (E, 2 * F, H), x.dtype, "w_gate_up", x.device), down
 
 
 def layer_workspace(num_tokens: int, hidden: int, ffn: int, num_experts: int, top_k: int, device) -> torch.Tensor:
@@ -105,19 +98,26 @@ def moe_layer(x: torch.Tensor, router: torch.Tensor, w_gate_up: torch.Tensor, w_
     dt = _act_dtype(x, "x")
     dev = x.device
     T, H = x.shape
-    E, F = _expert_weights(x, w_gate_up, w_down)
-    _shape(_need(router, x.dtype, "router", dev), (E, H), "router")
+    E, F, gate_up, down = _expert_weights(x, H, w_gate_up, w_down)
+    router_at = _take(router, (E, H), x.dtype, "router", dev)
     if mode not in _MODES:
         raise ValueError("mode must be softmax or sigmoid, got %r" % (mode,))
-    te, w = (None, None) if routing is None else routing
-    te = _out(te, (T, top_k), torch.int32, "top_expert", dev)
-    w = _out(w, (T, top_k), torch.float32, "weights", dev)
-    out = _out(out, (T, H), x.dtype, "out", dev)
-    ws = _workspace(workspace, _lib.load().moe_layer_workspace_size(T, H, F, E, top_k), dev)
-    rc = _lib.load().moe_layer(
-        x.data_ptr(), dt, stride, router.data_ptr(), w_gate_up.data_ptr(), w_down.data_ptr(), T, H, F, E, top_k,
-        _MODES[mode], int(bool(normalize)), te.data_ptr(), w.data_ptr(), out.data_ptr(), ws.data_ptr(),
-        ws.numel(), _status(status, dev), _stream(dev))
+    if routing is None:
+        te = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        w = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        te_at, w_at = te.data_ptr(), w.data_ptr()
+    else:
+        te, w = routing
+        te_at = _take(te, (T, top_k), torch.int32, "top_expert", dev)
+        w_at = _take(w, (T, top_k), torch.float32, "weights", dev)
+    if out is None:
+        out = torch.empty((T, H), dtype=x.dtype, device=dev)
+    out_at = _take(out, (T, H), x.dtype, "out", dev)
+    lib = _lib.load()
+    ws = _workspace(workspace, lib.moe_layer_workspace_size(T, H, F, E, top_k), dev)
+    rc = lib.moe_layer(
+        x.data_ptr(), dt, stride, router_at, gate_up, down, T, H, F, E, top_k, _MODES[mode], int(bool(normalize)),
+        te_at, w_at, out_at, ws.data_ptr(), ws.numel(), _status(status, dev), _stream(dev))
     _done("moe_layer", rc)
     return out, te, w
 
@@ -132,32 +132,31 @@ def moe_experts(x: torch.Tensor, top_expert: torch.Tensor, weights: torch.Tensor
     dt = _act_dtype(x, "x")
     dev = x.device
     T, H = x.shape
-    E, F = _expert_weights(x, w_gate_up, w_down)
+    E, F, gate_up, down = _expert_weights(x, H, w_gate_up, w_down)
     _need(top_expert, torch.int32, "top_expert", dev)
     if top_expert.dim() != 2 or top_expert.shape[0] != T:
         raise ValueError("top_expert must be [%d, top_k], got %s" % (T, list(top_expert.shape)))
     K = top_expert.shape[1]
-    _shape(_need(weights, torch.float32, "weights", dev), (T, K), "weights")
-    out = _out(out, (T, H), x.dtype, "out", dev)
-    ws = _workspace(workspace, _lib.load().moe_layer_workspace_size(T, H, F, E, K), dev)
-    rc = _lib.load().moe_experts(
-        x.data_ptr(), dt, stride, top_expert.data_ptr(), weights.data_ptr(), w_gate_up.data_ptr(), w_down.data_ptr(), T,
-        H, F, E, K, out.data_ptr(), ws.data_ptr(), ws.numel(), _status(status, dev), _stream(dev))
+    w_at = _take(weights, (T, K), torch.float32, "weights", dev)
+    if out is None:
+        out = torch.empty((T, H), dtype=x.dtype, device=dev)
+    out_at = _take(out, (T, H), x.dtype, "out", dev)
+    lib = _lib.load()
+    ws = _workspace(workspace, lib.moe_layer_workspace_size(T, H, F, E, K), dev)
+    rc = lib.moe_experts(
+        x.data_ptr(), dt, stride, top_expert.data_ptr(), w_at, gate_up, down, T, H, F, E, K, out_at, ws.data_ptr(),
+        ws.numel(), _status(status, dev), _stream(dev))
     _done("moe_experts", rc)
     return out
 
 
-def _affine(weight, bias, H, dev):
-    """The dtype of weight and bias ([H] each, or None), as a MOE_* value."""
-    code = _lib.MOE_F32
-    for t, name in ((bias, "bias"), (weight, "weight")):
-        if t is not None:
-            _need(t, None, name, dev)
-            _shape(t, (H,), name)
-            code = _act_dtype(t, name)
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise TypeError("weight and bias must have one dtype, got %s and %s" % (weight.dtype, bias.dtype))
-    return code
+def _affine(t, H, name, dev) -> tuple[int | None, int]:
+    """Address and MOE_* dtype of weight or bias ([H], or None)."""
+    if t is None:
+        return None, _lib.MOE_F32
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    return _take(t, (H,), t.dtype, name, dev), _act_dtype(t, name)
 
 
 def moe_layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
@@ -169,14 +168,28 @@ def moe_layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias
     dt = _act_dtype(x, "x")
     dev = x.device
     M, H = x.shape
-    wdt = _affine(weight, bias, H, dev)
-    out = _out(out, (M, H), x.dtype, "out", dev)
-    mean, rstd = (None, None) if stats is None else stats
-    mean = _out(mean, (M,), torch.float32, "mean", dev)
-    rstd = _out(rstd, (M,), torch.float32, "rstd", dev)
+    bias_at, wdt = _affine(bias, H, "bias", dev)
+    if weight is not None or bias is None:
+        weight_at, wdt = _affine(weight, H, "weight", dev)
+        if bias is not None and weight.dtype is not bias.dtype:
+            raise TypeError("weight and bias must have one dtype, got %s and %s" % (weight.dtype, bias.dtype))
+    else:
+        weight_at = None
+    if out is None:
+        out = torch.empty((M, H), dtype=x.dtype, device=dev)
+        out_at = out.data_ptr()
+    else:
+        out_at = _take(out, (M, H), x.dtype, "out", dev)
+    if stats is None:
+        mean = torch.empty(M, dtype=torch.float32, device=dev)
+        rstd = torch.empty(M, dtype=torch.float32, device=dev)
+        mean_at, rstd_at = mean.data_ptr(), rstd.data_ptr()
+    else:
+        mean, rstd = stats
+        mean_at = _take(mean, (M,), torch.float32, "mean", dev)
+        rstd_at = _take(rstd, (M,), torch.float32, "rstd", dev)
     rc = _lib.load().moe_layer_norm_fwd(
-        x.data_ptr(), dt, stride, _ptr(weight), _ptr(bias), wdt, M, H, eps, out.data_ptr(), mean.data_ptr(),
-        rstd.data_ptr(), _stream(dev))
+        x.data_ptr(), dt, stride, weight_at, bias_at, wdt, M, H, eps, out_at, mean_at, rstd_at, _stream(dev))
     _done("moe_layer_norm_fwd", rc)
     return out, mean, rstd
 
@@ -192,21 +205,29 @@ def moe_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor |
     dev = x.device
     M, H = x.shape
     dy_stride = _rows(dy, "dy", x.dtype, x.shape, dev)
-    _shape(_need(mean, torch.float32, "mean", dev), (M,), "mean")
-    _shape(_need(rstd, torch.float32, "rstd", dev), (M,), "rstd")
+    mean_at = _take(mean, (M,), torch.float32, "mean", dev)
+    rstd_at = _take(rstd, (M,), torch.float32, "rstd", dev)
+    weight_at, code = _affine(weight, H, "weight", dev)
     if weight is not None:
         weight_dtype = weight.dtype
-    wdt = weight_dtype or torch.float32
-    code = _affine(weight, None, H, dev) if weight is not None else _lib.MOE_BF16 if wdt == torch.bfloat16 else _lib.MOE_F32
-    out = _out(out, (M, H), x.dtype, "out", dev)
-    dw = db = ws = None
+    elif weight_dtype is None:
+        weight_dtype = torch.float32
+    elif weight_dtype is torch.bfloat16:
+        code = _lib.MOE_BF16
+    if out is None:
+        out = torch.empty((M, H), dtype=x.dtype, device=dev)
+    out_at = _take(out, (M, H), x.dtype, "out", dev)
+    lib = _lib.load()
+    dw = db = dw_at = db_at = ws_at = None
+    ws_bytes = 0
     if need_cols:
-        dw = torch.empty(H, dtype=wdt, device=dev)
-        db = torch.empty(H, dtype=wdt, device=dev)
-        ws = _workspace(workspace, _lib.load().moe_layer_norm_bwd_workspace_size(M, H), dev)
-    rc = _lib.load().moe_layer_norm_bwd(
-        dy.data_ptr(), dy_stride, x.data_ptr(), dt, stride, _ptr(weight), code, mean.data_ptr(), rstd.data_ptr(), M, H,
-        out.data_ptr(), _ptr(dw), _ptr(db), _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev))
+        dw = torch.empty(H, dtype=weight_dtype, device=dev)
+        db = torch.empty(H, dtype=weight_dtype, device=dev)
+        ws = _workspace(workspace, lib.moe_layer_norm_bwd_workspace_size(M, H), dev)
+        dw_at, db_at, ws_at, ws_bytes = dw.data_ptr(), db.data_ptr(), ws.data_ptr(), ws.numel()
+    rc = lib.moe_layer_norm_bwd(
+        dy.data_ptr(), dy_stride, x.data_ptr(), dt, stride, weight_at, code, mean_at, rstd_at, M, H, out_at, dw_at, db_at,
+        ws_at, ws_bytes, _stream(dev))
     _done("moe_layer_norm_bwd", rc)
     return out, dw, db
 
@@ -230,7 +251,7 @@ class GradSet:
         for i, g in enumerate(self.grads):
             _need(g, None, "grads[%d]" % i, dev)
             o = g if self.outs is None else self.outs[i]
-            _shape(_need(o, g.dtype, "outs[%d]" % i, dev), g.shape, "outs[%d]" % i)
+            _take(o, g.shape, g.dtype, "outs[%d]" % i, dev)
             entries[i] = _lib.GradTensor(g.data_ptr() or None, o.data_ptr() or None, g.numel(), _act_dtype(g, "grads[%d]" % i), 0)
         lib = _lib.load()
         self.pieces = lib.moe_grad_table_pieces(entries, len(entries))
