@@ -7,11 +7,13 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import re
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmoe_route.so")
+CALLS_PATH = os.path.join(PKG, "_block_calls.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "moe_route.h")
 BLOCK_HEADER = os.path.join(os.path.dirname(PKG), "include", "moe_block.h")
 
@@ -121,6 +123,26 @@ def load(path: str | None = None) -> ctypes.CDLL:
     if path is None:
         _lib = lib
     return lib
+
+
+calls = None  # the module _block_calls, once loaded
+
+
+def load_calls():
+    """Load the native marshalling of the block operators once. Raises if it has not been built."""
+    global calls
+    if calls is None:
+        if not os.path.exists(CALLS_PATH):
+            raise RuntimeError("_block_calls.so is not built (%s); run "
+                               "`python -m padded_permute_combine_gb300.build` first" % CALLS_PATH)
+        import torch  # noqa: F401  (its libraries, which the module needs)
+
+        load()
+        spec = importlib.util.spec_from_file_location("_block_calls", CALLS_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        calls = module
+    return calls
 
 
 def call(name: str, *args) -> None:

@@ -3,6 +3,9 @@ an MoE block (same names, same semantics).
 
 As in ops.py this is argument marshalling only. Rows (x, dy) may come with a
 row stride, such as a slice of a wider tensor; everything else is contiguous.
+The plain call (right arguments, outputs to be allocated) is marshalled by
+csrc/block_calls.cpp; it answers None to any other, which is then taken step by
+step here, with a message for what is wrong.
 """
 from __future__ import annotations
 
@@ -94,6 +97,10 @@ def moe_layer(x: torch.Tensor, router: torch.Tensor, w_gate_up: torch.Tensor, w_
     (y [T, H], top_expert [T, top_k] int32, weights [T, top_k] fp32). mode and
     normalize as for moe_topk_gating; ``routing``: the two tensors that take
     top_expert and weights."""
+    if out is None and routing is None and workspace is None and status is None and mode in _MODES:
+        done = (_lib.calls or _lib.load_calls()).layer(x, router, w_gate_up, w_down, top_k, _MODES[mode], bool(normalize))
+        if done is not None:
+            return done
     stride = _rows(x, "x")
     dt = _act_dtype(x, "x")
     dev = x.device
@@ -128,6 +135,10 @@ def moe_experts(x: torch.Tensor, top_expert: torch.Tensor, weights: torch.Tensor
     """The gated experts and their weighted sum for a routing already made:
     x [T, H], top_expert [T, top_k] int32 (-1: no expert), weights [T, top_k]
     fp32 -> y [T, H]. Sizes as for moe_layer."""
+    if out is None and workspace is None and status is None:
+        done = (_lib.calls or _lib.load_calls()).experts(x, top_expert, weights, w_gate_up, w_down)
+        if done is not None:
+            return done[0]
     stride = _rows(x, "x")
     dt = _act_dtype(x, "x")
     dev = x.device
@@ -164,6 +175,10 @@ def moe_layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias
                        stats: tuple[torch.Tensor, torch.Tensor] | None = None):
     """Layer norm of the rows of x [rows, H]: (y [rows, H], mean [rows] fp32,
     rstd [rows] fp32). ``stats``: the two tensors that take mean and rstd."""
+    if out is None and stats is None:
+        done = (_lib.calls or _lib.load_calls()).layer_norm_fwd(x, weight, bias, eps)
+        if done is not None:
+            return done
     stride = _rows(x, "x")
     dt = _act_dtype(x, "x")
     dev = x.device
@@ -200,6 +215,10 @@ def moe_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor |
     """Gradients of moe_layer_norm_fwd: (dx [rows, H], dweight [H], dbias [H]).
     dweight and dbias have weight's dtype (``weight_dtype`` without a weight,
     fp32 by default), and are None with need_cols=False."""
+    if out is None and workspace is None and (weight is not None or weight_dtype is None):
+        done = (_lib.calls or _lib.load_calls()).layer_norm_bwd(dy, x, weight, mean, rstd, bool(need_cols))
+        if done is not None:
+            return done
     stride = _rows(x, "x")
     dt = _act_dtype(x, "x")
     dev = x.device
@@ -281,6 +300,10 @@ def _grad_args(grads, norm, workspace):
 def moe_grad_norm(grads: GradSet | Sequence[torch.Tensor], norm: torch.Tensor | None = None,
                   workspace: torch.Tensor | None = None) -> torch.Tensor:
     """2-norm over all elements of all gradients, fp32 on the device."""
+    if norm is None and workspace is None and isinstance(grads, GradSet):
+        done = (_lib.calls or _lib.load_calls()).grads(grads.table, grads.workspace, grads.pieces)
+        if done is not None:
+            return done[0]
     s, norm, ws = _grad_args(grads, norm, workspace)
     rc = _lib.load().moe_grad_norm(
         s.table.data_ptr(), s.pieces, norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream(s.device))
@@ -292,6 +315,10 @@ def moe_clip_grads(grads: GradSet | Sequence[torch.Tensor], max_norm: float, nor
                    workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Scales the gradients by min(1, max_norm / (norm + 1e-6)), into the
     set's outs or in place, and returns their norm before that."""
+    if norm is None and workspace is None and isinstance(grads, GradSet):
+        done = (_lib.calls or _lib.load_calls()).grads(grads.table, grads.workspace, grads.pieces, max_norm)
+        if done is not None:
+            return done[0]
     s, norm, ws = _grad_args(grads, norm, workspace)
     rc = _lib.load().moe_clip_grads(
         s.table.data_ptr(), s.pieces, max_norm, norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream(s.device))

@@ -1,7 +1,9 @@
-"""Build libmoe_route.so in-tree with nvcc for sm_103a.
+"""Build libmoe_route.so in-tree with nvcc for sm_103a, and _block_calls.so.
 
 Each CUDA translation unit is compiled in parallel into ``_build/`` and the
 objects are linked into ``padded_permute_combine_gb300/libmoe_route.so``.
+``_block_calls.so``, the marshalling of the block operators' calls, is
+compiled beside them against the headers of the installed torch.
 Run ``python -m padded_permute_combine_gb300.build`` or call ``build()``.
 """
 from __future__ import annotations
@@ -9,10 +11,12 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_route.so")
+CALLS_SOURCE = os.path.join(CSRC, "block_calls.cpp")
+CALLS = os.path.join(PKG, "_block_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
@@ -97,16 +103,71 @@ def _compile(src: str, extra: list[str]) -> tuple[str, str]:
     return obj, res.stderr
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        raise RuntimeError("torch is not installed")
+    return os.path.dirname(spec.origin)
+
+
+def _calls_digest() -> str:
+    h = hashlib.sha256()
+    for f in [CALLS_SOURCE, os.path.join(_torch_dir(), "version.py")] + sorted(glob.glob(os.path.join(INCLUDE, "*.h"))):
+        with open(f, "rb") as fh:
+            h.update(fh.read())
+    return h.hexdigest()[:16]
+
+
+def _compile_calls() -> str:
+    obj = os.path.join(BUILD_DIR, "block_calls.o")
+    torch_include = os.path.join(_torch_dir(), "include")
+    cuda_include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-isystem", torch_include, "-isystem",
+           os.path.join(torch_include, "torch", "csrc", "api", "include"), "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", cuda_include, "-c", CALLS_SOURCE, "-o", obj]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("%s failed:\n%s" % (" ".join(cmd), res.stderr))
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    """Linked to the libraries by the names under which torch and the loader have them in the process already."""
+    tmp = CALLS + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", PKG, "-l:libmoe_route.so", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), res.stderr))
+    os.replace(tmp, CALLS)
+    with open(CALLS + ".digest", "w") as f:
+        f.write(_calls_digest() + "\n")
+
+
+def _fresh(path: str, digest: str) -> bool:
+    stamp = path + ".digest"
+    return os.path.exists(path) and os.path.exists(stamp) and open(stamp).read().strip() == digest
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile every .cu under csrc/ and link the shared library. Skipped when
-    the library was built from the current sources (same digest)."""
-    srcs = sources()
-    stamp = LIB + ".digest"
-    digest = source_digest()
-    if (not force and not verbose_ptxas and os.path.exists(LIB) and os.path.exists(stamp)
-            and open(stamp).read().strip() == digest):
-        return LIB
-    os.makedirs(BUILD_DIR, exist_ok=True)
+    """Compile every .cu under csrc/ and link the shared library, and the
+    module of the block operators' calls. Each is skipped when it was built
+    from the current sources (same digest)."""
+    again = force or verbose_ptxas
+    lib, calls = again or not _fresh(LIB, source_digest()), again or not _fresh(CALLS, _calls_digest())
+    if lib or calls:
+        os.makedirs(BUILD_DIR, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        obj = ex.submit(_compile_calls) if calls else None
+        if lib:
+            _build_lib(verbose_ptxas)
+        if obj is not None:
+            _link_calls(obj.result())
+    return LIB
+
+
+def _build_lib(verbose_ptxas: bool) -> None:
+    srcs, digest = sources(), source_digest()
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
         results = list(ex.map(lambda s: _compile(s, extra), srcs))
@@ -119,9 +180,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), res.stderr))
     os.replace(tmp, LIB)
-    with open(stamp, "w") as f:
+    with open(LIB + ".digest", "w") as f:
         f.write(digest + "\n")
-    return LIB
 
 
 if __name__ == "__main__":
