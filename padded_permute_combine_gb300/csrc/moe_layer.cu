@@ -148,9 +148,11 @@ __device__ __forceinline__ float warp_sum(float v) {
 // rows of fewer than 64 elements: a warp takes four weight rows by four
 // tokens, its lanes 16 bytes of each, so that 8 loads feed 16 dot products
 // (packed in pairs). Weight rows may begin anywhere (SHIFT): a lane then loads
-// the two aligned 16-byte pieces that hold its elements (the second is the
-// next lane's first, in L1) and shifts them together; a row's last piece is
-// masked. Loading such rows element by element reached a quarter of the rate
+// the aligned 16-byte piece that holds the first of its elements, an iteration
+// ahead, and shifts it together with the next lane's; the last lane's serves
+// its neighbour alone, and a row's last piece is masked (both pieces loaded by
+// every lane: 278 us instead of 251 for 16 tokens, fp32, 1501 x 2003, 4 of 16
+// experts). Loading such rows element by element reached a quarter of the rate
 // (the odd fp32 layer of 5 tokens, 1001 x 777: 26 and 68 us for the two
 // kernels). The tokens' rows are aligned, x in the workspace where it is not.
 
@@ -185,12 +187,16 @@ template <typename ET, bool SHIFT> struct WeightRow {
     len = (int)n;
     last = (int)((shift + n * Elem<ET>::kBytes - 1) / 16);
   }
-  // Piece i, zeros past the row's end.
-  __device__ __forceinline__ uint4 get(int i) const {
+  // The aligned piece i, zeros past the row's last.
+  __device__ __forceinline__ uint4 load(int i) const {
     if constexpr (!SHIFT) return __ldg(p + i);
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint4 a = i <= last ? __ldg(p + i) : zero, b = i < last ? __ldg(p + i + 1) : zero;
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    return i <= last ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
+  }
+  // The elements of piece i from it and the next lane's, zeros past the row's end.
+  __device__ __forceinline__ uint4 shifted(const uint4& a, int i) const {
+    const uint32_t b[4] = {__shfl_down_sync(0xffffffffu, a.x, 1), __shfl_down_sync(0xffffffffu, a.y, 1),
+                           __shfl_down_sync(0xffffffffu, a.z, 1), __shfl_down_sync(0xffffffffu, a.w, 1)};
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b[0], b[1], b[2], b[3]};
     if (shift & 8) {
 #pragma unroll
       for (int q = 0; q < 6; ++q) w[q] = w[q + 2];
@@ -244,14 +250,7 @@ __device__ __forceinline__ void dots(const WeightRow<ET, SHIFT> (&w)[kRows], con
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[r][c] = 0ull;
   }
-#pragma unroll(C == 1 ? 4 : 2)
-  for (int i = from + lane_id(); i < to; i += kWarp) {
-    uint4 wv[kRows];
-    uint64_t xv[C][kP];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) wv[r] = w[r].get(i);
-#pragma unroll
-    for (int c = 0; c < C; ++c) x[c].get(i, xv[c]);
+  auto add = [&](const uint4 (&wv)[kRows], const uint64_t (&xv)[C][kP]) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
 #pragma unroll
@@ -260,6 +259,46 @@ __device__ __forceinline__ void dots(const WeightRow<ET, SHIFT> (&w)[kRows], con
 #pragma unroll
         for (int c = 0; c < C; ++c) acc[r][c] = f2_fma(e, xv[c][q], acc[r][c]);
       }
+    }
+  };
+  if constexpr (SHIFT) {
+    // The last lane's piece serves its neighbour alone: it multiplies zeros.
+    constexpr int kUseful = kWarp - 1;
+    const int lane = lane_id();
+    uint4 raw[kRows], next[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) raw[r] = w[r].load(from + lane);
+    for (int i0 = from; i0 < to; i0 += kUseful) {
+      const int i = i0 + lane;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) next[r] = w[r].load(i + kUseful);
+      const bool mine = lane < kUseful && i < to;
+      uint64_t xv[C][kP];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        x[c].get(mine ? i : from, xv[c]);
+#pragma unroll
+        for (int q = 0; q < kP; ++q) xv[c][q] = mine ? xv[c][q] : 0ull;
+      }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        raw[r] = w[r].shifted(raw[r], i);
+        if (!mine) raw[r] = make_uint4(0, 0, 0, 0);
+      }
+      add(raw, xv);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) raw[r] = next[r];
+    }
+  } else {
+#pragma unroll(C == 1 ? 4 : 2)
+    for (int i = from + lane_id(); i < to; i += kWarp) {
+      uint4 wv[kRows];
+      uint64_t xv[C][kP];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) wv[r] = w[r].load(i);
+#pragma unroll
+      for (int c = 0; c < C; ++c) x[c].get(i, xv[c]);
+      add(wv, xv);
     }
   }
 #pragma unroll
