@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 2) down_rows_kernel(LayerArgs a, int
 //
 // Weights stream through a ring of shared-memory stages into the tensor cores:
 // tcgen05.mma with 128 weight rows as one operand and an expert's tokens (up
-// to 64 at a time) as the other, sums in tensor memory. With few tokens the
+// to 128 at a time) as the other, sums in tensor memory. With few tokens the
 // time is that of the weight bytes, so what matters is that copies are always
 // in flight: the copying warps run ahead across tiles, rows and experts, and
 // the work is cut so that each of the SMs streams the same number of bytes (an
@@ -524,7 +524,7 @@ constexpr int kMaxStages = 8;
 constexpr int kBlock = 64;       // elements of a block: the 128 bytes of a swizzled row
 constexpr int kRowBytes = 128;
 constexpr int kTileRows = 128;   // weight rows of a product
-constexpr int kMaxTokens = 64;   // of an expert at a time
+constexpr int kMaxTokens = 128;  // of an expert at a time (256 tokens of the Mixtral-8x7B shape: 788 us, with 64: 985)
 constexpr uint64_t kWaitNs = 2000000000;  // after which a wait gives up
 
 __device__ __forceinline__ uint32_t align_1k(uint32_t p) { return (p + 1023u) & ~1023u; }
@@ -1340,25 +1340,31 @@ template <bool SHIFT> int run_stream(const LayerArgs& a, float* parts, cudaStrea
   // 43 us and 3 instead of 78; 64 tokens, 1024 x 1024, 256 experts: 102 and 3
   // instead of 364). Stages of up to 64 KB, for the reason above: 48 tokens of
   // the Mixtral-8x22B shape 3.9 TB/s at 32 KB, 6.2 at 64.
+  // Where the sums of all tokens leave the ring too little, an expert's tokens
+  // take more passes first (64 at a time), then tiles get smaller.
   StreamShape d{};
-  d.tokens = round_to(a.T, 8) < cap ? round_to(a.T, 8) : cap;
-  d.cols = tmem_cols(4 * d.tokens);
+  const int d_tokens = round_to(a.T, 8) < cap ? round_to(a.T, 8) : cap;
   int64_t grid = 0;
   size_t d_smem = 0;
   bool fits = false;
-  for (int most = kTileRows; !fits && most >= 16; most /= 2) {  // sums of 256 tokens by 128 rows and the ring: too much for an SM
+  for (int most = kTileRows; !fits && most >= 16; most /= 2) {
     const int64_t need = (a.H + most - 1) / most;
     d.slices = need < sms ? (int)(sms / need) : 1;
     const int64_t tiles = sms / d.slices < a.H ? sms / d.slices : a.H, share = (a.H + tiles - 1) / tiles;
     d.rows = (int)(share < most ? share : most);
     grid = tiles * d.slices;
-    const int block = (round_to(d.rows, 8) + 2 * d.tokens) * kRowBytes;
-    // A product reads 128 rows from a block's start whatever the tile holds:
-    // behind the ring lie at least as many bytes of the CTA's memory.
-    d_smem = seg + sizeof(float) * a.T * d.rows;
-    if (d_smem < kTileRows * kRowBytes) d_smem = kTileRows * kRowBytes;
-    fits = cut_stages<SHIFT>(&d, block, SHIFT ? 3 : block < 65536 ? 65536 / block : 1, d_smem);
+    for (const int tokens : {d_tokens, d_tokens < 64 ? d_tokens : 64}) {
+      if (fits) break;
+      d.tokens = tokens;
+      const int block = (round_to(d.rows, 8) + 2 * d.tokens) * kRowBytes;
+      // A product reads 128 rows from a block's start whatever the tile holds:
+      // behind the ring lie at least as many bytes of the CTA's memory.
+      d_smem = seg + sizeof(float) * a.T * d.rows;
+      if (d_smem < kTileRows * kRowBytes) d_smem = kTileRows * kRowBytes;
+      fits = cut_stages<SHIFT>(&d, block, SHIFT ? 3 : block < 65536 ? 65536 / block : 1, d_smem);
+    }
   }
+  d.cols = tmem_cols(4 * d.tokens);
   if (!fits) return MOE_ERR_UNSUPPORTED;
   d_smem += (size_t)d.stages * d.stage_bytes + (SHIFT ? raw_bytes(d.blocks) : 0) + 1024;
 
