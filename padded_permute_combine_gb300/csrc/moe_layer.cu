@@ -147,15 +147,29 @@ __device__ __forceinline__ float warp_sum(float v) {
 // Products on the ordinary cores, in fp32, for fp32 layers, small ones and
 // rows of fewer than 64 elements: a warp takes four weight rows by four
 // tokens, its lanes 16 bytes of each, so that 8 loads feed 16 dot products
-// (packed in pairs). Weight rows may begin anywhere (SHIFT): a lane then loads
-// the aligned 16-byte piece that holds the first of its elements, an iteration
-// ahead, and shifts it together with the next lane's; the last lane's serves
-// its neighbour alone, and a row's last piece is masked (both pieces loaded by
-// every lane: 278 us instead of 251 for 16 tokens, fp32, 1501 x 2003, 4 of 16
-// experts). Loading such rows element by element reached a quarter of the rate
-// (the odd fp32 layer of 5 tokens, 1001 x 777: 26 and 68 us for the two
+// (packed in pairs). Weight rows may begin anywhere (SHIFT): a lane then takes
+// the aligned 16-byte piece that holds the first of its elements and shifts it
+// together with the next lane's; the last lane's serves its neighbour alone,
+// and a row's last piece is masked. These rows, and fp32 ones, come through
+// rings of asynchronous copies, four iterations ahead, since two CTAs an SM
+// have too few registers for as many loads (fp32, 1501 x 2003, 4 of 16
+// experts, 4 and 16 tokens: 131 and 251 us with loads one iteration ahead, 105
+// and 214 so, 110 and 222 six ahead; aligned 1504 x 2000, 4 tokens: 109 and
+// 101, but 16 tokens of 2048 x 1024, 2 of 8: 72 and 78). Aligned bf16 rows are
+// loaded directly: small layers have few iterations (one token 1024 x 2048:
+// 15.8 us, with rings 16.9). Loading unaligned rows element by element reached
+// a quarter of the rate (5 tokens fp32, 1001 x 777: 26 and 68 us for the two
 // kernels). The tokens' rows are aligned, x in the workspace where it is not.
 
+// 16 bytes from global to shared memory, not through L1; zeros when !in (src is not read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+  return v;
+}
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / kWarp;
 constexpr int kRows = 4;
@@ -187,16 +201,13 @@ template <typename ET, bool SHIFT> struct WeightRow {
     len = (int)n;
     last = (int)((shift + n * Elem<ET>::kBytes - 1) / 16);
   }
-  // The aligned piece i, zeros past the row's last.
-  __device__ __forceinline__ uint4 load(int i) const {
-    if constexpr (!SHIFT) return __ldg(p + i);
-    return i <= last ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
+  // The aligned piece i to shared memory, where the row has it.
+  __device__ __forceinline__ void fetch(uint32_t dst, int i) const {
+    if (i <= last) copy16(dst, p + i, true);
   }
-  // The elements of piece i from it and the next lane's, zeros past the row's end.
-  __device__ __forceinline__ uint4 shifted(const uint4& a, int i) const {
-    const uint32_t b[4] = {__shfl_down_sync(0xffffffffu, a.x, 1), __shfl_down_sync(0xffffffffu, a.y, 1),
-                           __shfl_down_sync(0xffffffffu, a.z, 1), __shfl_down_sync(0xffffffffu, a.w, 1)};
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b[0], b[1], b[2], b[3]};
+  // The elements of piece i from it and the one after it, zeros past the row's end.
+  __device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int i) const {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     if (shift & 8) {
 #pragma unroll
       for (int q = 0; q < 6; ++q) w[q] = w[q + 2];
@@ -239,11 +250,20 @@ template <typename ET, typename XT> struct TokenRow {
   }
 };
 
-// Dot products of kRows weight rows with C tokens over pieces [from, to): this lane's part.
+// A warp's ring in shared memory: kDepth iterations of kRows pieces a lane.
+constexpr int kDepth = 4;
+constexpr int kWarpRing = kDepth * kRows * kWarp * 16;
+template <typename ET, bool SHIFT> constexpr bool kRing = SHIFT || Elem<ET>::kBytes == 4;
+template <typename ET, bool SHIFT> constexpr int kRowsRing = kRing<ET, SHIFT> ? kWarps * kWarpRing : 0;
+
+// Dot products of kRows weight rows with C tokens over pieces [from, to): this
+// lane's part. With SHIFT the last lane's piece serves its neighbour alone.
 template <int C, typename ET, typename XT, bool SHIFT>
 __device__ __forceinline__ void dots(const WeightRow<ET, SHIFT> (&w)[kRows], const TokenRow<ET, XT> (&x)[C], int from, int to,
-                                     float (&out)[kRows][C]) {
-  constexpr int kP = WeightRow<ET, SHIFT>::kE / 2;
+                                     uint32_t rings, float (&out)[kRows][C]) {
+  constexpr int kP = WeightRow<ET, SHIFT>::kE / 2, kStep = SHIFT ? kWarp - 1 : kWarp;
+  const int lane = lane_id();
+  const uint32_t ring = rings + threadIdx.x / kWarp * kWarpRing + lane * 16;
   uint64_t acc[kRows][C];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
@@ -261,18 +281,31 @@ __device__ __forceinline__ void dots(const WeightRow<ET, SHIFT> (&w)[kRows], con
       }
     }
   };
-  if constexpr (SHIFT) {
-    // The last lane's piece serves its neighbour alone: it multiplies zeros.
-    constexpr int kUseful = kWarp - 1;
-    const int lane = lane_id();
-    uint4 raw[kRows], next[kRows];
+  if constexpr (!kRing<ET, SHIFT>) {
+#pragma unroll(C == 1 ? 4 : 2)
+    for (int i = from + lane; i < to; i += kWarp) {
+      uint4 wv[kRows];
+      uint64_t xv[C][kP];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) raw[r] = w[r].load(from + lane);
-    for (int i0 = from; i0 < to; i0 += kUseful) {
+      for (int r = 0; r < kRows; ++r) wv[r] = __ldg(w[r].p + i);
+#pragma unroll
+      for (int c = 0; c < C; ++c) x[c].get(i, xv[c]);
+      add(wv, xv);
+    }
+  } else {
+    auto fetch = [&](int slot, int i0) {
+      if (i0 < to) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) w[r].fetch(ring + (slot * kRows + r) * (kWarp * 16), i0 + lane);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) fetch(d, from + d * kStep);
+    int slot = 0;
+    for (int i0 = from; i0 < to; i0 += kStep) {
       const int i = i0 + lane;
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) next[r] = w[r].load(i + kUseful);
-      const bool mine = lane < kUseful && i < to;
+      const bool mine = lane < kStep && i < to;
       uint64_t xv[C][kP];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -280,24 +313,18 @@ __device__ __forceinline__ void dots(const WeightRow<ET, SHIFT> (&w)[kRows], con
 #pragma unroll
         for (int q = 0; q < kP; ++q) xv[c][q] = mine ? xv[c][q] : 0ull;
       }
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+      __syncwarp();
+      uint4 wv[kRows];
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
-        raw[r] = w[r].shifted(raw[r], i);
-        if (!mine) raw[r] = make_uint4(0, 0, 0, 0);
+        const uint32_t at = ring + (slot * kRows + r) * (kWarp * 16);
+        wv[r] = make_uint4(0, 0, 0, 0);
+        if (mine) wv[r] = SHIFT ? w[r].shifted(ld_shared16(at), ld_shared16(at + 16), i) : ld_shared16(at);
       }
-      add(raw, xv);
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) raw[r] = next[r];
-    }
-  } else {
-#pragma unroll(C == 1 ? 4 : 2)
-    for (int i = from + lane_id(); i < to; i += kWarp) {
-      uint4 wv[kRows];
-      uint64_t xv[C][kP];
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) wv[r] = w[r].load(i);
-#pragma unroll
-      for (int c = 0; c < C; ++c) x[c].get(i, xv[c]);
+      __syncwarp();
+      fetch(slot, i0 + kDepth * kStep);
+      slot = slot + 1 == kDepth ? 0 : slot + 1;
       add(wv, xv);
     }
   }
@@ -324,6 +351,7 @@ template <typename ET, bool SHIFT>
 __global__ void __launch_bounds__(kThreads)
     router_rows_kernel(const ET* __restrict__ x, int64_t x_ld, const ET* __restrict__ router, int64_t H, int32_t T, int32_t E,
                        float* __restrict__ logits) {
+  extern __shared__ __align__(16) int32_t smem[];
   __shared__ float part[kWarps][kRows * kCols];
   await_previous_kernel();
   allow_next_kernel();  // the gating, whose few CTAs then wait in place
@@ -339,7 +367,7 @@ __global__ void __launch_bounds__(kThreads)
   const int pieces = (int)((H + w[0].kE - 1) / w[0].kE);
   const int per = ((pieces + kWarps - 1) / kWarps + kWarp - 1) / kWarp * kWarp;
   float acc[kRows][kCols];
-  dots(w, xr, warp * per, (warp + 1) * per < pieces ? (warp + 1) * per : pieces, acc);
+  dots(w, xr, warp * per, (warp + 1) * per < pieces ? (warp + 1) * per : pieces, smem_u32(smem), acc);
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
 #pragma unroll
@@ -361,9 +389,10 @@ __global__ void __launch_bounds__(kThreads)
 // A warp takes the gate and up rows of two f's of one expert, for all its tokens.
 template <typename ET, bool SHIFT>
 __global__ void __launch_bounds__(kThreads, 2) gate_up_rows_kernel(LayerArgs a, const ET* __restrict__ x, int64_t x_ld, int64_t h_ld) {
-  extern __shared__ int32_t smem[];
+  extern __shared__ __align__(16) int32_t smem[];
+  int32_t* const seg = smem + kRowsRing<ET, SHIFT> / sizeof(int32_t);
   await_previous_kernel();
-  const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, a.status, smem);
+  const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, a.status, seg);
   const int lane = lane_id();
   const int64_t couples = (a.F + 1) / 2;
   const int pieces = (int)((a.H + WeightRow<ET, SHIFT>::kE - 1) / WeightRow<ET, SHIFT>::kE);
@@ -382,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 2) gate_up_rows_kernel(LayerArgs a, 
 #pragma unroll
       for (int c = 0; c < C; ++c) xr[c].p = reinterpret_cast<const char*>(x + s.token[i0 + c < last ? i0 + c : last] * x_ld);
       float acc[kRows][C];
-      dots(w, xr, 0, pieces, acc);
+      dots(w, xr, 0, pieces, smem_u32(smem), acc);
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
 #pragma unroll
@@ -416,11 +445,12 @@ __global__ void __launch_bounds__(kThreads, 2) gate_up_rows_kernel(LayerArgs a, 
 // in the order of its slots.
 template <typename ET, bool SHIFT>
 __global__ void __launch_bounds__(kThreads, 2) down_rows_kernel(LayerArgs a, int64_t h_ld) {
-  extern __shared__ int32_t smem[];
+  extern __shared__ __align__(16) int32_t smem[];
+  int32_t* const seg = smem + kRowsRing<ET, SHIFT> / sizeof(int32_t);
   await_previous_kernel();
-  const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, nullptr, smem);
+  const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, nullptr, seg);
   const int lane = lane_id(), warp = threadIdx.x / kWarp;
-  int32_t* place = smem + segments_bytes(a.n, a.E) / sizeof(int32_t);  // [n]: of an assignment, -1 without
+  int32_t* place = seg + segments_bytes(a.n, a.E) / sizeof(int32_t);  // [n]: of an assignment, -1 without
   float* part = reinterpret_cast<float*>(place + a.n);                 // [slices][n][kRows]
   for (int i = threadIdx.x; i < a.n; i += kThreads) place[i] = -1;
   __syncthreads();
@@ -443,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 2) down_rows_kernel(LayerArgs a, int
 #pragma unroll
         for (int c = 0; c < C; ++c) hr[c].p = reinterpret_cast<const char*>(a.h + (i0 + c < last ? i0 + c : last) * h_ld);
         float acc[kRows][C];
-        dots(w, hr, slice * per, (slice + 1) * per < pieces ? (slice + 1) * per : pieces, acc);
+        dots(w, hr, slice * per, (slice + 1) * per < pieces ? (slice + 1) * per : pieces, smem_u32(smem), acc);
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
 #pragma unroll
@@ -548,17 +578,8 @@ __device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
-// 16 bytes from global to shared memory, not through L1; zeros when !in (src is not read then).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ void st_shared16(uint32_t dst, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared16(uint32_t src) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
-  return v;
 }
 // The thread's arrival on the barrier, once all its copies so far have landed.
 __device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
@@ -1231,22 +1252,25 @@ int64_t padded_row(int64_t n) { return (n + 7) / 8 * 8; }
 template <typename ET, bool SHIFT>
 int run_router(const LayerArgs& a, const ET* x, int64_t x_ld, const void* router, float* logits, int32_t mode,
                int32_t normalize, int32_t* top_expert, float* weights, cudaStream_t s) {
-  launch(router_rows_kernel<ET, SHIFT>, dim3((unsigned)((a.E + kRows - 1) / kRows), (unsigned)((a.T + kCols - 1) / kCols)),
-         kThreads, 0, s, x, x_ld, static_cast<const ET*>(router), a.H, a.T, a.E, logits);
+  static std::atomic<int> granted[64];
+  auto r = router_rows_kernel<ET, SHIFT>;
+  if (!allow_smem(r, kRowsRing<ET, SHIFT>, granted)) return MOE_ERR_CUDA;
+  launch(r, dim3((unsigned)((a.E + kRows - 1) / kRows), (unsigned)((a.T + kCols - 1) / kCols)), kThreads, kRowsRing<ET, SHIFT>, s, x, x_ld, static_cast<const ET*>(router), a.H, a.T, a.E, logits);
   return moe_topk_gating(logits, a.T, a.E, a.K, mode, normalize, top_expert, weights,
                          reinterpret_cast<moe_stream_t>(s));
 }
 
 template <typename ET, bool SHIFT> int run_rows(const LayerArgs& a, const ET* x, int64_t x_ld, cudaStream_t s) {
-  static std::atomic<int> granted[64];
-  const size_t seg = segments_bytes(a.n, a.E);
+  static std::atomic<int> granted_g[64], granted_d[64];
+  const size_t seg = kRowsRing<ET, SHIFT> + segments_bytes(a.n, a.E);
   const int64_t h_ld = padded_row(a.F), couples = (a.F + 1) / 2;
   auto g = gate_up_rows_kernel<ET, SHIFT>;
+  if (!allow_smem(g, (int)seg, granted_g)) return MOE_ERR_CUDA;
   launch(g, persistent_grid(g, kThreads, seg, ((a.n < a.E ? a.n : a.E) * couples + kWarps - 1) / kWarps), kThreads, seg, s, a, x,
          x_ld, h_ld);
   const size_t smem = seg + sizeof(int32_t) * a.n + sizeof(float) * kRows * a.n * (a.n <= kSliceChoices ? kWarps : 1);
   auto d = down_rows_kernel<ET, SHIFT>;
-  if (!allow_smem(d, (int)smem, granted)) return MOE_ERR_CUDA;
+  if (!allow_smem(d, (int)smem, granted_d)) return MOE_ERR_CUDA;
   launch(d, persistent_grid(d, kThreads, smem, (a.H + kRows - 1) / kRows), kThreads, smem, s, a, h_ld);
   return check_launch();
 }
