@@ -627,6 +627,208 @@ __global__ void __maxnreg__(NV == 2 ? 96 : 128) bwd_ring_kernel(BwdArgs a, int s
   }
 }
 
+// ------------------------------------------- packed rows off 16 bytes
+//
+// Rows that follow one another without a gap, of a length that 16 bytes do not
+// divide: eight of them together are a multiple of 16 bytes whatever their
+// length, so a CTA copies eight in at once (and dy's), works on them element
+// by element in shared memory, and copies the results out the same way. First
+// a warp takes a row, for its sums, then a thread takes columns, with their
+// weights and sums over rows in registers. CTAs overlap their copies with one
+// another, two of them at least on an SM. Element loads from global memory
+// have too few bytes in flight: forward and backward 96 and 157 us, 55 and 112
+// so (58441 x 1001 bf16). fp32 rows have twice the bytes and gain less: 49 and
+// 85 against 41 and 95 (29220 x 1001), 70 and 116 against 51 and 77 (100000 x
+// 257). Few rows want a CTA each: backward 8.6 against 9.0 at 600 x 1001 bf16,
+// 10.2 against 9.8 at 1216. One CTA an SM: backward 146 against 173 (14000 x
+// 4095 bf16).
+
+constexpr int kChunk = 8;  // rows
+constexpr int kChunkThreads = kChunk * kWarp;
+constexpr int kChunkCols = 16;  // columns of a thread at most
+
+template <typename ET> __device__ __forceinline__ float to_float(ET v) { return static_cast<float>(v); }
+template <typename ET> __device__ __forceinline__ ET from_float(float v);
+template <> __device__ __forceinline__ float from_float<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// The elements of n that fill whole 16 bytes.
+template <typename ET> __device__ __forceinline__ int whole16(int n) { return n / Lanes<16, ET>::kElems * Lanes<16, ET>::kElems; }
+
+template <typename ET, typename WT, int NC> __global__ void __launch_bounds__(kChunkThreads) fwd_chunk_kernel(FwdArgs a) {
+  extern __shared__ __align__(128) unsigned char dyn[];
+  __shared__ uint64_t bar;
+  __shared__ float2 stat[kChunk];
+  ET* const sm = reinterpret_cast<ET*>(dyn);
+  const int t = threadIdx.x, lane = lane_id(), warp = t / kWarp, H = (int)a.H;
+  if (t == 0) {
+    mbar_init(smem_u32(&bar));
+    fence_mbarrier_init();
+  }
+  await_previous_kernel();
+  __syncthreads();
+  float w[NC], b[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    const int c = t + j * kChunkThreads;
+    w[j] = a.weight != nullptr && c < H ? load1<WT>(a.weight, c) : 1.0f;
+    b[j] = a.bias != nullptr && c < H ? load1<WT>(a.bias, c) : 0.0f;
+  }
+  const float inv_h = 1.0f / (float)H;
+  uint32_t parity = 0;
+  bool ok = true;
+  for (int64_t row = (int64_t)blockIdx.x * kChunk; row < a.rows; row += (int64_t)gridDim.x * kChunk) {
+    const int rows = a.rows - row < kChunk ? (int)(a.rows - row) : kChunk, n = rows * H, m = whole16<ET>(n);
+    const ET* x = static_cast<const ET*>(a.x) + row * H;
+    if (t == 0) {
+      bulk_wait_all();  // the last results have left shared memory
+      if (ok) bulk_load(smem_u32(dyn), x, (uint32_t)(m * sizeof(ET)), smem_u32(&bar));
+    }
+    // Bounded; a copy that does not land gets a second wait, then NaN is written.
+    ok = ok && (mbar_wait(smem_u32(&bar), parity) || (mbar_wait(smem_u32(&bar), parity), false));
+    parity ^= 1;
+    if (m < n) {
+      if (t < n - m) sm[m + t] = x[m + t];
+      __syncthreads();
+    }
+    if (warp < rows) {
+      const ET* r = sm + warp * H;
+      float s[1] = {0.0f}, d[1] = {0.0f};
+#pragma unroll 8
+      for (int c = lane; c < H; c += kWarp) s[0] += to_float(r[c]);
+      lane_sum<1, kWarp>(s);
+      const float mean = s[0] * inv_h;
+#pragma unroll 8
+      for (int c = lane; c < H; c += kWarp) {
+        const float e = to_float(r[c]) - mean;
+        d[0] = fmaf(e, e, d[0]);
+      }
+      lane_sum<1, kWarp>(d);
+      const float rstd = ok ? rsqrtf(d[0] * inv_h + a.eps) : __int_as_float(0x7fffffff);
+      if (lane == 0) {
+        stat[warp] = make_float2(mean, rstd);
+        if (a.mean != nullptr) a.mean[row + warp] = mean;
+        if (a.rstd != nullptr) a.rstd[row + warp] = rstd;
+      }
+    }
+    __syncthreads();
+    for (int r = 0; r < rows; ++r) {
+      const float2 st = stat[r];
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const int c = t + j * kChunkThreads;
+        if (c < H) sm[r * H + c] = from_float<ET>(fmaf((to_float(sm[r * H + c]) - st.x) * st.y, w[j], b[j]));
+      }
+    }
+    fence_async_shared();
+    __syncthreads();
+    ET* y = static_cast<ET*>(a.y) + row * H;
+    if (t == 0) {
+      bulk_store(y, smem_u32(dyn), (uint32_t)(m * sizeof(ET)));
+      bulk_commit();
+    }
+    if (t < n - m) y[m + t] = sm[m + t];
+  }
+  if (t == 0) bulk_wait_all();
+}
+
+template <typename ET, typename WT, int NC> __global__ void __launch_bounds__(kChunkThreads) bwd_chunk_kernel(BwdArgs a) {
+  extern __shared__ __align__(128) unsigned char dyn[];
+  __shared__ uint64_t bar;
+  __shared__ float4 stat[kChunk];
+  const int t = threadIdx.x, lane = lane_id(), warp = t / kWarp, H = (int)a.H;
+  ET *const sx = reinterpret_cast<ET*>(dyn), *const sd = sx + kChunk * H;
+  if (t == 0) {
+    mbar_init(smem_u32(&bar));
+    fence_mbarrier_init();
+  }
+  await_previous_kernel();
+  __syncthreads();
+  float w[NC], aw[NC], ab[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    const int c = t + j * kChunkThreads;
+    w[j] = a.weight != nullptr && c < H ? load1<WT>(a.weight, c) : 1.0f;
+    aw[j] = ab[j] = 0.0f;
+  }
+  const float inv_h = 1.0f / (float)H;
+  uint32_t parity = 0;
+  bool ok = true;
+  for (int64_t row = (int64_t)blockIdx.x * kChunk; row < a.rows; row += (int64_t)gridDim.x * kChunk) {
+    const int rows = a.rows - row < kChunk ? (int)(a.rows - row) : kChunk, n = rows * H, m = whole16<ET>(n);
+    const ET *x = static_cast<const ET*>(a.x) + row * H, *dy = static_cast<const ET*>(a.dy) + row * H;
+    if (t == 0) {
+      bulk_wait_all();
+      const uint32_t bytes = (uint32_t)(m * sizeof(ET)), at = smem_u32(&bar);
+      if (ok) {
+        mbar_expect(at, 2 * bytes);
+        bulk_copy_in(smem_u32(sx), x, bytes, at);
+        bulk_copy_in(smem_u32(sd), dy, bytes, at);
+      }
+    }
+    float mean = 0.0f, rstd = 0.0f;
+    if (warp < rows) {
+      mean = __ldg(a.mean + row + warp);
+      rstd = __ldg(a.rstd + row + warp);
+    }
+    ok = ok && (mbar_wait(smem_u32(&bar), parity) || (mbar_wait(smem_u32(&bar), parity), false));
+    parity ^= 1;
+    if (m < n) {
+      if (t < n - m) {
+        sx[m + t] = x[m + t];
+        sd[m + t] = dy[m + t];
+      }
+      __syncthreads();
+    }
+    if (warp < rows) {
+      const ET *rx = sx + warp * H, *rd = sd + warp * H;
+      float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 8
+      for (int c = lane; c < H; c += kWarp) {
+        const float v = to_float(rd[c]) * (a.weight != nullptr ? load1<WT>(a.weight, c) : 1.0f);
+        s0 += v;
+        s1 = fmaf(v, (to_float(rx[c]) - mean) * rstd, s1);
+      }
+      warp_sum2(s0, s1);
+      if (lane == 0) stat[warp] = make_float4(mean, ok ? rstd : __int_as_float(0x7fffffff), s0 * inv_h, -s1 * inv_h);
+    }
+    __syncthreads();
+    for (int r = 0; r < rows; ++r) {
+      const float4 st = stat[r];
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const int c = t + j * kChunkThreads;
+        if (c < H) {
+          const float dyv = to_float(sd[r * H + c]), xhat = (to_float(sx[r * H + c]) - st.x) * st.y;
+          aw[j] = fmaf(dyv, xhat, aw[j]);
+          ab[j] += ok ? dyv : __int_as_float(0x7fffffff);
+          sx[r * H + c] = from_float<ET>(fmaf(xhat, st.w, fmaf(dyv, w[j], -st.z)) * st.y);
+        }
+      }
+    }
+    fence_async_shared();
+    __syncthreads();
+    ET* dx = static_cast<ET*>(a.dx) + row * H;
+    if (t == 0) {
+      bulk_store(dx, smem_u32(sx), (uint32_t)(m * sizeof(ET)));
+      bulk_commit();
+    }
+    if (t < n - m) dx[m + t] = sx[m + t];
+  }
+  if (t == 0) bulk_wait_all();
+  if (a.partial == nullptr) return;
+  float* pw = a.partial + (int64_t)blockIdx.x * H;
+  float* pb = pw + (int64_t)gridDim.x * H;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    const int c = t + j * kChunkThreads;
+    if (c < H) {
+      pw[c] = aw[j];
+      pb[c] = ab[j];
+    }
+  }
+}
+
 // Rows of any length, one CTA each: a pass for the mean, one for the variance, one to write.
 template <typename ET, typename WT> __global__ void __launch_bounds__(512) fwd_long_kernel(FwdArgs a) {
   __shared__ float red[2 * kWarp];
@@ -775,6 +977,42 @@ template <typename Kernel> bool allow_smem(Kernel k, int bytes, std::atomic<int>
   return true;
 }
 
+// Whether the chunk kernels take the rows: packed, enough of them for every SM,
+// and `arrays` chunks in at most `most` bytes of shared memory.
+template <typename ET> bool chunks_ok(int64_t H, int64_t rows, int arrays, int64_t most, const int64_t* strides, const void* const* ptrs) {
+  bool ok = H > kChunkThreads && H <= kChunkCols * kChunkThreads && arrays * kChunk * H * Elem<ET>::kBytes <= most &&
+            rows >= kChunk * (int64_t)num_sms();
+  for (int i = 0; i < arrays; ++i) ok = ok && strides[i] == H;
+  for (int i = 0; i <= arrays; ++i) ok = ok && aligned(ptrs[i], 16);
+  return ok;
+}
+
+template <typename ET, typename WT, int NC> int go_fwd_chunk(const FwdArgs& a, cudaStream_t s) {
+  if constexpr (NC > 4) {
+    if (a.H <= NC / 2 * kChunkThreads) return go_fwd_chunk<ET, WT, NC / 2>(a, s);
+  }
+  static std::atomic<int> granted[64];
+  auto k = fwd_chunk_kernel<ET, WT, NC>;
+  const size_t smem = (size_t)kChunk * a.H * Elem<ET>::kBytes;
+  if (!allow_smem(k, (int)smem, granted)) return MOE_ERR_CUDA;
+  launch(k, persistent_grid(k, kChunkThreads, smem, (a.rows + kChunk - 1) / kChunk), kChunkThreads, smem, s, a);
+  return check_launch();
+}
+
+template <typename ET, typename WT, int NC> int go_bwd_chunk(const BwdArgs& a, int* parts, cudaStream_t s) {
+  if constexpr (NC > 4) {
+    if (a.H <= NC / 2 * kChunkThreads) return go_bwd_chunk<ET, WT, NC / 2>(a, parts, s);
+  }
+  static std::atomic<int> granted[64];
+  auto k = bwd_chunk_kernel<ET, WT, NC>;
+  const size_t smem = 2 * (size_t)kChunk * a.H * Elem<ET>::kBytes;
+  if (!allow_smem(k, (int)smem, granted)) return MOE_ERR_CUDA;
+  const int64_t most = bwd_parts(a.rows, a.H), work = (a.rows + kChunk - 1) / kChunk;
+  *parts = persistent_grid(k, kChunkThreads, smem, work < most ? work : most);
+  launch(k, *parts, kChunkThreads, smem, s, a);
+  return check_launch();
+}
+
 template <int VB, typename ET, typename WT, int NV, int LPR, int DEPTH, int MAXT = kMaxThreads>
 int go_fwd(const FwdArgs& a, cudaStream_t s) {
   const int threads = LPR ? kRowWarps * kWarp : cta_threads(a.H / Lanes<VB, ET>::kElems, NV);
@@ -898,6 +1136,7 @@ template <typename ET, typename WT> int run_fwd(FwdArgs a, cudaStream_t s) {
   constexpr int kCols = 16 / Elem<ET>::kBytes * Elem<WT>::kBytes;  // of the weights beside 16 bytes of a row
   if (rows_by_16<ET>(a.H, &a.x_stride, 1, ptrs, 2) && aligned(a.weight, kCols) && aligned(a.bias, kCols))
     return dispatch_fwd<16, ET, WT>(a, s);
+  if (chunks_ok<ET>(a.H, a.rows, 1, kRingSm / 2, &a.x_stride, ptrs)) return go_fwd_chunk<ET, WT, kChunkCols>(a, s);
   return dispatch_fwd<Elem<ET>::kBytes, ET, WT>(a, s);
 }
 
@@ -907,8 +1146,12 @@ template <typename ET, typename WT> int run_bwd(BwdArgs a, void* dweight, void* 
   if (a.rows > 0) {
     const int64_t strides[] = {a.x_stride, a.dy_stride};
     const void* ptrs[] = {a.x, a.dy, a.dx};
-    rc = rows_by_16<ET>(a.H, strides, 2, ptrs, 3) && aligned(a.weight, 16 / Elem<ET>::kBytes * Elem<WT>::kBytes) ? dispatch_bwd<16, ET, WT>(a, &parts, s)
-                                                  : dispatch_bwd<Elem<ET>::kBytes, ET, WT>(a, &parts, s);
+    if (rows_by_16<ET>(a.H, strides, 2, ptrs, 3) && aligned(a.weight, 16 / Elem<ET>::kBytes * Elem<WT>::kBytes))
+      rc = dispatch_bwd<16, ET, WT>(a, &parts, s);
+    else if (chunks_ok<ET>(a.H, a.rows, 2, Elem<ET>::kBytes == 2 ? kRingSm / 2 : kRingSm / 6, strides, ptrs))
+      rc = go_bwd_chunk<ET, WT, kChunkCols>(a, &parts, s);
+    else
+      rc = dispatch_bwd<Elem<ET>::kBytes, ET, WT>(a, &parts, s);
   }
   if (rc != MOE_OK || (dweight == nullptr && dbias == nullptr)) return rc;
   launch(cols_kernel<WT>, dim3((unsigned)((a.H + kWarp - 1) / kWarp), 2), 512, 0, s, (const float*)a.partial, parts,

@@ -484,6 +484,36 @@ def test_layer_norm_unaligned_rows(H, dtype):
     check(db, dy.double().sum(0), 64 * U * dy.double().abs().sum(0), "db")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,H", [(1216, 257), (1217, 1001), (1301, 303), (2439, 511), (1300, 2047), (1223, 4095), (4001, 999)])
+def test_layer_norm_many_packed_unaligned_rows(M, H, dtype):
+    """Rows without gaps, eight of which are a multiple of 16 bytes; the last few short of that, in place as well."""
+    x, dy = randn((M, H), M + H, dtype), randn((M, H), M, dtype)
+    w, b = 1 + randn((H,), 3, scale=0.1), randn((H,), 4)
+    guard = torch.full((2, M * H + 32), 7.0, dtype=dtype, device=DEV)
+    lo = 16 // x.element_size()
+    y, dx = guard[0, lo:lo + M * H].view(M, H), guard.reshape(-1)[-M * H - lo:-lo].view(M, H)
+    dx = dx if dx.data_ptr() % 16 == 0 else torch.empty_like(x)
+    _, mean, rstd = p.moe_layer_norm_fwd(x, w, b, out=y)
+    _, dw, db = p.moe_layer_norm_bwd(dy, x, w, mean, rstd, out=dx)
+    assert bool((guard[0, :lo] == 7).all()) and bool((guard[0, lo + M * H:] == 7).all())
+    ref, rmean, rrstd, xhat = norm_ref(x, w, b, 1e-5)
+    mag = x.double().abs().mean(1)[:, None]
+    check(mean, rmean, ROW * mag[:, 0], "mean")
+    check(y, ref, 3 * ROW * (mag * rrstd[:, None] + xhat.abs() + 1) * w.double().abs() + 4 * U * (ref.abs() + b.double().abs())
+          + type_round(ref, dtype), "y")
+    xh = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    v = dy.double() * w.double()
+    c0, c1 = v.mean(1, keepdim=True), (v * xh).mean(1, keepdim=True)
+    ref = rstd.double()[:, None] * (v - c0 - xh * c1)
+    size = rstd.double()[:, None] * (v.abs() + v.abs().mean(1, keepdim=True) + xh.abs() * (v * xh).abs().mean(1, keepdim=True))
+    check(dx, ref, 3 * ROW * size + type_round(ref, dtype), "dx")
+    check(dw, (dy.double() * xh).sum(0), 64 * U * (dy.double() * xh).abs().sum(0) + 16 * U * dy.double().abs().sum(0), "dw")
+    check(db, dy.double().sum(0), 64 * U * dy.double().abs().sum(0), "db")
+    again = p.moe_layer_norm_fwd(x, w, b, out=x)[0]
+    assert torch.equal(again, y)
+
+
 def test_layer_norm_special_rows():
     x = randn((6, 512), 1)
     clean = p.moe_layer_norm_fwd(x)[0]
