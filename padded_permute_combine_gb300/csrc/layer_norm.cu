@@ -900,12 +900,16 @@ template <typename ET> __global__ void __launch_bounds__(256) bwd_long_cols_kern
   a.partial[((int64_t)gridDim.y + blockIdx.y) * a.H + c] = sb;
 }
 
-// Adds the CTAs' partial sums: 32 columns per CTA, its 16 warps each a share
-// of the parts. blockIdx.y: 0 dweight, 1 dbias.
-template <typename WT>
-__global__ void __launch_bounds__(512) cols_kernel(const float* __restrict__ partial, int parts, int64_t H,
-                                                   WT* dweight, WT* dbias) {
-  __shared__ float red[16][kWarp];
+// Adds the CTAs' partial sums: 32 columns per CTA, its NW warps each a share
+// of the parts. blockIdx.y: 0 dweight, 1 dbias. Few columns make few CTAs: 32
+// warps then, with ten loads ahead (the whole backward pass, 1531 x 1001 fp32,
+// 9.2 us, with 16 warps and four 10.4; 4000 x 1000 bf16 12.1 and 15.9), 16
+// where the columns alone fill the chip (8192 x 7168: 67.4, with 32 69.6).
+constexpr int64_t kFewCols = 2048;
+template <typename WT, int NW>
+__global__ void __launch_bounds__(NW * kWarp) cols_kernel(const float* __restrict__ partial, int parts, int64_t H,
+                                                          WT* dweight, WT* dbias) {
+  __shared__ float red[NW][kWarp];
   await_previous_kernel();
   WT* out = blockIdx.y == 0 ? dweight : dbias;
   if (out == nullptr) return;
@@ -914,15 +918,15 @@ __global__ void __launch_bounds__(512) cols_kernel(const float* __restrict__ par
   float s = 0.0f;
   if (c < H) {
     const float* p = partial + (int64_t)blockIdx.y * parts * H + c;
-#pragma unroll 4
-    for (int g = warp; g < parts; g += 16) s += __ldcg(p + (int64_t)g * H);
+#pragma unroll(NW == 32 ? 10 : 4)
+    for (int g = warp; g < parts; g += NW) s += __ldcg(p + (int64_t)g * H);
   }
   red[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < H) {
     float t = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) t += red[w][lane];
+    for (int w = 0; w < NW; ++w) t += red[w][lane];
     store1(out, c, t);
   }
 }
@@ -932,9 +936,12 @@ __global__ void __launch_bounds__(512) cols_kernel(const float* __restrict__ par
 constexpr int kMinParts = 304;    // CTAs of the backward pass, each with a row of partial column sums,
 constexpr int kMaxParts = 2432;   // more of them for shorter rows:
 constexpr int64_t kPartElems = (int64_t)304 * 8192;
+constexpr int64_t kPartRows = 4;  // rows of a CTA at least, where there are kMinParts of them (4000 x 1000 bf16: 12.0 us, with 1.6 rows each 16.4)
 
 int64_t bwd_parts(int64_t rows, int64_t H) {
   int64_t most = kPartElems / H;
+  const int64_t few = rows / kPartRows < kMinParts ? kMinParts : rows / kPartRows;
+  if (most > few) most = few;
   most = most < kMinParts ? kMinParts : (most > kMaxParts ? kMaxParts : most);
   return rows < most ? rows : most;
 }
@@ -1154,8 +1161,14 @@ template <typename ET, typename WT> int run_bwd(BwdArgs a, void* dweight, void* 
       rc = dispatch_bwd<Elem<ET>::kBytes, ET, WT>(a, &parts, s);
   }
   if (rc != MOE_OK || (dweight == nullptr && dbias == nullptr)) return rc;
-  launch(cols_kernel<WT>, dim3((unsigned)((a.H + kWarp - 1) / kWarp), 2), 512, 0, s, (const float*)a.partial, parts,
-         a.H, static_cast<WT*>(dweight), static_cast<WT*>(dbias));
+  const dim3 grid((unsigned)((a.H + kWarp - 1) / kWarp), 2);
+  auto go = [&](auto k, int threads) {
+    launch(k, grid, threads, 0, s, (const float*)a.partial, parts, a.H, static_cast<WT*>(dweight), static_cast<WT*>(dbias));
+  };
+  if (a.H <= kFewCols)
+    go(cols_kernel<WT, 32>, 32 * kWarp);
+  else
+    go(cols_kernel<WT, 16>, 16 * kWarp);
   return check_launch();
 }
 
