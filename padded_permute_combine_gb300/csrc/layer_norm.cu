@@ -11,8 +11,9 @@
 // thread owns the same columns in every row it meets, so the two sums over
 // rows live in its registers; each CTA writes one row of partial sums, and a
 // second launch adds those in a fixed order. The backward pass takes rows of up
-// to 32 KB through a ring in shared memory. Rows too long for the registers take kernels that read a row
-// again for each pass over it.
+// to 32 KB (fp32 50 KB) through a ring in shared memory. Packed rows that 16
+// bytes do not divide go through shared memory eight at a time. Rows too long
+// for the registers take kernels that read a row again for each pass over it.
 #include <math.h>
 
 #include <atomic>
@@ -422,9 +423,11 @@ __global__ void __launch_bounds__(LPR ? kRowWarps * kWarp : MAXT, LPR ? 3 : 1) b
 
 // ------------------------------------------- rows through shared memory
 //
-// The backward pass for rows of more than 512 bytes, up to 32 KB: two 16-byte
-// vectors of the row per thread, two consecutive rows at a time (above 16 KB
-// four vectors and one row of bf16), copied into a ring of slots
+// The backward pass for rows of more than 512 bytes, up to 32 KB of bf16 and 50
+// of fp32: two 16-byte vectors of the row per thread, two consecutive rows at a
+// time (four vectors and one row above 16 KB of bf16 and 32 of fp32, where a
+// second reading of the rows would follow: 2000 x 9000 fp32 55 us instead of
+// 111, 4000 x 12800 96 instead of 259), copied into a ring of slots
 // by bulk copies (one for both rows where they are adjacent). What that buys
 // over loads into registers: the copies ahead cost none (they read x and dy
 // from the slot again after the sums instead of keeping them), and one barrier
@@ -436,6 +439,9 @@ __global__ void __launch_bounds__(LPR ? kRowWarps * kWarp : MAXT, LPR ? 3 : 1) b
 // this way: 47 us instead of 43.)
 
 constexpr int kRingThreads = 512;
+// fp32 with four vectors a thread: up to 1024 threads, for rows of 32 to 50 KB.
+template <typename ET> __host__ __device__ constexpr int ring_registers(int nv) { return nv == 2 ? 96 : Elem<ET>::kBytes == 4 ? 64 : 128; }
+template <typename ET> constexpr int ring_threads(int nv) { return nv == 4 && Elem<ET>::kBytes == 4 ? 1024 : kRingThreads; }
 constexpr int kMaxSlots = 16;
 constexpr int kRingSm = 200 * 1024;  // shared memory of an SM for rings
 
@@ -479,7 +485,7 @@ __device__ __forceinline__ uint4 lds_vec(uint32_t p) {
 // NV vectors a thread, R rows at a time; KEEP: the weights stay in registers;
 // FULL: every thread has all its vectors.
 template <typename ET, typename WT, int NV, int R, bool KEEP, bool FULL>
-__global__ void __maxnreg__(NV == 2 ? 96 : 128) bwd_ring_kernel(BwdArgs a, int slots) {
+__global__ void __maxnreg__(ring_registers<ET>(NV)) bwd_ring_kernel(BwdArgs a, int slots) {
   using L = Lanes<16, ET>;
   constexpr int kE = L::kElems;
   using P = Pack<kE>;
@@ -954,9 +960,9 @@ struct RingShape {
   int threads, grid, slots;
   size_t smem;
 };
-bool ring_shape(int64_t vecs, int nv, int r, int registers, int64_t rows, int64_t most, RingShape* z) {
+bool ring_shape(int64_t vecs, int nv, int r, int registers, int threads, int64_t rows, int64_t most, RingShape* z) {
   z->threads = cta_threads(vecs, nv);
-  if (vecs <= kWarp || z->threads > kRingThreads) return false;
+  if (vecs <= kWarp || z->threads > threads) return false;
   int per_sm = 65536 / ((registers + 7) / 8 * 8) / z->threads;
   if (per_sm > 16) per_sm = 16;
   if (per_sm < 1) per_sm = 1;
@@ -1085,7 +1091,7 @@ int go_ring(const BwdArgs& a, int* parts, cudaStream_t s) {
     regs = f.numRegs;
     registers.store(regs, std::memory_order_relaxed);
   }
-  if (!ring_shape(vecs, NV, R, regs, a.rows, bwd_parts(a.rows, a.H), &z) ||
+  if (!ring_shape(vecs, NV, R, regs, ring_threads<ET>(NV), a.rows, bwd_parts(a.rows, a.H), &z) ||
       !allow_smem(k, (int)z.smem, granted))
     return MOE_ERR_CUDA;
   *parts = z.grid;
@@ -1104,6 +1110,7 @@ template <int VB, typename ET, typename WT> int dispatch_bwd(const BwdArgs& a, i
       if (vecs <= 4 * kRingThreads) return go_ring<ET, WT, 4, 1, false>(a, parts, s);
     } else {
       if (vecs <= 2 * kMaxThreads) return go_bwd<VB, ET, WT, 2, 0, 1>(a, parts, s);
+      if (vecs <= kRingSm / 64) return go_ring<ET, WT, 4, 1, false>(a, parts, s);  // two slots
     }
   } else {
     if (vecs <= 4 * kMaxThreads) return go_bwd<VB, ET, WT, 4, 0, 2>(a, parts, s);

@@ -485,9 +485,11 @@ def test_layer_norm_unaligned_rows(H, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("M,H", [(1216, 257), (1217, 1001), (1301, 303), (2439, 511), (1300, 2047), (1223, 4095), (4001, 999)])
-def test_layer_norm_many_packed_unaligned_rows(M, H, dtype):
-    """Rows without gaps, eight of which are a multiple of 16 bytes; the last few short of that, in place as well."""
+@pytest.mark.parametrize("M,H", [(1216, 257), (1217, 1001), (1301, 303), (2439, 511), (1300, 2047), (1223, 4095), (4001, 999),
+                                 (331, 8196), (331, 9000), (310, 12800), (200, 12804)])
+def test_layer_norm_many_packed_rows(M, H, dtype):
+    """Rows without gaps, eight of which are a multiple of 16 bytes; the last few short of that, in place as well; and
+    long rows, several to a CTA."""
     x, dy = randn((M, H), M + H, dtype), randn((M, H), M, dtype)
     w, b = 1 + randn((H,), 3, scale=0.1), randn((H,), 4)
     guard = torch.full((2, M * H + 32), 7.0, dtype=dtype, device=DEV)
