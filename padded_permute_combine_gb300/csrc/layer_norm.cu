@@ -939,6 +939,12 @@ __global__ void __launch_bounds__(NW * kWarp) cols_kernel(const float* __restric
 
 // ------------------------------------------------------------------ host
 
+// persistent_grid, without the question about occupancy where every SM gets one CTA at most.
+template <typename Kernel> int grid_for(Kernel k, int threads, size_t smem, int64_t work_ctas) {
+  if (work_ctas <= num_sms()) return work_ctas < 1 ? 1 : (int)work_ctas;
+  return persistent_grid(k, threads, smem, work_ctas);
+}
+
 constexpr int kMinParts = 304;    // CTAs of the backward pass, each with a row of partial column sums,
 constexpr int kMaxParts = 2432;   // more of them for shorter rows:
 constexpr int64_t kPartElems = (int64_t)304 * 8192;
@@ -1008,7 +1014,7 @@ template <typename ET, typename WT, int NC> int go_fwd_chunk(const FwdArgs& a, c
   auto k = fwd_chunk_kernel<ET, WT, NC>;
   const size_t smem = (size_t)kChunk * a.H * Elem<ET>::kBytes;
   if (!allow_smem(k, (int)smem, granted)) return MOE_ERR_CUDA;
-  launch(k, persistent_grid(k, kChunkThreads, smem, (a.rows + kChunk - 1) / kChunk), kChunkThreads, smem, s, a);
+  launch(k, grid_for(k, kChunkThreads, smem, (a.rows + kChunk - 1) / kChunk), kChunkThreads, smem, s, a);
   return check_launch();
 }
 
@@ -1021,7 +1027,7 @@ template <typename ET, typename WT, int NC> int go_bwd_chunk(const BwdArgs& a, i
   const size_t smem = 2 * (size_t)kChunk * a.H * Elem<ET>::kBytes;
   if (!allow_smem(k, (int)smem, granted)) return MOE_ERR_CUDA;
   const int64_t most = bwd_parts(a.rows, a.H), work = (a.rows + kChunk - 1) / kChunk;
-  *parts = persistent_grid(k, kChunkThreads, smem, work < most ? work : most);
+  *parts = grid_for(k, kChunkThreads, smem, work < most ? work : most);
   launch(k, *parts, kChunkThreads, smem, s, a);
   return check_launch();
 }
@@ -1031,7 +1037,7 @@ int go_fwd(const FwdArgs& a, cudaStream_t s) {
   const int threads = LPR ? kRowWarps * kWarp : cta_threads(a.H / Lanes<VB, ET>::kElems, NV);
   constexpr int kRows = LPR ? kRowWarps * (kWarp / (LPR ? LPR : 1)) : 1;
   auto go = [&](auto k) {
-    launch(k, persistent_grid(k, threads, 0, (a.rows + kRows - 1) / kRows), threads, 0, s, a);
+    launch(k, grid_for(k, threads, 0, (a.rows + kRows - 1) / kRows), threads, 0, s, a);
     return check_launch();
   };
   if constexpr (LPR == 0 && VB == 16 && MAXT == 256) {
@@ -1056,7 +1062,7 @@ template <int VB, typename ET, typename WT> int dispatch_fwd(const FwdArgs& a, c
     if (vecs <= 16 * kMaxThreads) return go_fwd<VB, ET, WT, 16, 0, 1>(a, s);
   }
   auto k = fwd_long_kernel<ET, WT>;
-  launch(k, persistent_grid(k, 512, 0, a.rows), 512, 0, s, a);
+  launch(k, grid_for(k, 512, 0, a.rows), 512, 0, s, a);
   return check_launch();
 }
 
@@ -1067,7 +1073,7 @@ int go_bwd(const BwdArgs& a, int* parts, cudaStream_t s) {
   const int64_t most = bwd_parts(a.rows, a.H), work = (a.rows + kRows - 1) / kRows;
   const size_t smem = LPR ? sizeof(float) * 2 * NV * LPR * Lanes<VB, ET>::kElems : 0;
   auto k = bwd_kernel<VB, ET, WT, NV, LPR, DEPTH, MAXT>;
-  *parts = persistent_grid(k, threads, smem, work < most ? work : most);
+  *parts = grid_for(k, threads, smem, work < most ? work : most);
   launch(k, *parts, threads, smem, s, a);
   return check_launch();
 }
@@ -1117,7 +1123,7 @@ template <int VB, typename ET, typename WT> int dispatch_bwd(const BwdArgs& a, i
     if (vecs <= 8 * kMaxThreads) return go_bwd<VB, ET, WT, 8, 0, 1>(a, parts, s);
   }
   auto k = bwd_long_kernel<ET, WT>;
-  launch(k, persistent_grid(k, 512, 0, a.rows), 512, 0, s, a);
+  launch(k, grid_for(k, 512, 0, a.rows), 512, 0, s, a);
   *parts = (int)(a.rows < 32 ? a.rows : 32);
   if (a.partial != nullptr)
     launch(bwd_long_cols_kernel<ET>, dim3((unsigned)((a.H + 255) / 256), (unsigned)*parts), 256, 0, s, a);

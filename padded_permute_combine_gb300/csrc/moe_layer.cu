@@ -1232,6 +1232,12 @@ __global__ void __launch_bounds__(kThreads)
 
 // ------------------------------------------------------------------ host
 
+// persistent_grid, without the question about occupancy where every SM gets one CTA at most.
+template <typename Kernel> int grid_for(Kernel k, int threads, size_t smem, int64_t work_ctas) {
+  if (work_ctas <= num_sms()) return work_ctas < 1 ? 1 : (int)work_ctas;
+  return persistent_grid(k, threads, smem, work_ctas);
+}
+
 // Raises a kernel's dynamic shared memory limit once per device.
 template <typename Kernel> bool allow_smem(Kernel k, int bytes, std::atomic<int>* granted) {
   int dev = 0;
@@ -1255,7 +1261,8 @@ int run_router(const LayerArgs& a, const ET* x, int64_t x_ld, const void* router
   static std::atomic<int> granted[64];
   auto r = router_rows_kernel<ET, SHIFT>;
   if (!allow_smem(r, kRowsRing<ET, SHIFT>, granted)) return MOE_ERR_CUDA;
-  launch(r, dim3((unsigned)((a.E + kRows - 1) / kRows), (unsigned)((a.T + kCols - 1) / kCols)), kThreads, kRowsRing<ET, SHIFT>, s, x, x_ld, static_cast<const ET*>(router), a.H, a.T, a.E, logits);
+  launch(r, dim3((unsigned)((a.E + kRows - 1) / kRows), (unsigned)((a.T + kCols - 1) / kCols)), kThreads, kRowsRing<ET, SHIFT>, s, x, x_ld,
+         static_cast<const ET*>(router), a.H, a.T, a.E, logits);
   return moe_topk_gating(logits, a.T, a.E, a.K, mode, normalize, top_expert, weights,
                          reinterpret_cast<moe_stream_t>(s));
 }
@@ -1266,12 +1273,12 @@ template <typename ET, bool SHIFT> int run_rows(const LayerArgs& a, const ET* x,
   const int64_t h_ld = padded_row(a.F), couples = (a.F + 1) / 2;
   auto g = gate_up_rows_kernel<ET, SHIFT>;
   if (!allow_smem(g, (int)seg, granted_g)) return MOE_ERR_CUDA;
-  launch(g, persistent_grid(g, kThreads, seg, ((a.n < a.E ? a.n : a.E) * couples + kWarps - 1) / kWarps), kThreads, seg, s, a, x,
+  launch(g, grid_for(g, kThreads, seg, ((a.n < a.E ? a.n : a.E) * couples + kWarps - 1) / kWarps), kThreads, seg, s, a, x,
          x_ld, h_ld);
   const size_t smem = seg + sizeof(int32_t) * a.n + sizeof(float) * kRows * a.n * (a.n <= kSliceChoices ? kWarps : 1);
   auto d = down_rows_kernel<ET, SHIFT>;
   if (!allow_smem(d, (int)smem, granted_d)) return MOE_ERR_CUDA;
-  launch(d, persistent_grid(d, kThreads, smem, (a.H + kRows - 1) / kRows), kThreads, smem, s, a, h_ld);
+  launch(d, grid_for(d, kThreads, smem, (a.H + kRows - 1) / kRows), kThreads, smem, s, a, h_ld);
   return check_launch();
 }
 
