@@ -135,7 +135,7 @@ def _link_calls(obj: str) -> None:
     """Linked to the libraries by the names under which torch and the loader have them in the process already."""
     tmp = CALLS + ".tmp%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python",
-           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", PKG, "-l:libmoe_route.so", "-Wl,-rpath,$ORIGIN"]
+           "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L", PKG, "-l:libmoe_route.so", "-Wl,-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), res.stderr))

@@ -948,7 +948,8 @@ template <typename Kernel> int grid_for(Kernel k, int threads, size_t smem, int6
 constexpr int kMinParts = 304;    // CTAs of the backward pass, each with a row of partial column sums,
 constexpr int kMaxParts = 2432;   // more of them for shorter rows:
 constexpr int64_t kPartElems = (int64_t)304 * 8192;
-constexpr int64_t kPartRows = 4;  // rows of a CTA at least, where there are kMinParts of them (4000 x 1000 bf16: 12.0 us, with 1.6 rows each 16.4)
+constexpr int64_t kPartRows = 4;  // rows of a CTA at least, where there are kMinParts of them (4000 x 1000 bf16:
+                                  // 12.0 us, with 1.6 rows each 16.4)
 
 int64_t bwd_parts(int64_t rows, int64_t H) {
   int64_t most = kPartElems / H;
