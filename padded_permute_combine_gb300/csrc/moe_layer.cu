@@ -1105,7 +1105,11 @@ __global__ void __launch_bounds__(kStreamThreads<SHIFT>)
   const Segments s = sort_choices(a.top_expert, a.n, a.E, a.K, nullptr, seg);
   tmem_fence_after();
   allow_next_kernel();
-  float* ysum = reinterpret_cast<float*>(seg + segments_bytes(a.n, a.E) / sizeof(int32_t));  // [T, nr]
+  // [T, z.rows]: with a stride that is the same for all of a CTA's tiles, each
+  // thread meets its own places alone, in every tile, and the warps that add the
+  // sums need no barrier between tiles (with a tile's own number of columns for
+  // a stride, the next tile's places are other warps' in the one before).
+  float* ysum = reinterpret_cast<float*>(seg + segments_bytes(a.n, a.E) / sizeof(int32_t));
   DownWalk w(s, a, z);
   const int block = round_to(z.rows, 8) * kRowBytes;
   bool ok = true;
@@ -1156,7 +1160,7 @@ __global__ void __launch_bounds__(kStreamThreads<SHIFT>)
     for (int64_t r0 = a.H * tile_id / tiles; r0 < r_end; r0 += z.rows) {
       const int nr = r_end - r0 < z.rows ? (int)(r_end - r0) : z.rows;
       if (row < nr)
-        for (int t = 0; t < a.T; ++t) ysum[t * nr + row] = 0.0f;
+        for (int t = 0; t < a.T; ++t) ysum[t * z.rows + row] = 0.0f;
       for (; w.more() && w.r0 == r0; w.next_pass(), d.advance()) {
         ok = wait_bar(ok, &sh.sums_full[d.i], d.parity, a.status);
         tmem_fence_after();
@@ -1170,7 +1174,7 @@ __global__ void __launch_bounds__(kStreamThreads<SHIFT>)
             tmem_load8(lo, at + n + c0);
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-              if (row < nr && c0 + c < w.ntok) ysum[s.token[w.i0 + c0 + c] * nr + row] += hi[c] + lo[c];
+              if (row < nr && c0 + c < w.ntok) ysum[s.token[w.i0 + c0 + c] * z.rows + row] += hi[c] + lo[c];
           }
         }
         tmem_fence_before();
@@ -1179,10 +1183,10 @@ __global__ void __launch_bounds__(kStreamThreads<SHIFT>)
       }
       if (row < nr && z.slices == 1) {
         __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + r0 + row;
-        for (int t = 0; t < a.T; ++t) y[t * a.H] = __float2bfloat16_rn(ysum[t * nr + row]);
+        for (int t = 0; t < a.T; ++t) y[t * a.H] = __float2bfloat16_rn(ysum[t * z.rows + row]);
       } else if (row < nr && z.slices > 2) {
         float* part = p.parts + blockIdx.x % z.slices * p.parts_ld + r0 + row;
-        for (int t = 0; t < a.T; ++t) part[t * a.H] = ysum[t * nr + row];
+        for (int t = 0; t < a.T; ++t) part[t * a.H] = ysum[t * z.rows + row];
       }
     }
   }
@@ -1200,9 +1204,10 @@ __global__ void __launch_bounds__(kStreamThreads<SHIFT>)
     const int nr = (int)(a.H * (tile_id + 1) / tiles - r0), all = a.T * nr, slice = blockIdx.x % z.slices;
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + r0;
     for (int i = all * slice / z.slices + threadIdx.x; i < all * (slice + 1) / z.slices; i += kStreamThreads<SHIFT>) {
+      const int t = i / nr, row = i % nr;
       float sum = 0.0f;
-      for (int k = 0; k < z.slices; ++k) sum += load_peer(ysum + i, k);
-      y[i / nr * a.H + i % nr] = __float2bfloat16_rn(sum);
+      for (int k = 0; k < z.slices; ++k) sum += load_peer(ysum + t * z.rows + row, k);
+      y[t * a.H + row] = __float2bfloat16_rn(sum);
     }
     __syncwarp();
     cluster_sync();  // nobody leaves while its sums are read

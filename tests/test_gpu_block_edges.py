@@ -1,0 +1,31 @@
+"""The operators around the routing where a fault was found by reading: each
+test holds what went wrong, at sizes that reach it. References and tolerances
+as in test_gpu_block.py."""
+import pytest
+import torch
+
+import padded_permute_combine_gb300 as p
+from test_gpu_block import BF, DEV, check, experts_ref, layer_inputs, randn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib_loaded():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    p.load()
+
+
+# H from which on an SM has several tiles of y's columns (128 columns for each of 152 SMs, fewer where the sums of all
+# tokens leave less memory), the last tile with fewer columns than the others.
+@pytest.mark.parametrize("T,H,F,E,K", [(4, 24576, 96, 4, 2), (40, 24576, 96, 4, 2), (40, 38760, 72, 4, 2), (4, 24577, 97, 4, 2),
+                                       (256, 10001, 65, 8, 8), (256, 14001, 65, 8, 8), (256, 24576, 64, 8, 8)])
+def test_several_tiles_of_columns_an_sm(T, H, F, E, K):
+    """The warps that add a tile's sums keep apart from one tile to the next, however far apart they run."""
+    x, router, wgu, wd = layer_inputs(T, H, F, E, BF, T + H)
+    y, te, w = p.moe_layer(x, router, wgu, wd, K)
+    ref, tol = experts_ref(x, te, w.double(), wgu, wd)
+    check(y, ref, tol, "y")
+    for _ in range(20):
+        assert torch.equal(p.moe_experts(x, te, w, wgu, wd), y)
