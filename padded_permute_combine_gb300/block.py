@@ -15,7 +15,7 @@ from typing import Sequence
 import torch
 
 from . import _lib
-from .ops import _act_dtype, _need
+from .ops import _DTYPES, _act_dtype, _need
 
 _MODES = {"softmax": _lib.MOE_GATING_SOFTMAX, "sigmoid": _lib.MOE_GATING_SIGMOID}
 
@@ -231,8 +231,10 @@ def moe_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor |
         weight_dtype = weight.dtype
     elif weight_dtype is None:
         weight_dtype = torch.float32
-    elif weight_dtype is torch.bfloat16:
-        code = _lib.MOE_BF16
+    elif weight_dtype in _DTYPES:
+        code = _DTYPES[weight_dtype]
+    else:  # the kernels write four bytes or two an element
+        raise TypeError("weight_dtype must be float32 or bfloat16, got %s" % (weight_dtype,))
     if out is None:
         out = torch.empty((M, H), dtype=x.dtype, device=dev)
     out_at = _take(out, (M, H), x.dtype, "out", dev)

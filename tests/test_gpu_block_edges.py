@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import padded_permute_combine_gb300 as p
-from test_gpu_block import BF, DEV, check, experts_ref, layer_inputs, randn
+from test_gpu_block import BF, DEV, F32, check, experts_ref, layer_inputs, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +29,23 @@ def test_several_tiles_of_columns_an_sm(T, H, F, E, K):
     check(y, ref, tol, "y")
     for _ in range(20):
         assert torch.equal(p.moe_experts(x, te, w, wgu, wd), y)
+
+
+@pytest.mark.parametrize("need_cols", [True, False])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float64, torch.int32, "fp32"])
+def test_layer_norm_bwd_refuses_other_types_of_columns(dtype, need_cols):
+    x, row = randn((4, 64), 1), torch.ones(4, device=DEV)
+    with pytest.raises(TypeError):
+        p.moe_layer_norm_bwd(x, x, None, row, row, weight_dtype=dtype, need_cols=need_cols)
+
+
+@pytest.mark.parametrize("M,H", [(1, 1), (6, 1000), (40, 257)])
+def test_layer_norm_bwd_types_of_columns_without_a_weight(M, H):
+    """The type changes the last rounding alone."""
+    x, dy = randn((M, H), 1, BF), randn((M, H), 2, BF)
+    _, mean, rstd = p.moe_layer_norm_fwd(x)
+    dx, dw, db = p.moe_layer_norm_bwd(dy, x, None, mean, rstd)
+    for dtype in (F32, BF):
+        got = p.moe_layer_norm_bwd(dy, x, None, mean, rstd, weight_dtype=dtype)
+        assert got[1].dtype is got[2].dtype is dtype
+        assert all(torch.equal(a, b.to(a.dtype)) for a, b in zip(got, (dx, dw, db)))
