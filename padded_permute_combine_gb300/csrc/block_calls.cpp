@@ -1,7 +1,8 @@
 // The block operators' calls from Python, without ctypes: checks of the
 // tensors, outputs and workspace, and the C ABI call, for the plain case of
 // every one (tensors that are right, outputs to be allocated). Anything else
-// returns None, and block.py takes the call step by step, with its messages.
+// returns None, and block.py takes the call step by step, with its messages;
+// a call that failed once work may have been enqueued raises MoeError here.
 //
 // A call of these operators on a few rows runs for 3 to 14 us on the GPU. The
 // whole call takes 5.7 us for a layer norm forward of four rows, 9.4 backward,
@@ -78,6 +79,22 @@ template <typename F> PyObject* guarded(F f) {
   }
 }
 
+// What follows a code other than MOE_OK. Refused arguments (nothing is enqueued
+// then) answer none, and block.py words the error. After any other code work
+// may be enqueued already, and a second call would do it twice (gradients
+// clipped in place, say): MoeError.
+PyObject* failed(const char* name, int rc) {
+  if (rc == MOE_ERR_INVALID_ARG || rc == MOE_ERR_UNSUPPORTED) return nullptr;
+  PyObject* lib = PyImport_ImportModule("padded_permute_combine_gb300._lib");
+  PyObject* type = lib == nullptr ? nullptr : PyObject_GetAttrString(lib, "MoeError");
+  PyObject* error = type == nullptr ? nullptr : PyObject_CallFunction(type, "sis", name, rc, moe_error_string(rc));
+  if (error != nullptr) PyErr_SetObject(type, error);
+  Py_XDECREF(error);
+  Py_XDECREF(type);
+  Py_XDECREF(lib);
+  return nullptr;
+}
+
 // x, weight, bias, eps -> (y, mean, rstd)
 PyObject* layer_norm_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
@@ -90,11 +107,10 @@ PyObject* layer_norm_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if ((wt != at::kFloat && wt != at::kBFloat16) || (w.defined() && !plain(w, x, wt, {H})) || (b.defined() && !plain(b, x, wt, {H})))
       return nullptr;
     const Tensor y = make(x, x.scalar_type(), {M, H}), mean = make(x, at::kFloat, {M}), rstd = make(x, at::kFloat, {M});
-    if (moe_layer_norm_fwd(x.const_data_ptr(), dtype_of(x), stride, at_or_null(w), at_or_null(b), wt == at::kFloat ? MOE_F32 : MOE_BF16,
-                           M, H, (float)PyFloat_AS_DOUBLE(args[3]), y.data_ptr(), mean.data_ptr<float>(), rstd.data_ptr<float>(),
-                           stream_of(x)) != MOE_OK)
-      return nullptr;
-    return wrapped({y, mean, rstd});
+    const int rc = moe_layer_norm_fwd(x.const_data_ptr(), dtype_of(x), stride, at_or_null(w), at_or_null(b),
+                                      wt == at::kFloat ? MOE_F32 : MOE_BF16, M, H, (float)PyFloat_AS_DOUBLE(args[3]), y.data_ptr(),
+                                      mean.data_ptr<float>(), rstd.data_ptr<float>(), stream_of(x));
+    return rc == MOE_OK ? wrapped({y, mean, rstd}) : failed("moe_layer_norm_fwd", rc);
   });
 }
 
@@ -119,12 +135,12 @@ PyObject* layer_norm_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
       db = make(x, wt, {H});
       ws = make(x, at::kByte, {(int64_t)bytes});
     }
-    if (moe_layer_norm_bwd(dy.const_data_ptr(), dy_stride, x.const_data_ptr(), dtype_of(x), stride, at_or_null(w),
-                           wt == at::kFloat ? MOE_F32 : MOE_BF16, mean.const_data_ptr<float>(), rstd.const_data_ptr<float>(), M, H,
-                           dx.data_ptr(), dw.defined() ? dw.data_ptr() : nullptr, db.defined() ? db.data_ptr() : nullptr,
-                           ws.defined() ? ws.data_ptr() : nullptr, bytes, stream_of(x)) != MOE_OK)
-      return nullptr;
-    return wrapped({dx, dw, db});
+    const int rc = moe_layer_norm_bwd(dy.const_data_ptr(), dy_stride, x.const_data_ptr(), dtype_of(x), stride, at_or_null(w),
+                                      wt == at::kFloat ? MOE_F32 : MOE_BF16, mean.const_data_ptr<float>(), rstd.const_data_ptr<float>(),
+                                      M, H, dx.data_ptr(), dw.defined() ? dw.data_ptr() : nullptr,
+                                      db.defined() ? db.data_ptr() : nullptr, ws.defined() ? ws.data_ptr() : nullptr, bytes,
+                                      stream_of(x));
+    return rc == MOE_OK ? wrapped({dx, dw, db}) : failed("moe_layer_norm_bwd", rc);
   });
 }
 
@@ -151,11 +167,10 @@ PyObject* layer(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (bytes == 0) return nullptr;
     const Tensor y = make(x, x.scalar_type(), {T, H}), top = make(x, at::kInt, {T, K}), w = make(x, at::kFloat, {T, K}),
                  ws = make(x, at::kByte, {(int64_t)bytes});
-    if (moe_layer(x.const_data_ptr(), dtype_of(x), stride, router.const_data_ptr(), gate_up.const_data_ptr(), down.const_data_ptr(), T, H,
-                  F, (int32_t)E, (int32_t)K, mode, PyObject_IsTrue(args[6]), top.data_ptr<int32_t>(), w.data_ptr<float>(), y.data_ptr(),
-                  ws.data_ptr(), bytes, nullptr, stream_of(x)) != MOE_OK)
-      return nullptr;
-    return wrapped({y, top, w});
+    const int rc = moe_layer(x.const_data_ptr(), dtype_of(x), stride, router.const_data_ptr(), gate_up.const_data_ptr(),
+                             down.const_data_ptr(), T, H, F, (int32_t)E, (int32_t)K, mode, PyObject_IsTrue(args[6]),
+                             top.data_ptr<int32_t>(), w.data_ptr<float>(), y.data_ptr(), ws.data_ptr(), bytes, nullptr, stream_of(x));
+    return rc == MOE_OK ? wrapped({y, top, w}) : failed("moe_layer", rc);
   });
 }
 
@@ -173,11 +188,10 @@ PyObject* experts(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const size_t bytes = moe_layer_workspace_size(T, H, F, (int32_t)E, (int32_t)K);
     if (bytes == 0) return nullptr;
     const Tensor y = make(x, x.scalar_type(), {T, H}), ws = make(x, at::kByte, {(int64_t)bytes});
-    if (moe_experts(x.const_data_ptr(), dtype_of(x), stride, top.const_data_ptr<int32_t>(), w.const_data_ptr<float>(),
-                    gate_up.const_data_ptr(), down.const_data_ptr(), T, H, F, (int32_t)E, (int32_t)K, y.data_ptr(), ws.data_ptr(), bytes,
-                    nullptr, stream_of(x)) != MOE_OK)
-      return nullptr;
-    return wrapped({y});
+    const int rc = moe_experts(x.const_data_ptr(), dtype_of(x), stride, top.const_data_ptr<int32_t>(), w.const_data_ptr<float>(),
+                               gate_up.const_data_ptr(), down.const_data_ptr(), T, H, F, (int32_t)E, (int32_t)K, y.data_ptr(),
+                               ws.data_ptr(), bytes, nullptr, stream_of(x));
+    return rc == MOE_OK ? wrapped({y}) : failed("moe_experts", rc);
   });
 }
 
@@ -193,7 +207,7 @@ PyObject* grads(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int rc = n == 3 ? moe_grad_norm(p, pieces, norm.data_ptr<float>(), ws.data_ptr(), ws.numel(), stream_of(table))
                           : moe_clip_grads(p, pieces, (float)PyFloat_AS_DOUBLE(args[3]), norm.data_ptr<float>(), ws.data_ptr(), ws.numel(),
                                            stream_of(table));
-    return rc == MOE_OK ? wrapped({norm}) : nullptr;
+    return rc == MOE_OK ? wrapped({norm}) : failed(n == 3 ? "moe_grad_norm" : "moe_clip_grads", rc);
   });
 }
 
