@@ -79,6 +79,16 @@ template <typename F> PyObject* guarded(F f) {
   }
 }
 
+// The C ABI's call without the interpreter's lock, as ctypes makes it: a full
+// launch queue blocks it for as long as the queue is full, and other threads
+// go on meanwhile.
+template <typename F> int unlocked(F f) {
+  PyThreadState* state = PyEval_SaveThread();
+  const int rc = f();
+  PyEval_RestoreThread(state);
+  return rc;
+}
+
 // What follows a code other than MOE_OK. Refused arguments (nothing is enqueued
 // then) answer none, and block.py words the error. After any other code work
 // may be enqueued already, and a second call would do it twice (gradients
@@ -103,13 +113,16 @@ PyObject* layer_norm_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (n != 4 || !tensors(args, 3, t, 6) || !PyFloat_Check(args[3]) || !rows_ok(t[0], &stride)) return nullptr;
     const Tensor &x = t[0], &w = t[1], &b = t[2];
     const int64_t M = x.size(0), H = x.size(1);
+    const float eps = (float)PyFloat_AS_DOUBLE(args[3]);
     const at::ScalarType wt = w.defined() ? w.scalar_type() : b.defined() ? b.scalar_type() : at::kFloat;
     if ((wt != at::kFloat && wt != at::kBFloat16) || (w.defined() && !plain(w, x, wt, {H})) || (b.defined() && !plain(b, x, wt, {H})))
       return nullptr;
     const Tensor y = make(x, x.scalar_type(), {M, H}), mean = make(x, at::kFloat, {M}), rstd = make(x, at::kFloat, {M});
-    const int rc = moe_layer_norm_fwd(x.const_data_ptr(), dtype_of(x), stride, at_or_null(w), at_or_null(b),
-                                      wt == at::kFloat ? MOE_F32 : MOE_BF16, M, H, (float)PyFloat_AS_DOUBLE(args[3]), y.data_ptr(),
-                                      mean.data_ptr<float>(), rstd.data_ptr<float>(), stream_of(x));
+    const int rc = unlocked([&] {
+      return moe_layer_norm_fwd(x.const_data_ptr(), dtype_of(x), stride, at_or_null(w), at_or_null(b),
+                                wt == at::kFloat ? MOE_F32 : MOE_BF16, M, H, eps, y.data_ptr(), mean.data_ptr<float>(),
+                                rstd.data_ptr<float>(), stream_of(x));
+    });
     return rc == MOE_OK ? wrapped({y, mean, rstd}) : failed("moe_layer_norm_fwd", rc);
   });
 }
@@ -135,11 +148,12 @@ PyObject* layer_norm_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
       db = make(x, wt, {H});
       ws = make(x, at::kByte, {(int64_t)bytes});
     }
-    const int rc = moe_layer_norm_bwd(dy.const_data_ptr(), dy_stride, x.const_data_ptr(), dtype_of(x), stride, at_or_null(w),
-                                      wt == at::kFloat ? MOE_F32 : MOE_BF16, mean.const_data_ptr<float>(), rstd.const_data_ptr<float>(),
-                                      M, H, dx.data_ptr(), dw.defined() ? dw.data_ptr() : nullptr,
-                                      db.defined() ? db.data_ptr() : nullptr, ws.defined() ? ws.data_ptr() : nullptr, bytes,
-                                      stream_of(x));
+    const int rc = unlocked([&] {
+      return moe_layer_norm_bwd(dy.const_data_ptr(), dy_stride, x.const_data_ptr(), dtype_of(x), stride, at_or_null(w),
+                                wt == at::kFloat ? MOE_F32 : MOE_BF16, mean.const_data_ptr<float>(), rstd.const_data_ptr<float>(), M, H,
+                                dx.data_ptr(), dw.defined() ? dw.data_ptr() : nullptr, db.defined() ? db.data_ptr() : nullptr,
+                                ws.defined() ? ws.data_ptr() : nullptr, bytes, stream_of(x));
+    });
     return rc == MOE_OK ? wrapped({dx, dw, db}) : failed("moe_layer_norm_bwd", rc);
   });
 }
@@ -162,14 +176,16 @@ PyObject* layer(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const Tensor &x = t[0], &router = t[1], &gate_up = t[2], &down = t[3];
     const int64_t T = x.size(0), H = x.size(1), K = PyLong_AsLongLong(args[4]);
     if (!experts_ok(x, gate_up, down, &E, &F) || !plain(router, x, x.scalar_type(), {E, H}) || K < 1 || K > E) return nullptr;
-    const int32_t mode = (int32_t)PyLong_AsLong(args[5]);
+    const int32_t mode = (int32_t)PyLong_AsLong(args[5]), normalize = PyObject_IsTrue(args[6]);
     const size_t bytes = moe_layer_workspace_size(T, H, F, (int32_t)E, (int32_t)K);
     if (bytes == 0) return nullptr;
     const Tensor y = make(x, x.scalar_type(), {T, H}), top = make(x, at::kInt, {T, K}), w = make(x, at::kFloat, {T, K}),
                  ws = make(x, at::kByte, {(int64_t)bytes});
-    const int rc = moe_layer(x.const_data_ptr(), dtype_of(x), stride, router.const_data_ptr(), gate_up.const_data_ptr(),
-                             down.const_data_ptr(), T, H, F, (int32_t)E, (int32_t)K, mode, PyObject_IsTrue(args[6]),
-                             top.data_ptr<int32_t>(), w.data_ptr<float>(), y.data_ptr(), ws.data_ptr(), bytes, nullptr, stream_of(x));
+    const int rc = unlocked([&] {
+      return moe_layer(x.const_data_ptr(), dtype_of(x), stride, router.const_data_ptr(), gate_up.const_data_ptr(), down.const_data_ptr(), T,
+                       H, F, (int32_t)E, (int32_t)K, mode, normalize, top.data_ptr<int32_t>(), w.data_ptr<float>(), y.data_ptr(),
+                       ws.data_ptr(), bytes, nullptr, stream_of(x));
+    });
     return rc == MOE_OK ? wrapped({y, top, w}) : failed("moe_layer", rc);
   });
 }
@@ -188,9 +204,11 @@ PyObject* experts(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const size_t bytes = moe_layer_workspace_size(T, H, F, (int32_t)E, (int32_t)K);
     if (bytes == 0) return nullptr;
     const Tensor y = make(x, x.scalar_type(), {T, H}), ws = make(x, at::kByte, {(int64_t)bytes});
-    const int rc = moe_experts(x.const_data_ptr(), dtype_of(x), stride, top.const_data_ptr<int32_t>(), w.const_data_ptr<float>(),
-                               gate_up.const_data_ptr(), down.const_data_ptr(), T, H, F, (int32_t)E, (int32_t)K, y.data_ptr(),
-                               ws.data_ptr(), bytes, nullptr, stream_of(x));
+    const int rc = unlocked([&] {
+      return moe_experts(x.const_data_ptr(), dtype_of(x), stride, top.const_data_ptr<int32_t>(), w.const_data_ptr<float>(),
+                         gate_up.const_data_ptr(), down.const_data_ptr(), T, H, F, (int32_t)E, (int32_t)K, y.data_ptr(), ws.data_ptr(),
+                         bytes, nullptr, stream_of(x));
+    });
     return rc == MOE_OK ? wrapped({y}) : failed("moe_experts", rc);
   });
 }
@@ -204,9 +222,11 @@ PyObject* grads(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int64_t pieces = PyLong_AsLongLong(args[2]);
     const Tensor norm = make(table, at::kFloat, {});
     const auto* p = static_cast<const moe_grad_piece*>(table.const_data_ptr());
-    const int rc = n == 3 ? moe_grad_norm(p, pieces, norm.data_ptr<float>(), ws.data_ptr(), ws.numel(), stream_of(table))
-                          : moe_clip_grads(p, pieces, (float)PyFloat_AS_DOUBLE(args[3]), norm.data_ptr<float>(), ws.data_ptr(), ws.numel(),
-                                           stream_of(table));
+    const float max_norm = n == 3 ? 0.0f : (float)PyFloat_AS_DOUBLE(args[3]);
+    const int rc = unlocked([&] {
+      return n == 3 ? moe_grad_norm(p, pieces, norm.data_ptr<float>(), ws.data_ptr(), ws.numel(), stream_of(table))
+                    : moe_clip_grads(p, pieces, max_norm, norm.data_ptr<float>(), ws.data_ptr(), ws.numel(), stream_of(table));
+    });
     return rc == MOE_OK ? wrapped({norm}) : failed(n == 3 ? "moe_grad_norm" : "moe_clip_grads", rc);
   });
 }

@@ -84,3 +84,15 @@ for name, call in every.items():
 code.value = 0
 assert float(grads.grads[0].norm()) < 0.51
 """)
+
+
+def test_calls_leave_the_interpreter_to_other_threads(tmp_path):
+    """As ctypes' calls do: a launch that waits for room in a full queue must
+    not hold up the process's other Python threads."""
+    run_with_stub(tmp_path, """
+code.value = 0
+for name, call in every.items():
+    calls.value = locked.value = 0
+    call()
+    assert calls.value == 1 and locked.value == 0, name
+""")
