@@ -13,6 +13,7 @@ import glob
 import hashlib
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -45,7 +46,8 @@ def sources() -> list[str]:
 def source_digest() -> str:
     """Hash of every source and header the library is built from."""
     h = hashlib.sha256()
-    files = sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")))
+    files = sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+                               + glob.glob(os.path.join(INCLUDE, "*.h")))
     for f in files:
         h.update(os.path.basename(f).encode())
         with open(f, "rb") as fh:
@@ -81,11 +83,15 @@ def _code_only(text: str) -> str:
 
 def kernel_digest(unit: str) -> str:
     """Hash of one kernel family's translation unit (``csrc/<unit>.cu``), the
-    shared headers and the compile flags, comments and layout left out: it
+    shared headers (every ``.cuh``, and the ``.h`` of ``csrc/`` that the unit
+    includes) and the compile flags, comments and layout left out: it
     changes only when what that kernel is compiled from changes, so a profile
     taken on it stays valid while other kernels, or comments, are edited."""
     h = hashlib.sha256()
-    files = [os.path.join(CSRC, unit + ".cu")] + sorted(glob.glob(os.path.join(CSRC, "*.cuh")))
+    source = os.path.join(CSRC, unit + ".cu")
+    with open(source, encoding="utf-8") as fh:
+        own = [os.path.join(CSRC, name) for name in re.findall(r'^#include "(\w+\.h)"', fh.read(), re.M)]
+    files = [source] + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [f for f in own if os.path.exists(f)]
     for f in files:
         h.update(os.path.basename(f).encode())
         with open(f, encoding="utf-8") as fh:

@@ -21,6 +21,7 @@
 #include "bulk.cuh"
 #include "common.cuh"
 #include "moe_block.h"
+#include "smem_limit.h"
 #include "vec_math.cuh"
 
 namespace moe {
@@ -983,20 +984,6 @@ bool ring_shape(int64_t vecs, int nv, int r, int registers, int threads, int64_t
   return z->slots >= 2;
 }
 
-// Raises a kernel's dynamic shared memory limit once per device.
-template <typename Kernel> bool allow_smem(Kernel k, int bytes, std::atomic<int>* granted) {
-  int dev = 0;
-  (void)cudaGetDevice(&dev);
-  const bool cached = dev >= 0 && dev < 64;
-  if (cached && granted[dev].load(std::memory_order_relaxed) >= bytes) return true;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return false;
-  }
-  if (cached) granted[dev].store(bytes, std::memory_order_relaxed);
-  return true;
-}
-
 // Whether the chunk kernels take the rows: packed, enough of them for every SM,
 // and `arrays` chunks in at most `most` bytes of shared memory.
 template <typename ET> bool chunks_ok(int64_t H, int64_t rows, int arrays, int64_t most, const int64_t* strides, const void* const* ptrs) {
@@ -1011,10 +998,10 @@ template <typename ET, typename WT, int NC> int go_fwd_chunk(const FwdArgs& a, c
   if constexpr (NC > 4) {
     if (a.H <= NC / 2 * kChunkThreads) return go_fwd_chunk<ET, WT, NC / 2>(a, s);
   }
-  static std::atomic<int> granted[64];
+  static std::atomic<bool> raised[kSmemDevices];
   auto k = fwd_chunk_kernel<ET, WT, NC>;
   const size_t smem = (size_t)kChunk * a.H * Elem<ET>::kBytes;
-  if (!allow_smem(k, (int)smem, granted)) return MOE_ERR_CUDA;
+  if (!allow_smem(k, raised)) return MOE_ERR_CUDA;
   launch(k, grid_for(k, kChunkThreads, smem, (a.rows + kChunk - 1) / kChunk), kChunkThreads, smem, s, a);
   return check_launch();
 }
@@ -1023,10 +1010,10 @@ template <typename ET, typename WT, int NC> int go_bwd_chunk(const BwdArgs& a, i
   if constexpr (NC > 4) {
     if (a.H <= NC / 2 * kChunkThreads) return go_bwd_chunk<ET, WT, NC / 2>(a, parts, s);
   }
-  static std::atomic<int> granted[64];
+  static std::atomic<bool> raised[kSmemDevices];
   auto k = bwd_chunk_kernel<ET, WT, NC>;
   const size_t smem = 2 * (size_t)kChunk * a.H * Elem<ET>::kBytes;
-  if (!allow_smem(k, (int)smem, granted)) return MOE_ERR_CUDA;
+  if (!allow_smem(k, raised)) return MOE_ERR_CUDA;
   const int64_t most = bwd_parts(a.rows, a.H), work = (a.rows + kChunk - 1) / kChunk;
   *parts = grid_for(k, kChunkThreads, smem, work < most ? work : most);
   launch(k, *parts, kChunkThreads, smem, s, a);
@@ -1081,7 +1068,8 @@ int go_bwd(const BwdArgs& a, int* parts, cudaStream_t s) {
 
 template <typename ET, typename WT, int NV, int R, bool KEEP, bool FULL = false>
 int go_ring(const BwdArgs& a, int* parts, cudaStream_t s) {
-  static std::atomic<int> granted[64], registers{0};
+  static std::atomic<bool> raised[kSmemDevices];
+  static std::atomic<int> registers{0};
   RingShape z;
   const int64_t vecs = a.H / Lanes<16, ET>::kElems;
   if constexpr (!FULL) {
@@ -1099,7 +1087,7 @@ int go_ring(const BwdArgs& a, int* parts, cudaStream_t s) {
     registers.store(regs, std::memory_order_relaxed);
   }
   if (!ring_shape(vecs, NV, R, regs, ring_threads<ET>(NV), a.rows, bwd_parts(a.rows, a.H), &z) ||
-      !allow_smem(k, (int)z.smem, granted))
+      !allow_smem(k, raised))
     return MOE_ERR_CUDA;
   *parts = z.grid;
   launch(k, z.grid, z.threads, z.smem, s, a, z.slots);

@@ -20,6 +20,7 @@
 #include "bulk.cuh"
 #include "common.cuh"
 #include "moe_block.h"
+#include "smem_limit.h"
 #include "vec_math.cuh"
 
 namespace moe {
@@ -1243,29 +1244,15 @@ template <typename Kernel> int grid_for(Kernel k, int threads, size_t smem, int6
   return persistent_grid(k, threads, smem, work_ctas);
 }
 
-// Raises a kernel's dynamic shared memory limit once per device.
-template <typename Kernel> bool allow_smem(Kernel k, int bytes, std::atomic<int>* granted) {
-  int dev = 0;
-  (void)cudaGetDevice(&dev);
-  const bool cached = dev >= 0 && dev < 64;
-  if (cached && granted[dev].load(std::memory_order_relaxed) >= bytes) return true;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return false;
-  }
-  if (cached) granted[dev].store(bytes, std::memory_order_relaxed);
-  return true;
-}
-
 // Elements of a row padded to 32 bytes (of fp32, what 16 bytes of bf16 weights go with).
 int64_t padded_row(int64_t n) { return (n + 7) / 8 * 8; }
 
 template <typename ET, bool SHIFT>
 int run_router(const LayerArgs& a, const ET* x, int64_t x_ld, const void* router, float* logits, int32_t mode,
                int32_t normalize, int32_t* top_expert, float* weights, cudaStream_t s) {
-  static std::atomic<int> granted[64];
+  static std::atomic<bool> raised[kSmemDevices];
   auto r = router_rows_kernel<ET, SHIFT>;
-  if (!allow_smem(r, kRowsRing<ET, SHIFT>, granted)) return MOE_ERR_CUDA;
+  if (!allow_smem(r, raised)) return MOE_ERR_CUDA;
   launch(r, dim3((unsigned)((a.E + kRows - 1) / kRows), (unsigned)((a.T + kCols - 1) / kCols)), kThreads, kRowsRing<ET, SHIFT>, s, x, x_ld,
          static_cast<const ET*>(router), a.H, a.T, a.E, logits);
   return moe_topk_gating(logits, a.T, a.E, a.K, mode, normalize, top_expert, weights,
@@ -1273,16 +1260,16 @@ int run_router(const LayerArgs& a, const ET* x, int64_t x_ld, const void* router
 }
 
 template <typename ET, bool SHIFT> int run_rows(const LayerArgs& a, const ET* x, int64_t x_ld, cudaStream_t s) {
-  static std::atomic<int> granted_g[64], granted_d[64];
+  static std::atomic<bool> raised_g[kSmemDevices], raised_d[kSmemDevices];
   const size_t seg = kRowsRing<ET, SHIFT> + segments_bytes(a.n, a.E);
   const int64_t h_ld = padded_row(a.F), couples = (a.F + 1) / 2;
   auto g = gate_up_rows_kernel<ET, SHIFT>;
-  if (!allow_smem(g, (int)seg, granted_g)) return MOE_ERR_CUDA;
+  if (!allow_smem(g, raised_g)) return MOE_ERR_CUDA;
   launch(g, grid_for(g, kThreads, seg, ((a.n < a.E ? a.n : a.E) * couples + kWarps - 1) / kWarps), kThreads, seg, s, a, x,
          x_ld, h_ld);
   const size_t smem = seg + sizeof(int32_t) * a.n + sizeof(float) * kRows * a.n * (a.n <= kSliceChoices ? kWarps : 1);
   auto d = down_rows_kernel<ET, SHIFT>;
-  if (!allow_smem(d, (int)smem, granted_d)) return MOE_ERR_CUDA;
+  if (!allow_smem(d, raised_d)) return MOE_ERR_CUDA;
   launch(d, grid_for(d, kThreads, smem, (a.H + kRows - 1) / kRows), kThreads, smem, s, a, h_ld);
   return check_launch();
 }
@@ -1345,7 +1332,7 @@ template <bool SHIFT> bool cut_stages(StreamShape* z, int block_bytes, int most,
 }
 
 template <bool SHIFT> int run_stream(const LayerArgs& a, float* parts, cudaStream_t s) {
-  static std::atomic<int> granted_g[64], granted_d[64];
+  static std::atomic<bool> raised_g[kSmemDevices], raised_d[kSmemDevices];
   __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(a.h);
   const int64_t h_ld = padded_row(a.F), y_n = a.T * a.H, parts_ld = (y_n + 3) / 4 * 4;
   const StreamArgs p{a, h, h + a.n * h_ld, h_ld, parts, parts_ld};
@@ -1405,8 +1392,8 @@ template <bool SHIFT> int run_stream(const LayerArgs& a, float* parts, cudaStrea
   d_smem += (size_t)d.stages * d.stage_bytes + (SHIFT ? raw_bytes(d.blocks) : 0) + 1024;
 
   CUtensorMap g_map = {}, d_map = {};
-  if (!allow_smem(gate_up_stream_kernel<SHIFT>, (int)g_smem, granted_g) ||
-      !allow_smem(down_stream_kernel<SHIFT>, (int)d_smem, granted_d) ||
+  if (!allow_smem(gate_up_stream_kernel<SHIFT>, raised_g) ||
+      !allow_smem(down_stream_kernel<SHIFT>, raised_d) ||
       (!SHIFT && (!tensor_map(&g_map, a.w_gate_up, a.H, a.F, 2 * (int64_t)a.E, 16, 2) ||
                   !tensor_map(&d_map, a.w_down, a.F, a.H, a.E, d.rows, 1))))
     return MOE_ERR_CUDA;
