@@ -65,6 +65,15 @@ int moe_experts(const void* x, int32_t dtype, int64_t x_stride, const int32_t* t
                 int32_t* d_status, moe_stream_t stream);
 
 /*
+ * Testing only: bounded waits inside the kernels of this header give up at
+ * once, as if what they wait for never came, so that a test can see how such a
+ * call ends. Bits: the layer's copies of weights 1, its copies of tokens 2,
+ * its products 4, the reading of their sums 8; 0 restores all. Process-wide;
+ * not for concurrent use with real calls.
+ */
+void moe_test_block_waits(uint32_t give_up);
+
+/*
  * Layer norm over the last dimension:
  *   mean = sum(x) / H;  rstd = 1 / sqrt(sum((x - mean)^2) / H + eps)
  *   y    = (x - mean) * rstd * weight + bias

@@ -70,6 +70,7 @@ BLOCK_SIGNATURES = {
     "moe_layer": (ctypes.c_int, [_P, _I32, _I64, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _P, _P, _P, _P,
                                  _SZ, _P, _P]),
     "moe_experts": (ctypes.c_int, [_P, _I32, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _P, _P, _SZ, _P, _P]),
+    "moe_test_block_waits": (None, [ctypes.c_uint32]),
     "moe_layer_norm_fwd": (ctypes.c_int, [_P, _I32, _I64, _P, _P, _I32, _I64, _I64, ctypes.c_float, _P, _P, _P, _P]),
     "moe_layer_norm_bwd_workspace_size": (_SZ, [_I64, _I64]),
     "moe_layer_norm_bwd": (ctypes.c_int, [_P, _I64, _P, _I32, _I64, _P, _I32, _P, _P, _I64, _I64, _P, _P, _P, _P, _SZ,

@@ -543,7 +543,8 @@ __global__ void __launch_bounds__(kThreads, 2) down_rows_kernel(LayerArgs a, int
 // copy tokens, 8 (SHIFT: 8..23) copies weights, the last issues the products.
 // Sums are double buffered. Every wait is bounded: a warp that gives up sets
 // MOE_STATUS_TIMEOUT and does no more work; all warps meet at the end, where
-// the tensor memory is freed.
+// copies and products still in flight are waited for (bounded again) and the
+// tensor memory is freed.
 
 constexpr int kOutWarps = 4;
 constexpr int kTokenWarps = 4;
@@ -557,6 +558,9 @@ constexpr int kRowBytes = 128;
 constexpr int kTileRows = 128;   // weight rows of a product
 constexpr int kMaxTokens = 128;  // of an expert at a time (256 tokens of the Mixtral-8x7B shape: 788 us, with 64: 985)
 constexpr uint64_t kWaitNs = 2000000000;  // after which a wait gives up
+constexpr uint64_t kTestWaitNs = 20000000;  // the same while moe_test_block_waits makes some give up at once
+// The warps whose waits it makes give up.
+constexpr uint32_t kGiveUpWeights = 1, kGiveUpTokens = 2, kGiveUpProducts = 4, kGiveUpSums = 8;
 
 __device__ __forceinline__ uint32_t align_1k(uint32_t p) { return (p + 1023u) & ~1023u; }
 __host__ __device__ constexpr int round_to(int v, int m) { return (v + m - 1) / m * m; }
@@ -636,11 +640,15 @@ __device__ __forceinline__ void product(uint32_t sums, uint64_t rows, uint64_t c
       : "memory");
 }
 
-// Where a warp stands in the ring of stages or in the two buffers of sums.
+// Where a warp stands in the ring of stages or in the two buffers of sums, and
+// how many it has done.
 struct Ring {
   int n, i;
   uint32_t parity;
+  int done;
+  __device__ __forceinline__ Ring(int n_, uint32_t parity_) : n(n_), i(0), parity(parity_), done(0) {}
   __device__ __forceinline__ void advance() {
+    ++done;
     if (++i == n) {
       i = 0;
       parity ^= 1;
@@ -655,6 +663,7 @@ struct StreamArgs {
   int64_t h_ld;
   float* parts;  // [slices, T, H]: the slices' sums, where there are more than two
   int64_t parts_ld;
+  uint32_t give_up;  // kGiveUp*: 0 but in tests
 };
 // A kernel's cut of its work and of its shared memory.
 struct StreamShape {
@@ -668,6 +677,7 @@ struct StreamShape {
 struct StreamShared {
   uint64_t full[kMaxStages], empty[kMaxStages], sums_full[2], sums_empty[2];
   uint32_t tmem;
+  int issued;  // stages whose weights are on their way, set when a warp has given up
 };
 
 template <bool SHIFT> __device__ __forceinline__ void init_shared(StreamShared& sh, int stages) {
@@ -682,13 +692,23 @@ template <bool SHIFT> __device__ __forceinline__ void init_shared(StreamShared& 
   fence_mbarrier_init();
 }
 
+// How long a warp waits.
+struct Patience {
+  int polls;
+  uint64_t ns;
+  int32_t* status;
+  __device__ __forceinline__ Patience(int32_t* status_) : polls(kSpinLimit), ns(kWaitNs), status(status_) {}
+  __device__ __forceinline__ Patience(const StreamArgs& p, uint32_t who)
+      : polls(p.give_up & who ? 0 : kSpinLimit), ns(p.give_up ? kTestWaitNs : kWaitNs), status(p.a.status) {}
+};
+
 // By a whole warp, bounded in polls and in time; false once a wait has given up.
-__device__ __forceinline__ bool wait_bar(bool ok, uint64_t* bar, uint32_t parity, int32_t* status) {
+__device__ __forceinline__ bool wait_bar(bool ok, uint64_t* bar, uint32_t parity, const Patience& patience) {
   if (!ok) return false;
   const uint32_t at = smem_u32(bar);
   uint64_t since = 0;
   ok = false;
-  for (int it = 0; it < kSpinLimit; ++it) {
+  for (int it = 0; it < patience.polls; ++it) {
     uint32_t done;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
@@ -704,10 +724,10 @@ __device__ __forceinline__ bool wait_bar(bool ok, uint64_t* bar, uint32_t parity
       asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
       now = __shfl_sync(0xffffffffu, now, 0);
       if (since == 0) since = now;
-      if (now - since > kWaitNs) break;
+      if (now - since > patience.ns) break;
     }
   }
-  if (!ok && lane_id() == 0) flag_status(status, MOE_STATUS_TIMEOUT);
+  if (!ok && lane_id() == 0) flag_status(patience.status, MOE_STATUS_TIMEOUT);
   return ok;
 }
 
@@ -715,23 +735,24 @@ __device__ __forceinline__ bool wait_bar(bool ok, uint64_t* bar, uint32_t parity
 // stages; `columns(w)`: columns of a tile's products; `tokens_at(w)`: offset of
 // the tokens in a stage; block: bytes of a block of weight rows.
 template <typename WALK, typename C, typename O>
-__device__ __forceinline__ void multiply(WALK w, StreamShared& sh, const StreamShape& z, uint32_t ring, int block,
-                                         int32_t* status, C columns, O tokens_at) {
-  Ring r{z.stages, 0, 0}, d{2, 0, 1};
+__device__ __forceinline__ bool multiply(WALK w, StreamShared& sh, const StreamShape& z, uint32_t ring, int block,
+                                         const Patience& patience, C columns, O tokens_at) {
+  Ring r(z.stages, 0), d(2, 1);
   const uint32_t tmem = sh.tmem;
   bool ok = true;
   while (w.more()) {
-    ok = wait_bar(ok, &sh.sums_empty[d.i], d.parity, status);
+    ok = wait_bar(ok, &sh.sums_empty[d.i], d.parity, patience);
     tmem_fence_after();
     const int n = columns(w);
     bool add = false;
-    for (bool last = false; !last; w.next(), r.advance()) {
+    for (bool last = false; ok && !last; w.next(), r.advance()) {
       last = w.last_stage();
-      ok = wait_bar(ok, &sh.full[r.i], r.parity, status);
+      ok = wait_bar(ok, &sh.full[r.i], r.parity, patience);
+      if (!ok) break;
       fence_async_shared();  // the tokens' copies were ordinary writes; the products read by another path
       tmem_fence_after();
       __syncwarp();
-      if (ok && elect_lane()) {
+      if (elect_lane()) {
         const uint32_t at = ring + r.i * z.stage_bytes, sums = tmem + d.i * (z.cols / 2);
         const uint32_t tokens = at + tokens_at(w);
         const int kc = w.kc();
@@ -752,10 +773,34 @@ __device__ __forceinline__ void multiply(WALK w, StreamShared& sh, const StreamS
       add = true;
       __syncwarp();
     }
+    if (!ok) break;
     d.advance();
   }
-  // Every arrival lands before the CTA may end.
-  for (int i = 0; i < z.stages; ++i) ok = wait_bar(ok, &sh.empty[i], i < r.i ? r.parity : r.parity ^ 1, status);
+  // Every product is done and every arrival lands before the CTA may end, also
+  // after giving up: of the stages' last uses, and of the sums' (whose barriers'
+  // phases begin where sums_empty's second ones do).
+  const Patience last(patience.status);
+  for (int i = 0; i < z.stages; ++i) ok = wait_bar(true, &sh.empty[i], i < r.i ? r.parity : r.parity ^ 1, last) && ok;
+  for (int i = 0; i < 2; ++i) ok = wait_bar(true, &sh.sums_full[i], i < d.i ? d.parity ^ 1 : d.parity, last) && ok;
+  return ok;
+}
+
+// The end of a CTA's work, for all its threads: `ok` false in the warps that
+// gave up; r: where the warps that copy stand. A tensor copy in flight would
+// write to memory that is another CTA's by then, so its barrier's phase is
+// waited for; the token warps first arrive for the stages that they left.
+template <bool SHIFT> __device__ __forceinline__ void meet(StreamShared& sh, int warp, bool ok, Ring& r, int32_t* status) {
+  tmem_fence_before();
+  const bool failed = __syncthreads_or(!ok);
+  tmem_fence_after();
+  if (SHIFT || !failed) return;
+  if (threadIdx.x == kCopyWarp * kWarp) sh.issued = r.done;
+  __syncthreads();
+  if (warp >= kOutWarps && warp < kCopyWarp)
+    for (; r.done < sh.issued; r.advance()) mbar_arrive(smem_u32(&sh.full[r.i]));
+  if (warp == kCopyWarp)
+    for (int i = 0; i < r.n; ++i) wait_bar(true, &sh.full[i], i < r.i ? r.parity ^ 1 : r.parity, Patience(status));
+  __syncthreads();
 }
 
 // The weights of every stage where rows are not a multiple of 16 bytes (or do
@@ -775,8 +820,8 @@ __host__ __device__ constexpr int raw_row(int blocks) { return blocks * kRowByte
 __host__ __device__ constexpr int raw_bytes(int blocks) { return kRawDepth * kTileRows * raw_row(blocks); }
 
 template <typename WALK, typename ROWS>
-__device__ __forceinline__ void copy_shifted(WALK w, StreamShared& sh, const StreamShape& z, uint32_t ring, int block, int64_t len,
-                                             int32_t* status, const ROWS& rows) {
+__device__ __forceinline__ bool copy_shifted(WALK w, StreamShared& sh, const StreamShape& z, uint32_t ring, int block, int64_t len,
+                                             const Patience& patience, const ROWS& rows) {
   const int lane = lane_id(), row_bytes = raw_row(z.blocks);
   const uint32_t raw = ring + z.stages * z.stage_bytes + (threadIdx.x / kWarp - kCopyWarp) * (kRawDepth * kEach) * row_bytes + lane * 16;
   const bool mine = lane < z.blocks * 8;
@@ -801,11 +846,11 @@ __device__ __forceinline__ void copy_shifted(WALK w, StreamShared& sh, const Str
   for (int d = 0; d < kRawDepth; ++d) fetch(d);
   bool ok = true;
   int slot = 0;
-  for (Ring r{z.stages, 0, 1}; w.more(); w.next(), r.advance()) {
+  for (Ring r(z.stages, 1); w.more(); w.next(), r.advance()) {
     const int n = rows.count(w), left = (int)(len - w.k0) - lane * 8;  // elements of the row from this lane's piece on
     const int shift0 = (int)((rows.first(w) + 2 * w.k0) & 15);
     asm volatile("cp.async.wait_group %0;" ::"n"(kRawDepth - 1) : "memory");
-    ok = wait_bar(ok, &sh.empty[r.i], r.parity, status);
+    ok = wait_bar(ok, &sh.empty[r.i], r.parity, patience);
     if (!ok) break;
     __syncwarp();
     const uint32_t stage = ring + r.i * z.stage_bytes + (lane >> 3) * block, src = raw + slot * kEach * row_bytes;
@@ -841,6 +886,7 @@ __device__ __forceinline__ void copy_shifted(WALK w, StreamShared& sh, const Str
     mbar_arrive(smem_u32(&sh.full[r.i]));
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  return ok;
 }
 
 // Tiles of up to z.rows / 2 row pairs (gate, up) of one expert by up to
@@ -925,11 +971,12 @@ __global__ void __launch_bounds__(kStreamThreads<SHIFT>)
   allow_next_kernel();
   GateUpWalk w(s, a, z);
   bool ok = true;
+  Ring r(z.stages, 1);  // of the warps that copy
   if (SHIFT && warp >= kCopyWarp && warp < kMulWarp<SHIFT>) {
-    copy_shifted(w, sh, z, ring, block, a.H, a.status, GateUpRows(s, a, warp - kCopyWarp));
+    ok = copy_shifted(w, sh, z, ring, block, a.H, Patience(p, kGiveUpWeights), GateUpRows(s, a, warp - kCopyWarp));
   } else if (!SHIFT && warp == kCopyWarp) {
-    for (Ring r{z.stages, 0, 1}; w.more(); w.next(), r.advance()) {
-      ok = wait_bar(ok, &sh.empty[r.i], r.parity, a.status);
+    for (const Patience patience(p, kGiveUpWeights); w.more(); w.next(), r.advance()) {
+      ok = wait_bar(ok, &sh.empty[r.i], r.parity, patience);
       if (!ok) break;
       __syncwarp();
       if (elect_lane()) {
@@ -942,13 +989,13 @@ __global__ void __launch_bounds__(kStreamThreads<SHIFT>)
       }
     }
   } else if (warp == kMulWarp<SHIFT>) {
-    multiply(w, sh, z, ring, block, a.status, [](const GateUpWalk& v) { return round_to(v.ntok, 16); },
+    ok = multiply(w, sh, z, ring, block, Patience(p, kGiveUpProducts), [](const GateUpWalk& v) { return round_to(v.ntok, 16); },
              [&](const GateUpWalk&) { return z.blocks * block; });
   } else if (warp >= kOutWarps) {
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x);
     const int piece = lane & 7, first = (warp - kOutWarps) * 4 + (lane >> 3);
-    for (Ring r{z.stages, 0, 1}; w.more(); w.next(), r.advance()) {
-      ok = wait_bar(ok, &sh.empty[r.i], r.parity, a.status);
+    for (const Patience patience(p, kGiveUpTokens); w.more(); w.next(), r.advance()) {
+      ok = wait_bar(ok, &sh.empty[r.i], r.parity, patience);
       if (!ok) break;
       const uint32_t at = ring + r.i * z.stage_bytes + z.blocks * block;
       const int kc = w.kc(), n = round_to(w.ntok, 16);
@@ -962,12 +1009,14 @@ __global__ void __launch_bounds__(kStreamThreads<SHIFT>)
       }
       arrive_after_copies(smem_u32(&sh.full[r.i]));
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // Rows of the sums: 16 gate rows, their 16 up rows, the next 16 gate rows ...
     const bool gate = lane < 16;
     const int f = warp * 16 + (lane & 15);
-    for (Ring d{2, 0, 0}; w.more(); w.next_pass(), d.advance()) {
-      ok = wait_bar(ok, &sh.sums_full[d.i], d.parity, a.status);
+    const Patience patience(p, kGiveUpSums);
+    for (Ring d(2, 0); w.more(); w.next_pass(), d.advance()) {
+      ok = wait_bar(ok, &sh.sums_full[d.i], d.parity, patience);
       tmem_fence_after();
       if (ok && warp * 16 < w.nf) {
         const uint32_t at = sh.tmem + d.i * (z.cols / 2) + ((uint32_t)(warp * 32) << 16);
@@ -1002,9 +1051,7 @@ __global__ void __launch_bounds__(kStreamThreads<SHIFT>)
       if (lane == 0) mbar_arrive(smem_u32(&sh.sums_empty[d.i]));
     }
   }
-  tmem_fence_before();
-  __syncthreads();
-  tmem_fence_after();
+  meet<SHIFT>(sh, warp, ok, r, a.status);
   if (warp == kMulWarp<SHIFT>) tmem_free(sh.tmem, z.cols);
 }
 
@@ -1114,11 +1161,12 @@ __global__ void __launch_bounds__(kStreamThreads<SHIFT>)
   DownWalk w(s, a, z);
   const int block = round_to(z.rows, 8) * kRowBytes;
   bool ok = true;
+  Ring r(z.stages, 1);  // of the warps that copy
   if (SHIFT && warp >= kCopyWarp && warp < kMulWarp<SHIFT>) {
-    copy_shifted(w, sh, z, ring, block, a.F, a.status, DownRows(s, a, warp - kCopyWarp));
+    ok = copy_shifted(w, sh, z, ring, block, a.F, Patience(p, kGiveUpWeights), DownRows(s, a, warp - kCopyWarp));
   } else if (!SHIFT && warp == kCopyWarp) {
-    for (Ring r{z.stages, 0, 1}; w.more(); w.next(), r.advance()) {
-      ok = wait_bar(ok, &sh.empty[r.i], r.parity, a.status);
+    for (const Patience patience(p, kGiveUpWeights); w.more(); w.next(), r.advance()) {
+      ok = wait_bar(ok, &sh.empty[r.i], r.parity, patience);
       if (!ok) break;
       __syncwarp();
       if (elect_lane()) {
@@ -1131,13 +1179,13 @@ __global__ void __launch_bounds__(kStreamThreads<SHIFT>)
     }
   } else if (warp == kMulWarp<SHIFT>) {
     // The tile reads 128 rows; what lies beyond its weights lands in rows of the sums that nobody reads.
-    multiply(w, sh, z, ring, block, a.status, [](const DownWalk& v) { return 2 * round_to(v.ntok, 8); },
+    ok = multiply(w, sh, z, ring, block, Patience(p, kGiveUpProducts), [](const DownWalk& v) { return 2 * round_to(v.ntok, 8); },
              [&](const DownWalk&) { return z.blocks * block; });
   } else if (warp >= kOutWarps) {
     await_previous_kernel();
     const int piece = lane & 7, first = (warp - kOutWarps) * 4 + (lane >> 3);
-    for (Ring r{z.stages, 0, 1}; w.more(); w.next(), r.advance()) {
-      ok = wait_bar(ok, &sh.empty[r.i], r.parity, a.status);
+    for (const Patience patience(p, kGiveUpTokens); w.more(); w.next(), r.advance()) {
+      ok = wait_bar(ok, &sh.empty[r.i], r.parity, patience);
       if (!ok) break;
       // Columns: the tokens' high parts, then from a multiple of 8 on their low parts.
       const uint32_t at = ring + r.i * z.stage_bytes + z.blocks * block;
@@ -1153,17 +1201,19 @@ __global__ void __launch_bounds__(kStreamThreads<SHIFT>)
       }
       arrive_after_copies(smem_u32(&sh.full[r.i]));
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     const int64_t tiles = gridDim.x / z.slices, tile_id = blockIdx.x / z.slices;
     const int64_t r_end = a.H * (tile_id + 1) / tiles;
     const int row = threadIdx.x;  // of the tile: this thread's sums, for every token
-    Ring d{2, 0, 0};
+    const Patience patience(p, kGiveUpSums);
+    Ring d(2, 0);
     for (int64_t r0 = a.H * tile_id / tiles; r0 < r_end; r0 += z.rows) {
       const int nr = r_end - r0 < z.rows ? (int)(r_end - r0) : z.rows;
       if (row < nr)
         for (int t = 0; t < a.T; ++t) ysum[t * z.rows + row] = 0.0f;
       for (; w.more() && w.r0 == r0; w.next_pass(), d.advance()) {
-        ok = wait_bar(ok, &sh.sums_full[d.i], d.parity, a.status);
+        ok = wait_bar(ok, &sh.sums_full[d.i], d.parity, patience);
         tmem_fence_after();
         if (ok && warp * 32 < nr) {
           const uint32_t at = sh.tmem + d.i * (z.cols / 2) + ((uint32_t)(warp * 32) << 16);
@@ -1191,9 +1241,7 @@ __global__ void __launch_bounds__(kStreamThreads<SHIFT>)
       }
     }
   }
-  tmem_fence_before();
-  __syncthreads();
-  tmem_fence_after();
+  meet<SHIFT>(sh, warp, ok, r, a.status);
   if (warp == kMulWarp<SHIFT>) tmem_free(sh.tmem, z.cols);
   if (z.slices == 2) {
     // The cluster's CTAs hold sums over their slices for the same columns of y
@@ -1306,6 +1354,8 @@ bool tensor_map(CUtensorMap* map, const void* base, int64_t nx, int64_t ny, int6
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+std::atomic<uint32_t> g_give_up{0};  // moe_test_block_waits
+
 constexpr int kMaxSms = 192;             // that the layer uses: bounds the workspace
 constexpr int kSmBytes = 226 * 1024;  // dynamic shared memory of a CTA at most, beside its static part
 
@@ -1335,7 +1385,7 @@ template <bool SHIFT> int run_stream(const LayerArgs& a, float* parts, cudaStrea
   static std::atomic<bool> raised_g[kSmemDevices], raised_d[kSmemDevices];
   __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(a.h);
   const int64_t h_ld = padded_row(a.F), y_n = a.T * a.H, parts_ld = (y_n + 3) / 4 * 4;
-  const StreamArgs p{a, h, h + a.n * h_ld, h_ld, parts, parts_ld};
+  const StreamArgs p{a, h, h + a.n * h_ld, h_ld, parts, parts_ld, g_give_up.load(std::memory_order_relaxed)};
   const int64_t sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
   const size_t seg = segments_bytes(a.n, a.E);
   // Tokens of an expert at a time: twice the mean and 16, so that few experts
@@ -1531,3 +1581,5 @@ extern "C" int moe_experts(const void* x, int32_t dtype, int64_t x_stride, const
   return run_layer(x, dtype, x_stride, nullptr, w_gate_up, w_down, T, H, F, E, K, 0, 0, nullptr, nullptr, top_expert,
                    weights, y, workspace, workspace_bytes, d_status, stream);
 }
+
+extern "C" void moe_test_block_waits(uint32_t give_up) { g_give_up.store(give_up, std::memory_order_relaxed); }

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import padded_permute_combine_gb300 as p
+from padded_permute_combine_gb300 import _lib
 from test_gpu_block import BF, DEV, F32, check, experts_ref, layer_inputs, randn
 
 pytestmark = pytest.mark.gpu
@@ -49,3 +50,33 @@ def test_layer_norm_bwd_types_of_columns_without_a_weight(M, H):
         got = p.moe_layer_norm_bwd(dy, x, None, mean, rstd, weight_dtype=dtype)
         assert got[1].dtype is got[2].dtype is dtype
         assert all(torch.equal(a, b.to(a.dtype)) for a, b in zip(got, (dx, dw, db)))
+
+
+@pytest.fixture
+def give_up():
+    """Makes waits inside the kernels give up at once; restored at the end."""
+    lib = _lib.load()
+    yield lib.moe_test_block_waits
+    torch.cuda.synchronize()
+    lib.moe_test_block_waits(0)
+
+
+# One SM, two and more to a tile of y's columns; rows on 16 bytes and off them.
+@pytest.mark.parametrize("T,H,F,E,K", [(16, 1024, 1040, 8, 2), (8, 7168, 512, 32, 8), (3, 12288, 520, 6, 1),
+                                       (16, 1025, 1041, 8, 2), (8, 7167, 513, 32, 8), (3, 12289, 521, 6, 1)])
+@pytest.mark.parametrize("who", [1, 2, 4, 8, 15])
+def test_layer_that_gives_up_leaves_nothing_behind(T, H, F, E, K, who, give_up):
+    """Weights, tokens, products or sums that never come end the call with a
+    status; what was on its way is waited for, and the next call is right."""
+    x, router, wgu, wd = layer_inputs(T, H, F, E, BF, T + H)
+    y, te, w = p.moe_layer(x, router, wgu, wd, K)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    give_up(who)
+    p.moe_experts(x, te, w, wgu, wd, status=status)
+    torch.cuda.synchronize()
+    give_up(0)
+    assert int(status) == _lib.MOE_STATUS_TIMEOUT
+    status.zero_()
+    for _ in range(3):
+        assert torch.equal(p.moe_experts(x, te, w, wgu, wd, status=status), y)
+    assert int(status) == 0
