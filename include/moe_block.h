@@ -37,6 +37,9 @@ extern "C" {
  * Sums are held in fp32 and y is rounded once. A token's row depends on its
  * own experts only. The order of every sum is fixed: repeated calls give the
  * same bits.
+ * Waits inside the kernels are bounded. One that gives up (after some two
+ * seconds) sets MOE_STATUS_TIMEOUT, and what needed its data is NaN: whole rows
+ * of y, or whole columns.
  *   x         [T, H] dtype, row stride x_stride; router [E, H] dtype
  *   w_gate_up [E, 2F, H] dtype, the gate rows of an expert before its up rows
  *   w_down    [E, H, F] dtype

@@ -542,9 +542,12 @@ __global__ void __launch_bounds__(kThreads, 2) down_rows_kernel(LayerArgs a, int
 // Warps: 0..3 take sums out of tensor memory (warp w its lanes 32w ..), 4..7
 // copy tokens, 8 (SHIFT: 8..23) copies weights, the last issues the products.
 // Sums are double buffered. Every wait is bounded: a warp that gives up sets
-// MOE_STATUS_TIMEOUT and does no more work; all warps meet at the end, where
-// copies and products still in flight are waited for (bounded again) and the
-// tensor memory is freed.
+// MOE_STATUS_TIMEOUT and does no more work, nor lets others go on (it arrives
+// nowhere), so that they give up in turn. The warps that take sums out write
+// NaN where theirs did not come: to h, whence it reaches the rows of y of that
+// expert's tokens, or to the sums of y. All warps meet at the end, where copies
+// and products still in flight are waited for (bounded again) and the tensor
+// memory is freed.
 
 constexpr int kOutWarps = 4;
 constexpr int kTokenWarps = 4;
@@ -1042,13 +1045,17 @@ __global__ void __launch_bounds__(kStreamThreads<SHIFT>)
           }
         }
       }
+      if (!ok && f < w.nf) {
+        for (int i = w.i0 + (gate ? 0 : 1); i < w.i0 + w.ntok; i += 2)
+          p.h_hi[i * p.h_ld + w.f0 + f] = p.h_lo[i * p.h_ld + w.f0 + f] = __float2bfloat16_rn(__int_as_float(0x7fffffff));
+      }
       if (SHIFT && warp == 0 && w.f0 + w.nf == a.F && lane < p.h_ld - a.F) {
         for (int i = w.i0; i < w.i0 + w.ntok; ++i)
           p.h_hi[i * p.h_ld + a.F + lane] = p.h_lo[i * p.h_ld + a.F + lane] = __float2bfloat16_rn(0.0f);
       }
       tmem_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.sums_empty[d.i]));
+      if (ok && lane == 0) mbar_arrive(smem_u32(&sh.sums_empty[d.i]));
     }
   }
   meet<SHIFT>(sh, warp, ok, r, a.status);
@@ -1230,8 +1237,10 @@ __global__ void __launch_bounds__(kStreamThreads<SHIFT>)
         }
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.sums_empty[d.i]));
+        if (ok && lane == 0) mbar_arrive(smem_u32(&sh.sums_empty[d.i]));
       }
+      if (!ok && row < nr)
+        for (int t = 0; t < a.T; ++t) ysum[t * z.rows + row] = __int_as_float(0x7fffffff);
       if (row < nr && z.slices == 1) {
         __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + r0 + row;
         for (int t = 0; t < a.T; ++t) y[t * a.H] = __float2bfloat16_rn(ysum[t * z.rows + row]);

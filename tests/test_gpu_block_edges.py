@@ -80,3 +80,20 @@ def test_layer_that_gives_up_leaves_nothing_behind(T, H, F, E, K, who, give_up):
     for _ in range(3):
         assert torch.equal(p.moe_experts(x, te, w, wgu, wd, status=status), y)
     assert int(status) == 0
+
+
+@pytest.mark.parametrize("T,H,F,E,K", [(16, 1024, 1040, 8, 2), (8, 7168, 512, 32, 8), (3, 12288, 520, 6, 1), (40, 24576, 96, 4, 2),
+                                       (16, 1025, 1041, 8, 2), (8, 7167, 513, 32, 8), (3, 12289, 521, 6, 1)])
+@pytest.mark.parametrize("who", [1, 2, 4, 8, 15])
+def test_layer_that_gives_up_writes_nan(T, H, F, E, K, who, give_up):
+    """No plausible number where sums did not come, whether or not the caller reads a status."""
+    x, router, wgu, wd = layer_inputs(T, H, F, E, BF, T + H)
+    y, te, w = p.moe_layer(x, router, wgu, wd, K)
+    out, ws = torch.zeros_like(y), p.block.layer_workspace(T, H, F, E, K, DEV).zero_()
+    give_up(who)
+    p.moe_experts(x, te, w, wgu, wd, out=out, workspace=ws)
+    plain = p.moe_experts(x, te, w, wgu, wd)
+    torch.cuda.synchronize()
+    give_up(0)
+    assert bool(torch.isnan(out).all()) and bool(torch.isnan(plain).all())
+    assert torch.equal(p.moe_experts(x, te, w, wgu, wd, out=out, workspace=ws), y)
