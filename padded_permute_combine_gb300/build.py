@@ -88,10 +88,13 @@ def kernel_digest(unit: str) -> str:
     changes only when what that kernel is compiled from changes, so a profile
     taken on it stays valid while other kernels, or comments, are edited."""
     h = hashlib.sha256()
-    source = os.path.join(CSRC, unit + ".cu")
-    with open(source, encoding="utf-8") as fh:
-        own = [os.path.join(CSRC, name) for name in re.findall(r'^#include "(\w+\.h)"', fh.read(), re.M)]
-    files = [source] + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [f for f in own if os.path.exists(f)]
+    files, at = [os.path.join(CSRC, unit + ".cu")], 0
+    while at < len(files):  # csrc's .h files that the unit includes, by itself or through one of them
+        with open(files[at], encoding="utf-8") as fh:
+            own = [os.path.join(CSRC, name) for name in re.findall(r'^#include "(\w+\.h)"', fh.read(), re.M)]
+        files += [f for f in own if os.path.exists(f) and f not in files]
+        at += 1
+    files += sorted(glob.glob(os.path.join(CSRC, "*.cuh")))
     for f in files:
         h.update(os.path.basename(f).encode())
         with open(f, encoding="utf-8") as fh:

@@ -18,10 +18,10 @@
 
 #include <atomic>
 
+#include "block_common.h"
 #include "bulk.cuh"
 #include "common.cuh"
 #include "moe_block.h"
-#include "smem_limit.h"
 #include "vec_math.cuh"
 
 namespace moe {
@@ -65,11 +65,6 @@ __device__ __forceinline__ void store1(__nv_bfloat16* p, int64_t i, float v) { p
 // A row's values in registers: pairs for the packed fp32 instructions where a
 // vector holds several elements (they halve the arithmetic, which bounded the
 // bf16 kernels: 4.2 TB/s without them), single floats otherwise.
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
 template <int kE> struct Pack {
   using T = uint64_t;
   static constexpr int N = kE / 2;
@@ -939,12 +934,6 @@ __global__ void __launch_bounds__(NW * kWarp) cols_kernel(const float* __restric
 }
 
 // ------------------------------------------------------------------ host
-
-// persistent_grid, without the question about occupancy where every SM gets one CTA at most.
-template <typename Kernel> int grid_for(Kernel k, int threads, size_t smem, int64_t work_ctas) {
-  if (work_ctas <= num_sms()) return work_ctas < 1 ? 1 : (int)work_ctas;
-  return persistent_grid(k, threads, smem, work_ctas);
-}
 
 constexpr int kMinParts = 304;    // CTAs of the backward pass, each with a row of partial column sums,
 constexpr int kMaxParts = 2432;   // more of them for shorter rows:

@@ -17,10 +17,10 @@
 #include <atomic>
 #include <type_traits>
 
+#include "block_common.h"
 #include "bulk.cuh"
 #include "common.cuh"
 #include "moe_block.h"
-#include "smem_limit.h"
 #include "vec_math.cuh"
 
 namespace moe {
@@ -178,11 +178,6 @@ constexpr int kCols = 4;
 template <int N> using Cols = std::integral_constant<int, N>;
 constexpr int kSliceChoices = 256;  // up to so many choices, an expert's F may be sliced (its parts lie in shared memory)
 
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
 __device__ __forceinline__ float f2_sum(uint64_t v) {
   float a, b;
   f2_unpack(v, a, b);
@@ -1294,12 +1289,6 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ------------------------------------------------------------------ host
-
-// persistent_grid, without the question about occupancy where every SM gets one CTA at most.
-template <typename Kernel> int grid_for(Kernel k, int threads, size_t smem, int64_t work_ctas) {
-  if (work_ctas <= num_sms()) return work_ctas < 1 ? 1 : (int)work_ctas;
-  return persistent_grid(k, threads, smem, work_ctas);
-}
 
 // Elements of a row padded to 32 bytes (of fp32, what 16 bytes of bf16 weights go with).
 int64_t padded_row(int64_t n) { return (n + 7) / 8 * 8; }
