@@ -71,8 +71,8 @@ int moe_experts(const void* x, int32_t dtype, int64_t x_stride, const int32_t* t
  * Testing only: bounded waits inside the kernels of this header give up at
  * once, as if what they wait for never came, so that a test can see how such a
  * call ends. Bits: the layer's copies of weights 1, its copies of tokens 2,
- * its products 4, the reading of their sums 8; 0 restores all. Process-wide;
- * not for concurrent use with real calls.
+ * its products 4, the reading of their sums 8; layer norm's copies of rows 16;
+ * 0 restores all. Process-wide; not for concurrent use with real calls.
  */
 void moe_test_block_waits(uint32_t give_up);
 
@@ -81,6 +81,8 @@ void moe_test_block_waits(uint32_t give_up);
  *   mean = sum(x) / H;  rstd = 1 / sqrt(sum((x - mean)^2) / H + eps)
  *   y    = (x - mean) * rstd * weight + bias
  * Statistics are fp32, the variance from the centred values; y is rounded once.
+ * Waits inside the kernels are bounded; what needed the data of one that gave
+ * up is NaN (whole rows, and the gradients' columns).
  *   x [rows, H] dtype, row stride x_stride; y [rows, H] dtype
  *   weight, bias [H] of weight_dtype, each nullable (1 and 0)
  *   mean, rstd [rows] fp32, nullable: what the backward pass takes.

@@ -1,10 +1,16 @@
 // What the layer norm and the few-token layer share.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "smem_limit.h"
 
 namespace moe {
+
+// The waits that moe_test_block_waits makes give up.
+constexpr uint32_t kGiveUpWeights = 1, kGiveUpTokens = 2, kGiveUpProducts = 4, kGiveUpSums = 8, kGiveUpRows = 16;
+std::atomic<uint32_t>& test_give_up();
 
 // a * b + c of two packed fp32 pairs.
 __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {

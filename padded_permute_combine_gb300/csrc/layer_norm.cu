@@ -39,6 +39,7 @@ struct FwdArgs {
   float* rstd;
   int64_t x_stride, rows, H;
   float eps;
+  int waits;  // for rows' copies: 1, or 0 (all give up at once) in tests
 };
 
 struct BwdArgs {
@@ -50,6 +51,7 @@ struct BwdArgs {
   void* dx;
   float* partial;  // [2][CTAs][H]: dweight's partial sums, then dbias's; nullptr when neither is asked for
   int64_t dy_stride, x_stride, rows, H;
+  int waits;
 };
 
 template <typename ET> __device__ __forceinline__ float load1(const void* p, int64_t i);
@@ -417,6 +419,8 @@ __global__ void __launch_bounds__(LPR ? kRowWarps * kWarp : MAXT, LPR ? 3 : 1) b
   }
 }
 
+constexpr float kNaN = __builtin_nanf("");
+
 // ------------------------------------------- rows through shared memory
 //
 // The backward pass for rows of more than 512 bytes, up to 32 KB of bf16 and 50
@@ -430,14 +434,16 @@ __global__ void __launch_bounds__(LPR ? kRowWarps * kWarp : MAXT, LPR ? 3 : 1) b
 // and one round of exchanges serve two rows. Those are a warp's cost whatever
 // it holds: with one vector a thread they bounded the kernel (79 instead of 73
 // us at 8192 x 7168 bf16, 84 with loads into registers). A slot is free again
-// after the next iteration's barrier. Waits are bounded; after one gives up
-// the CTA writes NaN instead of waiting again. (The forward pass gains nothing
-// this way: 47 us instead of 43.)
+// after the next iteration's barrier. Waits are bounded. A thread that gave up
+// makes the CTA's rows NaN from then on, and its columns; the one that copies
+// also waits once more (bounded) for what is on its way, and copies no more.
+// (The forward pass gains nothing this way: 47 us instead of 43.)
 
 constexpr int kRingThreads = 512;
-// fp32 with four vectors a thread: up to 1024 threads, for rows of 32 to 50 KB.
+// fp32 with four vectors a thread: up to 31 warps (one place of the sums is no warp's), for rows of 32 to 50 KB.
+// Registers and shared memory decide how many CTAs an SM holds.
 template <typename ET> __host__ __device__ constexpr int ring_registers(int nv) { return nv == 2 ? 96 : Elem<ET>::kBytes == 4 ? 64 : 128; }
-template <typename ET> constexpr int ring_threads(int nv) { return nv == 4 && Elem<ET>::kBytes == 4 ? 1024 : kRingThreads; }
+template <typename ET> constexpr int ring_threads(int nv) { return nv == 4 && Elem<ET>::kBytes == 4 ? (kWarp - 1) * kWarp : kRingThreads; }
 constexpr int kMaxSlots = 16;
 constexpr int kRingSm = 200 * 1024;  // shared memory of an SM for rings
 
@@ -478,6 +484,20 @@ __device__ __forceinline__ uint4 lds_vec(uint32_t p) {
   return v;
 }
 
+// What a thread does that gave up its wait: the last of the warps' places in
+// both buffers of sums, which no warp has, makes all threads' sums NaN from now
+// on, and thread 0 waits once more (bounded) for the copies on their way, from
+// `slot` on, for rows `step` apart of which `left` are left. Not inline: inside
+// the loop it cost the whole kernel 2 to 8 % (8192 x 7168 bf16 68 us alone, with
+// it inline 69 to 74).
+__device__ __noinline__ bool give_up(float4* last, uint32_t bars, int slot, int slots, uint32_t parity, int64_t left, int64_t step) {
+  last[0] = last[kWarp] = make_float4(kNaN, kNaN, kNaN, kNaN);
+  if (threadIdx.x == 0)
+    for (int i = slot; i < slot + slots - 1 && (i - slot) * step < left; ++i)
+      mbar_wait(bars + 8 * (i < slots ? i : i - slots), i < slots ? parity : parity ^ 1);
+  return false;
+}
+
 // NV vectors a thread, R rows at a time; KEEP: the weights stay in registers;
 // FULL: every thread has all its vectors.
 template <typename ET, typename WT, int NV, int R, bool KEEP, bool FULL>
@@ -489,7 +509,7 @@ __global__ void __maxnreg__(ring_registers<ET>(NV)) bwd_ring_kernel(BwdArgs a, i
   extern __shared__ __align__(128) unsigned char dyn[];
   __shared__ uint64_t bars[kMaxSlots];
   __shared__ float4 red[2][kWarp];
-  const int lane = lane_id(), warp = threadIdx.x / kWarp, warps = blockDim.x / kWarp;
+  const int lane = lane_id(), warp = threadIdx.x / kWarp;
   const int vecs = (int)(a.H / kE), apart = (int)blockDim.x * 16;
   bool in[NV];
 #pragma unroll
@@ -500,6 +520,7 @@ __global__ void __maxnreg__(ring_registers<ET>(NV)) bwd_ring_kernel(BwdArgs a, i
     for (int i = 0; i < slots; ++i) mbar_init(ring.bars + 8 * i);
     fence_mbarrier_init();
   }
+  for (int i = threadIdx.x; i < 2 * kWarp; i += blockDim.x) red[i / kWarp][i % kWarp] = make_float4(0, 0, 0, 0);
   await_previous_kernel();
   __syncthreads();
   const int64_t x_stride = a.x_stride * Elem<ET>::kBytes, dy_stride = a.dy_stride * Elem<ET>::kBytes;
@@ -535,7 +556,8 @@ __global__ void __maxnreg__(ring_registers<ET>(NV)) bwd_ring_kernel(BwdArgs a, i
       mean[r] = r == 0 || second ? __ldg(a.mean + row + r) : 0.0f;
       rstd[r] = r == 0 || second ? __ldg(a.rstd + row + r) : 0.0f;
     }
-    ok = ok && mbar_wait(ring.bars + 8 * slot, parity);
+    ok = ok && ((a.waits && mbar_wait(ring.bars + 8 * slot, parity)) ||
+                give_up(&red[0][kWarp - 1], ring.bars, slot, slots, parity, a.rows - row, step));
     const uint32_t at = ring.data + slot * ring.slot_bytes + threadIdx.x * 16;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -573,9 +595,9 @@ __global__ void __maxnreg__(ring_registers<ET>(NV)) bwd_ring_kernel(BwdArgs a, i
     sums();
     if (lane == 0) red[buf][warp] = make_float4(s0[0], s0[R - 1], s1[0], s1[R - 1]);
     __syncthreads();
-    const float4 p = lane < warps ? red[buf][lane] : make_float4(0, 0, 0, 0);
+    const float4 p = red[buf][lane];
     buf ^= 1;
-    if (threadIdx.x == 0) {  // everybody has read the slot before this one
+    if (threadIdx.x == 0 && ok) {  // everybody has read the slot before this one
       fence_async_shared();
       fill(slot == 0 ? slots - 1 : slot - 1, row + (slots - 1) * step);
     }
@@ -587,7 +609,7 @@ __global__ void __maxnreg__(ring_registers<ET>(NV)) bwd_ring_kernel(BwdArgs a, i
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (r == 1 && !second) break;
-      const T m2 = P::splat(mean[r]), r2 = P::splat(ok ? rstd[r] : __int_as_float(0x7fffffff));
+      const T m2 = P::splat(mean[r]), r2 = P::splat(ok ? rstd[r] : kNaN);
       const T c0 = P::splat(s0[r] * inv_h), c1 = P::splat(-s1[r] * inv_h);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -620,10 +642,10 @@ __global__ void __maxnreg__(ring_registers<ET>(NV)) bwd_ring_kernel(BwdArgs a, i
     for (int q = 0; q < P::N; ++q) {
       float v[2];
       P::put(aw[j][q], v);
-      if (!ok) v[0] = v[1] = __int_as_float(0x7fffffff);
+      if (!ok) v[0] = v[1] = kNaN;
       *reinterpret_cast<float2*>(pw + 2 * q) = make_float2(v[0], v[1]);
       P::put(ab[j][q], v);
-      if (!ok) v[0] = v[1] = __int_as_float(0x7fffffff);
+      if (!ok) v[0] = v[1] = kNaN;
       *reinterpret_cast<float2*>(pb + 2 * q) = make_float2(v[0], v[1]);
     }
   }
@@ -686,8 +708,9 @@ template <typename ET, typename WT, int NC> __global__ void __launch_bounds__(kC
       bulk_wait_all();  // the last results have left shared memory
       if (ok) bulk_load(smem_u32(dyn), x, (uint32_t)(m * sizeof(ET)), smem_u32(&bar));
     }
-    // Bounded; a copy that does not land gets a second wait, then NaN is written.
-    ok = ok && (mbar_wait(smem_u32(&bar), parity) || (mbar_wait(smem_u32(&bar), parity), false));
+    // Bounded; a copy that does not land gets a second wait, then the row's
+    // sums are NaN, whichever of its threads gave up.
+    ok = ok && ((a.waits && mbar_wait(smem_u32(&bar), parity)) || (mbar_wait(smem_u32(&bar), parity), false));
     parity ^= 1;
     if (m < n) {
       if (t < n - m) sm[m + t] = x[m + t];
@@ -698,6 +721,7 @@ template <typename ET, typename WT, int NC> __global__ void __launch_bounds__(kC
       float s[1] = {0.0f}, d[1] = {0.0f};
 #pragma unroll 8
       for (int c = lane; c < H; c += kWarp) s[0] += to_float(r[c]);
+      if (!ok) s[0] = kNaN;
       lane_sum<1, kWarp>(s);
       const float mean = s[0] * inv_h;
 #pragma unroll 8
@@ -706,7 +730,7 @@ template <typename ET, typename WT, int NC> __global__ void __launch_bounds__(kC
         d[0] = fmaf(e, e, d[0]);
       }
       lane_sum<1, kWarp>(d);
-      const float rstd = ok ? rsqrtf(d[0] * inv_h + a.eps) : __int_as_float(0x7fffffff);
+      const float rstd = rsqrtf(d[0] * inv_h + a.eps);
       if (lane == 0) {
         stat[warp] = make_float2(mean, rstd);
         if (a.mean != nullptr) a.mean[row + warp] = mean;
@@ -773,7 +797,7 @@ template <typename ET, typename WT, int NC> __global__ void __launch_bounds__(kC
       mean = __ldg(a.mean + row + warp);
       rstd = __ldg(a.rstd + row + warp);
     }
-    ok = ok && (mbar_wait(smem_u32(&bar), parity) || (mbar_wait(smem_u32(&bar), parity), false));
+    ok = ok && ((a.waits && mbar_wait(smem_u32(&bar), parity)) || (mbar_wait(smem_u32(&bar), parity), false));
     parity ^= 1;
     if (m < n) {
       if (t < n - m) {
@@ -791,8 +815,9 @@ template <typename ET, typename WT, int NC> __global__ void __launch_bounds__(kC
         s0 += v;
         s1 = fmaf(v, (to_float(rx[c]) - mean) * rstd, s1);
       }
+      if (!ok) s0 = s1 = kNaN;
       warp_sum2(s0, s1);
-      if (lane == 0) stat[warp] = make_float4(mean, ok ? rstd : __int_as_float(0x7fffffff), s0 * inv_h, -s1 * inv_h);
+      if (lane == 0) stat[warp] = make_float4(mean, rstd, s0 * inv_h, -s1 * inv_h);
     }
     __syncthreads();
     for (int r = 0; r < rows; ++r) {
@@ -803,7 +828,7 @@ template <typename ET, typename WT, int NC> __global__ void __launch_bounds__(kC
         if (c < H) {
           const float dyv = to_float(sd[r * H + c]), xhat = (to_float(sx[r * H + c]) - st.x) * st.y;
           aw[j] = fmaf(dyv, xhat, aw[j]);
-          ab[j] += ok ? dyv : __int_as_float(0x7fffffff);
+          ab[j] += dyv;
           sx[r * H + c] = from_float<ET>(fmaf(xhat, st.w, fmaf(dyv, w[j], -st.z)) * st.y);
         }
       }
@@ -825,8 +850,8 @@ template <typename ET, typename WT, int NC> __global__ void __launch_bounds__(kC
   for (int j = 0; j < NC; ++j) {
     const int c = t + j * kChunkThreads;
     if (c < H) {
-      pw[c] = aw[j];
-      pb[c] = ab[j];
+      pw[c] = ok ? aw[j] : kNaN;
+      pb[c] = ok ? ab[j] : kNaN;
     }
   }
 }
@@ -1058,24 +1083,13 @@ int go_bwd(const BwdArgs& a, int* parts, cudaStream_t s) {
 template <typename ET, typename WT, int NV, int R, bool KEEP, bool FULL = false>
 int go_ring(const BwdArgs& a, int* parts, cudaStream_t s) {
   static std::atomic<bool> raised[kSmemDevices];
-  static std::atomic<int> registers{0};
   RingShape z;
   const int64_t vecs = a.H / Lanes<16, ET>::kElems;
   if constexpr (!FULL) {
     if (vecs == (int64_t)cta_threads(vecs, NV) * NV) return go_ring<ET, WT, NV, R, KEEP, true>(a, parts, s);
   }
   auto k = bwd_ring_kernel<ET, WT, NV, R, KEEP, FULL>;
-  int regs = registers.load(std::memory_order_relaxed);
-  if (regs == 0) {  // they and shared memory decide how many CTAs an SM holds
-    cudaFuncAttributes f;
-    if (cudaFuncGetAttributes(&f, k) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return MOE_ERR_CUDA;
-    }
-    regs = f.numRegs;
-    registers.store(regs, std::memory_order_relaxed);
-  }
-  if (!ring_shape(vecs, NV, R, regs, ring_threads<ET>(NV), a.rows, bwd_parts(a.rows, a.H), &z) ||
+  if (!ring_shape(vecs, NV, R, ring_registers<ET>(NV), ring_threads<ET>(NV), a.rows, bwd_parts(a.rows, a.H), &z) ||
       !allow_smem(k, raised))
     return MOE_ERR_CUDA;
   *parts = z.grid;
@@ -1116,6 +1130,8 @@ template <typename ET> bool rows_by_16(int64_t H, const int64_t* strides, int ns
   for (int i = 0; i < np; ++i) ok = ok && aligned(ptrs[i], 16);
   return ok;
 }
+
+int row_waits() { return test_give_up().load(std::memory_order_relaxed) & kGiveUpRows ? 0 : 1; }
 
 int shape_checks(int32_t dtype, int32_t wdtype, int64_t rows, int64_t H) {
   if (rows < 0 || H < 1) return MOE_ERR_INVALID_ARG;
@@ -1180,7 +1196,7 @@ extern "C" int moe_layer_norm_fwd(const void* x, int32_t dtype, int64_t x_stride
       !aligned(rstd, 4))
     return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
-  const FwdArgs a{x, weight, bias, y, mean, rstd, x_stride, rows, H, eps};
+  const FwdArgs a{x, weight, bias, y, mean, rstd, x_stride, rows, H, eps, row_waits()};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == MOE_F32) return wdtype == MOE_F32 ? run_fwd<float, float>(a, s) : run_fwd<float, __nv_bfloat16>(a, s);
   return wdtype == MOE_F32 ? run_fwd<__nv_bfloat16, float>(a, s) : run_fwd<__nv_bfloat16, __nv_bfloat16>(a, s);
@@ -1209,7 +1225,7 @@ extern "C" int moe_layer_norm_bwd(const void* dy, int64_t dy_stride, const void*
     return MOE_ERR_UNSUPPORTED;
   if (rows == 0 && !cols) return MOE_OK;
   const BwdArgs a{dy, x, weight, mean, rstd, dx, cols ? static_cast<float*>(workspace) : nullptr,
-                  dy_stride, x_stride, rows, H};
+                  dy_stride, x_stride, rows, H, row_waits()};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == MOE_F32)
     return wdtype == MOE_F32 ? run_bwd<float, float>(a, dweight, dbias, s)

@@ -557,8 +557,6 @@ constexpr int kTileRows = 128;   // weight rows of a product
 constexpr int kMaxTokens = 128;  // of an expert at a time (256 tokens of the Mixtral-8x7B shape: 788 us, with 64: 985)
 constexpr uint64_t kWaitNs = 2000000000;  // after which a wait gives up
 constexpr uint64_t kTestWaitNs = 20000000;  // the same while moe_test_block_waits makes some give up at once
-// The warps whose waits it makes give up.
-constexpr uint32_t kGiveUpWeights = 1, kGiveUpTokens = 2, kGiveUpProducts = 4, kGiveUpSums = 8;
 
 __device__ __forceinline__ uint32_t align_1k(uint32_t p) { return (p + 1023u) & ~1023u; }
 __host__ __device__ constexpr int round_to(int v, int m) { return (v + m - 1) / m * m; }
@@ -1352,8 +1350,6 @@ bool tensor_map(CUtensorMap* map, const void* base, int64_t nx, int64_t ny, int6
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-std::atomic<uint32_t> g_give_up{0};  // moe_test_block_waits
-
 constexpr int kMaxSms = 192;             // that the layer uses: bounds the workspace
 constexpr int kSmBytes = 226 * 1024;  // dynamic shared memory of a CTA at most, beside its static part
 
@@ -1383,7 +1379,7 @@ template <bool SHIFT> int run_stream(const LayerArgs& a, float* parts, cudaStrea
   static std::atomic<bool> raised_g[kSmemDevices], raised_d[kSmemDevices];
   __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(a.h);
   const int64_t h_ld = padded_row(a.F), y_n = a.T * a.H, parts_ld = (y_n + 3) / 4 * 4;
-  const StreamArgs p{a, h, h + a.n * h_ld, h_ld, parts, parts_ld, g_give_up.load(std::memory_order_relaxed)};
+  const StreamArgs p{a, h, h + a.n * h_ld, h_ld, parts, parts_ld, test_give_up().load(std::memory_order_relaxed)};
   const int64_t sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
   const size_t seg = segments_bytes(a.n, a.E);
   // Tokens of an expert at a time: twice the mean and 16, so that few experts
@@ -1553,6 +1549,12 @@ int run_layer(const void* x, int32_t dtype, int64_t x_stride, const void* router
 }
 
 }  // namespace
+
+std::atomic<uint32_t>& test_give_up() {
+  static std::atomic<uint32_t> bits{0};
+  return bits;
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -1580,4 +1582,4 @@ extern "C" int moe_experts(const void* x, int32_t dtype, int64_t x_stride, const
                    weights, y, workspace, workspace_bytes, d_status, stream);
 }
 
-extern "C" void moe_test_block_waits(uint32_t give_up) { g_give_up.store(give_up, std::memory_order_relaxed); }
+extern "C" void moe_test_block_waits(uint32_t give_up) { test_give_up().store(give_up, std::memory_order_relaxed); }

@@ -97,3 +97,29 @@ def test_layer_that_gives_up_writes_nan(T, H, F, E, K, who, give_up):
     give_up(0)
     assert bool(torch.isnan(out).all()) and bool(torch.isnan(plain).all())
     assert torch.equal(p.moe_experts(x, te, w, wgu, wd, out=out, workspace=ws), y)
+
+
+# Backward through rings of two and of four vectors a thread; rows off 16 bytes, eight at a time, forward and (the last:
+# two arrays of eight such rows are too much for it) backward. What has no copies to wait for gives its ordinary results.
+@pytest.mark.parametrize("M,H,dtype,copies", [(1300, 7168, BF, "b"), (3, 1000, BF, "b"), (701, 9000, BF, "b"), (700, 2048, F32, "b"),
+                                              (300, 12800, F32, "b"), (1301, 1001, BF, "fb"), (2439, 303, F32, "fb"),
+                                              (1223, 4095, BF, "f")])
+def test_layer_norm_that_gives_up_writes_nan(M, H, dtype, copies, give_up):
+    """Rows that never come leave no plausible number, neither in their own threads' columns nor in the others'; the copies
+    on their way are waited for, and the next call is right."""
+    x, dy, w = randn((M, H), 1, dtype), randn((M, H), 2, dtype), randn((H,), 3)
+    fwd = p.moe_layer_norm_fwd(x, w, w)
+    stats = fwd[1:]
+    bwd = p.moe_layer_norm_bwd(dy, x, w, *stats)
+    give_up(16)
+    fwd2, bwd2 = p.moe_layer_norm_fwd(x, w, w), p.moe_layer_norm_bwd(dy, x, w, *stats)
+    torch.cuda.synchronize()
+    give_up(0)
+    for which, got, ordinary in (("f", fwd2, fwd), ("b", bwd2, bwd)):
+        if which in copies:
+            assert all(bool(torch.isnan(t).all()) for t in got)
+        else:
+            assert all(torch.equal(a, b) for a, b in zip(got, ordinary))
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(p.moe_layer_norm_fwd(x, w, w), fwd))
+        assert all(torch.equal(a, b) for a, b in zip(p.moe_layer_norm_bwd(dy, x, w, *stats), bwd))
