@@ -16,10 +16,14 @@ the definitions the pages give:
   y[t] = sum_k w[a] * xe[row(a)], whose gradient is w[a] * dy[t] for the expert
   rows (the weighted gather) and dot(xe[row(a)], dy[t]) for the weights (wgrad).
 - LayerNorm (the norm in front of the router): moe_layer_norm_fwd / _bwd.
+
+The gradients have no graph of their own: differentiating one (a gradient
+penalty, say) raises instead of leaving its term out.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import block, ops
 
@@ -37,6 +41,7 @@ class RoutingMapToIndices(torch.autograd.Function):
         return probs_indices, indices
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_probs_indices, grad_indices):
         (indices,) = ctx.saved_tensors
         if grad_probs_indices is None:
@@ -65,6 +70,7 @@ class Permute(torch.autograd.Function):
                                      positions=route.positions)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_xe):
         r, g = ctx.route, grad_xe.contiguous()
         if ctx.capacity is not None:
@@ -92,6 +98,7 @@ class Combine(torch.autograd.Function):
         return ops.moe_binned_scatter(xe, r.indices, r.bin_ids, r.bins, w, num_tokens, top_k, positions=r.positions)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_y):
         xe, w = ctx.saved_tensors
         r, K, dy = ctx.route, ctx.top_k, grad_y.contiguous()
@@ -137,6 +144,7 @@ class LayerNorm(torch.autograd.Function):
         return y.view(x.shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_y):
         rows, weight, mean, rstd = ctx.saved_tensors
         cols = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]

@@ -6,6 +6,7 @@ import torch
 
 import padded_permute_combine_gb300 as p
 from padded_permute_combine_gb300 import _lib
+from padded_permute_combine_gb300 import autograd as ag
 from test_gpu_block import BF, DEV, F32, check, experts_ref, layer_inputs, randn
 
 pytestmark = pytest.mark.gpu
@@ -123,3 +124,20 @@ def test_layer_norm_that_gives_up_writes_nan(M, H, dtype, copies, give_up):
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(p.moe_layer_norm_fwd(x, w, w), fwd))
         assert all(torch.equal(a, b) for a, b in zip(p.moe_layer_norm_bwd(dy, x, w, *stats), bwd))
+
+
+def test_gradients_are_not_differentiated_in_silence():
+    """A second derivative that the functions do not have is an error, not a missing term."""
+    T, H, E, K = 6, 32, 4, 2
+    x, w = randn((T, H), 1).requires_grad_(), randn((H,), 2).requires_grad_()
+    probs = torch.softmax(randn((T, E), 3), 1).requires_grad_()
+    chosen = torch.zeros(T, E, dtype=torch.bool, device=DEV).scatter(1, probs.topk(K).indices, True)
+    weights, index = ag.routing_map_to_mok_inputs(probs, chosen, K)
+    route = p.moe_route_build(index, E)
+    xe = randn((E, T, H), 4).requires_grad_()
+    share = weights.detach().requires_grad_()
+    for out, leaf in ((ag.layer_norm(x, w), x), (ag.layer_norm(x, w), w), (weights, probs), (ag.permute(x, route, E, T, K), x),
+                      (ag.combine(xe, share, route, T, K), xe), (ag.combine(xe, share, route, T, K), share)):
+        (grad,) = torch.autograd.grad(out.square().sum(), leaf, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            grad.square().sum().backward()
