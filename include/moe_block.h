@@ -9,7 +9,8 @@
  * no allocation, work enqueued on `stream` without a host synchronisation,
  * outputs written completely and not aliasing inputs (moe_clip_grads may
  * write in place), MOE_* return codes before anything is enqueued, MOE_STATUS_*
- * bits OR-ed into a nullable `d_status`.
+ * bits OR-ed into a nullable `d_status`. The current device is the one of the
+ * pointers and the stream.
  * Rows passed with a stride (`*_stride`, in elements, from one row to the
  * next) are contiguous inside a row; the stride is at least the row's length
  * (any value for fewer than two rows).

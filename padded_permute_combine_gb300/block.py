@@ -9,6 +9,7 @@ step here, with a message for what is wrong.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Sequence
 
@@ -23,6 +24,15 @@ _MODES = {"softmax": _lib.MOE_GATING_SOFTMAX, "sigmoid": _lib.MOE_GATING_SIGMOID
 def _stream(device: torch.device) -> int:
     # torch.cuda.current_stream(device).cuda_stream without building the Stream object (2 us).
     return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+_SAME = contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """Makes the tensors' device current for a C call, whose launches, SM
+    counts and limits are those of the current device."""
+    return _SAME if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _rows(t: torch.Tensor, name: str, dtype: torch.dtype | None = None, shape=None, device=None) -> int:
@@ -122,9 +132,10 @@ def moe_layer(x: torch.Tensor, router: torch.Tensor, w_gate_up: torch.Tensor, w_
     out_at = _take(out, (T, H), x.dtype, "out", dev)
     lib = _lib.load()
     ws = _workspace(workspace, lib.moe_layer_workspace_size(T, H, F, E, top_k), dev)
-    rc = lib.moe_layer(
-        x.data_ptr(), dt, stride, router_at, gate_up, down, T, H, F, E, top_k, _MODES[mode], int(bool(normalize)),
-        te_at, w_at, out_at, ws.data_ptr(), ws.numel(), _status(status, dev), _stream(dev))
+    with _on(dev):
+        rc = lib.moe_layer(
+            x.data_ptr(), dt, stride, router_at, gate_up, down, T, H, F, E, top_k, _MODES[mode], int(bool(normalize)),
+            te_at, w_at, out_at, ws.data_ptr(), ws.numel(), _status(status, dev), _stream(dev))
     _done("moe_layer", rc)
     return out, te, w
 
@@ -154,9 +165,10 @@ def moe_experts(x: torch.Tensor, top_expert: torch.Tensor, weights: torch.Tensor
     out_at = _take(out, (T, H), x.dtype, "out", dev)
     lib = _lib.load()
     ws = _workspace(workspace, lib.moe_layer_workspace_size(T, H, F, E, K), dev)
-    rc = lib.moe_experts(
-        x.data_ptr(), dt, stride, top_expert.data_ptr(), w_at, gate_up, down, T, H, F, E, K, out_at, ws.data_ptr(),
-        ws.numel(), _status(status, dev), _stream(dev))
+    with _on(dev):
+        rc = lib.moe_experts(
+            x.data_ptr(), dt, stride, top_expert.data_ptr(), w_at, gate_up, down, T, H, F, E, K, out_at, ws.data_ptr(),
+            ws.numel(), _status(status, dev), _stream(dev))
     _done("moe_experts", rc)
     return out
 
@@ -203,8 +215,9 @@ def moe_layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias
         mean, rstd = stats
         mean_at = _take(mean, (M,), torch.float32, "mean", dev)
         rstd_at = _take(rstd, (M,), torch.float32, "rstd", dev)
-    rc = _lib.load().moe_layer_norm_fwd(
-        x.data_ptr(), dt, stride, weight_at, bias_at, wdt, M, H, eps, out_at, mean_at, rstd_at, _stream(dev))
+    with _on(dev):
+        rc = _lib.load().moe_layer_norm_fwd(
+            x.data_ptr(), dt, stride, weight_at, bias_at, wdt, M, H, eps, out_at, mean_at, rstd_at, _stream(dev))
     _done("moe_layer_norm_fwd", rc)
     return out, mean, rstd
 
@@ -246,9 +259,10 @@ def moe_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor |
         db = torch.empty(H, dtype=weight_dtype, device=dev)
         ws = _workspace(workspace, lib.moe_layer_norm_bwd_workspace_size(M, H), dev)
         dw_at, db_at, ws_at, ws_bytes = dw.data_ptr(), db.data_ptr(), ws.data_ptr(), ws.numel()
-    rc = lib.moe_layer_norm_bwd(
-        dy.data_ptr(), dy_stride, x.data_ptr(), dt, stride, weight_at, code, mean_at, rstd_at, M, H, out_at, dw_at, db_at,
-        ws_at, ws_bytes, _stream(dev))
+    with _on(dev):
+        rc = lib.moe_layer_norm_bwd(
+            dy.data_ptr(), dy_stride, x.data_ptr(), dt, stride, weight_at, code, mean_at, rstd_at, M, H, out_at, dw_at, db_at,
+            ws_at, ws_bytes, _stream(dev))
     _done("moe_layer_norm_bwd", rc)
     return out, dw, db
 
@@ -307,8 +321,9 @@ def moe_grad_norm(grads: GradSet | Sequence[torch.Tensor], norm: torch.Tensor | 
         if done is not None:
             return done[0]
     s, norm, ws = _grad_args(grads, norm, workspace)
-    rc = _lib.load().moe_grad_norm(
-        s.table.data_ptr(), s.pieces, norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream(s.device))
+    with _on(s.device):
+        rc = _lib.load().moe_grad_norm(
+            s.table.data_ptr(), s.pieces, norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream(s.device))
     _done("moe_grad_norm", rc)
     return norm
 
@@ -322,7 +337,8 @@ def moe_clip_grads(grads: GradSet | Sequence[torch.Tensor], max_norm: float, nor
         if done is not None:
             return done[0]
     s, norm, ws = _grad_args(grads, norm, workspace)
-    rc = _lib.load().moe_clip_grads(
-        s.table.data_ptr(), s.pieces, max_norm, norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream(s.device))
+    with _on(s.device):
+        rc = _lib.load().moe_clip_grads(
+            s.table.data_ptr(), s.pieces, max_norm, norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream(s.device))
     _done("moe_clip_grads", rc)
     return norm

@@ -11,6 +11,7 @@
 #include <Python.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty_cuda_dispatch.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -36,6 +37,8 @@ bool rows_ok(const Tensor& t, int64_t* stride) {
 bool plain(const Tensor& t, const Tensor& x, at::ScalarType type, at::IntArrayRef sizes) {
   return t.scalar_type() == type && t.device() == x.device() && t.is_contiguous() && t.sizes() == sizes;
 }
+// The C ABI works on the current device: its launches, SM counts and limits.
+using c10::cuda::CUDAGuard;
 Tensor make(const Tensor& x, at::ScalarType type, at::IntArrayRef sizes) {
   return at::cuda::empty(sizes, at::TensorOptions().dtype(type).device(x.device()));
 }
@@ -112,6 +115,7 @@ PyObject* layer_norm_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
     int64_t stride;
     if (n != 4 || !tensors(args, 3, t, 6) || !PyFloat_Check(args[3]) || !rows_ok(t[0], &stride)) return nullptr;
     const Tensor &x = t[0], &w = t[1], &b = t[2];
+    const CUDAGuard current(x.device());
     const int64_t M = x.size(0), H = x.size(1);
     const float eps = (float)PyFloat_AS_DOUBLE(args[3]);
     const at::ScalarType wt = w.defined() ? w.scalar_type() : b.defined() ? b.scalar_type() : at::kFloat;
@@ -134,6 +138,7 @@ PyObject* layer_norm_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
     int64_t stride, dy_stride;
     if (n != 6 || !tensors(args, 5, t, 4) || !rows_ok(t[1], &stride) || !rows_ok(t[0], &dy_stride)) return nullptr;
     const Tensor &dy = t[0], &x = t[1], &w = t[2], &mean = t[3], &rstd = t[4];
+    const CUDAGuard current(x.device());
     const int64_t M = x.size(0), H = x.size(1);
     const at::ScalarType wt = w.defined() ? w.scalar_type() : at::kFloat;
     if (dy.scalar_type() != x.scalar_type() || dy.device() != x.device() || dy.sizes() != x.sizes() || !plain(mean, x, at::kFloat, {M}) ||
@@ -174,6 +179,7 @@ PyObject* layer(PyObject*, PyObject* const* args, Py_ssize_t n) {
     int64_t stride, E, F;
     if (n != 7 || !tensors(args, 4, t) || !PyLong_Check(args[4]) || !rows_ok(t[0], &stride)) return nullptr;
     const Tensor &x = t[0], &router = t[1], &gate_up = t[2], &down = t[3];
+    const CUDAGuard current(x.device());
     const int64_t T = x.size(0), H = x.size(1), K = PyLong_AsLongLong(args[4]);
     if (!experts_ok(x, gate_up, down, &E, &F) || !plain(router, x, x.scalar_type(), {E, H}) || K < 1 || K > E) return nullptr;
     const int32_t mode = (int32_t)PyLong_AsLong(args[5]), normalize = PyObject_IsTrue(args[6]);
@@ -197,6 +203,7 @@ PyObject* experts(PyObject*, PyObject* const* args, Py_ssize_t n) {
     int64_t stride, E, F;
     if (n != 5 || !tensors(args, 5, t) || !rows_ok(t[0], &stride)) return nullptr;
     const Tensor &x = t[0], &top = t[1], &w = t[2], &gate_up = t[3], &down = t[4];
+    const CUDAGuard current(x.device());
     if (top.dim() != 2) return nullptr;
     const int64_t T = x.size(0), H = x.size(1), K = top.size(1);
     if (!experts_ok(x, gate_up, down, &E, &F) || !plain(top, x, at::kInt, {T, K}) || !plain(w, x, at::kFloat, {T, K}) || K < 1 || K > E)
@@ -219,6 +226,8 @@ PyObject* grads(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Tensor t[2];
     if ((n != 3 && n != 4) || !tensors(args, 2, t) || !PyLong_Check(args[2]) || (n == 4 && !PyFloat_Check(args[3]))) return nullptr;
     const Tensor &table = t[0], &ws = t[1];
+    if (!table.is_cuda()) return nullptr;
+    const CUDAGuard current(table.device());
     const int64_t pieces = PyLong_AsLongLong(args[2]);
     const Tensor norm = make(table, at::kFloat, {});
     const auto* p = static_cast<const moe_grad_piece*>(table.const_data_ptr());

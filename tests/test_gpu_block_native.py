@@ -96,3 +96,42 @@ for name, call in every.items():
     call()
     assert calls.value == 1 and locked.value == 0, name
 """)
+
+
+def test_calls_make_the_tensors_device_current(monkeypatch):
+    """A C call works on the current device, so another one that is current has
+    to give way for its length (there is one GPU here: which device is current
+    is faked, and the step-by-step calls' guard is seen to be entered)."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import padded_permute_combine_gb300 as p
+
+    x, w, row = torch.randn(4, 64, device="cuda"), torch.randn(64, device="cuda"), torch.ones(4, device="cuda")
+    out, norm = torch.empty_like(x), torch.empty((), device="cuda")
+    router, gate_up, down = (torch.randn(*s, device="cuda") for s in ((4, 64), (4, 32, 64), (4, 64, 16)))
+    top, share = torch.zeros(4, 2, dtype=torch.int32, device="cuda"), torch.randn(4, 2, device="cuda")
+    grads = p.moe_grad_set([torch.randn(100, device="cuda")])
+    calls = [lambda: p.moe_layer_norm_fwd(x, w, w, out=out), lambda: p.moe_layer_norm_bwd(x, x, w, row, row, out=out),
+             lambda: p.moe_layer(x, router, gate_up, down, 2, out=out), lambda: p.moe_experts(x, top, share, gate_up, down, out=out),
+             lambda: p.moe_grad_norm(grads, norm=norm), lambda: p.moe_clip_grads(grads, 1.0, norm=norm)]
+    entered = []
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            entered.append(self.device)
+
+        def __exit__(self, *_):
+            entered.append(None)
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    for call in calls:  # the tensors' device is current already
+        call()
+    assert entered == []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in calls:
+        entered.clear()
+        call()
+        assert entered == [x.device, None]
