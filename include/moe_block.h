@@ -35,7 +35,11 @@ extern "C" {
  * moe_topk_gating's), where an entry -1 is a slot without an expert: a token
  * whose slots are all -1 gets +0.0. Any other entry outside [0, E) sets
  * MOE_STATUS_BAD_EXPERT and counts as -1.
- * Sums are held in fp32 and y is rounded once. A token's row depends on its
+ * Sums are held in fp32 and y is rounded once. Larger bf16 layers (beyond some
+ * 2^24 elements of the choices' matrices, or four choices an expert) run on the
+ * tensor cores, which cut instead of rounding as they add (some 1e-5 of a sum),
+ * and keep h as the sum of two bf16 numbers, 16 significant bits; both are far
+ * below y's own rounding. A token's row depends on its
  * own experts only. The order of every sum is fixed: repeated calls give the
  * same bits.
  * Waits inside the kernels are bounded. One that gives up (after some two

@@ -24,7 +24,6 @@ MOE_STATUS_TIMEOUT = 16
 MOE_MAX_EXPERTS, MOE_MAX_TOP_K = 4096, 64
 MOE_GATING_SOFTMAX, MOE_GATING_SIGMOID = 0, 1
 MOE_GATING_MAX_EXPERTS = 1024
-MOE_LAYER_MAX_TOKENS, MOE_LAYER_MAX_CHOICES = 256, 2048
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64

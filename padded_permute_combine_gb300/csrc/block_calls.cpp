@@ -4,10 +4,11 @@
 // returns None, and block.py takes the call step by step, with its messages;
 // a call that failed once work may have been enqueued raises MoeError here.
 //
-// A call of these operators on a few rows runs for 3 to 14 us on the GPU. The
-// whole call takes 5.7 us for a layer norm forward of four rows, 9.4 backward,
-// 15 for an MoE layer of one token, some 2.2 for each launch and the rest for
-// three to five allocations; in Python the same steps took 14, 22 and 29.
+// A call of these operators on a few rows runs for 3 to 14 us on the GPU. On the
+// host the whole call takes 5.1 to 7.4 us (it varies from process to process) for
+// a layer norm forward of four rows, 8.1 to 10.7 backward, 14 to 16.2 for an MoE
+// layer of one token, some 2.2 for each launch and the rest for three to five
+// allocations; in Python the same steps took 14, 22 and 29.
 #include <Python.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty_cuda_dispatch.h>

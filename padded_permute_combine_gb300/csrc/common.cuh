@@ -171,13 +171,20 @@ __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
 // Programmatic dependent launch (every kernel of the library is launched
 // with it, see launch()): the kernel's grid may be launched while the
 // previous kernel on the stream is still finishing, so it waits here for
-// that kernel's results before its first global-memory access. No kernel
-// triggers its dependents early: the next grid launches as this one's CTAs
-// exit. (Triggering at kernel start let the next grid's CTAs settle on the
-// SMs unevenly while this one still ran, and the persistent grid-stride
-// kernels then lost more than the overlap gained: 1.11 vs 0.99 ms per
-// DeepSeek-V3-shaped routing step.) With a previous kernel that was
-// launched without the attribute, the wait is a no-op.
+// that kernel's results before its first global-memory access. The routing
+// kernels do not trigger their dependents early: the next grid launches as
+// this one's CTAs exit. (Triggering at kernel start let the next grid's CTAs
+// settle on the SMs unevenly while this one still ran, and the persistent
+// grid-stride kernels then lost more than the overlap gained: 1.11 vs 0.99 ms
+// per DeepSeek-V3-shaped routing step.) The few-token layer's kernels
+// (moe_layer.cu) do, on two rules that keep the chain whole. A kernel triggers
+// only after its own wait here, in every CTA: a dependent that starts then
+// finds all work before the triggering kernel done, and its own wait ends with
+// the triggering kernel. And only a kernel that is launched right after one
+// that triggers so may read ahead of its wait, and nothing that one writes:
+// down_stream_kernel reads the routing and copies weights while the gate/up
+// kernel before it still runs, and waits before it reads h. With a previous
+// kernel that was launched without the attribute, the wait is a no-op.
 __device__ __forceinline__ void await_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ------------------------------------------------------------------ host

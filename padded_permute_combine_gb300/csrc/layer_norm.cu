@@ -10,10 +10,12 @@
 // are on their way into registers while one is reduced. In the backward pass a
 // thread owns the same columns in every row it meets, so the two sums over
 // rows live in its registers; each CTA writes one row of partial sums, and a
-// second launch adds those in a fixed order. The backward pass takes rows of up
-// to 32 KB (fp32 50 KB) through a ring in shared memory. Packed rows that 16
-// bytes do not divide go through shared memory eight at a time. Rows too long
-// for the registers take kernels that read a row again for each pass over it.
+// second launch adds those in a fixed order. The backward pass takes rows of
+// more than 512 bytes through a ring in shared memory: bf16 up to 32 KB, fp32 up
+// to 16 KB and from 32 to 50 KB (between, they stay in registers). Packed rows
+// that 16 bytes do not divide go through shared memory eight at a time. Rows
+// too long for the registers take kernels that read a row again for each pass
+// over it.
 #include <math.h>
 
 #include <atomic>
@@ -423,11 +425,12 @@ constexpr float kNaN = __builtin_nanf("");
 
 // ------------------------------------------- rows through shared memory
 //
-// The backward pass for rows of more than 512 bytes, up to 32 KB of bf16 and 50
-// of fp32: two 16-byte vectors of the row per thread, two consecutive rows at a
-// time (four vectors and one row above 16 KB of bf16 and 32 of fp32, where a
-// second reading of the rows would follow: 2000 x 9000 fp32 55 us instead of
-// 111, 4000 x 12800 96 instead of 259), copied into a ring of slots
+// The backward pass for rows of more than 512 bytes. Up to 16 KB: two 16-byte
+// vectors of the row per thread, two consecutive rows at a time. Above, up to 32
+// KB of bf16 and from 32 to 50 of fp32, where a second reading of the rows would
+// follow (2000 x 9000 fp32 56 us instead of 111, 4000 x 12800 99 instead of
+// 259): four vectors and one row; fp32 rows of 16 to 32 KB fit in registers and
+// take bwd_kernel. The rows are copied into a ring of slots
 // by bulk copies (one for both rows where they are adjacent). What that buys
 // over loads into registers: the copies ahead cost none (they read x and dy
 // from the slot again after the sums instead of keeping them), and one barrier
@@ -929,9 +932,10 @@ template <typename ET> __global__ void __launch_bounds__(256) bwd_long_cols_kern
 
 // Adds the CTAs' partial sums: 32 columns per CTA, its NW warps each a share
 // of the parts. blockIdx.y: 0 dweight, 1 dbias. Few columns make few CTAs: 32
-// warps then, with ten loads ahead (the whole backward pass, 1531 x 1001 fp32,
-// 9.2 us, with 16 warps and four 10.4; 4000 x 1000 bf16 12.1 and 15.9), 16
-// where the columns alone fill the chip (8192 x 7168: 67.4, with 32 69.6).
+// warps then, with ten loads ahead (the whole backward pass, replayed from a
+// CUDA graph, 1531 x 1001 fp32, 9.2 us, with 16 warps and four 10.4; 4000 x 1000
+// bf16 12.1 and 15.9), 16 where the columns alone fill the chip (8192 x 7168:
+// 67.4, with 32 69.6).
 constexpr int64_t kFewCols = 2048;
 template <typename WT, int NW>
 __global__ void __launch_bounds__(NW * kWarp) cols_kernel(const float* __restrict__ partial, int parts, int64_t H,

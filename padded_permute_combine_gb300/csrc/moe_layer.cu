@@ -40,7 +40,9 @@ struct LayerArgs {
 };
 
 // Lets the next kernel on the stream start while this one runs; it waits for
-// this one's end before it reads what this one writes.
+// this one's end before it reads what this one writes. Called after
+// await_previous_kernel() alone (the rules are there); down_stream_kernel calls
+// it ahead of its own wait, since the kernel before it has waited.
 __device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ------------------------------------------------------- choices by expert
@@ -530,6 +532,19 @@ __global__ void __launch_bounds__(kThreads, 2) down_rows_kernel(LayerArgs a, int
 // 128 bytes a row, then the tokens, both in the 128-byte swizzle that the
 // tensor copies write and tcgen05 reads (16-byte piece q of row r lies at
 // place q ^ (r & 7); blocks start on 1 KB boundaries).
+//
+// All token warps take part in every stage, each with its rows. Warps that took
+// every fourth stage alone would wait for every fourth phase only, and a wait
+// tells the phases of a barrier apart by their parity: in a ring of three stages
+// such a warp took the phase before last for its own, wrote over a stage in use
+// and arrived twice. That ended in a GPU fault.
+//
+// The sums in tensor memory are fp32, but the tensor cores cut what they add
+// where an fp32 addition rounds: over the hundreds of steps of a row, sums come
+// out smaller by some 1e-5 of their size (48 tokens, 6144 x 16384: y by 1.9e-5
+// on average). Some 1 % of y's bf16 elements are the neighbour of the ones that
+// exact sums round to; the error against exact sums is that of the rounding, to
+// three digits.
 //
 // Rows that are not a multiple of 16 bytes, or do not begin on one, are out of
 // reach of tensor copies: 16 warps copy and shift their pieces.
@@ -1029,7 +1044,9 @@ __global__ void __launch_bounds__(kStreamThreads<SHIFT>)
             if (f < w.nf && col < w.ntok) {
               const int i = w.i0 + col;
               const float h = __ldcg(a.weights + s.order[i]) * (silu(g) * u);
-              // Two bf16 numbers keep 16 significant bits of h: one would round the layer's result twice.
+              // Two bf16 numbers keep 16 significant bits of h: 2^-16 of it is lost at most, where y's own
+              // rounding loses 2^-8. One alone would round the layer's result twice; three would make the
+              // second kernel's columns half as many again.
               const __nv_bfloat16 hi = __float2bfloat16_rn(h);
               const float rest = h - __bfloat162float(hi);
               p.h_hi[i * p.h_ld + w.f0 + f] = hi;
