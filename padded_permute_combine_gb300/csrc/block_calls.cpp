@@ -85,12 +85,15 @@ template <typename F> PyObject* guarded(F f) {
 
 // The C ABI's call without the interpreter's lock, as ctypes makes it: a full
 // launch queue blocks it for as long as the queue is full, and other threads
-// go on meanwhile.
-template <typename F> int unlocked(F f) {
+// go on meanwhile. The lock is taken again also when torch throws (a tensor
+// without memory, such as a fake one).
+struct Unlocked {
   PyThreadState* state = PyEval_SaveThread();
-  const int rc = f();
-  PyEval_RestoreThread(state);
-  return rc;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename F> int unlocked(F f) {
+  const Unlocked now;
+  return f();
 }
 
 // What follows a code other than MOE_OK. Refused arguments (nothing is enqueued

@@ -135,3 +135,20 @@ def test_calls_make_the_tensors_device_current(monkeypatch):
         entered.clear()
         call()
         assert entered == [x.device, None]
+
+
+def test_errors_of_torch_inside_a_call_are_exceptions():
+    """A tensor without memory raises: refused as a null pointer, or by torch while the interpreter's lock is given back."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import padded_permute_combine_gb300 as p
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    real = torch.randn(4, 64, device="cuda")
+    with FakeTensorMode():
+        fake = torch.empty(4, 64, device="cuda")
+    for call in (lambda: p.moe_layer_norm_fwd(fake), lambda: p.moe_layer_norm_bwd(fake, fake, None, real[:, 0].clone(), real[:, 0].clone())):
+        with pytest.raises(RuntimeError):
+            call()
+    y, mean, _ = p.moe_layer_norm_fwd(real)
+    assert torch.isfinite(y).all() and torch.isfinite(mean).all()
