@@ -16,6 +16,16 @@ from .block import (  # noqa: F401
     moe_layer_norm_bwd,
     moe_layer_norm_fwd,
 )
+from .decode import (  # noqa: F401
+    CacheCompact,
+    CacheFork,
+    moe_attention_decode,
+    moe_beam_select,
+    moe_cache_compact,
+    moe_cache_copy,
+    moe_cache_fork,
+    moe_cache_write,
+)
 from .ops import (  # noqa: F401
     Route,
     moe_binned_gather,

@@ -16,14 +16,19 @@ LIB_PATH = os.path.join(PKG, "libmoe_route.so")
 CALLS_PATH = os.path.join(PKG, "_block_calls.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "moe_route.h")
 BLOCK_HEADER = os.path.join(os.path.dirname(PKG), "include", "moe_block.h")
+DECODE_HEADER = os.path.join(os.path.dirname(PKG), "include", "moe_decode.h")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA = 0, 1, 2, 3
 MOE_F32, MOE_BF16 = 0, 1
 MOE_STATUS_BAD_EXPERT, MOE_STATUS_BAD_INDEX, MOE_STATUS_BAD_BINS, MOE_STATUS_ROWS_MISMATCH = 1, 2, 4, 8
 MOE_STATUS_TIMEOUT = 16
+MOE_STATUS_NO_PAGES = 32
 MOE_MAX_EXPERTS, MOE_MAX_TOP_K = 4096, 64
 MOE_GATING_SOFTMAX, MOE_GATING_SIGMOID = 0, 1
 MOE_GATING_MAX_EXPERTS = 1024
+MOE_ATTENTION_MAX_DIM = 256
+MOE_CACHE_MAX_ROWS, MOE_CACHE_MAX_PAGES, MOE_CACHE_MAX_CACHES = 4096, 1 << 22, 256
+MOE_BEAM_MAX_BEAMS, MOE_BEAM_MAX_OUT, MOE_BEAM_MAX_UNITS = 64, 128, 1 << 15
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -81,6 +86,38 @@ BLOCK_SIGNATURES = {
     "moe_clip_grads": (ctypes.c_int, [_P, _I64, ctypes.c_float, _P, _P, _SZ, _P]),
 }
 
+# The entry points of include/moe_decode.h, in its order.
+DECODE_SIGNATURES = {
+    "moe_attention_decode_workspace_size": (_SZ, [_I64, _I32, _I32, _I32]),
+    "moe_attention_decode": (ctypes.c_int, [_P, _P, _I32, _P, _I64, _I64, _P, _I64, _P, _P, ctypes.c_float, _I64, _P, _P,
+                                            _P, _SZ, _P, _P]),
+    "moe_cache_write": (ctypes.c_int, [_P, _P, _P, _I64, _P, _P, _I64, _I64, _P, _I64, _P, _P]),
+    "moe_cache_fork": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _P, _I64, _I32, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P]),
+    "moe_cache_compact": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _I32, _I64, _P, _P, _P, _P, _P, _P]),
+    "moe_cache_copy": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _I64, _P, _P, _P]),
+    "moe_beam_select_workspace_size": (_SZ, [_I64, _I32, _I64]),
+    "moe_beam_select": (ctypes.c_int, [_P, _I32, _I64, _P, _P, _I64, _I32, _I64, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
+}
+
+
+class KvCache(ctypes.Structure):
+    """moe_kv_cache."""
+
+    _fields_ = [("k", _P), ("v", _P), ("num_pages", _I64), ("page_stride", _I64), ("token_stride", _I64),
+                ("head_stride", _I64), ("dtype", _I32), ("page_size", _I32), ("num_kv_heads", _I32), ("head_dim", _I32)]
+
+
+class Heads(ctypes.Structure):
+    """moe_heads."""
+
+    _fields_ = [("data", _P), ("row_stride", _I64), ("head_stride", _I64)]
+
+
+class CachePages(ctypes.Structure):
+    """moe_cache_pages."""
+
+    _fields_ = [("data", _P), ("page_stride", _I64), ("page_bytes", _I64)]
+
 
 class GradTensor(ctypes.Structure):
     """moe_grad_tensor; moe_grad_piece has the same layout."""
@@ -116,7 +153,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
         raise RuntimeError("libmoe_route.so is not built (%s); run "
                            "`python -m padded_permute_combine_gb300.build` first" % p)
     lib = ctypes.CDLL(p)
-    for name, (res, args) in (SIGNATURES | BLOCK_SIGNATURES).items():
+    for name, (res, args) in (SIGNATURES | BLOCK_SIGNATURES | DECODE_SIGNATURES).items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

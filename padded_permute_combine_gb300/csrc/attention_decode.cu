@@ -1,0 +1,570 @@
+// Attention of one new token of every sequence over a key-value cache in pages:
+//   s_j = scale * q . k_j,  out = sum_j softmax(s)_j v_j
+//
+// Bound by HBM: every key and value of the cache is read once, for 2 * group
+// multiply-adds an element (group: query heads that share a kv head).
+//
+// One pass with a running maximum and sum: for each tile of keys m' = max(m, max s),
+// l' = l 2^(m - m') + sum 2^(s - m'), o' = o 2^(m - m') + sum 2^(s - m') v, with s in
+// units of log 2. The tiles of all sequences (16 tokens of one kv head) are one
+// long line, cut into equal ranges: a warp takes a range of one head, so long
+// sequences are split over many warps, short ones share one, and every SM gets
+// the same number of bytes whatever the lengths are. A sequence inside one range is
+// finished by its warp; the parts of the others are left in the workspace as
+// (o, m, l) and joined by a second kernel in the order of the ranges. Warps work
+// alone, each with its own ring of asynchronous copies: no barrier in the loop.
+// Neighbouring warps take neighbouring heads of the same range, so that an SM
+// reads whole rows of a page where heads lie side by side.
+#include <math.h>
+
+#include <atomic>
+
+#include "block_common.h"
+#include "bulk.cuh"
+#include "common.cuh"
+#include "moe_decode.h"
+#include "vec_math.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kTile = 16;      // tokens of a tile, the unit of the ranges
+constexpr int kSmWarps = 8;    // warps of an SM: a CTA of eight, one an SM
+constexpr int kMinTiles = 2;   // of a range, where there are fewer tiles than warps
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Quotients by a divisor known at launch, for numerators below 2^31: with
+// s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1, n / d = (mulhi(n, m) + n) >> s
+// (Granlund and Montgomery, Division by Invariant Integers, 1994).
+struct Divisor {
+  uint32_t d, m, s;
+  Divisor() : Divisor(1) {}
+  explicit Divisor(uint32_t by) : d(by), m(0), s(0) {
+    while ((1ull << s) < by) ++s;
+    m = (uint32_t)(((1ull << 32) * ((1ull << s) - by)) / by + 1);
+  }
+  __device__ __forceinline__ uint32_t of(uint32_t n) const { return (__umulhi(n, m) + n) >> s; }
+};
+
+struct AttendArgs {
+  char* k;  // the cache; strides in bytes
+  char* v;
+  int64_t page_stride, token_stride, head_stride;
+  const char* q;
+  const char* k_new;  // nullptr: the new token is in the cache already
+  const char* v_new;
+  int64_t q_row, q_head, kn_row, kn_head, vn_row, vn_head;
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* lengths;
+  void* out;
+  float* lse;
+  float* part_o;  // [slots][heads][D], not yet divided by the sum
+  float2* part_ml;  // [slots][heads]: maximum in units of log 2, and sum
+  int32_t* status;
+  Divisor page;
+  int64_t num_pages, window;
+  int32_t seqs, width, heads, kv_heads, group, D;
+  int32_t parts;       // pieces of a group, of kHeads query heads each
+  int32_t ranges;      // at most
+  int32_t max_tokens;  // table width * page size
+  float scale;         // times log2 e
+};
+
+// The positions of sequence b that are looked at: [first, n).
+__device__ __forceinline__ void span_of(const AttendArgs& a, int b, int& first, int& n) {
+  n = a.lengths[b];
+  n = n < 0 ? 0 : (n > a.max_tokens ? a.max_tokens : n);
+  first = a.window > 0 && n > a.window ? n - (int)a.window : 0;
+}
+__device__ __forceinline__ int tiles_of(const AttendArgs& a, int b) {
+  int first, n;
+  span_of(a, b, first, n);
+  return (n - first + kTile - 1) / kTile;
+}
+__device__ __forceinline__ int ranges_of(const AttendArgs& a, int total) {
+  const int most = total / kMinTiles;
+  return most < a.ranges ? (most < 1 ? 1 : most) : a.ranges;
+}
+__device__ __forceinline__ int range_begin(int r, int ranges, int total) { return (int)((int64_t)r * total / ranges); }
+// The range that tile x lies in: the last r whose begin is not behind x.
+__device__ __forceinline__ int range_at(int x, int ranges, int total) {
+  return (int)((((int64_t)x + 1) * ranges - 1) / total);
+}
+
+// Sum over the CTA of v, and in `before` the sum over the threads in front.
+__device__ __forceinline__ int block_prefix(int v, int* s_warp, int& before) {
+  const int lane = lane_id(), warp = threadIdx.x / kWarp, warps = blockDim.x / kWarp;
+  int x = v;
+#pragma unroll
+  for (int d = 1; d < kWarp; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += o;
+  }
+  if (lane == kWarp - 1) s_warp[warp] = x;
+  __syncthreads();
+  int sum = 0, total = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w < warp) sum += s_warp[w];
+    total += s_warp[w];
+  }
+  before = sum + x - v;
+  return total;
+}
+
+// Where a warp is in the line of tiles.
+struct Cursor {
+  int b, tile, tiles, first, n;
+  __device__ __forceinline__ void enter(const AttendArgs& a) {
+    span_of(a, b, first, n);
+    tiles = (n - first + kTile - 1) / kTile;
+  }
+  __device__ __forceinline__ void next(const AttendArgs& a) {  // there is a next tile
+    if (++tile < tiles) return;
+    tile = 0;
+    do {
+      ++b;
+      enter(a);
+    } while (tiles == 0);
+  }
+};
+
+// The CTA's view of the line: prefix[t] tiles in front of the sequences of thread t.
+__device__ __forceinline__ int line_prefix(const AttendArgs& a, int* prefix, int* s_warp) {
+  const int t = threadIdx.x, chunk = (a.seqs + blockDim.x - 1) / blockDim.x;
+  int mine = 0;
+  for (int b = t * chunk; b < a.seqs && b < (t + 1) * chunk; ++b) {
+    if (blockIdx.x == 0 && (a.lengths[b] < 0 || a.lengths[b] > a.max_tokens)) flag_status(a.status, MOE_STATUS_BAD_INDEX);
+    mine += tiles_of(a, b);
+  }
+  int before;
+  const int total = block_prefix(mine, s_warp, before);
+  prefix[t] = before;
+  __syncthreads();
+  return total;
+}
+__device__ __forceinline__ Cursor find_tile(const AttendArgs& a, const int* prefix, int x) {
+  const int chunk = (a.seqs + blockDim.x - 1) / blockDim.x;
+  int lo = 0, hi = blockDim.x;  // the last thread with prefix <= x
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (prefix[mid] <= x) lo = mid; else hi = mid;
+  }
+  Cursor c;
+  c.b = lo * chunk;
+  c.tile = x - prefix[lo];
+  c.enter(a);
+  while (c.tile >= c.tiles) {
+    c.tile -= c.tiles;
+    ++c.b;
+    c.enter(a);
+  }
+  return c;
+}
+
+// Where the keys of a tile are: each of the lanes 0 to 15 answers for one
+// position, with its page's number and then its offset in bytes (-1: absent).
+__device__ __forceinline__ int page_entry(const AttendArgs& a, const Cursor& c, int row) {
+  const int pos = c.first + c.tile * kTile + row;
+  return pos < c.n ? a.table[c.b * a.table_stride + a.page.of(pos)] : -1;
+}
+__device__ __forceinline__ int64_t row_offset(const AttendArgs& a, const Cursor& c, int row, int page, int kv) {
+  const int pos = c.first + c.tile * kTile + row;
+  if (pos >= c.n) return -1;
+  if (page < 0 || page >= a.num_pages) {
+    flag_status(a.status, MOE_STATUS_BAD_INDEX);
+    return -1;
+  }
+  return page * a.page_stride + (pos - a.page.of(pos) * a.page.d) * a.token_stride + kv * a.head_stride;
+}
+
+template <typename ET> __device__ __forceinline__ float to_float(ET v);
+template <> __device__ __forceinline__ float to_float<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Heads' rows on the ordinary cores, in fp32: a warp takes 8 keys at a time.
+// Scores: lane (key, quarter) takes the fourth of the key's elements that
+// `quarter` says, in pieces of four, for all GM heads; values: a lane owns
+// pieces of four of a row's elements for all heads.
+template <typename ET, int GM, int NC>
+__global__ void __launch_bounds__(kSmWarps * kWarp, 1) attend_rows_kernel(const AttendArgs a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ int s_prefix[kSmWarps * kWarp], s_warp[kSmWarps];
+  constexpr int kKeys = 8;
+  await_previous_kernel();
+  const int lane = lane_id(), warp = threadIdx.x / kWarp;
+  const int total = line_prefix(a, s_prefix, s_warp);
+  const int HV = a.kv_heads * a.parts, gw = blockIdx.x * kSmWarps + warp;
+  const int r = gw / HV, hv = gw - r * HV, kv = hv / a.parts, part = hv - kv * a.parts;
+  if (total == 0) return;
+  const int ranges = ranges_of(a, total);
+  if (r >= ranges) return;
+  const int lo = range_begin(r, ranges, total), hi = range_begin(r + 1, ranges, total);
+  if (lo >= hi) return;
+  Cursor c = find_tile(a, s_prefix, lo);
+
+  const int D = a.D, pieces = (D + 3) / 4;
+  const int pitch = (((pieces + 3) / 4) * 4 + ((((pieces + 3) / 4) & 1) ? 0 : 4)) * 4;  // floats; 64 bytes off a multiple of 128
+  float* ks = reinterpret_cast<float*>(smem) + (size_t)warp * (2 * kKeys * pitch + GM * pitch + GM * kKeys);
+  float* vs = ks + kKeys * pitch;
+  float* qs = vs + kKeys * pitch;
+  float* ps = qs + GM * pitch;
+  for (int i = lane; i < 2 * kKeys * pitch + GM * pitch; i += kWarp) ks[i] = 0.0f;  // what lies behind D stays zero
+  __syncwarp();
+
+  const int h0 = kv * a.group + part * GM, count = min(GM, a.group - part * GM);
+  const int key = lane >> 2, quarter = lane & 3;
+  float m[GM], l[GM], o[GM][NC][4];
+  bool fresh = true;
+  int first_tile = c.tile;
+  int64_t x = lo;
+  while (true) {
+    if (fresh) {
+      fresh = false;
+      first_tile = c.tile;
+      for (int h = 0; h < count; ++h) {
+        const ET* row = reinterpret_cast<const ET*>(a.q + c.b * a.q_row + (h0 + h) * a.q_head);
+        for (int d = lane; d < D; d += kWarp) qs[h * pitch + d] = to_float(row[d]) * a.scale;
+      }
+#pragma unroll
+      for (int h = 0; h < GM; ++h) {
+        m[h] = -INFINITY;
+        l[h] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[h][j][e] = 0.0f;
+      }
+      __syncwarp();
+    }
+    const int mine = lane & (kTile - 1);
+    const int64_t off = row_offset(a, c, mine, page_entry(a, c, mine), kv);
+    const int new_row = a.k_new != nullptr ? c.n - 1 - (c.first + c.tile * kTile) : -1;  // of the new token, if in 0 .. 15
+    const unsigned valid = __ballot_sync(0xffffffffu, off >= 0) & 0xffffu;
+    for (int half = 0; half < 2; ++half) {
+      const unsigned bits = valid >> (half * kKeys) & 0xffu;
+      if (bits == 0) continue;
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i) {
+        const int row = half * kKeys + i;
+        const int64_t at = __shfl_sync(0xffffffffu, off, row);
+        if (at < 0) {
+          for (int d = lane; d < D; d += kWarp) ks[i * pitch + d] = vs[i * pitch + d] = 0.0f;
+          continue;
+        }
+        ET* kc = reinterpret_cast<ET*>(a.k + at);
+        ET* vc = reinterpret_cast<ET*>(a.v + at);
+        if (row == new_row) {
+          const ET* kn = reinterpret_cast<const ET*>(a.k_new + c.b * a.kn_row + kv * a.kn_head);
+          const ET* vn = reinterpret_cast<const ET*>(a.v_new + c.b * a.vn_row + kv * a.vn_head);
+          for (int d = lane; d < D; d += kWarp) {
+            const ET kk = kn[d], vv = vn[d];
+            if (part == 0) {
+              kc[d] = kk;
+              vc[d] = vv;
+            }
+            ks[i * pitch + d] = to_float(kk);
+            vs[i * pitch + d] = to_float(vv);
+          }
+        } else {
+          for (int d = lane; d < D; d += kWarp) {
+            ks[i * pitch + d] = to_float(kc[d]);
+            vs[i * pitch + d] = to_float(vc[d]);
+          }
+        }
+      }
+      __syncwarp();
+      // Scores of (key, all heads), the same in the four lanes of a key.
+      float s[GM];
+#pragma unroll
+      for (int h = 0; h < GM; ++h) s[h] = 0.0f;
+      for (int p = quarter; p < pieces; p += 4) {
+        const float4 kk = *reinterpret_cast<const float4*>(ks + key * pitch + 4 * p);
+#pragma unroll
+        for (int h = 0; h < GM; ++h) {
+          const float4 qq = *reinterpret_cast<const float4*>(qs + h * pitch + 4 * p);
+          s[h] = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, fmaf(qq.z, kk.z, fmaf(qq.w, kk.w, s[h]))));
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < GM; ++h) {
+        s[h] += __shfl_xor_sync(0xffffffffu, s[h], 1);
+        s[h] += __shfl_xor_sync(0xffffffffu, s[h], 2);
+        if (!(bits >> key & 1)) s[h] = -INFINITY;
+        float t = s[h];
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+        const float now = fmaxf(m[h], t);
+        const float base = now == -INFINITY ? 0.0f : now;
+        const float keep = exp2f(m[h] - base);
+        const float pr = exp2f(s[h] - base);
+        m[h] = now;
+        l[h] = l[h] * keep + (quarter == 0 ? pr : 0.0f);
+        if (quarter == 0) ps[h * kKeys + key] = pr;
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[h][j][e] *= keep;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+          const int p = lane + j * kWarp;
+          if (p < pieces) {
+            const float4 vv = *reinterpret_cast<const float4*>(vs + i * pitch + 4 * p);
+#pragma unroll
+            for (int h = 0; h < GM; ++h) {
+              const float pr = ps[h * kKeys + i];
+              o[h][j][0] = fmaf(pr, vv.x, o[h][j][0]);
+              o[h][j][1] = fmaf(pr, vv.y, o[h][j][1]);
+              o[h][j][2] = fmaf(pr, vv.z, o[h][j][2]);
+              o[h][j][3] = fmaf(pr, vv.w, o[h][j][3]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+    }
+    ++x;
+    const bool last = c.tile == c.tiles - 1;
+    if (last || x == hi) {
+      const bool whole = last && first_tile == 0;
+      const int64_t slot = (int64_t)r + c.b;
+#pragma unroll
+      for (int h = 0; h < GM; ++h) {
+        float sum = l[h];
+#pragma unroll
+        for (int d = 1; d < kWarp; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (h >= count) continue;
+        const int64_t head = whole ? (int64_t)c.b * a.heads + h0 + h : slot * a.heads + h0 + h;
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int d = 4 * (lane + j * kWarp) + e;
+            if (d >= D) continue;
+            if (!whole) {
+              a.part_o[head * D + d] = o[h][j][e];
+            } else if constexpr (sizeof(ET) == 4) {
+              static_cast<float*>(a.out)[head * D + d] = o[h][j][e] * inv;
+            } else {
+              static_cast<__nv_bfloat16*>(a.out)[head * D + d] = __float2bfloat16_rn(o[h][j][e] * inv);
+            }
+          }
+        if (lane == 0) {
+          if (!whole) {
+            a.part_ml[head] = make_float2(m[h], sum);
+          } else if (a.lse != nullptr) {
+            a.lse[head] = sum > 0.0f ? (m[h] + log2f(sum)) * kLn2 : -INFINITY;
+          }
+        }
+      }
+      fresh = true;
+    }
+    if (x == hi) break;
+    c.next(a);
+  }
+}
+
+// Joins the parts of the sequences that more than one range covers, and
+// answers for those without a position. A warp takes a head.
+template <typename ET>
+__global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
+  __shared__ int s_warp[8], s_sum[8];
+  const int lane = lane_id(), warp = threadIdx.x / kWarp, b = blockIdx.x;
+  await_previous_kernel();
+  int total = 0, before = 0;  // tiles of all sequences, and of those in front of b
+  for (int i = threadIdx.x; i < a.seqs; i += blockDim.x) {
+    const int t = tiles_of(a, i);
+    total += t;
+    if (i < b) before += t;
+  }
+#pragma unroll
+  for (int d = 1; d < kWarp; d <<= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, d);
+    before += __shfl_xor_sync(0xffffffffu, before, d);
+  }
+  if (lane == 0) {
+    s_warp[warp] = total;
+    s_sum[warp] = before;
+  }
+  __syncthreads();
+  total = before = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    total += s_warp[w];
+    before += s_sum[w];
+  }
+  const int tiles = tiles_of(a, b), D = a.D;
+  int r0 = 0, parts = 0;
+  if (tiles > 0) {
+    const int ranges = ranges_of(a, total);
+    r0 = range_at(before, ranges, total);
+    parts = range_at(before + tiles - 1, ranges, total) - r0 + 1;
+    if (parts == 1) return;
+  }
+  for (int h = blockIdx.y * 8 + warp; h < a.heads; h += gridDim.y * 8) {
+    const int64_t head = (int64_t)b * a.heads + h;
+    const int64_t at = (int64_t)(r0 + b) * a.heads + h;  // its first part; the next is a.heads further
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += kWarp) m = fmaxf(m, a.part_ml[at + (int64_t)i * a.heads].x);
+#pragma unroll
+    for (int d = 1; d < kWarp; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float base = m == -INFINITY ? 0.0f : m;
+    float sum = 0.0f;
+    for (int i = lane; i < parts; i += kWarp) {
+      const float2 ml = a.part_ml[at + (int64_t)i * a.heads];
+      sum += ml.y * exp2f(ml.x - base);
+    }
+#pragma unroll
+    for (int d = 1; d < kWarp; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    for (int d0 = 0; d0 < D; d0 += kWarp) {
+      const int d = d0 + lane;
+      float o = 0.0f;
+      for (int i = 0; i < parts; ++i) {
+        const float w = exp2f(a.part_ml[at + (int64_t)i * a.heads].x - base);
+        if (d < D) o = fmaf(w, a.part_o[(at + (int64_t)i * a.heads) * D + d], o);
+      }
+      if (d < D) {
+        if constexpr (sizeof(ET) == 4) {
+          static_cast<float*>(a.out)[head * D + d] = o * inv;
+        } else {
+          static_cast<__nv_bfloat16*>(a.out)[head * D + d] = __float2bfloat16_rn(o * inv);
+        }
+      }
+    }
+    if (lane == 0 && a.lse != nullptr) a.lse[head] = sum > 0.0f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+  }
+}
+
+template <typename ET, int GM, int NC> int launch_rows(AttendArgs a, cudaStream_t s) {
+  static std::atomic<bool> raised[kSmemDevices];
+  auto k = attend_rows_kernel<ET, GM, NC>;
+  if (!allow_smem(k, raised)) return MOE_ERR_CUDA;
+  a.parts = (a.group + GM - 1) / GM;
+  const int64_t warps = (int64_t)num_sms() * kSmWarps, HV = (int64_t)a.kv_heads * a.parts;
+  a.ranges = (int32_t)(warps / HV < 1 ? 1 : warps / HV);
+  const int quads = (((a.D + 3) / 4) + 3) / 4;
+  const int pitch = (quads * 4 + ((quads & 1) ? 0 : 4)) * 4;
+  const size_t smem = (size_t)kSmWarps * (2 * 8 * pitch + GM * pitch + GM * 8) * 4;
+  const int64_t ctas = (a.ranges * HV + kSmWarps - 1) / kSmWarps;
+  launch(k, dim3((unsigned)ctas), dim3(kSmWarps * kWarp), smem, s, a);
+  return check_launch();
+}
+template <typename ET, int GM> int launch_rows_dim(const AttendArgs& a, cudaStream_t s) {
+  return a.D <= 128 ? launch_rows<ET, GM, 1>(a, s) : launch_rows<ET, GM, 2>(a, s);
+}
+template <typename ET> int run_attend(AttendArgs a, cudaStream_t s) {
+  int rc = a.group == 1 ? launch_rows_dim<ET, 1>(a, s)
+           : a.group == 2 ? launch_rows_dim<ET, 2>(a, s)
+           : a.group <= 4 ? launch_rows_dim<ET, 4>(a, s)
+                          : launch_rows_dim<ET, 8>(a, s);
+  if (rc != MOE_OK) return rc;
+  // The same ranges as the first kernel's.
+  const int gm = a.group <= 2 ? a.group : a.group <= 4 ? 4 : 8;
+  a.parts = (a.group + gm - 1) / gm;
+  const int64_t warps = (int64_t)num_sms() * kSmWarps, HV = (int64_t)a.kv_heads * a.parts;
+  a.ranges = (int32_t)(warps / HV < 1 ? 1 : warps / HV);
+  const int blocks = (a.heads + 7) / 8;
+  int y = (int)(4 * (int64_t)num_sms() / a.seqs);
+  y = y < 1 ? 1 : (y > blocks ? blocks : y);
+  launch(attend_join_kernel<ET>, dim3((unsigned)a.seqs, (unsigned)y), dim3(256), 0, s, a);
+  return check_launch();
+}
+
+int64_t slots_of(int64_t seqs, int32_t kv_heads) {
+  const int64_t r = (int64_t)num_sms() * kSmWarps / kv_heads;
+  return (r < 1 ? 1 : r) + seqs;
+}
+
+bool heads_ok(const moe_heads* h) { return h->row_stride >= 0 && h->head_stride >= 0; }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_attention_decode_workspace_size(int64_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                                                      int32_t head_dim) {
+  if (num_seqs < 0 || num_seqs > MOE_CACHE_MAX_ROWS || num_kv_heads < 1 || num_heads < 1 || num_heads % num_kv_heads ||
+      head_dim < 1 || head_dim > MOE_ATTENTION_MAX_DIM)
+    return 0;
+  const int64_t rows = slots_of(num_seqs, num_kv_heads) * num_heads;
+  return (size_t)(rows * head_dim * 4 + 15) / 16 * 16 + (size_t)rows * 8;
+}
+
+extern "C" int moe_attention_decode(const moe_kv_cache* cache, const moe_heads* q, int32_t num_heads,
+                                    const int32_t* page_table, int64_t table_stride, int64_t table_width,
+                                    const int32_t* lengths, int64_t num_seqs, const moe_heads* k_new,
+                                    const moe_heads* v_new, float scale, int64_t window, void* out, float* lse,
+                                    void* workspace, size_t workspace_bytes, int32_t* d_status, moe_stream_t stream) {
+  if (cache == nullptr || q == nullptr || (k_new == nullptr) != (v_new == nullptr)) return MOE_ERR_INVALID_ARG;
+  const int eb = dtype_bytes(cache->dtype);
+  if (eb == 0) return MOE_ERR_UNSUPPORTED;
+  if (num_seqs < 0 || num_heads < 1 || cache->num_kv_heads < 1 || num_heads % cache->num_kv_heads ||
+      cache->head_dim < 1 || cache->page_size < 1 || cache->num_pages < 0 || cache->page_stride < 0 ||
+      cache->token_stride < 0 || cache->head_stride < 0 || table_width < 0 || window < 0 || !(fabsf(scale) < INFINITY))
+    return MOE_ERR_INVALID_ARG;
+  if ((num_seqs > 1 && table_stride < table_width) || !heads_ok(q) || (k_new != nullptr && !(heads_ok(k_new) && heads_ok(v_new))))
+    return MOE_ERR_INVALID_ARG;
+  if (cache->head_dim > MOE_ATTENTION_MAX_DIM || num_seqs > MOE_CACHE_MAX_ROWS || cache->num_pages > INT32_MAX ||
+      table_width > INT32_MAX || table_width * cache->page_size > INT32_MAX - kTile ||
+      num_seqs * (table_width * cache->page_size) >= (int64_t)1 << 34)
+    return MOE_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return MOE_OK;
+  if ((cache->num_pages > 0 && (cache->k == nullptr || cache->v == nullptr)) || q->data == nullptr ||
+      (table_width > 0 && page_table == nullptr) || lengths == nullptr || out == nullptr || workspace == nullptr ||
+      (k_new != nullptr && (k_new->data == nullptr || v_new->data == nullptr)))
+    return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < moe_attention_decode_workspace_size(num_seqs, num_heads, cache->num_kv_heads, cache->head_dim))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(cache->k, eb) || !aligned(cache->v, eb) || !aligned(q->data, eb) || !aligned(out, eb) || !aligned(page_table, 4) ||
+      !aligned(lengths, 4) || !aligned(lse, 4) || !aligned(workspace, 16) || !aligned(d_status, 4) ||
+      (k_new != nullptr && !(aligned(k_new->data, eb) && aligned(v_new->data, eb))))
+    return MOE_ERR_UNSUPPORTED;
+  AttendArgs a = {};
+  a.k = static_cast<char*>(cache->k);
+  a.v = static_cast<char*>(cache->v);
+  a.page_stride = cache->page_stride * eb;
+  a.token_stride = cache->token_stride * eb;
+  a.head_stride = cache->head_stride * eb;
+  a.q = static_cast<const char*>(q->data);
+  a.q_row = q->row_stride * eb;
+  a.q_head = q->head_stride * eb;
+  if (k_new != nullptr) {
+    a.k_new = static_cast<const char*>(k_new->data);
+    a.v_new = static_cast<const char*>(v_new->data);
+    a.kn_row = k_new->row_stride * eb;
+    a.kn_head = k_new->head_stride * eb;
+    a.vn_row = v_new->row_stride * eb;
+    a.vn_head = v_new->head_stride * eb;
+  }
+  a.table = page_table;
+  a.table_stride = table_stride;
+  a.lengths = lengths;
+  a.out = out;
+  a.lse = lse;
+  a.part_o = static_cast<float*>(workspace);
+  const int64_t rows = slots_of(num_seqs, cache->num_kv_heads) * num_heads;
+  a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + (rows * cache->head_dim * 4 + 15) / 16 * 16);
+  a.status = d_status;
+  a.page = Divisor((uint32_t)cache->page_size);
+  a.num_pages = cache->num_pages;
+  a.window = window;
+  a.seqs = (int32_t)num_seqs;
+  a.width = (int32_t)table_width;
+  a.heads = num_heads;
+  a.kv_heads = cache->num_kv_heads;
+  a.group = num_heads / cache->num_kv_heads;
+  a.D = cache->head_dim;
+  a.max_tokens = (int32_t)(table_width * cache->page_size);
+  a.scale = scale * kLog2e;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return eb == 4 ? run_attend<float>(a, s) : run_attend<__nv_bfloat16>(a, s);
+}
