@@ -189,7 +189,7 @@ template <> __device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat
 // pieces of four of a row's elements for all heads.
 template <typename ET, int GM, int NC>
 __global__ void __launch_bounds__(kSmWarps * kWarp, 1) attend_rows_kernel(const AttendArgs a) {
-  extern __shared__ __align__(16) unsigned char smem[];
+  extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_prefix[kSmWarps * kWarp], s_warp[kSmWarps];
   constexpr int kKeys = 8;
   await_previous_kernel();
@@ -371,6 +371,291 @@ __global__ void __launch_bounds__(kSmWarps * kWarp, 1) attend_rows_kernel(const 
   }
 }
 
+// ------------------------------------------------- bf16, on the tensor cores
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void ldmatrix(uint32_t (&f)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3]) : "r"(at));
+}
+__device__ __forceinline__ void ldmatrix_trans(uint32_t (&f)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3]) : "r"(at));
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Sizes of a variant: DP elements of a padded row (64, 128 or 256), MT tiles of
+// 16 query heads (0: eight heads in one).
+template <int DP, int MT> struct Mma {
+  static constexpr int kHeads = MT == 0 ? 8 : 16 * MT, kTiles = MT == 0 ? 1 : MT;
+  static constexpr int kWarps = DP == 256 ? 4 : 8;
+  static constexpr int kStageBytes = 2 * kTile * DP * 2;
+  static constexpr int kStages = DP == 64 ? 6 : 3;  // 192 KB an SM
+  static constexpr size_t kSmem = (size_t)kWarps * kStages * kStageBytes;
+};
+
+// S = Q K^T and O += P V by m16n8k16 products: the query heads of a kv head are
+// the rows, 16 keys a step. Decoding has few rows, so the products are never
+// the bound (16 keys of 128 elements: 32 to 48 instructions in the 350 clocks
+// that the SM's share of HBM needs for them). P goes in as two bf16 numbers, the
+// second what the first one's rounding left; with eight heads or fewer the
+// second takes the rows that they leave empty, and costs nothing.
+template <int DP, int MT>
+__global__ void __launch_bounds__(Mma<DP, MT>::kWarps * kWarp, 1) attend_mma_kernel(const AttendArgs a) {
+  using S = Mma<DP, MT>;
+  constexpr int kWarps = S::kWarps, kStages = S::kStages, kTiles = S::kTiles;
+  constexpr int kChunks = DP / 8, kRowsPass = kWarp / kChunks, kPasses = kTile / kRowsPass;  // 16-byte pieces of a row
+  constexpr int kSteps = DP / 16;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int s_prefix[kWarps * kWarp], s_warp[kWarps];
+  __shared__ unsigned s_mask[kWarps][kStages];
+  await_previous_kernel();
+  const int lane = lane_id(), warp = threadIdx.x / kWarp;
+  const int total = line_prefix(a, s_prefix, s_warp);
+  const int HV = a.kv_heads * a.parts, gw = blockIdx.x * kWarps + warp;
+  const int r = gw / HV, hv = gw - r * HV, kv = hv / a.parts, part = hv - kv * a.parts;
+  if (total == 0) return;
+  const int ranges = ranges_of(a, total);
+  if (r >= ranges) return;
+  const int lo = range_begin(r, ranges, total), count = range_begin(r + 1, ranges, total) - lo;
+  if (count <= 0) return;
+  const int D = a.D, h0 = kv * a.group + part * S::kHeads, heads = min(S::kHeads, a.group - part * S::kHeads);
+  const uint32_t ring = smem_u32(smem) + warp * kStages * S::kStageBytes;
+  if (D < DP) {  // pieces behind D are never copied, and have to be numbers
+    uint4* z = reinterpret_cast<uint4*>(smem + (size_t)warp * kStages * S::kStageBytes);
+    for (int i = lane; i < kStages * S::kStageBytes / 16; i += kWarp) z[i] = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+  }
+
+  // Copies of a tile: K then V, 16 rows each, pieces swizzled by the row.
+  Cursor in = find_tile(a, s_prefix, lo);
+  Cursor at = in;
+  int issued = 0, page = page_entry(a, in, lane & (kTile - 1));
+  const int chunk = lane % kChunks, sub = lane / kChunks;
+  const bool copies = chunk * 8 < D;
+  const auto issue = [&]() {
+    if (issued < count) {
+      const int stage = issued % kStages, row = lane & (kTile - 1);
+      int64_t off = row_offset(a, in, row, page, kv);
+      const unsigned valid = __ballot_sync(0xffffffffu, off >= 0) & 0xffffu;
+      if (lane == 0) s_mask[warp][stage] = valid;
+      const int fresh = a.k_new != nullptr ? in.n - 1 - (in.first + in.tile * kTile) : -1;  // the new token's row
+      const uint32_t base = ring + stage * S::kStageBytes;
+      if (fresh >= 0 && fresh < kTile && (valid >> fresh & 1)) {
+        const int64_t to = __shfl_sync(0xffffffffu, off, fresh);
+        if (lane == fresh || lane == fresh + kTile) off = -2;
+        if (sub == 0 && copies) {
+          const char* kn = a.k_new + in.b * a.kn_row + kv * a.kn_head + chunk * 16;
+          const char* vn = a.v_new + in.b * a.vn_row + kv * a.vn_head + chunk * 16;
+          const uint32_t dst = base + fresh * DP * 2 + ((chunk ^ (fresh & 7)) * 16);
+          cp_async16(dst, kn, 16);
+          cp_async16(dst + kTile * DP * 2, vn, 16);
+          if (part == 0) {
+            *reinterpret_cast<uint4*>(a.k + to + chunk * 16) = *reinterpret_cast<const uint4*>(kn);
+            *reinterpret_cast<uint4*>(a.v + to + chunk * 16) = *reinterpret_cast<const uint4*>(vn);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const int row_i = i * kRowsPass + sub;
+        const int64_t from = __shfl_sync(0xffffffffu, off, row_i);
+        if (copies && from != -2) {
+          const int bytes = from < 0 ? 0 : 16;
+          const int64_t o = from < 0 ? 0 : from + chunk * 16;
+          const uint32_t dst = base + row_i * DP * 2 + ((chunk ^ (row_i & 7)) * 16);
+          cp_async16(dst, a.k + o, bytes);
+          cp_async16(dst + kTile * DP * 2, a.v + o, bytes);
+        }
+      }
+      if (++issued < count) {
+        in.next(a);
+        page = page_entry(a, in, row);
+      }
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue();
+
+  uint32_t q[kTiles][kSteps][4];
+  float o[kTiles][DP / 8][4], m[kTiles][2], l[kTiles][2];
+  const int g = lane >> 2, t = lane & 3;
+  const int mi = lane >> 3, lr = lane & 7;
+  const uint32_t k_at = ((mi >> 1) * 8 + lr) * DP * 2, v_at = ((mi & 1) * 8 + lr) * DP * 2 + kTile * DP * 2;
+  bool fresh = true;
+  int first_tile = at.tile;
+  for (int i = 0; i < count; ++i) {
+    if (fresh) {
+      fresh = false;
+      first_tile = at.tile;
+      const char* rows = a.q + at.b * a.q_row;
+#pragma unroll
+      for (int u = 0; u < kTiles; ++u) {
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int h = u * 16 + g + (e & 1) * 8, d = ks * 16 + t * 2 + (e >> 1) * 8;
+            q[u][ks][e] = (MT == 0 && (e & 1)) || h >= heads || d >= D
+                              ? 0u : __ldg(reinterpret_cast<const unsigned*>(rows + (h0 + h) * a.q_head + d * 2));
+          }
+#pragma unroll
+        for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[u][n][e] = 0.0f;
+        m[u][0] = m[u][1] = -INFINITY;
+        l[u][0] = l[u][1] = 0.0f;
+      }
+    }
+    cp_wait<kStages - 2>();
+    __syncwarp();
+    const int stage = i % kStages;
+    const unsigned valid = s_mask[warp][stage];
+    issue();  // into the stage that the previous tile left
+    const uint32_t base = ring + stage * S::kStageBytes;
+    float s[kTiles][2][4];
+#pragma unroll
+    for (int u = 0; u < kTiles; ++u)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[u][n][e] = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks) {
+      uint32_t b[4];
+      ldmatrix(b, base + k_at + (((ks * 2 + (mi & 1)) ^ lr) * 16));
+#pragma unroll
+      for (int u = 0; u < kTiles; ++u) {
+        mma(s[u][0], q[u][ks], b[0], b[1]);
+        mma(s[u][1], q[u][ks], b[2], b[3]);
+      }
+    }
+    uint32_t hi[kTiles][4], lo2[kTiles][4];
+#pragma unroll
+    for (int u = 0; u < kTiles; ++u) {
+      constexpr int kRows = MT == 0 ? 1 : 2;  // rows g and g + 8
+      float keep[2] = {1.0f, 1.0f};
+      bool moved = false;
+#pragma unroll
+      for (int w = 0; w < kRows; ++w) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& x = s[u][n][2 * w + e];
+            x *= a.scale;
+            if (valid != 0xffffu && !(valid >> (n * 8 + t * 2 + e) & 1)) x = -INFINITY;
+            top = fmaxf(top, x);
+          }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float now = fmaxf(m[u][w], top), from = now == -INFINITY ? 0.0f : now;
+        if (now > m[u][w]) {
+          moved = true;
+          keep[w] = ex2(m[u][w] - from);
+          m[u][w] = now;
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float p0 = ex2(s[u][n][2 * w] - from), p1 = ex2(s[u][n][2 * w + 1] - from);
+          sum += p0 + p1;
+          const uint32_t h = pack_bf16x2(p0, p1);
+          const uint32_t rest = pack_bf16x2(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u));
+          if constexpr (MT == 0) {
+            hi[u][2 * n] = h;
+            hi[u][2 * n + 1] = rest;
+          } else {
+            hi[u][2 * n + w] = h;
+            lo2[u][2 * n + w] = rest;
+          }
+        }
+        l[u][w] = l[u][w] * keep[w] + sum;
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+        if constexpr (MT == 0) keep[1] = keep[0];
+#pragma unroll
+        for (int n = 0; n < DP / 8; ++n) {
+          o[u][n][0] *= keep[0];
+          o[u][n][1] *= keep[0];
+          o[u][n][2] *= keep[1];
+          o[u][n][3] *= keep[1];
+        }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < kSteps; ++c) {
+      uint32_t b[4];
+      ldmatrix_trans(b, base + v_at + (((c * 2 + (mi >> 1)) ^ lr) * 16));
+#pragma unroll
+      for (int u = 0; u < kTiles; ++u) {
+        mma(o[u][2 * c], hi[u], b[0], b[1]);
+        mma(o[u][2 * c + 1], hi[u], b[2], b[3]);
+        if constexpr (MT > 0) {
+          mma(o[u][2 * c], lo2[u], b[0], b[1]);
+          mma(o[u][2 * c + 1], lo2[u], b[2], b[3]);
+        }
+      }
+    }
+    const bool last = at.tile == at.tiles - 1;
+    if (last || i == count - 1) {
+      const bool whole = last && first_tile == 0;
+#pragma unroll
+      for (int u = 0; u < kTiles; ++u)
+#pragma unroll
+        for (int w = 0; w < (MT == 0 ? 1 : 2); ++w) {
+          float sum = l[u][w];
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          const int h = u * 16 + g + w * 8;
+          if (h >= heads) continue;
+          const int64_t head = (whole ? (int64_t)at.b : (int64_t)r + at.b) * a.heads + h0 + h;
+          const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+          for (int n = 0; n < DP / 8; ++n) {
+            const int d = n * 8 + t * 2;
+            if (d >= D) continue;
+            float x = o[u][n][2 * w], y = o[u][n][2 * w + 1];
+            if constexpr (MT == 0) {
+              x += o[u][n][2];
+              y += o[u][n][3];
+            }
+            if (whole) {
+              *reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + (head * D + d) * 2) = pack_bf16x2(x * inv, y * inv);
+            } else {
+              *reinterpret_cast<float2*>(a.part_o + head * D + d) = make_float2(x, y);
+            }
+          }
+          if (t == 0) {
+            if (!whole) {
+              a.part_ml[head] = make_float2(m[u][w], sum);
+            } else if (a.lse != nullptr) {
+              a.lse[head] = sum > 0.0f ? (m[u][w] + log2f(sum)) * kLn2 : -INFINITY;
+            }
+          }
+        }
+      fresh = true;
+    }
+    if (i + 1 < count) at.next(a);
+  }
+}
+
 // Joins the parts of the sequences that more than one range covers, and
 // answers for those without a position. A warp takes a head.
 template <typename ET>
@@ -443,34 +728,61 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
   }
 }
 
-template <typename ET, int GM, int NC> int launch_rows(AttendArgs a, cudaStream_t s) {
+// Ranges of the line for a kernel of `warps` warps an SM that takes kHeads query heads at a time.
+void cut(AttendArgs& a, int heads_at_once, int warps) {
+  a.parts = (a.group + heads_at_once - 1) / heads_at_once;
+  const int64_t r = (int64_t)num_sms() * warps / ((int64_t)a.kv_heads * a.parts);
+  a.ranges = (int32_t)(r < 1 ? 1 : r);
+}
+unsigned ctas_of(const AttendArgs& a, int warps) {
+  return (unsigned)(((int64_t)a.ranges * a.kv_heads * a.parts + warps - 1) / warps);
+}
+
+template <typename ET, int GM, int NC> int launch_rows(AttendArgs& a, cudaStream_t s) {
   static std::atomic<bool> raised[kSmemDevices];
   auto k = attend_rows_kernel<ET, GM, NC>;
   if (!allow_smem(k, raised)) return MOE_ERR_CUDA;
-  a.parts = (a.group + GM - 1) / GM;
-  const int64_t warps = (int64_t)num_sms() * kSmWarps, HV = (int64_t)a.kv_heads * a.parts;
-  a.ranges = (int32_t)(warps / HV < 1 ? 1 : warps / HV);
+  cut(a, GM, kSmWarps);
   const int quads = (((a.D + 3) / 4) + 3) / 4;
   const int pitch = (quads * 4 + ((quads & 1) ? 0 : 4)) * 4;
   const size_t smem = (size_t)kSmWarps * (2 * 8 * pitch + GM * pitch + GM * 8) * 4;
-  const int64_t ctas = (a.ranges * HV + kSmWarps - 1) / kSmWarps;
-  launch(k, dim3((unsigned)ctas), dim3(kSmWarps * kWarp), smem, s, a);
+  launch(k, dim3(ctas_of(a, kSmWarps)), dim3(kSmWarps * kWarp), smem, s, a);
   return check_launch();
 }
-template <typename ET, int GM> int launch_rows_dim(const AttendArgs& a, cudaStream_t s) {
+template <typename ET, int GM> int launch_rows_dim(AttendArgs& a, cudaStream_t s) {
   return a.D <= 128 ? launch_rows<ET, GM, 1>(a, s) : launch_rows<ET, GM, 2>(a, s);
 }
-template <typename ET> int run_attend(AttendArgs a, cudaStream_t s) {
-  int rc = a.group == 1 ? launch_rows_dim<ET, 1>(a, s)
-           : a.group == 2 ? launch_rows_dim<ET, 2>(a, s)
-           : a.group <= 4 ? launch_rows_dim<ET, 4>(a, s)
-                          : launch_rows_dim<ET, 8>(a, s);
+template <int DP, int MT> int launch_mma(AttendArgs& a, cudaStream_t s) {
+  using S = Mma<DP, MT>;
+  static std::atomic<bool> raised[kSmemDevices];
+  auto k = attend_mma_kernel<DP, MT>;
+  if (!allow_smem(k, raised)) return MOE_ERR_CUDA;
+  cut(a, S::kHeads, S::kWarps);
+  launch(k, dim3(ctas_of(a, S::kWarps)), dim3(S::kWarps * kWarp), S::kSmem, s, a);
+  return check_launch();
+}
+template <int DP> int launch_mma_heads(AttendArgs& a, cudaStream_t s) {
+  if (a.group <= 8) return launch_mma<DP, 0>(a, s);
+  if constexpr (DP < 256)  // two tiles of heads at once: the registers hold them up to 128 elements
+    if (a.group > 16) return launch_mma<DP, 2>(a, s);
+  return launch_mma<DP, 1>(a, s);
+}
+template <typename ET> int run_attend(AttendArgs& a, cudaStream_t s) {
+  int rc;
+  // Rows of 16-byte pieces on 16 bytes (and query rows and outputs on 4) go to the tensor cores.
+  const int64_t pieces = a.page_stride | a.token_stride | a.head_stride | (int64_t)(reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) |
+                         (int64_t)(reinterpret_cast<uintptr_t>(a.k_new) | reinterpret_cast<uintptr_t>(a.v_new)) | a.kn_row | a.kn_head |
+                         a.vn_row | a.vn_head | a.D * (int64_t)sizeof(ET);
+  const int64_t pairs = a.q_row | a.q_head | (int64_t)(reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.out));
+  if (sizeof(ET) == 2 && pieces % 16 == 0 && pairs % 4 == 0) {
+    rc = a.D <= 64 ? launch_mma_heads<64>(a, s) : a.D <= 128 ? launch_mma_heads<128>(a, s) : launch_mma_heads<256>(a, s);
+  } else {
+    rc = a.group == 1 ? launch_rows_dim<ET, 1>(a, s)
+         : a.group == 2 ? launch_rows_dim<ET, 2>(a, s)
+         : a.group <= 4 ? launch_rows_dim<ET, 4>(a, s)
+                        : launch_rows_dim<ET, 8>(a, s);
+  }
   if (rc != MOE_OK) return rc;
-  // The same ranges as the first kernel's.
-  const int gm = a.group <= 2 ? a.group : a.group <= 4 ? 4 : 8;
-  a.parts = (a.group + gm - 1) / gm;
-  const int64_t warps = (int64_t)num_sms() * kSmWarps, HV = (int64_t)a.kv_heads * a.parts;
-  a.ranges = (int32_t)(warps / HV < 1 ? 1 : warps / HV);
   const int blocks = (a.heads + 7) / 8;
   int y = (int)(4 * (int64_t)num_sms() / a.seqs);
   y = y < 1 ? 1 : (y > blocks ? blocks : y);
