@@ -2,8 +2,8 @@
 
 Each CUDA translation unit is compiled in parallel into ``_build/`` and the
 objects are linked into ``padded_permute_combine_gb300/libmoe_route.so``.
-``_block_calls.so``, the marshalling of the block operators' calls, is
-compiled beside them against the headers of the installed torch.
+``_block_calls.so``, the marshalling of the block and decode operators' calls,
+is compiled beside them against the headers of the installed torch.
 Run ``python -m padded_permute_combine_gb300.build`` or call ``build()``.
 """
 from __future__ import annotations
@@ -25,7 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_route.so")
-CALLS_SOURCE = os.path.join(CSRC, "block_calls.cpp")
+CALLS_SOURCES = [os.path.join(CSRC, n) for n in ("block_calls.cpp", "decode_calls.cpp")]
 CALLS = os.path.join(PKG, "_block_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -121,29 +121,30 @@ def _torch_dir() -> str:
 
 def _calls_digest() -> str:
     h = hashlib.sha256()
-    for f in [CALLS_SOURCE, os.path.join(_torch_dir(), "version.py")] + sorted(glob.glob(os.path.join(INCLUDE, "*.h"))):
+    own = CALLS_SOURCES + [os.path.join(CSRC, "calls.h")] + sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
+    for f in own + [os.path.join(_torch_dir(), "version.py")]:
         with open(f, "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:16]
 
 
-def _compile_calls() -> str:
-    obj = os.path.join(BUILD_DIR, "block_calls.o")
+def _compile_calls(source: str) -> str:
+    obj = os.path.join(BUILD_DIR, os.path.basename(source)[:-4] + ".o")
     torch_include = os.path.join(_torch_dir(), "include")
     cuda_include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-isystem", torch_include, "-isystem",
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I", CSRC, "-isystem", torch_include, "-isystem",
            os.path.join(torch_include, "torch", "csrc", "api", "include"), "-isystem", sysconfig.get_paths()["include"],
-           "-isystem", cuda_include, "-c", CALLS_SOURCE, "-o", obj]
+           "-isystem", cuda_include, "-c", source, "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("%s failed:\n%s" % (" ".join(cmd), res.stderr))
     return obj
 
 
-def _link_calls(obj: str) -> None:
+def _link_calls(objs: list[str]) -> None:
     """Linked to the libraries by the names under which torch and the loader have them in the process already."""
     tmp = CALLS + ".tmp%d" % os.getpid()
-    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python",
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, *objs, "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python",
            "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L", PKG, "-l:libmoe_route.so", "-Wl,-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
@@ -166,12 +167,12 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     lib, calls = again or not _fresh(LIB, source_digest()), again or not _fresh(CALLS, _calls_digest())
     if lib or calls:
         os.makedirs(BUILD_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=1) as ex:
-        obj = ex.submit(_compile_calls) if calls else None
+    with cf.ThreadPoolExecutor(max_workers=len(CALLS_SOURCES)) as ex:
+        objs = [ex.submit(_compile_calls, f) for f in CALLS_SOURCES] if calls else []
         if lib:
             _build_lib(verbose_ptxas)
-        if obj is not None:
-            _link_calls(obj.result())
+        if objs:
+            _link_calls([o.result() for o in objs])
     return LIB
 
 

@@ -9,108 +9,12 @@
 // a layer norm forward of four rows, 8.1 to 10.7 backward, 14 to 16.2 for an MoE
 // layer of one token, some 2.2 for each launch and the rest for three to five
 // allocations; in Python the same steps took 14, 22 and 29.
-#include <Python.h>
-#include <ATen/core/Tensor.h>
-#include <ATen/ops/empty_cuda_dispatch.h>
-#include <c10/cuda/CUDAGuard.h>
-#include <c10/cuda/CUDAStream.h>
-#include <torch/csrc/autograd/python_variable.h>
-
+#include "calls.h"
 #include "moe_block.h"
-#include "moe_route.h"
 
 namespace {
 
-using at::Tensor;
-
-int dtype_of(const Tensor& t) {
-  if (t.scalar_type() == at::kBFloat16) return MOE_BF16;
-  return t.scalar_type() == at::kFloat ? MOE_F32 : -1;
-}
-
-// On a GPU, fp32 or bf16, [rows, H] with contiguous rows that do not overlap.
-bool rows_ok(const Tensor& t, int64_t* stride) {
-  if (!t.is_cuda() || t.dim() != 2 || dtype_of(t) < 0) return false;
-  const int64_t M = t.size(0), H = t.size(1);
-  *stride = t.is_contiguous() ? H : t.stride(0);
-  return t.is_contiguous() || ((H <= 1 || t.stride(1) == 1) && (M <= 1 || t.stride(0) >= H));
-}
-bool plain(const Tensor& t, const Tensor& x, at::ScalarType type, at::IntArrayRef sizes) {
-  return t.scalar_type() == type && t.device() == x.device() && t.is_contiguous() && t.sizes() == sizes;
-}
-// The C ABI works on the current device: its launches, SM counts and limits.
-using c10::cuda::CUDAGuard;
-Tensor make(const Tensor& x, at::ScalarType type, at::IntArrayRef sizes) {
-  return at::cuda::empty(sizes, at::TensorOptions().dtype(type).device(x.device()));
-}
-moe_stream_t stream_of(const Tensor& x) {
-  return reinterpret_cast<moe_stream_t>(c10::cuda::getCurrentCUDAStream(x.device().index()).stream());
-}
-const void* at_or_null(const Tensor& t) { return t.defined() ? t.const_data_ptr() : nullptr; }
-
-// Tensors of a call, in order; the ones that may be None come out undefined.
-bool tensors(PyObject* const* args, int n, Tensor* out, unsigned optional = 0) {
-  for (int i = 0; i < n; ++i) {
-    if ((optional >> i & 1) && args[i] == Py_None) continue;
-    if (!THPVariable_Check(args[i])) return false;
-    out[i] = THPVariable_Unpack(args[i]);
-  }
-  return true;
-}
-PyObject* wrapped(std::initializer_list<Tensor> ts) {
-  PyObject* r = PyTuple_New((Py_ssize_t)ts.size());
-  Py_ssize_t i = 0;
-  if (r != nullptr)
-    for (const Tensor& t : ts) {
-      if (t.defined()) {
-        PyTuple_SET_ITEM(r, i++, THPVariable_Wrap(t));
-      } else {
-        Py_INCREF(Py_None);
-        PyTuple_SET_ITEM(r, i++, Py_None);
-      }
-    }
-  return r;
-}
-// The call's result or, with errors of torch as exceptions of Python, none.
-template <typename F> PyObject* guarded(F f) {
-  try {
-    PyObject* r = f();
-    if (r == nullptr && !PyErr_Occurred()) Py_RETURN_NONE;
-    return r;
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
-  }
-}
-
-// The C ABI's call without the interpreter's lock, as ctypes makes it: a full
-// launch queue blocks it for as long as the queue is full, and other threads
-// go on meanwhile. The lock is taken again also when torch throws (a tensor
-// without memory, such as a fake one).
-struct Unlocked {
-  PyThreadState* state = PyEval_SaveThread();
-  ~Unlocked() { PyEval_RestoreThread(state); }
-};
-template <typename F> int unlocked(F f) {
-  const Unlocked now;
-  return f();
-}
-
-// What follows a code other than MOE_OK. Refused arguments (nothing is enqueued
-// then) answer none, and block.py words the error. After any other code work
-// may be enqueued already, and a second call would do it twice (gradients
-// clipped in place, say): MoeError.
-PyObject* failed(const char* name, int rc) {
-  if (rc == MOE_ERR_INVALID_ARG || rc == MOE_ERR_UNSUPPORTED) return nullptr;
-  PyObject* lib = PyImport_ImportModule("padded_permute_combine_gb300._lib");
-  PyObject* type = lib == nullptr ? nullptr : PyObject_GetAttrString(lib, "MoeError");
-  PyObject* error = type == nullptr ? nullptr : PyObject_CallFunction(type, "sis", name, rc, moe_error_string(rc));
-  if (error != nullptr) PyErr_SetObject(type, error);
-  Py_XDECREF(error);
-  Py_XDECREF(type);
-  Py_XDECREF(lib);
-  return nullptr;
-}
+using namespace moe_calls;
 
 // x, weight, bias, eps -> (y, mean, rstd)
 PyObject* layer_norm_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -244,11 +148,14 @@ PyObject* grads(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-#define CALL(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {CALL(layer_norm_fwd), CALL(layer_norm_bwd), CALL(layer), CALL(experts), CALL(grads),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block_calls", nullptr, -1, methods};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__block_calls() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__block_calls() {
+  PyObject* m = PyModule_Create(&module);
+  if (m != nullptr && PyModule_AddFunctions(m, moe_calls::decode_methods()) != 0) Py_CLEAR(m);
+  return m;
+}

@@ -4,7 +4,9 @@ few-token MoE layer (same names, same semantics).
 As in ops.py this is argument marshalling only. A cache is a pair of tensors
 [pages, page_size, kv_heads, head_dim] with any strides but in the last
 dimension (tokens first, or heads first as a transposed view), the same for keys
-and values.
+and values. The plain call (right arguments, outputs to be allocated) is
+marshalled by csrc/decode_calls.cpp; it answers None to any other, which is then
+taken step by step here, with a message for what is wrong.
 """
 from __future__ import annotations
 
@@ -113,6 +115,11 @@ def moe_attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     [B, kv_heads, head_dim] are written to position lengths - 1 on the way.
     scale: head_dim ** -0.5 by default; window: the last positions that are
     looked at, 0 for all."""
+    if out is None and lse is None and workspace is None and status is None:
+        done = (_lib.calls or _lib.load_calls()).attention_decode(
+            q, k_cache, v_cache, page_table, lengths, k_new, v_new, scale, window)
+        if done is not None:
+            return done
     _tensor(q, "q", 3, None, None)
     dev = q.device
     cache = _cache(k_cache, v_cache, dev)
@@ -147,6 +154,9 @@ def moe_cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
     """Writes the keys and values of many tokens into the cache: rows
     offsets[b] .. offsets[b + 1] - 1 of k and v [tokens, kv_heads, head_dim] are
     the last tokens of sequence b, whose length with them is lengths[b]."""
+    if status is None and (_lib.calls or _lib.load_calls()).cache_write(
+            k, v, k_cache, v_cache, page_table, offsets, lengths) is not None:
+        return
     cache = _cache(k_cache, v_cache)
     dev = k_cache.device
     _tensor(k, "k", 3, None, None)
@@ -168,6 +178,11 @@ def moe_cache_fork(page_table: torch.Tensor, lengths: torch.Tensor, parents: tor
     an empty row) with room for ``grow`` more tokens; see include/moe_decode.h.
     The copies src -> dst are moe_cache_copy's to make. ``width``: columns of the
     new table, page_table's by default."""
+    if out is None and status is None and isinstance(page_table, torch.Tensor) and page_table.dim() == 2:
+        done = (_lib.calls or _lib.load_calls()).cache_fork(
+            page_table, lengths, parents, page_size, num_pages, grow, page_table.shape[1] if width is None else width)
+        if done is not None:
+            return CacheFork._make(done)
     _tensor(page_table, "page_table", 2, _I32, None)
     dev = page_table.device
     table, stride, old, rows, lengths_at = _table(page_table, lengths, dev)
@@ -192,6 +207,10 @@ def moe_cache_compact(page_table: torch.Tensor, lengths: torch.Tensor, page_size
                       out: CacheCompact | None = None, status: torch.Tensor | None = None) -> CacheCompact:
     """Moves the pages in use to the front of the pool: the table with the new
     numbers, and the copies src -> dst (``count`` of them) for moe_cache_copy."""
+    if out is None and status is None:
+        done = (_lib.calls or _lib.load_calls()).cache_compact(page_table, lengths, page_size, num_pages)
+        if done is not None:
+            return CacheCompact._make(done)
     _tensor(page_table, "page_table", 2, _I32, None)
     dev = page_table.device
     table, stride, width, rows, lengths_at = _table(page_table, lengths, dev)
@@ -233,6 +252,8 @@ def moe_cache_copy(caches: Sequence[torch.Tensor], src: torch.Tensor, dst: torch
     being one block of memory), in place. Pairs with -1 are passed over;
     ``count``: how many pairs there are (int32 [1] on the device)."""
     caches = list(caches)
+    if status is None and (_lib.calls or _lib.load_calls()).cache_copy(caches, src, dst, count) is not None:
+        return
     _need(src, _I32, "src")
     dev = src.device
     n = src.numel()
@@ -257,6 +278,10 @@ def moe_beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int, en
     best first: (scores fp32, parents int32 = b * beams + beam, tokens int32),
     each [B, num_out]. A beam with ``ended`` (bool or uint8 [B, beams]) goes on
     with end_token alone, at the score that it has."""
+    if out is None and workspace is None:
+        done = (_lib.calls or _lib.load_calls()).beam_select(logits, scores, num_out, ended, end_token)
+        if done is not None:
+            return done
     _tensor(logits, "logits", 3, None, None)
     dt = _act_dtype(logits, "logits")
     dev = logits.device
