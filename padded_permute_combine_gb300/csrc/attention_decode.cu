@@ -130,6 +130,9 @@ struct Cursor {
   }
 };
 
+// The joining kernel may start: it waits for this one before it reads what it left.
+__device__ __forceinline__ void start_next_kernel() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 // The CTA's view of the line: prefix[t] tiles in front of the sequences of thread t.
 __device__ __forceinline__ int line_prefix(const AttendArgs& a, int* prefix, int* s_warp) {
   const int t = threadIdx.x, chunk = (a.seqs + blockDim.x - 1) / blockDim.x;
@@ -193,6 +196,7 @@ __global__ void __launch_bounds__(kSmWarps * kWarp, 1) attend_rows_kernel(const 
   __shared__ int s_prefix[kSmWarps * kWarp], s_warp[kSmWarps];
   constexpr int kKeys = 8;
   await_previous_kernel();
+  start_next_kernel();
   const int lane = lane_id(), warp = threadIdx.x / kWarp;
   const int total = line_prefix(a, s_prefix, s_warp);
   const int HV = a.kv_heads * a.parts, gw = blockIdx.x * kSmWarps + warp;
@@ -424,6 +428,7 @@ __global__ void __launch_bounds__(Mma<DP, MT>::kWarps * kWarp, 1) attend_mma_ker
   __shared__ int s_prefix[kWarps * kWarp], s_warp[kWarps];
   __shared__ unsigned s_mask[kWarps][kStages];
   await_previous_kernel();
+  start_next_kernel();
   const int lane = lane_id(), warp = threadIdx.x / kWarp;
   const int total = line_prefix(a, s_prefix, s_warp);
   const int HV = a.kv_heads * a.parts, gw = blockIdx.x * kWarps + warp;
@@ -657,12 +662,15 @@ __global__ void __launch_bounds__(Mma<DP, MT>::kWarps * kWarp, 1) attend_mma_ker
 }
 
 // Joins the parts of the sequences that more than one range covers, and
-// answers for those without a position. A warp takes a head.
+// answers for those without a position. Many parts of a head are shared by up
+// to eight warps, whose sums are joined in shared memory.
 template <typename ET>
 __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
-  __shared__ int s_warp[8], s_sum[8];
+  __shared__ int s_total[8], s_before[8];
+  __shared__ float s_o[8][MOE_ATTENTION_MAX_DIM];
+  __shared__ float2 s_ml[8];
   const int lane = lane_id(), warp = threadIdx.x / kWarp, b = blockIdx.x;
-  await_previous_kernel();
+  // The lengths are no output of the kernel before, which starts this one early.
   int total = 0, before = 0;  // tiles of all sequences, and of those in front of b
   for (int i = threadIdx.x; i < a.seqs; i += blockDim.x) {
     const int t = tiles_of(a, i);
@@ -675,15 +683,15 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
     before += __shfl_xor_sync(0xffffffffu, before, d);
   }
   if (lane == 0) {
-    s_warp[warp] = total;
-    s_sum[warp] = before;
+    s_total[warp] = total;
+    s_before[warp] = before;
   }
   __syncthreads();
   total = before = 0;
 #pragma unroll
   for (int w = 0; w < 8; ++w) {
-    total += s_warp[w];
-    before += s_sum[w];
+    total += s_total[w];
+    before += s_before[w];
   }
   const int tiles = tiles_of(a, b), D = a.D;
   int r0 = 0, parts = 0;
@@ -691,37 +699,77 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
     const int ranges = ranges_of(a, total);
     r0 = range_at(before, ranges, total);
     parts = range_at(before + tiles - 1, ranges, total) - r0 + 1;
-    if (parts == 1) return;
   }
-  for (int h = blockIdx.y * 8 + warp; h < a.heads; h += gridDim.y * 8) {
-    const int64_t head = (int64_t)b * a.heads + h;
-    const int64_t at = (int64_t)(r0 + b) * a.heads + h;  // its first part; the next is a.heads further
-    float m = -INFINITY;
-    for (int i = lane; i < parts; i += kWarp) m = fmaxf(m, a.part_ml[at + (int64_t)i * a.heads].x);
+  await_previous_kernel();
+  if (parts == 1) return;
+  const int split = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;  // warps of a head
+  const int at_once = 8 / split, sub = warp % split;
+  for (int h0 = blockIdx.y * at_once; h0 < a.heads; h0 += gridDim.y * at_once) {
+    const int h = h0 + warp / split;
+    float m = -INFINITY, sum = 0.0f, o[MOE_ATTENTION_MAX_DIM / kWarp];
 #pragma unroll
-    for (int d = 1; d < kWarp; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float base = m == -INFINITY ? 0.0f : m;
-    float sum = 0.0f;
-    for (int i = lane; i < parts; i += kWarp) {
-      const float2 ml = a.part_ml[at + (int64_t)i * a.heads];
-      sum += ml.y * exp2f(ml.x - base);
-    }
+    for (int j = 0; j < MOE_ATTENTION_MAX_DIM / kWarp; ++j) o[j] = 0.0f;
+    if (h < a.heads) {
+      const int64_t first = (int64_t)(r0 + b) * a.heads + h;  // of part 0; the next is a.heads further
+      for (int i0 = sub; i0 < parts; i0 += split * kWarp) {  // 32 of this warp's parts at a time
+        const int mine = i0 + lane * split, n = min(kWarp, (parts - i0 + split - 1) / split);
+        const float2 ml = mine < parts ? a.part_ml[first + (int64_t)mine * a.heads] : make_float2(-INFINITY, 0.0f);
+        float top = ml.x;
 #pragma unroll
-    for (int d = 1; d < kWarp; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    for (int d0 = 0; d0 < D; d0 += kWarp) {
-      const int d = d0 + lane;
-      float o = 0.0f;
-      for (int i = 0; i < parts; ++i) {
-        const float w = exp2f(a.part_ml[at + (int64_t)i * a.heads].x - base);
-        if (d < D) o = fmaf(w, a.part_o[(at + (int64_t)i * a.heads) * D + d], o);
-      }
-      if (d < D) {
-        if constexpr (sizeof(ET) == 4) {
-          static_cast<float*>(a.out)[head * D + d] = o * inv;
-        } else {
-          static_cast<__nv_bfloat16*>(a.out)[head * D + d] = __float2bfloat16_rn(o * inv);
+        for (int d = 1; d < kWarp; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float now = fmaxf(m, top), base = now == -INFINITY ? 0.0f : now;
+        const float keep = exp2f(m - base), weight = exp2f(ml.x - base);
+        m = now;
+        float all = ml.y * weight;
+#pragma unroll
+        for (int d = 1; d < kWarp; d <<= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+        sum = sum * keep + all;
+#pragma unroll
+        for (int j = 0; j < MOE_ATTENTION_MAX_DIM / kWarp; ++j) o[j] *= keep;
+        const float* rows = a.part_o + (first + (int64_t)i0 * a.heads) * D;
+        const int64_t step = (int64_t)split * a.heads * D;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+          const float w = __shfl_sync(0xffffffffu, weight, i);
+#pragma unroll
+          for (int j = 0; j < MOE_ATTENTION_MAX_DIM / kWarp; ++j)
+            if (j * kWarp + lane < D) o[j] = fmaf(w, rows[i * step + j * kWarp + lane], o[j]);
         }
+      }
+    }
+    if (split > 1) {
+      __syncthreads();
+      if (lane == 0) s_ml[warp] = make_float2(m, sum);
+#pragma unroll
+      for (int j = 0; j < MOE_ATTENTION_MAX_DIM / kWarp; ++j) s_o[warp][j * kWarp + lane] = o[j];
+      __syncthreads();
+      if (sub != 0) continue;
+      float top = -INFINITY;
+      for (int w = 0; w < split; ++w) top = fmaxf(top, s_ml[warp + w].x);
+      m = top;
+      sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < MOE_ATTENTION_MAX_DIM / kWarp; ++j) o[j] = 0.0f;
+      const float base = top == -INFINITY ? 0.0f : top;
+      for (int w = 0; w < split; ++w) {
+        const float2 ml = s_ml[warp + w];
+        const float weight = exp2f(ml.x - base);
+        sum += ml.y * weight;
+#pragma unroll
+        for (int j = 0; j < MOE_ATTENTION_MAX_DIM / kWarp; ++j) o[j] = fmaf(weight, s_o[warp + w][j * kWarp + lane], o[j]);
+      }
+    }
+    if (h >= a.heads) continue;
+    const int64_t head = (int64_t)b * a.heads + h;
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int j = 0; j < MOE_ATTENTION_MAX_DIM / kWarp; ++j) {
+      const int d = j * kWarp + lane;
+      if (d >= D) continue;
+      if constexpr (sizeof(ET) == 4) {
+        static_cast<float*>(a.out)[head * D + d] = o[j] * inv;
+      } else {
+        static_cast<__nv_bfloat16*>(a.out)[head * D + d] = __float2bfloat16_rn(o[j] * inv);
       }
     }
     if (lane == 0 && a.lse != nullptr) a.lse[head] = sum > 0.0f ? (m + log2f(sum)) * kLn2 : -INFINITY;
@@ -783,9 +831,8 @@ template <typename ET> int run_attend(AttendArgs& a, cudaStream_t s) {
                         : launch_rows_dim<ET, 8>(a, s);
   }
   if (rc != MOE_OK) return rc;
-  const int blocks = (a.heads + 7) / 8;
   int y = (int)(4 * (int64_t)num_sms() / a.seqs);
-  y = y < 1 ? 1 : (y > blocks ? blocks : y);
+  y = y < 1 ? 1 : (y > a.heads ? a.heads : y);
   launch(attend_join_kernel<ET>, dim3((unsigned)a.seqs, (unsigned)y), dim3(256), 0, s, a);
   return check_launch();
 }
