@@ -49,12 +49,13 @@ template <int DP, int MT, bool SHIFT>
 __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_mma_kernel(const AttendArgs a) {
   using S = Mma<DP, MT, SHIFT>;
   constexpr int kWarps = S::kWarps, kStages = S::kStages, kTiles = S::kTiles, kPitch = S::kPitch;
-  constexpr int kChunks = DP / 8, kRowsPass = kWarp / kChunks, kPasses = kTile / kRowsPass;  // 16-byte pieces of a row
+  constexpr int kTurns = DP / 32;  // of four lanes over the 16-byte pieces of a row
   constexpr int kSteps = DP / 16;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_prefix[kWarps * kWarp], s_warp[kWarps];
-  __shared__ unsigned s_mask[kWarps][kStages];
-  __shared__ uint64_t s_low[kWarps][SHIFT ? kStages : 1];  // four bits a row: its offset to 16 bytes
+  // Rows that are there: a bit each or, with SHIFT, four equal ones, rows 0 to 7 and 8 to 15.
+  __shared__ unsigned s_mask[kWarps][kStages][SHIFT ? 2 : 1];
+  __shared__ uint8_t s_low[kWarps][SHIFT ? kStages : 1][kTile];  // rows' offsets to 16 bytes
   await_previous_kernel();
   start_next_kernel();
   const int lane = lane_id(), warp = threadIdx.x / kWarp;
@@ -73,109 +74,140 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
     for (int i = lane; i < kStages * S::kStageBytes / 16; i += kWarp) z[i] = make_uint4(0, 0, 0, 0);
     __syncwarp();
   }
-  const auto place = [](int row, int c) { return row * kPitch + (SHIFT ? c : c ^ (row & 7)) * 16; };
 
-  // Copies of a tile: K then V, 16 rows each.
+  // Copies of a tile: K then V, 16 rows each, whole rows at a time, so that each
+  // fetch is one of 256 bytes (four lanes a row take 40 instructions instead of
+  // 150, but pieces of 64 bytes: 64 ragged sequences 157 us instead of 147). With
+  // SHIFT there are more instructions a copy, and four lanes a row win.
   Cursor in = find_tile(a, s_prefix, lo);
   Cursor at = in;
-  int issued = 0, page = page_entry(a, in, lane & (kTile - 1));
+  constexpr int kChunks = DP / 8, kRowsPass = kWarp / kChunks, kPasses = kTile / kRowsPass;
+  const int r0 = lane >> 2, quarter = lane & 3, pieces = (D + 7) / 8;
   const int chunk = lane % kChunks, sub = lane / kChunks;
-  const bool copies = chunk * 8 < D;
-  const int k_low = SHIFT ? (int)(reinterpret_cast<uintptr_t>(a.k) & 15) : 0, v_low = SHIFT ? (int)(reinterpret_cast<uintptr_t>(a.v) & 15) : 0;
+  int issued = 0, page[2] = {page_entry(a, in, SHIFT ? r0 : lane & (kTile - 1)), SHIFT ? page_entry(a, in, r0 + 8) : 0};
+  const intptr_t apart = a.v - a.k;
   const auto issue = [&]() {
     if (issued < count) {
-      const int stage = issued % kStages, row = lane & (kTile - 1);
-      int64_t off = row_offset(a, in, row, page, kv);
-      const unsigned valid = __ballot_sync(0xffffffffu, off >= 0) & 0xffffu;
-      if (lane == 0) s_mask[warp][stage] = valid;
-      if constexpr (SHIFT) {
-        uint64_t low = lane < kTile ? (uint64_t)(off & 15) << (4 * row) : 0;
-#pragma unroll
-        for (int d = 1; d < kTile; d <<= 1) low |= __shfl_xor_sync(0xffffffffu, low, d);
-        if (lane == 0) s_low[warp][stage] = low;
-      }
+      const int stage = issued % kStages;
       const int fresh = a.k_new != nullptr ? in.n - 1 - (in.first + in.tile * kTile) : -1;  // the new token's row
-      const uint32_t base = ring + stage * S::kStageBytes;
-      if (fresh >= 0 && fresh < kTile && (valid >> fresh & 1)) {
-        const int64_t to = __shfl_sync(0xffffffffu, off, fresh);
-        if (row == fresh) off = -2;
-        const char* kn = a.k_new + in.b * a.kn_row + kv * a.kn_head;
-        const char* vn = a.v_new + in.b * a.vn_row + kv * a.vn_head;
-        if constexpr (SHIFT) {  // to where the row's own bytes would lie
-          unsigned char* k_to = smem + (size_t)warp * kStages * S::kStageBytes + stage * S::kStageBytes + fresh * kPitch;
-          unsigned char* v_to = k_to + kTile * kPitch + ((to + v_low) & 15);
-          k_to += (to + k_low) & 15;
-          for (int d = lane; d < D; d += kWarp) {
-            const uint16_t kk = reinterpret_cast<const uint16_t*>(kn)[d], vv = reinterpret_cast<const uint16_t*>(vn)[d];
-            reinterpret_cast<uint16_t*>(k_to)[d] = kk;
-            reinterpret_cast<uint16_t*>(v_to)[d] = vv;
-            if (part == 0) {
-              reinterpret_cast<uint16_t*>(a.k + to)[d] = kk;
-              reinterpret_cast<uint16_t*>(a.v + to)[d] = vv;
+      const char* kn = a.k_new + in.b * a.kn_row + kv * a.kn_head;
+      const char* vn = a.v_new + in.b * a.vn_row + kv * a.vn_head;
+      if constexpr (SHIFT) {
+        const uint32_t base = ring + stage * S::kStageBytes + r0 * kPitch + quarter * 16;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const int64_t off = row_offset(a, in, r0 + 8 * w, page[w], kv);
+          const unsigned there = __ballot_sync(0xffffffffu, off >= 0);
+          if (lane == 0) s_mask[warp][stage][w] = there;
+          const int bytes = off >= 0 ? 16 : 0;
+          const uint32_t to = base + 8 * w * kPitch;
+          const uintptr_t k_from = reinterpret_cast<uintptr_t>(a.k) + (off < 0 ? 0 : off), v_from = k_from + apart;
+          // The aligned pieces from the row's first byte's on. A row that is not there is zero to its end.
+          const int k_low = (int)(k_from & 15), v_low = (int)(v_from & 15);
+          const int k_end = bytes == 0 ? 2 * DP + 16 : 2 * D + k_low, v_end = bytes == 0 ? 2 * DP + 16 : 2 * D + v_low;
+          if (quarter == 0) s_low[warp][stage][r0 + 8 * w] = (uint8_t)(k_low | v_low << 4);
+          if (off >= 0 && r0 + 8 * w == fresh) {  // to where the row's own bytes would lie
+            unsigned char* ks = smem + (to - quarter * 16 - smem_u32(smem));
+            unsigned char* vs = ks + kTile * kPitch;
+            for (int d = quarter; d < D; d += 4) {
+              const uint16_t kk = reinterpret_cast<const uint16_t*>(kn)[d], vv = reinterpret_cast<const uint16_t*>(vn)[d];
+              reinterpret_cast<uint16_t*>(ks + k_low)[d] = kk;
+              reinterpret_cast<uint16_t*>(vs + v_low)[d] = vv;
+              if (part == 0) {
+                reinterpret_cast<uint16_t*>(k_from)[d] = kk;
+                reinterpret_cast<uint16_t*>(v_from)[d] = vv;
+              }
+            }
+          } else {
+            const char* kp = reinterpret_cast<const char*>(k_from - k_low) + quarter * 16;
+            const char* vp = reinterpret_cast<const char*>(v_from - v_low) + quarter * 16;
+#pragma unroll
+            for (int i = 0; i <= kTurns; ++i) {
+              if (i == kTurns && quarter != 0) continue;
+              if (quarter * 16 + i * 64 < k_end) cp_async16(to + i * 64, kp + i * 64, bytes);
+              if (quarter * 16 + i * 64 < v_end) cp_async16(to + i * 64 + kTile * kPitch, vp + i * 64, bytes);
             }
           }
-        } else if (sub == 0 && copies) {
-          const uint32_t dst = base + place(fresh, chunk);
-          cp_async16(dst, kn + chunk * 16, 16);
-          cp_async16(dst + kTile * kPitch, vn + chunk * 16, 16);
-          if (part == 0) {
-            *reinterpret_cast<uint4*>(a.k + to + chunk * 16) = *reinterpret_cast<const uint4*>(kn + chunk * 16);
-            *reinterpret_cast<uint4*>(a.v + to + chunk * 16) = *reinterpret_cast<const uint4*>(vn + chunk * 16);
+        }
+      } else {
+        const int row = lane & (kTile - 1);
+        int64_t off = row_offset(a, in, row, page[0], kv);
+        const unsigned there = __ballot_sync(0xffffffffu, off >= 0) & 0xffffu;
+        if (lane == 0) s_mask[warp][stage][0] = there;
+        const uint32_t base = ring + stage * S::kStageBytes;
+        if (fresh >= 0 && fresh < kTile && (there >> fresh & 1)) {
+          const int64_t to = __shfl_sync(0xffffffffu, off, fresh);
+          if (row == fresh) off = -2;
+          if (sub == 0 && chunk < pieces) {
+            const uint32_t dst = base + fresh * kPitch + (chunk ^ (fresh & 7)) * 16;
+            cp_async16(dst, kn + chunk * 16, 16);
+            cp_async16(dst + kTile * kPitch, vn + chunk * 16, 16);
+            if (part == 0) {
+              *reinterpret_cast<uint4*>(a.k + to + chunk * 16) = *reinterpret_cast<const uint4*>(kn + chunk * 16);
+              *reinterpret_cast<uint4*>(a.v + to + chunk * 16) = *reinterpret_cast<const uint4*>(vn + chunk * 16);
+            }
           }
         }
-      }
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        const int row_i = i * kRowsPass + sub;
-        const int64_t from = __shfl_sync(0xffffffffu, off, row_i);
-        if (from == -2) continue;
-        const uint32_t dst = base + place(row_i, chunk);
-        if constexpr (SHIFT) {
-          // The pieces from the row's first byte's on; with an offset there may be one more than the row has.
-          const char* k_from = a.k + (from < 0 ? -k_low : from);
-          const char* v_from = a.v + (from < 0 ? -v_low : from);
-          const int k_off = (int)(reinterpret_cast<uintptr_t>(k_from) & 15), v_off = (int)(reinterpret_cast<uintptr_t>(v_from) & 15);
-          const int bytes = from < 0 ? 0 : 16;
-#pragma unroll
-          for (int c = chunk; c <= kChunks; c += kChunks) {
-            if (from < 0 || c * 16 < 2 * D + k_off) cp_async16(dst + (c - chunk) * 16, k_from - k_off + c * 16, bytes);
-            if (from < 0 || c * 16 < 2 * D + v_off) cp_async16(dst + (c - chunk) * 16 + kTile * kPitch, v_from - v_off + c * 16, bytes);
-          }
-        } else if (copies) {
+        for (int i = 0; i < kPasses; ++i) {
+          const int row_i = i * kRowsPass + sub;
+          const int64_t from = __shfl_sync(0xffffffffu, off, row_i);
+          if (from == -2 || chunk >= pieces) continue;
           const int bytes = from < 0 ? 0 : 16;
           const int64_t o = from < 0 ? 0 : from + chunk * 16;
+          const uint32_t dst = base + row_i * kPitch + (chunk ^ (row_i & 7)) * 16;
           cp_async16(dst, a.k + o, bytes);
           cp_async16(dst + kTile * kPitch, a.v + o, bytes);
         }
       }
       if (++issued < count) {
         in.next(a);
-        page = page_entry(a, in, row);
+        page[0] = page_entry(a, in, SHIFT ? r0 : lane & (kTile - 1));
+        if constexpr (SHIFT) page[1] = page_entry(a, in, r0 + 8);
       }
     }
     cp_commit();
   };
-  // SHIFT: moves a tile's rows to the beginnings of their places, zeros behind D.
+  // SHIFT: moves a tile's rows to the beginnings of their places, zeros behind
+  // D. In a turn the four lanes of a row take five pieces and put four.
   const auto align = [&](int stage) {
-    const uint64_t low = s_low[warp][SHIFT ? stage : 0];
-    unsigned char* base = smem + (size_t)warp * kStages * S::kStageBytes + stage * S::kStageBytes;
+    int low[4];  // K of rows r0 and r0 + 8, V of them
 #pragma unroll
-    for (int i = 0; i < 2 * kPasses; ++i) {
-      const int row = (i % kPasses) * kRowsPass + sub, off = ((int)(low >> (4 * row)) + (i < kPasses ? k_low : v_low)) & 15;
-      uint4* to = reinterpret_cast<uint4*>(base + (i < kPasses ? 0 : kTile * kPitch) + row * kPitch) + chunk;
-      const uint4 x = to[0], y = to[1];
-      const int left = 2 * (D - 8 * chunk);  // bytes of the row from this piece on
-      // off / 4 words further on (by two, then by one), and two bytes more where it is odd in them.
-      const bool two = off & 8, one = off & 4;
-      const uint32_t w0 = two ? x.z : x.x, w1 = two ? x.w : x.y, w2 = two ? y.x : x.z, w3 = two ? y.y : x.w, w4 = two ? y.z : y.x,
-                     w5 = two ? y.w : y.y;
-      const uint32_t t0 = one ? w1 : w0, t1 = one ? w2 : w1, t2 = one ? w3 : w2, t3 = one ? w4 : w3, t4 = one ? w5 : w4;
-      const int bits = (off & 2) * 8;
-      uint32_t v[4] = {__funnelshift_r(t0, t1, bits), __funnelshift_r(t1, t2, bits), __funnelshift_r(t2, t3, bits), __funnelshift_r(t3, t4, bits)};
+    for (int w = 0; w < 2; ++w) {
+      const int both = s_low[warp][SHIFT ? stage : 0][r0 + 8 * w];
+      low[w] = both & 15;
+      low[2 + w] = both >> 4;
+    }
+    uint4* base = reinterpret_cast<uint4*>(smem + (ring - smem_u32(smem)) + stage * S::kStageBytes + r0 * kPitch + quarter * 16);
+#pragma unroll 1
+    for (int i = 0; i * 4 < pieces; ++i) {
+      uint32_t v[4][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = left >= 4 * e + 4 ? v[e] : left <= 4 * e ? 0u : v[e] & 0xffffu;
+      for (int w = 0; w < 4; ++w) {
+        const uint4* from = base + ((w & 1) * 8 * kPitch + (w >> 1) * kTile * kPitch) / 16 + i * 4;
+        const uint4 x = from[0], y = from[1];
+        // low / 4 words further on (by two, then by one), and two bytes more where it is odd in them.
+        const bool two = low[w] & 8, one = low[w] & 4;
+        const uint32_t w0 = two ? x.z : x.x, w1 = two ? x.w : x.y, w2 = two ? y.x : x.z, w3 = two ? y.y : x.w, w4 = two ? y.z : y.x,
+                       w5 = two ? y.w : y.y;
+        const uint32_t t0 = one ? w1 : w0, t1 = one ? w2 : w1, t2 = one ? w3 : w2, t3 = one ? w4 : w3, t4 = one ? w5 : w4;
+        const int bits = (low[w] & 2) * 8;
+        v[w][0] = __funnelshift_r(t0, t1, bits);
+        v[w][1] = __funnelshift_r(t1, t2, bits);
+        v[w][2] = __funnelshift_r(t2, t3, bits);
+        v[w][3] = __funnelshift_r(t3, t4, bits);
+      }
+      const int left = D - 8 * (quarter + 4 * i);  // elements of the row from this piece on
+      if (left < 8) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[w][e] &= 2 * e + 2 <= left ? 0xffffffffu : 2 * e >= left ? 0u : 0xffffu;
+      }
       __syncwarp();
-      to[0] = make_uint4(v[0], v[1], v[2], v[3]);
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        base[((w & 1) * 8 * kPitch + (w >> 1) * kTile * kPitch) / 16 + i * 4] = make_uint4(v[w][0], v[w][1], v[w][2], v[w][3]);
     }
     __syncwarp();
   };
@@ -225,7 +257,10 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
     cp_wait<kStages - 2>();
     __syncwarp();
     const int stage = i % kStages;
-    const unsigned valid = s_mask[warp][stage];
+    unsigned there[2];  // of the first and last eight keys, four equal bits each with SHIFT
+    there[0] = s_mask[warp][stage][0];
+    there[1] = SHIFT ? s_mask[warp][stage][SHIFT ? 1 : 0] : there[0] >> 8;
+    const bool all = SHIFT ? (there[0] & there[1]) == 0xffffffffu : there[0] == 0xffffu;
     issue();  // into the stage that the previous tile left
     if constexpr (SHIFT) align(stage);
     const uint32_t base = ring + stage * S::kStageBytes;
@@ -238,6 +273,7 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
         for (int e = 0; e < 4; ++e) s[u][n][e] = 0.0f;
 #pragma unroll
     for (int ks = 0; ks < kSteps; ++ks) {
+      if (SHIFT && ks * 16 >= D) continue;
       uint32_t b[4];
       ldmatrix(b, base + k_at + (((ks * 2 + (mi & 1)) ^ swizzle) * 16));
 #pragma unroll
@@ -261,7 +297,7 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
           for (int e = 0; e < 2; ++e) {
             float& x = s[u][n][2 * w + e];
             x *= a.scale;
-            if (valid != 0xffffu && !(valid >> (n * 8 + t * 2 + e) & 1)) x = -INFINITY;
+            if (!all && !(there[n] >> (t * 2 + e) * (SHIFT ? 4 : 1) & 1)) x = -INFINITY;
             top = fmaxf(top, x);
           }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -293,6 +329,7 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
         if constexpr (MT == 0) keep[1] = keep[0];
 #pragma unroll
         for (int n = 0; n < DP / 8; ++n) {
+          if (SHIFT && n * 8 >= D) continue;
           o[u][n][0] *= keep[0];
           o[u][n][1] *= keep[0];
           o[u][n][2] *= keep[1];
@@ -302,6 +339,7 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
     }
 #pragma unroll
     for (int c = 0; c < kSteps; ++c) {
+      if (SHIFT && c * 16 >= D) continue;
       uint32_t b[4];
       ldmatrix_trans(b, base + v_at + (((c * 2 + (mi >> 1)) ^ swizzle) * 16));
 #pragma unroll

@@ -1,10 +1,9 @@
 // Decode attention of fp32 caches (attention_decode.cu has the whole of it).
 #include "attend.h"
+#include "vec_math.cuh"
 
 namespace moe {
 namespace {
-
-constexpr int kKeys = 8;  // of a step
 
 // A row in shared memory: pieces of 16 bytes, a multiple of four of them. The
 // lanes that read two neighbouring keys at once find them in different banks:
@@ -14,16 +13,21 @@ struct RowPieces {
   int pieces, pitch, swap;
   __host__ __device__ explicit RowPieces(int D) : pieces((D + 3) / 4), pitch((pieces + 3) / 4 * 4), swap(pitch % 8 == 0 ? 4 : 0) {}
 };
+constexpr int kSlots = 3;  // of a warp's ring, a tile's keys or values each
 
-// A warp takes 8 keys at a time through a ring of kStages of them. Scores: lane
-// (key, quarter) takes the fourth of the key's pieces that `quarter` says, for
-// all GM heads; values: a lane owns pieces of the rows for all heads. VB: bytes
-// of an asynchronous copy, 4 where rows are off 16.
-template <int GM, int NC, int VB, int kStages>
+__device__ __forceinline__ uint64_t pair(float a, float b) { return f2_pack(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) { return f2_pack(a, b); }
+
+// A warp takes a tile's 16 keys, then its values, through a ring of three slots:
+// while one is used the next two are on their way. Scores: lane (key, quarter)
+// takes the fourth of the pieces of two keys that `quarter` says, for all GM
+// heads; values: a lane owns pieces of the rows for all heads. Two elements an
+// instruction (fma.f32x2). VB: bytes of an asynchronous copy, 4 where rows are
+// off 16.
+template <int GM, int NC, int VB>
 __global__ void __launch_bounds__(kSmWarps * kWarp, 1) attend_rows_kernel(const AttendArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_prefix[kSmWarps * kWarp], s_warp[kSmWarps];
-  __shared__ unsigned s_mask[kSmWarps][kStages];
   await_previous_kernel();
   start_next_kernel();
   const int lane = lane_id(), warp = threadIdx.x / kWarp, warps = blockDim.x / kWarp;
@@ -33,86 +37,81 @@ __global__ void __launch_bounds__(kSmWarps * kWarp, 1) attend_rows_kernel(const 
   if (total == 0) return;
   const int ranges = ranges_of(a, total);
   if (r >= ranges) return;
-  const int lo = range_begin(r, ranges, total), count = 2 * (range_begin(r + 1, ranges, total) - lo);  // steps
+  const int lo = range_begin(r, ranges, total), count = range_begin(r + 1, ranges, total) - lo;
   if (count <= 0) return;
 
   const int D = a.D;
   const RowPieces row(D);
-  const int half_bytes = kKeys * row.pitch * 16, stage_bytes = 2 * half_bytes;
-  unsigned char* own = smem + (size_t)warp * (kStages * stage_bytes + GM * row.pitch * 16 + GM * kKeys * 4);
-  float* qs = reinterpret_cast<float*>(own + kStages * stage_bytes);
-  float* ps = qs + GM * row.pitch * 4;
+  const int slot_bytes = kTile * row.pitch * 16;
+  unsigned char* own = smem + (size_t)warp * (kSlots * slot_bytes + GM * row.pitch * 16 + GM * kTile * 8);
+  float* qs = reinterpret_cast<float*>(own + kSlots * slot_bytes);
+  uint64_t* ps = reinterpret_cast<uint64_t*>(qs + GM * row.pitch * 4);  // [GM][16], each probability twice
   const uint32_t ring = smem_u32(own);
-  for (int i = lane; i < (kStages * stage_bytes + GM * row.pitch * 16) / 16; i += kWarp)  // what lies behind D stays zero
+  for (int i = lane; i < (kSlots * slot_bytes + GM * row.pitch * 16) / 16; i += kWarp)  // what lies behind D stays zero
     reinterpret_cast<uint4*>(own)[i] = make_uint4(0, 0, 0, 0);
   __syncwarp();
 
-  // Copies of a step: 8 rows of keys, then of values.
+  // Copies of a tile's keys, then of its values: four lanes a row (rows r0 and
+  // r0 + 8), so that a copy's addresses are a register and a constant.
+  constexpr int kTurns = VB == 16 ? NC * 8 : NC * 32;  // of the four lanes over a row
   Cursor in = find_tile(a, s_prefix, lo);
   Cursor at = in;
-  int issued = 0, page = page_entry(a, in, lane & (kTile - 1));
-  int64_t off = -1;
-  unsigned valid = 0;
-  const int copies = VB == 16 ? row.pieces : D;  // of a row
-  const auto issue = [&]() {
+  const int r0 = lane >> 2, part4 = lane & 3, pieces = VB == 16 ? row.pieces : D;
+  int issued = 0, slot_in = 0, page[2] = {page_entry(a, in, r0), page_entry(a, in, r0 + 8)}, bytes[2];
+  unsigned there[2];  // rows of the tile issued last that are there, four equal bits each
+  const char* from[2];
+  const intptr_t apart = a.v - a.k;
+  const int flip = r0 & 1 ? row.swap * 16 : 0;
+  const uint32_t place = r0 * row.pitch * 16 + part4 * VB;
+  const auto issue = [&](bool values) {
     if (issued < count) {
-      const int stage = issued % kStages, part8 = issued & 1, mine = lane & (kTile - 1);
-      if (part8 == 0) {
-        off = row_offset(a, in, mine, page, kv);
-        valid = __ballot_sync(0xffffffffu, off >= 0) & 0xffffu;
-      }
-      if (lane == 0) s_mask[warp][stage] = valid >> (part8 * kKeys) & 0xffu;
-      const int fresh = a.k_new != nullptr ? in.n - 1 - (in.first + in.tile * kTile) - part8 * kKeys : -1;  // the new token's row
-      const uint32_t base = ring + stage * stage_bytes;
+      const uint32_t base = ring + slot_in * slot_bytes + place;
+      const int fresh = a.k_new != nullptr ? in.n - 1 - (in.first + in.tile * kTile) : -1;  // the new token's row
 #pragma unroll
-      for (int i = 0; i < kKeys; ++i) {
-        const int64_t from = __shfl_sync(0xffffffffu, off, part8 * kKeys + i);
-        if (from < 0) {
-          // A row that is not there: zeros, which its probability of zero can be multiplied by.
-          for (int c = lane; c < row.pieces; c += kWarp) {
-            uint4* dst = reinterpret_cast<uint4*>(own + stage * stage_bytes) + i * row.pitch + (c ^ (i & 1 ? row.swap : 0));
-            dst[0] = dst[kKeys * row.pitch] = make_uint4(0, 0, 0, 0);
-          }
-          continue;
+      for (int w = 0; w < 2; ++w) {
+        if (!values) {
+          const int64_t off = row_offset(a, in, r0 + 8 * w, page[w], kv);
+          there[w] = __ballot_sync(0xffffffffu, off >= 0);
+          bytes[w] = off >= 0 ? VB : 0;
+          from[w] = a.k + (off < 0 ? 0 : off);
         }
-        const char* ksrc = a.k + from;
-        const char* vsrc = a.v + from;
-        if (i == fresh) {
-          ksrc = a.k_new + in.b * a.kn_row + kv * a.kn_head;
-          vsrc = a.v_new + in.b * a.vn_row + kv * a.vn_head;
+        const char* src = from[w] + (values ? apart : 0);
+        if (r0 + 8 * w == fresh && bytes[w] != 0) {
+          const char* kept = src;
+          src = values ? a.v_new + in.b * a.vn_row + kv * a.vn_head : a.k_new + in.b * a.kn_row + kv * a.kn_head;
           if (part == 0)
-            for (int d = lane; d < D; d += kWarp) {
-              reinterpret_cast<float*>(a.k + from)[d] = reinterpret_cast<const float*>(ksrc)[d];
-              reinterpret_cast<float*>(a.v + from)[d] = reinterpret_cast<const float*>(vsrc)[d];
-            }
+            for (int d = part4; d < D; d += 4) reinterpret_cast<float*>(const_cast<char*>(kept))[d] = reinterpret_cast<const float*>(src)[d];
         }
-        for (int c = lane; c < copies; c += kWarp) {
+        src += part4 * VB;
+        const uint32_t to = base + 8 * w * row.pitch * 16, even = to + flip, odd = to - flip;  // 64 bytes on in every other 64
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+          if (part4 + 4 * i >= pieces) continue;
           if constexpr (VB == 16) {
-            const uint32_t dst = base + (i * row.pitch + (c ^ (i & 1 ? row.swap : 0))) * 16;
-            cp_async16(dst, ksrc + c * 16, 16);
-            cp_async16(dst + half_bytes, vsrc + c * 16, 16);
+            cp_async16((i & 1 ? odd : even) + i * 64, src + i * 64, bytes[w]);
           } else {
-            const uint32_t dst = base + (i * row.pitch + ((c >> 2) ^ (i & 1 ? row.swap : 0))) * 16 + (c & 3) * 4;
-            cp_async4(dst, ksrc + c * 4, 4);
-            cp_async4(dst + half_bytes, vsrc + c * 4, 4);
+            cp_async4((i & 4 ? odd : even) + i * 16, src + i * 16, bytes[w]);
           }
         }
       }
-      if (++issued < count && part8 == 1) {
+      if (values && ++issued < count) {
         in.next(a);
-        page = page_entry(a, in, mine);
+        page[0] = page_entry(a, in, r0);
+        page[1] = page_entry(a, in, r0 + 8);
       }
+      slot_in = slot_in == kSlots - 1 ? 0 : slot_in + 1;
     }
     cp_commit();
   };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue();
+  issue(false);
+  issue(true);
 
   const int h0 = kv * a.group + part * GM, heads = min(GM, a.group - part * GM);
   const int key = lane >> 2, quarter = lane & 3, swap = key & 1 ? row.swap : 0;
-  float m[GM], l[GM], o[GM][NC][4];
+  float m[GM], l[GM];
+  uint64_t o[GM][NC][2];
   bool fresh = true;
-  int first_tile = at.tile;
+  int first_tile = at.tile, slot = 0;
   for (int i = 0; i < count; ++i) {
     if (fresh) {
       fresh = false;
@@ -126,88 +125,91 @@ __global__ void __launch_bounds__(kSmWarps * kWarp, 1) attend_rows_kernel(const 
         m[h] = -INFINITY;
         l[h] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NC; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[h][j][e] = 0.0f;
+        for (int j = 0; j < NC; ++j) o[h][j][0] = o[h][j][1] = 0;
       }
     }
-    cp_wait<kStages - 2>();
+    cp_wait<1>();
     __syncwarp();
-    const int stage = i % kStages;
-    const unsigned bits = s_mask[warp][stage];
-    issue();  // into the stage that the previous step left
-    const float4* ks = reinterpret_cast<const float4*>(own + stage * stage_bytes);
-    const float4* vs = ks + kKeys * row.pitch;
-    if (bits != 0) {
-      // Scores of (key, all heads), the same in the four lanes of a key.
-      float s[GM];
+    const unsigned now_there[2] = {there[0], there[1]};  // no later tile's keys are issued yet
+    issue(false);      // into the slot that the previous tile's values left
+    {
+      // Scores of two keys, all heads, the same in the four lanes of a key.
+      const uint4* ks = reinterpret_cast<const uint4*>(own + slot * slot_bytes) + key * row.pitch;
+      uint64_t s[GM][2];
 #pragma unroll
-      for (int h = 0; h < GM; ++h) s[h] = 0.0f;
-#pragma unroll 4
+      for (int h = 0; h < GM; ++h) s[h][0] = s[h][1] = 0;
+#pragma unroll 2
       for (int p = quarter; p < row.pieces; p += 4) {
-        const float4 kk = ks[key * row.pitch + (p ^ swap)];
+        const uint4 k0 = ks[p ^ swap], k1 = ks[8 * row.pitch + (p ^ swap)];
+        const uint64_t k00 = pair(k0.x, k0.y), k01 = pair(k0.z, k0.w), k10 = pair(k1.x, k1.y), k11 = pair(k1.z, k1.w);
 #pragma unroll
         for (int h = 0; h < GM; ++h) {
-          const float4 qq = reinterpret_cast<const float4*>(qs)[h * row.pitch + p];
-          s[h] = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, fmaf(qq.z, kk.z, fmaf(qq.w, kk.w, s[h]))));
+          const uint4 qq = reinterpret_cast<const uint4*>(qs)[h * row.pitch + p];
+          const uint64_t q0 = pair(qq.x, qq.y), q1 = pair(qq.z, qq.w);
+          s[h][0] = f2_fma(q1, k01, f2_fma(q0, k00, s[h][0]));
+          s[h][1] = f2_fma(q1, k11, f2_fma(q0, k10, s[h][1]));
         }
       }
 #pragma unroll
       for (int h = 0; h < GM; ++h) {
-        s[h] += __shfl_xor_sync(0xffffffffu, s[h], 1);
-        s[h] += __shfl_xor_sync(0xffffffffu, s[h], 2);
-        if (!(bits >> key & 1)) s[h] = -INFINITY;
-        float t = s[h];
+        float x[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float lo2, hi2;
+          f2_unpack(s[h][e], lo2, hi2);
+          x[e] = lo2 + hi2;
+          x[e] += __shfl_xor_sync(0xffffffffu, x[e], 1);
+          x[e] += __shfl_xor_sync(0xffffffffu, x[e], 2);
+          if (!(now_there[e] >> (4 * key) & 1)) x[e] = -INFINITY;
+        }
+        float t = fmaxf(x[0], x[1]);
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-        const float now = fmaxf(m[h], t), base = now == -INFINITY ? 0.0f : now;
+        const float now = fmaxf(m[h], t), from = now == -INFINITY ? 0.0f : now;
         if (now > m[h]) {  // the same in every lane
-          const float keep = exp2f(m[h] - base);
+          const float keep = exp2f(m[h] - from);
           m[h] = now;
           l[h] *= keep;
 #pragma unroll
           for (int j = 0; j < NC; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[h][j][e] *= keep;
+            for (int e = 0; e < 2; ++e) o[h][j][e] = f2_mul(o[h][j][e], pair(keep, keep));
         }
-        const float pr = exp2f(s[h] - base);
+        const float p0 = exp2f(x[0] - from), p1 = exp2f(x[1] - from);
+        l[h] += p0 + p1;  // four lanes have each
         if (quarter == 0) {
-          l[h] += pr;
-          ps[h * kKeys + key] = pr;
+          ps[h * kTile + key] = pair(p0, p0);
+          ps[h * kTile + key + 8] = pair(p1, p1);
         }
       }
-      __syncwarp();
-      float pr[GM][kKeys];
+    }
+    slot = slot == kSlots - 1 ? 0 : slot + 1;
+    cp_wait<1>();
+    __syncwarp();
+    issue(true);
+    {
+      const uint4* vs = reinterpret_cast<const uint4*>(own + slot * slot_bytes);
+#pragma unroll 4
+      for (int e = 0; e < kTile; e += 2) {
+        uint4 pr[GM];  // the probabilities of two keys, each twice
 #pragma unroll
-      for (int h = 0; h < GM; ++h)
+        for (int h = 0; h < GM; ++h) pr[h] = *reinterpret_cast<const uint4*>(ps + h * kTile + e);
 #pragma unroll
-        for (int e = 0; e < kKeys; e += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(ps + h * kKeys + e);
-          pr[h][e] = x.x;
-          pr[h][e + 1] = x.y;
-          pr[h][e + 2] = x.z;
-          pr[h][e + 3] = x.w;
-        }
+        for (int j = 0; j < NC; ++j) {
+          const int p = lane + j * kWarp;
+          if (p >= row.pieces) continue;
+          const uint4 v0 = vs[e * row.pitch + p], v1 = vs[(e + 1) * row.pitch + (p ^ row.swap)];
 #pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        const int p = lane + j * kWarp;
-        if (p < row.pieces) {
-#pragma unroll
-          for (int e = 0; e < kKeys; ++e) {
-            const float4 vv = vs[e * row.pitch + (p ^ (e & 1 ? row.swap : 0))];
-#pragma unroll
-            for (int h = 0; h < GM; ++h) {
-              o[h][j][0] = fmaf(pr[h][e], vv.x, o[h][j][0]);
-              o[h][j][1] = fmaf(pr[h][e], vv.y, o[h][j][1]);
-              o[h][j][2] = fmaf(pr[h][e], vv.z, o[h][j][2]);
-              o[h][j][3] = fmaf(pr[h][e], vv.w, o[h][j][3]);
-            }
+          for (int h = 0; h < GM; ++h) {
+            const uint64_t p0 = pair(pr[h].x, pr[h].y), p1 = pair(pr[h].z, pr[h].w);
+            o[h][j][0] = f2_fma(p1, pair(v1.x, v1.y), f2_fma(p0, pair(v0.x, v0.y), o[h][j][0]));
+            o[h][j][1] = f2_fma(p1, pair(v1.z, v1.w), f2_fma(p0, pair(v0.z, v0.w), o[h][j][1]));
           }
         }
       }
     }
-    if ((i & 1) == 0) continue;
+    slot = slot == kSlots - 1 ? 0 : slot + 1;
     const bool last = at.tile == at.tiles - 1;
     if (last || i == count - 1) {
       const bool whole = last && first_tile == 0;
@@ -215,18 +217,22 @@ __global__ void __launch_bounds__(kSmWarps * kWarp, 1) attend_rows_kernel(const 
       for (int h = 0; h < GM; ++h) {
         float sum = l[h];
 #pragma unroll
-        for (int d = 1; d < kWarp; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        for (int d = 4; d < kWarp; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if (h >= heads) continue;
         const int64_t head = (whole ? (int64_t)at.b : (int64_t)r + at.b) * a.heads + h0 + h;
         const float inv = whole ? (sum > 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
         float* to = (whole ? static_cast<float*>(a.out) : a.part_o) + head * D;
 #pragma unroll
-        for (int j = 0; j < NC; ++j)
+        for (int j = 0; j < NC; ++j) {
+          float v[4];
+          f2_unpack(o[h][j][0], v[0], v[1]);
+          f2_unpack(o[h][j][1], v[2], v[3]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int d = 4 * (lane + j * kWarp) + e;
-            if (d < D) to[d] = o[h][j][e] * inv;
+            if (d < D) to[d] = v[e] * inv;
           }
+        }
         if (lane == 0) {
           if (!whole) {
             a.part_ml[head] = make_float2(m[h], sum);
@@ -236,25 +242,25 @@ __global__ void __launch_bounds__(kSmWarps * kWarp, 1) attend_rows_kernel(const 
         }
       }
       fresh = true;
+      __syncwarp();  // the next query comes into the same place
     }
     if (i + 1 < count) at.next(a);
   }
 }
 
-template <int GM, int NC, int VB, int kStages> int launch_rows(AttendArgs& a, int warps, size_t smem, cudaStream_t s) {
+template <int GM, int NC, int VB> int launch_rows(AttendArgs& a, cudaStream_t s) {
   static std::atomic<bool> raised[kSmemDevices];
-  auto k = attend_rows_kernel<GM, NC, VB, kStages>;
+  auto k = attend_rows_kernel<GM, NC, VB>;
   if (!allow_smem(k, raised)) return MOE_ERR_CUDA;
+  const RowPieces row(a.D);
+  const int bytes = kSlots * kTile * row.pitch * 16 + GM * row.pitch * 16 + GM * kTile * 8;  // of a warp
+  const int fit = 224 * 1024 / bytes, warps = fit < kSmWarps ? fit : kSmWarps;
   cut(a, GM, warps);
-  launch(k, dim3(ctas_of(a, warps)), dim3(warps * kWarp), smem, s, a);
+  launch(k, dim3(ctas_of(a, warps)), dim3(warps * kWarp), (size_t)warps * bytes, s, a);
   return check_launch();
 }
 template <int GM, int VB> int launch_rows_dim(AttendArgs& a, cudaStream_t s) {
-  constexpr int kStages = GM == 8 ? 2 : 3;  // eight heads' rows need the room of the third
-  const RowPieces row(a.D);
-  const auto bytes = [&](int stages) { return (size_t)2 * stages * kKeys * row.pitch * 16 + GM * row.pitch * 16 + GM * kKeys * 4; };
-  if (a.D <= 128) return launch_rows<GM, 1, VB, kStages>(a, 8, 8 * bytes(kStages), s);
-  return launch_rows<GM, 2, VB, 2>(a, 5, 5 * bytes(2), s);
+  return a.D <= 128 ? launch_rows<GM, 1, VB>(a, s) : launch_rows<GM, 2, VB>(a, s);
 }
 template <int VB> int launch_rows_heads(AttendArgs& a, cudaStream_t s) {
   return a.group <= 2 ? launch_rows_dim<2, VB>(a, s) : a.group <= 4 ? launch_rows_dim<4, VB>(a, s) : launch_rows_dim<8, VB>(a, s);
