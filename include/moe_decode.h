@@ -188,8 +188,8 @@ int moe_cache_copy(const moe_cache_pages* caches, int64_t num_caches, int64_t nu
  * A logit of -infinity is no candidate, and neither is anything of a beam whose
  * score or log sum is not finite (logits with a NaN or +infinity, or all
  * -infinity). Where candidates run out, score -infinity, parent -1 and token -1.
- * Totals are compared in 64 bits; the log sums come from 32-bit exponentials,
- * off by some 1e-8 relative. Repeated calls give the same bits.
+ * Totals are compared in 48 bits; the log sums come from 32-bit exponentials, off
+ * by some 1e-8. Repeated calls give the same bits.
  * num_beams <= MOE_BEAM_MAX_BEAMS, num_out <= MOE_BEAM_MAX_OUT, num_beams * ceil(vocab / 512) <= MOE_BEAM_MAX_UNITS
  * and num_requests * num_beams < 2^31, else MOE_ERR_UNSUPPORTED.
  */

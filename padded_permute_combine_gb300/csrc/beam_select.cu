@@ -9,7 +9,7 @@
 // ones in front of it, one in each of those). The second kernel, a CTA for each
 // request, joins the units' sums into the rows' log sums, finds a bound that at
 // least n units reach, reads those units again (some n KB) and sorts what passes
-// the bound by the exact comparison: totals in 64 bits, then positions.
+// the bound by the exact comparison: totals in some 48 bits, then positions.
 #include <math.h>
 
 #include <atomic>
@@ -25,7 +25,7 @@ namespace {
 constexpr int kUnit = 512;            // elements that a warp reduces at a time
 constexpr int kThreads = 256;         // of the first kernel
 constexpr int kJoinThreads = 1024;    // of the second
-constexpr int kBests = 256;           // among them the bound is found, one of four threads each
+constexpr int kBests = 256;           // most sets of units among whose best ones the bound is found
 constexpr int kList = 1024;           // candidates at hand
 constexpr int kEach = kUnit / kWarp;  // elements of a unit for a lane
 constexpr int kCached = 8192;         // units of a request that fit shared memory beside the list of those picked
@@ -166,15 +166,49 @@ __global__ void __launch_bounds__(kThreads) select_units_kernel(const SelectArgs
   }
 }
 
-// Orders as its double does, NaN excluded.
-__device__ __forceinline__ uint64_t key_of(double v) {
-  const int64_t b = __double_as_longlong(v + 0.0);  // -0.0 as +0.0
-  return (uint64_t)(b ^ ((b >> 63) | INT64_MIN));
+// Numbers of some 48 bits as sums of two 32-bit ones, the second at most half
+// a unit of the first's last place. (In 64-bit arithmetic, of which the GPU has
+// little, the rows' logarithms alone took 3.7 us, and the candidates' totals 3.)
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair sum_of(float a, float b) {
+  Pair p;
+  two_sum(a, b, p.hi, p.lo);
+  return p;
 }
-__device__ __forceinline__ double value_of(uint64_t k) {
-  const int64_t b = (int64_t)k;
-  return __longlong_as_double(b < 0 ? b ^ INT64_MIN : ~b);
+// log of s in [1, 2^100), off by 3e-9 at most: with s = 2^k f, f in [sqrt(1/2), sqrt(2)) and
+// z = (f - 1) / (f + 1), log s = k log 2 + 2 z + 2 z^3 (1/3 + z^2/5 + ...), the first two terms in pairs.
+__device__ __forceinline__ Pair log_of(Pair s) {
+  int k = (int)(__float_as_uint(s.hi) >> 23) - 127;  // s.hi in 2^k [1, 2)
+  if ((__float_as_uint(s.hi) & 0x7fffffu) > 0x3504f3u) ++k;
+  const float down = __uint_as_float((uint32_t)(127 - k) << 23);
+  const float f = s.hi * down, rest = s.lo * down;  // exact
+  const float num = f - 1.0f, den = f + 1.0f, den_rest = f - (den - 1.0f) + rest;
+  const float z = __fdiv_rn(num, den);
+  const float z_rest = (fmaf(-z, den, num) + (rest - z * den_rest)) / den;
+  const float w = z * z;
+  const float cubic = 2.0f * z * w * fmaf(fmaf(fmaf(fmaf(1.0f / 11, w, 1.0f / 9), w, 1.0f / 7), w, 1.0f / 5), w, 1.0f / 3);
+  constexpr float kHigh = 11356.0f / 16384, kLow = 3.194618495e-05f;  // of log 2: 14 bits, whose products with k are exact, and the rest
+  const Pair p = sum_of((float)k * kHigh, 2.0f * z);
+  return sum_of(p.hi, p.lo + fmaf((float)k, kLow, 2.0f * z_rest + cubic));
 }
+// score + ((x - m) - log_sum). The maximum goes off first: a row of a type's
+// lowest value has a log sum that vanishes beside it.
+__device__ __forceinline__ Pair total_of(float score, float x, float m, Pair log_sum) {
+  const Pair d = sum_of(x, -m), t = sum_of(d.hi, -log_sum.hi), u = sum_of(score, t.hi);
+  const Pair total = sum_of(u.hi, u.lo + (t.lo + (d.lo - log_sum.lo)));
+  // Differences beyond 32 bits' range: a candidate all the same, behind every other.
+  return fabsf(total.hi) < INFINITY && fabsf(total.lo) < INFINITY ? total : Pair{-3.0e38f, 0.0f};
+}
+// Orders as the pair does.
+__device__ __forceinline__ uint32_t key_half(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);  // -0.0 as +0.0
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float half_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
+__device__ __forceinline__ uint64_t key_of(Pair p) { return (uint64_t)key_half(p.hi) << 32 | key_half(p.lo); }
+__device__ __forceinline__ Pair value_of(uint64_t k) { return {half_value((uint32_t)(k >> 32)), half_value((uint32_t)k)}; }
 __device__ __forceinline__ bool better(uint64_t ka, uint32_t ia, uint64_t kb, uint32_t ib) {
   return ka > kb || (ka == kb && ia < ib);
 }
@@ -210,18 +244,19 @@ __device__ __forceinline__ void sort_list(uint64_t* keys, uint32_t* at, int n) {
 // and the sum are each off by 2^-23 of their size at most.
 __device__ __forceinline__ float slack(float t, float size) { return 3e-7f * (fabsf(t) + size); }
 
-template <typename ET>
+// The whole kernel is one request's, on one SM, and runs once: what counts is
+// the number of instructions of all its warps, and the trips to memory.
+template <typename ET, int VB>
 __global__ void __launch_bounds__(kJoinThreads) select_join_kernel(const SelectArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ uint64_t s_keys[kList];
   __shared__ uint32_t s_at[kList];
   __shared__ float s_x[kList];
-  __shared__ double s_log[MOE_BEAM_MAX_BEAMS];  // of the row's sum exp(x - maximum)
-  __shared__ float2 s_sum[MOE_BEAM_MAX_BEAMS];
+  __shared__ Pair s_log[MOE_BEAM_MAX_BEAMS];  // of the row's sum exp(x - maximum)
   __shared__ float s_max[MOE_BEAM_MAX_BEAMS], s_score[MOE_BEAM_MAX_BEAMS];
   __shared__ float s_shift[MOE_BEAM_MAX_BEAMS], s_size[MOE_BEAM_MAX_BEAMS];  // total - logit, rounded; NaN: no candidates
-  __shared__ __align__(16) float s_best[kBests];
-  __shared__ float s_bound;
+  __shared__ __align__(16) uint32_t s_best[kBests];
+  __shared__ uint32_t s_bound;
   __shared__ int s_picked, s_count, s_more;
   await_previous_kernel();
   const int lane = lane_id(), warp = threadIdx.x / kWarp, n = a.num_out, C = a.per_row, all = a.beams * C;
@@ -236,19 +271,21 @@ __global__ void __launch_bounds__(kJoinThreads) select_join_kernel(const SelectA
   }
   if (threadIdx.x == 0) {
     s_picked = s_count = s_more = 0;
-    s_bound = -INFINITY;
+    s_bound = 0;
   }
   __syncthreads();
   for (int w = warp; w < a.beams; w += kJoinThreads / kWarp) {
     float m = -INFINITY;
+#pragma unroll 4
     for (int i = lane; i < C; i += kWarp) m = fmaxf(m, units[w * C + i].x);
 #pragma unroll
     for (int d = 1; d < kWarp; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    float sum = 0.0f, rest = 0.0f, e;  // sum + rest: the GPU has few 64-bit units
+    float sum = 0.0f, rest = 0.0f, e;
+#pragma unroll 4
     for (int i = lane; i < C; i += kWarp) {
       const float2 u = units[w * C + i];
-      if (u.x == -INFINITY && u.y == u.y) continue;
-      two_sum(sum, u.y * ex2((u.x - m) * kLog2e), sum, e);
+      const bool none = u.x == -INFINITY && u.y == u.y;
+      two_sum(sum, none ? 0.0f : u.y * ex2((u.x - m) * kLog2e), sum, e);
       rest += e;
     }
 #pragma unroll
@@ -259,13 +296,14 @@ __global__ void __launch_bounds__(kJoinThreads) select_join_kernel(const SelectA
       rest += e;
     }
     if (lane == 0) {
-      const float score = s_score[w], log_sum = logf(sum);
+      const float score = s_score[w];
       const bool ended = a.ended != nullptr && a.ended[row0 + w];
-      const float shift = (score - m) - log_sum;
+      const bool finite = isfinite(m) && sum > 0.0f && sum < INFINITY && isfinite(score);
+      const Pair log_sum = finite ? log_of(sum_of(sum, rest)) : Pair{0.0f, 0.0f};
+      s_log[w] = log_sum;
       s_max[w] = m;
-      s_sum[w] = make_float2(sum, rest);
-      s_shift[w] = !ended && isfinite(m) && isfinite(log_sum) && isfinite(score) ? shift : NAN;
-      s_size[w] = fabsf(score) + fabsf(m) + fabsf(log_sum);
+      s_shift[w] = !ended && finite ? (score - m) - log_sum.hi : NAN;
+      s_size[w] = fabsf(score) + fabsf(m) + fabsf(log_sum.hi);
       if (ended && isfinite(score)) {
         const int at = atomicAdd(&s_count, 1);
         s_x[at] = score;
@@ -274,50 +312,44 @@ __global__ void __launch_bounds__(kJoinThreads) select_join_kernel(const SelectA
     }
   }
   __syncthreads();
-  // The rows' logarithms, for the totals in 64 bits, by one warp while the others go on.
-  if (warp == kJoinThreads / kWarp - 1)
-    for (int w = lane; w < a.beams; w += kWarp) s_log[w] = log((double)s_sum[w].x + (double)s_sum[w].y);
-  // A bound that n units reach: the n-th of kBests sets' best ones, in 32 bits.
+  // A bound that n units reach: the n-th of the best ones of 128 sets of units
+  // (256 for more than 32), as whole numbers that order as they do, cut to 24
+  // bits, with the set's number below to keep them apart.
+  const int group = n <= 32 ? 8 : 4, sets = kJoinThreads / group;  // threads of a set
   float best = -INFINITY;
   for (int i = threadIdx.x; i < all; i += kJoinThreads) {
     const int w = i / C;
     const float t = units[i].x + s_shift[w];
     best = fmaxf(best, t - slack(t, s_size[w]));  // NaN leaves best as it is
   }
-  best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
-  best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
-  const int mine = threadIdx.x / 4, quarter = threadIdx.x & 3;
-  if (quarter == 0) s_best[mine] = best;
+  for (int d = 1; d < group; d <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
+  const int mine = threadIdx.x / group, member = threadIdx.x % group;
+  const uint32_t key = (best > -INFINITY ? key_half(best) & ~255u : 0u) | (uint32_t)(sets - 1 - mine);
+  if (member == 0) s_best[mine] = key;
   __syncthreads();
   int rank = 0;
-#pragma unroll 4
-  for (int i = quarter; i < kBests / 4; i += 4) {
-    const float4 o = reinterpret_cast<const float4*>(s_best)[i];
-    rank += (o.x > best || (o.x == best && 4 * i < mine)) + (o.y > best || (o.y == best && 4 * i + 1 < mine)) +
-            (o.z > best || (o.z == best && 4 * i + 2 < mine)) + (o.w > best || (o.w == best && 4 * i + 3 < mine));
+  for (int i = member; i < sets / 4; i += group) {
+    const uint4 o = reinterpret_cast<const uint4*>(s_best)[i];
+    rank += (o.x > key) + (o.y > key) + (o.z > key) + (o.w > key);
   }
-  rank += __shfl_xor_sync(0xffffffffu, rank, 1);
-  rank += __shfl_xor_sync(0xffffffffu, rank, 2);
-  if (rank == n - 1 && quarter == 0) s_bound = best;
+  for (int d = 1; d < group; d <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, d);
+  if (rank == n - 1 && member == 0) s_bound = key & ~255u;
   __syncthreads();
-  float bound = s_bound;
-  const auto passes = [&](float x, float shift, float size) {
-    const float t = x + shift;
-    return x > -INFINITY && t + slack(t, size) >= bound;  // false for a NaN shift
-  };
+  float bound = s_bound == 0 ? -INFINITY : half_value(s_bound);
+  // The least logit of a row whose total may reach the bound; -infinity never does.
+  const auto least = [&](int w) { return fmaxf((bound - s_shift[w]) - 6e-7f * (fabsf(bound) + s_size[w]), -3.4028235e38f); };
   for (int i = threadIdx.x; i < all; i += kJoinThreads) {
     const int w = i / C;
-    if (passes(units[i].x, s_shift[w], s_size[w])) picks[atomicAdd(&s_picked, 1)] = i;
+    if (s_shift[w] == s_shift[w] && units[i].x >= least(w)) picks[atomicAdd(&s_picked, 1)] = i;
   }
   __syncthreads();
   // Entries of the list from `done` on get their keys.
   int done = 0;
   const auto keys_to = [&](int count) {
     for (int i = done + threadIdx.x; i < count; i += kJoinThreads) {
-      const int w = (int)(s_at[i] / a.vocab);
-      // The maximum off first: a row of a type's lowest value has a log sum that 64 bits lose beside it.
-      s_keys[i] = s_shift[w] == s_shift[w] ? key_of((double)s_score[w] + (((double)s_x[i] - (double)s_max[w]) - s_log[w]))
-                                           : key_of((double)s_x[i]);  // a beam at its end: its score
+      const int w = (int)(s_at[i] / (uint32_t)a.vocab);
+      s_keys[i] = key_of(s_shift[w] == s_shift[w] ? total_of(s_score[w], s_x[i], s_max[w], s_log[w])
+                                                  : Pair{s_x[i], 0.0f});  // a beam at its end: its score
     }
     done = count;
     __syncthreads();
@@ -325,38 +357,51 @@ __global__ void __launch_bounds__(kJoinThreads) select_join_kernel(const SelectA
   const int picked = s_picked;
   for (int p0 = 0; p0 < picked; p0 += kJoinThreads / kWarp) {
     const int u = p0 + warp < picked ? picks[p0 + warp] : -1;
-    const int w = u < 0 ? 0 : u / C, first = (u < 0 ? 0 : u - w * C) * kUnit;
-    const float shift = s_shift[w], size = s_size[w];
-    const auto* row = reinterpret_cast<const typename Vec<Elem<ET>::kBytes>::T*>(
-        static_cast<const char*>(a.logits) + (row0 + w) * a.row_stride * Elem<ET>::kBytes);
+    using P = Part<ET, VB>;
+    int w = 0, first = 0;
     float x[kEach];
     unsigned pass = 0;
+    const auto place = [&](int j) { return first + (j / P::kElems * kWarp + lane) * P::kElems + j % P::kElems; };  // of element j
+    if (u >= 0) {
+      w = u / C;
+      first = (u - w * C) * kUnit;
+      const char* row = static_cast<const char*>(a.logits) + (row0 + w) * a.row_stride * Elem<ET>::kBytes;
+      if (first + kUnit <= a.vocab) {
+        P part;
+        part.load(row, first, lane);
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      const int t = first + j * kWarp + lane;
-      x[j] = u >= 0 && t < a.vocab ? Lanes<Elem<ET>::kBytes, ET>::get(ld_stream(row + t), 0) : -INFINITY;
+        for (int j = 0; j < kEach; ++j) x[j] = Lanes<VB, ET>::get(part.v[j / P::kElems], j % P::kElems);
+      } else {
+        using E1 = typename Vec<Elem<ET>::kBytes>::T;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+          x[j] = place(j) < a.vocab ? Lanes<Elem<ET>::kBytes, ET>::get(ld_stream(reinterpret_cast<const E1*>(row) + place(j)), 0) : -INFINITY;
+      }
+      const float limit = least(w);
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) pass |= (x[j] >= limit ? 1u : 0u) << j;
+      const int more = __reduce_add_sync(0xffffffffu, __popc(pass));
+      if (lane == 0 && more > 0) atomicAdd(&s_more, more);
     }
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) pass |= (passes(x[j], shift, size) ? 1u : 0u) << j;
     const auto add = [&](int j) {
       const int at = atomicAdd(&s_count, 1);
       s_x[at] = x[j];
-      s_at[at] = (uint32_t)(w * a.vocab + first + j * kWarp + lane);
+      s_at[at] = (uint32_t)(w * a.vocab + place(j));
     };
-    const int more = __reduce_add_sync(0xffffffffu, __popc(pass));
-    if (lane == 0 && more > 0) atomicAdd(&s_more, more);
     __syncthreads();
     const bool room = s_count + s_more <= kList;
     __syncthreads();
     if (threadIdx.x == 0) s_more = 0;  // the next round adds to it behind the barrier below
     if (room) {
+      if (__any_sync(0xffffffffu, pass != 0)) {
 #pragma unroll
-      for (int j = 0; j < kEach; ++j)
-        if (pass >> j & 1) add(j);
+        for (int j = 0; j < kEach; ++j)
+          if (pass >> j & 1) add(j);
+      }
       __syncthreads();
       continue;
     }
-    // One element of each lane of half a warp of them at a time, the list cut to the best n in between.
+    // An element of each lane of half of the warps at a time, the list cut to the best n in between.
     for (int j2 = 0; j2 < 2 * kEach; ++j2) {
       __syncthreads();
       const int have = s_count;
@@ -364,14 +409,18 @@ __global__ void __launch_bounds__(kJoinThreads) select_join_kernel(const SelectA
       if (have > kList - kJoinThreads / 2) {
         keys_to(have);
         sort_list(s_keys, s_at, have);
-        if (have >= n) bound = fmaxf(bound, __double2float_rd(value_of(s_keys[n - 1])));
+        if (have >= n) {
+          const Pair last = value_of(s_keys[n - 1]);
+          bound = fmaxf(bound, __fadd_rd(last.hi, last.lo));
+        }
         done = min(have, n);
         if (threadIdx.x == 0) s_count = done;
         __syncthreads();
       }
+      const float limit = least(w);
 #pragma unroll
       for (int j = 0; j < kEach; ++j)
-        if (j == j2 / 2 && (warp & 1) == (j2 & 1) && (pass >> j & 1) && passes(x[j], shift, size)) add(j);
+        if (j == j2 / 2 && (warp & 1) == (j2 & 1) && (pass >> j & 1) && x[j] >= limit) add(j);
     }
     __syncthreads();
   }
@@ -379,21 +428,22 @@ __global__ void __launch_bounds__(kJoinThreads) select_join_kernel(const SelectA
   keys_to(count);
   const auto put = [&](int i, int to) {
     const int64_t o = (int64_t)blockIdx.x * n + to;
-    const int64_t w = i >= 0 ? s_at[i] / a.vocab : 0;
-    a.out_scores[o] = i >= 0 ? (float)value_of(s_keys[i]) : -INFINITY;
+    const uint32_t V = (uint32_t)a.vocab, w = i >= 0 ? s_at[i] / V : 0;
+    a.out_scores[o] = i >= 0 ? value_of(s_keys[i]).hi : -INFINITY;
     a.out_parents[o] = i >= 0 ? (int32_t)(row0 + w) : -1;
-    a.out_tokens[o] = i >= 0 ? (int32_t)(s_at[i] - w * a.vocab) : -1;
+    a.out_tokens[o] = i >= 0 ? (int32_t)(s_at[i] - w * V) : -1;
   };
   if (count <= kBests) {  // an entry's place is the number of better ones; four threads count for one
-    int place = 0;
-    if (mine < count) {
-      const uint64_t key = s_keys[mine];
-      const uint32_t at = s_at[mine];
-      for (int i = quarter; i < count; i += 4) place += better(s_keys[i], s_at[i], key, at);
+    const int entry = threadIdx.x / 4;
+    if (entry - (lane >> 2) < count) {  // the warp has one
+      int place = 0;
+      const uint64_t own = s_keys[entry];
+      const uint32_t at = s_at[entry];
+      for (int i = threadIdx.x & 3; i < count; i += 4) place += better(s_keys[i], s_at[i], own, at);
+      place += __shfl_xor_sync(0xffffffffu, place, 1);
+      place += __shfl_xor_sync(0xffffffffu, place, 2);
+      if ((threadIdx.x & 3) == 0 && entry < count && place < n) put(entry, place);
     }
-    place += __shfl_xor_sync(0xffffffffu, place, 1);
-    place += __shfl_xor_sync(0xffffffffu, place, 2);
-    if (quarter == 0 && mine < count && place < n) put(mine, place);
   } else {
     sort_list(s_keys, s_at, count);
     if (threadIdx.x < n) put(threadIdx.x, threadIdx.x);
@@ -401,25 +451,28 @@ __global__ void __launch_bounds__(kJoinThreads) select_join_kernel(const SelectA
   if (threadIdx.x < n && (int)threadIdx.x >= count) put(-1, threadIdx.x);
 }
 
-template <typename ET> int run_select(const SelectArgs& a, cudaStream_t s) {
+template <typename ET, int VB> int launch_select(const SelectArgs& a, cudaStream_t s) {
   const int64_t units = a.requests * a.beams * a.per_row;
-  const void* ptrs[1] = {a.logits};
-  const int64_t stride = a.requests * a.beams > 1 ? a.row_stride * Elem<ET>::kBytes : 0;
-  const int vb = pick_vec_bytes(stride, ptrs, 1, Elem<ET>::kBytes);
-  const auto go = [&](auto k) {
-    launch(k, persistent_grid(k, kThreads, 0, (units + kThreads / kWarp - 1) / (kThreads / kWarp)), kThreads, 0, s, a);
-  };
-  if (vb == 16) go(select_units_kernel<ET, 16>);
-  else if (vb == 8) go(select_units_kernel<ET, 8>);
-  else if (vb == 4) go(select_units_kernel<ET, 4>);
-  else if constexpr (Elem<ET>::kBytes == 2) go(select_units_kernel<ET, 2>);
+  auto k = select_units_kernel<ET, VB>;
+  launch(k, persistent_grid(k, kThreads, 0, (units + kThreads / kWarp - 1) / (kThreads / kWarp)), kThreads, 0, s, a);
   const int rc = check_launch();
   if (rc != MOE_OK) return rc;
   static std::atomic<bool> raised[kSmemDevices];
-  if (!allow_smem(select_join_kernel<ET>, raised)) return MOE_ERR_CUDA;
+  auto join = select_join_kernel<ET, VB>;
+  if (!allow_smem(join, raised)) return MOE_ERR_CUDA;
   const size_t all = (size_t)a.beams * a.per_row;
-  launch(select_join_kernel<ET>, dim3((unsigned)a.requests), dim3(kJoinThreads), (all + 1) / 2 * 8 + (all <= kCached ? 8 * all : 0), s, a);
+  launch(join, dim3((unsigned)a.requests), dim3(kJoinThreads), (all + 1) / 2 * 8 + (all <= kCached ? 8 * all : 0), s, a);
   return check_launch();
+}
+template <typename ET> int run_select(const SelectArgs& a, cudaStream_t s) {
+  const void* ptrs[1] = {a.logits};
+  const int64_t stride = a.requests * a.beams > 1 ? a.row_stride * Elem<ET>::kBytes : 0;
+  const int vb = pick_vec_bytes(stride, ptrs, 1, Elem<ET>::kBytes);
+  if (vb == 16) return launch_select<ET, 16>(a, s);
+  if (vb == 8) return launch_select<ET, 8>(a, s);
+  if (Elem<ET>::kBytes == 4 || vb == 4) return launch_select<ET, 4>(a, s);
+  if constexpr (Elem<ET>::kBytes == 2) return launch_select<ET, 2>(a, s);
+  return MOE_ERR_UNSUPPORTED;
 }
 
 bool select_ok(int64_t num_requests, int32_t num_beams, int64_t vocab) { return num_requests >= 0 && num_beams >= 1 && vocab >= 1; }
