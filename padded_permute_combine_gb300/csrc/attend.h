@@ -9,6 +9,7 @@
 #include "block_common.h"
 #include "bulk.cuh"
 #include "common.cuh"
+#include "divisor.h"
 #include "moe_decode.h"
 
 namespace moe {
@@ -18,19 +19,6 @@ constexpr int kSmWarps = 8;    // warps of an SM: a CTA of eight, one an SM
 constexpr int kMinTiles = 2;   // of a range, where there are fewer tiles than warps
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-
-// Quotients by a divisor known at launch, for numerators below 2^31: with
-// s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1, n / d = (mulhi(n, m) + n) >> s
-// (Granlund and Montgomery, Division by Invariant Integers, 1994).
-struct Divisor {
-  uint32_t d, m, s;
-  Divisor() : Divisor(1) {}
-  explicit Divisor(uint32_t by) : d(by), m(0), s(0) {
-    while ((1ull << s) < by) ++s;
-    m = (uint32_t)(((1ull << 32) * ((1ull << s) - by)) / by + 1);
-  }
-  __device__ __forceinline__ uint32_t of(uint32_t n) const { return (__umulhi(n, m) + n) >> s; }
-};
 
 struct AttendArgs {
   char* k;  // the cache; strides in bytes

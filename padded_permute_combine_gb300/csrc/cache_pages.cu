@@ -3,18 +3,19 @@
 // copies that both ask for.
 //
 // A pool keeps no counts: a page is in use when a row of the table names it.
-// Both table kernels run as one cluster of eight CTAs. Its shared memory holds a
-// bit for every page of the pool, in eight slices; all CTAs set the bits of the
-// rows' pages in it, and after the cluster's barrier each counts its own slice,
-// so the i-th free page is known without a second launch, and without a word of
-// workspace to clear. The barriers are the hardware's, of one cluster: its CTAs
-// run together or not at all.
+// Both table kernels run as one CTA or, for large tables and pools, as one
+// cluster of eight. Their shared memory holds a bit for every page of the pool
+// (a slice of it in each CTA); the rows' pages set theirs, and after a barrier
+// each CTA counts its own slice, so the i-th free page is known without a second
+// launch, and without a word of workspace to clear. The barriers are the
+// hardware's, of one cluster: its CTAs run together or not at all.
 #include <cooperative_groups.h>
 
 #include <atomic>
 
 #include "block_common.h"
 #include "common.cuh"
+#include "divisor.h"
 #include "moe_decode.h"
 
 namespace moe {
@@ -98,33 +99,49 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const WriteArgs a) {
 
 // ------------------------------------------------------------------ tables
 
-constexpr int kCtas = 8, kThreads = 1024, kWarps = kThreads / kWarp;
+constexpr int kThreads = 1024, kWarps = kThreads / kWarp;
+
+// The CTAs of a table kernel.
+template <int CTAS> struct Group {
+  __device__ __forceinline__ static int rank() { return (int)cg::this_cluster().block_rank(); }
+  __device__ __forceinline__ static void sync() { cg::this_cluster().sync(); }
+  template <typename T> __device__ __forceinline__ static T* map(T* p, int rank) { return cg::this_cluster().map_shared_rank(p, rank); }
+};
+template <> struct Group<1> {
+  __device__ __forceinline__ static int rank() { return 0; }
+  __device__ __forceinline__ static void sync() { __syncthreads(); }
+  template <typename T> __device__ __forceinline__ static T* map(T* p, int) { return p; }
+};
+constexpr int kBatch = 4;  // entries of the table that a thread takes at a time
 
 struct TableArgs {
   const int32_t* table;
-  int64_t table_stride, width;
+  int64_t table_stride;
   const int32_t* lengths;
   const int32_t* parents;  // nullptr in compaction: every row is its own
   int32_t* new_table;
-  int64_t new_width;
   int32_t* new_lengths;
   int32_t* src;
   int32_t* dst;
   int32_t* count;
   int32_t* status;
-  int64_t seqs, rows, num_pages, grow, page;
+  Divisor page, columns;  // columns: of the new table
+  int32_t width, new_width, seqs, rows, num_pages;
+  int64_t grow;
   int32_t words_shift;  // log2 of the words of a slice
+  int32_t whole;        // whether every CTA has bits of the whole pool, CTAS slices
+  int32_t whole_at;     // in words of the shared memory
   int32_t hash_bits;
 };
 
 // What a row goes on from.
 struct Parent {
-  int row;      // -1: none
-  int length;   // tokens
-  int held;     // pages
+  int row;     // -1: none
+  int length;  // tokens
+  int held;    // pages
 };
-__device__ __forceinline__ Parent parent_of(const TableArgs& a, int64_t r, bool flag) {
-  Parent p = {(int)r, 0, 0};
+__device__ __forceinline__ Parent parent_of(const TableArgs& a, int r, bool flag) {
+  Parent p = {r, 0, 0};
   if (a.parents != nullptr) {
     p.row = a.parents[r];
     if (p.row < -1 || p.row >= a.seqs) {
@@ -133,13 +150,14 @@ __device__ __forceinline__ Parent parent_of(const TableArgs& a, int64_t r, bool 
     }
   }
   if (p.row < 0) return p;
-  const int64_t n = a.lengths[p.row], most = a.width * a.page;
+  const int n = a.lengths[p.row], most = a.width * (int)a.page.d;
   if (flag && (n < 0 || n > most)) flag_status(a.status, MOE_STATUS_BAD_INDEX);
-  p.length = (int)(n < 0 ? 0 : (n > most ? most : n));
-  p.held = (int)((p.length + a.page - 1) / a.page);
+  p.length = n < 0 ? 0 : (n > most ? most : n);
+  p.held = (int)a.page.of(p.length);
+  p.held += p.held * (int)a.page.d < p.length;
   return p;
 }
-__device__ __forceinline__ int page_of(const TableArgs& a, int row, int64_t j) {
+__device__ __forceinline__ int page_of(const TableArgs& a, int row, int j) {
   const int id = a.table[row * a.table_stride + j];
   return id >= 0 && id < a.num_pages ? id : -1;
 }
@@ -169,26 +187,56 @@ __device__ __forceinline__ int cta_prefix(int v, int* s_warp, int& before) {
 }
 
 // Copies the rows' pages into the new table, with -1 behind them, and sets
-// their bits. Rows go round over the cluster's CTAs, several warps to a row.
-__device__ __forceinline__ void mark_rows(cg::cluster_group& cluster, const TableArgs& a, unsigned* bits) {
-  const int rank = cluster.block_rank();
-  const int64_t total = a.rows * a.new_width;
-  // One entry a thread, in the table's order, so that few and many rows go alike.
-  for (int64_t i = (int64_t)rank * kThreads + threadIdx.x; i < total; i += (int64_t)kCtas * kThreads) {
-    const int64_t r = i / a.new_width, j = i - r * a.new_width;
-    const Parent p = parent_of(a, r, false);
-    int id = -1;
-    if (j < p.held) {
-      id = page_of(a, p.row, j);
-      if (id < 0) {
-        flag_status(a.status, MOE_STATUS_BAD_INDEX);
-      } else {
-        const int w = id >> 5;
-        atomicOr(cluster.map_shared_rank(bits, w >> a.words_shift) + (w & ((1 << a.words_shift) - 1)), 1u << (id & 31));
-      }
+// their bits. The entries go round over all threads in the table's order, some
+// at a time so that their loads are on their way together. s_row, s_held:
+// every row's parent and pages.
+template <int CTAS> __device__ __forceinline__ void mark_rows(const TableArgs& a, unsigned* bits, unsigned* whole, const int* s_row, const int* s_held) {
+  using G = Group<CTAS>;
+  const int total = a.rows * a.new_width;  // below 2^31 by more than the steps: checked at the call
+  for (int i0 = G::rank() * kThreads + (int)threadIdx.x; i0 < total; i0 += kBatch * CTAS * kThreads) {
+    int id[kBatch];
+    bool in[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int i = i0 + e * CTAS * kThreads;
+      if (i >= total) break;
+      const int r = (int)a.columns.of(i), j = i - r * a.new_width;
+      in[e] = j < s_held[r];
+      id[e] = in[e] ? a.table[s_row[r] * a.table_stride + j] : -1;
     }
-    a.new_table[i] = id;
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int i = i0 + e * CTAS * kThreads;
+      if (i >= total) break;
+      if (id[e] >= 0 && id[e] < a.num_pages) {
+        const int w = id[e] >> 5;
+        unsigned* at = CTAS == 1 || a.whole ? whole + w : G::map(bits, w >> a.words_shift) + (w & ((1 << a.words_shift) - 1));
+        atomicOr(at, 1u << (id[e] & 31));
+      } else {
+        if (in[e]) flag_status(a.status, MOE_STATUS_BAD_INDEX);
+        id[e] = -1;
+      }
+      a.new_table[i] = id[e];
+    }
   }
+}
+template <int CTAS> __device__ __forceinline__ void clear_marks(const TableArgs& a, unsigned* bits, unsigned* whole) {
+  const int words = 1 << a.words_shift;
+  for (int w = threadIdx.x; w < words; w += kThreads) bits[w] = 0;
+  if (CTAS > 1 && a.whole)
+    for (int w = threadIdx.x; w < words * CTAS; w += kThreads) whole[w] = 0;
+}
+// Behind a barrier: this CTA's slice of the bits.
+template <int CTAS> __device__ __forceinline__ void join_marks(const TableArgs& a, unsigned* bits, unsigned* whole) {
+  if (CTAS == 1 || !a.whole) return;
+  const int words = 1 << a.words_shift, rank = Group<CTAS>::rank();
+  for (int w = threadIdx.x; w < words; w += kThreads) {
+    unsigned v = 0;
+#pragma unroll
+    for (int k = 0; k < CTAS; ++k) v |= Group<CTAS>::map(whole, k)[(rank << a.words_shift) + w];
+    bits[w] = v;
+  }
+  __syncthreads();
 }
 // The bits of word w of this CTA's slice that are pages of the pool.
 __device__ __forceinline__ unsigned pool_mask(const TableArgs& a, int rank, int w) {
@@ -196,53 +244,63 @@ __device__ __forceinline__ unsigned pool_mask(const TableArgs& a, int rank, int 
   return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1;
 }
 
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) cache_fork_kernel(const TableArgs a) {
+template <int CTAS> __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1) cache_fork_kernel(const TableArgs a) {
+  using G = Group<CTAS>;
   extern __shared__ unsigned smem[];
-  __shared__ int s_warp[kWarps], s_totals[kCtas];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = cluster.block_rank(), words = 1 << a.words_shift, R = (int)a.rows;
+  __shared__ int s_warp[kWarps], s_totals[CTAS];
+  const int rank = G::rank(), words = 1 << a.words_shift, R = a.rows;
   unsigned* bits = smem;
-  int* start = reinterpret_cast<int*>(smem + words);  // [R]: requests of the rows in front
-  int* last = start + R;                              // [R]: page that is copied, or -1
-  int* keys = last + R;                               // hash of the last pages that are not full
-  int* vals = keys + (1 << a.hash_bits);              // the first row that holds one
-  await_previous_kernel();
-  for (int w = threadIdx.x; w < words; w += kThreads) bits[w] = 0;
+  int* row = reinterpret_cast<int*>(smem + words);  // [R]: parents
+  int* held = row + R;                              // [R]: pages
+  int* start = held + R;                            // [R]: requests of the rows in front
+  int* last = start + R;                            // [R]: page that is copied, or -1
+  int* keys = last + R;                             // hash of the last pages that are not full; then the words' free pages
+  int* vals = keys + (1 << a.hash_bits);            // the first row that holds one
+  unsigned* whole = CTAS == 1 ? bits : smem + a.whole_at;
+  clear_marks<CTAS>(a, bits, whole);
   for (int i = threadIdx.x; i < 1 << a.hash_bits; i += kThreads) {
     keys[i] = -1;
     vals[i] = INT32_MAX;
   }
-  cluster.sync();
-  mark_rows(cluster, a, bits);
-  // Every CTA knows all rows' requests.
-  const unsigned mask = (1u << a.hash_bits) - 1;
+  await_previous_kernel();
+  // Every CTA knows all rows.
   for (int r = threadIdx.x; r < R; r += kThreads) {
     const Parent p = parent_of(a, r, rank == 0);
-    int id = -1;
-    if (a.grow > 0 && p.row >= 0 && p.length % a.page != 0) {
-      id = page_of(a, p.row, p.held - 1);
-      if (id >= 0) {
-        unsigned at = (unsigned)id * 2654435761u >> (32 - a.hash_bits);
-        for (unsigned i = 0; i <= mask; ++i, at = (at + 1) & mask) {  // twice as many places as rows
-          const int old = atomicCAS(&keys[at], -1, id);
-          if (old == -1 || old == id) {
-            atomicMin(&vals[at], r);
-            break;
-          }
-        }
+    row[r] = p.row;
+    held[r] = p.held;
+    start[r] = p.length;  // for now
+    last[r] = a.grow > 0 && p.row >= 0 && p.held * (int)a.page.d != p.length ? page_of(a, p.row, p.held - 1) : -1;
+    if (rank == 0) {
+      a.new_lengths[r] = p.length;
+      a.src[r] = a.dst[r] = -1;
+    }
+  }
+  G::sync();
+  mark_rows<CTAS>(a, bits, whole, row, held);
+  const unsigned mask = (1u << a.hash_bits) - 1;
+  for (int r = threadIdx.x; r < R; r += kThreads) {
+    const int id = last[r];
+    if (id < 0) continue;
+    unsigned at = (unsigned)id * 2654435761u >> (32 - a.hash_bits);
+    for (unsigned i = 0; i <= mask; ++i, at = (at + 1) & mask) {  // twice as many places as rows
+      const int old = atomicCAS(&keys[at], -1, id);
+      if (old == -1 || old == id) {
+        atomicMin(&vals[at], r);
+        break;
       }
     }
-    last[r] = id;
   }
   __syncthreads();
   const int chunk = (R + kThreads - 1) / kThreads;
   int mine = 0;
   for (int r = threadIdx.x * chunk; r < R && r < (int)(threadIdx.x + 1) * chunk; ++r) {
-    const Parent p = parent_of(a, r, false);
     int need = 0;
-    if (p.row >= 0) {
-      const int64_t want = (p.length + a.grow + a.page - 1) / a.page, all = want < a.new_width ? want : a.new_width;
-      need = all > p.held ? (int)all - p.held : 0;
+    if (row[r] >= 0) {
+      const int64_t tokens = start[r] + a.grow;  // at most 2^32
+      const int64_t want = tokens < INT32_MAX ? a.page.of((uint32_t)tokens) + (a.page.of((uint32_t)tokens) * a.page.d < tokens)
+                                              : (tokens + a.page.d - 1) / a.page.d;
+      const int all = (int)(want < a.new_width ? want : a.new_width);
+      need = all > held[r] ? all - held[r] : 0;
       if (rank == 0 && want > a.new_width) flag_status(a.status, MOE_STATUS_NO_PAGES);
     }
     if (last[r] >= 0) {
@@ -256,83 +314,83 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) cac
   int before;
   const int requests = cta_prefix(mine, s_warp, before);
   for (int r = threadIdx.x * chunk; r < R && r < (int)(threadIdx.x + 1) * chunk; ++r) start[r] += before;
-  if (rank == 0) {
-    for (int r = threadIdx.x; r < R; r += kThreads) {
-      a.new_lengths[r] = parent_of(a, r, false).length;
-      a.src[r] = a.dst[r] = -1;
-    }
-  }
-  cluster.sync();  // all bits are set, and what the requests overwrite is written
-  // Free pages in front of each word of the slice, and of the slice.
+  G::sync();  // all bits are set, and what the requests overwrite is written
+  join_marks<CTAS>(a, bits, whole);
+  // Free pages in front of each word of the slice.
+  int* front = keys;  // [words]: the hash is done with
   const int per = (words + kThreads - 1) / kThreads;
   int free_here = 0;
   for (int w = threadIdx.x * per; w < words && w < (int)(threadIdx.x + 1) * per; ++w)
     free_here += __popc(~bits[w] & pool_mask(a, rank, w));
   const int slice = cta_prefix(free_here, s_warp, before);
-  if (threadIdx.x < kCtas) cluster.map_shared_rank(s_totals, threadIdx.x)[rank] = slice;
-  cluster.sync();
+  if (threadIdx.x < CTAS) G::map(s_totals, threadIdx.x)[rank] = slice;
+  G::sync();
   int all_free = 0;
-  for (int i = 0; i < kCtas; ++i) {
+  for (int i = 0; i < CTAS; ++i) {
     if (i < rank) before += s_totals[i];
     all_free += s_totals[i];
   }
   if (rank == 0 && threadIdx.x == 0 && requests > all_free) flag_status(a.status, MOE_STATUS_NO_PAGES);
-  // A warp hands out its words' pages, a word at a time, each lane one of its bits.
+  for (int w = threadIdx.x * per; w < words && w < (int)(threadIdx.x + 1) * per; ++w) {
+    front[w] = before;
+    before += __popc(~bits[w] & pool_mask(a, rank, w));
+  }
+  __syncthreads();
+  // A warp hands out a word's pages, each lane one of its bits.
   const int lane = lane_id();
-  for (int i = 0; i < per; ++i) {
-    const int w = threadIdx.x * per + i;
-    const unsigned own = w < words ? ~bits[w] & pool_mask(a, rank, w) : 0u;
-    if (!__any_sync(0xffffffffu, own != 0 && before < requests)) break;  // a thread's later words begin no lower
-    for (int k = 0; k < kWarp; ++k) {
-      const unsigned free = __shfl_sync(0xffffffffu, own, k);
-      const int base = __shfl_sync(0xffffffffu, before, k), word = __shfl_sync(0xffffffffu, w, k);
-      const int q = base + __popc(free & lanemask_lt());
-      if (base >= requests || !(free >> lane & 1) || q >= requests) continue;
-      int lo = 0, hi = R;  // the last row whose requests begin at or before q
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (start[mid] <= q) lo = mid; else hi = mid;
-      }
-      const Parent p = parent_of(a, lo, false);
-      const int copied = last[lo] >= 0, id = (((rank << a.words_shift) + word) << 5) + lane;
-      a.new_table[lo * a.new_width + p.held - copied + (q - start[lo])] = id;
-      if (copied && q == start[lo]) {
-        a.src[lo] = last[lo];
-        a.dst[lo] = id;
-      }
+  for (int w = threadIdx.x / kWarp; w < words; w += kWarps) {
+    if (front[w] >= requests) break;  // and neither are the later ones asked for
+    const unsigned free = ~bits[w] & pool_mask(a, rank, w);
+    const int q = front[w] + __popc(free & lanemask_lt());
+    if (!(free >> lane & 1) || q >= requests) continue;
+    int lo = 0, hi = R;  // the last row whose requests begin at or before q
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (start[mid] <= q) lo = mid; else hi = mid;
     }
-    before += __popc(own);
+    const int copied = last[lo] >= 0, id = (((rank << a.words_shift) + w) << 5) + lane;
+    a.new_table[(int64_t)lo * a.new_width + held[lo] - copied + (q - start[lo])] = id;
+    if (copied && q == start[lo]) {
+      a.src[lo] = last[lo];
+      a.dst[lo] = id;
+    }
   }
   // A copied page that none was free for: the row must not write the one that it shares.
   if (rank == 0)
     for (int r = threadIdx.x; r < R; r += kThreads)
-      if (last[r] >= 0 && start[r] >= all_free) a.new_table[r * a.new_width + parent_of(a, r, false).held - 1] = -1;
-  cluster.sync();  // no CTA leaves while others use its shared memory
+      if (last[r] >= 0 && start[r] >= all_free) a.new_table[(int64_t)r * a.new_width + held[r] - 1] = -1;
+  // Nothing of another CTA is used behind the last barrier: none has to stay.
 }
 
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) cache_compact_kernel(const TableArgs a) {
+template <int CTAS> __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1) cache_compact_kernel(const TableArgs a) {
+  using G = Group<CTAS>;
   extern __shared__ unsigned smem[];
-  __shared__ int s_warp[kWarps], s_totals[kCtas];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = cluster.block_rank(), words = 1 << a.words_shift;
+  __shared__ int s_warp[kWarps], s_totals[CTAS];
+  const int rank = G::rank(), words = 1 << a.words_shift;
   unsigned* bits = smem;
   int* front = reinterpret_cast<int*>(smem + words);  // pages in use in front of each word
+  int* row = front + words;                           // [rows]
+  int* held = row + a.rows;                           // [rows]: pages
+  unsigned* whole = CTAS == 1 ? bits : smem + a.whole_at;
+  clear_marks<CTAS>(a, bits, whole);
   await_previous_kernel();
-  for (int w = threadIdx.x; w < words; w += kThreads) bits[w] = 0;
-  cluster.sync();
-  if (rank == 0)
-    for (int r = threadIdx.x; r < a.rows; r += kThreads) (void)parent_of(a, r, true);
-  mark_rows(cluster, a, bits);
-  cluster.sync();
+  for (int r = threadIdx.x; r < a.rows; r += kThreads) {
+    row[r] = r;
+    held[r] = parent_of(a, r, rank == 0).held;
+  }
+  G::sync();
+  mark_rows<CTAS>(a, bits, whole, row, held);
+  G::sync();
+  join_marks<CTAS>(a, bits, whole);
   const int per = (words + kThreads - 1) / kThreads;
   int used_here = 0;
   for (int w = threadIdx.x * per; w < words && w < (int)(threadIdx.x + 1) * per; ++w) used_here += __popc(bits[w]);
   int before;
   const int slice = cta_prefix(used_here, s_warp, before);
-  if (threadIdx.x < kCtas) cluster.map_shared_rank(s_totals, threadIdx.x)[rank] = slice;
-  cluster.sync();
+  if (threadIdx.x < CTAS) G::map(s_totals, threadIdx.x)[rank] = slice;
+  G::sync();
   int live = 0;
-  for (int i = 0; i < kCtas; ++i) {
+  for (int i = 0; i < CTAS; ++i) {
     if (i < rank) before += s_totals[i];
     live += s_totals[i];
   }
@@ -340,50 +398,62 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) cac
     front[w] = x;
     x += __popc(bits[w]);
   }
-  cluster.sync();
+  G::sync();
   // Pages in use in front of page number `id`.
   const auto used_before = [&](int id) {
     const int w = id >> 5, at = w & (words - 1), in = w >> a.words_shift;
-    if (in >= kCtas) return live;
-    return cluster.map_shared_rank(front, in)[at] + __popc(cluster.map_shared_rank(bits, in)[at] & ((1u << (id & 31)) - 1));
+    if (in >= CTAS) return live;
+    return G::map(front, in)[at] + __popc(G::map(bits, in)[at] & ((1u << (id & 31)) - 1));
   };
   const int kept = used_before(live), moves = live - kept;  // in use below `live`; holes there = live - kept
-  for (int w = threadIdx.x * per; w < words && w < (int)(threadIdx.x + 1) * per; ++w) {
-    const int first = ((rank << a.words_shift) + w) << 5;
-    unsigned used = bits[w];
-    const unsigned low = first + 32 <= live ? 0xffffffffu : first >= live ? 0u : (1u << (live - first)) - 1;  // pages below `live`
-    unsigned holes = ~used & low, movers = used & ~low;
-    for (int x = first - front[w]; holes != 0; holes &= holes - 1) {  // holes in front of the word's first
-      const int bit = __ffs(holes) - 1;
-      a.dst[x + __popc(~used & ((1u << bit) - 1))] = first + bit;
-    }
-    for (; movers != 0; movers &= movers - 1) {
-      const int bit = __ffs(movers) - 1;
-      a.src[front[w] + __popc(used & ((1u << bit) - 1)) - kept] = first + bit;
+  // A warp writes a word's holes and movers, each lane one of its bits.
+  const int lane = lane_id();
+  for (int w = threadIdx.x / kWarp; w < words; w += kWarps) {
+    const unsigned used = bits[w];
+    const int id = (((rank << a.words_shift) + w) << 5) + lane;
+    const int here = front[w] + __popc(used & lanemask_lt());  // in use in front of the lane's page
+    if (used >> lane & 1) {
+      if (id >= live) a.src[here - kept] = id;
+    } else if (id < live) {
+      a.dst[id - here] = id;
     }
   }
-  for (int64_t i = moves + (int64_t)rank * kThreads + threadIdx.x; i < a.num_pages / 2; i += kCtas * kThreads)
+  for (int i = moves + rank * kThreads + (int)threadIdx.x; i < a.num_pages / 2; i += CTAS * kThreads)
     a.src[i] = a.dst[i] = -1;
   if (rank == 0 && threadIdx.x == 0) *a.count = moves;
-  cluster.sync();
+  G::sync();
   // Entries at or above `live` get their new numbers: each thread those that it wrote itself.
-  for (int64_t i = (int64_t)rank * kThreads + threadIdx.x; i < a.rows * a.new_width; i += (int64_t)kCtas * kThreads) {
-    const int id = a.new_table[i];
-    if (id >= live) a.new_table[i] = __ldcg(a.dst + (used_before(id) - kept));
+  const int total = a.rows * a.new_width;
+  for (int i0 = rank * kThreads + (int)threadIdx.x; i0 < total; i0 += kBatch * CTAS * kThreads) {
+    int id[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int i = i0 + e * CTAS * kThreads;
+      id[e] = i < total ? a.new_table[i] : -1;
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e)
+      if (id[e] >= live) id[e] = __ldcg(a.dst + (used_before(id[e]) - kept)); else id[e] = -1;
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e)
+      if (id[e] >= 0) a.new_table[i0 + e * CTAS * kThreads] = id[e];
   }
-  cluster.sync();
+  if (CTAS > 1) G::sync();  // no CTA leaves while others use its shared memory
 }
 
-int words_shift_of(int64_t num_pages) {
+constexpr int kCtas = 8;
+bool one_cta(int64_t entries, int64_t num_pages) { return entries <= 4096 && num_pages <= 32768; }
+
+int words_shift_of(int64_t num_pages, int ctas) {
   const int64_t words = (num_pages + 31) / 32;
   int s = 0;
-  while (((int64_t)kCtas << s) < words) ++s;
+  while (((int64_t)ctas << s) < words) ++s;
   return s;
 }
 
-int launch_table(void (*k)(TableArgs), std::atomic<bool>* raised, const TableArgs& a, size_t smem, cudaStream_t s) {
+int launch_table(void (*k)(TableArgs), std::atomic<bool>* raised, const TableArgs& a, int ctas, size_t smem, cudaStream_t s) {
   if (!allow_smem(k, raised)) return MOE_ERR_CUDA;
-  launch(k, dim3(kCtas), dim3(kThreads), smem, s, a);
+  launch(k, dim3(ctas), dim3(kThreads), smem, s, a);
   return check_launch();
 }
 
@@ -393,6 +463,23 @@ bool table_ok(int64_t table_stride, int64_t table_width, int64_t num_seqs, int32
 bool table_supported(int64_t table_width, int64_t num_seqs, int32_t page_size, int64_t num_pages) {
   return num_seqs <= MOE_CACHE_MAX_ROWS && num_pages <= MOE_CACHE_MAX_PAGES && table_width <= INT32_MAX &&
          table_width * page_size <= INT32_MAX;
+}
+int set_table(TableArgs& a, const int32_t* table, int64_t stride, int64_t width, const int32_t* lengths, int64_t seqs, int64_t rows,
+              int64_t new_width, int32_t page_size, int64_t num_pages) {
+  const int ctas = one_cta(rows * new_width, num_pages) ? 1 : kCtas;
+  a.table = table;
+  a.table_stride = stride;
+  a.width = (int32_t)width;
+  a.lengths = lengths;
+  a.seqs = (int32_t)seqs;
+  a.rows = (int32_t)rows;
+  a.new_width = (int32_t)new_width;
+  a.page = Divisor((uint32_t)page_size);
+  a.columns = Divisor((uint32_t)(new_width < 1 ? 1 : new_width));
+  a.num_pages = (int32_t)num_pages;
+  a.words_shift = words_shift_of(num_pages, ctas);
+  a.whole = ctas > 1 && (ctas << a.words_shift) <= 8192;
+  return ctas;
 }
 
 // ------------------------------------------------------------------ copies
@@ -520,7 +607,7 @@ extern "C" int moe_cache_fork(const int32_t* page_table, int64_t table_stride, i
   if (!table_ok(table_stride, table_width, num_seqs, page_size, num_pages) || num_rows < 0 || grow < 0 || new_width < 0)
     return MOE_ERR_INVALID_ARG;
   if (!table_supported(table_width, num_seqs, page_size, num_pages) || num_rows > MOE_CACHE_MAX_ROWS || new_width > INT32_MAX ||
-      grow > INT32_MAX)
+      num_rows * new_width > INT32_MAX - kBatch * kCtas * kThreads || grow > INT32_MAX)
     return MOE_ERR_UNSUPPORTED;
   if (new_width < table_width) return MOE_ERR_INVALID_ARG;
   if (num_rows == 0) return MOE_OK;
@@ -531,28 +618,21 @@ extern "C" int moe_cache_fork(const int32_t* page_table, int64_t table_stride, i
                         (const void*)new_lengths, (const void*)src, (const void*)dst, (const void*)d_status})
     if (!aligned(p, 4)) return MOE_ERR_UNSUPPORTED;
   TableArgs a = {};
-  a.table = page_table;
-  a.table_stride = table_stride;
-  a.width = table_width;
-  a.lengths = lengths;
+  const int ctas = set_table(a, page_table, table_stride, table_width, lengths, num_seqs, num_rows, new_width, page_size, num_pages);
   a.parents = parents;
   a.new_table = new_table;
-  a.new_width = new_width;
   a.new_lengths = new_lengths;
   a.src = src;
   a.dst = dst;
   a.status = d_status;
-  a.seqs = num_seqs;
-  a.rows = num_rows;
-  a.num_pages = num_pages;
   a.grow = grow;
-  a.page = page_size;
-  a.words_shift = words_shift_of(num_pages);
   a.hash_bits = 1;
   while ((1 << a.hash_bits) < 2 * num_rows) ++a.hash_bits;
-  const size_t smem = 4 * ((size_t)(1 << a.words_shift) + 2 * num_rows + 2 * ((size_t)1 << a.hash_bits));
-  static std::atomic<bool> raised[kSmemDevices];
-  return launch_table(cache_fork_kernel, raised, a, smem, reinterpret_cast<cudaStream_t>(stream));
+  const size_t words = (size_t)1 << a.words_shift, hash = (size_t)2 << a.hash_bits;
+  a.whole_at = (int32_t)(words + 4 * num_rows + (hash > words ? hash : words));
+  const size_t smem = 4 * ((size_t)a.whole_at + (a.whole ? words * kCtas : 0));
+  static std::atomic<bool> raised[2][kSmemDevices];
+  return launch_table(ctas == 1 ? cache_fork_kernel<1> : cache_fork_kernel<kCtas>, raised[ctas > 1], a, ctas, smem, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int moe_cache_compact(const int32_t* page_table, int64_t table_stride, int64_t table_width,
@@ -560,7 +640,8 @@ extern "C" int moe_cache_compact(const int32_t* page_table, int64_t table_stride
                                  int32_t* new_table, int32_t* src, int32_t* dst, int32_t* count, int32_t* d_status,
                                  moe_stream_t stream) {
   if (!table_ok(table_stride, table_width, num_seqs, page_size, num_pages)) return MOE_ERR_INVALID_ARG;
-  if (!table_supported(table_width, num_seqs, page_size, num_pages)) return MOE_ERR_UNSUPPORTED;
+  if (!table_supported(table_width, num_seqs, page_size, num_pages) || num_seqs * table_width > INT32_MAX - kBatch * kCtas * kThreads)
+    return MOE_ERR_UNSUPPORTED;
   if ((num_seqs > 0 && (lengths == nullptr || (table_width > 0 && (page_table == nullptr || new_table == nullptr)))) ||
       (num_pages > 1 && (src == nullptr || dst == nullptr)) || count == nullptr)
     return MOE_ERR_INVALID_ARG;
@@ -568,22 +649,17 @@ extern "C" int moe_cache_compact(const int32_t* page_table, int64_t table_stride
                         (const void*)count, (const void*)d_status})
     if (!aligned(p, 4)) return MOE_ERR_UNSUPPORTED;
   TableArgs a = {};
-  a.table = page_table;
-  a.table_stride = table_stride;
-  a.width = table_width;
-  a.lengths = lengths;
+  const int ctas = set_table(a, page_table, table_stride, table_width, lengths, num_seqs, num_seqs, table_width, page_size, num_pages);
   a.new_table = new_table;
-  a.new_width = table_width;
   a.src = src;
   a.dst = dst;
   a.count = count;
   a.status = d_status;
-  a.seqs = a.rows = num_seqs;
-  a.num_pages = num_pages;
-  a.page = page_size;
-  a.words_shift = words_shift_of(num_pages);
-  static std::atomic<bool> raised[kSmemDevices];
-  return launch_table(cache_compact_kernel, raised, a, (size_t)8 << a.words_shift, reinterpret_cast<cudaStream_t>(stream));
+  const size_t words = (size_t)1 << a.words_shift;
+  a.whole_at = (int32_t)(2 * words + 2 * num_seqs);
+  static std::atomic<bool> raised[2][kSmemDevices];
+  return launch_table(ctas == 1 ? cache_compact_kernel<1> : cache_compact_kernel<kCtas>, raised[ctas > 1], a, ctas,
+                      4 * ((size_t)a.whole_at + (a.whole ? words * kCtas : 0)), reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int moe_cache_copy(const moe_cache_pages* caches, int64_t num_caches, int64_t num_pages, const int32_t* src,
