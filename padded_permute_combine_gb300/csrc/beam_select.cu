@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kUnit = 512;            // elements that a warp reduces at a time
 constexpr int kThreads = 256;         // of the first kernel
+constexpr int kUnitCtas = 4;          // of it, on an SM
 constexpr int kJoinThreads = 1024;    // of the second
 constexpr int kBests = 256;           // most sets of units among whose best ones the bound is found
 constexpr int kList = 1024;           // candidates at hand
@@ -73,7 +74,7 @@ template <typename ET, int VB> struct Part {
 };
 
 template <typename ET, int VB>
-__global__ void __launch_bounds__(kThreads) select_units_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kThreads, kUnitCtas) select_units_kernel(const SelectArgs a) {
   using P = Part<ET, VB>;
   using E1 = typename Vec<Elem<ET>::kBytes>::T;
   constexpr bool kPairs = VB >= 4 && Elem<ET>::kBytes == 2;
@@ -454,7 +455,8 @@ __global__ void __launch_bounds__(kJoinThreads) select_join_kernel(const SelectA
 template <typename ET, int VB> int launch_select(const SelectArgs& a, cudaStream_t s) {
   const int64_t units = a.requests * a.beams * a.per_row;
   auto k = select_units_kernel<ET, VB>;
-  launch(k, persistent_grid(k, kThreads, 0, (units + kThreads / kWarp - 1) / (kThreads / kWarp)), kThreads, 0, s, a);
+  const int64_t work = (units + kThreads / kWarp - 1) / (kThreads / kWarp), most = (int64_t)num_sms() * kUnitCtas;
+  launch(k, dim3((unsigned)(work < most ? work : most)), dim3(kThreads), 0, s, a);
   const int rc = check_launch();
   if (rc != MOE_OK) return rc;
   static std::atomic<bool> raised[kSmemDevices];

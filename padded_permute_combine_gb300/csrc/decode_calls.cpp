@@ -30,6 +30,26 @@ bool ints_of(const Tensor& t, c10::Device device, at::IntArrayRef sizes) {
   return on(t, at::kInt, (int64_t)sizes.size(), device) && t.is_contiguous() && t.sizes() == sizes;
 }
 
+// Several small outputs as parts of one allocation (an allocation costs the
+// host 0.7 us or more, a part 0.2): each on 16 bytes, contiguous.
+template <int N> void parts_of(const Tensor& like, const at::ScalarType (&types)[N], const std::initializer_list<int64_t> (&sizes)[N], Tensor (&out)[N]) {
+  int64_t bytes = 0, at[N];
+  for (int i = 0; i < N; ++i) {
+    int64_t n = (int64_t)c10::elementSize(types[i]);
+    for (const int64_t d : sizes[i]) n *= d;
+    at[i] = bytes;
+    bytes += (n + 15) / 16 * 16;
+  }
+  const Tensor whole = make(like, at::kByte, {bytes});
+  for (int i = 0; i < N; ++i) {
+    out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                      c10::scalarTypeToTypeMeta(types[i]));
+    c10::TensorImpl* impl = out[i].unsafeGetTensorImpl();
+    impl->set_storage_offset(at[i] / (int64_t)c10::elementSize(types[i]));
+    impl->set_sizes_contiguous(sizes[i]);
+  }
+}
+
 // The stride of dimension i, 0 where it has one element.
 int64_t step(const Tensor& t, int64_t i) { return t.size(i) <= 1 ? 0 : t.stride(i); }
 
@@ -125,13 +145,17 @@ PyObject* cache_fork(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     Tensor t[3];
     int64_t v[4], stride;
-    if (n != 7 || !tensors(args, 3, t) || !ints(args + 3, 4, v) || !fits32(v[0]) || !t[0].is_cuda()) return nullptr;
+    const bool same = n == 7 && args[6] == Py_None;
+    if (n != 7 || !tensors(args, 3, t) || !ints(args + 3, same ? 3 : 4, v) || !fits32(v[0]) || !t[0].is_cuda()) return nullptr;
     const Tensor &table = t[0], &lengths = t[1], &parents = t[2];
+    if (same) v[3] = table.dim() == 2 ? table.size(1) : -1;
     if (!table_of(table, lengths, table.device(), &stride) || parents.dim() != 1 || !ints_of(parents, table.device(), {parents.size(0)}) || v[3] < 0)
       return nullptr;
     const c10::cuda::CUDAGuard current(table.device());
     const int64_t R = parents.size(0);
-    const Tensor next = make(table, at::kInt, {R, v[3]}), len = make(table, at::kInt, {R}), src = make(table, at::kInt, {R}), dst = make(table, at::kInt, {R});
+    Tensor o[4];
+    parts_of(table, {at::kInt, at::kInt, at::kInt, at::kInt}, {{R, v[3]}, {R}, {R}, {R}}, o);
+    const Tensor &next = o[0], &len = o[1], &src = o[2], &dst = o[3];
     const int rc = unlocked([&] {
       return moe_cache_fork(table.const_data_ptr<int32_t>(), stride, table.size(1), lengths.const_data_ptr<int32_t>(), table.size(0),
                             parents.const_data_ptr<int32_t>(), R, (int32_t)v[0], v[1], v[2], next.data_ptr<int32_t>(), v[3], len.data_ptr<int32_t>(),
@@ -150,8 +174,9 @@ PyObject* cache_compact(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const Tensor &table = t[0], &lengths = t[1];
     if (!table_of(table, lengths, table.device(), &stride) || v[1] > MOE_CACHE_MAX_PAGES) return nullptr;
     const c10::cuda::CUDAGuard current(table.device());
-    const Tensor next = make(table, at::kInt, table.sizes()), src = make(table, at::kInt, {v[1] / 2}), dst = make(table, at::kInt, {v[1] / 2}),
-                 count = make(table, at::kInt, {1});
+    Tensor o[4];
+    parts_of(table, {at::kInt, at::kInt, at::kInt, at::kInt}, {{table.size(0), table.size(1)}, {v[1] / 2}, {v[1] / 2}, {1}}, o);
+    const Tensor &next = o[0], &src = o[1], &dst = o[2], &count = o[3];
     const int rc = unlocked([&] {
       return moe_cache_compact(table.const_data_ptr<int32_t>(), stride, table.size(1), lengths.const_data_ptr<int32_t>(), table.size(0), (int32_t)v[0],
                                v[1], next.data_ptr<int32_t>(), src.data_ptr<int32_t>(), dst.data_ptr<int32_t>(), count.data_ptr<int32_t>(), nullptr,
@@ -222,8 +247,9 @@ PyObject* beam_select(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const c10::cuda::CUDAGuard current(x.device());
     const size_t bytes = moe_beam_select_workspace_size(B, (int32_t)W, V);
     if (bytes == 0) return nullptr;
-    const Tensor best = make(x, at::kFloat, {B, num_out}), from = make(x, at::kInt, {B, num_out}), token = make(x, at::kInt, {B, num_out}),
-                 ws = make(x, at::kByte, {(int64_t)bytes});
+    Tensor o[3];
+    parts_of(x, {at::kFloat, at::kInt, at::kInt}, {{B, num_out}, {B, num_out}, {B, num_out}}, o);
+    const Tensor &best = o[0], &from = o[1], &token = o[2], ws = make(x, at::kByte, {(int64_t)bytes});
     const int rc = unlocked([&] {
       return moe_beam_select(x.const_data_ptr(), dtype_of(x), stride, scores.const_data_ptr<float>(),
                              static_cast<const uint8_t*>(ended.defined() ? ended.const_data_ptr() : nullptr), B, (int32_t)W, V, (int32_t)num_out,

@@ -178,11 +178,10 @@ def moe_cache_fork(page_table: torch.Tensor, lengths: torch.Tensor, parents: tor
     an empty row) with room for ``grow`` more tokens; see include/moe_decode.h.
     The copies src -> dst are moe_cache_copy's to make. ``width``: columns of the
     new table, page_table's by default."""
-    if out is None and status is None and isinstance(page_table, torch.Tensor) and page_table.dim() == 2:
-        done = (_lib.calls or _lib.load_calls()).cache_fork(
-            page_table, lengths, parents, page_size, num_pages, grow, page_table.shape[1] if width is None else width)
+    if out is None and status is None:
+        done = (_lib.calls or _lib.load_calls()).cache_fork(page_table, lengths, parents, page_size, num_pages, grow, width)
         if done is not None:
-            return CacheFork._make(done)
+            return tuple.__new__(CacheFork, done)
     _tensor(page_table, "page_table", 2, _I32, None)
     dev = page_table.device
     table, stride, old, rows, lengths_at = _table(page_table, lengths, dev)
@@ -210,7 +209,7 @@ def moe_cache_compact(page_table: torch.Tensor, lengths: torch.Tensor, page_size
     if out is None and status is None:
         done = (_lib.calls or _lib.load_calls()).cache_compact(page_table, lengths, page_size, num_pages)
         if done is not None:
-            return CacheCompact._make(done)
+            return tuple.__new__(CacheCompact, done)
     _tensor(page_table, "page_table", 2, _I32, None)
     dev = page_table.device
     table, stride, width, rows, lengths_at = _table(page_table, lengths, dev)
