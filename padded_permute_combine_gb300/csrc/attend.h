@@ -16,7 +16,7 @@ namespace moe {
 
 constexpr int kTile = 16;      // tokens of a tile, the unit of the ranges
 constexpr int kSmWarps = 8;    // warps of an SM: a CTA of eight, one an SM
-constexpr int kMinTiles = 2;   // of a range, where there are fewer tiles than warps
+constexpr int kMinTiles = 1;   // of a range, where there are fewer tiles than warps
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -106,12 +106,16 @@ struct Cursor {
 // The joining kernel may start: it waits for this one before it reads what it left.
 __device__ __forceinline__ void start_next_kernel() { asm volatile("griddepcontrol.launch_dependents;"); }
 
-// The CTA's view of the line: prefix[t] tiles in front of the sequences of thread t.
+__device__ __forceinline__ void check_length(const AttendArgs& a, int n) {
+  if (blockIdx.x == 0 && (n < 0 || n > a.max_tokens)) flag_status(a.status, MOE_STATUS_BAD_INDEX);
+}
+
+// The tiles in front of the sequences of each thread, in prefix, and their sum.
 __device__ __forceinline__ int line_prefix(const AttendArgs& a, int* prefix, int* s_warp) {
   const int t = threadIdx.x, chunk = (a.seqs + blockDim.x - 1) / blockDim.x;
   int mine = 0;
   for (int b = t * chunk; b < a.seqs && b < (t + 1) * chunk; ++b) {
-    if (blockIdx.x == 0 && (a.lengths[b] < 0 || a.lengths[b] > a.max_tokens)) flag_status(a.status, MOE_STATUS_BAD_INDEX);
+    check_length(a, a.lengths[b]);
     mine += tiles_of(a, b);
   }
   int before;
@@ -153,6 +157,44 @@ __device__ __forceinline__ int64_t row_offset(const AttendArgs& a, const Cursor&
     return -1;
   }
   return page * a.page_stride + (pos - a.page.of(pos) * a.page.d) * a.token_stride + kv * a.head_stride;
+}
+
+// The range of warp r of a head: how many tiles, and where the first is.
+__device__ __forceinline__ int my_range(const AttendArgs& a, int r, int* prefix, int* s_warp, Cursor& c) {
+  int total, before = 0, x = 0;  // x: tiles up to the lane's sequence
+  const bool few = a.seqs <= kWarp;
+  Cursor own = {lane_id(), 0, 0, 0, 0};
+  if (few) {  // every warp for itself
+    if (own.b < a.seqs) {
+      check_length(a, a.lengths[own.b]);
+      own.enter(a);
+    }
+    x = own.tiles;
+#pragma unroll
+    for (int d = 1; d < kWarp; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, x, d);
+      if (own.b >= d) x += o;
+    }
+    total = __shfl_sync(0xffffffffu, x, kWarp - 1);
+  } else {
+    total = line_prefix(a, prefix, s_warp);
+  }
+  if (total == 0) return 0;
+  const int ranges = ranges_of(a, total);
+  if (r >= ranges) return 0;
+  const int lo = range_begin(r, ranges, total), count = range_begin(r + 1, ranges, total) - lo;
+  if (count <= 0) return 0;
+  if (few) {
+    c.b = __ffs(__ballot_sync(0xffffffffu, x > lo)) - 1;
+    before = __shfl_sync(0xffffffffu, x - own.tiles, c.b);
+    c.tile = lo - before;
+    c.tiles = __shfl_sync(0xffffffffu, own.tiles, c.b);
+    c.first = __shfl_sync(0xffffffffu, own.first, c.b);
+    c.n = __shfl_sync(0xffffffffu, own.n, c.b);
+  } else {
+    c = find_tile(a, prefix, lo);
+  }
+  return count;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {

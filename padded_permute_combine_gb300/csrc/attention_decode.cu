@@ -20,6 +20,8 @@
 namespace moe {
 namespace {
 
+constexpr int kLanes = MOE_ATTENTION_MAX_DIM / kWarp;  // elements of a row for a lane
+
 // Joins the parts of the sequences that more than one range covers, and
 // answers for those without a position. Many parts of a head are shared by up
 // to eight warps, whose sums are joined in shared memory.
@@ -61,18 +63,23 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
   }
   await_previous_kernel();
   if (parts == 1) return;
-  const int split = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;  // warps of a head
+  const int split = parts <= 2 ? 1 : parts <= 4 ? 2 : parts <= 8 ? 4 : 8;  // warps of a head
   const int at_once = 8 / split, sub = warp % split;
   for (int h0 = blockIdx.y * at_once; h0 < a.heads; h0 += gridDim.y * at_once) {
     const int h = h0 + warp / split;
-    float m = -INFINITY, sum = 0.0f, o[MOE_ATTENTION_MAX_DIM / kWarp];
+    float m = -INFINITY, sum = 0.0f, o[kLanes];
 #pragma unroll
-    for (int j = 0; j < MOE_ATTENTION_MAX_DIM / kWarp; ++j) o[j] = 0.0f;
+    for (int j = 0; j < kLanes; ++j) o[j] = 0.0f;
     if (h < a.heads) {
       const int64_t first = (int64_t)(r0 + b) * a.heads + h;  // of part 0; the next is a.heads further
       for (int i0 = sub; i0 < parts; i0 += split * kWarp) {  // 32 of this warp's parts at a time
         const int mine = i0 + lane * split, n = min(kWarp, (parts - i0 + split - 1) / split);
+        const float* rows = a.part_o + (first + (int64_t)i0 * a.heads) * D;
+        const int64_t step = (int64_t)split * a.heads * D;
         const float2 ml = mine < parts ? a.part_ml[first + (int64_t)mine * a.heads] : make_float2(-INFINITY, 0.0f);
+        float next[kLanes];  // of the first part: on its way with the maxima and sums
+#pragma unroll
+        for (int j = 0; j < kLanes; ++j) next[j] = j * kWarp + lane < D ? rows[j * kWarp + lane] : 0.0f;
         float top = ml.x;
 #pragma unroll
         for (int d = 1; d < kWarp; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -84,14 +91,12 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
         for (int d = 1; d < kWarp; d <<= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
         sum = sum * keep + all;
 #pragma unroll
-        for (int j = 0; j < MOE_ATTENTION_MAX_DIM / kWarp; ++j) o[j] *= keep;
-        const float* rows = a.part_o + (first + (int64_t)i0 * a.heads) * D;
-        const int64_t step = (int64_t)split * a.heads * D;
+        for (int j = 0; j < kLanes; ++j) o[j] = fmaf(__shfl_sync(0xffffffffu, weight, 0), next[j], o[j] * keep);
 #pragma unroll 4
-        for (int i = 0; i < n; ++i) {
+        for (int i = 1; i < n; ++i) {
           const float w = __shfl_sync(0xffffffffu, weight, i);
 #pragma unroll
-          for (int j = 0; j < MOE_ATTENTION_MAX_DIM / kWarp; ++j)
+          for (int j = 0; j < kLanes; ++j)
             if (j * kWarp + lane < D) o[j] = fmaf(w, rows[i * step + j * kWarp + lane], o[j]);
         }
       }
@@ -100,7 +105,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
       __syncthreads();
       if (lane == 0) s_ml[warp] = make_float2(m, sum);
 #pragma unroll
-      for (int j = 0; j < MOE_ATTENTION_MAX_DIM / kWarp; ++j) s_o[warp][j * kWarp + lane] = o[j];
+      for (int j = 0; j < kLanes; ++j) s_o[warp][j * kWarp + lane] = o[j];
       __syncthreads();
       if (sub != 0) continue;
       float top = -INFINITY;
@@ -108,21 +113,21 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
       m = top;
       sum = 0.0f;
 #pragma unroll
-      for (int j = 0; j < MOE_ATTENTION_MAX_DIM / kWarp; ++j) o[j] = 0.0f;
+      for (int j = 0; j < kLanes; ++j) o[j] = 0.0f;
       const float base = top == -INFINITY ? 0.0f : top;
       for (int w = 0; w < split; ++w) {
         const float2 ml = s_ml[warp + w];
         const float weight = exp2f(ml.x - base);
         sum += ml.y * weight;
 #pragma unroll
-        for (int j = 0; j < MOE_ATTENTION_MAX_DIM / kWarp; ++j) o[j] = fmaf(weight, s_o[warp + w][j * kWarp + lane], o[j]);
+        for (int j = 0; j < kLanes; ++j) o[j] = fmaf(weight, s_o[warp + w][j * kWarp + lane], o[j]);
       }
     }
     if (h >= a.heads) continue;
     const int64_t head = (int64_t)b * a.heads + h;
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
-    for (int j = 0; j < MOE_ATTENTION_MAX_DIM / kWarp; ++j) {
+    for (int j = 0; j < kLanes; ++j) {
       const int d = j * kWarp + lane;
       if (d >= D) continue;
       if constexpr (sizeof(ET) == 4) {

@@ -59,14 +59,11 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
   await_previous_kernel();
   start_next_kernel();
   const int lane = lane_id(), warp = threadIdx.x / kWarp;
-  const int total = line_prefix(a, s_prefix, s_warp);
   const int HV = a.kv_heads * a.parts, gw = blockIdx.x * kWarps + warp;
   const int r = gw / HV, hv = gw - r * HV, kv = hv / a.parts, part = hv - kv * a.parts;
-  if (total == 0) return;
-  const int ranges = ranges_of(a, total);
-  if (r >= ranges) return;
-  const int lo = range_begin(r, ranges, total), count = range_begin(r + 1, ranges, total) - lo;
-  if (count <= 0) return;
+  Cursor in;
+  const int count = my_range(a, r, s_prefix, s_warp, in);
+  if (count == 0) return;
   const int D = a.D, h0 = kv * a.group + part * S::kHeads, heads = min(S::kHeads, a.group - part * S::kHeads);
   const uint32_t ring = smem_u32(smem) + warp * kStages * S::kStageBytes;
   if (SHIFT || D < DP) {  // pieces behind D are never copied, and have to be numbers
@@ -79,14 +76,13 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
   // fetch is one of 256 bytes (four lanes a row take 40 instructions instead of
   // 150, but pieces of 64 bytes: 64 ragged sequences 157 us instead of 147). With
   // SHIFT there are more instructions a copy, and four lanes a row win.
-  Cursor in = find_tile(a, s_prefix, lo);
   Cursor at = in;
   constexpr int kChunks = DP / 8, kRowsPass = kWarp / kChunks, kPasses = kTile / kRowsPass;
   const int r0 = lane >> 2, quarter = lane & 3, pieces = (D + 7) / 8;
   const int chunk = lane % kChunks, sub = lane / kChunks;
   int issued = 0, page[2] = {page_entry(a, in, SHIFT ? r0 : lane & (kTile - 1)), SHIFT ? page_entry(a, in, r0 + 8) : 0};
   const intptr_t apart = a.v - a.k;
-  const auto issue = [&]() {
+  const auto issue = [&](bool look) {  // look: for the next tile's page
     if (issued < count) {
       const int stage = issued % kStages;
       const int fresh = a.k_new != nullptr ? in.n - 1 - (in.first + in.tile * kTile) : -1;  // the new token's row
@@ -162,8 +158,10 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
       }
       if (++issued < count) {
         in.next(a);
-        page[0] = page_entry(a, in, SHIFT ? r0 : lane & (kTile - 1));
-        if constexpr (SHIFT) page[1] = page_entry(a, in, r0 + 8);
+        if (look) {
+          page[0] = page_entry(a, in, SHIFT ? r0 : lane & (kTile - 1));
+          if constexpr (SHIFT) page[1] = page_entry(a, in, r0 + 8);
+        }
       }
     }
     cp_commit();
@@ -211,8 +209,23 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
     }
     __syncwarp();
   };
+  {  // the first tiles' pages on their way together
+    int first[kStages][2];
+    Cursor ahead = in;
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue();
+    for (int i = 1; i < kStages; ++i) {
+      if (i >= count) continue;
+      ahead.next(a);
+      first[i][0] = page_entry(a, ahead, SHIFT ? r0 : lane & (kTile - 1));
+      if constexpr (SHIFT) first[i][1] = page_entry(a, ahead, r0 + 8);
+    }
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      issue(false);
+      page[0] = first[i + 1][0];
+      if constexpr (SHIFT) page[1] = first[i + 1][1];
+    }
+  }
 
   uint32_t q[kTiles][kSteps][4];
   float o[kTiles][DP / 8][4], m[kTiles][2], l[kTiles][2];
@@ -261,7 +274,7 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
     there[0] = s_mask[warp][stage][0];
     there[1] = SHIFT ? s_mask[warp][stage][SHIFT ? 1 : 0] : there[0] >> 8;
     const bool all = SHIFT ? (there[0] & there[1]) == 0xffffffffu : there[0] == 0xffffu;
-    issue();  // into the stage that the previous tile left
+    issue(true);  // into the stage that the previous tile left
     if constexpr (SHIFT) align(stage);
     const uint32_t base = ring + stage * S::kStageBytes;
     float s[kTiles][2][4];

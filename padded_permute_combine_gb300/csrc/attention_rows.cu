@@ -31,14 +31,11 @@ __global__ void __launch_bounds__(kSmWarps * kWarp, 1) attend_rows_kernel(const 
   await_previous_kernel();
   start_next_kernel();
   const int lane = lane_id(), warp = threadIdx.x / kWarp, warps = blockDim.x / kWarp;
-  const int total = line_prefix(a, s_prefix, s_warp);
   const int HV = a.kv_heads * a.parts, gw = blockIdx.x * warps + warp;
   const int r = gw / HV, hv = gw - r * HV, kv = hv / a.parts, part = hv - kv * a.parts;
-  if (total == 0) return;
-  const int ranges = ranges_of(a, total);
-  if (r >= ranges) return;
-  const int lo = range_begin(r, ranges, total), count = range_begin(r + 1, ranges, total) - lo;
-  if (count <= 0) return;
+  Cursor in;
+  const int count = my_range(a, r, s_prefix, s_warp, in);
+  if (count == 0) return;
 
   const int D = a.D;
   const RowPieces row(D);
@@ -54,7 +51,6 @@ __global__ void __launch_bounds__(kSmWarps * kWarp, 1) attend_rows_kernel(const 
   // Copies of a tile's keys, then of its values: four lanes a row (rows r0 and
   // r0 + 8), so that a copy's addresses are a register and a constant.
   constexpr int kTurns = VB == 16 ? NC * 8 : NC * 32;  // of the four lanes over a row
-  Cursor in = find_tile(a, s_prefix, lo);
   Cursor at = in;
   const int r0 = lane >> 2, part4 = lane & 3, pieces = VB == 16 ? row.pieces : D;
   int issued = 0, slot_in = 0, page[2] = {page_entry(a, in, r0), page_entry(a, in, r0 + 8)}, bytes[2];
