@@ -22,10 +22,32 @@ namespace {
 
 constexpr int kLanes = MOE_ATTENTION_MAX_DIM / kWarp;  // elements of a row for a lane
 
+// A lane's elements of a row of D: fours of them (QUADS, where D is a multiple
+// of four), or every 32nd.
+template <bool QUADS> struct RowPart {
+  float v[kLanes];
+  __device__ __forceinline__ static int place(int j) { return QUADS ? (j / 4 * kWarp + lane_id()) * 4 + j % 4 : j * kWarp + lane_id(); }
+  __device__ __forceinline__ void load(const float* row, int D) {
+    if constexpr (QUADS) {
+#pragma unroll
+      for (int j = 0; j < kLanes; j += 4) {
+        const float4 x = place(j) < D ? *reinterpret_cast<const float4*>(row + place(j)) : make_float4(0, 0, 0, 0);
+        v[j] = x.x;
+        v[j + 1] = x.y;
+        v[j + 2] = x.z;
+        v[j + 3] = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kLanes; ++j) v[j] = place(j) < D ? row[place(j)] : 0.0f;
+    }
+  }
+};
+
 // Joins the parts of the sequences that more than one range covers, and
 // answers for those without a position. Many parts of a head are shared by up
 // to eight warps, whose sums are joined in shared memory.
-template <typename ET>
+template <typename ET, bool QUADS>
 __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
   __shared__ int s_total[8], s_before[8];
   __shared__ float s_o[8][MOE_ATTENTION_MAX_DIM];
@@ -67,6 +89,8 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
   const int at_once = 8 / split, sub = warp % split;
   for (int h0 = blockIdx.y * at_once; h0 < a.heads; h0 += gridDim.y * at_once) {
     const int h = h0 + warp / split;
+    using P = RowPart<QUADS>;
+    constexpr int kAhead = 8;  // parts on their way together
     float m = -INFINITY, sum = 0.0f, o[kLanes];
 #pragma unroll
     for (int j = 0; j < kLanes; ++j) o[j] = 0.0f;
@@ -77,9 +101,10 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
         const float* rows = a.part_o + (first + (int64_t)i0 * a.heads) * D;
         const int64_t step = (int64_t)split * a.heads * D;
         const float2 ml = mine < parts ? a.part_ml[first + (int64_t)mine * a.heads] : make_float2(-INFINITY, 0.0f);
-        float next[kLanes];  // of the first part: on its way with the maxima and sums
+        P next[kAhead];  // the first parts are on their way with the maxima and sums
 #pragma unroll
-        for (int j = 0; j < kLanes; ++j) next[j] = j * kWarp + lane < D ? rows[j * kWarp + lane] : 0.0f;
+        for (int i = 0; i < kAhead; ++i)
+          if (i < n) next[i].load(rows + i * step, D);
         float top = ml.x;
 #pragma unroll
         for (int d = 1; d < kWarp; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -91,13 +116,20 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
         for (int d = 1; d < kWarp; d <<= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
         sum = sum * keep + all;
 #pragma unroll
-        for (int j = 0; j < kLanes; ++j) o[j] = fmaf(__shfl_sync(0xffffffffu, weight, 0), next[j], o[j] * keep);
-#pragma unroll 4
-        for (int i = 1; i < n; ++i) {
-          const float w = __shfl_sync(0xffffffffu, weight, i);
+        for (int j = 0; j < kLanes; ++j) o[j] *= keep;
+        for (int i = 0; i < n; i += kAhead) {
+          if (i > 0) {
 #pragma unroll
-          for (int j = 0; j < kLanes; ++j)
-            if (j * kWarp + lane < D) o[j] = fmaf(w, rows[i * step + j * kWarp + lane], o[j]);
+            for (int k = 0; k < kAhead; ++k)
+              if (i + k < n) next[k].load(rows + (i + k) * step, D);
+          }
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            if (i + k >= n) continue;
+            const float w = __shfl_sync(0xffffffffu, weight, i + k);
+#pragma unroll
+            for (int j = 0; j < kLanes; ++j) o[j] = fmaf(w, next[k].v[j], o[j]);
+          }
         }
       }
     }
@@ -105,7 +137,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
       __syncthreads();
       if (lane == 0) s_ml[warp] = make_float2(m, sum);
 #pragma unroll
-      for (int j = 0; j < kLanes; ++j) s_o[warp][j * kWarp + lane] = o[j];
+      for (int j = 0; j < kLanes; ++j) s_o[warp][P::place(j)] = o[j];
       __syncthreads();
       if (sub != 0) continue;
       float top = -INFINITY;
@@ -120,7 +152,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
         const float weight = exp2f(ml.x - base);
         sum += ml.y * weight;
 #pragma unroll
-        for (int j = 0; j < kLanes; ++j) o[j] = fmaf(weight, s_o[warp + w][j * kWarp + lane], o[j]);
+        for (int j = 0; j < kLanes; ++j) o[j] = fmaf(weight, s_o[warp + w][P::place(j)], o[j]);
       }
     }
     if (h >= a.heads) continue;
@@ -128,7 +160,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
     for (int j = 0; j < kLanes; ++j) {
-      const int d = j * kWarp + lane;
+      const int d = P::place(j);
       if (d >= D) continue;
       if constexpr (sizeof(ET) == 4) {
         static_cast<float*>(a.out)[head * D + d] = o[j] * inv;
@@ -155,7 +187,7 @@ template <typename ET> int run_attend(AttendArgs& a, cudaStream_t s) {
   if (rc != MOE_OK) return rc;
   int y = (int)(4 * (int64_t)num_sms() / a.seqs);
   y = y < 1 ? 1 : (y > a.heads ? a.heads : y);
-  launch(attend_join_kernel<ET>, dim3((unsigned)a.seqs, (unsigned)y), dim3(256), 0, s, a);
+  launch(a.D % 4 == 0 ? attend_join_kernel<ET, true> : attend_join_kernel<ET, false>, dim3((unsigned)a.seqs, (unsigned)y), dim3(256), 0, s, a);
   return check_launch();
 }
 

@@ -107,7 +107,9 @@ PyObject* attention_decode(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const c10::cuda::CUDAGuard current(k.device());
     const size_t bytes = moe_attention_decode_workspace_size(B, (int32_t)H, cache.num_kv_heads, (int32_t)D);
     if (bytes == 0) return nullptr;
-    const Tensor out = make(k, k.scalar_type(), {B, H, D}), lse = make(k, at::kFloat, {B, H}), ws = make(k, at::kByte, {(int64_t)bytes});
+    Tensor o[2];
+    parts_of(k, {k.scalar_type(), at::kFloat}, {{B, H, D}, {B, H}}, o);
+    const Tensor &out = o[0], &lse = o[1], ws = make(k, at::kByte, {(int64_t)bytes});
     const float scale = args[7] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : (float)PyFloat_AS_DOUBLE(args[7]);
     const int rc = unlocked([&] {
       return moe_attention_decode(&cache, &qs, (int32_t)H, table.const_data_ptr<int32_t>(), stride, table.size(1), lengths.const_data_ptr<int32_t>(), B,
