@@ -15,7 +15,7 @@
 namespace moe {
 
 constexpr int kTile = 16;      // tokens of a tile, the unit of the ranges
-constexpr int kSmWarps = 8;    // warps of an SM: a CTA of eight, one an SM
+constexpr int kMostWarps = 16; // of an SM, which has one CTA
 constexpr int kMinTiles = 1;   // of a range, where there are fewer tiles than warps
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;

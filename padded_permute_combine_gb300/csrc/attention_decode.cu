@@ -192,7 +192,7 @@ template <typename ET> int run_attend(AttendArgs& a, cudaStream_t s) {
 }
 
 int64_t slots_of(int64_t seqs, int32_t kv_heads) {
-  const int64_t r = (int64_t)num_sms() * kSmWarps / kv_heads;
+  const int64_t r = (int64_t)num_sms() * kMostWarps / kv_heads;
   return (r < 1 ? 1 : r) + seqs;
 }
 

@@ -24,16 +24,19 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Sizes of a variant: DP elements of a padded row (64, 128 or 256), MT tiles of
-// 16 query heads (0: eight heads in one), SHIFT for rows off 16 bytes.
-template <int DP, int MT, bool SHIFT> struct Mma {
+// Sizes of a variant: DP elements of a row for a warp (64 or 128), TEAM warps that
+// share the row, MT tiles of 16 query heads (0: eight heads in one), SHIFT for
+// rows off 16 bytes.
+template <int DP, int MT, bool SHIFT, int TEAM> struct Mma {
   static constexpr int kHeads = MT == 0 ? 8 : 16 * MT, kTiles = MT == 0 ? 1 : MT;
-  static constexpr int kWarps = DP == 256 ? 4 : 8;
+  static constexpr int kWarps = DP == 128 ? 8 : (SHIFT ? 12 : 16) / TEAM * TEAM;
   // Pieces of a row are swizzled by its number, or rows are one piece further apart: no two rows' pieces in one bank.
   static constexpr int kPitch = DP * 2 + (SHIFT ? 16 : 0);
   static constexpr int kStageBytes = 2 * kTile * kPitch;
-  static constexpr int kStages = DP == 64 ? 6 : 3;  // 192 to 221 KB an SM
-  static constexpr size_t kSmem = (size_t)kWarps * kStages * kStageBytes;
+  static constexpr int kStages = 3;  // 162 to 192 KB an SM
+  static constexpr int kScores = 4 * (MT == 0 ? 1 : 2 * kTiles);  // of a lane
+  static constexpr size_t kRings = (size_t)kWarps * kStages * kStageBytes;
+  static constexpr size_t kSmem = kRings + (TEAM > 1 ? (size_t)2 * kWarps * kWarp * kScores * 4 : 0);
 };
 
 // S = Q K^T and O += P V by m16n8k16 products: the query heads of a kv head are
@@ -45,26 +48,33 @@ template <int DP, int MT, bool SHIFT> struct Mma {
 // Rows off 16 bytes (SHIFT) are copied as the aligned pieces that hold them (a
 // piece that holds an element lies inside the element's allocation) and moved
 // into place in shared memory, piece by piece, when they have come.
-template <int DP, int MT, bool SHIFT>
-__global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_mma_kernel(const AttendArgs a) {
-  using S = Mma<DP, MT, SHIFT>;
+// What takes longer than its bytes do is bound by the latency of a warp's
+// instructions, eight warps an SM with rows of 128 elements. So the warps of a
+// team share the rows, 64 elements each: they copy, multiply and sum their own
+// columns, twice as many warps on an SM, and meet once a tile to add up the
+// scores, of which each has a part.
+template <int DP, int MT, bool SHIFT, int TEAM>
+__global__ void __launch_bounds__(Mma<DP, MT, SHIFT, TEAM>::kWarps * kWarp, 1) attend_mma_kernel(const AttendArgs a) {
+  using S = Mma<DP, MT, SHIFT, TEAM>;
   constexpr int kWarps = S::kWarps, kStages = S::kStages, kTiles = S::kTiles, kPitch = S::kPitch;
   constexpr int kTurns = DP / 32;  // of four lanes over the 16-byte pieces of a row
   constexpr int kSteps = DP / 16;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_prefix[kWarps * kWarp], s_warp[kWarps];
-  // Rows that are there: a bit each or, with SHIFT, four equal ones, rows 0 to 7 and 8 to 15.
-  __shared__ unsigned s_mask[kWarps][kStages][SHIFT ? 2 : 1];
+  __shared__ unsigned s_mask[kWarps][kStages][SHIFT ? 2 : 1];  // rows that are there: all 16 or, with SHIFT, eight and eight
   __shared__ uint8_t s_low[kWarps][SHIFT ? kStages : 1][kTile];  // rows' offsets to 16 bytes
   await_previous_kernel();
   start_next_kernel();
   const int lane = lane_id(), warp = threadIdx.x / kWarp;
-  const int HV = a.kv_heads * a.parts, gw = blockIdx.x * kWarps + warp;
-  const int r = gw / HV, hv = gw - r * HV, kv = hv / a.parts, part = hv - kv * a.parts;
+  const int HV = a.kv_heads * a.parts, team = warp / TEAM, rank = warp - team * TEAM, gt = blockIdx.x * (kWarps / TEAM) + team;
+  const int r = gt / HV, hv = gt - r * HV, kv = hv / a.parts, part = hv - kv * a.parts;
   Cursor in;
   const int count = my_range(a, r, s_prefix, s_warp, in);
   if (count == 0) return;
-  const int D = a.D, h0 = kv * a.group + part * S::kHeads, heads = min(S::kHeads, a.group - part * S::kHeads);
+  const int col0 = rank * DP, D = min(DP, a.D - col0);  // the warp's columns
+  char* const keys = a.k + 2 * col0;
+  char* const values = a.v + 2 * col0;
+  const int h0 = kv * a.group + part * S::kHeads, heads = min(S::kHeads, a.group - part * S::kHeads);
   const uint32_t ring = smem_u32(smem) + warp * kStages * S::kStageBytes;
   if (SHIFT || D < DP) {  // pieces behind D are never copied, and have to be numbers
     uint4* z = reinterpret_cast<uint4*>(smem + (size_t)warp * kStages * S::kStageBytes);
@@ -78,26 +88,26 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
   // SHIFT there are more instructions a copy, and four lanes a row win.
   Cursor at = in;
   constexpr int kChunks = DP / 8, kRowsPass = kWarp / kChunks, kPasses = kTile / kRowsPass;
-  const int r0 = lane >> 2, quarter = lane & 3, pieces = (D + 7) / 8;
+  const int r0 = lane & 7, quarter = lane >> 3, pieces = (D + 7) / 8;  // eight lanes that meet in shared memory have eight rows: eight banks
   const int chunk = lane % kChunks, sub = lane / kChunks;
   int issued = 0, page[2] = {page_entry(a, in, SHIFT ? r0 : lane & (kTile - 1)), SHIFT ? page_entry(a, in, r0 + 8) : 0};
-  const intptr_t apart = a.v - a.k;
+  const intptr_t apart = values - keys;
   const auto issue = [&](bool look) {  // look: for the next tile's page
     if (issued < count) {
       const int stage = issued % kStages;
       const int fresh = a.k_new != nullptr ? in.n - 1 - (in.first + in.tile * kTile) : -1;  // the new token's row
-      const char* kn = a.k_new + in.b * a.kn_row + kv * a.kn_head;
-      const char* vn = a.v_new + in.b * a.vn_row + kv * a.vn_head;
+      const char* kn = a.k_new + in.b * a.kn_row + kv * a.kn_head + 2 * col0;
+      const char* vn = a.v_new + in.b * a.vn_row + kv * a.vn_head + 2 * col0;
       if constexpr (SHIFT) {
         const uint32_t base = ring + stage * S::kStageBytes + r0 * kPitch + quarter * 16;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const int64_t off = row_offset(a, in, r0 + 8 * w, page[w], kv);
           const unsigned there = __ballot_sync(0xffffffffu, off >= 0);
-          if (lane == 0) s_mask[warp][stage][w] = there;
+          if (lane == 0) s_mask[warp][stage][w] = there & 0xffu;
           const int bytes = off >= 0 ? 16 : 0;
           const uint32_t to = base + 8 * w * kPitch;
-          const uintptr_t k_from = reinterpret_cast<uintptr_t>(a.k) + (off < 0 ? 0 : off), v_from = k_from + apart;
+          const uintptr_t k_from = reinterpret_cast<uintptr_t>(keys) + (off < 0 ? 0 : off), v_from = k_from + apart;
           // The aligned pieces from the row's first byte's on. A row that is not there is zero to its end.
           const int k_low = (int)(k_from & 15), v_low = (int)(v_from & 15);
           const int k_end = bytes == 0 ? 2 * DP + 16 : 2 * D + k_low, v_end = bytes == 0 ? 2 * DP + 16 : 2 * D + v_low;
@@ -139,8 +149,8 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
             cp_async16(dst, kn + chunk * 16, 16);
             cp_async16(dst + kTile * kPitch, vn + chunk * 16, 16);
             if (part == 0) {
-              *reinterpret_cast<uint4*>(a.k + to + chunk * 16) = *reinterpret_cast<const uint4*>(kn + chunk * 16);
-              *reinterpret_cast<uint4*>(a.v + to + chunk * 16) = *reinterpret_cast<const uint4*>(vn + chunk * 16);
+              *reinterpret_cast<uint4*>(keys + to + chunk * 16) = *reinterpret_cast<const uint4*>(kn + chunk * 16);
+              *reinterpret_cast<uint4*>(values + to + chunk * 16) = *reinterpret_cast<const uint4*>(vn + chunk * 16);
             }
           }
         }
@@ -152,8 +162,8 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
           const int bytes = from < 0 ? 0 : 16;
           const int64_t o = from < 0 ? 0 : from + chunk * 16;
           const uint32_t dst = base + row_i * kPitch + (chunk ^ (row_i & 7)) * 16;
-          cp_async16(dst, a.k + o, bytes);
-          cp_async16(dst + kTile * kPitch, a.v + o, bytes);
+          cp_async16(dst, keys + o, bytes);
+          cp_async16(dst + kTile * kPitch, values + o, bytes);
         }
       }
       if (++issued < count) {
@@ -239,7 +249,7 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
     if (fresh) {
       fresh = false;
       first_tile = at.tile;
-      const char* rows = a.q + at.b * a.q_row;
+      const char* rows = a.q + at.b * a.q_row + 2 * col0;
 #pragma unroll
       for (int u = 0; u < kTiles; ++u) {
 #pragma unroll
@@ -270,10 +280,8 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
     cp_wait<kStages - 2>();
     __syncwarp();
     const int stage = i % kStages;
-    unsigned there[2];  // of the first and last eight keys, four equal bits each with SHIFT
-    there[0] = s_mask[warp][stage][0];
-    there[1] = SHIFT ? s_mask[warp][stage][SHIFT ? 1 : 0] : there[0] >> 8;
-    const bool all = SHIFT ? (there[0] & there[1]) == 0xffffffffu : there[0] == 0xffffu;
+    const unsigned there = SHIFT ? s_mask[warp][stage][0] | s_mask[warp][stage][SHIFT ? 1 : 0] << 8 : s_mask[warp][stage][0];
+    const bool all = there == 0xffffu;
     issue(true);  // into the stage that the previous tile left
     if constexpr (SHIFT) align(stage);
     const uint32_t base = ring + stage * S::kStageBytes;
@@ -295,6 +303,36 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
         mma(s[u][1], q[u][ks], b[2], b[3]);
       }
     }
+    if constexpr (TEAM > 1) {
+      // The scores' parts, added up in the same order by every warp. Two places in turn: who writes one again
+      // has met, a tile earlier, those who read it.
+      float* mine = reinterpret_cast<float*>(smem + S::kRings) + ((i & 1) * kWarps + team * TEAM) * kWarp * S::kScores + lane * 4;
+      float part[S::kScores];
+#pragma unroll
+      for (int k = 0; k < S::kScores; ++k) part[k] = MT == 0 ? s[0][k / 2][k % 2] : s[k / 8][k / 4 % 2][k % 4];
+#pragma unroll
+      for (int k = 0; k < S::kScores; k += 4)
+        *reinterpret_cast<float4*>(mine + rank * kWarp * S::kScores + k * kWarp) = make_float4(part[k], part[k + 1], part[k + 2], part[k + 3]);
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(TEAM * kWarp) : "memory");
+#pragma unroll
+      for (int k = 0; k < S::kScores; k += 4) {
+        float4 sum = *reinterpret_cast<const float4*>(mine + k * kWarp);
+#pragma unroll
+        for (int w = 1; w < TEAM; ++w) {
+          const float4 x = *reinterpret_cast<const float4*>(mine + w * kWarp * S::kScores + k * kWarp);
+          sum.x += x.x;
+          sum.y += x.y;
+          sum.z += x.z;
+          sum.w += x.w;
+        }
+        part[k] = sum.x;
+        part[k + 1] = sum.y;
+        part[k + 2] = sum.z;
+        part[k + 3] = sum.w;
+      }
+#pragma unroll
+      for (int k = 0; k < S::kScores; ++k) (MT == 0 ? s[0][k / 2][k % 2] : s[k / 8][k / 4 % 2][k % 4]) = part[k];
+    }
     uint32_t hi[kTiles][4], lo2[kTiles][4];
 #pragma unroll
     for (int u = 0; u < kTiles; ++u) {
@@ -310,7 +348,7 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
           for (int e = 0; e < 2; ++e) {
             float& x = s[u][n][2 * w + e];
             x *= a.scale;
-            if (!all && !(there[n] >> (t * 2 + e) * (SHIFT ? 4 : 1) & 1)) x = -INFINITY;
+            if (!all && !(there >> (n * 8 + t * 2 + e) & 1)) x = -INFINITY;
             top = fmaxf(top, x);
           }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -388,22 +426,22 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
               x += o[u][n][2];
               y += o[u][n][3];
             }
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + head * D + d;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + head * a.D + col0 + d;
             if constexpr (SHIFT) {  // D may be odd
               if (whole) {
                 out[0] = __float2bfloat16_rn(x * inv);
                 if (d + 1 < D) out[1] = __float2bfloat16_rn(y * inv);
               } else {
-                a.part_o[head * D + d] = x;
-                if (d + 1 < D) a.part_o[head * D + d + 1] = y;
+                a.part_o[head * a.D + col0 + d] = x;
+                if (d + 1 < D) a.part_o[head * a.D + col0 + d + 1] = y;
               }
             } else if (whole) {
               *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(x * inv, y * inv);
             } else {
-              *reinterpret_cast<float2*>(a.part_o + head * D + d) = make_float2(x, y);
+              *reinterpret_cast<float2*>(a.part_o + head * a.D + col0 + d) = make_float2(x, y);
             }
           }
-          if (t == 0) {
+          if (t == 0 && rank == 0) {
             if (!whole) {
               a.part_ml[head] = make_float2(m[u][w], sum);
             } else if (a.lse != nullptr) {
@@ -417,23 +455,26 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT>::kWarps * kWarp, 1) attend_
   }
 }
 
-template <int DP, int MT, bool SHIFT> int launch_mma(AttendArgs& a, cudaStream_t s) {
-  using S = Mma<DP, MT, SHIFT>;
+template <int DP, int MT, bool SHIFT, int TEAM> int launch_mma(AttendArgs& a, cudaStream_t s) {
+  using S = Mma<DP, MT, SHIFT, TEAM>;
   static std::atomic<bool> raised[kSmemDevices];
-  auto k = attend_mma_kernel<DP, MT, SHIFT>;
+  auto k = attend_mma_kernel<DP, MT, SHIFT, TEAM>;
   if (!allow_smem(k, raised)) return MOE_ERR_CUDA;
-  cut(a, S::kHeads, S::kWarps);
-  launch(k, dim3(ctas_of(a, S::kWarps)), dim3(S::kWarps * kWarp), S::kSmem, s, a);
+  cut(a, S::kHeads, S::kWarps / TEAM);
+  launch(k, dim3(ctas_of(a, S::kWarps / TEAM)), dim3(S::kWarps * kWarp), S::kSmem, s, a);
   return check_launch();
 }
-template <int DP, bool SHIFT> int launch_mma_heads(AttendArgs& a, cudaStream_t s) {
-  if (a.group <= 8) return launch_mma<DP, 0, SHIFT>(a, s);
-  if constexpr (DP < 256 && !SHIFT)  // two tiles of heads at once: the registers hold them up to 128 elements
-    if (a.group > 16) return launch_mma<DP, 2, SHIFT>(a, s);
-  return launch_mma<DP, 1, SHIFT>(a, s);
+template <int DP, bool SHIFT, int TEAM> int launch_mma_heads(AttendArgs& a, cudaStream_t s) {
+  return a.group <= 8 ? launch_mma<DP, 0, SHIFT, TEAM>(a, s) : launch_mma<DP, 1, SHIFT, TEAM>(a, s);
 }
 template <bool SHIFT> int launch_mma_dim(AttendArgs& a, cudaStream_t s) {
-  return a.D <= 64 ? launch_mma_heads<64, SHIFT>(a, s) : a.D <= 128 ? launch_mma_heads<128, SHIFT>(a, s) : launch_mma_heads<256, SHIFT>(a, s);
+  // Aligned rows of up to 128 elements are one warp's: 64 ragged sequences 147 us, with teams of two 151.
+  if constexpr (!SHIFT)
+    if (a.D > 64 && a.D <= 128) return launch_mma_heads<128, false, 1>(a, s);
+  return a.D <= 64    ? launch_mma_heads<64, SHIFT, 1>(a, s)
+         : SHIFT && a.D <= 128 ? launch_mma_heads<64, true, 2>(a, s)
+         : a.D <= 192 ? launch_mma_heads<64, SHIFT, 3>(a, s)
+                      : launch_mma_heads<64, SHIFT, 4>(a, s);
 }
 
 }  // namespace

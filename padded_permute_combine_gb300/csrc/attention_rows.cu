@@ -13,6 +13,7 @@ struct RowPieces {
   int pieces, pitch, swap;
   __host__ __device__ explicit RowPieces(int D) : pieces((D + 3) / 4), pitch((pieces + 3) / 4 * 4), swap(pitch % 8 == 0 ? 4 : 0) {}
 };
+constexpr int kSmWarps = 8;
 constexpr int kSlots = 3;  // of a warp's ring, a tile's keys or values each
 
 __device__ __forceinline__ uint64_t pair(float a, float b) { return f2_pack(__float_as_uint(a), __float_as_uint(b)); }
