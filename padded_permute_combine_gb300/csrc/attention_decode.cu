@@ -264,6 +264,7 @@ extern "C" int moe_attention_decode(const moe_kv_cache* cache, const moe_heads* 
   a.out = out;
   a.lse = lse;
   a.part_o = static_cast<float*>(workspace);
+  if (cache->num_pages == 0) a.k = a.v = static_cast<char*>(workspace);  // an address for the copies of nothing
   const int64_t rows = slots_of(num_seqs, cache->num_kv_heads) * num_heads;
   a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + (rows * cache->head_dim * 4 + 15) / 16 * 16);
   a.status = d_status;

@@ -496,6 +496,22 @@ struct CopyArgs {
 constexpr int kCopyThreads = 256;
 constexpr int64_t kPieceBytes = 16384;  // of a page, for a CTA at a time
 
+// Four vectors of a thread on their way together.
+template <typename V> __device__ __forceinline__ void copy_piece(const char* in, char* out, int64_t bytes) {
+  const int n = (int)(bytes / (int64_t)sizeof(V));
+  const V* from = reinterpret_cast<const V*>(in);
+  V* to = reinterpret_cast<V*>(out);
+  for (int k = threadIdx.x; k < n; k += 4 * kCopyThreads) {
+    V v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (k + e * kCopyThreads < n) v[e] = ld_stream(from + k + e * kCopyThreads);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (k + e * kCopyThreads < n) to[k + e * kCopyThreads] = v[e];
+  }
+}
+
 // CTA (x, y): every gridDim.x-th pair in piece y of the caches' pages, counted over all caches.
 __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const __grid_constant__ CopyArgs a, int num_caches) {
   await_previous_kernel();
@@ -525,9 +541,13 @@ __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const __grid_c
     }
     const char* in = base + s * stride;
     char* out = base + d * stride;
-    if (((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out) | (uintptr_t)bytes) & 15) == 0) {
-      for (int64_t k = threadIdx.x; k < bytes / 16; k += kCopyThreads)
-        reinterpret_cast<uint4*>(out)[k] = ld_stream(reinterpret_cast<const uint4*>(in) + k);
+    const uintptr_t all = reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out) | (uintptr_t)bytes;
+    if ((all & 15) == 0) {
+      copy_piece<uint4>(in, out, bytes);
+    } else if ((all & 3) == 0) {
+      copy_piece<uint32_t>(in, out, bytes);
+    } else if ((all & 1) == 0) {
+      copy_piece<uint16_t>(in, out, bytes);
     } else {
       for (int64_t k = threadIdx.x; k < bytes; k += kCopyThreads) out[k] = in[k];
     }

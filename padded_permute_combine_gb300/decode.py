@@ -50,6 +50,12 @@ def _tensor(t, name: str, dims: int, dtype: torch.dtype | None, device) -> torch
     return t
 
 
+def _int32(v: int, name: str) -> int:
+    if not -2 ** 31 <= v < 2 ** 31:  # ctypes would cut it
+        raise ValueError("%s does not fit 32 bits: %d" % (name, v))
+    return v
+
+
 def _strides(t: torch.Tensor, name: str, apart: bool) -> tuple:
     """The strides of a tensor that is contiguous in its last dimension (0 for
     dimensions of one element). ``apart``: elements may not overlap."""
@@ -196,7 +202,7 @@ def moe_cache_fork(page_table: torch.Tensor, lengths: torch.Tensor, parents: tor
           zip(out, ((R, new_width), (R,), (R,), (R,)), ("out.page_table", "out.lengths", "out.src", "out.dst"))]
     with _on(dev):
         rc = _lib.load().moe_cache_fork(
-            table, stride, old, lengths_at, rows, parents_at or None, R, page_size, num_pages, grow, at[0], new_width, *at[1:],
+            table, stride, old, lengths_at, rows, parents_at or None, R, _int32(page_size, "page_size"), num_pages, grow, at[0], new_width, *at[1:],
             _status(status, dev), _stream(dev))
     _done("moe_cache_fork", rc)
     return CacheFork(*out)
@@ -221,7 +227,7 @@ def moe_cache_compact(page_table: torch.Tensor, lengths: torch.Tensor, page_size
           zip(out, ((rows, width), (half,), (half,), (1,)), ("out.page_table", "out.src", "out.dst", "out.count"))]
     with _on(dev):
         rc = _lib.load().moe_cache_compact(
-            table, stride, width, lengths_at, rows, page_size, num_pages, *at, _status(status, dev), _stream(dev))
+            table, stride, width, lengths_at, rows, _int32(page_size, "page_size"), num_pages, *at, _status(status, dev), _stream(dev))
     _done("moe_cache_compact", rc)
     return CacheCompact(*out)
 
@@ -307,7 +313,7 @@ def moe_beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int, en
     ws = _workspace(workspace, lib.moe_beam_select_workspace_size(B, W, V), dev)
     with _on(dev):
         rc = lib.moe_beam_select(
-            logits.data_ptr() or None, dt, stride, scores_at or None, ended_at or None, B, W, V, num_out, end_token, *at,
+            logits.data_ptr() or None, dt, stride, scores_at or None, ended_at or None, B, W, V, num_out, _int32(end_token, "end_token"), *at,
             ws.data_ptr() or None, ws.numel(), _stream(dev))
     _done("moe_beam_select", rc)
     return tuple(out)
