@@ -161,3 +161,17 @@ def test_the_binding_refuses_tensors_that_are_not_on_a_gpu():
                  lambda: p.moe_beam_select([1], x, 2), lambda: p.moe_cache_copy([c], None, i)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_native_marshalling_leaves_the_rest_to_the_caller():
+    libbuild.build()
+    calls = _lib.load_calls()
+    c, q, i, t = torch.zeros(3, 4, 2, 8), torch.zeros(2, 4, 8), torch.zeros(2, dtype=torch.int32), torch.zeros(2, 3, dtype=torch.int32)
+    assert calls.attention_decode(q, c, c, t, i, None, None, None, 0) is None  # not on a GPU
+    assert calls.attention_decode(q, c, c, t, i, None, None, "a", 0) is None and calls.attention_decode(q) is None
+    assert calls.attention_decode(q, None, c, t, i, None, None, None, 0) is None
+    assert calls.cache_write(q, q, c, c, t, i, i) is None and calls.cache_write(1, 2, 3, 4, 5, 6, 7) is None
+    assert calls.cache_fork(t, i, i, 4, 3, 1, None) is None and calls.cache_fork(t, i, i, 4, 3, 1, 2 ** 70) is None
+    assert calls.cache_compact(t, i, 4, 3) is None and calls.cache_compact(t, i, 4.0, 3) is None
+    assert calls.cache_copy([c], i, i, None) is None and calls.cache_copy((c,), i, i, None) is None and calls.cache_copy([], i, i, None) is None
+    assert calls.beam_select(q, q[:, :, 0], 2, None, -1) is None and calls.beam_select(q, q[:, :, 0], 2 ** 70, None, -1) is None

@@ -107,7 +107,7 @@ def rand(*shape, dtype=BF16, seed=1, scale=1.5):
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("heads,kv,dim,page", [
     (8, 8, 64, 16), (8, 2, 128, 16), (6, 1, 128, 1), (7, 1, 80, 13), (12, 2, 96, 32), (16, 1, 128, 64), (24, 2, 256, 16),
-    (40, 2, 128, 8), (3, 3, 33, 5), (5, 5, 1, 4), (32, 4, 72, 7), (33, 1, 250, 100), (18, 2, 192, 16), (64, 1, 64, 16)])
+    (40, 2, 128, 8), (6, 2, 150, 16), (20, 1, 187, 9), (3, 3, 33, 5), (5, 5, 1, 4), (32, 4, 72, 7), (33, 1, 250, 100), (18, 2, 192, 16), (64, 1, 64, 16)])
 def test_head_layouts(dtype, heads_first, heads, kv, dim, page):
     lengths = [1, 0, 37, 16, 15, 17, 300, 2]
     k, v, table, dev = make(lengths, page, kv, dim, dtype, heads_first)
