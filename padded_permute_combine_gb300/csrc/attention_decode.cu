@@ -20,11 +20,9 @@
 namespace moe {
 namespace {
 
-constexpr int kLanes = MOE_ATTENTION_MAX_DIM / kWarp;  // elements of a row for a lane
-
 // A lane's elements of a row of D: fours of them (QUADS, where D is a multiple
 // of four), or every 32nd.
-template <bool QUADS> struct RowPart {
+template <bool QUADS, int kLanes> struct RowPart {
   float v[kLanes];
   __device__ __forceinline__ static int place(int j) { return QUADS ? (j / 4 * kWarp + lane_id()) * 4 + j % 4 : j * kWarp + lane_id(); }
   __device__ __forceinline__ void load(const float* row, int D) {
@@ -46,12 +44,13 @@ template <bool QUADS> struct RowPart {
 
 // Joins the parts of the sequences that more than one range covers, and
 // answers for those without a position. Many parts of a head are shared by up
-// to eight warps, whose sums are joined in shared memory.
-template <typename ET, bool QUADS>
-__global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
-  __shared__ int s_total[8], s_before[8];
-  __shared__ float s_o[8][MOE_ATTENTION_MAX_DIM];
-  __shared__ float2 s_ml[8];
+// to WARPS warps, whose sums are joined in shared memory. kLanes: elements of a
+// row for a lane.
+template <typename ET, bool QUADS, int kLanes, int WARPS>
+__global__ void __launch_bounds__(WARPS * kWarp) attend_join_kernel(const AttendArgs a) {
+  __shared__ int s_total[WARPS], s_before[WARPS];
+  __shared__ float s_o[WARPS][kLanes * kWarp];
+  __shared__ float2 s_ml[WARPS];
   const int lane = lane_id(), warp = threadIdx.x / kWarp, b = blockIdx.x;
   // The lengths are no output of the kernel before, which starts this one early.
   int total = 0, before = 0;  // tiles of all sequences, and of those in front of b
@@ -72,7 +71,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
   __syncthreads();
   total = before = 0;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     total += s_total[w];
     before += s_before[w];
   }
@@ -85,12 +84,13 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
   }
   await_previous_kernel();
   if (parts == 1) return;
-  const int split = parts <= 2 ? 1 : parts <= 4 ? 2 : parts <= 8 ? 4 : 8;  // warps of a head
-  const int at_once = 8 / split, sub = warp % split;
+  int split = 1;  // warps of a head: two parts or so each
+  while (split < WARPS && 2 * split < parts) split *= 2;
+  const int at_once = WARPS / split, sub = warp % split;
   for (int h0 = blockIdx.y * at_once; h0 < a.heads; h0 += gridDim.y * at_once) {
     const int h = h0 + warp / split;
-    using P = RowPart<QUADS>;
-    constexpr int kAhead = 8;  // parts on their way together
+    using P = RowPart<QUADS, kLanes>;
+    constexpr int kAhead = WARPS * kLanes > 128 ? 4 : 8;  // parts on their way together, as the registers allow
     float m = -INFINITY, sum = 0.0f, o[kLanes];
 #pragma unroll
     for (int j = 0; j < kLanes; ++j) o[j] = 0.0f;
@@ -172,6 +172,21 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a) {
   }
 }
 
+template <typename ET, bool QUADS> int launch_join(const AttendArgs& a, cudaStream_t s) {
+  // Where a head may have more than 64 parts, 32 warps share it (one sequence of 80000 tokens, six heads of 600
+  // parts: 26 us in all with eight warps, 21 with 32; 9 sequences with some 33 parts: 20 and 21).
+  const int most = a.max_tokens / kTile < a.ranges ? a.max_tokens / kTile : a.ranges;
+  const bool few = most / a.seqs > 64;
+  int y = (int)(4 * (int64_t)num_sms() / a.seqs);
+  y = y < 1 ? 1 : (y > a.heads ? a.heads : y);
+  const auto go = [&](auto kernel, int warps) { launch(kernel, dim3((unsigned)a.seqs, (unsigned)y), dim3(warps * kWarp), 0, s, a); };
+  if (a.D <= 128) {
+    if (few) go(attend_join_kernel<ET, QUADS, 4, 32>, 32); else go(attend_join_kernel<ET, QUADS, 4, 8>, 8);
+  } else {
+    if (few) go(attend_join_kernel<ET, QUADS, 8, 32>, 32); else go(attend_join_kernel<ET, QUADS, 8, 8>, 8);
+  }
+  return check_launch();
+}
 template <typename ET> int run_attend(AttendArgs& a, cudaStream_t s) {
   int rc;
   // Rows of whole 16-byte pieces on 16 bytes, and query rows and outputs on 4?
@@ -185,10 +200,7 @@ template <typename ET> int run_attend(AttendArgs& a, cudaStream_t s) {
     rc = attend_rows(a, pieces % 16 == 0, s);
   }
   if (rc != MOE_OK) return rc;
-  int y = (int)(4 * (int64_t)num_sms() / a.seqs);
-  y = y < 1 ? 1 : (y > a.heads ? a.heads : y);
-  launch(a.D % 4 == 0 ? attend_join_kernel<ET, true> : attend_join_kernel<ET, false>, dim3((unsigned)a.seqs, (unsigned)y), dim3(256), 0, s, a);
-  return check_launch();
+  return a.D % 4 == 0 ? launch_join<ET, true>(a, s) : launch_join<ET, false>(a, s);
 }
 
 int64_t slots_of(int64_t seqs, int32_t kv_heads) {

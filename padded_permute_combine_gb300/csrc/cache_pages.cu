@@ -38,61 +38,73 @@ struct WriteArgs {
   const int32_t* lengths;
   int32_t* status;
   int64_t tokens, num_pages, width;
-  int32_t seqs, kv_heads, page, row_bytes;
+  Divisor page, per_row, per_token;  // vectors of a head's row, and of all heads'
+  int32_t seqs, together;  // together: tokens that a warp takes at a time
 };
 
-// A warp takes a token: all heads of its key, then of its value.
+// Where token t goes: bytes from the cache's start, or -1.
+__device__ __forceinline__ int64_t place_of(const WriteArgs& a, int64_t t) {
+  int lo = 0, hi = a.seqs + 1;  // the last sequence that begins at or before t, if any
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (a.offsets[mid] <= t) lo = mid; else hi = mid;
+  }
+  const int64_t from = a.offsets[lo];
+  if (lo == a.seqs && from <= t) return -1;  // behind the last sequence
+  const int64_t end = lo < a.seqs ? a.offsets[lo + 1] : 0;
+  if (from > t || from < 0 || end <= t || end > a.tokens) {
+    flag_status(a.status, MOE_STATUS_BAD_BINS);
+    return -1;
+  }
+  const int64_t pos = a.lengths[lo] - (end - t);
+  const int64_t entry = pos < 0 ? 0 : a.page.of((uint32_t)pos);  // lengths have 32 bits
+  int page = -1;
+  if (pos >= 0 && entry < a.width) page = a.table[lo * a.table_stride + entry];
+  if (page < 0 || page >= a.num_pages) {
+    flag_status(a.status, MOE_STATUS_BAD_INDEX);
+    return -1;
+  }
+  return page * a.page_stride + (pos - entry * a.page.d) * a.token_stride;
+}
+
+// A warp takes a few tokens at a time: as many lanes find their places, then
+// all lanes copy their heads' vectors, one token's after the other.
 template <int VB>
 __global__ void __launch_bounds__(256) cache_write_kernel(const WriteArgs a) {
   using V = typename Vec<VB>::T;
+  constexpr int kBatchVecs = 4;
   await_previous_kernel();
   const int lane = lane_id(), warps = blockDim.x / kWarp;
-  const int per_row = a.row_bytes / VB, per_token = per_row * a.kv_heads;
+  const int per_token = (int)a.per_token.d;
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i <= a.seqs; i += blockDim.x) {
       const int64_t from = a.offsets[i], to = i < a.seqs ? a.offsets[i + 1] : a.tokens;
       if (from < 0 || from > to || (i == 0 && from != 0)) flag_status(a.status, MOE_STATUS_BAD_BINS);
     }
-  for (int64_t t = (int64_t)blockIdx.x * warps + threadIdx.x / kWarp; t < a.tokens; t += (int64_t)gridDim.x * warps) {
-    // The last sequence that begins at or before t, 32 ways at a time.
-    int lo = 0, n = a.seqs + 1;  // entries lo .. lo + n - 1 of offsets may be it
-    while (n > 1) {
-      const int step = (n + kWarp - 1) / kWarp, i = lane * step;
-      const bool le = i < n && a.offsets[lo + i] <= t;
-      const unsigned hit = __ballot_sync(0xffffffffu, le);
-      if (hit == 0) {
-        n = 0;
-        break;
+  for (int64_t t0 = ((int64_t)blockIdx.x * warps + threadIdx.x / kWarp) * a.together; t0 < a.tokens; t0 += (int64_t)gridDim.x * warps * a.together) {
+    const int n = a.tokens - t0 < a.together ? (int)(a.tokens - t0) : a.together;
+    const int64_t mine = lane < n ? place_of(a, t0 + lane) : -1;
+    for (int i0 = lane; i0 - lane < n * per_token; i0 += kBatchVecs * kWarp) {  // some vectors on their way together
+      V k[kBatchVecs], v[kBatchVecs];
+      int64_t dst[kBatchVecs];
+#pragma unroll
+      for (int e = 0; e < kBatchVecs; ++e) {
+        const int i = i0 + e * kWarp;
+        const int token = i < n * per_token ? (int)a.per_token.of(i) : 0;
+        const int64_t to = __shfl_sync(0xffffffffu, mine, token);
+        dst[e] = -1;
+        if (i >= n * per_token || to < 0) continue;
+        const int j = i - token * per_token, h = (int)a.per_row.of(j), c = (j - h * (int)a.per_row.d) * VB;
+        dst[e] = to + h * a.head_stride + c;
+        k[e] = ld_stream(reinterpret_cast<const V*>(a.k_new + (t0 + token) * a.k_row + h * a.k_head + c));
+        v[e] = ld_stream(reinterpret_cast<const V*>(a.v_new + (t0 + token) * a.v_row + h * a.v_head + c));
       }
-      const int j = (kWarp - 1 - __clz(hit)) * step;
-      lo += j;
-      n = min(step, n - j);
-    }
-    if (n == 0 || lo >= a.seqs) {
-      if (n == 0 && lane == 0) flag_status(a.status, MOE_STATUS_BAD_BINS);
-      continue;  // behind the last sequence
-    }
-    const int64_t end = a.offsets[lo + 1];
-    if (a.offsets[lo] > t || end <= t || end > a.tokens || a.offsets[lo] < 0) {
-      if (lane == 0) flag_status(a.status, MOE_STATUS_BAD_BINS);
-      continue;
-    }
-    const int64_t pos = a.lengths[lo] - (end - t);
-    const int64_t entry = pos / a.page;
-    int page = -1;
-    if (pos >= 0 && entry < a.width) page = a.table[lo * a.table_stride + entry];
-    if (page < 0 || page >= a.num_pages) {
-      if (lane == 0) flag_status(a.status, MOE_STATUS_BAD_INDEX);
-      continue;
-    }
-    const int64_t to = page * a.page_stride + (pos - entry * a.page) * a.token_stride;
-    for (int i = lane; i < per_token; i += kWarp) {
-      const int h = i / per_row, c = i - h * per_row;
-      const int64_t dst = to + h * a.head_stride + (int64_t)c * VB;
-      const V k = ld_stream(reinterpret_cast<const V*>(a.k_new + t * a.k_row + h * a.k_head + (int64_t)c * VB));
-      const V v = ld_stream(reinterpret_cast<const V*>(a.v_new + t * a.v_row + h * a.v_head + (int64_t)c * VB));
-      *reinterpret_cast<V*>(a.k + dst) = k;
-      *reinterpret_cast<V*>(a.v + dst) = v;
+#pragma unroll
+      for (int e = 0; e < kBatchVecs; ++e) {
+        if (dst[e] < 0) continue;
+        *reinterpret_cast<V*>(a.k + dst[e]) = k[e];
+        *reinterpret_cast<V*>(a.v + dst[e]) = v[e];
+      }
     }
   }
 }
@@ -602,20 +614,34 @@ extern "C" int moe_cache_write(const moe_kv_cache* cache, const moe_heads* k, co
   a.num_pages = cache->num_pages;
   a.width = table_width;
   a.seqs = (int32_t)num_seqs;
-  a.kv_heads = cache->num_kv_heads;
-  a.page = cache->page_size;
-  a.row_bytes = cache->head_dim * eb;
+  a.page = Divisor((uint32_t)cache->page_size);
+  // Heads that lie side by side on both sides are one row.
+  int64_t row_bytes = (int64_t)cache->head_dim * eb, rows = cache->num_kv_heads;
+  if (rows > 1 && a.head_stride == row_bytes && a.k_head == row_bytes && a.v_head == row_bytes) {
+    row_bytes *= rows;
+    rows = 1;
+  }
+  if (rows == 1) a.head_stride = a.k_head = a.v_head = 0;
   // Vectors as wide as every row's start and length allow.
-  const int64_t all = a.row_bytes | a.page_stride | a.token_stride | a.head_stride | a.k_row | a.k_head | a.v_row | a.v_head |
+  const int64_t all = row_bytes | a.page_stride | a.token_stride | a.head_stride | a.k_row | a.k_head | a.v_row | a.v_head |
                       (int64_t)(reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
                                 reinterpret_cast<uintptr_t>(a.k_new) | reinterpret_cast<uintptr_t>(a.v_new));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int64_t ctas = (num_tokens + 7) / 8;
-  const auto go = [&](auto kernel) { launch(kernel, dim3((unsigned)(ctas < 65535 ? ctas : 65535)), dim3(256), 0, s, a); };
-  if (all % 16 == 0) go(cache_write_kernel<16>);
-  else if (all % 8 == 0) go(cache_write_kernel<8>);
-  else if (all % 4 == 0) go(cache_write_kernel<4>);
-  else go(cache_write_kernel<2>);
+  const auto go = [&](auto kernel, int vb) {
+    a.per_row = Divisor((uint32_t)(row_bytes / vb));
+    a.per_token = Divisor((uint32_t)(row_bytes / vb * rows));
+    // Up to 256 vectors at a time, eight tokens at most, and 32 warps' work for every SM first (100000 tokens of
+    // two heads of 64: 51 us with one token at a time).
+    int64_t together = 256 / a.per_token.d, each = num_tokens / ((int64_t)num_sms() * 32);
+    together = together < each ? together : each;
+    a.together = (int32_t)(together < 1 ? 1 : together > 8 ? 8 : together);
+    const int64_t ctas = (num_tokens + 8 * a.together - 1) / (8 * a.together);
+    launch(kernel, dim3((unsigned)(ctas < 65535 ? ctas : 65535)), dim3(256), 0, s, a);
+  };
+  if (all % 16 == 0) go(cache_write_kernel<16>, 16);
+  else if (all % 8 == 0) go(cache_write_kernel<8>, 8);
+  else if (all % 4 == 0) go(cache_write_kernel<4>, 4);
+  else go(cache_write_kernel<2>, 2);
   return check_launch();
 }
 
