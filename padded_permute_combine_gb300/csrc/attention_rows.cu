@@ -13,7 +13,8 @@ struct RowPieces {
   int pieces, pitch, swap;
   __host__ __device__ explicit RowPieces(int D) : pieces((D + 3) / 4), pitch((pieces + 3) / 4 * 4), swap(pitch % 8 == 0 ? 4 : 0) {}
 };
-constexpr int kSmWarps = 8;
+// Warps of an SM, as registers and shared memory allow: twelve with rows of up to some 80 elements.
+template <int GM, int NC> constexpr int kSmWarps = GM <= 4 && NC == 1 ? 12 : 8;
 constexpr int kSlots = 3;  // of a warp's ring, a tile's keys or values each
 
 __device__ __forceinline__ uint64_t pair(float a, float b) { return f2_pack(__float_as_uint(a), __float_as_uint(b)); }
@@ -26,9 +27,9 @@ __device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) { return f2_pac
 // instruction (fma.f32x2). VB: bytes of an asynchronous copy, 4 where rows are
 // off 16.
 template <int GM, int NC, int VB>
-__global__ void __launch_bounds__(kSmWarps * kWarp, 1) attend_rows_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(kSmWarps<GM, NC> * kWarp, 1) attend_rows_kernel(const AttendArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ int s_prefix[kSmWarps * kWarp], s_warp[kSmWarps];
+  __shared__ int s_prefix[kSmWarps<GM, NC> * kWarp], s_warp[kSmWarps<GM, NC>];
   await_previous_kernel();
   start_next_kernel();
   const int lane = lane_id(), warp = threadIdx.x / kWarp, warps = blockDim.x / kWarp;
@@ -251,7 +252,7 @@ template <int GM, int NC, int VB> int launch_rows(AttendArgs& a, cudaStream_t s)
   if (!allow_smem(k, raised)) return MOE_ERR_CUDA;
   const RowPieces row(a.D);
   const int bytes = kSlots * kTile * row.pitch * 16 + GM * row.pitch * 16 + GM * kTile * 8;  // of a warp
-  const int fit = 224 * 1024 / bytes, warps = fit < kSmWarps ? fit : kSmWarps;
+  const int fit = 224 * 1024 / bytes, warps = fit < kSmWarps<GM, NC> ? fit : kSmWarps<GM, NC>;
   cut(a, GM, warps);
   launch(k, dim3(ctas_of(a, warps)), dim3(warps * kWarp), (size_t)warps * bytes, s, a);
   return check_launch();
