@@ -29,11 +29,11 @@ __device__ __forceinline__ float ex2(float x) {
 // rows off 16 bytes.
 template <int DP, int MT, bool SHIFT, int TEAM> struct Mma {
   static constexpr int kHeads = MT == 0 ? 8 : 16 * MT, kTiles = MT == 0 ? 1 : MT;
-  static constexpr int kWarps = DP == 128 ? 8 : (SHIFT ? 12 : 16) / TEAM * TEAM;
+  static constexpr int kWarps = DP == 128 ? (MT == 0 ? 8 : 12) : (SHIFT ? 12 : 16) / TEAM * TEAM;
   // Pieces of a row are swizzled by its number, or rows are one piece further apart: no two rows' pieces in one bank.
   static constexpr int kPitch = DP * 2 + (SHIFT ? 16 : 0);
   static constexpr int kStageBytes = 2 * kTile * kPitch;
-  static constexpr int kStages = 3;  // 162 to 192 KB an SM
+  static constexpr int kStages = DP == 128 && MT > 0 ? 2 : 3;  // 162 to 192 KB an SM
   static constexpr int kScores = 4 * (MT == 0 ? 1 : 2 * kTiles);  // of a lane
   static constexpr size_t kRings = (size_t)kWarps * kStages * kStageBytes;
   static constexpr size_t kSmem = kRings + (TEAM > 1 ? (size_t)2 * kWarps * kWarp * kScores * 4 : 0);
