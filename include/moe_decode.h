@@ -83,7 +83,9 @@ typedef struct moe_heads {
  *          the size is that of the current device (0 for sizes that the call refuses).
  * Sums and the softmax's statistics are fp32, out is rounded once. bf16 caches
  * run on the tensor cores with the probabilities as sums of two bf16 numbers
- * (16 significant bits). A sequence's result depends on the other sequences'
+ * (16 significant bits). A NaN or an infinite score among a head's makes its
+ * out and lse NaN, as the formulas say; an infinite value makes its element of
+ * out infinite or NaN. A sequence's result depends on the other sequences'
  * lengths in the order of its sums alone; repeated calls give the same bits.
  * head_dim <= MOE_ATTENTION_MAX_DIM, num_seqs * table_width * page_size < 2^34
  * and table_width * page_size < 2^31, else MOE_ERR_UNSUPPORTED.

@@ -16,7 +16,6 @@ namespace moe {
 
 constexpr int kTile = 16;      // tokens of a tile, the unit of the ranges
 constexpr int kMostWarps = 16; // of an SM, which has one CTA
-constexpr int kMinTiles = 1;   // of a range, where there are fewer tiles than warps
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -38,7 +37,7 @@ struct AttendArgs {
   int32_t* status;
   Divisor page;
   int64_t num_pages, window;
-  int32_t seqs, width, heads, kv_heads, group, D;
+  int32_t seqs, heads, kv_heads, group, D;
   int32_t parts;       // pieces of a group, of kHeads query heads each
   int32_t ranges;      // at most
   int32_t max_tokens;  // table width * page size
@@ -56,9 +55,8 @@ __device__ __forceinline__ int tiles_of(const AttendArgs& a, int b) {
   span_of(a, b, first, n);
   return (n - first + kTile - 1) / kTile;
 }
-__device__ __forceinline__ int ranges_of(const AttendArgs& a, int total) {
-  const int most = total / kMinTiles;
-  return most < a.ranges ? (most < 1 ? 1 : most) : a.ranges;
+__device__ __forceinline__ int ranges_of(const AttendArgs& a, int total) {  // total > 0
+  return total < a.ranges ? total : a.ranges;
 }
 __device__ __forceinline__ int range_begin(int r, int ranges, int total) { return (int)((int64_t)r * total / ranges); }
 // The range that tile x lies in: the last r whose begin is not behind x.
@@ -93,15 +91,21 @@ struct Cursor {
     span_of(a, b, first, n);
     tiles = (n - first + kTile - 1) / kTile;
   }
-  __device__ __forceinline__ void next(const AttendArgs& a) {  // there is a next tile
+  // There is a next tile. (The bounds on b keep the steps inside the table should lengths change meanwhile.)
+  __device__ __forceinline__ void next(const AttendArgs& a) {
     if (++tile < tiles) return;
     tile = 0;
     do {
-      ++b;
+      if (b < a.seqs - 1) ++b;
       enter(a);
-    } while (tiles == 0);
+    } while (tiles == 0 && b < a.seqs - 1);
   }
 };
+
+// From a maximum (in units of log 2) and a sum: what the sums are multiplied by, and
+// the log sum. A row without positions has sum 0; a NaN stays one.
+__device__ __forceinline__ float share_of(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
+__device__ __forceinline__ float log_sum_of(float m, float sum) { return sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2; }
 
 // The joining kernel may start: it waits for this one before it reads what it left.
 __device__ __forceinline__ void start_next_kernel() { asm volatile("griddepcontrol.launch_dependents;"); }
@@ -135,7 +139,7 @@ __device__ __forceinline__ Cursor find_tile(const AttendArgs& a, const int* pref
   c.b = lo * chunk;
   c.tile = x - prefix[lo];
   c.enter(a);
-  while (c.tile >= c.tiles) {
+  while (c.tile >= c.tiles && c.b < a.seqs - 1) {
     c.tile -= c.tiles;
     ++c.b;
     c.enter(a);

@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(WARPS * kWarp) attend_join_kernel(const Attend
     }
     if (h >= a.heads) continue;
     const int64_t head = (int64_t)b * a.heads + h;
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = share_of(sum);
 #pragma unroll
     for (int j = 0; j < kLanes; ++j) {
       const int d = P::place(j);
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(WARPS * kWarp) attend_join_kernel(const Attend
         static_cast<__nv_bfloat16*>(a.out)[head * D + d] = __float2bfloat16_rn(o[j] * inv);
       }
     }
-    if (lane == 0 && a.lse != nullptr) a.lse[head] = sum > 0.0f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+    if (lane == 0 && a.lse != nullptr) a.lse[head] = log_sum_of(m, sum);
   }
 }
 
@@ -284,7 +284,6 @@ extern "C" int moe_attention_decode(const moe_kv_cache* cache, const moe_heads* 
   a.num_pages = cache->num_pages;
   a.window = window;
   a.seqs = (int32_t)num_seqs;
-  a.width = (int32_t)table_width;
   a.heads = num_heads;
   a.kv_heads = cache->num_kv_heads;
   a.group = num_heads / cache->num_kv_heads;

@@ -25,16 +25,14 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // Sizes of a variant: DP elements of a row for a warp (64 or 128), TEAM warps that
-// share the row, MT tiles of 16 query heads (0: eight heads in one), SHIFT for
-// rows off 16 bytes.
-template <int DP, int MT, bool SHIFT, int TEAM> struct Mma {
-  static constexpr int kHeads = MT == 0 ? 8 : 16 * MT, kTiles = MT == 0 ? 1 : MT;
-  static constexpr int kWarps = DP == 128 ? (MT == 0 ? 8 : 12) : (SHIFT ? 12 : 16) / TEAM * TEAM;
+// share the row, HEADS query heads at a time (8 or 16), SHIFT for rows off 16 bytes.
+template <int DP, int HEADS, bool SHIFT, int TEAM> struct Mma {
+  static constexpr int kWarps = DP == 128 ? (HEADS == 8 ? 8 : 12) : (SHIFT ? 12 : 16) / TEAM * TEAM;
   // Pieces of a row are swizzled by its number, or rows are one piece further apart: no two rows' pieces in one bank.
   static constexpr int kPitch = DP * 2 + (SHIFT ? 16 : 0);
   static constexpr int kStageBytes = 2 * kTile * kPitch;
-  static constexpr int kStages = DP == 128 && MT > 0 ? 2 : 3;  // 162 to 192 KB an SM
-  static constexpr int kScores = 4 * (MT == 0 ? 1 : 2 * kTiles);  // of a lane
+  static constexpr int kStages = DP == 128 && HEADS == 16 ? 2 : 3;  // 162 to 192 KB an SM
+  static constexpr int kScores = HEADS / 2;  // of a lane
   static constexpr size_t kRings = (size_t)kWarps * kStages * kStageBytes;
   static constexpr size_t kSmem = kRings + (TEAM > 1 ? (size_t)2 * kWarps * kWarp * kScores * 4 : 0);
 };
@@ -53,10 +51,10 @@ template <int DP, int MT, bool SHIFT, int TEAM> struct Mma {
 // team share the rows, 64 elements each: they copy, multiply and sum their own
 // columns, twice as many warps on an SM, and meet once a tile to add up the
 // scores, of which each has a part.
-template <int DP, int MT, bool SHIFT, int TEAM>
-__global__ void __launch_bounds__(Mma<DP, MT, SHIFT, TEAM>::kWarps * kWarp, 1) attend_mma_kernel(const AttendArgs a) {
-  using S = Mma<DP, MT, SHIFT, TEAM>;
-  constexpr int kWarps = S::kWarps, kStages = S::kStages, kTiles = S::kTiles, kPitch = S::kPitch;
+template <int DP, int HEADS, bool SHIFT, int TEAM>
+__global__ void __launch_bounds__(Mma<DP, HEADS, SHIFT, TEAM>::kWarps * kWarp, 1) attend_mma_kernel(const AttendArgs a) {
+  using S = Mma<DP, HEADS, SHIFT, TEAM>;
+  constexpr int kWarps = S::kWarps, kStages = S::kStages, kPitch = S::kPitch;
   constexpr int kTurns = DP / 32;  // of four lanes over the 16-byte pieces of a row
   constexpr int kSteps = DP / 16;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -74,7 +72,7 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT, TEAM>::kWarps * kWarp, 1) a
   const int col0 = rank * DP, D = min(DP, a.D - col0);  // the warp's columns
   char* const keys = a.k + 2 * col0;
   char* const values = a.v + 2 * col0;
-  const int h0 = kv * a.group + part * S::kHeads, heads = min(S::kHeads, a.group - part * S::kHeads);
+  const int h0 = kv * a.group + part * HEADS, heads = min(HEADS, a.group - part * HEADS);
   const uint32_t ring = smem_u32(smem) + warp * kStages * S::kStageBytes;
   if (SHIFT || D < DP) {  // pieces behind D are never copied, and have to be numbers
     uint4* z = reinterpret_cast<uint4*>(smem + (size_t)warp * kStages * S::kStageBytes);
@@ -237,8 +235,8 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT, TEAM>::kWarps * kWarp, 1) a
     }
   }
 
-  uint32_t q[kTiles][kSteps][4];
-  float o[kTiles][DP / 8][4], m[kTiles][2], l[kTiles][2];
+  uint32_t q[kSteps][4];
+  float o[DP / 8][4], m[2], l[2];
   const int g = lane >> 2, t = lane & 3;
   const int mi = lane >> 3, lr = lane & 7;
   const int swizzle = SHIFT ? 0 : lr;
@@ -251,31 +249,28 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT, TEAM>::kWarps * kWarp, 1) a
       first_tile = at.tile;
       const char* rows = a.q + at.b * a.q_row + 2 * col0;
 #pragma unroll
-      for (int u = 0; u < kTiles; ++u) {
+      for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int h = u * 16 + g + (e & 1) * 8, d = ks * 16 + t * 2 + (e >> 1) * 8;
-            const char* from = rows + (h0 + h) * a.q_head + d * 2;
-            uint32_t x = 0;
-            if (!((MT == 0 && (e & 1)) || h >= heads || d >= D)) {
-              if constexpr (SHIFT) {
-                x = __ldg(reinterpret_cast<const unsigned short*>(from));
-                if (d + 1 < D) x |= (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(from) + 1) << 16;
-              } else {
-                x = __ldg(reinterpret_cast<const unsigned*>(from));
-              }
+        for (int e = 0; e < 4; ++e) {
+          const int h = g + (e & 1) * 8, d = ks * 16 + t * 2 + (e >> 1) * 8;
+          const char* from = rows + (h0 + h) * a.q_head + d * 2;
+          uint32_t x = 0;
+          if (!((HEADS == 8 && (e & 1)) || h >= heads || d >= D)) {
+            if constexpr (SHIFT) {
+              x = __ldg(reinterpret_cast<const unsigned short*>(from));
+              if (d + 1 < D) x |= (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(from) + 1) << 16;
+            } else {
+              x = __ldg(reinterpret_cast<const unsigned*>(from));
             }
-            q[u][ks][e] = x;
           }
+          q[ks][e] = x;
+        }
 #pragma unroll
-        for (int n = 0; n < DP / 8; ++n)
+      for (int n = 0; n < DP / 8; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[u][n][e] = 0.0f;
-        m[u][0] = m[u][1] = -INFINITY;
-        l[u][0] = l[u][1] = 0.0f;
-      }
+        for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
+      m[0] = m[1] = -INFINITY;
+      l[0] = l[1] = 0.0f;
     }
     cp_wait<kStages - 2>();
     __syncwarp();
@@ -285,23 +280,18 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT, TEAM>::kWarps * kWarp, 1) a
     issue(true);  // into the stage that the previous tile left
     if constexpr (SHIFT) align(stage);
     const uint32_t base = ring + stage * S::kStageBytes;
-    float s[kTiles][2][4];
+    float s[2][4];
 #pragma unroll
-    for (int u = 0; u < kTiles; ++u)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[u][n][e] = 0.0f;
+      for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
 #pragma unroll
     for (int ks = 0; ks < kSteps; ++ks) {
       if (SHIFT && ks * 16 >= D) continue;
       uint32_t b[4];
       ldmatrix(b, base + k_at + (((ks * 2 + (mi & 1)) ^ swizzle) * 16));
-#pragma unroll
-      for (int u = 0; u < kTiles; ++u) {
-        mma(s[u][0], q[u][ks], b[0], b[1]);
-        mma(s[u][1], q[u][ks], b[2], b[3]);
-      }
+      mma(s[0], q[ks], b[0], b[1]);
+      mma(s[1], q[ks], b[2], b[3]);
     }
     if constexpr (TEAM > 1) {
       // The scores' parts, added up in the same order by every warp. Two places in turn: who writes one again
@@ -309,7 +299,7 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT, TEAM>::kWarps * kWarp, 1) a
       float* mine = reinterpret_cast<float*>(smem + S::kRings) + ((i & 1) * kWarps + team * TEAM) * kWarp * S::kScores + lane * 4;
       float part[S::kScores];
 #pragma unroll
-      for (int k = 0; k < S::kScores; ++k) part[k] = MT == 0 ? s[0][k / 2][k % 2] : s[k / 8][k / 4 % 2][k % 4];
+      for (int k = 0; k < S::kScores; ++k) part[k] = HEADS == 8 ? s[k / 2][k % 2] : s[k / 4 % 2][k % 4];
 #pragma unroll
       for (int k = 0; k < S::kScores; k += 4)
         *reinterpret_cast<float4*>(mine + rank * kWarp * S::kScores + k * kWarp) = make_float4(part[k], part[k + 1], part[k + 2], part[k + 3]);
@@ -331,61 +321,58 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT, TEAM>::kWarps * kWarp, 1) a
         part[k + 3] = sum.w;
       }
 #pragma unroll
-      for (int k = 0; k < S::kScores; ++k) (MT == 0 ? s[0][k / 2][k % 2] : s[k / 8][k / 4 % 2][k % 4]) = part[k];
+      for (int k = 0; k < S::kScores; ++k) (HEADS == 8 ? s[k / 2][k % 2] : s[k / 4 % 2][k % 4]) = part[k];
     }
-    uint32_t hi[kTiles][4], lo2[kTiles][4];
+    uint32_t hi[4], lo2[4];
+    constexpr int kRows = HEADS == 8 ? 1 : 2;  // rows g and g + 8
+    float keep[2] = {1.0f, 1.0f};
+    bool moved = false;
 #pragma unroll
-    for (int u = 0; u < kTiles; ++u) {
-      constexpr int kRows = MT == 0 ? 1 : 2;  // rows g and g + 8
-      float keep[2] = {1.0f, 1.0f};
-      bool moved = false;
+    for (int w = 0; w < kRows; ++w) {
+      float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kRows; ++w) {
-        float top = -INFINITY;
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float& x = s[u][n][2 * w + e];
-            x *= a.scale;
-            if (!all && !(there >> (n * 8 + t * 2 + e) & 1)) x = -INFINITY;
-            top = fmaxf(top, x);
-          }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float now = fmaxf(m[u][w], top), from = now == -INFINITY ? 0.0f : now;
-        if (now > m[u][w]) {
-          moved = true;
-          keep[w] = ex2(m[u][w] - from);
-          m[u][w] = now;
+        for (int e = 0; e < 2; ++e) {
+          float& x = s[n][2 * w + e];
+          x *= a.scale;
+          if (!all && !(there >> (n * 8 + t * 2 + e) & 1)) x = -INFINITY;
+          top = fmaxf(top, x);
         }
-        float sum = 0.0f;
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float p0 = ex2(s[u][n][2 * w] - from), p1 = ex2(s[u][n][2 * w + 1] - from);
-          sum += p0 + p1;
-          const uint32_t h = pack_bf16x2(p0, p1);
-          const uint32_t rest = pack_bf16x2(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u));
-          if constexpr (MT == 0) {
-            hi[u][2 * n] = h;
-            hi[u][2 * n + 1] = rest;
-          } else {
-            hi[u][2 * n + w] = h;
-            lo2[u][2 * n + w] = rest;
-          }
-        }
-        l[u][w] = l[u][w] * keep[w] + sum;
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float now = fmaxf(m[w], top), from = now == -INFINITY ? 0.0f : now;
+      if (now > m[w]) {
+        moved = true;
+        keep[w] = ex2(m[w] - from);
+        m[w] = now;
       }
-      if (__any_sync(0xffffffffu, moved)) {
-        if constexpr (MT == 0) keep[1] = keep[0];
+      float sum = 0.0f;
 #pragma unroll
-        for (int n = 0; n < DP / 8; ++n) {
-          if (SHIFT && n * 8 >= D) continue;
-          o[u][n][0] *= keep[0];
-          o[u][n][1] *= keep[0];
-          o[u][n][2] *= keep[1];
-          o[u][n][3] *= keep[1];
+      for (int n = 0; n < 2; ++n) {
+        const float p0 = ex2(s[n][2 * w] - from), p1 = ex2(s[n][2 * w + 1] - from);
+        sum += p0 + p1;
+        const uint32_t h = pack_bf16x2(p0, p1);
+        const uint32_t rest = pack_bf16x2(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u));
+        if constexpr (HEADS == 8) {
+          hi[2 * n] = h;
+          hi[2 * n + 1] = rest;
+        } else {
+          hi[2 * n + w] = h;
+          lo2[2 * n + w] = rest;
         }
+      }
+      l[w] = l[w] * keep[w] + sum;
+    }
+    if (__any_sync(0xffffffffu, moved)) {
+      if constexpr (HEADS == 8) keep[1] = keep[0];
+#pragma unroll
+      for (int n = 0; n < DP / 8; ++n) {
+        if (SHIFT && n * 8 >= D) continue;
+        o[n][0] *= keep[0];
+        o[n][1] *= keep[0];
+        o[n][2] *= keep[1];
+        o[n][3] *= keep[1];
       }
     }
 #pragma unroll
@@ -393,79 +380,74 @@ __global__ void __launch_bounds__(Mma<DP, MT, SHIFT, TEAM>::kWarps * kWarp, 1) a
       if (SHIFT && c * 16 >= D) continue;
       uint32_t b[4];
       ldmatrix_trans(b, base + v_at + (((c * 2 + (mi >> 1)) ^ swizzle) * 16));
-#pragma unroll
-      for (int u = 0; u < kTiles; ++u) {
-        mma(o[u][2 * c], hi[u], b[0], b[1]);
-        mma(o[u][2 * c + 1], hi[u], b[2], b[3]);
-        if constexpr (MT > 0) {
-          mma(o[u][2 * c], lo2[u], b[0], b[1]);
-          mma(o[u][2 * c + 1], lo2[u], b[2], b[3]);
-        }
+      mma(o[2 * c], hi, b[0], b[1]);
+      mma(o[2 * c + 1], hi, b[2], b[3]);
+      if constexpr (HEADS == 16) {
+        mma(o[2 * c], lo2, b[0], b[1]);
+        mma(o[2 * c + 1], lo2, b[2], b[3]);
       }
     }
     const bool last = at.tile == at.tiles - 1;
     if (last || i == count - 1) {
       const bool whole = last && first_tile == 0;
 #pragma unroll
-      for (int u = 0; u < kTiles; ++u)
+      for (int w = 0; w < kRows; ++w) {
+        float sum = l[w];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const int h = g + w * 8;
+        if (h >= heads) continue;
+        const int64_t head = (whole ? (int64_t)at.b : (int64_t)r + at.b) * a.heads + h0 + h;
+        const float inv = share_of(sum);
 #pragma unroll
-        for (int w = 0; w < (MT == 0 ? 1 : 2); ++w) {
-          float sum = l[u][w];
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          const int h = u * 16 + g + w * 8;
-          if (h >= heads) continue;
-          const int64_t head = (whole ? (int64_t)at.b : (int64_t)r + at.b) * a.heads + h0 + h;
-          const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-#pragma unroll
-          for (int n = 0; n < DP / 8; ++n) {
-            const int d = n * 8 + t * 2;
-            if (d >= D) continue;
-            float x = o[u][n][2 * w], y = o[u][n][2 * w + 1];
-            if constexpr (MT == 0) {
-              x += o[u][n][2];
-              y += o[u][n][3];
-            }
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + head * a.D + col0 + d;
-            if constexpr (SHIFT) {  // D may be odd
-              if (whole) {
-                out[0] = __float2bfloat16_rn(x * inv);
-                if (d + 1 < D) out[1] = __float2bfloat16_rn(y * inv);
-              } else {
-                a.part_o[head * a.D + col0 + d] = x;
-                if (d + 1 < D) a.part_o[head * a.D + col0 + d + 1] = y;
-              }
-            } else if (whole) {
-              *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(x * inv, y * inv);
-            } else {
-              *reinterpret_cast<float2*>(a.part_o + head * a.D + col0 + d) = make_float2(x, y);
-            }
+        for (int n = 0; n < DP / 8; ++n) {
+          const int d = n * 8 + t * 2;
+          if (d >= D) continue;
+          float x = o[n][2 * w], y = o[n][2 * w + 1];
+          if constexpr (HEADS == 8) {
+            x += o[n][2];
+            y += o[n][3];
           }
-          if (t == 0 && rank == 0) {
-            if (!whole) {
-              a.part_ml[head] = make_float2(m[u][w], sum);
-            } else if (a.lse != nullptr) {
-              a.lse[head] = sum > 0.0f ? (m[u][w] + log2f(sum)) * kLn2 : -INFINITY;
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + head * a.D + col0 + d;
+          if constexpr (SHIFT) {  // D may be odd
+            if (whole) {
+              out[0] = __float2bfloat16_rn(x * inv);
+              if (d + 1 < D) out[1] = __float2bfloat16_rn(y * inv);
+            } else {
+              a.part_o[head * a.D + col0 + d] = x;
+              if (d + 1 < D) a.part_o[head * a.D + col0 + d + 1] = y;
             }
+          } else if (whole) {
+            *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(x * inv, y * inv);
+          } else {
+            *reinterpret_cast<float2*>(a.part_o + head * a.D + col0 + d) = make_float2(x, y);
           }
         }
+        if (t == 0 && rank == 0) {
+          if (!whole) {
+            a.part_ml[head] = make_float2(m[w], sum);
+          } else if (a.lse != nullptr) {
+            a.lse[head] = log_sum_of(m[w], sum);
+          }
+        }
+      }
       fresh = true;
     }
     if (i + 1 < count) at.next(a);
   }
 }
 
-template <int DP, int MT, bool SHIFT, int TEAM> int launch_mma(AttendArgs& a, cudaStream_t s) {
-  using S = Mma<DP, MT, SHIFT, TEAM>;
+template <int DP, int HEADS, bool SHIFT, int TEAM> int launch_mma(AttendArgs& a, cudaStream_t s) {
+  using S = Mma<DP, HEADS, SHIFT, TEAM>;
   static std::atomic<bool> raised[kSmemDevices];
-  auto k = attend_mma_kernel<DP, MT, SHIFT, TEAM>;
+  auto k = attend_mma_kernel<DP, HEADS, SHIFT, TEAM>;
   if (!allow_smem(k, raised)) return MOE_ERR_CUDA;
-  cut(a, S::kHeads, S::kWarps / TEAM);
+  cut(a, HEADS, S::kWarps / TEAM);
   launch(k, dim3(ctas_of(a, S::kWarps / TEAM)), dim3(S::kWarps * kWarp), S::kSmem, s, a);
   return check_launch();
 }
 template <int DP, bool SHIFT, int TEAM> int launch_mma_heads(AttendArgs& a, cudaStream_t s) {
-  return a.group <= 8 ? launch_mma<DP, 0, SHIFT, TEAM>(a, s) : launch_mma<DP, 1, SHIFT, TEAM>(a, s);
+  return a.group <= 8 ? launch_mma<DP, 8, SHIFT, TEAM>(a, s) : launch_mma<DP, 16, SHIFT, TEAM>(a, s);
 }
 template <bool SHIFT> int launch_mma_dim(AttendArgs& a, cudaStream_t s) {
   // Aligned rows of up to 128 elements are one warp's: 64 ragged sequences 147 us, with teams of two 151.

@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kSmWarps<GM, NC> * kWarp, 1) attend_rows_kerne
         for (int d = 4; d < kWarp; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if (h >= heads) continue;
         const int64_t head = (whole ? (int64_t)at.b : (int64_t)r + at.b) * a.heads + h0 + h;
-        const float inv = whole ? (sum > 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
+        const float inv = whole ? share_of(sum) : 1.0f;
         float* to = (whole ? static_cast<float*>(a.out) : a.part_o) + head * D;
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kSmWarps<GM, NC> * kWarp, 1) attend_rows_kerne
           if (!whole) {
             a.part_ml[head] = make_float2(m[h], sum);
           } else if (a.lse != nullptr) {
-            a.lse[head] = sum > 0.0f ? (m[h] + log2f(sum)) * kLn2 : -INFINITY;
+            a.lse[head] = log_sum_of(m[h], sum);
           }
         }
       }

@@ -192,6 +192,20 @@ def test_extreme_scores():
         assert bool(((out[1].double() - want).abs() <= 2.0 ** -7 * (1 + want.abs())).all()) and bool(torch.isfinite(lse).all())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dim", [64, 128, 77, 200])
+@pytest.mark.parametrize("lengths", [[40, 200], [9000, 200]])
+def test_nan_stays_with_its_row(dtype, dim, lengths):
+    k, v, table, dev = make(lengths, 16, 2, dim, dtype)
+    q = rand(2, 8, dim, dtype=dtype)
+    want = p.moe_attention_decode(q, k, v, table, dev)
+    k[table[0, 1].long(), 3, 0] = math.nan  # a key of the first sequence's first kv head
+    out, lse = p.moe_attention_decode(q, k, v, table, dev)
+    assert bool(torch.isnan(out[0, :4]).all()) and bool(torch.isnan(lse[0, :4]).all())
+    assert torch.equal(out[0, 4:], want[0][0, 4:]) and torch.equal(lse[0, 4:], want[1][0, 4:])
+    assert torch.equal(out[1], want[0][1]) and torch.equal(lse[1], want[1][1])
+
+
 def test_bad_pages_and_lengths_are_flagged_and_left_out():
     lengths = [40, 64, 33]
     k, v, table, _ = make(lengths, 16, 2, 64, BF16)
