@@ -210,6 +210,10 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int byt
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
+template <int BYTES> __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int bytes) {
+  if constexpr (BYTES == 16) cp_async16(dst, src, bytes); else cp_async4(dst, src, bytes);
+}
+
 // Ranges of the line for a kernel of `warps` warps an SM that takes kHeads query heads at a time.
 inline void cut(AttendArgs& a, int heads_at_once, int warps) {
   a.parts = (a.group + heads_at_once - 1) / heads_at_once;
@@ -222,6 +226,8 @@ inline unsigned ctas_of(const AttendArgs& a, int warps) {
 
 // The first kernels (they set a.parts and a.ranges, which the joining kernel needs too).
 int attend_rows(AttendArgs& a, bool pieces, cudaStream_t s);  // fp32; pieces: rows of 16-byte pieces on 16 bytes
-int attend_mma(AttendArgs& a, bool pieces, cudaStream_t s);   // bf16; pieces: that too, and query rows and outputs on 4
+int attend_mma_16(AttendArgs& a, cudaStream_t s);  // bf16 rows of 16-byte pieces on 16 bytes, and
+int attend_mma_4(AttendArgs& a, cudaStream_t s);   // rows of 4-byte words on 4; query rows and outputs on 4 for both
+int attend_mma_2(AttendArgs& a, cudaStream_t s);   // any bf16 rows
 
 }  // namespace moe

@@ -189,13 +189,13 @@ template <typename ET, bool QUADS> int launch_join(const AttendArgs& a, cudaStre
 }
 template <typename ET> int run_attend(AttendArgs& a, cudaStream_t s) {
   int rc;
-  // Rows of whole 16-byte pieces on 16 bytes, and query rows and outputs on 4?
+  // What all rows are aligned to and multiples of, and query rows and outputs.
   const int64_t pieces = a.page_stride | a.token_stride | a.head_stride | (int64_t)(reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) |
                          (int64_t)(reinterpret_cast<uintptr_t>(a.k_new) | reinterpret_cast<uintptr_t>(a.v_new)) | a.kn_row | a.kn_head |
                          a.vn_row | a.vn_head | a.D * (int64_t)sizeof(ET);
   const int64_t pairs = a.q_row | a.q_head | (int64_t)(reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.out));
   if constexpr (sizeof(ET) == 2) {
-    rc = attend_mma(a, pieces % 16 == 0 && pairs % 4 == 0, s);
+    rc = pairs % 4 != 0 || pieces % 4 != 0 ? attend_mma_2(a, s) : pieces % 16 != 0 ? attend_mma_4(a, s) : attend_mma_16(a, s);
   } else {
     rc = attend_rows(a, pieces % 16 == 0, s);
   }
