@@ -52,9 +52,9 @@ __global__ void __launch_bounds__(kSmWarps<GM, NC> * kWarp, 1) attend_rows_kerne
 
   // Copies of a tile's keys, then of its values: four lanes a row (rows r0 and
   // r0 + 8), so that a copy's addresses are a register and a constant.
-  constexpr int kTurns = VB == 16 ? NC * 8 : NC * 32;  // of the four lanes over a row
+  constexpr int kTurns = NC * 8;  // of the four lanes over a row
   Cursor at = in;
-  const int r0 = lane >> 2, part4 = lane & 3, pieces = VB == 16 ? row.pieces : D;
+  const int r0 = lane >> 2, part4 = lane & 3, pieces = row.pieces;
   int issued = 0, slot_in = 0, page[2] = {page_entry(a, in, r0), page_entry(a, in, r0 + 8)}, bytes[2];
   unsigned there[2];  // rows of the tile issued last that are there, four equal bits each
   const char* from[2];
@@ -80,15 +80,25 @@ __global__ void __launch_bounds__(kSmWarps<GM, NC> * kWarp, 1) attend_rows_kerne
           if (part == 0)
             for (int d = part4; d < D; d += 4) reinterpret_cast<float*>(const_cast<char*>(kept))[d] = reinterpret_cast<const float*>(src)[d];
         }
-        src += part4 * VB;
-        const uint32_t to = base + 8 * w * row.pitch * 16, even = to + flip, odd = to - flip;  // 64 bytes on in every other 64
+        if constexpr (VB == 16) {
+          src += part4 * VB;
+          const uint32_t to = base + 8 * w * row.pitch * 16, even = to + flip, odd = to - flip;  // 64 bytes on in every other 64
 #pragma unroll
-        for (int i = 0; i < kTurns; ++i) {
-          if (part4 + 4 * i >= pieces) continue;
-          if constexpr (VB == 16) {
+          for (int i = 0; i < kTurns; ++i) {
+            if (part4 + 4 * i >= pieces) continue;
             cp_async16((i & 1 ? odd : even) + i * 64, src + i * 64, bytes[w]);
-          } else {
-            cp_async4((i & 4 ? odd : even) + i * 16, src + i * 16, bytes[w]);
+          }
+        } else {  // a row at a time, 32 words side by side
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint64_t row_at = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), 4 * i);
+            const int n = __shfl_sync(0xffffffffu, bytes[w], 4 * i);
+            const uint32_t to = ring + slot_in * slot_bytes + (8 * w + i) * row.pitch * 16;
+#pragma unroll
+            for (int j = 0; j < 4 * NC; ++j) {
+              const int d = lane + j * kWarp;
+              if (d < D) cp_async4(to + ((d >> 2) ^ (i & 1 ? row.swap : 0)) * 16 + (d & 3) * 4, reinterpret_cast<const char*>(row_at) + d * 4, n);
+            }
           }
         }
       }
