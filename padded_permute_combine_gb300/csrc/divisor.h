@@ -16,7 +16,13 @@ struct Divisor {
     while ((1ull << s) < by) ++s;
     m = (uint32_t)(((1ull << 32) * ((1ull << s) - by)) / by + 1);
   }
-  __device__ __forceinline__ uint32_t of(uint32_t n) const { return (__umulhi(n, m) + n) >> s; }
+  __host__ __device__ uint32_t of(uint32_t n) const {
+#ifdef __CUDA_ARCH__
+    return (__umulhi(n, m) + n) >> s;
+#else
+    return ((uint32_t)((uint64_t)n * m >> 32) + n) >> s;
+#endif
+  }
 };
 
 }  // namespace moe
