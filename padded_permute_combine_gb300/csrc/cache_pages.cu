@@ -454,6 +454,8 @@ template <int CTAS> __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds
 }
 
 constexpr int kCtas = 8;
+// One CTA needs no cluster's barriers, but one SM reads the table alone (with copies, 16 rows of 65: 6.6 us against 9;
+// 256 rows of 52: 36 against 30).
 bool one_cta(int64_t entries, int64_t num_pages) { return entries <= 4096 && num_pages <= 32768; }
 
 int words_shift_of(int64_t num_pages, int ctas) {
