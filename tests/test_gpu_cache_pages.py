@@ -147,9 +147,9 @@ def test_fork_large_pools():
 
 def compact(table, lengths, page, pool):
     rows = [t[:-(-n // page)] for t, n in zip(table, lengths)]
-    used = sorted({i for row in rows for i in row})
-    n = len(used)
-    movers, holes = [i for i in used if i >= n], [i for i in range(n) if i not in set(used)]
+    named = {i for row in rows for i in row}
+    n = len(named)
+    movers, holes = sorted(i for i in named if i >= n), [i for i in range(n) if i not in named]
     now = dict(zip(movers, holes))
     return [[now.get(i, i) for i in row] + [-1] * (len(t) - len(row)) for row, t in zip(rows, table)], movers, holes
 
