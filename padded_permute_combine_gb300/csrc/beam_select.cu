@@ -79,20 +79,17 @@ __global__ void __launch_bounds__(kThreads, kUnitCtas) select_units_kernel(const
   using E1 = typename Vec<Elem<ET>::kBytes>::T;
   constexpr bool kPairs = VB >= 4 && Elem<ET>::kBytes == 2;
   await_previous_kernel();
-  const int lane = lane_id(), C = a.per_row;
-  const int64_t total = a.requests * a.beams * C, warps = (int64_t)gridDim.x * (kThreads / kWarp);
-  const int64_t rows_on = warps / C;
-  const int units_on = (int)(warps - rows_on * C);
-  int64_t u = (int64_t)blockIdx.x * (kThreads / kWarp) + threadIdx.x / kWarp;
-  int64_t row = u / C;
-  int c = (int)(u - row * C);
-  const auto at = [&](int64_t r) { return static_cast<const char*>(a.logits) + r * a.row_stride * Elem<ET>::kBytes; };
-  const auto full = [&](int unit) { return (int64_t)(unit + 1) * kUnit <= a.vocab; };
+  const int lane = lane_id(), C = a.per_row, rows = (int)(a.requests * a.beams), warps = (int)gridDim.x * (kThreads / kWarp);
+  const int whole = (int)(a.vocab / kUnit);  // units that are full
+  const int rows_on = warps / C, units_on = warps - rows_on * C;
+  const int first = (int)blockIdx.x * (kThreads / kWarp) + (int)threadIdx.x / kWarp;
+  int row = first / C, c = first - row * C;
+  const int64_t stride = a.row_stride * Elem<ET>::kBytes;
+  const auto at = [&](int r, int unit) { return static_cast<const char*>(a.logits) + r * stride + (int64_t)unit * kUnit * Elem<ET>::kBytes; };
   P next;
-  if (u < total && full(c)) next.load(at(row), c * kUnit, lane);
-  for (; u < total; u += warps) {
-    const int64_t row_now = row;
-    const int c_now = c;
+  if (row < rows && c < whole) next.load(at(row, c), 0, lane);
+  while (row < rows) {
+    const int row_now = row, c_now = c;
     P part = next;
     row += rows_on;
     c += units_on;
@@ -100,26 +97,26 @@ __global__ void __launch_bounds__(kThreads, kUnitCtas) select_units_kernel(const
       c -= C;
       ++row;
     }
-    if (u + warps < total && full(c)) next.load(at(row), c * kUnit, lane);  // on its way while this one is reduced
+    if (row < rows && c < whole) next.load(at(row, c), 0, lane);  // on its way while this one is reduced
     if (a.ended != nullptr && a.ended[row_now]) continue;
-    if (!full(c_now)) {  // the row's last unit, element by element
-      const E1* p = reinterpret_cast<const E1*>(at(row_now)) + (int64_t)c_now * kUnit;
-      const int n = (int)(a.vocab - (int64_t)c_now * kUnit);
-      float x[kEach], m = -INFINITY;
+    float2* const to = a.units + ((int64_t)row_now * C + c_now);
+    if (c_now >= whole) {  // the row's last unit, element by element
+      float x[kEach], m = -INFINITY, sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        x[i] = i * kWarp + lane < n ? Lanes<Elem<ET>::kBytes, ET>::get(ld_stream(p + i * kWarp + lane), 0) : -INFINITY;
-        m = max_nan(m, x[i]);
+        const int64_t t = (int64_t)c_now * kUnit + i * kWarp + lane;
+        x[i] = t < a.vocab ? Lanes<Elem<ET>::kBytes, ET>::get(ld_stream(reinterpret_cast<const E1*>(at(row_now, 0)) + t), 0) : -INFINITY;
       }
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) m = max_nan(m, x[i]);
 #pragma unroll
       for (int d = 1; d < kWarp; d <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
       const float base = m == -INFINITY ? 0.0f : m;
-      float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) sum += ex2((x[i] - base) * kLog2e);
 #pragma unroll
       for (int d = 1; d < kWarp; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (lane == 0) a.units[u] = make_float2(m, sum);
+      if (lane == 0) *to = make_float2(m, sum);
       continue;
     }
     float m;
@@ -163,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, kUnitCtas) select_units_kernel(const
     float sum = s0 + s1;
 #pragma unroll
     for (int d = 1; d < kWarp; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane == 0) a.units[u] = make_float2(m, sum);
+    if (lane == 0) *to = make_float2(m, sum);
   }
 }
 
