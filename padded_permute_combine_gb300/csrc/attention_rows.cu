@@ -18,7 +18,6 @@ template <int GM, int NC> constexpr int kSmWarps = GM <= 4 && NC == 1 ? 12 : 8;
 constexpr int kSlots = 3;  // of a warp's ring, a tile's keys or values each
 
 __device__ __forceinline__ uint64_t pair(float a, float b) { return f2_pack(__float_as_uint(a), __float_as_uint(b)); }
-__device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) { return f2_pack(a, b); }
 
 // A warp takes a tile's 16 keys, then its values, through a ring of three slots:
 // while one is used the next two are on their way. Scores: lane (key, quarter)
@@ -142,20 +141,18 @@ __global__ void __launch_bounds__(kSmWarps<GM, NC> * kWarp, 1) attend_rows_kerne
     issue(false);      // into the slot that the previous tile's values left
     {
       // Scores of two keys, all heads, the same in the four lanes of a key.
-      const uint4* ks = reinterpret_cast<const uint4*>(own + slot * slot_bytes) + key * row.pitch;
+      const ulonglong2* ks = reinterpret_cast<const ulonglong2*>(own + slot * slot_bytes) + key * row.pitch;
       uint64_t s[GM][2];
 #pragma unroll
       for (int h = 0; h < GM; ++h) s[h][0] = s[h][1] = 0;
 #pragma unroll 2
       for (int p = quarter; p < row.pieces; p += 4) {
-        const uint4 k0 = ks[p ^ swap], k1 = ks[8 * row.pitch + (p ^ swap)];
-        const uint64_t k00 = pair(k0.x, k0.y), k01 = pair(k0.z, k0.w), k10 = pair(k1.x, k1.y), k11 = pair(k1.z, k1.w);
+        const ulonglong2 k0 = ks[p ^ swap], k1 = ks[8 * row.pitch + (p ^ swap)];  // pairs of elements
 #pragma unroll
         for (int h = 0; h < GM; ++h) {
-          const uint4 qq = reinterpret_cast<const uint4*>(qs)[h * row.pitch + p];
-          const uint64_t q0 = pair(qq.x, qq.y), q1 = pair(qq.z, qq.w);
-          s[h][0] = f2_fma(q1, k01, f2_fma(q0, k00, s[h][0]));
-          s[h][1] = f2_fma(q1, k11, f2_fma(q0, k10, s[h][1]));
+          const ulonglong2 qq = reinterpret_cast<const ulonglong2*>(qs)[h * row.pitch + p];
+          s[h][0] = f2_fma(qq.y, k0.y, f2_fma(qq.x, k0.x, s[h][0]));
+          s[h][1] = f2_fma(qq.y, k1.y, f2_fma(qq.x, k1.x, s[h][1]));
         }
       }
 #pragma unroll
@@ -197,22 +194,21 @@ __global__ void __launch_bounds__(kSmWarps<GM, NC> * kWarp, 1) attend_rows_kerne
     __syncwarp();
     issue(true);
     {
-      const uint4* vs = reinterpret_cast<const uint4*>(own + slot * slot_bytes);
+      const ulonglong2* vs = reinterpret_cast<const ulonglong2*>(own + slot * slot_bytes);
 #pragma unroll 4
       for (int e = 0; e < kTile; e += 2) {
-        uint4 pr[GM];  // the probabilities of two keys, each twice
+        ulonglong2 pr[GM];  // the probabilities of two keys, each twice
 #pragma unroll
-        for (int h = 0; h < GM; ++h) pr[h] = *reinterpret_cast<const uint4*>(ps + h * kTile + e);
+        for (int h = 0; h < GM; ++h) pr[h] = *reinterpret_cast<const ulonglong2*>(ps + h * kTile + e);
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
           const int p = lane + j * kWarp;
           if (p >= row.pieces) continue;
-          const uint4 v0 = vs[e * row.pitch + p], v1 = vs[(e + 1) * row.pitch + (p ^ row.swap)];
+          const ulonglong2 v0 = vs[e * row.pitch + p], v1 = vs[(e + 1) * row.pitch + (p ^ row.swap)];
 #pragma unroll
           for (int h = 0; h < GM; ++h) {
-            const uint64_t p0 = pair(pr[h].x, pr[h].y), p1 = pair(pr[h].z, pr[h].w);
-            o[h][j][0] = f2_fma(p1, pair(v1.x, v1.y), f2_fma(p0, pair(v0.x, v0.y), o[h][j][0]));
-            o[h][j][1] = f2_fma(p1, pair(v1.z, v1.w), f2_fma(p0, pair(v0.z, v0.w), o[h][j][1]));
+            o[h][j][0] = f2_fma(pr[h].y, v1.x, f2_fma(pr[h].x, v0.x, o[h][j][0]));
+            o[h][j][1] = f2_fma(pr[h].y, v1.y, f2_fma(pr[h].x, v0.y, o[h][j][1]));
           }
         }
       }
