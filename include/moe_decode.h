@@ -167,7 +167,7 @@ typedef struct moe_cache_pages {
  * copies read what was there before the call: no page is both a src and a dst,
  * or dst twice.
  * num_caches <= MOE_CACHE_MAX_CACHES, and at most 1 GB in one page of all of
- * them together (65535 pieces of up to 16 KB), else MOE_ERR_UNSUPPORTED.
+ * them together (65535 pieces of up to 32 KB), else MOE_ERR_UNSUPPORTED.
  */
 int moe_cache_copy(const moe_cache_pages* caches, int64_t num_caches, int64_t num_pages, const int32_t* src,
                    const int32_t* dst, int64_t num_copies, const int32_t* count, int32_t* d_status,

@@ -508,7 +508,8 @@ struct CopyArgs {
 };
 
 constexpr int kCopyThreads = 256;
-constexpr int64_t kPieceBytes = 16384;  // of a page, for a CTA at a time
+// Of a page, for a CTA at a time: four vectors of 32 bytes a thread (0.6 GB moved: 186 us, with 16 bytes and 16 KB 197).
+constexpr int64_t kPieceBytes = 32768;
 
 // Four vectors of a thread on their way together.
 template <typename V> __device__ __forceinline__ void copy_piece(const char* in, char* out, int64_t bytes) {
@@ -556,7 +557,9 @@ __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const __grid_c
     const char* in = base + s * stride;
     char* out = base + d * stride;
     const uintptr_t all = reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out) | (uintptr_t)bytes;
-    if ((all & 15) == 0) {
+    if ((all & 31) == 0) {
+      copy_piece<u32x8>(in, out, bytes);
+    } else if ((all & 15) == 0) {
       copy_piece<uint4>(in, out, bytes);
     } else if ((all & 3) == 0) {
       copy_piece<uint32_t>(in, out, bytes);
