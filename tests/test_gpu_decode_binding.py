@@ -175,3 +175,59 @@ def test_another_current_stream_and_no_synchronisation():
     assert not done.query()
     side.synchronize()
     assert all(torch.equal(u, v) for u, v in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_keys_and_values_in_one_tensor_and_other_orders(dtype):
+    """[pages, 2, page_size, kv_heads, head_dim], and pages behind tokens: the same numbers give the same bits."""
+    g = {n: t.to(dtype) if t.dtype == BF16 else t for n, t in good().items()}
+    want = p.moe_attention_decode(**(g | {n: g[n].clone() for n in ("k_cache", "v_cache")}))
+    both = torch.stack([g["k_cache"], g["v_cache"]], 1)
+    got = p.moe_attention_decode(**(g | dict(k_cache=both[:, 0], v_cache=both[:, 1])))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for order in ((1, 0, 2, 3), (2, 1, 0, 3), (0, 2, 1, 3)):
+        back = [order.index(i) for i in range(4)]
+        k, v = (g[n].permute(order).contiguous().permute(back) for n in ("k_cache", "v_cache"))
+        got = p.moe_attention_decode(**(g | dict(k_cache=k, v_cache=v)))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.equal(k[0, 1, 0], g["k_cache"][0, 1, 0])
+    flat = both.clone()
+    p.moe_cache_write(g["k_new"], g["v_new"], flat[:, 0], flat[:, 1], g["page_table"], ints(0, 1, 2), g["lengths"])
+    assert torch.equal(flat[2, 0, 7], g["k_new"][0]) and torch.equal(flat[2, 1, 7], g["v_new"][0])
+    assert torch.equal(flat[3, 0, 6], g["k_new"][1]) and torch.equal(flat[3, 1, 6], g["v_new"][1])
+
+
+def test_as_many_rows_as_there_may_be():
+    R = _lib.MOE_CACHE_MAX_ROWS
+    k, v = new(R, 2, 1, 16, dtype=F32), new(R + 1, 2, 1, 16, dtype=F32)[1:]
+    table = torch.arange(R, dtype=I32, device="cuda")[:, None]
+    lengths = (torch.arange(R, device="cuda") % 3).to(I32)
+    q = new(R, 2, 16, dtype=F32)
+    out, lse = p.moe_attention_decode(q, k, v, table, lengths)
+    n = lengths.long()
+    x = torch.einsum("rhd,rtd->rht", q.double(), k[:, :, 0].double()) / 4
+    x = torch.where(torch.arange(2, device="cuda") < n[:, None, None], x, -torch.inf)
+    want = torch.einsum("rht,rtd->rhd", torch.softmax(x, 2).nan_to_num(0), v[:, :, 0].double())
+    assert bool(((out.double() - want).abs() <= 1e-5).all())  # two terms of order one: some 2^-20
+    assert torch.equal(torch.isinf(lse), (n == 0)[:, None].expand(R, 2))
+
+
+def test_inference_mode_and_concurrent_streams():
+    with torch.inference_mode():
+        g = good()
+        out, lse = p.moe_attention_decode(**g)
+        f = p.moe_cache_fork(g["page_table"], g["lengths"], ints(0, 1, 1), 16, 9)
+        assert out.is_inference() and f.lengths.is_inference()
+        f.lengths.add_(1)
+    g = [good() | dict(q=new(2, 4, 64) * (1 + i), k_new=None, v_new=None) for i in range(4)]
+    x, s = [new(2, 3, 4000 + 8 * i) for i in range(4)], torch.zeros(2, 3, device="cuda")
+    want = [(*p.moe_attention_decode(**a), *p.moe_beam_select(b, s, 5)) for a, b in zip(g, x)]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    for _ in range(20):  # four streams at the same time, each call with a workspace of its own
+        got = []
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got.append((*p.moe_attention_decode(**g[i]), *p.moe_beam_select(x[i], s, 5)))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for u, w in zip(got, want) for a, b in zip(u, w))
