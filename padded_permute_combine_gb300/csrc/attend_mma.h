@@ -67,24 +67,24 @@ __global__ void __launch_bounds__(Mma<DP, HEADS, BY, TEAM>::kWarps * kWarp, 1) a
   __shared__ int s_prefix[kWarps * kWarp], s_warp[kWarps];
   __shared__ unsigned s_mask[kWarps][kStages][SHIFT ? 2 : 1];  // rows that are there: all 16 or, with SHIFT, eight and eight
   __shared__ uint8_t s_low[kWarps][SHIFT ? kStages : 1][kTile];  // rows' offsets to 16 bytes
-  await_previous_kernel();
-  start_next_kernel();
-  const int lane = lane_id(), warp = threadIdx.x / kWarp;
-  const int HV = a.kv_heads * a.parts, team = warp / TEAM, rank = warp - team * TEAM, gt = blockIdx.x * (kWarps / TEAM) + team;
-  const int r = gt / HV, hv = gt - r * HV, kv = hv / a.parts, part = hv - kv * a.parts;
-  Cursor in;
-  const int count = my_range(a, r, s_prefix, s_warp, in);
-  if (count == 0) return;
+  const int lane = lane_id(), warp = threadIdx.x / kWarp, team = warp / TEAM, rank = warp - team * TEAM;
   const int col0 = rank * DP, D = min(DP, a.D - col0);  // the warp's columns
-  char* const keys = a.k + 2 * col0;
-  char* const values = a.v + 2 * col0;
-  const int h0 = kv * a.group + part * HEADS, heads = min(HEADS, a.group - part * HEADS);
   const uint32_t ring = smem_u32(smem) + warp * kStages * S::kStageBytes;
   if (SHIFT || D < DP) {  // pieces behind D are never copied, and have to be numbers
     uint4* z = reinterpret_cast<uint4*>(smem + (size_t)warp * kStages * S::kStageBytes);
     for (int i = lane; i < kStages * S::kStageBytes / 16; i += kWarp) z[i] = make_uint4(0, 0, 0, 0);
-    __syncwarp();
   }
+  await_previous_kernel();
+  start_next_kernel();
+  const int HV = a.kv_heads * a.parts, gt = blockIdx.x * (kWarps / TEAM) + team;
+  const int r = gt / HV, hv = gt - r * HV, kv = hv / a.parts, part = hv - kv * a.parts;
+  Cursor in;
+  const int count = my_range(a, r, s_prefix, s_warp, in);
+  if (count == 0) return;
+  __syncwarp();
+  char* const keys = a.k + 2 * col0;
+  char* const values = a.v + 2 * col0;
+  const int h0 = kv * a.group + part * HEADS, heads = min(HEADS, a.group - part * HEADS);
 
   // Copies of a tile: K then V, 16 rows each, whole rows at a time, so that each
   // fetch is one of 256 bytes (four lanes a row take 40 instructions instead of

@@ -29,15 +29,7 @@ template <int GM, int NC, int VB>
 __global__ void __launch_bounds__(kSmWarps<GM, NC> * kWarp, 1) attend_rows_kernel(const AttendArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_prefix[kSmWarps<GM, NC> * kWarp], s_warp[kSmWarps<GM, NC>];
-  await_previous_kernel();
-  start_next_kernel();
   const int lane = lane_id(), warp = threadIdx.x / kWarp, warps = blockDim.x / kWarp;
-  const int HV = a.kv_heads * a.parts, gw = blockIdx.x * warps + warp;
-  const int r = gw / HV, hv = gw - r * HV, kv = hv / a.parts, part = hv - kv * a.parts;
-  Cursor in;
-  const int count = my_range(a, r, s_prefix, s_warp, in);
-  if (count == 0) return;
-
   const int D = a.D;
   const RowPieces row(D);
   const int slot_bytes = kTile * row.pitch * 16;
@@ -45,8 +37,16 @@ __global__ void __launch_bounds__(kSmWarps<GM, NC> * kWarp, 1) attend_rows_kerne
   float* qs = reinterpret_cast<float*>(own + kSlots * slot_bytes);
   uint64_t* ps = reinterpret_cast<uint64_t*>(qs + GM * row.pitch * 4);  // [GM][16], each probability twice
   const uint32_t ring = smem_u32(own);
-  for (int i = lane; i < (kSlots * slot_bytes + GM * row.pitch * 16) / 16; i += kWarp)  // what lies behind D stays zero
+  // What lies behind D in a row's last piece stays zero, and the query rows of heads behind the group.
+  for (int i = (VB == 16 ? kSlots * slot_bytes / 16 : 0) + lane; i < (kSlots * slot_bytes + GM * row.pitch * 16) / 16; i += kWarp)
     reinterpret_cast<uint4*>(own)[i] = make_uint4(0, 0, 0, 0);
+  await_previous_kernel();
+  start_next_kernel();
+  const int HV = a.kv_heads * a.parts, gw = blockIdx.x * warps + warp;
+  const int r = gw / HV, hv = gw - r * HV, kv = hv / a.parts, part = hv - kv * a.parts;
+  Cursor in;
+  const int count = my_range(a, r, s_prefix, s_warp, in);
+  if (count == 0) return;
   __syncwarp();
 
   // Copies of a tile's keys, then of its values: four lanes a row (rows r0 and
