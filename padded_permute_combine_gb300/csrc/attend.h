@@ -163,8 +163,20 @@ __device__ __forceinline__ int64_t row_offset(const AttendArgs& a, const Cursor&
   return page * a.page_stride + (pos - a.page.of(pos) * a.page.d) * a.token_stride + kv * a.head_stride;
 }
 
-// The range of warp r of a head: how many tiles, and where the first is.
-__device__ __forceinline__ int my_range(const AttendArgs& a, int r, int* prefix, int* s_warp, Cursor& c) {
+// A warp's (or team's) range r of a head's line, and which piece hv of a group of heads.
+struct Share {
+  int r, hv;
+};
+__device__ __forceinline__ Share share_at(int unit, int pieces) { return {unit / pieces, unit % pieces}; }
+
+// The share of worker `place` of the CTA's `workers`: how many tiles, and where
+// the first is. Neighbouring workers take neighbouring heads of a range; where
+// there are fewer tiles than ranges the CTAs take turns, so that every SM has some
+// (one of 600 tokens, 32 heads of 128 on 8, fp32: 14.1 us instead of 15.3).
+__device__ __forceinline__ int my_range(const AttendArgs& a, int place, int workers, int* prefix, int* s_warp, Share& share, Cursor& c) {
+  const int pieces = a.kv_heads * a.parts;
+  share = share_at(blockIdx.x * workers + place, pieces);
+  const Share spread = share_at(place * gridDim.x + blockIdx.x, pieces);
   int total, before = 0, x = 0;  // x: tiles up to the lane's sequence
   const bool few = a.seqs <= kWarp;
   Cursor own = {lane_id(), 0, 0, 0, 0};
@@ -185,6 +197,8 @@ __device__ __forceinline__ int my_range(const AttendArgs& a, int r, int* prefix,
   }
   if (total == 0) return 0;
   const int ranges = ranges_of(a, total);
+  if (total < a.ranges) share = spread;
+  const int r = share.r;
   if (r >= ranges) return 0;
   const int lo = range_begin(r, ranges, total), count = range_begin(r + 1, ranges, total) - lo;
   if (count <= 0) return 0;

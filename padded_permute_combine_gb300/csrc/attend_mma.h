@@ -76,11 +76,11 @@ __global__ void __launch_bounds__(Mma<DP, HEADS, BY, TEAM>::kWarps * kWarp, 1) a
   }
   await_previous_kernel();
   start_next_kernel();
-  const int HV = a.kv_heads * a.parts, gt = blockIdx.x * (kWarps / TEAM) + team;
-  const int r = gt / HV, hv = gt - r * HV, kv = hv / a.parts, part = hv - kv * a.parts;
+  Share share;
   Cursor in;
-  const int count = my_range(a, r, s_prefix, s_warp, in);
+  const int count = my_range(a, team, kWarps / TEAM, s_prefix, s_warp, share, in);
   if (count == 0) return;
+  const int r = share.r, kv = share.hv / a.parts, part = share.hv - kv * a.parts;
   __syncwarp();
   char* const keys = a.k + 2 * col0;
   char* const values = a.v + 2 * col0;

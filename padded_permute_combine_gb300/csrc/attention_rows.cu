@@ -42,11 +42,11 @@ __global__ void __launch_bounds__(kSmWarps<GM, NC> * kWarp, 1) attend_rows_kerne
     reinterpret_cast<uint4*>(own)[i] = make_uint4(0, 0, 0, 0);
   await_previous_kernel();
   start_next_kernel();
-  const int HV = a.kv_heads * a.parts, gw = blockIdx.x * warps + warp;
-  const int r = gw / HV, hv = gw - r * HV, kv = hv / a.parts, part = hv - kv * a.parts;
+  Share share;
   Cursor in;
-  const int count = my_range(a, r, s_prefix, s_warp, in);
+  const int count = my_range(a, warp, warps, s_prefix, s_warp, share, in);
   if (count == 0) return;
+  const int r = share.r, kv = share.hv / a.parts, part = share.hv - kv * a.parts;
   __syncwarp();
 
   // Copies of a tile's keys, then of its values: four lanes a row (rows r0 and
