@@ -73,12 +73,8 @@ __global__ void __launch_bounds__(kSmWarps<GM, NC> * kWarp, 1) attend_rows_kerne
           from[w] = a.k + (off < 0 ? 0 : off);
         }
         const char* src = from[w] + (values ? apart : 0);
-        if (r0 + 8 * w == fresh && bytes[w] != 0) {
-          const char* kept = src;
+        if (r0 + 8 * w == fresh && bytes[w] != 0)
           src = values ? a.v_new + in.b * a.vn_row + kv * a.vn_head : a.k_new + in.b * a.kn_row + kv * a.kn_head;
-          if (part == 0)
-            for (int d = part4; d < D; d += 4) reinterpret_cast<float*>(const_cast<char*>(kept))[d] = reinterpret_cast<const float*>(src)[d];
-        }
         if constexpr (VB == 16) {
           src += part4 * VB;
           const uint32_t to = base + 8 * w * row.pitch * 16, even = to + flip, odd = to - flip;  // 64 bytes on in every other 64
@@ -98,6 +94,31 @@ __global__ void __launch_bounds__(kSmWarps<GM, NC> * kWarp, 1) attend_rows_kerne
               const int d = lane + j * kWarp;
               if (d < D) cp_async4(to + ((d >> 2) ^ (i & 1 ? row.swap : 0)) * 16 + (d & 3) * 4, reinterpret_cast<const char*>(row_at) + d * 4, n);
             }
+          }
+        }
+      }
+      if (!values && part == 0 && fresh >= 0 && fresh < kTile) {
+        // The new token into the cache, by the whole warp while the tile is on its way (by the row's four
+        // lanes, in front of the copies: one sequence of 600 tokens 14.2 us instead of 9.5, 16 of 4000 95 instead of 85).
+        const int row_lane = fresh % 8 * 4;
+        float* k_to = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(fresh < 8 ? from[0] : from[1]), row_lane));
+        if (__shfl_sync(0xffffffffu, fresh < 8 ? bytes[0] : bytes[1], row_lane) != 0) {
+          float* v_to = k_to + apart / 4;
+          const float* kn = reinterpret_cast<const float*>(a.k_new + in.b * a.kn_row + kv * a.kn_head);
+          const float* vn = reinterpret_cast<const float*>(a.v_new + in.b * a.vn_row + kv * a.vn_head);
+          float kk[4 * NC], vv[4 * NC];
+#pragma unroll
+          for (int j = 0; j < 4 * NC; ++j) {
+            const int d = lane + j * kWarp;
+            kk[j] = d < D ? kn[d] : 0.0f;
+            vv[j] = d < D ? vn[d] : 0.0f;
+          }
+#pragma unroll
+          for (int j = 0; j < 4 * NC; ++j) {
+            const int d = lane + j * kWarp;
+            if (d >= D) continue;
+            k_to[d] = kk[j];
+            v_to[d] = vv[j];
           }
         }
       }
