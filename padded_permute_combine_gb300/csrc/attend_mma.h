@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(Mma<DP, HEADS, BY, TEAM>::kWarps * kWarp, 1) a
       const char* vn = a.v_new + in.b * a.vn_row + kv * a.vn_head + 2 * col0;
       if constexpr (SHIFT) {
         const uint32_t base = ring + stage * S::kStageBytes + r0 * kPitch + quarter * 16;
+        int64_t new_at = -1;  // of the new token's row, in its lanes
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const int64_t off = row_offset(a, in, r0 + 8 * w, page[w], kv);
@@ -119,19 +120,8 @@ __global__ void __launch_bounds__(Mma<DP, HEADS, BY, TEAM>::kWarps * kWarp, 1) a
           const int k_low = (int)(k_from & 15), v_low = (int)(v_from & 15);
           const int k_end = bytes == 0 ? 2 * DP + 16 : 2 * D + k_low, v_end = bytes == 0 ? 2 * DP + 16 : 2 * D + v_low;
           if (quarter == 0) s_low[warp][stage][r0 + 8 * w] = (uint8_t)(k_low | v_low << 4);
-          if (off >= 0 && r0 + 8 * w == fresh) {  // to where the row's own bytes would lie
-            unsigned char* ks = smem + (to - quarter * 16 - smem_u32(smem));
-            unsigned char* vs = ks + kTile * kPitch;
-            for (int d = quarter; d < D; d += 4) {
-              const uint16_t kk = reinterpret_cast<const uint16_t*>(kn)[d], vv = reinterpret_cast<const uint16_t*>(vn)[d];
-              reinterpret_cast<uint16_t*>(ks + k_low)[d] = kk;
-              reinterpret_cast<uint16_t*>(vs + v_low)[d] = vv;
-              if (part == 0) {
-                reinterpret_cast<uint16_t*>(k_from)[d] = kk;
-                reinterpret_cast<uint16_t*>(v_from)[d] = vv;
-              }
-            }
-          } else {
+          if (fresh == r0 + 8 * w) new_at = off;
+          if (off < 0 || r0 + 8 * w != fresh) {
             const char* kp = reinterpret_cast<const char*>(k_from - k_low) + quarter * 16;
             const char* vp = reinterpret_cast<const char*>(v_from - v_low) + quarter * 16;
 #pragma unroll
@@ -139,6 +129,31 @@ __global__ void __launch_bounds__(Mma<DP, HEADS, BY, TEAM>::kWarps * kWarp, 1) a
               if (i == kTurns && quarter != 0) continue;
               if (quarter * 16 + i * 64 < k_end) cp_async16(to + i * 64, kp + i * 64, bytes);
               if (quarter * 16 + i * 64 < v_end) cp_async16(to + i * 64 + kTile * kPitch, vp + i * 64, bytes);
+            }
+          }
+        }
+        if (fresh >= 0 && fresh < kTile) {  // the new token, by the whole warp, to where the row's own bytes would lie
+          new_at = __shfl_sync(0xffffffffu, new_at, fresh & 7);
+          if (new_at >= 0) {
+            const uintptr_t k_to = reinterpret_cast<uintptr_t>(keys) + new_at, v_to = k_to + apart;
+            unsigned char* row = smem + (size_t)warp * kStages * S::kStageBytes + stage * S::kStageBytes + fresh * kPitch;
+            uint16_t kk[DP / kWarp], vv[DP / kWarp];
+#pragma unroll
+            for (int j = 0; j < DP / kWarp; ++j) {
+              const int d = lane + j * kWarp;
+              kk[j] = d < D ? reinterpret_cast<const uint16_t*>(kn)[d] : 0;
+              vv[j] = d < D ? reinterpret_cast<const uint16_t*>(vn)[d] : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < DP / kWarp; ++j) {
+              const int d = lane + j * kWarp;
+              if (d >= D) continue;
+              reinterpret_cast<uint16_t*>(row + (k_to & 15))[d] = kk[j];
+              reinterpret_cast<uint16_t*>(row + kTile * kPitch + (v_to & 15))[d] = vv[j];
+              if (part == 0) {
+                reinterpret_cast<uint16_t*>(k_to)[d] = kk[j];
+                reinterpret_cast<uint16_t*>(v_to)[d] = vv[j];
+              }
             }
           }
         }
@@ -157,8 +172,9 @@ __global__ void __launch_bounds__(Mma<DP, HEADS, BY, TEAM>::kWarps * kWarp, 1) a
             cp_async<kPiece>(dst + kTile * kPitch, vn + chunk * kPiece, kPiece);
             if (part == 0) {
               using V = typename Vec<kPiece>::T;
-              *reinterpret_cast<V*>(keys + to + chunk * kPiece) = *reinterpret_cast<const V*>(kn + chunk * kPiece);
-              *reinterpret_cast<V*>(values + to + chunk * kPiece) = *reinterpret_cast<const V*>(vn + chunk * kPiece);
+              const V kk = *reinterpret_cast<const V*>(kn + chunk * kPiece), vv = *reinterpret_cast<const V*>(vn + chunk * kPiece);
+              *reinterpret_cast<V*>(keys + to + chunk * kPiece) = kk;
+              *reinterpret_cast<V*>(values + to + chunk * kPiece) = vv;
             }
           }
         }
