@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(WARPS * kWarp) attend_join_kernel(const Attend
 
 template <typename ET, bool QUADS> int launch_join(const AttendArgs& a, cudaStream_t s) {
   // Where a head may have more than 64 parts, 32 warps share it (one sequence of 80000 tokens, six heads of 600
-  // parts: 26 us in all with eight warps, 21 with 32; 9 sequences with some 33 parts: 20 and 21).
+  // parts: 26 us in all with eight warps, 21 with 32; 9 sequences with some 33 parts: 1 us more).
   const int most = a.max_tokens / kTile < a.ranges ? a.max_tokens / kTile : a.ranges;
   const bool few = most / a.seqs > 64;
   int y = (int)(4 * (int64_t)num_sms() / a.seqs);
