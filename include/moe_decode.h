@@ -76,7 +76,9 @@ typedef struct moe_heads {
  *          num_kv_heads, and head h reads kv head h / (num_heads / num_kv_heads)
  *   k_new, v_new  [num_seqs, num_kv_heads, head_dim], both or neither: written
  *          to position L - 1 of the cache, and read from here. The page that
- *          takes it belongs to one sequence alone.
+ *          takes it belongs to one sequence alone. A token without a place is
+ *          left out: its page's number is bad, or its length lies beyond the
+ *          table (then only what the table holds is looked at).
  *   out    [num_seqs, num_heads, head_dim] of the cache's dtype, contiguous
  *   lse    [num_seqs, num_heads] fp32, nullable
  *   workspace >= moe_attention_decode_workspace_size(...) bytes, 16-byte aligned, contents need no initialisation;

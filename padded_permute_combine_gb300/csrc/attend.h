@@ -163,6 +163,15 @@ __device__ __forceinline__ int64_t row_offset(const AttendArgs& a, const Cursor&
   return page * a.page_stride + (pos - a.page.of(pos) * a.page.d) * a.token_stride + kv * a.head_stride;
 }
 
+// The new token's row of the cursor's tile; outside [0, kTile): the tile has none. A length
+// beyond the table has no place for it: the last position that there is holds a token
+// already, in a page that other sequences may share.
+__device__ __forceinline__ int new_row(const AttendArgs& a, const Cursor& c) {
+  if (a.k_new == nullptr) return -1;
+  const int row = c.n - 1 - (c.first + c.tile * kTile);
+  return row < kTile && c.n == a.max_tokens && a.lengths[c.b] > c.n ? -1 : row;
+}
+
 // A warp's (or team's) range r of a head's line, and which piece hv of a group of heads.
 struct Share {
   int r, hv;

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kSmWarps<GM, NC> * kWarp, 1) attend_rows_kerne
   const auto issue = [&](bool values) {
     if (issued < count) {
       const uint32_t base = ring + slot_in * slot_bytes + place;
-      const int fresh = a.k_new != nullptr ? in.n - 1 - (in.first + in.tile * kTile) : -1;  // the new token's row
+      const int fresh = new_row(a, in);
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         if (!values) {

@@ -1,0 +1,54 @@
+"""The decode operators where their arguments end: tables that are full, numbers
+that need more than 32 bits. What is compared is exact."""
+import pytest
+import torch
+
+import padded_permute_combine_gb300 as p
+from padded_permute_combine_gb300 import _lib
+
+pytestmark = pytest.mark.gpu
+BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+@pytest.fixture(autouse=True)
+def needs_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def rand(*shape, dtype=BF16, seed=1):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).cuda().to(dtype)
+
+
+def ints(*v):
+    return torch.tensor(v, dtype=I32, device="cuda")
+
+
+def equal(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF16, 64), (BF16, 128), (BF16, 77), (BF16, 100), (BF16, 250), (F32, 64), (F32, 77), (F32, 200)])
+@pytest.mark.parametrize("rows,window", [(1, 0), (3, 0), (3, 20), (40, 0)])
+def test_a_new_token_beyond_the_table_is_left_out(dtype, dim, rows, window):
+    """Rows whose table is full, their length one more: nothing is written, and what the table holds is looked at.
+    With several rows, the second and third name the same last page, as after a fork without a column to grow into."""
+    width, page = 3, 16
+    table = torch.arange(rows * width, dtype=I32, device="cuda").view(rows, width)
+    if rows > 2:
+        table[2, width - 1] = table[1, width - 1]
+    k, v = (rand(rows * width, page, 2, dim, dtype=dtype, seed=s) for s in (2, 3))
+    q, kn, vn = (rand(rows, h, dim, dtype=dtype, seed=s) for h, s in ((6, 4), (2, 5), (2, 6)))
+    full = torch.full((rows,), width * page, dtype=I32, device="cuda")
+    want = p.moe_attention_decode(q, k, v, table, full, window=window)
+    before, status = (k.clone(), v.clone()), ints(0)
+    for more in (1, 1000):
+        got = p.moe_attention_decode(q, k, v, table, full + more, kn, vn, window=window, status=status)
+        assert int(status) == _lib.MOE_STATUS_BAD_INDEX
+        assert equal((k, v), before) and equal(got, want)
+        assert equal(p.moe_attention_decode(q, k, v, table, full + more, kn, vn, window=window), want) and equal((k, v), before)
+    # The last place of a table is one all the same.
+    own = table.clone()
+    own[:, width - 1] = torch.arange(rows, device="cuda") * width + width - 1
+    p.moe_attention_decode(q, k, v, own, full, kn, vn, window=window)
+    assert torch.equal(k[own[:, -1].long(), page - 1], kn) and torch.equal(v[own[:, -1].long(), page - 1], vn)
