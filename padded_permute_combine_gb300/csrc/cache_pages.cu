@@ -17,6 +17,7 @@
 #include "common.cuh"
 #include "divisor.h"
 #include "moe_decode.h"
+#include "search.h"
 
 namespace moe {
 namespace {
@@ -44,11 +45,7 @@ struct WriteArgs {
 
 // Where token t goes: bytes from the cache's start, or -1.
 __device__ __forceinline__ int64_t place_of(const WriteArgs& a, int64_t t) {
-  int lo = 0, hi = a.seqs + 1;  // the last sequence that begins at or before t, if any
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.offsets[mid] <= t) lo = mid; else hi = mid;
-  }
+  const int lo = last_at_most(a.offsets, a.seqs + 1, t);  // the last sequence that begins at or before t, if any
   const int64_t from = a.offsets[lo];
   if (lo == a.seqs && from <= t) return -1;  // behind the last sequence
   const int64_t end = lo < a.seqs ? a.offsets[lo + 1] : 0;
@@ -77,7 +74,7 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const WriteArgs a) {
   const int lane = lane_id(), warps = blockDim.x / kWarp;
   const int per_token = (int)a.per_token.d;
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= a.seqs; i += blockDim.x) {
+    for (uint32_t i = threadIdx.x; i <= (uint32_t)a.seqs; i += blockDim.x) {  // seqs may be all that 31 bits hold
       const int64_t from = a.offsets[i], to = i < a.seqs ? a.offsets[i + 1] : a.tokens;
       if (from < 0 || from > to || (i == 0 && from != 0)) flag_status(a.status, MOE_STATUS_BAD_BINS);
     }

@@ -52,3 +52,20 @@ def test_a_new_token_beyond_the_table_is_left_out(dtype, dim, rows, window):
     own[:, width - 1] = torch.arange(rows, device="cuda") * width + width - 1
     p.moe_attention_decode(q, k, v, own, full, kn, vn, window=window)
     assert torch.equal(k[own[:, -1].long(), page - 1], kn) and torch.equal(v[own[:, -1].long(), page - 1], vn)
+
+
+def test_a_write_of_more_than_2_to_the_30_sequences():
+    """Three tokens, of the sequences 5, 2^30 + 7 and the last one."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    n = (1 << 30) + 1000
+    offsets, lengths, table = (torch.zeros(n + i, dtype=I32, device="cuda") for i in (1, 0, 0))
+    table = table[:, None]
+    for i, b in enumerate((5, (1 << 30) + 7, n - 1)):
+        offsets[b + 1:], lengths[b], table[b, 0] = i + 1, i + 1, i  # to position i of page i
+    k, v, new, status = rand(4, 4, 1, 8), rand(4, 4, 1, 8, seed=2), rand(3, 1, 8, seed=3), ints(0)
+    want = k.clone(), v.clone()
+    for i in range(3):
+        want[0][i, i], want[1][i, i] = new[i], -new[i]
+    p.moe_cache_write(new, -new, k, v, table, offsets, lengths, status=status)
+    assert equal((k, v), want) and int(status) == 0
