@@ -17,6 +17,7 @@
 #include "block_common.h"
 #include "common.cuh"
 #include "moe_decode.h"
+#include "unit_turns.h"
 #include "vec_math.cuh"
 
 namespace moe {
@@ -79,25 +80,20 @@ __global__ void __launch_bounds__(kThreads, kUnitCtas) select_units_kernel(const
   using E1 = typename Vec<Elem<ET>::kBytes>::T;
   constexpr bool kPairs = VB >= 4 && Elem<ET>::kBytes == 2;
   await_previous_kernel();
-  const int lane = lane_id(), C = a.per_row, rows = (int)(a.requests * a.beams), warps = (int)gridDim.x * (kThreads / kWarp);
+  const int lane = lane_id(), C = a.per_row, warps = (int)gridDim.x * (kThreads / kWarp);
+  const uint32_t rows = (uint32_t)(a.requests * a.beams);
   const int whole = (int)(a.vocab / kUnit);  // units that are full
-  const int rows_on = warps / C, units_on = warps - rows_on * C;
-  const int first = (int)blockIdx.x * (kThreads / kWarp) + (int)threadIdx.x / kWarp;
-  int row = first / C, c = first - row * C;
+  UnitTurns turn((int)blockIdx.x * (kThreads / kWarp) + (int)threadIdx.x / kWarp, warps, C);
   const int64_t stride = a.row_stride * Elem<ET>::kBytes;
-  const auto at = [&](int r, int unit) { return static_cast<const char*>(a.logits) + r * stride + (int64_t)unit * kUnit * Elem<ET>::kBytes; };
+  const auto at = [&](uint32_t r, int unit) { return static_cast<const char*>(a.logits) + r * stride + (int64_t)unit * kUnit * Elem<ET>::kBytes; };
   P next;
-  if (row < rows && c < whole) next.load(at(row, c), 0, lane);
-  while (row < rows) {
-    const int row_now = row, c_now = c;
+  if (turn.row < rows && turn.c < whole) next.load(at(turn.row, turn.c), 0, lane);
+  while (turn.row < rows) {
+    const uint32_t row_now = turn.row;
+    const int c_now = turn.c;
     P part = next;
-    row += rows_on;
-    c += units_on;
-    if (c >= C) {
-      c -= C;
-      ++row;
-    }
-    if (row < rows && c < whole) next.load(at(row, c), 0, lane);  // on its way while this one is reduced
+    turn.next();
+    if (turn.row < rows && turn.c < whole) next.load(at(turn.row, turn.c), 0, lane);  // on its way while this one is reduced
     if (a.ended != nullptr && a.ended[row_now]) continue;
     float2* const to = a.units + ((int64_t)row_now * C + c_now);
     if (c_now >= whole) {  // the row's last unit, element by element

@@ -69,3 +69,16 @@ def test_a_write_of_more_than_2_to_the_30_sequences():
         want[0][i, i], want[1][i, i] = new[i], -new[i]
     p.moe_cache_write(new, -new, k, v, table, offsets, lengths, status=status)
     assert equal((k, v), want) and int(status) == 0
+
+
+def test_a_selection_over_almost_2_to_the_31_rows():
+    """A vocabulary of one token, so that totals are the scores: the best beam of each request."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    B, W = (1 << 25) - 1, 64
+    logits = torch.zeros(B, W, 1, dtype=BF16, device="cuda")
+    scores = torch.rand(B, W, generator=torch.Generator(device="cuda").manual_seed(0), device="cuda")
+    best, parents, tokens = p.moe_beam_select(logits, scores, 1)
+    assert torch.equal(best[:, 0], scores.amax(1)) and bool((tokens == 0).all())
+    assert torch.equal(parents[:, 0].long() // W, torch.arange(B, device="cuda"))
+    assert torch.equal(scores.view(-1)[parents[:, 0].long()], best[:, 0])
