@@ -474,7 +474,7 @@ bool select_ok(int64_t num_requests, int32_t num_beams, int64_t vocab) { return 
 bool select_supported(int64_t num_requests, int32_t num_beams, int64_t vocab) {
   // The last: the second kernel keeps a list of units in shared memory.
   return num_beams <= MOE_BEAM_MAX_BEAMS && vocab <= INT32_MAX && num_beams * vocab <= INT32_MAX &&
-         num_requests * num_beams <= INT32_MAX && num_beams * ((vocab + kUnit - 1) / kUnit) <= MOE_BEAM_MAX_UNITS;
+         num_requests <= INT32_MAX / num_beams && num_beams * ((vocab + kUnit - 1) / kUnit) <= MOE_BEAM_MAX_UNITS;
 }
 
 }  // namespace
@@ -494,7 +494,7 @@ extern "C" int moe_beam_select(const void* logits, int32_t dtype, int64_t row_st
                                int32_t* out_tokens, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
   const int eb = dtype_bytes(dtype);
   if (!select_ok(num_requests, num_beams, vocab) || num_out < 1) return MOE_ERR_INVALID_ARG;
-  if (num_requests * num_beams > 1 && row_stride < vocab) return MOE_ERR_INVALID_ARG;
+  if (num_requests > 0 && (num_requests > 1 || num_beams > 1) && row_stride < vocab) return MOE_ERR_INVALID_ARG;
   if (ended != nullptr && (end_token < 0 || end_token >= vocab)) return MOE_ERR_INVALID_ARG;
   if (eb == 0 || num_out > MOE_BEAM_MAX_OUT || !select_supported(num_requests, num_beams, vocab)) return MOE_ERR_UNSUPPORTED;
   if (num_requests == 0) return MOE_OK;
