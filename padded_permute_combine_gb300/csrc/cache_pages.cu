@@ -721,6 +721,7 @@ extern "C" int moe_cache_copy(const moe_cache_pages* caches, int64_t num_caches,
     if (caches[c].page_bytes < 0 || caches[c].page_stride < 0) return MOE_ERR_INVALID_ARG;
     if (num_pages > 1 && caches[c].page_stride < caches[c].page_bytes) return MOE_ERR_INVALID_ARG;
     if (num_pages > 0 && caches[c].page_bytes > 0 && caches[c].data == nullptr) return MOE_ERR_INVALID_ARG;
+    if (caches[c].page_bytes > 65535 * kPieceBytes) return MOE_ERR_UNSUPPORTED;
     a.caches[c] = caches[c];
     pieces += (caches[c].page_bytes + kPieceBytes - 1) / kPieceBytes;
   }

@@ -24,3 +24,10 @@ def test_select(lib, requests):
     """2^58 x 64 rows are 2^64, which 64 bits hold as none."""
     assert lib.moe_beam_select_workspace_size(requests, 64, 10) == 0
     assert lib.moe_beam_select(FAKE, 1, 10, FAKE, None, requests, 64, 10, 2, -1, FAKE, FAKE, FAKE, FAKE, 1 << 40, None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("size", [1 << 31, 1 << 62, MOST])
+def test_copy(lib, size):
+    """A page's pieces are counted, and the count of 2^63 - 1 bytes does not come out negative."""
+    some = (_lib.CachePages * 1)(_lib.CachePages(FAKE, MOST, size))
+    assert lib.moe_cache_copy(some, 1, 10, FAKE, FAKE, 3, None, None, None) == UNSUPPORTED
