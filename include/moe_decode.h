@@ -89,7 +89,8 @@ typedef struct moe_heads {
  * out and lse NaN, as the formulas say; an infinite value makes its element of
  * out infinite or NaN. A sequence's result depends on the other sequences'
  * lengths in the order of its sums alone; repeated calls give the same bits.
- * head_dim <= MOE_ATTENTION_MAX_DIM, num_seqs * table_width * page_size < 2^34
+ * head_dim <= MOE_ATTENTION_MAX_DIM, num_heads <= 2^30,
+ * num_seqs * table_width * page_size < 2^34
  * and table_width * page_size < 2^31, else MOE_ERR_UNSUPPORTED.
  */
 size_t moe_attention_decode_workspace_size(int64_t num_seqs, int32_t num_heads, int32_t num_kv_heads,

@@ -208,6 +208,8 @@ int64_t slots_of(int64_t seqs, int32_t kv_heads) {
   return (r < 1 ? 1 : r) + seqs;
 }
 
+constexpr int32_t kMostHeads = 1 << 30;  // with the last CTA's share, or the last step over heads, within 31 bits
+
 bool heads_ok(const moe_heads* h) { return h->row_stride >= 0 && h->head_stride >= 0; }
 
 }  // namespace
@@ -217,7 +219,7 @@ using namespace moe;
 
 extern "C" size_t moe_attention_decode_workspace_size(int64_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
                                                       int32_t head_dim) {
-  if (num_seqs < 0 || num_seqs > MOE_CACHE_MAX_ROWS || num_kv_heads < 1 || num_heads < 1 || num_heads % num_kv_heads ||
+  if (num_seqs < 0 || num_seqs > MOE_CACHE_MAX_ROWS || num_kv_heads < 1 || num_heads < 1 || num_heads > kMostHeads || num_heads % num_kv_heads ||
       head_dim < 1 || head_dim > MOE_ATTENTION_MAX_DIM)
     return 0;
   const int64_t rows = slots_of(num_seqs, num_kv_heads) * num_heads;
@@ -238,7 +240,7 @@ extern "C" int moe_attention_decode(const moe_kv_cache* cache, const moe_heads* 
     return MOE_ERR_INVALID_ARG;
   if ((num_seqs > 1 && table_stride < table_width) || !heads_ok(q) || (k_new != nullptr && !(heads_ok(k_new) && heads_ok(v_new))))
     return MOE_ERR_INVALID_ARG;
-  if (cache->head_dim > MOE_ATTENTION_MAX_DIM || num_seqs > MOE_CACHE_MAX_ROWS || cache->num_pages > INT32_MAX ||
+  if (cache->head_dim > MOE_ATTENTION_MAX_DIM || num_heads > kMostHeads || num_seqs > MOE_CACHE_MAX_ROWS || cache->num_pages > INT32_MAX ||
       table_width > INT32_MAX || table_width * cache->page_size > INT32_MAX - kTile ||
       num_seqs * (table_width * cache->page_size) >= (int64_t)1 << 34)
     return MOE_ERR_UNSUPPORTED;

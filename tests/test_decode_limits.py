@@ -31,3 +31,13 @@ def test_copy(lib, size):
     """A page's pieces are counted, and the count of 2^63 - 1 bytes does not come out negative."""
     some = (_lib.CachePages * 1)(_lib.CachePages(FAKE, MOST, size))
     assert lib.moe_cache_copy(some, 1, 10, FAKE, FAKE, 3, None, None, None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("heads,kv", [((1 << 30) + 1, 1), ((1 << 31) - 1, 1), ((1 << 31) - 1, (1 << 31) - 1), ((1 << 30) + 2, (1 << 29) + 1)])
+def test_attention_heads(lib, heads, kv):
+    """Warps' shares of the heads are counted in 32 bits."""
+    assert lib.moe_attention_decode_workspace_size(1, heads, kv, 1) == 0
+    cache = ctypes.byref(_lib.KvCache(FAKE, FAKE, 8, 16 * kv, kv, 1, 1, 16, kv, 1))
+    rows = ctypes.byref(_lib.Heads(FAKE, heads, 1))
+    assert lib.moe_attention_decode(cache, rows, heads, FAKE, 4, 4, FAKE, 1, None, None, 0.1, 0, FAKE, FAKE, FAKE, 1 << 60, None, None) == UNSUPPORTED
+    assert lib.moe_attention_decode_workspace_size(1, 1 << 30, 1 << 30, 1) > 0
