@@ -50,9 +50,9 @@ def _tensor(t, name: str, dims: int, dtype: torch.dtype | None, device) -> torch
     return t
 
 
-def _int32(v: int, name: str) -> int:
-    if not -2 ** 31 <= v < 2 ** 31:  # ctypes would cut it
-        raise ValueError("%s does not fit 32 bits: %d" % (name, v))
+def _int(v: int, name: str, bits: int = 32) -> int:
+    if not -2 ** (bits - 1) <= v < 2 ** (bits - 1):  # ctypes would cut it
+        raise ValueError("%s does not fit %d bits: %d" % (name, bits, v))
     return v
 
 
@@ -80,7 +80,8 @@ def _cache(k_cache, v_cache, device=None) -> _lib.KvCache:
     s = _strides(k_cache, "k_cache", True)
     if _strides(v_cache, "v_cache", True) != s:
         raise ValueError("k_cache and v_cache must have the same strides")
-    n, page, heads, dim = k_cache.shape
+    n, *rest = k_cache.shape
+    page, heads, dim = (_int(v, "k_cache's %s" % name) for v, name in zip(rest, ("page size", "kv heads", "head size")))
     return _lib.KvCache(k_cache.data_ptr() or None, v_cache.data_ptr() or None, n, *s, dt, page, heads, dim)
 
 
@@ -130,6 +131,8 @@ def moe_attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     dev = q.device
     cache = _cache(k_cache, v_cache, dev)
     B, H, D = q.shape
+    _int(H, "q's heads")
+    _int(window, "window", 64)
     q_at = _heads(q, "q", B, None, k_cache)
     table, stride, width, rows, lengths_at = _table(page_table, lengths, dev)
     if rows != B:
@@ -191,6 +194,8 @@ def moe_cache_fork(page_table: torch.Tensor, lengths: torch.Tensor, parents: tor
     _tensor(page_table, "page_table", 2, _I32, None)
     dev = page_table.device
     table, stride, old, rows, lengths_at = _table(page_table, lengths, dev)
+    for v, name, bits in ((page_size, "page_size", 32), (num_pages, "num_pages", 64), (grow, "grow", 64)):
+        _int(v, name, bits)
     _tensor(parents, "parents", 1, _I32, dev)
     R = parents.shape[0]
     parents_at = _take(parents, (R,), _I32, "parents", dev)
@@ -202,7 +207,7 @@ def moe_cache_fork(page_table: torch.Tensor, lengths: torch.Tensor, parents: tor
           zip(out, ((R, new_width), (R,), (R,), (R,)), ("out.page_table", "out.lengths", "out.src", "out.dst"))]
     with _on(dev):
         rc = _lib.load().moe_cache_fork(
-            table, stride, old, lengths_at, rows, parents_at or None, R, _int32(page_size, "page_size"), num_pages, grow, at[0], new_width, *at[1:],
+            table, stride, old, lengths_at, rows, parents_at or None, R, page_size, num_pages, grow, at[0], new_width, *at[1:],
             _status(status, dev), _stream(dev))
     _done("moe_cache_fork", rc)
     return CacheFork(*out)
@@ -219,7 +224,8 @@ def moe_cache_compact(page_table: torch.Tensor, lengths: torch.Tensor, page_size
     _tensor(page_table, "page_table", 2, _I32, None)
     dev = page_table.device
     table, stride, width, rows, lengths_at = _table(page_table, lengths, dev)
-    half = max(0, num_pages) // 2
+    _int(page_size, "page_size")
+    half = max(0, _int(num_pages, "num_pages", 64)) // 2
     if out is None:
         new = lambda *shape: torch.empty(shape, dtype=_I32, device=dev)  # noqa: E731
         out = CacheCompact(new(rows, width), new(half), new(half), new(1))
@@ -227,7 +233,7 @@ def moe_cache_compact(page_table: torch.Tensor, lengths: torch.Tensor, page_size
           zip(out, ((rows, width), (half,), (half,), (1,)), ("out.page_table", "out.src", "out.dst", "out.count"))]
     with _on(dev):
         rc = _lib.load().moe_cache_compact(
-            table, stride, width, lengths_at, rows, _int32(page_size, "page_size"), num_pages, *at, _status(status, dev), _stream(dev))
+            table, stride, width, lengths_at, rows, page_size, num_pages, *at, _status(status, dev), _stream(dev))
     _done("moe_cache_compact", rc)
     return CacheCompact(*out)
 
@@ -291,6 +297,8 @@ def moe_beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int, en
     dt = _act_dtype(logits, "logits")
     dev = logits.device
     B, W, V = logits.shape
+    for v, name in ((W, "beams"), (num_out, "num_out"), (end_token, "end_token")):
+        _int(v, name)
     per_request, stride = _strides(logits, "logits", False)
     if W == 1:
         stride = per_request
@@ -313,7 +321,7 @@ def moe_beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int, en
     ws = _workspace(workspace, lib.moe_beam_select_workspace_size(B, W, V), dev)
     with _on(dev):
         rc = lib.moe_beam_select(
-            logits.data_ptr() or None, dt, stride, scores_at or None, ended_at or None, B, W, V, num_out, _int32(end_token, "end_token"), *at,
+            logits.data_ptr() or None, dt, stride, scores_at or None, ended_at or None, B, W, V, num_out, end_token, *at,
             ws.data_ptr() or None, ws.numel(), _stream(dev))
     _done("moe_beam_select", rc)
     return tuple(out)

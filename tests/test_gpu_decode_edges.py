@@ -82,3 +82,40 @@ def test_a_selection_over_almost_2_to_the_31_rows():
     assert torch.equal(best[:, 0], scores.amax(1)) and bool((tokens == 0).all())
     assert torch.equal(parents[:, 0].long() // W, torch.arange(B, device="cuda"))
     assert torch.equal(scores.view(-1)[parents[:, 0].long()], best[:, 0])
+
+
+def test_numbers_beyond_what_the_c_abi_takes_are_refused():
+    """Not cut to their low bits: a window of 2^64 + 7 is none of 7 tokens."""
+    table, lengths, parents = ints(0, 1, 2).view(1, 3), ints(40), ints(0, 0)
+    q, k = rand(1, 4, 64), rand(4, 16, 2, 64)
+    x, s = rand(1, 3, 100), torch.zeros(1, 3, device="cuda")
+    for call, bits in ((lambda: p.moe_attention_decode(q, k, k, table, lengths, window=2 ** 64 + 7), 64),
+                       (lambda: p.moe_cache_fork(table, lengths, parents, 16, 9, 2 ** 64 + 1), 64),
+                       (lambda: p.moe_cache_fork(table, lengths, parents, 16, 2 ** 64 + 9), 64),
+                       (lambda: p.moe_cache_compact(table, lengths, 16, 2 ** 64 + 9), 64),
+                       (lambda: p.moe_beam_select(x, s, 2 ** 32 + 3), 32)):
+        with pytest.raises(ValueError, match="%d bits" % bits):
+            call()
+
+
+@pytest.mark.parametrize("dim", [1, 2, 3])
+def test_sizes_beyond_32_bits_are_refused(dim):
+    """A cache's page size, kv heads or head size of 2^32 and some: their low bits alone would be a small cache."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    shape = [1, 1, 1, 1]
+    shape[dim] = 2 ** 32 + 2
+    k = torch.empty(shape, dtype=BF16, device="cuda")
+    new = k[:, 0]
+    for call in (lambda: p.moe_attention_decode(new, k, k, ints(0).view(1, 1), ints(1)),
+                 lambda: p.moe_cache_write(new, new, k, k, ints(0).view(1, 1), ints(0, 1), ints(1))):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+
+
+def test_beams_beyond_32_bits_are_refused():
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    x = torch.zeros(1, 2 ** 32 + 5, 1, dtype=BF16, device="cuda")
+    with pytest.raises(ValueError, match="32 bits"):
+        p.moe_beam_select(x, torch.zeros(1, 2 ** 32 + 5, device="cuda"), 2)
