@@ -87,10 +87,16 @@ __device__ __forceinline__ int block_prefix(int v, int* s_warp, int& before) {
 // Where a warp is in the line of tiles.
 struct Cursor {
   int b, tile, tiles, first, n;
+  // The new token's position, or -1. A length beyond the table has no place for it: the last
+  // position that there is holds a token already, in a page that other sequences may share.
+  int fresh;
   __device__ __forceinline__ void enter(const AttendArgs& a) {
     span_of(a, b, first, n);
     tiles = (n - first + kTile - 1) / kTile;
+    fresh = a.k_new != nullptr && a.lengths[b] <= a.max_tokens ? n - 1 : -1;
   }
+  // Its row of the tile; outside [0, kTile): the tile has none.
+  __device__ __forceinline__ int fresh_row() const { return fresh - (first + tile * kTile); }
   // There is a next tile. (The bounds on b keep the steps inside the table should lengths change meanwhile.)
   __device__ __forceinline__ void next(const AttendArgs& a) {
     if (++tile < tiles) return;
@@ -163,15 +169,6 @@ __device__ __forceinline__ int64_t row_offset(const AttendArgs& a, const Cursor&
   return page * a.page_stride + (pos - a.page.of(pos) * a.page.d) * a.token_stride + kv * a.head_stride;
 }
 
-// The new token's row of the cursor's tile; outside [0, kTile): the tile has none. A length
-// beyond the table has no place for it: the last position that there is holds a token
-// already, in a page that other sequences may share.
-__device__ __forceinline__ int new_row(const AttendArgs& a, const Cursor& c) {
-  if (a.k_new == nullptr) return -1;
-  const int row = c.n - 1 - (c.first + c.tile * kTile);
-  return row < kTile && c.n == a.max_tokens && a.lengths[c.b] > c.n ? -1 : row;
-}
-
 // A warp's (or team's) range r of a head's line, and which piece hv of a group of heads.
 struct Share {
   int r, hv;
@@ -188,7 +185,7 @@ __device__ __forceinline__ int my_range(const AttendArgs& a, int place, int work
   const Share spread = share_at(place * gridDim.x + blockIdx.x, pieces);
   int total, before = 0, x = 0;  // x: tiles up to the lane's sequence
   const bool few = a.seqs <= kWarp;
-  Cursor own = {lane_id(), 0, 0, 0, 0};
+  Cursor own = {lane_id(), 0, 0, 0, 0, -1};
   if (few) {  // every warp for itself
     if (own.b < a.seqs) {
       check_length(a, a.lengths[own.b]);
@@ -218,6 +215,7 @@ __device__ __forceinline__ int my_range(const AttendArgs& a, int place, int work
     c.tiles = __shfl_sync(0xffffffffu, own.tiles, c.b);
     c.first = __shfl_sync(0xffffffffu, own.first, c.b);
     c.n = __shfl_sync(0xffffffffu, own.n, c.b);
+    c.fresh = __shfl_sync(0xffffffffu, own.fresh, c.b);
   } else {
     c = find_tile(a, prefix, lo);
   }

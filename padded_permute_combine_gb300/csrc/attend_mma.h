@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(Mma<DP, HEADS, BY, TEAM>::kWarps * kWarp, 1) a
   const auto issue = [&](bool look) {  // look: for the next tile's page
     if (issued < count) {
       const int stage = issued % kStages;
-      const int fresh = new_row(a, in);
+      const int fresh = in.fresh_row();  // the new token's
       const char* kn = a.k_new + in.b * a.kn_row + kv * a.kn_head + 2 * col0;
       const char* vn = a.v_new + in.b * a.vn_row + kv * a.vn_head + 2 * col0;
       if constexpr (SHIFT) {

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kSmWarps<GM, NC> * kWarp, 1) attend_rows_kerne
   const auto issue = [&](bool values) {
     if (issued < count) {
       const uint32_t base = ring + slot_in * slot_bytes + place;
-      const int fresh = new_row(a, in);
+      const int fresh = in.fresh_row();  // the new token's
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         if (!values) {
