@@ -119,3 +119,25 @@ def test_beams_beyond_32_bits_are_refused():
     x = torch.zeros(1, 2 ** 32 + 5, 1, dtype=BF16, device="cuda")
     with pytest.raises(ValueError, match="32 bits"):
         p.moe_beam_select(x, torch.zeros(1, 2 ** 32 + 5, device="cuda"), 2)
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF16, 64), (BF16, 100), (BF16, 77), (F32, 64), (F32, 77)])
+@pytest.mark.parametrize("length", [40, 5000])
+def test_infinite_scores(dtype, dim, length):
+    """+infinity among a head's scores: NaN. -infinity: no weight; nothing else: as without positions."""
+    pages = -(-length // 16)
+    k, v = rand(pages, 16, 2, dim, dtype=dtype, seed=2), rand(pages, 16, 2, dim, dtype=dtype, seed=3)
+    q = rand(1, 6, dim, dtype=dtype, seed=4).abs() + 0.5  # positive: an infinite key has a score of its sign
+    table, lengths = torch.arange(pages, dtype=I32, device="cuda")[None], ints(length)
+    want = p.moe_attention_decode(q, k, v, table, lengths)
+    k[1, 5, 0] = torch.inf
+    out, lse = p.moe_attention_decode(q, k, v, table, lengths)
+    assert bool(torch.isnan(out[0, :3]).all()) and bool(torch.isnan(lse[0, :3]).all())
+    assert equal((out[0, 3:], lse[0, 3:]), (want[0][0, 3:], want[1][0, 3:]))
+    k[:, :, 0] = -torch.inf
+    out, lse = p.moe_attention_decode(q, k, v, table, lengths)
+    assert bool((out[0, :3] == 0).all()) and bool((lse[0, :3] == -torch.inf).all())
+    assert equal((out[0, 3:], lse[0, 3:]), (want[0][0, 3:], want[1][0, 3:]))
+    k[0, 7, 0] = 0.25  # one score is a number: all weight
+    out, lse = p.moe_attention_decode(q, k, v, table, lengths)
+    assert torch.equal(out[0, :3], v[0, 7, 0].expand(3, dim)) and bool(torch.isfinite(lse).all())
