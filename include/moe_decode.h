@@ -85,13 +85,16 @@ typedef struct moe_heads {
  *          the size is that of the current device (0 for sizes that the call refuses).
  * Sums and the softmax's statistics are fp32, out is rounded once. bf16 caches
  * run on the tensor cores with the probabilities as sums of two bf16 numbers
- * (16 significant bits). A NaN or an infinite score among a head's makes its
- * out and lse NaN, as the formulas say; an infinite value makes its element of
- * out infinite or NaN. A sequence's result depends on the other sequences'
+ * (16 significant bits). The sums of values are divided last: values whose sum
+ * over the positions passes fp32's largest number come out infinite or NaN,
+ * although their mean does not. A NaN or +infinity among a head's scores makes
+ * its out and lse NaN; a score of -infinity has weight 0, and a head all of
+ * whose scores are -infinity counts as one without positions. An infinite value
+ * makes its element of out infinite or NaN. A sequence's result depends on the other sequences'
  * lengths in the order of its sums alone; repeated calls give the same bits.
- * head_dim <= MOE_ATTENTION_MAX_DIM, num_heads <= 2^30,
- * num_seqs * table_width * page_size < 2^34
- * and table_width * page_size < 2^31, else MOE_ERR_UNSUPPORTED.
+ * head_dim <= MOE_ATTENTION_MAX_DIM, num_seqs <= MOE_CACHE_MAX_ROWS, num_heads
+ * <= 2^30, num_pages < 2^31, table_width * page_size < 2^31 - 16 and
+ * num_seqs * table_width * page_size < 2^34, else MOE_ERR_UNSUPPORTED.
  */
 size_t moe_attention_decode_workspace_size(int64_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
                                            int32_t head_dim);
@@ -112,6 +115,8 @@ int moe_attention_decode(const moe_kv_cache* cache, const moe_heads* q, int32_t 
  *           [0, num_tokens) is read.
  * A token whose position is negative or lies beyond the table, or whose page is
  * bad, is left out (MOE_STATUS_BAD_INDEX). Nothing else of the cache changes.
+ * head_dim <= 2^20, num_kv_heads * head_dim <= 2^26, num_tokens and num_pages
+ * < 2^31 and num_seqs < 2^31 - 1, else MOE_ERR_UNSUPPORTED.
  */
 int moe_cache_write(const moe_kv_cache* cache, const moe_heads* k, const moe_heads* v, int64_t num_tokens,
                     const int32_t* offsets, const int32_t* page_table, int64_t table_stride, int64_t table_width,
@@ -119,7 +124,8 @@ int moe_cache_write(const moe_kv_cache* cache, const moe_heads* k, const moe_hea
 
 /*
  * The page table of the next step: row r goes on from row parents[r] of the old
- * table (-1: from nothing, an empty row), with room for `grow` more tokens.
+ * table, with room for `grow` more tokens (-1: from nothing; an empty row
+ * without a page, whatever `grow` is).
  *   new_lengths[r] = lengths[parents[r]] (the tokens to come are not counted)
  *   new_table[r]   = the parent's pages, then fresh ones up to
  *                    ceil((length + grow) / page_size), then -1
@@ -136,7 +142,9 @@ int moe_cache_write(const moe_kv_cache* cache, const moe_heads* k, const moe_hea
  *   page_table, lengths [num_seqs] as above; parents [num_rows] int32: an entry
  *   outside [-1, num_seqs) sets MOE_STATUS_BAD_INDEX and counts as -1
  *   new_table [num_rows, new_width] int32, contiguous; new_lengths, src, dst [num_rows] int32
- * num_seqs and num_rows <= MOE_CACHE_MAX_ROWS, num_pages <= MOE_CACHE_MAX_PAGES, else MOE_ERR_UNSUPPORTED.
+ * new_width >= table_width. num_seqs and num_rows <= MOE_CACHE_MAX_ROWS, num_pages
+ * <= MOE_CACHE_MAX_PAGES, grow and table_width * page_size < 2^31 and
+ * num_rows * new_width < 2^31 - 2^15, else MOE_ERR_UNSUPPORTED.
  */
 int moe_cache_fork(const int32_t* page_table, int64_t table_stride, int64_t table_width, const int32_t* lengths,
                    int64_t num_seqs, const int32_t* parents, int64_t num_rows, int32_t page_size, int64_t num_pages,
@@ -150,7 +158,7 @@ int moe_cache_fork(const int32_t* page_table, int64_t table_stride, int64_t tabl
  *             numbers, -1 behind each row's pages
  *   src, dst  [num_pages / 2] int32: the copies for moe_cache_copy, then -1
  *   count     [1] int32: their number
- * Limits as for moe_cache_fork.
+ * Limits as for moe_cache_fork, with num_seqs rows of table_width.
  */
 int moe_cache_compact(const int32_t* page_table, int64_t table_stride, int64_t table_width, const int32_t* lengths,
                       int64_t num_seqs, int32_t page_size, int64_t num_pages, int32_t* new_table, int32_t* src,
@@ -169,8 +177,9 @@ typedef struct moe_cache_pages {
  * passed over; numbers from num_pages on too, with MOE_STATUS_BAD_INDEX. All
  * copies read what was there before the call: no page is both a src and a dst,
  * or dst twice.
- * num_caches <= MOE_CACHE_MAX_CACHES, and at most 1 GB in one page of all of
- * them together (65535 pieces of up to 32 KB), else MOE_ERR_UNSUPPORTED.
+ * num_caches <= MOE_CACHE_MAX_CACHES, num_pages < 2^31, and less than 2 GB in one
+ * page of all of them together (65535 pieces of up to 32 KB, of which a tensor
+ * has whole ones), else MOE_ERR_UNSUPPORTED.
  */
 int moe_cache_copy(const moe_cache_pages* caches, int64_t num_caches, int64_t num_pages, const int32_t* src,
                    const int32_t* dst, int64_t num_copies, const int32_t* count, int32_t* d_status,
@@ -193,8 +202,11 @@ int moe_cache_copy(const moe_cache_pages* caches, int64_t num_caches, int64_t nu
  * A logit of -infinity is no candidate, and neither is anything of a beam whose
  * score or log sum is not finite (logits with a NaN or +infinity, or all
  * -infinity). Where candidates run out, score -infinity, parent -1 and token -1.
- * Totals are compared in 48 bits; the log sums come from 32-bit exponentials, off
- * by some 1e-8. Repeated calls give the same bits.
+ * Totals are compared in 48 bits. The log sums come from 32-bit exponentials and
+ * sums: off by 5e-8 as a rule (root mean square over vocabularies of 2 to 129280),
+ * 4e-7 at most in all that was measured. Totals of one beam come in their order;
+ * those of different beams that are nearer than twice that error in either.
+ * Repeated calls give the same bits.
  * num_beams <= MOE_BEAM_MAX_BEAMS, num_out <= MOE_BEAM_MAX_OUT, num_beams * ceil(vocab / 512) <= MOE_BEAM_MAX_UNITS
  * and num_requests * num_beams < 2^31, else MOE_ERR_UNSUPPORTED.
  */

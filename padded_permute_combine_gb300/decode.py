@@ -6,7 +6,13 @@ As in ops.py this is argument marshalling only. A cache is a pair of tensors
 dimension (tokens first, or heads first as a transposed view), the same for keys
 and values. The plain call (right arguments, outputs to be allocated) is
 marshalled by csrc/decode_calls.cpp; it answers None to any other, which is then
-taken step by step here, with a message for what is wrong.
+taken step by step here, with a message for what is wrong. The small outputs that
+a plain call allocates share one allocation, which lives as long as any of them
+(a page table kept from moe_cache_compact holds src and dst too): pass ``out``, or
+clone what is kept for long, where that matters.
+
+Nothing here is differentiable: outputs never require gradients, whatever the
+inputs do, and caches are written in place behind autograd's back.
 """
 from __future__ import annotations
 
@@ -119,7 +125,9 @@ def moe_attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     q [B, heads, head_dim], k_cache and v_cache [pages, page_size, kv_heads,
     head_dim], page_table [B, width] int32, lengths [B] int32 (the new token
     counted) -> (out [B, heads, head_dim], lse [B, heads] fp32). k_new and v_new
-    [B, kv_heads, head_dim] are written to position lengths - 1 on the way.
+    [B, kv_heads, head_dim] are written to position lengths - 1 on the way; a
+    token whose length lies beyond the table (a fork without a column to grow
+    into), or whose page is bad, is left out, and ``status`` says so.
     scale: head_dim ** -0.5 by default; window: the last positions that are
     looked at, 0 for all."""
     if out is None and lse is None and workspace is None and status is None:
