@@ -3,7 +3,9 @@
 routing-map compaction, as hand-written sm_103a CUDA kernels behind the C ABI
 in include/moe_route.h, with a thin Python binding of the same names; and, by
 include/moe_block.h, what an MoE block needs around them: the whole layer for
-a few tokens, the layer norm, and the global gradient norm and clipping."""
+a few tokens, the layer norm, and the global gradient norm and clipping; and, by
+include/moe_decode.h, what a decode step needs around that layer: attention over
+a cache in pages, the moves of its pages, and beam search's selection."""
 from . import autograd, block  # noqa: F401
 from ._lib import MoeError, load  # noqa: F401
 from .block import (  # noqa: F401
